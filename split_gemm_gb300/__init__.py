@@ -12,6 +12,11 @@ loaded, every call raises.
 
     y = conv2d_fwd(x, w, bias, relu=True, out_dtype=torch.bfloat16)
       the fused epilogue: ReLU after the bias, y stored as bf16 (whole-tile plans)
+
+Between convolutions: ``layer_norm_fwd`` / ``layer_norm_bwd`` over the channels
+(``layer_norm.py``), and 4-bit microscaled matrices (``mxfp4.py``):
+``mxfp4_quantize``, ``mxfp4_quantize_both``, ``mxfp4_dequantize``,
+``mxfp4_matmul`` (a pointwise convolution of NHWC rows) and ``layer_norm_mxfp4``.
 """
 from __future__ import annotations
 
@@ -31,6 +36,9 @@ __all__ = [
     "wgrad_workspace_bytes", "query_wgrad_algo", "conv2d_bwd_data", "conv2d_bwd_data_into", "dgrad_workspace_bytes",
     "query_dgrad_algo", "conv_transpose2d", "conv2d_fwd", "conv2d_fwd_into", "conv2d_fwd_host", "host_staging_bytes", "status",
     "last_launch_count", "strerror", "EXPORTED_SYMBOLS", "tensor_map_cache_stats",
+    "layer_norm_fwd", "layer_norm_fwd_into", "layer_norm_bwd", "layer_norm_bwd_into", "layer_norm_mxfp4",
+    "layer_norm_bwd_workspace_bytes", "LayerNormParams", "Mxfp4", "mxfp4_empty", "mxfp4_quantize", "mxfp4_quantize_both", "mxfp4_quantize_into",
+    "mxfp4_dequantize", "mxfp4_matmul", "mxfp4_matmul_into", "Mxfp4MatmulParams",
 ]
 
 LOADER_AUTO, LOADER_TMA_IM2COL, LOADER_CPASYNC, LOADER_SCALAR, LOADER_HYBRID, LOADER_ROW_WINDOW = 0, 1, 2, 3, 4, 5
@@ -57,6 +65,8 @@ EXPORTED_SYMBOLS = [
     "conv2d_fwd_query_algo_epi", "conv2d_fwd_epi_workspace_bytes", "conv2d_bwd_weight_workspace_bytes",
     "conv2d_bwd_weight", "conv2d_bwd_weight_query_algo", "conv2d_bwd_data_workspace_bytes", "conv2d_bwd_data",
     "conv2d_bwd_data_query_algo",
+    "layer_norm_fwd", "layer_norm_bwd_workspace_bytes", "layer_norm_bwd", "layer_norm_mxfp4",
+    "mxfp4_data_bytes", "mxfp4_scale_bytes", "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_matmul",
 ]
 
 
@@ -86,6 +96,16 @@ class Algo(ctypes.Structure):
 
 class Epilogue(ctypes.Structure):
     _fields_ = [("activation", ctypes.c_int32), ("out_dtype", ctypes.c_int32)]
+
+
+class LayerNormParams(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("x_stride", ctypes.c_int64),
+                ("y_stride", ctypes.c_int64), ("x_dtype", ctypes.c_int32), ("y_dtype", ctypes.c_int32),
+                ("eps", ctypes.c_float)]
+
+
+class Mxfp4MatmulParams(ctypes.Structure):
+    _fields_ = [("m", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64)]
 
 
 _lock = threading.Lock()
@@ -142,6 +162,20 @@ def _bind(lib):
     lib.conv2d_fwd_noalloc.restype = ctypes.c_int
     lib.conv2d_strerror.argtypes = [ctypes.c_int]
     lib.conv2d_strerror.restype = ctypes.c_char_p
+    L = ctypes.POINTER(LayerNormParams)
+    i64, i32 = ctypes.c_int64, ctypes.c_int32
+    lib.layer_norm_fwd.argtypes = [L, vp, vp, vp, vp, vp, vp, vp]
+    lib.layer_norm_bwd_workspace_bytes.argtypes = [L]
+    lib.layer_norm_bwd_workspace_bytes.restype = sz
+    lib.layer_norm_bwd.argtypes = [L, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.layer_norm_mxfp4.argtypes = [L, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.mxfp4_data_bytes.argtypes = [i64, i64]
+    lib.mxfp4_data_bytes.restype = sz
+    lib.mxfp4_scale_bytes.argtypes = [i64, i64]
+    lib.mxfp4_scale_bytes.restype = sz
+    lib.mxfp4_quantize.argtypes = [i64, i64, vp, i32, i64, vp, vp, vp, vp, vp]
+    lib.mxfp4_dequantize.argtypes = [i64, i64, vp, vp, vp, i32, vp]
+    lib.mxfp4_matmul.argtypes = [ctypes.POINTER(Mxfp4MatmulParams), vp, vp, vp, vp, vp, vp, ctypes.POINTER(Epilogue), vp]
     return lib
 
 
@@ -469,3 +503,9 @@ def status(workspace, stream=None) -> int:
     st = torch.cuda.current_stream() if stream is None else stream
     return int(load_library().conv2d_fwd_status(workspace.data_ptr(),
                                                 workspace.numel() * workspace.element_size(), st.cuda_stream))
+
+
+from .mxfp4 import (Mxfp4, mxfp4_dequantize, mxfp4_empty, mxfp4_matmul, mxfp4_matmul_into,  # noqa: E402
+                    mxfp4_quantize, mxfp4_quantize_both, mxfp4_quantize_into)
+from .layer_norm import (layer_norm_bwd, layer_norm_bwd_into, layer_norm_bwd_workspace_bytes,  # noqa: E402
+                         layer_norm_fwd, layer_norm_fwd_into, layer_norm_mxfp4)

@@ -16,6 +16,7 @@ from typing import List, Optional
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
+CSRC_NN = os.path.join(PKG, "csrc_nn")  # layer normalisation and 4-bit products
 INCLUDE = os.path.join(ROOT, "include")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libconv2d.so")
@@ -23,6 +24,7 @@ OBJ_DIR = os.path.join(PKG, "_build")
 
 SOURCES = ["conv2d_api.cu", "conv2d_bn64.cu", "conv2d_bn128.cu", "conv2d_bn256.cu", "conv2d_rowwin.cu", "conv2d_direct.cu",
            "conv2d_noalloc.cu", "conv2d_pair_kb1.cu", "conv2d_pair_kb2.cu"]
+SOURCES_NN = ["layer_norm.cu", "mxfp4.cu", "mxfp4_matmul.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-I", INCLUDE, "-I", CSRC]
@@ -36,8 +38,7 @@ def nvcc() -> str:
 
 
 def _deps() -> List[str]:
-    out = [os.path.join(CSRC, f) for f in os.listdir(CSRC)]
-    out.append(os.path.join(INCLUDE, "conv2d.h"))
+    out = [os.path.join(d, f) for d in (CSRC, CSRC_NN, INCLUDE) for f in os.listdir(d)]
     out.append(os.path.abspath(__file__))
     return out
 
@@ -51,7 +52,8 @@ def up_to_date() -> bool:
 
 def _compile(src: str, extra: List[str]) -> str:
     obj = os.path.join(OBJ_DIR, os.path.splitext(src)[0] + ".o")
-    cmd = [nvcc(), *ARCH, *NVCC_FLAGS, *extra, "-c", os.path.join(CSRC, src), "-o", obj]
+    folder = CSRC_NN if src in SOURCES_NN else CSRC
+    cmd = [nvcc(), *ARCH, *NVCC_FLAGS, *extra, "-c", os.path.join(folder, src), "-o", obj]
     res = subprocess.run(cmd, capture_output=True, text=True)
     if res.returncode != 0:
         raise RuntimeError(f"nvcc failed for {src}:\n{' '.join(cmd)}\n{res.stdout}\n{res.stderr}")
@@ -67,8 +69,9 @@ def build(force: bool = False, verbose_ptxas: bool = False, jobs: Optional[int] 
     os.makedirs(OBJ_DIR, exist_ok=True)
     os.makedirs(LIB_DIR, exist_ok=True)
     extra = ["-Xptxas", "-v"] if verbose_ptxas else []
-    with cf.ThreadPoolExecutor(max_workers=jobs or len(SOURCES)) as ex:
-        objs = list(ex.map(lambda s: _compile(s, extra), SOURCES))
+    sources = SOURCES + SOURCES_NN
+    with cf.ThreadPoolExecutor(max_workers=jobs or len(sources)) as ex:
+        objs = list(ex.map(lambda s: _compile(s, extra), sources))
     tmp = LIB_PATH + f".tmp{os.getpid()}"
     cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs]
     res = subprocess.run(cmd, capture_output=True, text=True)

@@ -1,0 +1,78 @@
+"""What the row operators (layer normalisation, 4-bit matrices) share: argument checks and streams."""
+from __future__ import annotations
+
+import contextlib
+from typing import Optional, Tuple
+
+import torch
+
+from . import OUT_BF16, OUT_F32
+
+DTYPE_CODES = {torch.float32: OUT_F32, torch.bfloat16: OUT_BF16}
+
+
+def rows_of(t, name) -> Tuple[int, int, int]:
+    """(rows, cols, elements between rows) of a CUDA tensor whose last dimension is dense and whose
+    leading dimensions (any number of them) fold into one of equal steps; fp32 or bf16."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in DTYPE_CODES:
+        raise TypeError(f"{name} must be torch.float32 or torch.bfloat16, got {t.dtype}")
+    shape = t.shape
+    if not shape:
+        raise ValueError(f"{name} must have at least 1 dimension")
+    cols = shape[-1]
+    if cols < 1:
+        raise ValueError(f"{name} must have at least one column")
+    if t.is_contiguous():
+        return t.numel() // cols, cols, cols
+    strides = t.stride()
+    if strides[-1] != 1 and cols > 1:
+        raise ValueError(f"{name}'s last dimension must be dense")
+    rows, step = 1, None
+    for n, s in zip(reversed(shape[:-1]), reversed(strides[:-1])):
+        if n == 1:
+            continue
+        if step is None:
+            step = s
+        elif s != rows * step:
+            raise ValueError(f"{name}'s leading dimensions must fold into rows of equal steps")
+        rows *= n
+    step = cols if step is None else step
+    if step < cols and rows > 1:
+        raise ValueError(f"{name}'s rows must not overlap")
+    return rows, cols, max(step, cols)
+
+
+def check_vector(t, name, n, like) -> Optional[int]:
+    """Device pointer of an optional dense fp32 [n] tensor on the device of ``like``."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.device != like.device:
+        raise ValueError(f"{name} must be a CUDA tensor on {like.device}")
+    if t.dtype != torch.float32:
+        raise TypeError(f"{name} must be torch.float32, got {t.dtype}")
+    if t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous with {n} elements")
+    return t.data_ptr()
+
+
+def check_out_dtype(dtype) -> int:
+    code = DTYPE_CODES.get(dtype)
+    if code is None:
+        raise TypeError(f"out_dtype must be torch.float32 or torch.bfloat16, got {dtype}")
+    return code
+
+
+def stream_of(t, stream):
+    return torch.cuda.current_stream(t.device) if stream is None else stream
+
+
+def allocating_on(stream):
+    """Context in which new tensors belong to ``stream`` (None: the current one), so that their
+    memory is neither taken from nor given back to work of another stream."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)

@@ -1,0 +1,82 @@
+// The MXFP4 format on the device (OCP Microscaling Formats v1.0: E2M1 elements,
+// blocks of 32, E8M0 scales) and small helpers shared by the kernels of this folder.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_bf16.h>
+#include <cuda_runtime.h>
+
+namespace sgb {
+namespace mx {
+
+constexpr int BLOCK = 32;          // elements that share a scale
+constexpr int TILE_ROWS = 128;     // scale tile: 128 rows x 4 blocks = 512 bytes
+constexpr int TILE_BLOCKS = 4;
+constexpr int TILE_BYTES = 512;
+
+template <typename T>
+__host__ __device__ constexpr T cdiv(T a, T b) { return (a + b - 1) / b; }
+
+// Byte of row r, block b within the scales of a matrix with `btiles` tiles to a row of tiles.
+__host__ __device__ __forceinline__ int64_t scale_at(int64_t r, int64_t b, int64_t btiles)
+{
+    return ((r >> 7) * btiles + (b >> 2)) * TILE_BYTES + ((r & 31) << 4) + ((r & 127) >> 5 << 2) + (b & 3);
+}
+
+// Scale byte of a block from the largest absolute value's fp32 bits.  The biased
+// exponent E is floor(log2) + 127, so the byte is E - 2, clamped at 0 (zeros and
+// values below 2^-125); E = 255, which any NaN or infinity of the block gives
+// because the bits of absolute values order like integers, marks the block as NaN.
+__device__ __forceinline__ uint32_t scale_byte(uint32_t amax_bits)
+{
+    const uint32_t e = amax_bits >> 23;
+    return e == 255u ? 255u : (e > 2u ? e - 2u : 0u);
+}
+
+// 2^-e for scale byte e + 127: always a normal number (the byte is at most 252).
+// A NaN block's elements are stored as they come (their scale makes them NaN).
+__device__ __forceinline__ float inverse_scale(uint32_t byte)
+{
+    return __uint_as_float((byte == 255u ? 127u : 254u - byte) << 23);
+}
+
+// 2^e; byte 0 is 2^-127, a subnormal number, and byte 255 is NaN.
+__device__ __forceinline__ float scale_value(uint32_t byte)
+{
+    return byte == 255u ? __uint_as_float(0x7fffffffu) : __uint_as_float(byte == 0u ? 0x00400000u : byte << 23);
+}
+
+// Eight fp32 values to E2M1 (nearest even, saturating), the first in the lowest four bits.
+__device__ __forceinline__ uint32_t pack_e2m1x8(const float (&v)[8])
+{
+    uint32_t r;
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b32 %0, {a, b, c, d};\n\t}"
+        : "=r"(r)
+        : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
+    return r;
+}
+
+// The value of one E2M1 code (0 .. 15).
+__device__ __forceinline__ float e2m1_value(uint32_t c)
+{
+    const uint32_t e = (c >> 1) & 3u, m = c & 1u;
+    // e = 0: m/2; else (1 + m/2) * 2^(e-1)
+    const float a = e == 0u ? 0.5f * static_cast<float>(m) : __uint_as_float(((126u + e) << 23) | (m << 22));
+    return (c & 8u) ? -a : a;
+}
+
+__device__ __forceinline__ float to_float(float v) { return v; }
+__device__ __forceinline__ float to_float(__nv_bfloat16 v) { return __bfloat162float(v); }
+__device__ __forceinline__ void from_float(float& d, float v) { d = v; }
+__device__ __forceinline__ void from_float(__nv_bfloat16& d, float v) { d = __float2bfloat16_rn(v); }
+
+__device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+}  // namespace mx
+}  // namespace sgb
