@@ -65,6 +65,11 @@ int mxfp4_matmul(const mxfp4_matmul_params* params, const void* a_data_dev, cons
                  const void* b_data_dev, const void* b_scales_dev, const float* bias_dev, void* y_dev,
                  const conv2d_epilogue* epi, conv2d_stream_t stream);
 
+/* Synchronises `stream` and returns CONV2D_OK, or CONV2D_ERR_TIMEOUT if a
+ * device-side wait (each is bounded, by seconds) ran out in any mxfp4_matmul on
+ * the current device since the last time this was asked; that call's y is undefined then. */
+int mxfp4_matmul_status(conv2d_stream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -38,7 +38,7 @@ __all__ = [
     "last_launch_count", "strerror", "EXPORTED_SYMBOLS", "tensor_map_cache_stats",
     "layer_norm_fwd", "layer_norm_fwd_into", "layer_norm_bwd", "layer_norm_bwd_into", "layer_norm_mxfp4",
     "layer_norm_bwd_workspace_bytes", "LayerNormParams", "Mxfp4", "mxfp4_empty", "mxfp4_quantize", "mxfp4_quantize_both", "mxfp4_quantize_into",
-    "mxfp4_dequantize", "mxfp4_matmul", "mxfp4_matmul_into", "Mxfp4MatmulParams",
+    "mxfp4_dequantize", "mxfp4_matmul", "mxfp4_matmul_into", "mxfp4_matmul_status", "Mxfp4MatmulParams",
 ]
 
 LOADER_AUTO, LOADER_TMA_IM2COL, LOADER_CPASYNC, LOADER_SCALAR, LOADER_HYBRID, LOADER_ROW_WINDOW = 0, 1, 2, 3, 4, 5
@@ -66,7 +66,7 @@ EXPORTED_SYMBOLS = [
     "conv2d_bwd_weight", "conv2d_bwd_weight_query_algo", "conv2d_bwd_data_workspace_bytes", "conv2d_bwd_data",
     "conv2d_bwd_data_query_algo",
     "layer_norm_fwd", "layer_norm_bwd_workspace_bytes", "layer_norm_bwd", "layer_norm_mxfp4",
-    "mxfp4_data_bytes", "mxfp4_scale_bytes", "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_matmul",
+    "mxfp4_data_bytes", "mxfp4_scale_bytes", "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_matmul", "mxfp4_matmul_status",
 ]
 
 
@@ -176,6 +176,7 @@ def _bind(lib):
     lib.mxfp4_quantize.argtypes = [i64, i64, vp, i32, i64, vp, vp, vp, vp, vp]
     lib.mxfp4_dequantize.argtypes = [i64, i64, vp, vp, vp, i32, vp]
     lib.mxfp4_matmul.argtypes = [ctypes.POINTER(Mxfp4MatmulParams), vp, vp, vp, vp, vp, vp, ctypes.POINTER(Epilogue), vp]
+    lib.mxfp4_matmul_status.argtypes = [vp]
     return lib
 
 
@@ -505,7 +506,7 @@ def status(workspace, stream=None) -> int:
                                                 workspace.numel() * workspace.element_size(), st.cuda_stream))
 
 
-from .mxfp4 import (Mxfp4, mxfp4_dequantize, mxfp4_empty, mxfp4_matmul, mxfp4_matmul_into,  # noqa: E402
+from .mxfp4 import (Mxfp4, mxfp4_dequantize, mxfp4_empty, mxfp4_matmul, mxfp4_matmul_into, mxfp4_matmul_status,  # noqa: E402
                     mxfp4_quantize, mxfp4_quantize_both, mxfp4_quantize_into)
 from .layer_norm import (layer_norm_bwd, layer_norm_bwd_into, layer_norm_bwd_workspace_bytes,  # noqa: E402
                          layer_norm_fwd, layer_norm_fwd_into, layer_norm_mxfp4)

@@ -1,0 +1,69 @@
+// Inline-PTX wrappers for the 4-bit tensor-core path, written from the PTX ISA's
+// instruction descriptions; the wrappers it has in common with the convolution
+// kernels are in ptx.cuh.
+#pragma once
+
+#include "ptx.cuh"
+
+namespace sgb {
+namespace ptx {
+
+// Instruction descriptor for kind::mxf4 (E2M1 operands, E8M0 scales, fp32 D):
+// scale-factor id of B (bits 4-5) and of A (bits 29-30), the half of a 32-bit
+// scale column (0 or 2) that the instruction's two blocks of 32 use; A and B format E2M1 (bits 7-9
+// and 10-11 = 1), N >> 3 in bits 17-22, scale type E8M0 (bit 23 = 1), M >> 4 in bits 24-28.
+__host__ __device__ constexpr uint32_t idesc_mxf4(int m, int n, int sf_id)
+{
+    return (static_cast<uint32_t>(sf_id) << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(n >> 3) << 17) | (1u << 23) |
+           (static_cast<uint32_t>(m >> 4) << 24) | (static_cast<uint32_t>(sf_id) << 29);
+}
+
+// D[tmem] (+)= A * B^T over 64 reduction elements with one scale per 32 of each row, one thread issues.
+__device__ __forceinline__ void mma_mxf4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t sfa,
+                                         uint32_t sfb, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate)
+        : "memory");
+}
+
+// Copies 32 rows of 16 bytes from shared memory into 4 tensor-memory columns, the
+// same in each of the four groups of 32 lanes.
+__device__ __forceinline__ void tmem_cp_32x128b(uint32_t taddr, uint64_t s_desc)
+{
+    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(taddr), "l"(s_desc) : "memory");
+}
+
+// Contiguous copy of a multiple of 16 bytes into this CTA's shared memory, counted on `bar`.
+__device__ __forceinline__ void bulk_load(void* dst, const void* src, uint32_t bytes, uint64_t* bar)
+{
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                     smem_addr(dst)),
+                 "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_addr(bar))
+                 : "memory");
+}
+
+// 32 lanes x 16 consecutive 32-bit columns.
+__device__ __forceinline__ void tmem_ld_32x32b_x16(uint32_t taddr, uint32_t (&v)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr)
+        : "memory");
+}
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+    return v;
+}
+
+}  // namespace ptx
+}  // namespace sgb

@@ -1,0 +1,219 @@
+// Product of microscaled 4-bit matrices on one CTA's tensor core, with the sum
+// split over a cluster: for results of few tiles, where a long sum or the
+// reading of a weight has to be spread over the SMs.
+//
+// A tile is 128 rows of one operand (P) by BN rows of the other (Q); the
+// accumulator has P's rows in its lanes.  For many rows of y, P is a and Q is b.
+// For few (SWAP), P is b, the weight: its rows fill the 128 lanes whatever the
+// number of rows of y, and consecutive lanes are consecutive elements of a row of y.
+//
+// The reduction runs in stages of 256 elements (128 bytes of a row): one TMA box
+// for each operand (128-byte swizzle), and the stage's scales, which lie in memory as 512-byte tiles of
+// 128 rows x 4 blocks, by bulk copies.  tcgen05.cp spreads a scale tile over 4
+// columns of tensor memory; every ring slot has columns of its own, so a slot's
+// scales are overwritten only after the MMAs that read them have completed.
+// Four MMAs of 64 elements make a stage.
+//
+// CTA r of a cluster of S takes the stages [r*T/S, (r+1)*T/S).  The partial tiles
+// meet in shared memory: each CTA sums 128/S rows of P over the cluster, always
+// from CTA 0 to CTA S-1, so the result does not depend on timing and needs no
+// workspace and no atomics.
+//
+// Warps 0..3: accumulator to shared memory; warp 4: copies; warp 5: MMAs.  All
+// six write the result.  Every wait is bounded: on running out the status word is set and
+// the CTA goes through its remaining barriers without waiting or storing.
+#pragma once
+
+#include <cuda.h>
+
+#include "mx_common.cuh"
+#include "mx_ptx.cuh"
+
+namespace sgb {
+namespace mx {
+
+constexpr int T_THREADS = 192;
+constexpr int T_ROWS = 128;
+constexpr int T_STAGE_BYTES_ROW = 128;           // of a row, in a stage
+constexpr int T_STAGE_BLOCKS = 8;                // blocks of 32 in a stage
+constexpr uint64_t T_WAIT_NS = 1000000000ull;
+
+struct TileParams {
+    const uint8_t *p_scales, *q_scales;
+    const float* bias;
+    void* y;
+    uint32_t* status;
+    int64_t ldy;
+    int p_rows, q_rows;      // extents of the operands
+    int blocks, btiles;      // of 32, and scale tiles, along the reduction
+    int stages;              // T
+    int q_tiles, splits;     // splits <= T, a power of two
+    int relu;
+};
+
+template <int BN>
+struct TileConfig {
+    static constexpr int P_BYTES = T_ROWS * T_STAGE_BYTES_ROW;
+    static constexpr int Q_BYTES = BN * T_STAGE_BYTES_ROW;
+    static constexpr int Q_STILES = (BN + 127) / 128;             // scale tiles along Q's rows
+    static constexpr int SF_BYTES = (1 + Q_STILES) * 2 * TILE_BYTES;
+    static constexpr int STAGE = P_BYTES + Q_BYTES + (SF_BYTES + 1023) / 1024 * 1024;
+    static constexpr int RING_MAX = 200 * 1024;
+    static constexpr int STAGES = RING_MAX / STAGE > 8 ? 8 : RING_MAX / STAGE;
+    static constexpr int SF_COLS = (1 + Q_STILES) * 8;            // tensor-memory columns of a slot's scales
+    static constexpr int COLS_USED = (BN < 32 ? 32 : BN) + STAGES * SF_COLS;
+    static constexpr uint32_t TMEM_COLS = COLS_USED <= 128 ? 128 : (COLS_USED <= 256 ? 256 : 512);
+    static_assert(COLS_USED <= 512, "tensor memory");
+    static constexpr int PITCH = T_ROWS + 1;                      // words between staged columns
+    static constexpr int STAGED = BN * PITCH * 4;
+    static constexpr int RING = STAGES * STAGE > STAGED ? STAGES * STAGE : STAGED;
+    static constexpr int SMEM = RING + 1024 + 256;                // + alignment, barriers
+};
+
+template <int BN, bool SWAP, typename T>
+__global__ void __launch_bounds__(T_THREADS) tile_kernel(const __grid_constant__ CUtensorMap tm_p,
+                                                         const __grid_constant__ CUtensorMap tm_q, const TileParams p)
+{
+    using C = TileConfig<BN>;
+    extern __shared__ uint8_t raw[];
+    uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    uint64_t* full = reinterpret_cast<uint64_t*>(ring + C::RING);
+    uint64_t* empty = full + C::STAGES;
+    uint64_t* done = empty + C::STAGES;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(done + 1);
+    volatile uint32_t* abort_flag = tmem_slot + 1;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int rank = blockIdx.x % p.splits, tile = blockIdx.x / p.splits;
+    const int p0 = tile / p.q_tiles * T_ROWS, q0 = tile % p.q_tiles * BN;
+    const int s0 = static_cast<int>(static_cast<int64_t>(rank) * p.stages / p.splits);
+    const int s1 = static_cast<int>(static_cast<int64_t>(rank + 1) * p.stages / p.splits);
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < C::STAGES; ++i) {
+            ptx::mbar_init(&full[i], 1);
+            ptx::mbar_init(&empty[i], 1);
+        }
+        ptx::mbar_init(done, 1);
+        *abort_flag = 0u;
+        ptx::mbar_init_fence();
+    }
+    if (warp == 5) {
+        ptx::tmem_alloc(tmem_slot, C::TMEM_COLS);
+        ptx::tmem_relinquish();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t acc = *tmem_slot, sf = acc + (BN < 32 ? 32 : BN);
+
+    if (warp == 4 && lane == 0) {
+        int it = 0;
+        for (int s = s0; s < s1; ++s, ++it) {
+            const int slot = it % C::STAGES;
+            if (!ptx::mbar_wait(&empty[slot], (static_cast<uint32_t>(it / C::STAGES) & 1u) ^ 1u, T_WAIT_NS)) {
+                *abort_flag = 1u;
+                break;
+            }
+            uint8_t* st = ring + slot * C::STAGE;
+            uint8_t* sfs = st + C::P_BYTES + C::Q_BYTES;
+            const int left = p.btiles - 2 * s;
+            const uint32_t sbytes = static_cast<uint32_t>(left < 2 ? left : 2) * TILE_BYTES;
+            const int q_stiles = (p.q_rows - q0 + 127) / 128;
+            const int nq = q_stiles < C::Q_STILES ? q_stiles : C::Q_STILES;
+            ptx::mbar_arrive_expect_tx(&full[slot], C::P_BYTES + C::Q_BYTES + sbytes * (1 + nq));
+            ptx::tma_load_2d(st, &tm_p, &full[slot], s * T_STAGE_BYTES_ROW, p0);
+            ptx::tma_load_2d(st + C::P_BYTES, &tm_q, &full[slot], s * T_STAGE_BYTES_ROW, q0);
+            ptx::bulk_load(sfs, p.p_scales + (static_cast<int64_t>(p0 / 128) * p.btiles + 2 * s) * TILE_BYTES, sbytes, &full[slot]);
+            for (int q = 0; q < nq; ++q)
+                ptx::bulk_load(sfs + (1 + q) * 2 * TILE_BYTES,
+                               p.q_scales + (static_cast<int64_t>(q0 / 128 + q) * p.btiles + 2 * s) * TILE_BYTES, sbytes, &full[slot]);
+        }
+        // copies in flight land before the CTA ends
+        for (int i = it > C::STAGES ? it - C::STAGES : 0; i < it; ++i)
+            if (!ptx::mbar_wait(&full[i % C::STAGES], static_cast<uint32_t>(i / C::STAGES) & 1u, T_WAIT_NS)) *abort_flag = 1u;
+    } else if (warp == 5 && lane == 0) {
+        int it = 0;
+        for (int s = s0; s < s1; ++s, ++it) {
+            const int slot = it % C::STAGES;
+            if (!ptx::mbar_wait(&full[slot], static_cast<uint32_t>(it / C::STAGES) & 1u, T_WAIT_NS)) {
+                *abort_flag = 1u;
+                break;
+            }
+            ptx::tc_fence_after();
+            const uint32_t st = ptx::smem_addr(ring + slot * C::STAGE);
+            const uint32_t sfs = st + C::P_BYTES + C::Q_BYTES;
+            const uint32_t sfa = sf + slot * C::SF_COLS, sfb = sfa + 8;
+            const int left = p.blocks - s * T_STAGE_BLOCKS;
+            const int mmas = left >= T_STAGE_BLOCKS ? 4 : (left + 1) / 2;
+            for (int t = 0; t < (mmas + 1) / 2; ++t) {  // scale tile t covers MMAs 2t and 2t+1
+                ptx::tmem_cp_32x128b(sfa + 4 * t, ptx::plain_kmajor_desc(sfs + t * TILE_BYTES, 128, 128));
+#pragma unroll
+                for (int q = 0; q < C::Q_STILES; ++q)
+                    ptx::tmem_cp_32x128b(sfb + t * 4 * C::Q_STILES + 4 * q,
+                                         ptx::plain_kmajor_desc(sfs + (2 + 2 * q + t) * TILE_BYTES, 128, 128));
+            }
+            const uint64_t da = ptx::sw128_kmajor_desc(st), db = ptx::sw128_kmajor_desc(st + C::P_BYTES);
+            for (int j = 0; j < mmas; ++j)
+                ptx::mma_mxf4(acc, da + 2 * j, db + 2 * j, ptx::idesc_mxf4(T_ROWS, BN, j % 2 * 2), sfa + 4 * (j / 2),
+                              sfb + 4 * C::Q_STILES * (j / 2), it > 0 || j > 0);
+            ptx::mma_commit(&empty[slot]);
+        }
+        ptx::mma_commit(done);
+    }
+    __syncwarp();
+
+    // The accumulator to shared memory, column by column (the ring is free once all MMAs are done).
+    float* staged = reinterpret_cast<float*>(ring);
+    const int q_left = p.q_rows - q0;
+    const int q_valid = q_left < BN ? q_left : BN;
+    const bool ok = ptx::mbar_wait(done, 0, 2 * T_WAIT_NS);
+    if (!ok) *abort_flag = 1u;
+    __syncthreads();  // also: the copies' thread has seen its last copy land
+    if (warp < 4) {
+        ptx::tc_fence_after();
+        for (int c = 0; c < q_valid; c += 16) {
+            uint32_t v[16];
+            ptx::tmem_ld_32x32b_x16(acc + (static_cast<uint32_t>(warp * 32) << 16) + c, v);
+            ptx::tmem_ld_wait();
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                staged[(c + i) * C::PITCH + warp * 32 + lane] = __uint_as_float(v[i]);
+        }
+        ptx::tc_fence_before();
+    }
+    const bool failed = *abort_flag != 0u;
+    if (p.splits > 1)
+        ptx::cluster_sync();
+    else
+        __syncthreads();
+    if (failed) {
+        if (threadIdx.x == 0 && p.status) atomicMax(p.status, 6u);
+    } else {
+        const int share = T_ROWS / p.splits, r0 = rank * share;
+        const uint32_t base = ptx::smem_addr(staged);
+        T* y = static_cast<T*>(p.y);
+        for (int e = threadIdx.x; e < share * q_valid; e += T_THREADS) {
+            const int i = r0 + (SWAP ? e % share : e / q_valid), j = SWAP ? e / share : e % q_valid;
+            if (p0 + i >= p.p_rows) continue;
+            const uint32_t at = base + static_cast<uint32_t>(j * C::PITCH + i) * 4u;
+            float s;
+            if (p.splits == 1) {
+                s = staged[j * C::PITCH + i];
+            } else {
+                s = 0.f;
+                for (int k = 0; k < p.splits; ++k) s += ptx::ld_cluster_f32(ptx::mapa_shared(at, k));
+            }
+            const int64_t row = SWAP ? q0 + j : p0 + i, col = SWAP ? p0 + i : q0 + j;
+            if (p.bias) s += p.bias[col];
+            if (p.relu && s < 0.f) s = 0.f;
+            from_float(y[row * p.ldy + col], s);
+        }
+    }
+    if (p.splits > 1) ptx::cluster_sync();  // the others have read this CTA's part
+    __syncthreads();
+    if (warp == 5) ptx::tmem_dealloc(acc, C::TMEM_COLS);
+}
+
+}  // namespace mx
+}  // namespace sgb

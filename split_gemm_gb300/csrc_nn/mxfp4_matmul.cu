@@ -1,59 +1,122 @@
 // The product of two microscaled 4-bit matrices: host side and kernels.
 #include "mxfp4.h"
 
-#include "mx_common.cuh"
+#include <atomic>
+#include <mutex>
+
+#include <cudaTypedefs.h>
+
+#include "mx_tile.cuh"
 
 namespace sgb {
 namespace mx {
 
-struct ProductParams {
-    int64_t m, n, k, blocks, btiles;
-    const uint8_t *a, *a_scales, *b, *b_scales;
-    const float* bias;
-    int relu;
+constexpr int SMS = 152;
+
+
+std::once_flag encode_once;
+PFN_cuTensorMapEncodeTiled_v12000 encode_tiled = nullptr;
+
+bool load_encoder()
+{
+    std::call_once(encode_once, [] {
+        cudaDriverEntryPointQueryResult q{};
+        void* fn = nullptr;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+            q == cudaDriverEntryPointSuccess)
+            encode_tiled = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
+    });
+    return encode_tiled != nullptr;
+}
+
+// Map of an operand's data: boxes of 128 bytes (256 elements) x box_rows rows, 128-byte swizzle; what lies
+// beyond the matrix reads as zero.
+bool encode(CUtensorMap* map, const void* data, int64_t rows, int64_t blocks, int box_rows)
+{
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(blocks * 16), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(blocks * 16)};
+    const cuuint32_t box[2] = {T_STAGE_BYTES_ROW, static_cast<cuuint32_t>(box_rows)}, steps[2] = {1, 1};
+    return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(data), dims, strides, box, steps,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Device status word of this library's product kernels; read and cleared by mxfp4_matmul_status.
+__device__ uint32_t product_status;
+
+struct Operand {
+    const void* data;
+    const void* scales;
+    int64_t rows;
 };
 
-constexpr int P_TILE = 64;
-
-// y = relu?(a b^T + bias) in fp32 multiply-adds: a 64 x 64 tile per block of
-// threads, one block of 32 along the reduction at a time.
-template <typename T>
-__global__ void __launch_bounds__(256) product_kernel(T* y, const ProductParams p)
+// Sets the kernel's shared-memory limit once per device.
+template <typename K>
+bool allow_smem(K kernel, int bytes, std::atomic<uint64_t>& done)
 {
-    __shared__ float a[P_TILE][BLOCK + 1], b[P_TILE][BLOCK + 1];
-    const int64_t ntiles = cdiv<int64_t>(p.n, P_TILE);
-    const int64_t m0 = blockIdx.x / ntiles * P_TILE, n0 = blockIdx.x % ntiles * P_TILE;
-    const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-    float acc[4][4] = {};
-    for (int64_t kb = 0; kb < p.blocks; ++kb) {
-        const int i = threadIdx.x >> 2, w = threadIdx.x & 3;  // row of the tile, word of the block
-        const int64_t ra = m0 + i, rb = n0 + i;
-        const uint32_t wa = ra < p.m ? *reinterpret_cast<const uint32_t*>(p.a + (ra * p.blocks + kb) * 16 + 4 * w) : 0u;
-        const uint32_t wb = rb < p.n ? *reinterpret_cast<const uint32_t*>(p.b + (rb * p.blocks + kb) * 16 + 4 * w) : 0u;
-        const float sa = ra < p.m ? scale_value(p.a_scales[scale_at(ra, kb, p.btiles)]) : 0.f;
-        const float sb = rb < p.n ? scale_value(p.b_scales[scale_at(rb, kb, p.btiles)]) : 0.f;
-        for (int j = 0; j < 8; ++j) {
-            a[i][8 * w + j] = e2m1_value(wa >> (4 * j) & 15u) * sa;
-            b[i][8 * w + j] = e2m1_value(wb >> (4 * j) & 15u) * sb;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (dev < 64 && (done.load(std::memory_order_acquire) & bit)) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+    if (dev < 64) done.fetch_or(bit, std::memory_order_release);
+    return true;
+}
+
+template <int BN, bool SWAP, typename T>
+int launch_tile(const Operand& P, const Operand& Q, TileParams& k, cudaStream_t stream)
+{
+    static std::atomic<uint64_t> done{0};
+    using C = TileConfig<BN>;
+    CUtensorMap tm_p, tm_q;
+    if (!encode(&tm_p, P.data, P.rows, k.blocks, T_ROWS) || !encode(&tm_q, Q.data, Q.rows, k.blocks, BN)) return CONV2D_ERR_CUDA;
+    if (!allow_smem(tile_kernel<BN, SWAP, T>, C::SMEM, done)) return CONV2D_ERR_CUDA;
+    k.q_tiles = cdiv(k.q_rows, BN);
+    const int64_t tiles = cdiv<int64_t>(k.p_rows, T_ROWS) * k.q_tiles;
+    // The sum is split while that still gives every SM at most one CTA and every CTA two stages.
+    k.splits = 1;
+    while (k.splits < 8 && tiles * k.splits * 2 <= SMS && k.stages >= 4 * k.splits) k.splits *= 2;
+    if (tiles * k.splits > INT32_MAX) return CONV2D_ERR_UNSUPPORTED;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(tiles * k.splits));
+    cfg.blockDim = dim3(T_THREADS);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = static_cast<unsigned>(k.splits);
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, tile_kernel<BN, SWAP, T>, tm_p, tm_q, k) == cudaSuccess ? CONV2D_OK : CONV2D_ERR_CUDA;
+}
+
+template <typename T>
+int product(const Operand& a, const Operand& b, TileParams& k, cudaStream_t stream)
+{
+    // Up to 128 rows of y: the weight's rows in the accumulator's lanes, y's rows in
+    // its columns, as few as cover them.
+    const bool swap = a.rows <= 128;
+    const Operand &P = swap ? b : a, &Q = swap ? a : b;
+    k.p_scales = static_cast<const uint8_t*>(P.scales);
+    k.q_scales = static_cast<const uint8_t*>(Q.scales);
+    k.p_rows = static_cast<int>(P.rows);
+    k.q_rows = static_cast<int>(Q.rows);
+    const int bn = Q.rows <= 16 ? 16 : Q.rows <= 32 ? 32 : Q.rows <= 64 ? 64 : 128;
+    if (swap) {
+        switch (bn) {
+            case 16: return launch_tile<16, true, T>(P, Q, k, stream);
+            case 32: return launch_tile<32, true, T>(P, Q, k, stream);
+            case 64: return launch_tile<64, true, T>(P, Q, k, stream);
+            default: return launch_tile<128, true, T>(P, Q, k, stream);
         }
-        __syncthreads();
-        for (int k = 0; k < BLOCK; ++k)
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-#pragma unroll
-                for (int v = 0; v < 4; ++v) acc[u][v] = fmaf(a[ty + 16 * u][k], b[tx + 16 * v][k], acc[u][v]);
-        __syncthreads();
     }
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-#pragma unroll
-        for (int v = 0; v < 4; ++v) {
-            const int64_t r = m0 + ty + 16 * u, c = n0 + tx + 16 * v;
-            if (r >= p.m || c >= p.n) continue;
-            float s = acc[u][v] + (p.bias ? p.bias[c] : 0.f);
-            if (p.relu && !(s > 0.f) && s == s) s = 0.f;  // NaN stays
-            from_float(y[r * p.n + c], s);
-        }
+    switch (bn) {
+        case 16: return launch_tile<16, false, T>(P, Q, k, stream);
+        case 32: return launch_tile<32, false, T>(P, Q, k, stream);
+        case 64: return launch_tile<64, false, T>(P, Q, k, stream);
+        default: return launch_tile<128, false, T>(P, Q, k, stream);
+    }
 }
 
 }  // namespace mx
@@ -76,23 +139,29 @@ extern "C" int mxfp4_matmul(const mxfp4_matmul_params* params, const void* a_dat
     for (const void* p : {a_data_dev, a_scales_dev, b_data_dev, b_scales_dev, static_cast<const void*>(y_dev)})
         if (reinterpret_cast<uintptr_t>(p) % 16) return CONV2D_ERR_ALIGNMENT;
     if (reinterpret_cast<uintptr_t>(bias_dev) % 4) return CONV2D_ERR_ALIGNMENT;
-    mx::ProductParams k{};
-    k.m = params->m;
-    k.n = params->n;
-    k.k = params->k;
-    k.blocks = mx::cdiv<int64_t>(k.k, mx::BLOCK);
-    k.btiles = mx::cdiv<int64_t>(k.blocks, mx::TILE_BLOCKS);
-    k.a = static_cast<const uint8_t*>(a_data_dev);
-    k.a_scales = static_cast<const uint8_t*>(a_scales_dev);
-    k.b = static_cast<const uint8_t*>(b_data_dev);
-    k.b_scales = static_cast<const uint8_t*>(b_scales_dev);
+    if (!mx::load_encoder()) return CONV2D_ERR_CUDA;
+    mx::TileParams k{};
+    k.blocks = static_cast<int>(mx::cdiv<int64_t>(params->k, mx::BLOCK));
+    k.btiles = mx::cdiv(k.blocks, mx::TILE_BLOCKS);
+    k.stages = mx::cdiv(k.blocks, mx::T_STAGE_BLOCKS);
     k.bias = bias_dev;
     k.relu = act == CONV2D_ACT_RELU;
-    const int64_t grid = mx::cdiv<int64_t>(k.m, mx::P_TILE) * mx::cdiv<int64_t>(k.n, mx::P_TILE);
-    if (grid > most) return CONV2D_ERR_UNSUPPORTED;
-    if (out == CONV2D_OUT_BF16)
-        mx::product_kernel<<<static_cast<unsigned>(grid), 256, 0, stream>>>(static_cast<__nv_bfloat16*>(y_dev), k);
-    else
-        mx::product_kernel<<<static_cast<unsigned>(grid), 256, 0, stream>>>(static_cast<float*>(y_dev), k);
-    return cudaGetLastError() == cudaSuccess ? CONV2D_OK : CONV2D_ERR_CUDA;
+    k.y = y_dev;
+    k.ldy = params->n;
+    void* status = nullptr;
+    if (cudaGetSymbolAddress(&status, mx::product_status) != cudaSuccess) return CONV2D_ERR_CUDA;
+    k.status = static_cast<uint32_t*>(status);
+    const mx::Operand a{a_data_dev, a_scales_dev, params->m}, b{b_data_dev, b_scales_dev, params->n};
+    return out == CONV2D_OUT_BF16 ? mx::product<__nv_bfloat16>(a, b, k, stream) : mx::product<float>(a, b, k, stream);
+}
+
+extern "C" int mxfp4_matmul_status(conv2d_stream_t stream)
+{
+    uint32_t word = 0;
+    if (cudaStreamSynchronize(stream) != cudaSuccess) return CONV2D_ERR_CUDA;
+    if (cudaMemcpyFromSymbol(&word, mx::product_status, sizeof word) != cudaSuccess) return CONV2D_ERR_CUDA;
+    if (word == 0) return CONV2D_OK;
+    word = 0;
+    if (cudaMemcpyToSymbol(mx::product_status, &word, sizeof word) != cudaSuccess) return CONV2D_ERR_CUDA;
+    return CONV2D_ERR_TIMEOUT;
 }

@@ -145,3 +145,9 @@ def mxfp4_matmul(a: Mxfp4, b: Mxfp4, bias=None, *, relu: bool = False, out_dtype
         y = torch.empty((a.rows, b.rows), dtype=out_dtype, device=a.data.device)
     mxfp4_matmul_into(y, a, b, bias, relu=relu, stream=stream)
     return y
+
+
+def mxfp4_matmul_status(stream=None) -> int:
+    """Synchronises the stream; 0, or CONV2D_ERR_TIMEOUT if a device-side wait of a product ran out since last asked."""
+    st = torch.cuda.current_stream() if stream is None else stream
+    return int(load_library().mxfp4_matmul_status(st.cuda_stream))
