@@ -24,7 +24,7 @@ OBJ_DIR = os.path.join(PKG, "_build")
 
 SOURCES = ["conv2d_api.cu", "conv2d_bn64.cu", "conv2d_bn128.cu", "conv2d_bn256.cu", "conv2d_rowwin.cu", "conv2d_direct.cu",
            "conv2d_noalloc.cu", "conv2d_pair_kb1.cu", "conv2d_pair_kb2.cu"]
-SOURCES_NN = ["layer_norm.cu", "mxfp4.cu", "mxfp4_matmul.cu"]
+SOURCES_NN = ["layer_norm.cu", "ln_fwd_rows.cu", "ln_bwd_rows.cu", "mxfp4.cu", "mxfp4_matmul.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-I", INCLUDE, "-I", CSRC]

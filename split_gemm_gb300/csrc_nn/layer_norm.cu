@@ -1,178 +1,12 @@
-// Layer normalisation forward and backward: host side and the kernels for rows of any width.
+// Layer normalisation: the C entry points.
 #include "layer_norm.h"
 
-#include "mxfp4.h"
-#include "mx_common.cuh"
+#include <type_traits>
+
+#include "ln_any.cuh"
 
 namespace sgb {
 namespace ln {
-
-constexpr int THREADS = 256;
-
-// Sum over the block's threads, the same value (and the same order of additions) in all of them.
-__device__ __forceinline__ float block_sum(float v, float* warp_sums)
-{
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    const int warp = threadIdx.x >> 5;
-    __syncthreads();  // warp_sums may still be read from the previous sum
-    if ((threadIdx.x & 31) == 0) warp_sums[warp] = v;
-    __syncthreads();
-    v = warp_sums[threadIdx.x & (THREADS / 32 - 1)];
-#pragma unroll
-    for (int o = THREADS / 64; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-    return v;
-}
-
-struct FwdParams {
-    int64_t rows, x_stride, y_stride, padded_rows;
-    int cols;
-    float eps, inv_cols;
-    const float *weight, *bias;
-    float *mean, *rstd;
-    uint8_t *data, *scales;
-};
-
-// mean and rstd of row x by the block: two readings, the second of the deviations' squares.
-template <typename TX>
-__device__ __forceinline__ void row_stats(const TX* x, const FwdParams& p, float* warp_sums, float& mean, float& rstd)
-{
-    float s = 0.f;
-    for (int c = threadIdx.x; c < p.cols; c += THREADS) s += mx::to_float(x[c]);
-    mean = block_sum(s, warp_sums) * p.inv_cols;
-    float q = 0.f;
-    for (int c = threadIdx.x; c < p.cols; c += THREADS) {
-        const float d = mx::to_float(x[c]) - mean;
-        q = fmaf(d, d, q);
-    }
-    rstd = 1.f / sqrtf(block_sum(q, warp_sums) * p.inv_cols + p.eps);
-}
-
-__device__ __forceinline__ float normalised(float x, float mean, float rstd, const FwdParams& p, int c)
-{
-    const float w = p.weight ? p.weight[c] : 1.f, b = p.bias ? p.bias[c] : 0.f;
-    return fmaf((x - mean) * rstd, w, b);
-}
-
-// One block per row, the row read three times.
-template <typename TX, typename TY>
-__global__ void __launch_bounds__(THREADS) fwd_any(const TX* x, TY* y, const FwdParams p)
-{
-    __shared__ float warp_sums[THREADS / 32];
-    for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
-        const TX* xr = x + r * p.x_stride;
-        float mean, rstd;
-        row_stats(xr, p, warp_sums, mean, rstd);
-        for (int c = threadIdx.x; c < p.cols; c += THREADS)
-            mx::from_float(y[r * p.y_stride + c], normalised(mx::to_float(xr[c]), mean, rstd, p, c));
-        if (threadIdx.x == 0) {
-            if (p.mean) p.mean[r] = mean;
-            if (p.rstd) p.rstd[r] = rstd;
-        }
-    }
-}
-
-// The same with a quantised result: a warp takes 32 columns, one block of the format, at a time.
-template <typename TX>
-__global__ void __launch_bounds__(THREADS) fwd_mx_any(const TX* x, const FwdParams p)
-{
-    __shared__ float warp_sums[THREADS / 32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int blocks = mx::cdiv(p.cols, mx::BLOCK), btiles = mx::cdiv(blocks, mx::TILE_BLOCKS);
-    for (int64_t r = blockIdx.x; r < p.padded_rows; r += gridDim.x) {
-        if (r >= p.rows) {  // the scale tiles' padding rows
-            for (int b = threadIdx.x; b < btiles * mx::TILE_BLOCKS; b += THREADS) p.scales[mx::scale_at(r, b, btiles)] = 0;
-            continue;
-        }
-        const TX* xr = x + r * p.x_stride;
-        float mean, rstd;
-        row_stats(xr, p, warp_sums, mean, rstd);
-        for (int b = warp; b < btiles * mx::TILE_BLOCKS; b += THREADS / 32) {
-            const int c = b * mx::BLOCK + lane;
-            const float v = c < p.cols ? normalised(mx::to_float(xr[c]), mean, rstd, p, c) : 0.f;
-            const uint32_t byte = mx::scale_byte(__reduce_max_sync(0xffffffffu, mx::abs_bits(v)));
-            if (lane == 0) p.scales[mx::scale_at(r, b, btiles)] = static_cast<uint8_t>(byte);
-            if (b >= blocks) continue;
-            const float q = v * mx::inverse_scale(byte);
-            float e[8];
-#pragma unroll
-            for (int j = 0; j < 8; ++j) e[j] = __shfl_sync(0xffffffffu, q, 8 * (lane & 3) + j);
-            const uint32_t word = mx::pack_e2m1x8(e);
-            if (lane < 4) *reinterpret_cast<uint32_t*>(p.data + (r * blocks + b) * 16 + 4 * lane) = word;
-        }
-        if (threadIdx.x == 0) {
-            if (p.mean) p.mean[r] = mean;
-            if (p.rstd) p.rstd[r] = rstd;
-        }
-    }
-}
-
-struct BwdParams {
-    int64_t rows, x_stride, dy_stride, chunk;
-    int cols;
-    float inv_cols;
-    const float *mean, *rstd, *weight;
-    float *dweight, *dbias, *part;  // part: [chunks][2][cols]
-    int chunks;
-};
-
-// dx, one block per row, the row read twice.
-template <typename TX, typename TY>
-__global__ void __launch_bounds__(THREADS) bwd_dx_any(const TY* dy, const TX* x, TX* dx, const BwdParams p)
-{
-    __shared__ float warp_sums[THREADS / 32];
-    for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
-        const TX* xr = x + r * p.x_stride;
-        const TY* dyr = dy + r * p.dy_stride;
-        const float mean = p.mean[r], rstd = p.rstd[r];
-        float s1 = 0.f, s2 = 0.f;
-        for (int c = threadIdx.x; c < p.cols; c += THREADS) {
-            const float g = mx::to_float(dyr[c]) * (p.weight ? p.weight[c] : 1.f);
-            s1 += g;
-            s2 = fmaf(g, (mx::to_float(xr[c]) - mean) * rstd, s2);
-        }
-        s1 = block_sum(s1, warp_sums) * p.inv_cols;
-        s2 = block_sum(s2, warp_sums) * p.inv_cols;
-        for (int c = threadIdx.x; c < p.cols; c += THREADS) {
-            const float g = mx::to_float(dyr[c]) * (p.weight ? p.weight[c] : 1.f);
-            const float xh = (mx::to_float(xr[c]) - mean) * rstd;
-            mx::from_float(dx[r * p.cols + c], rstd * (g - s1 - xh * s2));
-        }
-    }
-}
-
-// Partial sums of dweight and dbias over one chunk of rows, a thread to a column.
-template <typename TX, typename TY>
-__global__ void __launch_bounds__(THREADS) bwd_part_any(const TY* dy, const TX* x, const BwdParams p)
-{
-    const int c = blockIdx.x * THREADS + threadIdx.x;
-    if (c >= p.cols) return;
-    for (int k = blockIdx.y; k < p.chunks; k += gridDim.y) {
-        const int64_t r0 = k * p.chunk, r1 = r0 + p.chunk < p.rows ? r0 + p.chunk : p.rows;
-        float dw = 0.f, db = 0.f;
-        for (int64_t r = r0; r < r1; ++r) {
-            const float g = mx::to_float(dy[r * p.dy_stride + c]);
-            dw = fmaf(g, (mx::to_float(x[r * p.x_stride + c]) - p.mean[r]) * p.rstd[r], dw);
-            db += g;
-        }
-        p.part[(2 * static_cast<int64_t>(k)) * p.cols + c] = dw;
-        p.part[(2 * static_cast<int64_t>(k) + 1) * p.cols + c] = db;
-    }
-}
-
-// Joins the partial sums, in the chunks' order.
-__global__ void __launch_bounds__(THREADS) bwd_join(const BwdParams p)
-{
-    const int c = blockIdx.x * THREADS + threadIdx.x;
-    if (c >= p.cols) return;
-    float dw = 0.f, db = 0.f;
-    for (int k = 0; k < p.chunks; ++k) {
-        dw += p.part[(2 * static_cast<int64_t>(k)) * p.cols + c];
-        db += p.part[(2 * static_cast<int64_t>(k) + 1) * p.cols + c];
-    }
-    if (p.dweight) p.dweight[c] = dw;
-    if (p.dbias) p.dbias[c] = db;
-}
 
 // ---------------------------------------------------------------- host
 constexpr int64_t MAX_ROWS = (int64_t(1) << 31) - 1;
@@ -224,14 +58,31 @@ void by_types(int32_t x, int32_t y, F&& f)
         y == CONV2D_OUT_BF16 ? f(f32, b16) : f(f32, f32);
 }
 
-constexpr int64_t PART_ROWS = 64;    // rows of one chunk, at least
-constexpr int64_t PART_CHUNKS = 512;  // chunks, at most
+// Parts that the sums over the rows are made in: one for each block of the kernel that takes them.
+constexpr int64_t PART_ROWS = 64;     // rows too wide for registers: of one part, at least
+constexpr int64_t PART_CHUNKS = 512;  // and parts, at most
 
-int64_t part_chunks(int64_t rows)
+int64_t bwd_parts(int64_t rows, int64_t cols)
 {
-    const int64_t n = mx::cdiv(rows, PART_ROWS);
-    return n < PART_CHUNKS ? n : PART_CHUNKS;
+    const RowShape s = row_shape(cols);
+    if (s.threads == 0 || s.threads > 512) {
+        const int64_t n = mx::cdiv(rows, PART_ROWS);
+        return n < PART_CHUNKS ? n : PART_CHUNKS;
+    }
+    // resident blocks: 512 threads of 128 registers, or as many of 64 or fewer registers
+    const int64_t most = SMS * (s.elems == 16 ? 512 : 1024) / (s.threads <= 32 ? 256 : s.threads);
+    const int64_t n = mx::cdiv<int64_t>(rows, rows_per_block(s));
+    return n < most ? n : most;
 }
+
+// Whether rows at `p`, `stride` elements apart, are read or written in vectors of `vec` elements.
+bool in_vectors(const void* p, int64_t stride, int64_t cols, size_t elem, int64_t vec)
+{
+    const size_t bytes = vec * elem < 16 ? vec * elem : 16;
+    return cols % vec == 0 && stride % vec == 0 && aligned(p, bytes);
+}
+
+int64_t vector_of(int32_t x_dtype) { return x_dtype == CONV2D_OUT_BF16 ? 8 : 4; }
 
 }  // namespace ln
 }  // namespace sgb
@@ -248,10 +99,17 @@ extern "C" int layer_norm_fwd(const layer_norm_params* params, const void* x_dev
     if (!ln::aligned(x_dev, ln::dtype_size(params->x_dtype)) || !ln::aligned(y_dev, ln::dtype_size(params->y_dtype)) ||
         !ln::aligned(weight_dev, 4) || !ln::aligned(bias_dev, 4) || !ln::aligned(mean_dev, 4) || !ln::aligned(rstd_dev, 4))
         return CONV2D_ERR_ALIGNMENT;
-    const ln::FwdParams k = ln::fwd_params(params, weight_dev, bias_dev, mean_dev, rstd_dev);
+    ln::FwdParams k = ln::fwd_params(params, weight_dev, bias_dev, mean_dev, rstd_dev);
+    k.x = x_dev;
+    k.y = y_dev;
+    const int64_t v = ln::vector_of(params->x_dtype);
+    const bool vec = ln::in_vectors(x_dev, k.x_stride, k.cols, ln::dtype_size(params->x_dtype), v) &&
+                     ln::in_vectors(y_dev, k.y_stride, k.cols, ln::dtype_size(params->y_dtype), v);
     ln::by_types(params->x_dtype, params->y_dtype, [&](auto* tx, auto* ty) {
-        ln::fwd_any<<<ln::row_grid(k.rows), ln::THREADS, 0, stream>>>(static_cast<decltype(tx)>(const_cast<void*>(x_dev)),
-                                                                     static_cast<decltype(ty)>(y_dev), k);
+        using TX = std::remove_pointer_t<decltype(tx)>;
+        using TY = std::remove_pointer_t<decltype(ty)>;
+        if (!ln::launch_fwd_rows<TX, TY>(k, vec, stream))
+            ln::fwd_any<<<ln::row_grid(k.rows), ln::THREADS, 0, stream>>>(static_cast<const TX*>(x_dev), static_cast<TY*>(y_dev), k);
     });
     return ln::launched();
 }
@@ -267,11 +125,14 @@ extern "C" int layer_norm_mxfp4(const layer_norm_params* params, const void* x_d
         !ln::aligned(weight_dev, 4) || !ln::aligned(bias_dev, 4) || !ln::aligned(mean_dev, 4) || !ln::aligned(rstd_dev, 4))
         return CONV2D_ERR_ALIGNMENT;
     ln::FwdParams k = ln::fwd_params(params, weight_dev, bias_dev, mean_dev, rstd_dev);
+    k.x = x_dev;
+    const bool vec = ln::in_vectors(x_dev, k.x_stride, k.cols, ln::dtype_size(params->x_dtype), ln::vector_of(params->x_dtype));
     k.data = static_cast<uint8_t*>(data_dev);
     k.scales = static_cast<uint8_t*>(scales_dev);
     ln::by_types(params->x_dtype, CONV2D_OUT_F32, [&](auto* tx, auto*) {
-        ln::fwd_mx_any<<<ln::row_grid(k.padded_rows), ln::THREADS, 0, stream>>>(
-            static_cast<decltype(tx)>(const_cast<void*>(x_dev)), k);
+        using TX = std::remove_pointer_t<decltype(tx)>;
+        if (!ln::launch_fwd_rows<TX, void>(k, vec, stream))
+            ln::fwd_mx_any<<<ln::row_grid(k.padded_rows), ln::THREADS, 0, stream>>>(static_cast<const TX*>(x_dev), k);
     });
     return ln::launched();
 }
@@ -279,7 +140,7 @@ extern "C" int layer_norm_mxfp4(const layer_norm_params* params, const void* x_d
 extern "C" size_t layer_norm_bwd_workspace_bytes(const layer_norm_params* params)
 {
     if (ln::check(params, true)) return 0;
-    return static_cast<size_t>(ln::part_chunks(params->rows)) * 2 * static_cast<size_t>(params->cols) * sizeof(float);
+    return static_cast<size_t>(ln::bwd_parts(params->rows, params->cols)) * 2 * static_cast<size_t>(params->cols) * sizeof(float);
 }
 
 extern "C" int layer_norm_bwd(const layer_norm_params* params, const void* dy_dev, const void* x_dev,
@@ -307,17 +168,27 @@ extern "C" int layer_norm_bwd(const layer_norm_params* params, const void* dy_de
     k.weight = weight_dev;
     k.dweight = dweight_dev;
     k.dbias = dbias_dev;
-    k.part = static_cast<float*>(workspace_dev);
-    k.chunks = static_cast<int>(ln::part_chunks(params->rows));
+    k.x = x_dev;
+    k.dy = dy_dev;
+    k.dx = dx_dev;
+    k.part = sums ? static_cast<float*>(workspace_dev) : nullptr;
+    k.chunks = static_cast<int>(ln::bwd_parts(params->rows, params->cols));
     k.chunk = k.chunks ? mx::cdiv<int64_t>(params->rows, k.chunks) : 0;
-    const unsigned col_grid = static_cast<unsigned>(mx::cdiv(k.cols, ln::THREADS));
+    const int64_t v = ln::vector_of(params->x_dtype);
+    const size_t sx = ln::dtype_size(params->x_dtype);
+    const bool vec = ln::in_vectors(x_dev, k.x_stride, k.cols, sx, v) && ln::in_vectors(dx_dev, k.cols, k.cols, sx, v) &&
+                     ln::in_vectors(dy_dev, k.dy_stride, k.cols, ln::dtype_size(params->y_dtype), v);
     if (params->rows > 0)
         ln::by_types(params->x_dtype, params->y_dtype, [&](auto* tx, auto* ty) {
-            auto* x = static_cast<decltype(tx)>(const_cast<void*>(x_dev));
-            auto* dy = static_cast<decltype(ty)>(const_cast<void*>(dy_dev));
-            ln::bwd_dx_any<<<ln::row_grid(k.rows), ln::THREADS, 0, stream>>>(dy, x, static_cast<decltype(tx)>(dx_dev), k);
-            if (sums) ln::bwd_part_any<<<dim3(col_grid, k.chunks), ln::THREADS, 0, stream>>>(dy, x, k);
+            using TX = std::remove_pointer_t<decltype(tx)>;
+            using TY = std::remove_pointer_t<decltype(ty)>;
+            if (ln::launch_bwd_rows<TX, TY>(k, vec, k.chunks, stream)) return;
+            const TX* x = static_cast<const TX*>(x_dev);
+            const TY* dy = static_cast<const TY*>(dy_dev);
+            ln::bwd_dx_any<<<ln::row_grid(k.rows), ln::THREADS, 0, stream>>>(dy, x, static_cast<TX*>(dx_dev), k);
+            const dim3 grid(static_cast<unsigned>(mx::cdiv(k.cols, ln::THREADS)), static_cast<unsigned>(k.chunks));
+            if (sums) ln::bwd_part_any<<<grid, ln::THREADS, 0, stream>>>(dy, x, k);
         });
-    if (sums) ln::bwd_join<<<col_grid, ln::THREADS, 0, stream>>>(k);
+    if (sums) ln::bwd_join<<<static_cast<unsigned>(mx::cdiv(k.cols, 32)), 1024, 0, stream>>>(k);
     return ln::launched();
 }
