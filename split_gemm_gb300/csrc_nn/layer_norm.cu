@@ -69,8 +69,7 @@ int64_t bwd_parts(int64_t rows, int64_t cols)
         const int64_t n = mx::cdiv(rows, PART_ROWS);
         return n < PART_CHUNKS ? n : PART_CHUNKS;
     }
-    // resident blocks: 512 threads of 128 registers, or as many of 64 or fewer registers
-    const int64_t most = SMS * (s.elems == 16 ? 512 : 1024) / (s.threads <= 32 ? 256 : s.threads);
+    const int64_t most = SMS * bwd_resident(s);
     const int64_t n = mx::cdiv<int64_t>(rows, rows_per_block(s));
     return n < most ? n : most;
 }

@@ -7,7 +7,7 @@ namespace ln {
 template <typename TX, typename TY, int VEC, int E, int G>
 void start_bwd(const BwdParams& p, int grid, cudaStream_t stream)
 {
-    bwd_rows<TX, TY, VEC, E, G><<<static_cast<unsigned>(grid), block_threads<G>(), 0, stream>>>(
+    bwd_rows<TX, TY, VEC, E, G><<<static_cast<unsigned>(grid), block_threads(G), 0, stream>>>(
         static_cast<const TY*>(p.dy), static_cast<const TX*>(p.x), static_cast<TX*>(p.dx), p);
 }
 

@@ -7,9 +7,9 @@ namespace ln {
 template <typename TX, typename TY, int VEC, int E, int G>
 void start_fwd(const FwdParams& p, cudaStream_t stream)
 {
-    constexpr int T = block_threads<G>(), R = T / G;
+    constexpr int T = block_threads(G), R = T / G;
     const int64_t rows = std::is_same_v<TY, void> ? p.padded_rows : p.rows;
-    const int64_t blocks = mx::cdiv<int64_t>(rows, R), most = SMS * (2048 / T);
+    const int64_t blocks = mx::cdiv<int64_t>(rows, R), most = SMS * fwd_resident({G, E});
     fwd_rows<TX, TY, VEC, E, G><<<static_cast<unsigned>(blocks < most ? blocks : most), T, 0, stream>>>(
         static_cast<const TX*>(p.x), static_cast<TY*>(p.y), p);
 }

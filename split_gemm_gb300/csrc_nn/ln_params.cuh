@@ -43,7 +43,21 @@ __host__ __device__ constexpr RowShape row_shape(int64_t cols)
          : cols <= 8192 ? RowShape{512, 16} : cols <= 16384 ? RowShape{1024, 16} : RowShape{0, 0};
 }
 
-__host__ __device__ constexpr int rows_per_block(RowShape s) { return s.threads <= 32 ? 256 / s.threads : 1; }
+__host__ __device__ constexpr int block_threads(int threads) { return threads <= 32 ? 256 : threads; }
+__host__ __device__ constexpr int rows_per_block(RowShape s) { return block_threads(s.threads) / s.threads; }
+
+// Blocks that stay on an SM, by the registers their rows, weights and sums need: forward 64 a thread for 8
+// elements and 80 for 16; backward 85 (a row's 8 elements), 128 for 16.
+__host__ __device__ constexpr int fwd_resident(RowShape s)
+{
+    const int t = block_threads(s.threads);
+    return s.elems == 8 ? 1024 / t : t >= 512 ? 1 : 768 / t;
+}
+__host__ __device__ constexpr int bwd_resident(RowShape s)
+{
+    const int t = block_threads(s.threads);
+    return s.elems == 8 && t <= 256 ? 640 / t : t >= 512 ? 1 : 512 / t;
+}
 
 constexpr int SMS = 152;
 
