@@ -1,0 +1,260 @@
+// Product of microscaled 4-bit matrices on CTA pairs: 256 x 256 tiles, persistent.
+//
+// What bounds it: at 4-bit rates a 256 x 256 x 64 MMA of a pair takes 128 cycles, in which each SM needs 8 KB
+// of operands; the largest tile that tensor memory holds (256 fp32 columns beside the scales) is therefore taken
+// even though a second accumulator does not fit.  Its place is taken by a short drain: eight warps read the
+// accumulator into registers (about 128 columns each, a few hundred cycles), hand it back to the MMAs of the next tile and
+// write y while those run.
+//
+// A stage is 256 reduction elements.  Each CTA loads its 128 rows of a, its half of b's 256 rows (128-byte
+// swizzle), the scales of its rows of a and of all the tile's rows of b (512-byte scale tiles as a tensor of
+// 128 words x blocks/4 x rows/128, so that what lies beyond reads as zero).  Both CTAs' loads count on the leader's
+// barrier; the leader's commit frees the slot in both.  Scales have tensor-memory columns of their own for every
+// slot, so a slot's scales are overwritten only after the MMAs that read them have completed.
+//
+// Warps: 0 copies (one thread), 1 MMAs (one thread of the leader), 2..9 accumulator to y.  y goes out by TMA
+// stores of 32-row boxes, or element by element where its rows are not a multiple of 16 bytes.
+#pragma once
+
+#include "mx_tile.cuh"
+
+namespace sgb {
+namespace mx {
+
+constexpr int W_TILE = 256;
+constexpr int W_ROWS = 128;        // of a, and of b, that a CTA holds
+constexpr int W_STAGES = 5;
+constexpr int W_AB = W_ROWS * T_STAGE_BYTES_ROW;
+constexpr int W_SFA = 2 * TILE_BYTES, W_SFB = 4 * TILE_BYTES;
+constexpr int W_STAGE = 2 * W_AB + W_SFA + W_SFB;      // 35 KB
+constexpr int W_EPI_WARPS = 8;
+constexpr int W_BOX = 32 * 128;                        // 32 rows of 128 bytes
+constexpr int W_THREADS = 32 * (2 + W_EPI_WARPS);
+constexpr int W_SMEM = W_STAGES * W_STAGE + W_EPI_WARPS * W_BOX + 1024 + 256;
+constexpr int W_SF_COLS = 24;                          // of a slot: 2 x 4 for a, 2 x 8 for b
+static_assert(W_TILE + W_STAGES * W_SF_COLS <= 512, "tensor memory");
+static_assert(W_SMEM <= 232448 && W_STAGE % 1024 == 0, "shared memory");
+
+struct PairParams {
+    const float* bias;
+    void* y;
+    uint32_t* status;
+    int64_t ldy;
+    int m, n;
+    int blocks, stages;
+    int m_tiles, n_tiles;
+    int relu, tma_store;
+};
+
+// Tile number to row and column block: bands of 8 row blocks, columns within a band, rows fastest, so that the
+// tiles in flight share few rows and columns of the operands in L2.
+__device__ __forceinline__ void tile_of(int i, const PairParams& p, int& tm, int& tn)
+{
+    const int band = i / (8 * p.n_tiles), rest = i - band * 8 * p.n_tiles;
+    const int rows = p.m_tiles - band * 8 < 8 ? p.m_tiles - band * 8 : 8;
+    tn = rest / rows;
+    tm = band * 8 + rest - tn * rows;
+}
+
+template <typename T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
+    pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
+                const __grid_constant__ CUtensorMap tm_sa, const __grid_constant__ CUtensorMap tm_sb,
+                const __grid_constant__ CUtensorMap tm_y, const PairParams p)
+{
+    extern __shared__ uint8_t raw[];
+    uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    uint8_t* boxes = ring + W_STAGES * W_STAGE;
+    uint64_t* full = reinterpret_cast<uint64_t*>(boxes + W_EPI_WARPS * W_BOX);
+    uint64_t* empty = full + W_STAGES;
+    uint64_t* acc_full = empty + W_STAGES;
+    uint64_t* acc_empty = acc_full + 1;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(acc_empty + 1);
+    volatile uint32_t* abort_flag = tmem_slot + 1;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = ptx::cluster_ctarank();
+    const int cluster = static_cast<int>(ptx::cluster_id_x()), clusters = static_cast<int>(ptx::cluster_count_x());
+    const int tiles = p.m_tiles * p.n_tiles;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < W_STAGES; ++i) {
+            ptx::mbar_init(&full[i], 1);
+            ptx::mbar_init(&empty[i], 1);
+        }
+        ptx::mbar_init(acc_full, 1);
+        ptx::mbar_init(acc_empty, 2 * W_EPI_WARPS);
+        *abort_flag = 0u;
+        ptx::mbar_init_fence();
+    }
+    if (warp == 1) {
+        ptx::tmem_alloc_pair(tmem_slot, 512);
+        ptx::tmem_relinquish_pair();
+    }
+    ptx::tc_fence_before();
+    __syncthreads();
+    ptx::cluster_sync();
+    ptx::tc_fence_after();
+    const uint32_t acc = *tmem_slot, sf = acc + W_TILE;
+
+    if (warp == 0 && lane == 0) {
+        const uint32_t full0 = ptx::mapa_shared(ptx::smem_addr(full), 0);
+        int it = 0;
+        for (int tile = cluster; tile < tiles && !*abort_flag; tile += clusters) {
+            int tm, tn;
+            tile_of(tile, p, tm, tn);
+            const int row_a = tm * W_TILE + static_cast<int>(rank) * W_ROWS, row_b = tn * W_TILE + static_cast<int>(rank) * W_ROWS;
+            for (int s = 0; s < p.stages; ++s, ++it) {
+                const int slot = it % W_STAGES;
+                if (!ptx::mbar_wait(&empty[slot], (static_cast<uint32_t>(it / W_STAGES) & 1u) ^ 1u, T_WAIT_NS)) {
+                    *abort_flag = 1u;
+                    break;
+                }
+                uint8_t* st = ring + slot * W_STAGE;
+                const uint32_t bar = full0 + slot * 8;
+                if (rank == 0) ptx::mbar_arrive_expect_tx(&full[slot], 2 * W_STAGE);
+                ptx::tma_load_2d_pair(st, &tm_a, bar, s * T_STAGE_BYTES_ROW, row_a);
+                ptx::tma_load_2d_pair(st + W_AB, &tm_b, bar, s * T_STAGE_BYTES_ROW, row_b);
+                ptx::tma_load_3d_pair(st + 2 * W_AB, &tm_sa, bar, 0, 2 * s, row_a / TILE_ROWS);
+                ptx::tma_load_3d_pair(st + 2 * W_AB + W_SFA, &tm_sb, bar, 0, 2 * s, tn * 2);
+            }
+        }
+        // The last use of each slot is over (its copies have landed and been read) once the leader frees it.
+        for (int i = it > W_STAGES ? it - W_STAGES : 0; i < it; ++i)
+            if (!ptx::mbar_wait(&empty[i % W_STAGES], static_cast<uint32_t>(i / W_STAGES) & 1u, T_WAIT_NS)) *abort_flag = 1u;
+    } else if (warp == 1 && lane == 0 && rank == 0) {
+        int it = 0, n = 0;
+        for (int tile = cluster; tile < tiles && !*abort_flag; tile += clusters, ++n) {
+            if (!ptx::mbar_wait(acc_empty, (static_cast<uint32_t>(n) & 1u) ^ 1u, T_WAIT_NS)) {
+                *abort_flag = 1u;
+                break;
+            }
+            ptx::tc_fence_after();
+            for (int s = 0; s < p.stages; ++s, ++it) {
+                const int slot = it % W_STAGES;
+                if (!ptx::mbar_wait_spin(&full[slot], static_cast<uint32_t>(it / W_STAGES) & 1u, T_WAIT_NS)) {
+                    *abort_flag = 1u;
+                    break;
+                }
+                ptx::tc_fence_after();
+                const uint32_t st = ptx::smem_addr(ring + slot * W_STAGE);
+                const uint32_t sfs = st + 2 * W_AB, sfa = sf + slot * W_SF_COLS, sfb = sfa + 8;
+                const int left = p.blocks - s * T_STAGE_BLOCKS;
+                const int mmas = left >= T_STAGE_BLOCKS ? 4 : (left + 1) / 2;
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    ptx::tmem_cp_32x128b_pair(sfa + 4 * t, ptx::plain_kmajor_desc(sfs + t * TILE_BYTES, 128, 128));
+                    ptx::tmem_cp_32x128b_pair(sfb + 8 * t, ptx::plain_kmajor_desc(sfs + W_SFA + t * TILE_BYTES, 128, 128));
+                    ptx::tmem_cp_32x128b_pair(sfb + 8 * t + 4, ptx::plain_kmajor_desc(sfs + W_SFA + (2 + t) * TILE_BYTES, 128, 128));
+                }
+                const uint64_t da = ptx::sw128_kmajor_desc(st), db = ptx::sw128_kmajor_desc(st + W_AB);
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (j < mmas)
+                        ptx::mma_mxf4_pair(acc, da + 2 * j, db + 2 * j, ptx::idesc_mxf4(W_TILE, W_TILE, j % 2 * 2), sfa + 4 * (j / 2),
+                                           sfb + 8 * (j / 2), s > 0 || j > 0);
+                ptx::mma_commit_pair(&empty[slot], 3);
+            }
+            ptx::mma_commit_pair(acc_full, 3);
+        }
+    } else if (warp >= 2) {
+        const int quad = warp & 3, half = (warp - 2) >> 2;  // lanes 32*quad.., columns 128*half..
+        uint8_t* box = boxes + (warp - 2) * W_BOX;
+        const uint32_t box_addr = ptx::smem_addr(box);
+        const uint32_t release = ptx::mapa_shared(ptx::smem_addr(acc_empty), 0);
+        constexpr int COLS = 128 / sizeof(T);  // of a box
+        int n = 0;
+        for (int tile = cluster; tile < tiles && !*abort_flag; tile += clusters, ++n) {
+            int tm, tn;
+            tile_of(tile, p, tm, tn);
+            if (!ptx::mbar_wait(acc_full, static_cast<uint32_t>(n) & 1u, 2 * T_WAIT_NS)) {
+                *abort_flag = 1u;
+                break;
+            }
+            ptx::tc_fence_after();
+            uint32_t v[4][32];
+#pragma unroll
+            for (int c = 0; c < 4; ++c)
+                ptx::tmem_ld_32x32b_x32(acc + (static_cast<uint32_t>(quad * 32) << 16) + half * 128 + c * 32, v[c]);
+            ptx::tmem_ld_wait();
+            ptx::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive_cluster(release);
+            const int row0 = tm * W_TILE + static_cast<int>(rank) * W_ROWS + quad * 32, col0 = tn * W_TILE + half * 128;
+            if (row0 >= p.m || col0 >= p.n) continue;
+            if (p.bias) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        const int col = col0 + c * 32 + i;
+                        v[c][i] = __float_as_uint(__uint_as_float(v[c][i]) + (col < p.n ? __ldg(p.bias + col) : 0.f));
+                    }
+            }
+            if (p.relu) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (__uint_as_float(v[c][i]) < 0.f) v[c][i] = 0u;
+            }
+#pragma unroll
+            for (int b = 0; b < 128 / COLS; ++b) {
+                if (col0 + b * COLS >= p.n) break;
+                // the box is free once the last store from it has been read
+                if (lane == 0) ptx::bulk_wait_read_all();
+                __syncwarp();
+                const uint32_t at = box_addr + lane * 128;
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {  // 16 bytes each, swizzled by the row
+                    uint32_t w[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if constexpr (sizeof(T) == 4) {
+                            w[i] = v[b][4 * q + i];
+                        } else {
+                            const int e = b * 64 + q * 8 + 2 * i;
+                            const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(v[e / 32][e % 32]), __uint_as_float(v[e / 32][e % 32 + 1]));
+                            w[i] = *reinterpret_cast<const uint32_t*>(&h);
+                        }
+                    }
+                    ptx::st_shared_v4(at + ((q ^ (lane & 7)) << 4), w[0], w[1], w[2], w[3]);
+                }
+                if (p.tma_store) {
+                    ptx::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) {
+                        ptx::tma_store_2d(&tm_y, box, col0 + b * COLS, row0);
+                        ptx::bulk_commit();
+                    }
+                } else {
+                    __syncwarp();
+                    T* y = static_cast<T*>(p.y);
+                    for (int e = lane; e < 32 * COLS; e += 32) {
+                        const int r = e / COLS, c = e % COLS;
+                        const int byte = r * 128 + ((c * static_cast<int>(sizeof(T))) ^ ((r & 7) << 4));
+                        if (row0 + r < p.m && col0 + b * COLS + c < p.n)
+                            y[static_cast<int64_t>(row0 + r) * p.ldy + col0 + b * COLS + c] = *reinterpret_cast<const T*>(box + byte);
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+        if (lane == 0) ptx::bulk_wait_read_all();
+    }
+    __syncwarp();
+    __syncthreads();
+    if (*abort_flag && threadIdx.x == 0) {
+        // let copies in flight land before this CTA's memory goes
+        const uint64_t t0 = ptx::clock64();
+        while (ptx::clock64() - t0 < ptx::ns_to_cycles(1000000ull)) {
+        }
+        if (p.status) atomicMax(p.status, 6u);
+    }
+    __syncthreads();
+    ptx::cluster_sync();
+    if (warp == 1) ptx::tmem_dealloc_pair(acc, 512);
+}
+
+}  // namespace mx
+}  // namespace sgb

@@ -6,7 +6,7 @@
 
 #include <cudaTypedefs.h>
 
-#include "mx_tile.cuh"
+#include "mx_pair.cuh"
 
 namespace sgb {
 namespace mx {
@@ -91,12 +91,66 @@ int launch_tile(const Operand& P, const Operand& Q, TileParams& k, cudaStream_t 
     return cudaLaunchKernelEx(&cfg, tile_kernel<BN, SWAP, T>, tm_p, tm_q, k) == cudaSuccess ? CONV2D_OK : CONV2D_ERR_CUDA;
 }
 
+// Map of an operand's scales: tiles of 128 words, `tiles` of them to a row of tiles; boxes of 2 x box_rows tiles.
+bool encode_scales(CUtensorMap* map, const void* scales, int64_t rows, int btiles, int box_rows)
+{
+    const cuuint64_t dims[3] = {TILE_BYTES / 4, static_cast<cuuint64_t>(btiles), static_cast<cuuint64_t>(cdiv<int64_t>(rows, TILE_ROWS))};
+    const cuuint64_t strides[2] = {TILE_BYTES, static_cast<cuuint64_t>(btiles) * TILE_BYTES};
+    const cuuint32_t box[3] = {TILE_BYTES / 4, 2, static_cast<cuuint32_t>(box_rows)}, steps[3] = {1, 1, 1};
+    return encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT32, 3, const_cast<void*>(scales), dims, strides, box, steps,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Map of y [m][n] for stores of 32 rows x 128 bytes.
+bool encode_y(CUtensorMap* map, void* y, int64_t m, int64_t n, int elem)
+{
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(n), static_cast<cuuint64_t>(m)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(n * elem)};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / elem), 32}, steps[2] = {1, 1};
+    return encode_tiled(map, elem == 2 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 2, y, dims, strides, box,
+                        steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename T>
+int launch_pair(const Operand& a, const Operand& b, const TileParams& k, cudaStream_t stream)
+{
+    static std::atomic<uint64_t> done{0};
+    PairParams p{};
+    p.bias = k.bias;
+    p.y = k.y;
+    p.status = k.status;
+    p.ldy = k.ldy;
+    p.m = static_cast<int>(a.rows);
+    p.n = static_cast<int>(b.rows);
+    p.blocks = k.blocks;
+    p.stages = k.stages;
+    p.m_tiles = cdiv(p.m, W_TILE);
+    p.n_tiles = cdiv(p.n, W_TILE);
+    p.relu = k.relu;
+    p.tma_store = b.rows * sizeof(T) % 16 == 0;
+    const int64_t tiles = static_cast<int64_t>(p.m_tiles) * p.n_tiles;
+    if (tiles > INT32_MAX - SMS) return CONV2D_ERR_UNSUPPORTED;
+    CUtensorMap tm_a, tm_b, tm_sa, tm_sb, tm_y{};
+    if (!encode(&tm_a, a.data, a.rows, k.blocks, W_ROWS) || !encode(&tm_b, b.data, b.rows, k.blocks, W_ROWS) ||
+        !encode_scales(&tm_sa, a.scales, a.rows, k.btiles, 1) || !encode_scales(&tm_sb, b.scales, b.rows, k.btiles, 2) ||
+        (p.tma_store && !encode_y(&tm_y, k.y, a.rows, b.rows, sizeof(T))))
+        return CONV2D_ERR_CUDA;
+    if (!allow_smem(pair_kernel<T>, W_SMEM, done)) return CONV2D_ERR_CUDA;
+    const unsigned grid = 2 * static_cast<unsigned>(tiles < SMS / 2 ? tiles : SMS / 2);
+    pair_kernel<T><<<grid, W_THREADS, W_SMEM, stream>>>(tm_a, tm_b, tm_sa, tm_sb, tm_y, p);
+    return cudaGetLastError() == cudaSuccess ? CONV2D_OK : CONV2D_ERR_CUDA;
+}
+
 template <typename T>
 int product(const Operand& a, const Operand& b, TileParams& k, cudaStream_t stream)
 {
     // Up to 128 rows of y: the weight's rows in the accumulator's lanes, y's rows in
     // its columns, as few as cover them.
     const bool swap = a.rows <= 128;
+    // 256 x 256 tiles where they fill half of the SM pairs.
+    if (!swap && cdiv<int64_t>(a.rows, W_TILE) * cdiv<int64_t>(b.rows, W_TILE) * 4 >= SMS) return launch_pair<T>(a, b, k, stream);
     const Operand &P = swap ? b : a, &Q = swap ? a : b;
     k.p_scales = static_cast<const uint8_t*>(P.scales);
     k.q_scales = static_cast<const uint8_t*>(Q.scales);

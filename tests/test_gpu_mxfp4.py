@@ -110,7 +110,8 @@ def _check_product(y, a, b, bias, relu, dtype):
 
 MNK = [(1, 1, 1), (1, 64, 32), (1, 1000, 4096), (2, 4096, 64), (3, 129, 2000), (5, 300, 16384), (8, 513, 1024), (17, 256, 96),
        (33, 77, 200), (64, 64, 64), (100, 1000, 160), (127, 128, 129), (128, 256, 512), (130, 130, 130), (255, 257, 1000),
-       (300, 40, 3000), (777, 1001, 2000), (1024, 256, 5000), (1500, 8, 512), (2049, 640, 256), (512, 2560, 320)]
+       (300, 40, 3000), (777, 1001, 2000), (1024, 256, 5000), (1500, 8, 512), (2049, 640, 256), (512, 2560, 320),
+       (2500, 2600, 100), (2304, 1100, 2080), (5000, 1003, 770), (300, 10000, 64), (2561, 2056, 33), (3000, 1284, 1500)]
 
 
 @pytest.mark.parametrize("m,n,k", MNK)
