@@ -22,6 +22,7 @@ namespace sgb {
 namespace mx {
 
 constexpr int W_TILE = 256;
+constexpr int W_BAND = 16;         // row blocks of tiles taken together
 constexpr int W_ROWS = 128;        // of a, and of b, that a CTA holds
 constexpr int W_STAGES = 5;
 constexpr int W_AB = W_ROWS * T_STAGE_BYTES_ROW;
@@ -46,14 +47,14 @@ struct PairParams {
     int relu, tma_store;
 };
 
-// Tile number to row and column block: bands of 8 row blocks, columns within a band, rows fastest, so that the
+// Tile number to row and column block: bands of 16 row blocks, columns within a band, rows fastest, so that the
 // tiles in flight share few rows and columns of the operands in L2.
 __device__ __forceinline__ void tile_of(int i, const PairParams& p, int& tm, int& tn)
 {
-    const int band = i / (8 * p.n_tiles), rest = i - band * 8 * p.n_tiles;
-    const int rows = p.m_tiles - band * 8 < 8 ? p.m_tiles - band * 8 : 8;
+    const int band = i / (W_BAND * p.n_tiles), rest = i - band * W_BAND * p.n_tiles;
+    const int rows = p.m_tiles - band * W_BAND < W_BAND ? p.m_tiles - band * W_BAND : W_BAND;
     tn = rest / rows;
-    tm = band * 8 + rest - tn * rows;
+    tm = band * W_BAND + rest - tn * rows;
 }
 
 template <typename T>
@@ -122,7 +123,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
         // The last use of each slot is over (its copies have landed and been read) once the leader frees it.
         for (int i = it > W_STAGES ? it - W_STAGES : 0; i < it; ++i)
             if (!ptx::mbar_wait(&empty[i % W_STAGES], static_cast<uint32_t>(i / W_STAGES) & 1u, T_WAIT_NS)) *abort_flag = 1u;
-    } else if (warp == 1 && lane == 0 && rank == 0) {
+    } else if (warp == 1 && rank == 0) {  // the whole warp, so that operands stay uniform; one lane issues
         int it = 0, n = 0;
         for (int tile = cluster; tile < tiles && !*abort_flag; tile += clusters, ++n) {
             if (!ptx::mbar_wait(acc_empty, (static_cast<uint32_t>(n) & 1u) ^ 1u, T_WAIT_NS)) {
@@ -137,25 +138,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
                     break;
                 }
                 ptx::tc_fence_after();
+                // Past the reduction's end elements and scales read as zero, so the last stage takes four MMAs too.
                 const uint32_t st = ptx::smem_addr(ring + slot * W_STAGE);
-                const uint32_t sfs = st + 2 * W_AB, sfa = sf + slot * W_SF_COLS, sfb = sfa + 8;
-                const int left = p.blocks - s * T_STAGE_BLOCKS;
-                const int mmas = left >= T_STAGE_BLOCKS ? 4 : (left + 1) / 2;
-#pragma unroll
-                for (int t = 0; t < 2; ++t) {
-                    ptx::tmem_cp_32x128b_pair(sfa + 4 * t, ptx::plain_kmajor_desc(sfs + t * TILE_BYTES, 128, 128));
-                    ptx::tmem_cp_32x128b_pair(sfb + 8 * t, ptx::plain_kmajor_desc(sfs + W_SFA + t * TILE_BYTES, 128, 128));
-                    ptx::tmem_cp_32x128b_pair(sfb + 8 * t + 4, ptx::plain_kmajor_desc(sfs + W_SFA + (2 + t) * TILE_BYTES, 128, 128));
-                }
-                const uint64_t da = ptx::sw128_kmajor_desc(st), db = ptx::sw128_kmajor_desc(st + W_AB);
-#pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    if (j < mmas)
-                        ptx::mma_mxf4_pair(acc, da + 2 * j, db + 2 * j, ptx::idesc_mxf4(W_TILE, W_TILE, j % 2 * 2), sfa + 4 * (j / 2),
-                                           sfb + 8 * (j / 2), s > 0 || j > 0);
-                ptx::mma_commit_pair(&empty[slot], 3);
+                ptx::mma_mxf4_pair_stage(acc, ptx::sw128_kmajor_desc(st), ptx::sw128_kmajor_desc(st + W_AB),
+                                         ptx::plain_kmajor_desc(st + 2 * W_AB, 128, 128), sf + slot * W_SF_COLS,
+                                         ptx::idesc_mxf4(W_TILE, W_TILE, 0), ptx::idesc_mxf4(W_TILE, W_TILE, 2), s > 0);
+                ptx::mma_commit_pair_elect(&empty[slot], 3);
             }
-            ptx::mma_commit_pair(acc_full, 3);
+            ptx::mma_commit_pair_elect(acc_full, 3);
         }
     } else if (warp >= 2) {
         const int quad = warp & 3, half = (warp - 2) >> 2;  // lanes 32*quad.., columns 128*half..

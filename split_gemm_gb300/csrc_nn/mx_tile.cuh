@@ -55,12 +55,11 @@ template <int BN>
 struct TileConfig {
     static constexpr int P_BYTES = T_ROWS * T_STAGE_BYTES_ROW;
     static constexpr int Q_BYTES = BN * T_STAGE_BYTES_ROW;
-    static constexpr int Q_STILES = (BN + 127) / 128;             // scale tiles along Q's rows
-    static constexpr int SF_BYTES = (1 + Q_STILES) * 2 * TILE_BYTES;
-    static constexpr int STAGE = P_BYTES + Q_BYTES + (SF_BYTES + 1023) / 1024 * 1024;
+    static_assert(BN <= 128, "one scale tile along Q's rows");
+    static constexpr int STAGE = P_BYTES + Q_BYTES + 4 * TILE_BYTES;  // with two scale tiles of each
     static constexpr int RING_MAX = 200 * 1024;
     static constexpr int STAGES = RING_MAX / STAGE > 8 ? 8 : RING_MAX / STAGE;
-    static constexpr int SF_COLS = (1 + Q_STILES) * 8;            // tensor-memory columns of a slot's scales
+    static constexpr int SF_COLS = 16;                            // tensor-memory columns of a slot's scales
     static constexpr int COLS_USED = (BN < 32 ? 32 : BN) + STAGES * SF_COLS;
     static constexpr uint32_t TMEM_COLS = COLS_USED <= 128 ? 128 : (COLS_USED <= 256 ? 256 : 512);
     static_assert(COLS_USED <= 512, "tensor memory");
@@ -119,47 +118,34 @@ __global__ void __launch_bounds__(T_THREADS) tile_kernel(const __grid_constant__
             uint8_t* sfs = st + C::P_BYTES + C::Q_BYTES;
             const int left = p.btiles - 2 * s;
             const uint32_t sbytes = static_cast<uint32_t>(left < 2 ? left : 2) * TILE_BYTES;
-            const int q_stiles = (p.q_rows - q0 + 127) / 128;
-            const int nq = q_stiles < C::Q_STILES ? q_stiles : C::Q_STILES;
-            ptx::mbar_arrive_expect_tx(&full[slot], C::P_BYTES + C::Q_BYTES + sbytes * (1 + nq));
+            ptx::mbar_arrive_expect_tx(&full[slot], C::P_BYTES + C::Q_BYTES + 2 * sbytes);
             ptx::tma_load_2d(st, &tm_p, &full[slot], s * T_STAGE_BYTES_ROW, p0);
             ptx::tma_load_2d(st + C::P_BYTES, &tm_q, &full[slot], s * T_STAGE_BYTES_ROW, q0);
             ptx::bulk_load(sfs, p.p_scales + (static_cast<int64_t>(p0 / 128) * p.btiles + 2 * s) * TILE_BYTES, sbytes, &full[slot]);
-            for (int q = 0; q < nq; ++q)
-                ptx::bulk_load(sfs + (1 + q) * 2 * TILE_BYTES,
-                               p.q_scales + (static_cast<int64_t>(q0 / 128 + q) * p.btiles + 2 * s) * TILE_BYTES, sbytes, &full[slot]);
+            ptx::bulk_load(sfs + 2 * TILE_BYTES, p.q_scales + (static_cast<int64_t>(q0 / 128) * p.btiles + 2 * s) * TILE_BYTES, sbytes,
+                           &full[slot]);
         }
         // copies in flight land before the CTA ends
         for (int i = it > C::STAGES ? it - C::STAGES : 0; i < it; ++i)
             if (!ptx::mbar_wait(&full[i % C::STAGES], static_cast<uint32_t>(i / C::STAGES) & 1u, T_WAIT_NS)) *abort_flag = 1u;
-    } else if (warp == 5 && lane == 0) {
+    } else if (warp == 5) {  // the whole warp, so that operands stay uniform; one lane issues
         int it = 0;
         for (int s = s0; s < s1; ++s, ++it) {
             const int slot = it % C::STAGES;
-            if (!ptx::mbar_wait(&full[slot], static_cast<uint32_t>(it / C::STAGES) & 1u, T_WAIT_NS)) {
+            if (!ptx::mbar_wait_spin(&full[slot], static_cast<uint32_t>(it / C::STAGES) & 1u, T_WAIT_NS)) {
                 *abort_flag = 1u;
                 break;
             }
             ptx::tc_fence_after();
             const uint32_t st = ptx::smem_addr(ring + slot * C::STAGE);
-            const uint32_t sfs = st + C::P_BYTES + C::Q_BYTES;
-            const uint32_t sfa = sf + slot * C::SF_COLS, sfb = sfa + 8;
             const int left = p.blocks - s * T_STAGE_BLOCKS;
-            const int mmas = left >= T_STAGE_BLOCKS ? 4 : (left + 1) / 2;
-            for (int t = 0; t < (mmas + 1) / 2; ++t) {  // scale tile t covers MMAs 2t and 2t+1
-                ptx::tmem_cp_32x128b(sfa + 4 * t, ptx::plain_kmajor_desc(sfs + t * TILE_BYTES, 128, 128));
-#pragma unroll
-                for (int q = 0; q < C::Q_STILES; ++q)
-                    ptx::tmem_cp_32x128b(sfb + t * 4 * C::Q_STILES + 4 * q,
-                                         ptx::plain_kmajor_desc(sfs + (2 + 2 * q + t) * TILE_BYTES, 128, 128));
-            }
-            const uint64_t da = ptx::sw128_kmajor_desc(st), db = ptx::sw128_kmajor_desc(st + C::P_BYTES);
-            for (int j = 0; j < mmas; ++j)
-                ptx::mma_mxf4(acc, da + 2 * j, db + 2 * j, ptx::idesc_mxf4(T_ROWS, BN, j % 2 * 2), sfa + 4 * (j / 2),
-                              sfb + 4 * C::Q_STILES * (j / 2), it > 0 || j > 0);
-            ptx::mma_commit(&empty[slot]);
+            ptx::mma_mxf4_stage(acc, ptx::sw128_kmajor_desc(st), ptx::sw128_kmajor_desc(st + C::P_BYTES),
+                                ptx::plain_kmajor_desc(st + C::P_BYTES + C::Q_BYTES, 128, 128), sf + slot * C::SF_COLS,
+                                ptx::idesc_mxf4(T_ROWS, BN, 0), ptx::idesc_mxf4(T_ROWS, BN, 2), it > 0,
+                                left >= T_STAGE_BLOCKS ? 4 : (left + 1) / 2);
+            ptx::mma_commit_elect(&empty[slot]);
         }
-        ptx::mma_commit(done);
+        ptx::mma_commit_elect(done);
     }
     __syncwarp();
 
