@@ -123,10 +123,11 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const void* map, uin
         : "memory");
 }
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr)
+__device__ __forceinline__ float4 ld_cluster_v4(uint32_t cluster_addr)
 {
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];" : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w) : "r"(cluster_addr)
+                 : "memory");
     return v;
 }
 

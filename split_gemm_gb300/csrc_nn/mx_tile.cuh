@@ -49,9 +49,10 @@ struct TileParams {
     int stages;              // T
     int q_tiles, splits;     // splits <= T, a power of two
     int relu;
+    int vec_y;               // rows of y are whole groups of four elements
 };
 
-template <int BN>
+template <int BN, bool SWAP>
 struct TileConfig {
     static constexpr int P_BYTES = T_ROWS * T_STAGE_BYTES_ROW;
     static constexpr int Q_BYTES = BN * T_STAGE_BYTES_ROW;
@@ -63,8 +64,10 @@ struct TileConfig {
     static constexpr int COLS_USED = (BN < 32 ? 32 : BN) + STAGES * SF_COLS;
     static constexpr uint32_t TMEM_COLS = COLS_USED <= 128 ? 128 : (COLS_USED <= 256 ? 256 : 512);
     static_assert(COLS_USED <= 512, "tensor memory");
-    static constexpr int PITCH = T_ROWS + 1;                      // words between staged columns
-    static constexpr int STAGED = BN * PITCH * 4;
+    // The staged tile, in y's order: rows of BN (SWAP: of 128) words and 4 more, so that 16-byte accesses of
+    // neighbouring rows fall into different banks.
+    static constexpr int PITCH = (SWAP ? T_ROWS : BN) + 4;
+    static constexpr int STAGED = (SWAP ? BN : T_ROWS) * PITCH * 4;
     static constexpr int RING = STAGES * STAGE > STAGED ? STAGES * STAGE : STAGED;
     static constexpr int SMEM = RING + 1024 + 256;                // + alignment, barriers
 };
@@ -73,7 +76,7 @@ template <int BN, bool SWAP, typename T>
 __global__ void __launch_bounds__(T_THREADS) tile_kernel(const __grid_constant__ CUtensorMap tm_p,
                                                          const __grid_constant__ CUtensorMap tm_q, const TileParams p)
 {
-    using C = TileConfig<BN>;
+    using C = TileConfig<BN, SWAP>;
     extern __shared__ uint8_t raw[];
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(ring + C::RING);
@@ -149,7 +152,7 @@ __global__ void __launch_bounds__(T_THREADS) tile_kernel(const __grid_constant__
     }
     __syncwarp();
 
-    // The accumulator to shared memory, column by column (the ring is free once all MMAs are done).
+    // The accumulator to shared memory (the ring is free once all MMAs are done).
     float* staged = reinterpret_cast<float*>(ring);
     const int q_left = p.q_rows - q0;
     const int q_valid = q_left < BN ? q_left : BN;
@@ -162,9 +165,15 @@ __global__ void __launch_bounds__(T_THREADS) tile_kernel(const __grid_constant__
             uint32_t v[16];
             ptx::tmem_ld_32x32b_x16(acc + (static_cast<uint32_t>(warp * 32) << 16) + c, v);
             ptx::tmem_ld_wait();
+            const int row = warp * 32 + lane;
+            if constexpr (SWAP) {
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-                staged[(c + i) * C::PITCH + warp * 32 + lane] = __uint_as_float(v[i]);
+                for (int i = 0; i < 16; ++i) staged[(c + i) * C::PITCH + row] = __uint_as_float(v[i]);
+            } else {
+                const uint32_t at = ptx::smem_addr(staged + row * C::PITCH + c);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) ptx::st_shared_v4(at + 16 * i, v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+            }
         }
         ptx::tc_fence_before();
     }
@@ -176,24 +185,49 @@ __global__ void __launch_bounds__(T_THREADS) tile_kernel(const __grid_constant__
     if (failed) {
         if (threadIdx.x == 0 && p.status) atomicMax(p.status, 6u);
     } else {
+        // This CTA's share of the tile, four elements of a row of y at a time: 128/S of P's rows.
         const int share = T_ROWS / p.splits, r0 = rank * share;
+        const int width = (SWAP ? share : BN) / 4, height = SWAP ? q_valid : share;
         const uint32_t base = ptx::smem_addr(staged);
         T* y = static_cast<T*>(p.y);
-        for (int e = threadIdx.x; e < share * q_valid; e += T_THREADS) {
-            const int i = r0 + (SWAP ? e % share : e / q_valid), j = SWAP ? e / share : e % q_valid;
-            if (p0 + i >= p.p_rows) continue;
-            const uint32_t at = base + static_cast<uint32_t>(j * C::PITCH + i) * 4u;
-            float s;
-            if (p.splits == 1) {
-                s = staged[j * C::PITCH + i];
-            } else {
-                s = 0.f;
-                for (int k = 0; k < p.splits; ++k) s += ptx::ld_cluster_f32(ptx::mapa_shared(at, k));
+        for (int e = threadIdx.x; e < width * height; e += T_THREADS) {
+            const int h = e / width, w = 4 * (e - h * width);
+            const int sr = SWAP ? h : r0 + h, sc = SWAP ? r0 + w : w;  // row and column of the staged tile
+            const int64_t row = (SWAP ? q0 : p0) + sr;
+            const int col = (SWAP ? p0 : q0) + sc;
+            const int rows = SWAP ? p.q_rows : p.p_rows, cols = SWAP ? p.p_rows : p.q_rows;
+            if (row >= rows || col >= cols) continue;
+            const uint32_t at = base + static_cast<uint32_t>(sr * C::PITCH + sc) * 4u;
+            float4 s = ptx::ld_cluster_v4(ptx::mapa_shared(at, 0));
+#pragma unroll 7
+            for (int k = 1; k < p.splits; ++k) {
+                const float4 t = ptx::ld_cluster_v4(ptx::mapa_shared(at, k));
+                s.x += t.x;
+                s.y += t.y;
+                s.z += t.z;
+                s.w += t.w;
             }
-            const int64_t row = SWAP ? q0 + j : p0 + i, col = SWAP ? p0 + i : q0 + j;
-            if (p.bias) s += p.bias[col];
-            if (p.relu && s < 0.f) s = 0.f;
-            from_float(y[row * p.ldy + col], s);
+            float v[4] = {s.x, s.y, s.z, s.w};
+            const bool whole = col + 4 <= cols;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (p.bias && (whole || col + i < cols)) v[i] += __ldg(p.bias + col + i);
+                if (p.relu && v[i] < 0.f) v[i] = 0.f;
+            }
+            T* out = y + row * p.ldy + col;
+            if (whole && p.vec_y) {
+                if constexpr (sizeof(T) == 4) {
+                    *reinterpret_cast<float4*>(out) = make_float4(v[0], v[1], v[2], v[3]);
+                } else {
+                    const __nv_bfloat162 lo = __floats2bfloat162_rn(v[0], v[1]), hi = __floats2bfloat162_rn(v[2], v[3]);
+                    *reinterpret_cast<uint2*>(out) =
+                        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+                }
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (col + i < cols) from_float(out[i], v[i]);
+            }
         }
     }
     if (p.splits > 1) ptx::cluster_sync();  // the others have read this CTA's part

@@ -67,7 +67,7 @@ template <int BN, bool SWAP, typename T>
 int launch_tile(const Operand& P, const Operand& Q, TileParams& k, cudaStream_t stream)
 {
     static std::atomic<uint64_t> done{0};
-    using C = TileConfig<BN>;
+    using C = TileConfig<BN, SWAP>;
     CUtensorMap tm_p, tm_q;
     if (!encode(&tm_p, P.data, P.rows, k.blocks, T_ROWS) || !encode(&tm_q, Q.data, Q.rows, k.blocks, BN)) return CONV2D_ERR_CUDA;
     if (!allow_smem(tile_kernel<BN, SWAP, T>, C::SMEM, done)) return CONV2D_ERR_CUDA;
@@ -202,6 +202,7 @@ extern "C" int mxfp4_matmul(const mxfp4_matmul_params* params, const void* a_dat
     k.relu = act == CONV2D_ACT_RELU;
     k.y = y_dev;
     k.ldy = params->n;
+    k.vec_y = params->n % 4 == 0;
     void* status = nullptr;
     if (cudaGetSymbolAddress(&status, mx::product_status) != cudaSuccess) return CONV2D_ERR_CUDA;
     k.status = static_cast<uint32_t*>(status);
