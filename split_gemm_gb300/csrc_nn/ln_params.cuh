@@ -59,7 +59,7 @@ __host__ __device__ constexpr int bwd_resident(RowShape s)
     return s.elems == 8 && t <= 256 ? 640 / t : t >= 512 ? 1 : 512 / t;
 }
 
-constexpr int SMS = 152;
+constexpr int SMS = mx::SMS;
 
 // Launches by element types (one translation unit each); `vec`: rows can be read and written in vectors.
 // False: the row does not fit and nothing was launched.

@@ -5,11 +5,13 @@
 #include <cstdint>
 
 #include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 namespace sgb {
 namespace mx {
 
+constexpr int SMS = 152;           // of a GB300
 constexpr int BLOCK = 32;          // elements that share a scale
 constexpr int TILE_ROWS = 128;     // scale tile: 128 rows x 4 blocks = 512 bytes
 constexpr int TILE_BLOCKS = 4;
@@ -62,13 +64,20 @@ __device__ __forceinline__ uint32_t pack_e2m1x8(const float (&v)[8])
     return r;
 }
 
-// The value of one E2M1 code (0 .. 15).
-__device__ __forceinline__ float e2m1_value(uint32_t c)
+// The values of four bytes' eight E2M1 codes, the lowest first (exact: E2M1 values are fp16 numbers).
+__device__ __forceinline__ void unpack_e2m1x8(float2 (&v)[4], uint32_t word)
 {
-    const uint32_t e = (c >> 1) & 3u, m = c & 1u;
-    // e = 0: m/2; else (1 + m/2) * 2^(e-1)
-    const float a = e == 0u ? 0.5f * static_cast<float>(m) : __uint_as_float(((126u + e) << 23) | (m << 22));
-    return (c & 8u) ? -a : a;
+    uint32_t h[4];
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "mov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(word));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = __half22float2(*reinterpret_cast<const __half2*>(&h[i]));
 }
 
 __device__ __forceinline__ float to_float(float v) { return v; }

@@ -31,7 +31,7 @@ constexpr int W_STAGE = 2 * W_AB + W_SFA + W_SFB;      // 35 KB
 constexpr int W_EPI_WARPS = 8;
 constexpr int W_BOX = 32 * 128;                        // 32 rows of 128 bytes
 constexpr int W_THREADS = 32 * (2 + W_EPI_WARPS);
-constexpr int W_SMEM = W_STAGES * W_STAGE + W_EPI_WARPS * W_BOX + 1024 + 256;
+constexpr int W_SMEM = W_STAGES * W_STAGE + W_EPI_WARPS * (W_BOX + 512) + 1024 + 256;  // + each warp's bias, alignment, barriers
 constexpr int W_SF_COLS = 24;                          // of a slot: 2 x 4 for a, 2 x 8 for b
 static_assert(W_TILE + W_STAGES * W_SF_COLS <= 512, "tensor memory");
 static_assert(W_SMEM <= 232448 && W_STAGE % 1024 == 0, "shared memory");
@@ -66,7 +66,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
     extern __shared__ uint8_t raw[];
     uint8_t* ring = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     uint8_t* boxes = ring + W_STAGES * W_STAGE;
-    uint64_t* full = reinterpret_cast<uint64_t*>(boxes + W_EPI_WARPS * W_BOX);
+    float* biases = reinterpret_cast<float*>(boxes + W_EPI_WARPS * W_BOX);
+    uint64_t* full = reinterpret_cast<uint64_t*>(biases + W_EPI_WARPS * 128);
     uint64_t* empty = full + W_STAGES;
     uint64_t* acc_full = empty + W_STAGES;
     uint64_t* acc_empty = acc_full + 1;
@@ -157,6 +158,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
         for (int tile = cluster; tile < tiles && !*abort_flag; tile += clusters, ++n) {
             int tm, tn;
             tile_of(tile, p, tm, tn);
+            const int row0 = tm * W_TILE + static_cast<int>(rank) * W_ROWS + quad * 32, col0 = tn * W_TILE + half * 128;
+            if (p.bias) {  // this warp's 128 columns, while the MMAs run
+                __syncwarp();
+                float* mine = biases + (warp - 2) * 128;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int c = lane + 32 * i;
+                    mine[c] = col0 + c < p.n ? __ldg(p.bias + col0 + c) : 0.f;
+                }
+                __syncwarp();
+            }
             if (!ptx::mbar_wait(acc_full, static_cast<uint32_t>(n) & 1u, 2 * T_WAIT_NS)) {
                 *abort_flag = 1u;
                 break;
@@ -170,15 +182,18 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
             ptx::tc_fence_before();
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive_cluster(release);
-            const int row0 = tm * W_TILE + static_cast<int>(rank) * W_ROWS + quad * 32, col0 = tn * W_TILE + half * 128;
             if (row0 >= p.m || col0 >= p.n) continue;
             if (p.bias) {
+                const float4* mine = reinterpret_cast<const float4*>(biases + (warp - 2) * 128);
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
 #pragma unroll
-                    for (int i = 0; i < 32; ++i) {
-                        const int col = col0 + c * 32 + i;
-                        v[c][i] = __float_as_uint(__uint_as_float(v[c][i]) + (col < p.n ? __ldg(p.bias + col) : 0.f));
+                    for (int i = 0; i < 8; ++i) {
+                        const float4 b = mine[c * 8 + i];
+                        v[c][4 * i] = __float_as_uint(__uint_as_float(v[c][4 * i]) + b.x);
+                        v[c][4 * i + 1] = __float_as_uint(__uint_as_float(v[c][4 * i + 1]) + b.y);
+                        v[c][4 * i + 2] = __float_as_uint(__uint_as_float(v[c][4 * i + 2]) + b.z);
+                        v[c][4 * i + 3] = __float_as_uint(__uint_as_float(v[c][4 * i + 3]) + b.w);
                     }
             }
             if (p.relu) {

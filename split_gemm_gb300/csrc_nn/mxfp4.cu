@@ -16,78 +16,239 @@ struct QuantParams {
     uint8_t *data, *scales, *data_t, *scales_t;
 };
 
-// A block of threads takes a tile of 128 x 128 elements, which is one scale tile
-// of either form.  A warp quantises one block of 32 at a time, a lane to an element.
+// A block of threads takes a tile of 128 x 128 elements, which is one scale tile of either form, through shared memory, so
+// that both forms come from one reading of x.  A thread quantises 8 neighbouring elements of a row (4 or 8 of them make
+// a block's 32), or 32 elements of one column (two columns where x is bf16, which come as one word); what it makes is
+// gathered in shared memory and leaves in whole rows: 64 bytes of data, 512 bytes of scales.  Bound by HBM: x is read
+// once and 17/32 of a byte written for each element of each form.
 constexpr int Q_TILE = 128;
 constexpr int Q_THREADS = 256;
 
-// Quantises the lanes' values as one block: returns the block's scale byte in
-// every lane and, in lanes 0..3, the words of its 16 bytes.
-__device__ __forceinline__ uint32_t quantize_warp(float v, uint32_t& word)
-{
-    const int lane = threadIdx.x & 31;
-    const uint32_t byte = scale_byte(__reduce_max_sync(0xffffffffu, abs_bits(v)));
-    const float q = v * inverse_scale(byte);
-    float e[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) e[j] = __shfl_sync(0xffffffffu, q, 8 * (lane & 3) + j);
-    word = pack_e2m1x8(e);
-    return byte;
-}
-
 template <typename T>
-__global__ void __launch_bounds__(Q_THREADS) quantize_kernel(const T* x, const QuantParams p)
+struct alignas(16) QuantTile {
+    T x[Q_TILE][Q_TILE];
+    uint8_t out[Q_TILE * Q_TILE / 2];  // [row or column][64 bytes], see out_at
+    uint8_t scales[TILE_BYTES];
+};
+
+// Where block q of line l is gathered: lines by twos in 128 bytes, whose eight 16-byte units are permuted by the
+// line so that threads with lines in turn write to different banks.
+__device__ __forceinline__ int out_at(int l, int q) { return (l >> 1) * 128 + ((((l & 1) * 4 + q) ^ ((l >> 1) & 7)) << 4); }
+
+// Largest absolute value's bits of 32 values in a register, as fp32 bits; bf16 pairs are compared as pairs.
+__device__ __forceinline__ uint32_t join_max(uint32_t m, uint32_t v, float) { return max(m, v & 0x7fffffffu); }
+__device__ __forceinline__ uint32_t join_max(uint32_t m, uint32_t v, __nv_bfloat16) { return __vmaxu2(m, v & 0x7fff7fffu); }
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(Q_THREADS) quantize_kernel(const T* __restrict__ x, const QuantParams p)
 {
-    __shared__ float tile[Q_TILE][33];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t rb = blockIdx.x / p.col_tiles, cb = blockIdx.x % p.col_tiles;
-    const int64_t row_blocks = cdiv<int64_t>(p.rows, BLOCK), col_blocks = cdiv<int64_t>(p.cols, BLOCK);
-    for (int b = 0; b < TILE_BLOCKS; ++b) {  // 32 columns at a time
-        const int64_t kb = cb * TILE_BLOCKS + b;
-        const int64_t c = kb * BLOCK + lane;
-        for (int i = warp; i < Q_TILE; i += Q_THREADS / 32) {
-            const int64_t r = rb * Q_TILE + i;
-            const float v = r < p.rows && c < p.cols ? to_float(x[r * p.x_stride + c]) : 0.f;
-            tile[i][lane] = v;
-            if (!p.data) continue;
-            uint32_t word;
-            const uint32_t byte = quantize_warp(v, word);
-            if (lane == 0) p.scales[scale_at(r, kb, p.col_tiles)] = static_cast<uint8_t>(byte);
-            if (r < p.rows && kb < col_blocks && lane < 4)
-                *reinterpret_cast<uint32_t*>(p.data + (r * col_blocks + kb) * 16 + 4 * lane) = word;
+    extern __shared__ uint8_t raw[];
+    QuantTile<T>& s = *reinterpret_cast<QuantTile<T>*>(raw);
+    const int64_t rb = blockIdx.x / p.col_tiles, cb = blockIdx.x - rb * p.col_tiles;
+    const int64_t r0 = rb * Q_TILE, c0 = cb * Q_TILE;
+    const int rows = static_cast<int>(p.rows - r0 < Q_TILE ? p.rows - r0 : Q_TILE);
+    const int cols = static_cast<int>(p.cols - c0 < Q_TILE ? p.cols - c0 : Q_TILE);
+    const T* src = x + r0 * p.x_stride + c0;
+    if constexpr (VEC) {
+        constexpr int V = 16 / sizeof(T), PER = Q_TILE / V, STEP = Q_THREADS / PER;
+        const int c = threadIdx.x % PER * V;
+        uint4 v[Q_TILE / STEP];
+#pragma unroll
+        for (int i = 0; i < Q_TILE / STEP; ++i) {
+            const int r = threadIdx.x / PER + i * STEP;
+            v[i] = r < rows && c < cols ? __ldg(reinterpret_cast<const uint4*>(src + r * p.x_stride + c)) : make_uint4(0, 0, 0, 0);
         }
+#pragma unroll
+        for (int i = 0; i < Q_TILE / STEP; ++i) *reinterpret_cast<uint4*>(&s.x[threadIdx.x / PER + i * STEP][c]) = v[i];
+    } else {
+        const int c = threadIdx.x % Q_TILE;
+#pragma unroll 16
+        for (int r = threadIdx.x / Q_TILE; r < Q_TILE; r += Q_THREADS / Q_TILE)
+            s.x[r][c] = r < rows && c < cols ? src[r * p.x_stride + c] : T(0.f);
+    }
+    __syncthreads();
+
+    const int64_t row_blocks = cdiv<int64_t>(p.rows, BLOCK), col_blocks = cdiv<int64_t>(p.cols, BLOCK);
+    // Copies the gathered lines of `n` rows (of the form's matrix) and the scale tile; `left` blocks of a line exist.
+    auto flush = [&](uint8_t* data, uint8_t* scales, int64_t line0, int n, int64_t pitch, int64_t block0, int64_t left, int64_t tile) {
         __syncthreads();
-        if (p.data_t) {
-            for (int i = warp; i < 32 * TILE_BLOCKS; i += Q_THREADS / 32) {
-                const int col = i & 31, g = i >> 5;
-                uint32_t word;
-                const uint32_t byte = quantize_warp(tile[g * BLOCK + lane][col], word);
-                const int64_t r = kb * BLOCK + col, k = rb * TILE_BLOCKS + g;  // row and block of the transpose
-                if (lane == 0) p.scales_t[scale_at(r, k, p.row_tiles)] = static_cast<uint8_t>(byte);
-                if (r < p.cols && k < row_blocks && lane < 4)
-                    *reinterpret_cast<uint32_t*>(p.data_t + (r * row_blocks + k) * 16 + 4 * lane) = word;
+        const int q = threadIdx.x % TILE_BLOCKS;
+        for (int l = threadIdx.x / TILE_BLOCKS; l < n; l += Q_THREADS / TILE_BLOCKS)
+            if (q < left)
+                *reinterpret_cast<uint4*>(data + ((line0 + l) * pitch + block0 + q) * 16) =
+                    *reinterpret_cast<const uint4*>(s.out + out_at(l, q));
+        if (threadIdx.x < TILE_BYTES / 16)
+            reinterpret_cast<uint4*>(scales + tile * TILE_BYTES)[threadIdx.x] = reinterpret_cast<const uint4*>(s.scales)[threadIdx.x];
+    };
+
+    if (p.data) {
+        const int lane = threadIdx.x % 16, c = 8 * lane;
+#pragma unroll
+        for (int i = 0; i < Q_TILE / 16; ++i) {
+            const int r = threadIdx.x / 16 + 16 * i;
+            float v[8];
+            uint32_t m = 0;
+            if constexpr (sizeof(T) == 2) {
+                const uint4 w = *reinterpret_cast<const uint4*>(&s.x[r][c]);
+                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    m = join_max(m, u[j], T());
+                    v[2 * j] = __uint_as_float(u[j] << 16);
+                    v[2 * j + 1] = __uint_as_float(u[j] & 0xffff0000u);
+                }
+                m = max(m << 16, m & 0xffff0000u);
+            } else {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    v[j] = s.x[r][c + j];
+                    m = max(m, abs_bits(v[j]));
+                }
+            }
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+            m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+            const uint32_t byte = scale_byte(m);
+            const float inv = inverse_scale(byte);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) v[j] *= inv;
+            *reinterpret_cast<uint32_t*>(s.out + out_at(r, lane / 4) + 4 * (lane % 4)) = pack_e2m1x8(v);
+            if (lane % 4 == 0) s.scales[(r % 32) * 16 + r / 32 * 4 + lane / 4] = static_cast<uint8_t>(byte);
+        }
+        flush(p.data, p.scales, r0, rows, col_blocks, cb * TILE_BLOCKS, col_blocks - cb * TILE_BLOCKS, rb * p.col_tiles + cb);
+        __syncthreads();
+    }
+    if (p.data_t) {
+        constexpr int PAIR = 4 / sizeof(T);  // columns in a word
+        constexpr int WORDS = Q_TILE / PAIR;
+        for (int u = threadIdx.x; u < WORDS * TILE_BLOCKS; u += Q_THREADS) {
+            const int w = u % WORDS, g = u / WORDS;
+            uint32_t v[BLOCK], m = 0;
+#pragma unroll
+            for (int i = 0; i < BLOCK; ++i) {
+                v[i] = reinterpret_cast<const uint32_t*>(&s.x[g * BLOCK + i][0])[w];
+                m = join_max(m, v[i], T());
+            }
+#pragma unroll
+            for (int h = 0; h < PAIR; ++h) {
+                const int c = w * PAIR + h;
+                const uint32_t byte = scale_byte(PAIR == 1 ? m : h ? m & 0xffff0000u : m << 16);
+                const float inv = inverse_scale(byte);
+                uint32_t o[4];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    float f[8];
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const uint32_t b = v[8 * q + j];
+                        f[j] = __uint_as_float(PAIR == 1 ? b : h ? b & 0xffff0000u : b << 16) * inv;
+                    }
+                    o[q] = pack_e2m1x8(f);
+                }
+                *reinterpret_cast<uint4*>(s.out + out_at(c, g)) = make_uint4(o[0], o[1], o[2], o[3]);
+                s.scales[(c % 32) * 16 + c / 32 * 4 + g] = static_cast<uint8_t>(byte);
             }
         }
-        __syncthreads();
+        flush(p.data_t, p.scales_t, c0, cols, row_blocks, rb * TILE_BLOCKS, row_blocks - rb * TILE_BLOCKS, cb * p.row_tiles + rb);
     }
 }
 
-// A thread takes 8 elements: 4 bytes in, 16 or 32 out.
-template <typename T>
-__global__ void __launch_bounds__(256) dequantize_kernel(const uint8_t* data, const uint8_t* scales, T* y, int64_t rows,
-                                                         int64_t cols)
+// A thread takes 8 elements: 4 bytes in, 16 or 32 out (in one or two 16-byte stores where rows are whole vectors; else a
+// warp's 256 elements go through shared memory and leave element by element in order).
+constexpr int D_THREADS = 256;
+
+template <typename T, bool VEC>
+__global__ void __launch_bounds__(D_THREADS) dequantize_kernel(const uint8_t* __restrict__ data, const uint8_t* __restrict__ scales, T* y,
+                                                               int64_t rows, int64_t cols)
 {
+    __shared__ float gather[VEC ? 1 : D_THREADS][9];
     const int64_t blocks = cdiv<int64_t>(cols, BLOCK), btiles = cdiv<int64_t>(blocks, TILE_BLOCKS);
-    const int64_t n = rows * blocks * 4;
-    for (int64_t i = blockIdx.x * int64_t(blockDim.x) + threadIdx.x; i < n; i += int64_t(gridDim.x) * blockDim.x) {
-        const int64_t r = i / (blocks * 4), w = i - r * (blocks * 4);
-        const uint32_t word = reinterpret_cast<const uint32_t*>(data)[i];
-        const float s = scale_value(scales[scale_at(r, w >> 2, btiles)]);
-        for (int j = 0; j < 8; ++j) {
-            const int64_t c = w * 8 + j;
-            if (c < cols) from_float(y[r * cols + c], e2m1_value(word >> (4 * j) & 15u) * s);
+    const int64_t words = blocks * 4, n = rows * words;
+    const int64_t step = int64_t(gridDim.x) * D_THREADS;
+    const int64_t step_r = step / words, step_w = step - step_r * words;
+    const int64_t i0 = int64_t(blockIdx.x) * D_THREADS + threadIdx.x;
+    int64_t r = i0 / words, w = i0 - r * words;
+    const int lane = threadIdx.x & 31;
+    for (int64_t i = i0; i - lane < n; i += step) {  // a warp's lanes stay together
+        float2 v[4];
+        if (i < n) {
+            const uint32_t word = __ldg(reinterpret_cast<const uint32_t*>(data) + i);
+            const float s = scale_value(__ldg(scales + scale_at(r, w >> 2, btiles)));
+            unpack_e2m1x8(v, word);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = make_float2(v[j].x * s, v[j].y * s);
+        }
+        if constexpr (VEC) {
+            if (i < n && w * 8 < cols) {
+                T* out = y + r * cols + w * 8;
+                if constexpr (sizeof(T) == 4) {
+                    reinterpret_cast<float4*>(out)[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+                    reinterpret_cast<float4*>(out)[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+                } else {
+                    uint32_t o[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(v[j].x, v[j].y);
+                        o[j] = *reinterpret_cast<const uint32_t*>(&h);
+                    }
+                    *reinterpret_cast<uint4*>(out) = make_uint4(o[0], o[1], o[2], o[3]);
+                }
+            }
+        } else {
+            float(*mine)[9] = gather + (threadIdx.x & ~31);
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                mine[lane][2 * j] = v[j].x;
+                mine[lane][2 * j + 1] = v[j].y;
+            }
+            __syncwarp();
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int from = 4 * k + lane / 8;  // the thread whose element this is
+                const int64_t fr = __shfl_sync(0xffffffffu, r, from), fw = __shfl_sync(0xffffffffu, w, from);
+                const int64_t c = fw * 8 + lane % 8;
+                if (fr < rows && c < cols) from_float(y[fr * cols + c], mine[from][lane % 8]);
+            }
+        }
+        r += step_r;
+        w += step_w;
+        if (w >= words) {
+            w -= words;
+            ++r;
         }
     }
+}
+
+// Sets the kernel's shared-memory limit and launches one block to a tile.
+template <typename T, bool VEC>
+int launch_quantize(const T* x, const QuantParams& p, cudaStream_t stream)
+{
+    constexpr int smem = sizeof(QuantTile<T>);
+    if (smem > 48 * 1024 && cudaFuncSetAttribute(quantize_kernel<T, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
+        return CONV2D_ERR_CUDA;
+    quantize_kernel<T, VEC><<<static_cast<unsigned>(p.row_tiles * p.col_tiles), Q_THREADS, smem, stream>>>(x, p);
+    return cudaGetLastError() == cudaSuccess ? CONV2D_OK : CONV2D_ERR_CUDA;
+}
+
+template <typename T>
+int quantize(const void* x, const QuantParams& p, cudaStream_t stream)
+{
+    constexpr int V = 16 / sizeof(T);
+    const bool vec = p.cols % V == 0 && p.x_stride % V == 0 && reinterpret_cast<uintptr_t>(x) % 16 == 0;
+    return vec ? launch_quantize<T, true>(static_cast<const T*>(x), p, stream) : launch_quantize<T, false>(static_cast<const T*>(x), p, stream);
+}
+
+template <typename T>
+int dequantize(const uint8_t* data, const uint8_t* scales, void* y, int64_t rows, int64_t cols, cudaStream_t stream)
+{
+    // Eight blocks to an SM at most: they stay, and take one group after another.
+    const int64_t need = cdiv<int64_t>(rows * cdiv<int64_t>(cols, BLOCK) * 4, D_THREADS);
+    const unsigned grid = static_cast<unsigned>(need < SMS * 8 ? need : SMS * 8);
+    if (cols % 8 == 0)
+        dequantize_kernel<T, true><<<grid, D_THREADS, 0, stream>>>(data, scales, static_cast<T*>(y), rows, cols);
+    else
+        dequantize_kernel<T, false><<<grid, D_THREADS, 0, stream>>>(data, scales, static_cast<T*>(y), rows, cols);
+    return cudaGetLastError() == cudaSuccess ? CONV2D_OK : CONV2D_ERR_CUDA;
 }
 
 }  // namespace mx
@@ -134,11 +295,7 @@ extern "C" int mxfp4_quantize(int64_t rows, int64_t cols, const void* x_dev, int
     k.scales_t = static_cast<uint8_t*>(scales_t_dev);
     const int64_t grid = k.row_tiles * k.col_tiles;
     if (grid > mx::MAX_EXTENT) return CONV2D_ERR_UNSUPPORTED;
-    if (x_dtype == CONV2D_OUT_BF16)
-        mx::quantize_kernel<<<static_cast<unsigned>(grid), mx::Q_THREADS, 0, stream>>>(static_cast<const __nv_bfloat16*>(x_dev), k);
-    else
-        mx::quantize_kernel<<<static_cast<unsigned>(grid), mx::Q_THREADS, 0, stream>>>(static_cast<const float*>(x_dev), k);
-    return cudaGetLastError() == cudaSuccess ? CONV2D_OK : CONV2D_ERR_CUDA;
+    return x_dtype == CONV2D_OUT_BF16 ? mx::quantize<__nv_bfloat16>(x_dev, k, stream) : mx::quantize<float>(x_dev, k, stream);
 }
 
 extern "C" int mxfp4_dequantize(int64_t rows, int64_t cols, const void* data_dev, const void* scales_dev, void* y_dev,
@@ -151,12 +308,7 @@ extern "C" int mxfp4_dequantize(int64_t rows, int64_t cols, const void* data_dev
     if (reinterpret_cast<uintptr_t>(data_dev) % 16 || reinterpret_cast<uintptr_t>(scales_dev) % 16 ||
         reinterpret_cast<uintptr_t>(y_dev) % 16)
         return CONV2D_ERR_ALIGNMENT;
-    const int64_t n = rows * mx::cdiv<int64_t>(cols, mx::BLOCK) * 4;
-    const unsigned grid = static_cast<unsigned>(mx::cdiv<int64_t>(n, 256) < 152 * 64 ? mx::cdiv<int64_t>(n, 256) : 152 * 64);
     const uint8_t *d = static_cast<const uint8_t*>(data_dev), *s = static_cast<const uint8_t*>(scales_dev);
-    if (y_dtype == CONV2D_OUT_BF16)
-        mx::dequantize_kernel<<<grid, 256, 0, stream>>>(d, s, static_cast<__nv_bfloat16*>(y_dev), rows, cols);
-    else
-        mx::dequantize_kernel<<<grid, 256, 0, stream>>>(d, s, static_cast<float*>(y_dev), rows, cols);
-    return cudaGetLastError() == cudaSuccess ? CONV2D_OK : CONV2D_ERR_CUDA;
+    return y_dtype == CONV2D_OUT_BF16 ? mx::dequantize<__nv_bfloat16>(d, s, y_dev, rows, cols, stream)
+                                      : mx::dequantize<float>(d, s, y_dev, rows, cols, stream);
 }

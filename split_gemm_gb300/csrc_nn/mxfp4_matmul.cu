@@ -11,8 +11,6 @@
 namespace sgb {
 namespace mx {
 
-constexpr int SMS = 152;
-
 
 std::once_flag encode_once;
 PFN_cuTensorMapEncodeTiled_v12000 encode_tiled = nullptr;
