@@ -1,14 +1,26 @@
-"""What the row operators (layer normalisation, 4-bit matrices) share: argument checks and streams."""
+"""What the row operators (layer normalisation, 4-bit matrices) share: argument checks, streams and the library.
+
+The checks are written for their cost: a decoding step's calls take a few microseconds each, so the usual case is
+decided by few attribute reads and what is wrong is named only once something is.
+"""
 from __future__ import annotations
 
-import contextlib
 from typing import Optional, Tuple
 
 import torch
 
-from . import OUT_BF16, OUT_F32
+from . import OUT_BF16, OUT_F32, load_library
 
 DTYPE_CODES = {torch.float32: OUT_F32, torch.bfloat16: OUT_BF16}
+_lib = None
+
+
+def library():
+    """The loaded library, looked up without load_library's lock after the first call."""
+    global _lib
+    if _lib is None:
+        _lib = load_library()
+    return _lib
 
 
 def rows_of(t, name) -> Tuple[int, int, int]:
@@ -52,13 +64,18 @@ def check_vector(t, name, n, like) -> Optional[int]:
         return None
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device != like.device:
+    if t.get_device() != like.get_device():
         raise ValueError(f"{name} must be a CUDA tensor on {like.device}")
     if t.dtype != torch.float32:
         raise TypeError(f"{name} must be torch.float32, got {t.dtype}")
     if t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous with {n} elements")
     return t.data_ptr()
+
+
+def same_device(t, name, like) -> None:
+    if t.get_device() != like.get_device():
+        raise ValueError(f"{name} must be a CUDA tensor on {like.device}")
 
 
 def check_out_dtype(dtype) -> int:
@@ -68,11 +85,15 @@ def check_out_dtype(dtype) -> int:
     return code
 
 
-def stream_of(t, stream):
-    return torch.cuda.current_stream(t.device) if stream is None else stream
+def stream_handle(t, stream) -> int:
+    """cudaStream_t of ``stream`` (None: the current stream of t's device)."""
+    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
 
 
-def allocating_on(stream):
-    """Context in which new tensors belong to ``stream`` (None: the current one), so that their
-    memory is neither taken from nor given back to work of another stream."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+def empty_on(stream, shape, dtype, device):
+    """A new tensor that belongs to ``stream`` (None: the current one), so that its memory is neither taken
+    from nor given back to work of another stream."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)

@@ -18,8 +18,8 @@ from typing import NamedTuple, Tuple
 
 import torch
 
-from . import ACT_NONE, ACT_RELU, Conv2dError, Epilogue, Mxfp4MatmulParams, load_library
-from ._rows import DTYPE_CODES, allocating_on, check_out_dtype, check_vector, rows_of, stream_of
+from . import ACT_NONE, ACT_RELU, Conv2dError, Epilogue, Mxfp4MatmulParams
+from ._rows import DTYPE_CODES, check_out_dtype, check_vector, empty_on, library, rows_of, same_device, stream_handle
 
 
 class Mxfp4(NamedTuple):
@@ -38,116 +38,135 @@ class Mxfp4(NamedTuple):
 def mxfp4_empty(rows: int, cols: int, device, *, stream=None) -> Mxfp4:
     """An unwritten quantised matrix, for mxfp4_quantize_into."""
     blocks = (cols + 31) // 32
-    with allocating_on(stream):
-        data = torch.empty((rows, 16 * blocks), dtype=torch.uint8, device=device)
-        scales = torch.empty((rows + 127) // 128 * ((blocks + 3) // 4) * 512, dtype=torch.uint8, device=device)
+    data = empty_on(stream, (rows, 16 * blocks), torch.uint8, device)
+    scales = empty_on(stream, ((rows + 127) // 128 * ((blocks + 3) // 4) * 512,), torch.uint8, device)
     return Mxfp4(data, scales, rows, cols)
 
 
-def _check_mx(q, name) -> None:
+def _check_mx(q, name) -> Tuple[int, int]:
+    """The device pointers of a quantised matrix's data and scales."""
     if not isinstance(q, Mxfp4):
         raise TypeError(f"{name} must be an Mxfp4")
     data, scales, rows, cols = q
-    blocks = (cols + 31) // 32
     if data.dtype != torch.uint8 or scales.dtype != torch.uint8:
         raise TypeError(f"{name}.data and {name}.scales must be torch.uint8")
-    if not data.is_cuda or not scales.is_cuda:
-        raise ValueError(f"{name}.data and {name}.scales must be CUDA tensors")
+    if not data.is_cuda or scales.get_device() != data.get_device():
+        raise ValueError(f"{name}.data and {name}.scales must be CUDA tensors of one device")
+    blocks = (cols + 31) // 32
     if data.numel() != rows * 16 * blocks or scales.numel() != (rows + 127) // 128 * ((blocks + 3) // 4) * 512:
         raise ValueError(f"{name}.data or {name}.scales has the wrong size for {rows} x {cols}")
     if not data.is_contiguous() or not scales.is_contiguous():
         raise ValueError(f"{name}.data and {name}.scales must be contiguous")
+    return data.data_ptr(), scales.data_ptr()
+
+
+def _quantize(x, layout, ptr, ptr_t, stream) -> None:
+    rows, cols, x_stride = layout
+    if rows == 0:
+        return
+    rc = library().mxfp4_quantize(rows, cols, x.data_ptr(), DTYPE_CODES[x.dtype], x_stride, *ptr, *ptr_t, stream_handle(x, stream))
+    if rc:
+        raise Conv2dError(rc, "mxfp4_quantize")
+
+
+_NOT_WANTED = (None, None)
 
 
 def mxfp4_quantize_into(q, x, q_t=None, *, stream=None) -> None:
     """Quantises x [..., C], seen as [rows, C], into ``q`` (None: not wanted) and its transpose into ``q_t``."""
     rows, cols, x_stride = rows_of(x, "x")
-    ptr = [None] * 4
+    ptr = ptr_t = _NOT_WANTED
     if q is not None:
-        _check_mx(q, "q")
+        ptr = _check_mx(q, "q")
         if (q.rows, q.cols) != (rows, cols):
             raise ValueError(f"q must be {rows} x {cols}, got {q.rows} x {q.cols}")
-        ptr[:2] = q.data.data_ptr(), q.scales.data_ptr()
+        same_device(q.data, "q", x)
     if q_t is not None:
-        _check_mx(q_t, "q_t")
+        ptr_t = _check_mx(q_t, "q_t")
         if (q_t.rows, q_t.cols) != (cols, rows):
             raise ValueError(f"q_t must be {cols} x {rows}, got {q_t.rows} x {q_t.cols}")
-        ptr[2:] = q_t.data.data_ptr(), q_t.scales.data_ptr()
-    if rows == 0:
-        return
-    rc = load_library().mxfp4_quantize(rows, cols, x.data_ptr(), DTYPE_CODES[x.dtype], x_stride, *ptr,
-                                       stream_of(x, stream).cuda_stream)
-    if rc:
-        raise Conv2dError(rc, "mxfp4_quantize")
+        same_device(q_t.data, "q_t", x)
+    _quantize(x, (rows, cols, x_stride), ptr, ptr_t, stream)
+
+
+def _new(rows, cols, device, stream):
+    q = mxfp4_empty(rows, cols, device, stream=stream)
+    return q, (q.data.data_ptr(), q.scales.data_ptr())
 
 
 def mxfp4_quantize(x, *, transpose: bool = False, stream=None) -> Mxfp4:
     """Quantises x [..., C] (bf16 or fp32), seen as [rows, C]; with ``transpose`` the result is [C, rows], in blocks
     along x's columns."""
-    rows, cols, _ = rows_of(x, "x")
+    rows, cols, x_stride = rows_of(x, "x")
     if transpose:
-        q = mxfp4_empty(cols, rows, x.device, stream=stream)
-        mxfp4_quantize_into(None, x, q, stream=stream)
+        q, ptr_t = _new(cols, rows, x.device, stream)
+        _quantize(x, (rows, cols, x_stride), _NOT_WANTED, ptr_t, stream)
     else:
-        q = mxfp4_empty(rows, cols, x.device, stream=stream)
-        mxfp4_quantize_into(q, x, stream=stream)
+        q, ptr = _new(rows, cols, x.device, stream)
+        _quantize(x, (rows, cols, x_stride), ptr, _NOT_WANTED, stream)
     return q
 
 
 def mxfp4_quantize_both(x, *, stream=None) -> Tuple[Mxfp4, Mxfp4]:
     """(mxfp4_quantize(x), mxfp4_quantize(x, transpose=True)) from one reading of x."""
-    rows, cols, _ = rows_of(x, "x")
-    q = mxfp4_empty(rows, cols, x.device, stream=stream)
-    q_t = mxfp4_empty(cols, rows, x.device, stream=stream)
-    mxfp4_quantize_into(q, x, q_t, stream=stream)
+    rows, cols, x_stride = rows_of(x, "x")
+    q, ptr = _new(rows, cols, x.device, stream)
+    q_t, ptr_t = _new(cols, rows, x.device, stream)
+    _quantize(x, (rows, cols, x_stride), ptr, ptr_t, stream)
     return q, q_t
 
 
 def mxfp4_dequantize(q: Mxfp4, *, out_dtype=torch.bfloat16, stream=None):
     """The values that q stands for, [rows, cols] bf16 or fp32 (exact in either)."""
-    _check_mx(q, "q")
+    data, scales = _check_mx(q, "q")
     code = check_out_dtype(out_dtype)
-    with allocating_on(stream):
-        y = torch.empty((q.rows, q.cols), dtype=out_dtype, device=q.data.device)
+    y = empty_on(stream, (q.rows, q.cols), out_dtype, q.data.device)
     if q.rows == 0:
         return y
-    rc = load_library().mxfp4_dequantize(q.rows, q.cols, q.data.data_ptr(), q.scales.data_ptr(), y.data_ptr(), code,
-                                         stream_of(q.data, stream).cuda_stream)
+    rc = library().mxfp4_dequantize(q.rows, q.cols, data, scales, y.data_ptr(), code, stream_handle(q.data, stream))
     if rc:
         raise Conv2dError(rc, "mxfp4_dequantize")
     return y
 
 
-def mxfp4_matmul_into(y, a: Mxfp4, b: Mxfp4, bias=None, *, relu: bool = False, stream=None) -> None:
-    """Writes a b^T + bias (ReLU after the bias with ``relu``; NaN stays NaN) into the contiguous y [a.rows, b.rows],
-    fp32 or bf16.  ``bias``: [b.rows] fp32 or None."""
-    _check_mx(a, "a")
-    _check_mx(b, "b")
+def _operands(a, b):
+    pa, pb = _check_mx(a, "a"), _check_mx(b, "b")
     if a.cols != b.cols:
         raise ValueError(f"a has {a.cols} columns, b has {b.cols}")
-    if not y.is_cuda or not y.is_contiguous() or y.numel() != a.rows * b.rows:
-        raise ValueError(f"y must be a contiguous CUDA tensor of {a.rows} x {b.rows}")
-    epi = Epilogue(ACT_RELU if relu else ACT_NONE, check_out_dtype(y.dtype))
+    same_device(b.data, "b", a.data)
+    return pa + pb
+
+
+def _matmul(y, ptrs, a, b, bias, relu, stream) -> None:
+    epi = Epilogue(ACT_RELU if relu else ACT_NONE, DTYPE_CODES[y.dtype])
     params = Mxfp4MatmulParams(a.rows, b.rows, a.cols)
-    rc = load_library().mxfp4_matmul(ctypes.byref(params), a.data.data_ptr(), a.scales.data_ptr(), b.data.data_ptr(),
-                                     b.scales.data_ptr(), check_vector(bias, "bias", b.rows, a.data), y.data_ptr(),
-                                     ctypes.byref(epi), stream_of(a.data, stream).cuda_stream)
+    rc = library().mxfp4_matmul(ctypes.byref(params), *ptrs, check_vector(bias, "bias", b.rows, a.data), y.data_ptr(),
+                                ctypes.byref(epi), stream_handle(a.data, stream))
     if rc:
         raise Conv2dError(rc, "mxfp4_matmul")
 
 
+def mxfp4_matmul_into(y, a: Mxfp4, b: Mxfp4, bias=None, *, relu: bool = False, stream=None) -> None:
+    """Writes a b^T + bias (ReLU after the bias with ``relu``; NaN stays NaN) into the contiguous y [a.rows, b.rows],
+    fp32 or bf16.  ``bias``: [b.rows] fp32 or None."""
+    ptrs = _operands(a, b)
+    check_out_dtype(y.dtype)
+    if not y.is_cuda or not y.is_contiguous() or y.numel() != a.rows * b.rows:
+        raise ValueError(f"y must be a contiguous CUDA tensor of {a.rows} x {b.rows}")
+    same_device(y, "y", a.data)
+    _matmul(y, ptrs, a, b, bias, relu, stream)
+
+
 def mxfp4_matmul(a: Mxfp4, b: Mxfp4, bias=None, *, relu: bool = False, out_dtype=torch.float32, stream=None):
     """Returns a b^T + bias as a new [a.rows, b.rows] tensor of ``out_dtype`` (asynchronous)."""
-    _check_mx(a, "a")
-    _check_mx(b, "b")
+    ptrs = _operands(a, b)
     check_out_dtype(out_dtype)
-    with allocating_on(stream):
-        y = torch.empty((a.rows, b.rows), dtype=out_dtype, device=a.data.device)
-    mxfp4_matmul_into(y, a, b, bias, relu=relu, stream=stream)
+    y = empty_on(stream, (a.rows, b.rows), out_dtype, a.data.device)
+    _matmul(y, ptrs, a, b, bias, relu, stream)
     return y
 
 
 def mxfp4_matmul_status(stream=None) -> int:
     """Synchronises the stream; 0, or CONV2D_ERR_TIMEOUT if a device-side wait of a product ran out since last asked."""
     st = torch.cuda.current_stream() if stream is None else stream
-    return int(load_library().mxfp4_matmul_status(st.cuda_stream))
+    return int(library().mxfp4_matmul_status(st.cuda_stream))
