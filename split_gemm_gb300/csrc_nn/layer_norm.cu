@@ -62,23 +62,32 @@ void by_types(int32_t x, int32_t y, F&& f)
 constexpr int64_t PART_ROWS = 64;     // rows too wide for registers: of one part, at least
 constexpr int64_t PART_CHUNKS = 512;  // and parts, at most
 
-int64_t bwd_parts(int64_t rows, int64_t cols)
+// Columns that the threads of a row have to hold: where rows do not start at whole vectors, up to 7 elements
+// stand in front of them.
+int64_t span_of(const layer_norm_params* p)
 {
-    const RowShape s = row_shape(cols);
-    if (s.threads == 0 || s.threads > 512) {
-        const int64_t n = mx::cdiv(rows, PART_ROWS);
-        return n < PART_CHUNKS ? n : PART_CHUNKS;
-    }
-    const int64_t most = SMS * bwd_resident(s);
-    const int64_t n = mx::cdiv<int64_t>(rows, rows_per_block(s));
-    return n < most ? n : most;
+    return (p->cols | p->x_stride | p->y_stride) % 8 == 0 ? p->cols : p->cols + 7;
 }
 
-// Whether rows at `p`, `stride` elements apart, are read or written in vectors of `vec` elements.
-bool in_vectors(const void* p, int64_t stride, int64_t cols, size_t elem, int64_t vec)
+// Whether the kernel that computes dx holds the sums over its rows as well.
+bool sums_in_rows(RowShape s) { return s.elems == 8 || s.elems == 16; }
+
+int64_t bwd_parts(const layer_norm_params* p)
+{
+    const RowShape s = row_shape(span_of(p));
+    if (!sums_in_rows(s)) {
+        const int64_t n = mx::cdiv(p->rows, PART_ROWS);
+        return n < PART_CHUNKS ? n : PART_CHUNKS;
+    }
+    return row_blocks(p->rows, s, bwd_resident(s));
+}
+
+// Whether rows at `p`, `stride` elements apart, lie to vectors of `vec` elements as those of x do, x starting at a
+// whole one.
+bool in_vectors(const void* p, int64_t stride, int64_t x_stride, size_t elem, int64_t vec)
 {
     const size_t bytes = vec * elem < 16 ? vec * elem : 16;
-    return cols % vec == 0 && stride % vec == 0 && aligned(p, bytes);
+    return (stride - x_stride) % vec == 0 && aligned(p, bytes);
 }
 
 int64_t vector_of(int32_t x_dtype) { return x_dtype == CONV2D_OUT_BF16 ? 8 : 4; }
@@ -102,15 +111,19 @@ extern "C" int layer_norm_fwd(const layer_norm_params* params, const void* x_dev
     k.x = x_dev;
     k.y = y_dev;
     const int64_t v = ln::vector_of(params->x_dtype);
-    const bool vec = ln::in_vectors(x_dev, k.x_stride, k.cols, ln::dtype_size(params->x_dtype), v) &&
-                     ln::in_vectors(y_dev, k.y_stride, k.cols, ln::dtype_size(params->y_dtype), v);
+    const bool vec = ln::in_vectors(x_dev, k.x_stride, k.x_stride, ln::dtype_size(params->x_dtype), v) &&
+                     ln::in_vectors(y_dev, k.y_stride, k.x_stride, ln::dtype_size(params->y_dtype), v);
+    k.span = static_cast<int>(ln::span_of(params));
+    int rc = CONV2D_OK;
     ln::by_types(params->x_dtype, params->y_dtype, [&](auto* tx, auto* ty) {
         using TX = std::remove_pointer_t<decltype(tx)>;
         using TY = std::remove_pointer_t<decltype(ty)>;
-        if (!ln::launch_fwd_rows<TX, TY>(k, vec, stream))
-            ln::fwd_any<<<ln::row_grid(k.rows), ln::THREADS, 0, stream>>>(static_cast<const TX*>(x_dev), static_cast<TY*>(y_dev), k);
+        rc = ln::launch_fwd_rows<TX, TY>(k, vec, stream);
+        if (rc != CONV2D_ERR_UNSUPPORTED) return;
+        ln::fwd_any<<<ln::row_grid(k.rows), ln::THREADS, 0, stream>>>(static_cast<const TX*>(x_dev), static_cast<TY*>(y_dev), k);
+        rc = ln::launched();
     });
-    return ln::launched();
+    return rc;
 }
 
 extern "C" int layer_norm_mxfp4(const layer_norm_params* params, const void* x_dev, const float* weight_dev,
@@ -125,21 +138,27 @@ extern "C" int layer_norm_mxfp4(const layer_norm_params* params, const void* x_d
         return CONV2D_ERR_ALIGNMENT;
     ln::FwdParams k = ln::fwd_params(params, weight_dev, bias_dev, mean_dev, rstd_dev);
     k.x = x_dev;
-    const bool vec = ln::in_vectors(x_dev, k.x_stride, k.cols, ln::dtype_size(params->x_dtype), ln::vector_of(params->x_dtype));
+    // the format's blocks start with the row: whole vectors only
+    const int64_t v = ln::vector_of(params->x_dtype);
+    const bool vec = k.cols % v == 0 && k.x_stride % v == 0 && ln::aligned(x_dev, 16);
+    k.span = k.cols;
     k.data = static_cast<uint8_t*>(data_dev);
     k.scales = static_cast<uint8_t*>(scales_dev);
+    int rc = CONV2D_OK;
     ln::by_types(params->x_dtype, CONV2D_OUT_F32, [&](auto* tx, auto*) {
         using TX = std::remove_pointer_t<decltype(tx)>;
-        if (!ln::launch_fwd_rows<TX, void>(k, vec, stream))
-            ln::fwd_mx_any<<<ln::row_grid(k.padded_rows), ln::THREADS, 0, stream>>>(static_cast<const TX*>(x_dev), k);
+        rc = ln::launch_fwd_rows<TX, void>(k, vec, stream);
+        if (rc != CONV2D_ERR_UNSUPPORTED) return;
+        ln::fwd_mx_any<<<ln::row_grid(k.padded_rows), ln::THREADS, 0, stream>>>(static_cast<const TX*>(x_dev), k);
+        rc = ln::launched();
     });
-    return ln::launched();
+    return rc;
 }
 
 extern "C" size_t layer_norm_bwd_workspace_bytes(const layer_norm_params* params)
 {
     if (ln::check(params, true)) return 0;
-    return static_cast<size_t>(ln::bwd_parts(params->rows, params->cols)) * 2 * static_cast<size_t>(params->cols) * sizeof(float);
+    return static_cast<size_t>(ln::bwd_parts(params)) * 2 * static_cast<size_t>(params->cols) * sizeof(float);
 }
 
 extern "C" int layer_norm_bwd(const layer_norm_params* params, const void* dy_dev, const void* x_dev,
@@ -171,23 +190,30 @@ extern "C" int layer_norm_bwd(const layer_norm_params* params, const void* dy_de
     k.dy = dy_dev;
     k.dx = dx_dev;
     k.part = sums ? static_cast<float*>(workspace_dev) : nullptr;
-    k.chunks = static_cast<int>(ln::bwd_parts(params->rows, params->cols));
+    k.chunks = static_cast<int>(ln::bwd_parts(params));
     k.chunk = k.chunks ? mx::cdiv<int64_t>(params->rows, k.chunks) : 0;
     const int64_t v = ln::vector_of(params->x_dtype);
     const size_t sx = ln::dtype_size(params->x_dtype);
-    const bool vec = ln::in_vectors(x_dev, k.x_stride, k.cols, sx, v) && ln::in_vectors(dx_dev, k.cols, k.cols, sx, v) &&
-                     ln::in_vectors(dy_dev, k.dy_stride, k.cols, ln::dtype_size(params->y_dtype), v);
+    const bool vec = ln::in_vectors(x_dev, k.x_stride, k.x_stride, sx, v) && ln::in_vectors(dx_dev, k.cols, k.x_stride, sx, v) &&
+                     ln::in_vectors(dy_dev, k.dy_stride, k.x_stride, ln::dtype_size(params->y_dtype), v);
+    k.span = static_cast<int>(ln::span_of(params));
+    int rc = CONV2D_OK;
     if (params->rows > 0)
         ln::by_types(params->x_dtype, params->y_dtype, [&](auto* tx, auto* ty) {
             using TX = std::remove_pointer_t<decltype(tx)>;
             using TY = std::remove_pointer_t<decltype(ty)>;
-            if (ln::launch_bwd_rows<TX, TY>(k, vec, k.chunks, stream)) return;
+            rc = ln::launch_bwd_rows<TX, TY>(k, vec, k.chunks, stream);
+            if (rc != CONV2D_OK && rc != CONV2D_ERR_UNSUPPORTED) return;
+            if (rc == CONV2D_OK && ln::sums_in_rows(ln::row_shape(k.span))) return;
             const TX* x = static_cast<const TX*>(x_dev);
             const TY* dy = static_cast<const TY*>(dy_dev);
-            ln::bwd_dx_any<<<ln::row_grid(k.rows), ln::THREADS, 0, stream>>>(dy, x, static_cast<TX*>(dx_dev), k);
+            if (rc == CONV2D_ERR_UNSUPPORTED)
+                ln::bwd_dx_any<<<ln::row_grid(k.rows), ln::THREADS, 0, stream>>>(dy, x, static_cast<TX*>(dx_dev), k);
             const dim3 grid(static_cast<unsigned>(mx::cdiv(k.cols, ln::THREADS)), static_cast<unsigned>(k.chunks));
             if (sums) ln::bwd_part_any<<<grid, ln::THREADS, 0, stream>>>(dy, x, k);
+            rc = ln::launched();
         });
+    if (rc) return rc;
     if (sums) ln::bwd_join<<<static_cast<unsigned>(mx::cdiv(k.cols, 32)), 1024, 0, stream>>>(k);
     return ln::launched();
 }

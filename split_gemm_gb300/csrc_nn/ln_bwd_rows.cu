@@ -1,40 +1,48 @@
 // Instantiates the backward kernels that hold their row in registers.
+#include "conv2d.h"
 #include "ln_rows.cuh"
 
 namespace sgb {
 namespace ln {
 
-template <typename TX, typename TY, int VEC, int E, int G>
-void start_bwd(const BwdParams& p, int grid, cudaStream_t stream)
+template <typename TX, typename TY, int VEC, int E, int G, int MOST, bool SUMS>
+int start_bwd(const BwdParams& p, RowShape s, int grid, cudaStream_t stream)
 {
-    bwd_rows<TX, TY, VEC, E, G><<<static_cast<unsigned>(grid), block_threads(G), 0, stream>>>(
+    static std::atomic<uint64_t> done{0};
+    constexpr int DEPTH = ring_depth(RowShape{G ? G : MOST, E, MOST}, sizeof(TX), sizeof(TY)), V = VEC == 1 ? 8 : VEC;
+    constexpr int ring = VEC > 1 ? Ring<TX, V, E / V, DEPTH>::THREAD_BYTES + Ring<TY, V, E / V, DEPTH>::THREAD_BYTES : 0;
+    constexpr int join = G ? 2 * E * 4 : 0;  // a block's sums by row and column
+    constexpr int per_thread = ring > join ? ring : join;
+    if (!allow_smem(bwd_rows<TX, TY, VEC, E, G, MOST, SUMS>, per_thread * MOST, done)) return CONV2D_ERR_CUDA;
+    const int threads = block_threads(s);
+    bwd_rows<TX, TY, VEC, E, G, MOST, SUMS><<<static_cast<unsigned>(grid), threads, per_thread * threads, stream>>>(
         static_cast<const TY*>(p.dy), static_cast<const TX*>(p.x), static_cast<TX*>(p.dx), p);
+    return cudaGetLastError() == cudaSuccess ? CONV2D_OK : CONV2D_ERR_CUDA;
 }
 
 template <typename TX, typename TY, int VEC>
-bool bwd_by_shape(const BwdParams& p, int grid, cudaStream_t stream)
+int bwd_by_shape(const BwdParams& p, int grid, cudaStream_t stream)
 {
-    const RowShape s = row_shape(p.cols);
-    switch (s.threads * 100 + s.elems) {
-        case 808: start_bwd<TX, TY, VEC, 8, 8>(p, grid, stream); return true;
-        case 1608: start_bwd<TX, TY, VEC, 8, 16>(p, grid, stream); return true;
-        case 3208: start_bwd<TX, TY, VEC, 8, 32>(p, grid, stream); return true;
-        case 3216: start_bwd<TX, TY, VEC, 16, 32>(p, grid, stream); return true;
-        case 12808: start_bwd<TX, TY, VEC, 8, 128>(p, grid, stream); return true;
-        case 25608: start_bwd<TX, TY, VEC, 8, 256>(p, grid, stream); return true;
-        case 25616: start_bwd<TX, TY, VEC, 16, 256>(p, grid, stream); return true;
-        case 51216: start_bwd<TX, TY, VEC, 16, 512>(p, grid, stream); return true;
-        default: return false;
-    }
+    const RowShape s = row_shape(p.span);
+    if (s.threads == 0) return CONV2D_ERR_UNSUPPORTED;
+    if (s.threads == 8) return start_bwd<TX, TY, VEC, 8, 8, 256, true>(p, s, grid, stream);
+    if (s.threads == 16) return start_bwd<TX, TY, VEC, 8, 16, 256, true>(p, s, grid, stream);
+    if (s.threads == 32)
+        return s.elems == 8 ? start_bwd<TX, TY, VEC, 8, 32, 256, true>(p, s, grid, stream) : start_bwd<TX, TY, VEC, 16, 32, 256, true>(p, s, grid, stream);
+    if (s.elems == 8) return start_bwd<TX, TY, VEC, 8, 0, 256, true>(p, s, grid, stream);
+    if (s.elems == 16)
+        return s.most == 256 ? start_bwd<TX, TY, VEC, 16, 0, 256, true>(p, s, grid, stream) : start_bwd<TX, TY, VEC, 16, 0, 512, true>(p, s, grid, stream);
+    // No registers are left for the sums: dx alone, in blocks of its own number.
+    return start_bwd<TX, TY, VEC, 32, 0, 512, false>(p, s, static_cast<int>(row_blocks(p.rows, s, bwd_resident(s))), stream);
 }
 
 template <typename TX, typename TY>
-bool launch_bwd_rows(const BwdParams& p, bool vec, int grid, cudaStream_t stream)
+int launch_bwd_rows(const BwdParams& p, bool vec, int grid, cudaStream_t stream)
 {
     return vec ? bwd_by_shape<TX, TY, 16 / sizeof(TX)>(p, grid, stream) : bwd_by_shape<TX, TY, 1>(p, grid, stream);
 }
 
-#define SGB_BWD(TX, TY) template bool launch_bwd_rows<TX, TY>(const BwdParams&, bool, int, cudaStream_t);
+#define SGB_BWD(TX, TY) template int launch_bwd_rows<TX, TY>(const BwdParams&, bool, int, cudaStream_t);
 SGB_BWD(float, float)
 SGB_BWD(float, __nv_bfloat16)
 SGB_BWD(__nv_bfloat16, float)
