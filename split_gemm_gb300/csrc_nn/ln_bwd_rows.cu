@@ -5,28 +5,40 @@
 namespace sgb {
 namespace ln {
 
-template <typename TX, typename TY, int VEC, int E, int G, int MOST, bool SUMS>
-int start_bwd(const BwdParams& p, RowShape s, int grid, cudaStream_t stream)
+template <typename TX, typename TY, int VEC, int E, int G, int MOST, bool SUMS, bool FULL>
+int start_bwd_as(const BwdParams& p, RowShape s, int grid, cudaStream_t stream)
 {
     static std::atomic<uint64_t> done{0};
     constexpr int DEPTH = ring_depth(RowShape{G ? G : MOST, E, MOST}, sizeof(TX), sizeof(TY)), V = VEC == 1 ? 8 : VEC;
     constexpr int ring = VEC > 1 ? Ring<TX, V, E / V, DEPTH>::THREAD_BYTES + Ring<TY, V, E / V, DEPTH>::THREAD_BYTES : 0;
     constexpr int join = G ? 2 * E * 4 : 0;  // a block's sums by row and column
     constexpr int per_thread = ring > join ? ring : join;
-    if (!allow_smem(bwd_rows<TX, TY, VEC, E, G, MOST, SUMS>, per_thread * MOST, done)) return CONV2D_ERR_CUDA;
+    const auto kernel = bwd_rows<TX, TY, VEC, E, G, MOST, SUMS, FULL>;
+    if (!allow_smem(kernel, per_thread * MOST, done)) return CONV2D_ERR_CUDA;
     const int threads = block_threads(s);
-    bwd_rows<TX, TY, VEC, E, G, MOST, SUMS><<<static_cast<unsigned>(grid), threads, per_thread * threads, stream>>>(
-        static_cast<const TY*>(p.dy), static_cast<const TX*>(p.x), static_cast<TX*>(p.dx), p);
+    kernel<<<static_cast<unsigned>(grid), threads, per_thread * threads, stream>>>(static_cast<const TY*>(p.dy), static_cast<const TX*>(p.x),
+                                                                                   static_cast<TX*>(p.dx), p);
     return cudaGetLastError() == cudaSuccess ? CONV2D_OK : CONV2D_ERR_CUDA;
+}
+
+template <typename TX, typename TY, int VEC, int E, int G, int MOST, bool SUMS>
+int start_bwd(const BwdParams& p, RowShape s, int grid, cudaStream_t stream)
+{
+    if constexpr (VEC > 1)
+        if (p.span == p.cols && p.cols == s.threads * E) return start_bwd_as<TX, TY, VEC, E, G, MOST, SUMS, true>(p, s, grid, stream);
+    return start_bwd_as<TX, TY, VEC, E, G, MOST, SUMS, false>(p, s, grid, stream);
 }
 
 template <typename TX, typename TY, int VEC>
 int bwd_by_shape(const BwdParams& p, int grid, cudaStream_t stream)
 {
-    const RowShape s = row_shape(p.span);
+    const RowShape s = bwd_shape(p.rows, p.span, sizeof(TX));
     if (s.threads == 0) return CONV2D_ERR_UNSUPPORTED;
-    if (s.threads == 8) return start_bwd<TX, TY, VEC, 8, 8, 256, true>(p, s, grid, stream);
-    if (s.threads == 16) return start_bwd<TX, TY, VEC, 8, 16, 256, true>(p, s, grid, stream);
+    if (s.threads == 4) return start_bwd<TX, TY, VEC, 16, 4, 256, true>(p, s, grid, stream);
+    if (s.threads == 8)
+        return s.elems == 8 ? start_bwd<TX, TY, VEC, 8, 8, 256, true>(p, s, grid, stream) : start_bwd<TX, TY, VEC, 16, 8, 256, true>(p, s, grid, stream);
+    if (s.threads == 16)
+        return s.elems == 8 ? start_bwd<TX, TY, VEC, 8, 16, 256, true>(p, s, grid, stream) : start_bwd<TX, TY, VEC, 16, 16, 256, true>(p, s, grid, stream);
     if (s.threads == 32)
         return s.elems == 8 ? start_bwd<TX, TY, VEC, 8, 32, 256, true>(p, s, grid, stream) : start_bwd<TX, TY, VEC, 16, 32, 256, true>(p, s, grid, stream);
     if (s.elems == 8) return start_bwd<TX, TY, VEC, 8, 0, 256, true>(p, s, grid, stream);

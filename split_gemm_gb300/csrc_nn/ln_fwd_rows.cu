@@ -5,19 +5,27 @@
 namespace sgb {
 namespace ln {
 
-template <typename TX, typename TY, int VEC, int E, int G, int MOST>
-int start_fwd(const FwdParams& p, RowShape s, cudaStream_t stream)
+template <typename TX, typename TY, int VEC, int E, int G, int MOST, bool FULL>
+int start_fwd_as(const FwdParams& p, RowShape s, cudaStream_t stream)
 {
     static std::atomic<uint64_t> done{0};
     constexpr int V = VEC == 1 ? 8 : VEC;
     constexpr int per_thread = VEC > 1 ? Ring<TX, V, E / V, ring_depth(RowShape{G ? G : MOST, E, MOST}, sizeof(TX), 0)>::THREAD_BYTES : 0;
-    if (G) s = RowShape{G, E, MOST};
-    if (!allow_smem(fwd_rows<TX, TY, VEC, E, G, MOST>, per_thread * MOST, done)) return CONV2D_ERR_CUDA;
+    const auto kernel = fwd_rows<TX, TY, VEC, E, G, MOST, FULL>;
+    if (!allow_smem(kernel, per_thread * MOST, done)) return CONV2D_ERR_CUDA;
     const int64_t grid = row_blocks(std::is_same_v<TY, void> ? p.padded_rows : p.rows, s, fwd_resident(s));
     const int threads = block_threads(s);
-    fwd_rows<TX, TY, VEC, E, G, MOST><<<static_cast<unsigned>(grid), threads, per_thread * threads, stream>>>(
-        static_cast<const TX*>(p.x), static_cast<TY*>(p.y), p);
+    kernel<<<static_cast<unsigned>(grid), threads, per_thread * threads, stream>>>(static_cast<const TX*>(p.x), static_cast<TY*>(p.y), p);
     return cudaGetLastError() == cudaSuccess ? CONV2D_OK : CONV2D_ERR_CUDA;
+}
+
+template <typename TX, typename TY, int VEC, int E, int G, int MOST>
+int start_fwd(const FwdParams& p, RowShape s, cudaStream_t stream)
+{
+    if (G) s = RowShape{G, E, MOST};
+    if constexpr (VEC > 1)
+        if (p.span == p.cols && p.cols == s.threads * E) return start_fwd_as<TX, TY, VEC, E, G, MOST, true>(p, s, stream);
+    return start_fwd_as<TX, TY, VEC, E, G, MOST, false>(p, s, stream);
 }
 
 template <typename TX, typename TY, int VEC>
@@ -25,17 +33,23 @@ int fwd_by_shape(const FwdParams& p, cudaStream_t stream)
 {
     // a quantised row needs the 128 columns of a scale tile in one vector of its group, single elements a whole warp
     constexpr bool MX = std::is_same_v<TY, void>;
-    constexpr int LEAST = !MX ? 8 : VEC == 8 ? 16 : 32;
-    const RowShape s = row_shape(p.span);
+    constexpr int LEAST = !MX ? 4 : VEC == 8 ? 16 : 32;
+    RowShape s = fwd_shape(p.rows, p.span, sizeof(TX));
     if (s.threads == 0) return CONV2D_ERR_UNSUPPORTED;
+    if (s.threads < LEAST) s = RowShape{LEAST, 8, 256};
+    if constexpr (LEAST <= 4)
+        if (s.threads == 4) return start_fwd<TX, TY, VEC, 16, 4, 256>(p, s, stream);
     if constexpr (LEAST <= 8)
-        if (s.threads == 8) return start_fwd<TX, TY, VEC, 8, 8, 256>(p, s, stream);
+        if (s.threads == 8) return s.elems == 8 ? start_fwd<TX, TY, VEC, 8, 8, 256>(p, s, stream) : start_fwd<TX, TY, VEC, 16, 8, 256>(p, s, stream);
     if constexpr (LEAST <= 16)
-        if (s.threads <= 16) return start_fwd<TX, TY, VEC, 8, 16, 256>(p, s, stream);
-    if (s.threads <= 32) return s.elems == 8 ? start_fwd<TX, TY, VEC, 8, 32, 256>(p, s, stream) : start_fwd<TX, TY, VEC, 16, 32, 256>(p, s, stream);
+        if (s.threads == 16) return s.elems == 8 ? start_fwd<TX, TY, VEC, 8, 16, 256>(p, s, stream) : start_fwd<TX, TY, VEC, 16, 16, 256>(p, s, stream);
+    if (s.threads == 32 && s.most == 256)
+        return s.elems == 8    ? start_fwd<TX, TY, VEC, 8, 32, 256>(p, s, stream)
+               : s.elems == 16 ? start_fwd<TX, TY, VEC, 16, 32, 256>(p, s, stream)
+                               : start_fwd<TX, TY, VEC, 32, 32, 256>(p, s, stream);
     if (s.elems == 8) return start_fwd<TX, TY, VEC, 8, 0, 256>(p, s, stream);
     if (s.elems == 16) return s.most == 256 ? start_fwd<TX, TY, VEC, 16, 0, 256>(p, s, stream) : start_fwd<TX, TY, VEC, 16, 0, 512>(p, s, stream);
-    return start_fwd<TX, TY, VEC, 32, 0, 512>(p, s, stream);
+    return s.most == 128 ? start_fwd<TX, TY, VEC, 32, 0, 128>(p, s, stream) : start_fwd<TX, TY, VEC, 32, 0, 512>(p, s, stream);
 }
 
 template <typename TX, typename TY>

@@ -37,24 +37,55 @@ struct RowShape {
     int threads, elems, most;
 };
 
-// The fewest threads that hold the row: groups inside a warp up to 512 columns (no barriers), then blocks of whole
-// warps of 8, 16 and 32 elements to a thread.
-__host__ __device__ constexpr RowShape row_shape(int64_t cols)
+// A row's two sums cost each of its threads some 40 instructions of shuffles whatever it holds, so threads hold much
+// where there are rows enough to keep the SMs busy with few threads to a row, and 16-bit rows, which bring twice the
+// elements for their bytes, hold twice what fp32 rows do.  (bf16, 65536 x 1024 forward: 32 elements 45 us, 8 elements 54;
+// fp32, 401408 x 64 backward: 16 elements 69 us, 8 elements 57.)
+__host__ __device__ constexpr bool many_rows(int64_t rows, int x_bytes, int threads) { return x_bytes == 2 && rows * threads >= 4 * 512 * 152; }
+
+// The shape of `elems` elements to a thread in whole warps; 0 threads where that is over `most`.
+__host__ __device__ constexpr RowShape warps_of(int n, int elems, int most)
 {
+    const int t = (n + 32 * elems - 1) / (32 * elems) * 32;
+    return t <= most ? RowShape{t, elems, most} : RowShape{0, 0, 0};
+}
+
+// Up to 512 columns: groups inside a warp.
+__host__ __device__ constexpr RowShape group_shape(int n, bool many)
+{
+    return n > 256 ? RowShape{32, 16, 256} : many ? (n <= 64 ? RowShape{4, 16, 256} : n <= 128 ? RowShape{8, 16, 256} : RowShape{16, 16, 256})
+                                                  : (n <= 64 ? RowShape{8, 8, 256} : n <= 128 ? RowShape{16, 8, 256} : RowShape{32, 8, 256});
+}
+
+// Forward: where there are many rows and they fill whole warps of 32 elements to a thread, those (a warp to a row of 1024 columns);
+// else blocks of 8, 16 or 32, as rows that do not fill their threads need registers for masks too.
+__host__ __device__ constexpr RowShape fwd_shape(int64_t rows, int64_t cols, int x_bytes)
+{
+    if (cols > 16384) return RowShape{0, 0, 0};
     const int n = static_cast<int>(cols);
-    return cols <= 64 ? RowShape{8, 8, 256} : cols <= 128 ? RowShape{16, 8, 256} : cols <= 256 ? RowShape{32, 8, 256}
-         : cols <= 512 ? RowShape{32, 16, 256} : cols <= 2048 ? RowShape{(n + 255) / 256 * 32, 8, 256}
-         : cols <= 4096 ? RowShape{(n + 511) / 512 * 32, 16, 256} : cols <= 8192 ? RowShape{(n + 511) / 512 * 32, 16, 512}
-         : cols <= 16384 ? RowShape{(n + 1023) / 1024 * 32, 32, 512} : RowShape{0, 0, 0};
+    if (n <= 512) return group_shape(n, many_rows(rows, x_bytes, 16));
+    if (many_rows(rows, x_bytes, 32) && n % 1024 == 0) return n == 1024 ? RowShape{32, 32, 256} : warps_of(n, 32, n <= 4096 ? 128 : 512);
+    return n <= 2048 ? warps_of(n, 8, 256) : n <= 4096 ? warps_of(n, 16, 256) : n <= 8192 ? warps_of(n, 16, 512) : warps_of(n, 32, 512);
+}
+
+// Backward: the sums of dweight and dbias leave registers for 16 elements; above 8192 columns dx alone takes 32.
+__host__ __device__ constexpr RowShape bwd_shape(int64_t rows, int64_t cols, int x_bytes)
+{
+    if (cols > 16384) return RowShape{0, 0, 0};
+    const int n = static_cast<int>(cols);
+    if (n <= 512) return group_shape(n, many_rows(rows, x_bytes, 16));
+    if (n > 8192) return warps_of(n, 32, 512);
+    const bool wide = n > 2048 || (many_rows(rows, x_bytes, 64) && n % 512 == 0);
+    return wide ? warps_of(n, 16, n <= 4096 ? 256 : 512) : warps_of(n, 8, 256);
 }
 
 __host__ __device__ constexpr int block_threads(RowShape s) { return s.threads <= 32 ? s.most : s.threads; }
 __host__ __device__ constexpr int rows_per_block(RowShape s) { return s.threads <= 32 ? s.most / s.threads : 1; }
 
-// Threads that stay on an SM, by the registers that rows, weights and sums need: forward 64 to a thread for 8
-// elements, 85 for 16, 128 for 16 or 32 in wide blocks; backward 85 and 128.  And the blocks of a shape that they make.
-__host__ __device__ constexpr int fwd_threads(RowShape s) { return s.most == 512 ? 512 : s.elems == 8 ? 1024 : 768; }
-__host__ __device__ constexpr int bwd_threads(RowShape s) { return s.most == 512 || s.elems > 8 ? 512 : 768; }
+// Threads that stay on an SM, by the registers that rows, weights and sums need: forward 64 to a thread of 8 elements, 85 of
+// 16, 128 of 32; backward 85 and 128.  And the blocks of a shape that they make.
+__host__ __device__ constexpr int fwd_threads(RowShape s) { return s.elems == 8 ? 1024 : s.elems == 16 && s.most == 256 ? 768 : 512; }
+__host__ __device__ constexpr int bwd_threads(RowShape s) { return s.elems == 8 ? 768 : 512; }
 __host__ __device__ constexpr int fwd_resident(RowShape s) { return fwd_threads(s) / block_threads(s); }
 __host__ __device__ constexpr int bwd_resident(RowShape s) { return bwd_threads(s) / block_threads(s); }
 
@@ -80,7 +111,7 @@ __host__ __device__ constexpr int64_t row_blocks(int64_t rows, RowShape s, int r
 template <typename K>
 bool allow_smem(K kernel, int bytes, std::atomic<uint64_t>& done)
 {
-    if (bytes <= 48 * 1024) return true;
+    if (bytes <= 40 * 1024) return true;  // 48 KB with the static arrays needs no asking
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return false;
     const uint64_t bit = uint64_t(1) << (dev & 63);

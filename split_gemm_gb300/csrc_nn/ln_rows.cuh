@@ -1,7 +1,7 @@
 // Layer normalisation kernels that hold their row in registers: one reading of x.
 //
 // A group of threads shares a row, each with E elements in E/VEC vectors of 16 bytes of x; vector k of thread t is
-// number k*(group) + t of the row, so neighbouring threads read neighbouring vectors.  G = 8, 16, 32: groups of G, a warp holds
+// number k*(group) + t of the row, so neighbouring threads read neighbouring vectors.  G = 4 .. 32: groups of G, a warp holds
 // 32/G rows and sums by shuffles.  G = 0: a block of as many warps as the row needs holds one row and sums through shared
 // memory, one barrier to a sum.  Blocks stay for many rows: a thread's columns are the same in each, so weight and bias (forward, backward) and the sums of
 // dweight and dbias (backward) stay in registers.
@@ -97,26 +97,36 @@ struct Ring {
 };
 
 // A thread's E elements of a row as units of H pairs for two-wide arithmetic: a unit is a vector, or (VEC = 1) two
-// single elements a group apart.
-template <int VEC, int E>
+// single elements a group apart.  FULL: every unit lies in the row; else a bit mask for each element zeroes what does not
+// (a mask and not a factor, as the row before may hold NaN; kept in registers, as branches around the few edge vectors cost more).
+template <int VEC, int E, bool FULL>
 struct Units {
     static constexpr int U = VEC > 1 ? E / VEC : E / 2;
     static constexpr int H = VEC > 1 ? VEC / 2 : 1;
     static constexpr int NV = E / VEC;
     int t, g, off, cols;  // thread of its group of g
+    uint32_t mask[FULL ? 1 : U][2 * H];
+    __device__ __forceinline__ Units(int t, int g, int off, int cols) : t(t), g(g), off(off), cols(cols)
+    {
+        if constexpr (!FULL)
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int i = 0; i < 2 * H; ++i) mask[u][i] = in(u, i) ? 0xffffffffu : 0u;
+    }
     // column of element i of unit u: below 0 or past the end outside the row
     __device__ __forceinline__ int col(int u, int i) const { return VEC > 1 ? (u * g + t) * VEC + i - off : (2 * u + i) * g + t; }
-    __device__ __forceinline__ bool in(int u, int i) const { return static_cast<unsigned>(col(u, i)) < static_cast<unsigned>(cols); }
-    __device__ __forceinline__ bool none(int u) const { return col(u, 0) >= cols; }
-    __device__ __forceinline__ bool whole(int u) const { return VEC > 1 ? col(u, 0) >= 0 && col(u, 2 * H - 1) < cols : in(u, 1); }
-    // Zeroes what lies outside the row; only a row's first and last vector have to look.
+    __device__ __forceinline__ bool in(int u, int i) const { return FULL || static_cast<unsigned>(col(u, i)) < static_cast<unsigned>(cols); }
+    __device__ __forceinline__ bool none(int u) const { return !FULL && col(u, 0) >= cols; }
+    __device__ __forceinline__ bool whole(int u) const { return FULL || (VEC > 1 ? col(u, 0) >= 0 && col(u, 2 * H - 1) < cols : in(u, 1)); }
+    // Zeroes what lies outside the row.
     __device__ __forceinline__ void cut(float2 (&d)[H], int u) const
     {
-        if (!whole(u)) {
+        if constexpr (!FULL) {
 #pragma unroll
             for (int i = 0; i < H; ++i) {
-                if (!in(u, 2 * i)) d[i].x = 0.f;
-                if (!in(u, 2 * i + 1)) d[i].y = 0.f;
+                d[i].x = __uint_as_float(__float_as_uint(d[i].x) & mask[u][2 * i]);
+                d[i].y = __uint_as_float(__float_as_uint(d[i].y) & mask[u][2 * i + 1]);
             }
         }
     }
@@ -142,7 +152,7 @@ struct Units {
             Pack<T, VEC> v;
             ring.get(v, slot, u);
             widen(d, v);
-            if (off) cut(d, u);  // the copy has cut the end off
+            cut(d, u);
         }
     }
     // Stores the unit's values that lie in the row.
@@ -252,13 +262,13 @@ __device__ __forceinline__ void store_mx(const float2 (&v)[(VEC + 1) / 2], int c
 }
 
 // Forward.  TY = void: the result quantised; rows from p.rows to p.padded_rows are the scale tiles' padding (and `off` is 0).
-template <typename TX, typename TY, int VEC, int E, int G, int MOST>
+template <typename TX, typename TY, int VEC, int E, int G, int MOST, bool FULL>
 __global__ void __launch_bounds__(MOST, FWD_RESIDENT<G, E, MOST>) fwd_rows(const TX* __restrict__ x, TY* y, const FwdParams p)
 {
     constexpr bool MX = std::is_same_v<TY, void>;
     constexpr int ROWS = G ? MOST / G : 1, DEPTH = ring_depth(RowShape{G ? G : MOST, E, MOST}, sizeof(TX), 0);
     static_assert(!MX || G == 0 || (VEC == 1 ? G >= 32 : G * VEC >= 128), "four blocks' scales are joined within a row's lanes");
-    using Un = Units<VEC, E>;
+    using Un = Units<VEC, E, FULL>;
     constexpr int U = Un::U, H = Un::H;
     extern __shared__ __align__(16) uint8_t ring_mem[];
     __shared__ float sums[2][1][32];
@@ -268,7 +278,7 @@ __global__ void __launch_bounds__(MOST, FWD_RESIDENT<G, E, MOST>) fwd_rows(const
     const int g = G ? G : blockDim.x;
     const int64_t first = static_cast<int64_t>(blockIdx.x) * ROWS + (G ? threadIdx.x / (G ? G : 1) : 0);
     const int64_t lead = G && G < 32 ? static_cast<int64_t>(blockIdx.x) * ROWS + (threadIdx.x & ~31) / (G ? G : 1) : first;
-    const Un un{G ? static_cast<int>(threadIdx.x) % (G ? G : 1) : static_cast<int>(threadIdx.x), g, VEC > 1 ? static_cast<int>(first * p.x_stride % VEC) : 0, p.cols};
+    const Un un(G ? threadIdx.x % (G ? G : 1) : threadIdx.x, g, FULL || VEC == 1 ? 0 : static_cast<int>(first * p.x_stride % VEC), p.cols);
     const int blocks = MX ? mx::cdiv(p.cols, mx::BLOCK) : 0, btiles = MX ? mx::cdiv(blocks, mx::TILE_BLOCKS) : 0;
 
     const Ring<TX, VEC == 1 ? 8 : VEC, VEC == 1 ? 1 : Un::NV, DEPTH> ring(ring_mem, blockDim.x);
@@ -307,14 +317,13 @@ __global__ void __launch_bounds__(MOST, FWD_RESIDENT<G, E, MOST>) fwd_rows(const
         const float2 minus = make_float2(-mean, -mean);
         s2 = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int u = 0; u < U; ++u)
-            if (!un.none(u)) {
+        for (int u = 0; u < U; ++u) {
 #pragma unroll
-                for (int i = 0; i < H; ++i) d[u][i] = add2(d[u][i], minus);
-                un.cut(d[u], u);
+            for (int i = 0; i < H; ++i) d[u][i] = add2(d[u][i], minus);
+            un.cut(d[u], u);
 #pragma unroll
-                for (int i = 0; i < H; ++i) s2 = fma2(d[u][i], d[u][i], s2);
-            }
+            for (int i = 0; i < H; ++i) s2 = fma2(d[u][i], d[u][i], s2);
+        }
         s[0] = s2.x + s2.y;
         row_sum<G>(s, sums[1]);
         const float rstd = rsqrtf(s[0] * p.inv_cols + p.eps);
@@ -337,12 +346,12 @@ __global__ void __launch_bounds__(MOST, FWD_RESIDENT<G, E, MOST>) fwd_rows(const
             const int live_blocks = live ? blocks : 0, tiles = r < end ? btiles : 0;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                if (!live || un.none(u)) {
+                un.cut(d[u], u);
+                if (!live) {
 #pragma unroll
                     for (int i = 0; i < H; ++i) d[u][i] = make_float2(0.f, 0.f);
                 }
                 if constexpr (VEC == 1) {
-                    un.cut(d[u], u);
                     const float2 second[1] = {make_float2(d[u][0].y, 0.f)};
                     store_mx<1>(d[u], un.col(u, 0), data, scales, live_blocks, tiles);
                     store_mx<1>(second, un.col(u, 1), data, scales, live_blocks, tiles);
@@ -356,12 +365,12 @@ __global__ void __launch_bounds__(MOST, FWD_RESIDENT<G, E, MOST>) fwd_rows(const
 }
 
 // Backward: dx and, with SUMS, this block's part of dweight and dbias.
-template <typename TX, typename TY, int VEC, int E, int G, int MOST, bool SUMS>
+template <typename TX, typename TY, int VEC, int E, int G, int MOST, bool SUMS, bool FULL>
 __global__ void __launch_bounds__(MOST, BWD_RESIDENT<G, E, MOST>) bwd_rows(const TY* __restrict__ dy, const TX* __restrict__ x,
                                                                                   TX* __restrict__ dx, const BwdParams p)
 {
     constexpr int ROWS = G ? MOST / G : 1, DEPTH = ring_depth(RowShape{G ? G : MOST, E, MOST}, sizeof(TX), sizeof(TY));
-    using Un = Units<VEC, E>;
+    using Un = Units<VEC, E, FULL>;
     constexpr int U = Un::U, H = Un::H;
     extern __shared__ __align__(16) uint8_t ring_mem[];
     __shared__ float sums[2][2][32];
@@ -369,7 +378,7 @@ __global__ void __launch_bounds__(MOST, BWD_RESIDENT<G, E, MOST>) bwd_rows(const
     const int group = G ? G : blockDim.x;
     const int64_t first = static_cast<int64_t>(blockIdx.x) * ROWS + (G ? threadIdx.x / (G ? G : 1) : 0);
     const int64_t lead = G && G < 32 ? static_cast<int64_t>(blockIdx.x) * ROWS + (threadIdx.x & ~31) / (G ? G : 1) : first;
-    const Un un{G ? static_cast<int>(threadIdx.x) % (G ? G : 1) : static_cast<int>(threadIdx.x), group, VEC > 1 ? static_cast<int>(first * p.x_stride % VEC) : 0, p.cols};
+    const Un un(G ? threadIdx.x % (G ? G : 1) : threadIdx.x, group, FULL || VEC == 1 ? 0 : static_cast<int>(first * p.x_stride % VEC), p.cols);
 
     using RingX = Ring<TX, VEC == 1 ? 8 : VEC, VEC == 1 ? 1 : Un::NV, DEPTH>;
     using RingG = Ring<TY, VEC == 1 ? 8 : VEC, VEC == 1 ? 1 : Un::NV, DEPTH>;
@@ -409,20 +418,16 @@ __global__ void __launch_bounds__(MOST, BWD_RESIDENT<G, E, MOST>) bwd_rows(const
         for (int u = 0; u < U; ++u) {
             un.take(xh[u], ring_x, slot, x + r * p.x_stride, u, live);
             un.take(g[u], ring_g, slot, dy + r * p.dy_stride, u, live);
-            if (!un.none(u)) {
 #pragma unroll
-                for (int i = 0; i < H; ++i) xh[u][i] = mul2(add2(xh[u][i], minus), scale);
-                un.cut(xh[u], u);
-#pragma unroll
-                for (int i = 0; i < H; ++i) {
-                    if constexpr (SUMS) {
-                        dw[u][i] = fma2(g[u][i], xh[u][i], dw[u][i]);
-                        db[u][i] = add2(db[u][i], g[u][i]);
-                    }
-                    g[u][i] = mul2(g[u][i], w[u][i]);
-                    s0 = add2(s0, g[u][i]);
-                    s1 = fma2(g[u][i], xh[u][i], s1);
+            for (int i = 0; i < H; ++i) {  // outside the row dy is zero and the normalised value finite where mean and rstd are
+                xh[u][i] = mul2(add2(xh[u][i], minus), scale);
+                if constexpr (SUMS) {
+                    dw[u][i] = fma2(g[u][i], xh[u][i], dw[u][i]);
+                    db[u][i] = add2(db[u][i], g[u][i]);
                 }
+                g[u][i] = mul2(g[u][i], w[u][i]);
+                s0 = add2(s0, g[u][i]);
+                s1 = fma2(g[u][i], xh[u][i], s1);
             }
         }
         float s[2] = {s0.x + s0.y, s1.x + s1.y};

@@ -53,9 +53,11 @@ def layer_norm_fwd(x, weight=None, bias=None, eps: float = 1e-5, *, out_dtype=No
     return y, mean, rstd
 
 
-def layer_norm_bwd_workspace_bytes(rows: int, cols: int) -> int:
-    """Bytes of workspace (of any content) that the sums over the rows need."""
-    params = LayerNormParams(rows, cols, cols, cols, 0, 0, 0.0)
+def layer_norm_bwd_workspace_bytes(x, dy) -> int:
+    """Bytes of workspace (of any content) that layer_norm_bwd needs for these tensors."""
+    rows, cols, x_stride = rows_of(x, "x")
+    _, _, dy_stride = rows_of(dy, "dy")
+    params = LayerNormParams(rows, cols, x_stride, dy_stride, DTYPE_CODES[x.dtype], DTYPE_CODES[dy.dtype], 0.0)
     return int(library().layer_norm_bwd_workspace_bytes(ctypes.byref(params)))
 
 
