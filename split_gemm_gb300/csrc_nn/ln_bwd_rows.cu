@@ -5,7 +5,7 @@
 namespace sgb {
 namespace ln {
 
-template <typename TX, typename TY, int VEC, int E, int G, int MOST, bool SUMS, bool FULL>
+template <typename TX, typename TY, int VEC, int E, int G, int MOST, bool SUMS, bool WHOLE>
 int start_bwd_as(const BwdParams& p, RowShape s, int grid, cudaStream_t stream)
 {
     static std::atomic<uint64_t> done{0};
@@ -13,7 +13,7 @@ int start_bwd_as(const BwdParams& p, RowShape s, int grid, cudaStream_t stream)
     constexpr int ring = VEC > 1 ? Ring<TX, V, E / V, DEPTH>::THREAD_BYTES + Ring<TY, V, E / V, DEPTH>::THREAD_BYTES : 0;
     constexpr int join = G ? 2 * E * 4 : 0;  // a block's sums by row and column
     constexpr int per_thread = ring > join ? ring : join;
-    const auto kernel = bwd_rows<TX, TY, VEC, E, G, MOST, SUMS, FULL>;
+    const auto kernel = bwd_rows<TX, TY, VEC, E, G, MOST, SUMS, WHOLE>;
     if (!allow_smem(kernel, per_thread * MOST, done)) return CONV2D_ERR_CUDA;
     const int threads = block_threads(s);
     kernel<<<static_cast<unsigned>(grid), threads, per_thread * threads, stream>>>(static_cast<const TY*>(p.dy), static_cast<const TX*>(p.x),
@@ -25,7 +25,7 @@ template <typename TX, typename TY, int VEC, int E, int G, int MOST, bool SUMS>
 int start_bwd(const BwdParams& p, RowShape s, int grid, cudaStream_t stream)
 {
     if constexpr (VEC > 1)
-        if (p.span == p.cols && p.cols == s.threads * E) return start_bwd_as<TX, TY, VEC, E, G, MOST, SUMS, true>(p, s, grid, stream);
+        if (p.span == p.cols) return start_bwd_as<TX, TY, VEC, E, G, MOST, SUMS, true>(p, s, grid, stream);
     return start_bwd_as<TX, TY, VEC, E, G, MOST, SUMS, false>(p, s, grid, stream);
 }
 

@@ -5,13 +5,13 @@
 namespace sgb {
 namespace ln {
 
-template <typename TX, typename TY, int VEC, int E, int G, int MOST, bool FULL>
+template <typename TX, typename TY, int VEC, int E, int G, int MOST, bool WHOLE>
 int start_fwd_as(const FwdParams& p, RowShape s, cudaStream_t stream)
 {
     static std::atomic<uint64_t> done{0};
     constexpr int V = VEC == 1 ? 8 : VEC;
     constexpr int per_thread = VEC > 1 ? Ring<TX, V, E / V, ring_depth(RowShape{G ? G : MOST, E, MOST}, sizeof(TX), 0)>::THREAD_BYTES : 0;
-    const auto kernel = fwd_rows<TX, TY, VEC, E, G, MOST, FULL>;
+    const auto kernel = fwd_rows<TX, TY, VEC, E, G, MOST, WHOLE>;
     if (!allow_smem(kernel, per_thread * MOST, done)) return CONV2D_ERR_CUDA;
     const int64_t grid = row_blocks(std::is_same_v<TY, void> ? p.padded_rows : p.rows, s, fwd_resident(s));
     const int threads = block_threads(s);
@@ -24,7 +24,7 @@ int start_fwd(const FwdParams& p, RowShape s, cudaStream_t stream)
 {
     if (G) s = RowShape{G, E, MOST};
     if constexpr (VEC > 1)
-        if (p.span == p.cols && p.cols == s.threads * E) return start_fwd_as<TX, TY, VEC, E, G, MOST, true>(p, s, stream);
+        if (p.span == p.cols) return start_fwd_as<TX, TY, VEC, E, G, MOST, true>(p, s, stream);
     return start_fwd_as<TX, TY, VEC, E, G, MOST, false>(p, s, stream);
 }
 
@@ -49,7 +49,7 @@ int fwd_by_shape(const FwdParams& p, cudaStream_t stream)
                                : start_fwd<TX, TY, VEC, 32, 32, 256>(p, s, stream);
     if (s.elems == 8) return start_fwd<TX, TY, VEC, 8, 0, 256>(p, s, stream);
     if (s.elems == 16) return s.most == 256 ? start_fwd<TX, TY, VEC, 16, 0, 256>(p, s, stream) : start_fwd<TX, TY, VEC, 16, 0, 512>(p, s, stream);
-    return s.most == 128 ? start_fwd<TX, TY, VEC, 32, 0, 128>(p, s, stream) : start_fwd<TX, TY, VEC, 32, 0, 512>(p, s, stream);
+    return start_fwd<TX, TY, VEC, 32, 0, 512>(p, s, stream);
 }
 
 template <typename TX, typename TY>

@@ -57,15 +57,16 @@ __host__ __device__ constexpr RowShape group_shape(int n, bool many)
                                                   : (n <= 64 ? RowShape{8, 8, 256} : n <= 128 ? RowShape{16, 8, 256} : RowShape{32, 8, 256});
 }
 
-// Forward: where there are many rows and they fill whole warps of 32 elements to a thread, those (a warp to a row of 1024 columns);
-// else blocks of 8, 16 or 32, as rows that do not fill their threads need registers for masks too.
+// Forward: a warp to a row of up to 1024 columns where there are many rows and those fill it, else blocks of 8, 16 or 32
+// elements to a thread.
 __host__ __device__ constexpr RowShape fwd_shape(int64_t rows, int64_t cols, int x_bytes)
 {
     if (cols > 16384) return RowShape{0, 0, 0};
     const int n = static_cast<int>(cols);
     if (n <= 512) return group_shape(n, many_rows(rows, x_bytes, 16));
-    if (many_rows(rows, x_bytes, 32) && n % 1024 == 0) return n == 1024 ? RowShape{32, 32, 256} : warps_of(n, 32, n <= 4096 ? 128 : 512);
-    return n <= 2048 ? warps_of(n, 8, 256) : n <= 4096 ? warps_of(n, 16, 256) : n <= 8192 ? warps_of(n, 16, 512) : warps_of(n, 32, 512);
+    if (n > 768 && n <= 1024 && n % 8 == 0 && many_rows(rows, x_bytes, 32)) return RowShape{32, 32, 256};
+    return n <= (many_rows(rows, x_bytes, 64) ? 1024 : 2048) ? warps_of(n, 8, 256) : n <= 4096 ? warps_of(n, 16, 256)
+         : n <= 8192 && n % 8                                ? warps_of(n, 16, 512) : warps_of(n, 32, 512);
 }
 
 // Backward: the sums of dweight and dbias leave registers for 16 elements; above 8192 columns dx alone takes 32.
@@ -75,7 +76,7 @@ __host__ __device__ constexpr RowShape bwd_shape(int64_t rows, int64_t cols, int
     const int n = static_cast<int>(cols);
     if (n <= 512) return group_shape(n, many_rows(rows, x_bytes, 16));
     if (n > 8192) return warps_of(n, 32, 512);
-    const bool wide = n > 2048 || (many_rows(rows, x_bytes, 64) && n % 512 == 0);
+    const bool wide = n > 2048 || (many_rows(rows, x_bytes, 64) && n % 8 == 0 && (n + 511) / 512 * 512 <= n + n / 4);
     return wide ? warps_of(n, 16, n <= 4096 ? 256 : 512) : warps_of(n, 8, 256);
 }
 
@@ -89,11 +90,13 @@ __host__ __device__ constexpr int bwd_threads(RowShape s) { return s.elems == 8 
 __host__ __device__ constexpr int fwd_resident(RowShape s) { return fwd_threads(s) / block_threads(s); }
 __host__ __device__ constexpr int bwd_resident(RowShape s) { return bwd_threads(s) / block_threads(s); }
 
-// Rows of a block's ring: up to four, within 200 KB of an SM's shared memory.
+// Rows of a block's ring.  Forward some 72 KB of them on an SM, as more in flight slows HBM down (bf16, 32768 x 4096, rows of
+// all blocks 24 KB: two 89.5 us, three 88.4, four 93.3); backward 128 KB (four rows of 32 KB 141 us, two 173).
 __host__ __device__ constexpr int ring_depth(RowShape s, int x_bytes, int y_bytes)
 {
-    const int n = 200 * 1024 / ((y_bytes ? bwd_threads(s) : fwd_threads(s)) * s.elems * (x_bytes + y_bytes));
-    return n > 4 ? 4 : n;
+    const int row = (y_bytes ? bwd_threads(s) : fwd_threads(s)) * s.elems * (x_bytes + y_bytes);
+    const int n = (y_bytes ? 128 : 72) * 1024 / row;
+    return n > 4 ? 4 : n >= 2 ? n : 2 * row <= 200 * 1024 ? 2 : 1;
 }
 
 constexpr int SMS = mx::SMS;

@@ -97,32 +97,39 @@ struct Ring {
 };
 
 // A thread's E elements of a row as units of H pairs for two-wide arithmetic: a unit is a vector, or (VEC = 1) two
-// single elements a group apart.  FULL: every unit lies in the row; else a bit mask for each element zeroes what does not
-// (a mask and not a factor, as the row before may hold NaN; kept in registers, as branches around the few edge vectors cost more).
-template <int VEC, int E, bool FULL>
+// single elements a group apart.  WHOLE: rows are whole vectors, so that a unit lies in the row or beyond its end.  Else a bit
+// mask for each element zeroes what lies outside (a mask and not a factor, as the row before may hold NaN; kept in
+// registers, as branches around the few edge vectors cost more).
+template <int VEC, int E, bool WHOLE>
 struct Units {
     static constexpr int U = VEC > 1 ? E / VEC : E / 2;
     static constexpr int H = VEC > 1 ? VEC / 2 : 1;
     static constexpr int NV = E / VEC;
     int t, g, off, cols;  // thread of its group of g
-    uint32_t mask[FULL ? 1 : U][2 * H];
+    bool edge = false;    // a unit lies partly in the row
+    uint32_t mask[WHOLE ? 1 : U][2 * H];
     __device__ __forceinline__ Units(int t, int g, int off, int cols) : t(t), g(g), off(off), cols(cols)
     {
-        if constexpr (!FULL)
+        if constexpr (!WHOLE)
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+            for (int u = 0; u < U; ++u) {
+                edge |= !none(u) && !whole(u);
 #pragma unroll
                 for (int i = 0; i < 2 * H; ++i) mask[u][i] = in(u, i) ? 0xffffffffu : 0u;
+            }
     }
     // column of element i of unit u: below 0 or past the end outside the row
     __device__ __forceinline__ int col(int u, int i) const { return VEC > 1 ? (u * g + t) * VEC + i - off : (2 * u + i) * g + t; }
-    __device__ __forceinline__ bool in(int u, int i) const { return FULL || static_cast<unsigned>(col(u, i)) < static_cast<unsigned>(cols); }
-    __device__ __forceinline__ bool none(int u) const { return !FULL && col(u, 0) >= cols; }
-    __device__ __forceinline__ bool whole(int u) const { return FULL || (VEC > 1 ? col(u, 0) >= 0 && col(u, 2 * H - 1) < cols : in(u, 1)); }
+    __device__ __forceinline__ bool in(int u, int i) const
+    {
+        return WHOLE ? col(u, 0) < cols : static_cast<unsigned>(col(u, i)) < static_cast<unsigned>(cols);
+    }
+    __device__ __forceinline__ bool none(int u) const { return col(u, 0) >= cols; }
+    __device__ __forceinline__ bool whole(int u) const { return WHOLE || (VEC > 1 ? col(u, 0) >= 0 && col(u, 2 * H - 1) < cols : in(u, 1)); }
     // Zeroes what lies outside the row.
     __device__ __forceinline__ void cut(float2 (&d)[H], int u) const
     {
-        if constexpr (!FULL) {
+        if constexpr (!WHOLE) {
 #pragma unroll
             for (int i = 0; i < H; ++i) {
                 d[i].x = __uint_as_float(__float_as_uint(d[i].x) & mask[u][2 * i]);
@@ -155,39 +162,49 @@ struct Units {
             cut(d, u);
         }
     }
-    // Stores the unit's values that lie in the row.
+    // Stores the values that lie in the row.  A vector is made before anything is asked, so that its store is one predicated
+    // instruction (a branch around both cost the backward pass a quarter of its time), and a row's first and last vector wait for one branch at the end.
     template <typename T>
-    __device__ __forceinline__ void put(T* row, const float2 (&d)[H], int u, bool live) const
+    __device__ __forceinline__ void put(T* row, const float2 (&d)[U][H], bool live) const
     {
-        if (!live || none(u)) return;
-        if (VEC == 1 || !whole(u)) {
+        if constexpr (VEC > 1) {
 #pragma unroll
-            for (int i = 0; i < H; ++i) {
-                if (in(u, 2 * i)) mx::from_float(row[col(u, 2 * i)], d[i].x);
-                if (in(u, 2 * i + 1)) mx::from_float(row[col(u, 2 * i + 1)], d[i].y);
-            }
-        } else if constexpr (VEC > 1) {
-            Pack<T, VEC> o;
+            for (int u = 0; u < U; ++u) {
+                Pack<T, VEC> o;
 #pragma unroll
-            for (int i = 0; i < H; ++i) {
-                if constexpr (sizeof(T) == 2) {
-                    const __nv_bfloat162 b = __floats2bfloat162_rn(d[i].x, d[i].y);
-                    o.v[2 * i] = b.x;
-                    o.v[2 * i + 1] = b.y;
-                } else {
-                    o.v[2 * i] = d[i].x;
-                    o.v[2 * i + 1] = d[i].y;
+                for (int i = 0; i < H; ++i) {
+                    if constexpr (sizeof(T) == 2) {
+                        const __nv_bfloat162 b = __floats2bfloat162_rn(d[u][i].x, d[u][i].y);
+                        o.v[2 * i] = b.x;
+                        o.v[2 * i + 1] = b.y;
+                    } else {
+                        o.v[2 * i] = d[u][i].x;
+                        o.v[2 * i + 1] = d[u][i].y;
+                    }
                 }
+                if (live && !none(u) && whole(u)) *reinterpret_cast<Pack<T, VEC>*>(row + col(u, 0)) = o;
             }
-            *reinterpret_cast<Pack<T, VEC>*>(row + col(u, 0)) = o;
+            if constexpr (WHOLE) return;
+        }
+        if (live && (VEC == 1 || edge)) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (VEC == 1 || (!none(u) && !whole(u))) {
+#pragma unroll
+                    for (int i = 0; i < H; ++i) {
+                        if (in(u, 2 * i)) mx::from_float(row[col(u, 2 * i)], d[u][i].x);
+                        if (in(u, 2 * i + 1)) mx::from_float(row[col(u, 2 * i + 1)], d[u][i].y);
+                    }
+                }
         }
     }
-    // The unit's values of a per-column fp32 vector (`other` where there is none).
+    // The unit's values of a per-column fp32 vector: `other` where there is none, 0 outside the row.
     __device__ __forceinline__ void params(float2 (&d)[H], const float* v, int u, float other) const
     {
 #pragma unroll
         for (int i = 0; i < H; ++i)
-            d[i] = make_float2(v && in(u, 2 * i) ? __ldg(v + col(u, 2 * i)) : other, v && in(u, 2 * i + 1) ? __ldg(v + col(u, 2 * i + 1)) : other);
+            d[i] = make_float2(!in(u, 2 * i) ? 0.f : v ? __ldg(v + col(u, 2 * i)) : other,
+                               !in(u, 2 * i + 1) ? 0.f : v ? __ldg(v + col(u, 2 * i + 1)) : other);
     }
 };
 
@@ -262,13 +279,13 @@ __device__ __forceinline__ void store_mx(const float2 (&v)[(VEC + 1) / 2], int c
 }
 
 // Forward.  TY = void: the result quantised; rows from p.rows to p.padded_rows are the scale tiles' padding (and `off` is 0).
-template <typename TX, typename TY, int VEC, int E, int G, int MOST, bool FULL>
+template <typename TX, typename TY, int VEC, int E, int G, int MOST, bool WHOLE>
 __global__ void __launch_bounds__(MOST, FWD_RESIDENT<G, E, MOST>) fwd_rows(const TX* __restrict__ x, TY* y, const FwdParams p)
 {
     constexpr bool MX = std::is_same_v<TY, void>;
     constexpr int ROWS = G ? MOST / G : 1, DEPTH = ring_depth(RowShape{G ? G : MOST, E, MOST}, sizeof(TX), 0);
     static_assert(!MX || G == 0 || (VEC == 1 ? G >= 32 : G * VEC >= 128), "four blocks' scales are joined within a row's lanes");
-    using Un = Units<VEC, E, FULL>;
+    using Un = Units<VEC, E, WHOLE>;
     constexpr int U = Un::U, H = Un::H;
     extern __shared__ __align__(16) uint8_t ring_mem[];
     __shared__ float sums[2][1][32];
@@ -278,7 +295,7 @@ __global__ void __launch_bounds__(MOST, FWD_RESIDENT<G, E, MOST>) fwd_rows(const
     const int g = G ? G : blockDim.x;
     const int64_t first = static_cast<int64_t>(blockIdx.x) * ROWS + (G ? threadIdx.x / (G ? G : 1) : 0);
     const int64_t lead = G && G < 32 ? static_cast<int64_t>(blockIdx.x) * ROWS + (threadIdx.x & ~31) / (G ? G : 1) : first;
-    const Un un(G ? threadIdx.x % (G ? G : 1) : threadIdx.x, g, FULL || VEC == 1 ? 0 : static_cast<int>(first * p.x_stride % VEC), p.cols);
+    const Un un(G ? threadIdx.x % (G ? G : 1) : threadIdx.x, g, WHOLE || VEC == 1 ? 0 : static_cast<int>(first * p.x_stride % VEC), p.cols);
     const int blocks = MX ? mx::cdiv(p.cols, mx::BLOCK) : 0, btiles = MX ? mx::cdiv(blocks, mx::TILE_BLOCKS) : 0;
 
     const Ring<TX, VEC == 1 ? 8 : VEC, VEC == 1 ? 1 : Un::NV, DEPTH> ring(ring_mem, blockDim.x);
@@ -318,8 +335,9 @@ __global__ void __launch_bounds__(MOST, FWD_RESIDENT<G, E, MOST>) fwd_rows(const
         s2 = make_float2(0.f, 0.f);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
+            const float2 m = WHOLE && un.none(u) ? make_float2(0.f, 0.f) : minus;  // zeros beyond the row stay
 #pragma unroll
-            for (int i = 0; i < H; ++i) d[u][i] = add2(d[u][i], minus);
+            for (int i = 0; i < H; ++i) d[u][i] = add2(d[u][i], m);
             un.cut(d[u], u);
 #pragma unroll
             for (int i = 0; i < H; ++i) s2 = fma2(d[u][i], d[u][i], s2);
@@ -337,17 +355,14 @@ __global__ void __launch_bounds__(MOST, FWD_RESIDENT<G, E, MOST>) fwd_rows(const
 #pragma unroll
             for (int i = 0; i < H; ++i) d[u][i] = fma2(mul2(d[u][i], scale), w[u][i], b[u][i]);
         if constexpr (!MX) {
-            TY* out = y + r * p.y_stride;
-#pragma unroll
-            for (int u = 0; u < U; ++u) un.put(out, d[u], u, live);
+            un.put(y + r * p.y_stride, d, live);
         } else {
             uint8_t* data = p.data + r * (static_cast<int64_t>(blocks) * 16);
             uint8_t* scales = p.scales + mx::scale_at(r, 0, btiles);
             const int live_blocks = live ? blocks : 0, tiles = r < end ? btiles : 0;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                un.cut(d[u], u);
-                if (!live) {
+                if (!live) {  // outside the row weight and bias are zero
 #pragma unroll
                     for (int i = 0; i < H; ++i) d[u][i] = make_float2(0.f, 0.f);
                 }
@@ -365,12 +380,12 @@ __global__ void __launch_bounds__(MOST, FWD_RESIDENT<G, E, MOST>) fwd_rows(const
 }
 
 // Backward: dx and, with SUMS, this block's part of dweight and dbias.
-template <typename TX, typename TY, int VEC, int E, int G, int MOST, bool SUMS, bool FULL>
+template <typename TX, typename TY, int VEC, int E, int G, int MOST, bool SUMS, bool WHOLE>
 __global__ void __launch_bounds__(MOST, BWD_RESIDENT<G, E, MOST>) bwd_rows(const TY* __restrict__ dy, const TX* __restrict__ x,
                                                                                   TX* __restrict__ dx, const BwdParams p)
 {
     constexpr int ROWS = G ? MOST / G : 1, DEPTH = ring_depth(RowShape{G ? G : MOST, E, MOST}, sizeof(TX), sizeof(TY));
-    using Un = Units<VEC, E, FULL>;
+    using Un = Units<VEC, E, WHOLE>;
     constexpr int U = Un::U, H = Un::H;
     extern __shared__ __align__(16) uint8_t ring_mem[];
     __shared__ float sums[2][2][32];
@@ -378,7 +393,7 @@ __global__ void __launch_bounds__(MOST, BWD_RESIDENT<G, E, MOST>) bwd_rows(const
     const int group = G ? G : blockDim.x;
     const int64_t first = static_cast<int64_t>(blockIdx.x) * ROWS + (G ? threadIdx.x / (G ? G : 1) : 0);
     const int64_t lead = G && G < 32 ? static_cast<int64_t>(blockIdx.x) * ROWS + (threadIdx.x & ~31) / (G ? G : 1) : first;
-    const Un un(G ? threadIdx.x % (G ? G : 1) : threadIdx.x, group, FULL || VEC == 1 ? 0 : static_cast<int>(first * p.x_stride % VEC), p.cols);
+    const Un un(G ? threadIdx.x % (G ? G : 1) : threadIdx.x, group, WHOLE || VEC == 1 ? 0 : static_cast<int>(first * p.x_stride % VEC), p.cols);
 
     using RingX = Ring<TX, VEC == 1 ? 8 : VEC, VEC == 1 ? 1 : Un::NV, DEPTH>;
     using RingG = Ring<TY, VEC == 1 ? 8 : VEC, VEC == 1 ? 1 : Un::NV, DEPTH>;
@@ -438,11 +453,10 @@ __global__ void __launch_bounds__(MOST, BWD_RESIDENT<G, E, MOST>) bwd_rows(const
         s0 = make_float2(m0, m0);
         s1 = make_float2(m1, m1);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
+        for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int i = 0; i < H; ++i) xh[u][i] = mul2(scale, fma2(xh[u][i], s1, add2(g[u][i], s0)));
-            un.put(dx + r * p.cols, xh[u], u, live);
-        }
+        un.put(dx + r * p.cols, xh, live);
     }
     if constexpr (VEC > 1) ptx::cp_async_wait_all();
     if constexpr (SUMS) {
