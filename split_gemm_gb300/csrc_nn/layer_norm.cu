@@ -79,7 +79,7 @@ int64_t bwd_parts(const layer_norm_params* p)
         const int64_t n = mx::cdiv(p->rows, PART_ROWS);
         return n < PART_CHUNKS ? n : PART_CHUNKS;
     }
-    return row_blocks(p->rows, s, bwd_resident(s));
+    return bwd_blocks(p->rows, s);
 }
 
 // Whether rows at `p`, `stride` elements apart, lie to vectors of `vec` elements as those of x do, x starting at a
@@ -214,6 +214,6 @@ extern "C" int layer_norm_bwd(const layer_norm_params* params, const void* dy_de
             rc = ln::launched();
         });
     if (rc) return rc;
-    if (sums) ln::bwd_join<<<static_cast<unsigned>(mx::cdiv(k.cols, 32)), 1024, 0, stream>>>(k);
-    return ln::launched();
+    if (!sums) return CONV2D_OK;
+    return ln::launch_after(ln::bwd_join, static_cast<unsigned>(mx::cdiv(k.cols, 32)), 1024u, stream, k) == cudaSuccess ? CONV2D_OK : CONV2D_ERR_CUDA;
 }

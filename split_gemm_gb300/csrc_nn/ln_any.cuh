@@ -3,6 +3,7 @@
 #pragma once
 
 #include "ln_params.cuh"
+#include "ptx.cuh"
 
 namespace sgb {
 namespace ln {
@@ -149,6 +150,7 @@ __global__ void __launch_bounds__(1024) bwd_join(const BwdParams p)
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
     const int c = blockIdx.x * 32 + tx;
     float dw = 0.f, db = 0.f;
+    ptx::grid_dependency_wait();  // started early
     if (c < p.cols)
         for (int k = ty; k < p.chunks; k += 32) {
             dw += p.part[(2 * static_cast<int64_t>(k)) * p.cols + c];

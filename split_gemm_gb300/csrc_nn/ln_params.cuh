@@ -110,6 +110,31 @@ __host__ __device__ constexpr int64_t row_blocks(int64_t rows, RowShape s, int r
     return n < SMS * resident ? n : SMS * resident;
 }
 
+// Backward: each block also writes a part of the sums over the rows, as many bytes as two rows of them; so blocks take four rows
+// at least where that leaves one to an SM.
+__host__ __device__ constexpr int64_t bwd_blocks(int64_t rows, RowShape s)
+{
+    const int64_t n = row_blocks(rows, s, bwd_resident(s));
+    const int64_t fourth = mx::cdiv<int64_t>(rows, int64_t(32) * rows_per_block(s)) * 8, few = fourth > SMS ? fourth : SMS;
+    return n < few ? n : few;
+}
+
+// Launches a kernel that starts while the one before it on the stream ends, and waits for it by itself (griddepcontrol.wait).
+template <typename... P, typename... A>
+cudaError_t launch_after(void (*kernel)(P...), unsigned grid, unsigned threads, cudaStream_t stream, A... args)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr{};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Lets a kernel have `bytes` of dynamic shared memory; asked of the driver once per device.
 template <typename K>
 bool allow_smem(K kernel, int bytes, std::atomic<uint64_t>& done)

@@ -18,12 +18,12 @@ from ._rows import DTYPE_CODES, check_out_dtype, check_vector, empty_on, library
 from .mxfp4 import Mxfp4, mxfp4_empty
 
 
-def _fwd(y, x, layout, weight, bias, eps, mean, rstd, stream) -> None:
+def _fwd(y, x, layout, weight, bias, eps, mean_ptr, rstd_ptr, stream) -> None:
     rows, cols, x_stride, y_stride = layout
     params = LayerNormParams(rows, cols, x_stride, y_stride, DTYPE_CODES[x.dtype], DTYPE_CODES[y.dtype], eps)
     rc = library().layer_norm_fwd(
         ctypes.byref(params), x.data_ptr(), check_vector(weight, "weight", cols, x), check_vector(bias, "bias", cols, x),
-        y.data_ptr(), check_vector(mean, "mean", rows, x), check_vector(rstd, "rstd", rows, x), stream_handle(x, stream))
+        y.data_ptr(), mean_ptr, rstd_ptr, stream_handle(x, stream))
     if rc:
         raise Conv2dError(rc, "layer_norm_fwd")
 
@@ -36,7 +36,8 @@ def layer_norm_fwd_into(y, x, weight=None, bias=None, eps: float = 1e-5, *, mean
     if y.shape != x.shape:
         raise ValueError(f"y must be {list(x.shape)}, got {list(y.shape)}")
     same_device(y, "y", x)
-    _fwd(y, x, (rows, cols, x_stride, y_stride), weight, bias, eps, mean, rstd, stream)
+    _fwd(y, x, (rows, cols, x_stride, y_stride), weight, bias, eps, check_vector(mean, "mean", rows, x),
+         check_vector(rstd, "rstd", rows, x), stream)
 
 
 def layer_norm_fwd(x, weight=None, bias=None, eps: float = 1e-5, *, out_dtype=None, stream=None):
@@ -49,7 +50,7 @@ def layer_norm_fwd(x, weight=None, bias=None, eps: float = 1e-5, *, out_dtype=No
     y = empty_on(stream, shape, out_dtype, device)
     mean = empty_on(stream, shape[:-1], torch.float32, device)
     rstd = empty_on(stream, shape[:-1], torch.float32, device)
-    _fwd(y, x, (rows, cols, x_stride, cols), weight, bias, eps, mean, rstd, stream)
+    _fwd(y, x, (rows, cols, x_stride, cols), weight, bias, eps, mean.data_ptr(), rstd.data_ptr(), stream)
     return y, mean, rstd
 
 
@@ -61,42 +62,50 @@ def layer_norm_bwd_workspace_bytes(x, dy) -> int:
     return int(library().layer_norm_bwd_workspace_bytes(ctypes.byref(params)))
 
 
-def layer_norm_bwd_into(dx, dweight, dbias, dy, x, mean, rstd, weight=None, *, workspace=None, stream=None) -> None:
-    """Writes the gradients for the output gradient ``dy`` (x's shape): ``dx`` (x's shape and type, dense) and the
-    fp32 ``dweight`` and ``dbias`` [C] (either may be None: not computed).  Asynchronous."""
-    rows, cols, x_stride = rows_of(x, "x")
+def _bwd(dx, dw_ptr, db_ptr, dy, x, layout, mean, rstd, weight, workspace, stream) -> None:
+    rows, cols, x_stride = layout
     _, _, dy_stride = rows_of(dy, "dy")
-    shape = x.shape
-    if dy.shape != shape:
-        raise ValueError(f"dy must be {list(shape)}, got {list(dy.shape)}")
-    if dx.shape != shape or dx.dtype != x.dtype or not dx.is_cuda or not dx.is_contiguous():
-        raise ValueError(f"dx must be a contiguous CUDA tensor of {list(shape)}, {x.dtype}")
-    same_device(dx, "dx", x)
+    if dy.shape != x.shape:
+        raise ValueError(f"dy must be {list(x.shape)}, got {list(dy.shape)}")
     same_device(dy, "dy", x)
     if mean is None or rstd is None:
         raise ValueError("mean and rstd of the forward pass are needed")
     params = ctypes.byref(LayerNormParams(rows, cols, x_stride, dy_stride, DTYPE_CODES[x.dtype], DTYPE_CODES[dy.dtype], 0.0))
     lib = library()
-    if workspace is None and (dweight is not None or dbias is not None):
-        workspace = empty_on(stream, (lib.layer_norm_bwd_workspace_bytes(params),), torch.uint8, x.device)
-    ws_ptr, ws_len = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel() * workspace.element_size())
+    ws_ptr, ws_len = None, 0
+    if workspace is not None:
+        ws_ptr, ws_len = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+    elif dw_ptr or db_ptr:
+        ws_len = lib.layer_norm_bwd_workspace_bytes(params)
+        workspace = empty_on(stream, (ws_len,), torch.uint8, x.device)
+        ws_ptr = workspace.data_ptr()
     rc = lib.layer_norm_bwd(
         params, dy.data_ptr(), x.data_ptr(), check_vector(mean, "mean", rows, x), check_vector(rstd, "rstd", rows, x),
-        check_vector(weight, "weight", cols, x), dx.data_ptr(), check_vector(dweight, "dweight", cols, x),
-        check_vector(dbias, "dbias", cols, x), ws_ptr, ws_len, stream_handle(x, stream))
+        check_vector(weight, "weight", cols, x), dx.data_ptr(), dw_ptr, db_ptr, ws_ptr, ws_len, stream_handle(x, stream))
     if rc:
         raise Conv2dError(rc, "layer_norm_bwd")
+
+
+def layer_norm_bwd_into(dx, dweight, dbias, dy, x, mean, rstd, weight=None, *, workspace=None, stream=None) -> None:
+    """Writes the gradients for the output gradient ``dy`` (x's shape): ``dx`` (x's shape and type, dense) and the
+    fp32 ``dweight`` and ``dbias`` [C] (either may be None: not computed).  Asynchronous."""
+    layout = rows_of(x, "x")
+    if dx.shape != x.shape or dx.dtype != x.dtype or not dx.is_cuda or not dx.is_contiguous():
+        raise ValueError(f"dx must be a contiguous CUDA tensor of {list(x.shape)}, {x.dtype}")
+    same_device(dx, "dx", x)
+    _bwd(dx, check_vector(dweight, "dweight", layout[1], x), check_vector(dbias, "dbias", layout[1], x), dy, x, layout, mean, rstd,
+         weight, workspace, stream)
 
 
 def layer_norm_bwd(dy, x, mean, rstd, weight=None, *, workspace=None, stream=None):
     """Returns (dx, dweight, dbias) for y = layer_norm_fwd(x, weight, bias): dx of x's shape and type, dweight and
     dbias [C] fp32, summed over all rows in a fixed order."""
-    _, cols, _ = rows_of(x, "x")
+    layout = rows_of(x, "x")
     device = x.device
     dx = empty_on(stream, x.shape, x.dtype, device)
-    dweight = empty_on(stream, (cols,), torch.float32, device)
-    dbias = empty_on(stream, (cols,), torch.float32, device)
-    layer_norm_bwd_into(dx, dweight, dbias, dy, x, mean, rstd, weight, workspace=workspace, stream=stream)
+    dweight = empty_on(stream, (layout[1],), torch.float32, device)
+    dbias = empty_on(stream, (layout[1],), torch.float32, device)
+    _bwd(dx, dweight.data_ptr(), dbias.data_ptr(), dy, x, layout, mean, rstd, weight, workspace, stream)
     return dx, dweight, dbias
 
 
