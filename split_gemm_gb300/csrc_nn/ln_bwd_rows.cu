@@ -14,11 +14,12 @@ int start_bwd_as(const BwdParams& p, RowShape s, int grid, cudaStream_t stream)
     constexpr int join = G ? 2 * E * 4 : 0;  // a block's sums by row and column
     constexpr int per_thread = ring > join ? ring : join;
     const auto kernel = bwd_rows<TX, TY, VEC, E, G, MOST, SUMS, WHOLE>;
-    if (!allow_smem(kernel, per_thread * MOST, done)) return CONV2D_ERR_CUDA;
+    if (!mx::allow_smem(kernel, per_thread * MOST, done)) return CONV2D_ERR_CUDA;
     const int threads = block_threads(s);
-    kernel<<<static_cast<unsigned>(grid), threads, per_thread * threads, stream>>>(static_cast<const TY*>(p.dy), static_cast<const TX*>(p.x),
-                                                                                   static_cast<TX*>(p.dx), p);
-    return cudaGetLastError() == cudaSuccess ? CONV2D_OK : CONV2D_ERR_CUDA;
+    return mx::launch(kernel, grid, threads, per_thread * threads, stream, 1, static_cast<const TY*>(p.dy), static_cast<const TX*>(p.x),
+                      static_cast<TX*>(p.dx), p) == cudaSuccess
+               ? CONV2D_OK
+               : CONV2D_ERR_CUDA;
 }
 
 template <typename TX, typename TY, int VEC, int E, int G, int MOST, bool SUMS>

@@ -12,11 +12,12 @@ int start_fwd_as(const FwdParams& p, RowShape s, cudaStream_t stream)
     constexpr int V = VEC == 1 ? 8 : VEC;
     constexpr int per_thread = VEC > 1 ? Ring<TX, V, E / V, ring_depth(RowShape{G ? G : MOST, E, MOST}, sizeof(TX), 0)>::THREAD_BYTES : 0;
     const auto kernel = fwd_rows<TX, TY, VEC, E, G, MOST, WHOLE>;
-    if (!allow_smem(kernel, per_thread * MOST, done)) return CONV2D_ERR_CUDA;
+    if (!mx::allow_smem(kernel, per_thread * MOST, done)) return CONV2D_ERR_CUDA;
     const int64_t grid = row_blocks(std::is_same_v<TY, void> ? p.padded_rows : p.rows, s, fwd_resident(s));
     const int threads = block_threads(s);
-    kernel<<<static_cast<unsigned>(grid), threads, per_thread * threads, stream>>>(static_cast<const TX*>(p.x), static_cast<TY*>(p.y), p);
-    return cudaGetLastError() == cudaSuccess ? CONV2D_OK : CONV2D_ERR_CUDA;
+    return mx::launch(kernel, grid, threads, per_thread * threads, stream, 1, static_cast<const TX*>(p.x), static_cast<TY*>(p.y), p) == cudaSuccess
+               ? CONV2D_OK
+               : CONV2D_ERR_CUDA;
 }
 
 template <typename TX, typename TY, int VEC, int E, int G, int MOST>

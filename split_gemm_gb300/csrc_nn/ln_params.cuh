@@ -1,8 +1,6 @@
 // Kernel parameters of the layer normalisation kernels.
 #pragma once
 
-#include <atomic>
-
 #include "mx_common.cuh"
 
 namespace sgb {
@@ -117,36 +115,6 @@ __host__ __device__ constexpr int64_t bwd_blocks(int64_t rows, RowShape s)
     const int64_t n = row_blocks(rows, s, bwd_resident(s));
     const int64_t fourth = mx::cdiv<int64_t>(rows, int64_t(32) * rows_per_block(s)) * 8, few = fourth > SMS ? fourth : SMS;
     return n < few ? n : few;
-}
-
-// Launches a kernel that starts while the one before it on the stream ends, and waits for it by itself (griddepcontrol.wait).
-template <typename... P, typename... A>
-cudaError_t launch_after(void (*kernel)(P...), unsigned grid, unsigned threads, cudaStream_t stream, A... args)
-{
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(threads);
-    cfg.stream = stream;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
-// Lets a kernel have `bytes` of dynamic shared memory; asked of the driver once per device.
-template <typename K>
-bool allow_smem(K kernel, int bytes, std::atomic<uint64_t>& done)
-{
-    if (bytes <= 40 * 1024) return true;  // 48 KB with the static arrays needs no asking
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return false;
-    const uint64_t bit = uint64_t(1) << (dev & 63);
-    if (dev < 64 && (done.load(std::memory_order_acquire) & bit)) return true;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
-    if (dev < 64) done.fetch_or(bit, std::memory_order_release);
-    return true;
 }
 
 // Launches by element types (one translation unit each); `vec`: rows can be read and written in vectors.

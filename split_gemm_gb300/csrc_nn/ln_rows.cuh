@@ -305,6 +305,8 @@ __global__ void __launch_bounds__(MOST, FWD_RESIDENT<G, E, MOST>) fwd_rows(const
             ptx::cp_async_commit();
         }
     };
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
 #pragma unroll
     for (int k = 0; k < DEPTH; ++k) ask(k, first + k * step);
 
@@ -407,6 +409,8 @@ __global__ void __launch_bounds__(MOST, BWD_RESIDENT<G, E, MOST>) bwd_rows(const
             ptx::cp_async_commit();
         }
     };
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
 #pragma unroll
     for (int k = 0; k < DEPTH; ++k) ask(k, first + k * step);
     float mean = first < p.rows ? __ldg(p.mean + first) : 0.f, rstd = first < p.rows ? __ldg(p.rstd + first) : 0.f;
@@ -419,7 +423,6 @@ __global__ void __launch_bounds__(MOST, BWD_RESIDENT<G, E, MOST>) bwd_rows(const
 #pragma unroll
             for (int i = 0; i < H; ++i) dw[u][i] = db[u][i] = make_float2(0.f, 0.f);
     }
-    ptx::grid_launch_dependents();  // the join may get ready
     int slot = 0, flip = 0;
     for (int64_t r = first, r_lead = lead; r_lead < p.rows; r += step, r_lead += step, flip ^= 1) {
         // Lanes past the last row take a row of zeros, so that they add nothing.

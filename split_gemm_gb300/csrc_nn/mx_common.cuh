@@ -2,6 +2,7 @@
 // blocks of 32, E8M0 scales) and small helpers shared by the kernels of this folder.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 
 #include <cuda_bf16.h>
@@ -86,6 +87,41 @@ __device__ __forceinline__ void from_float(float& d, float v) { d = v; }
 __device__ __forceinline__ void from_float(__nv_bfloat16& d, float v) { d = __float2bfloat16_rn(v); }
 
 __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v) & 0x7fffffffu; }
+
+// Launches a kernel that may get ready while the one before it on the stream ends; it waits for that one itself
+// (griddepcontrol.wait) before it touches global memory.  cluster > 1: in clusters of so many blocks.
+template <typename... P, typename... A>
+cudaError_t launch(void (*kernel)(P...), int64_t grid, int threads, int smem, cudaStream_t stream, int cluster, A... args)
+{
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2]{};
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+// Lets a kernel have `bytes` of dynamic shared memory; asked of the driver once per device.
+template <typename K>
+bool allow_smem(K kernel, int bytes, std::atomic<uint64_t>& done)
+{
+    if (bytes <= 40 * 1024) return true;  // 48 KB with the static arrays needs no asking
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    const uint64_t bit = uint64_t(1) << (dev & 63);
+    if (dev < 64 && (done.load(std::memory_order_acquire) & bit)) return true;
+    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
+    if (dev < 64) done.fetch_or(bit, std::memory_order_release);
+    return true;
+}
 
 }  // namespace mx
 }  // namespace sgb

@@ -58,7 +58,7 @@ __device__ __forceinline__ void tile_of(int i, const PairParams& p, int& tm, int
 }
 
 template <typename T>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
+__global__ void __launch_bounds__(W_THREADS, 1)
     pair_kernel(const __grid_constant__ CUtensorMap tm_a, const __grid_constant__ CUtensorMap tm_b,
                 const __grid_constant__ CUtensorMap tm_sa, const __grid_constant__ CUtensorMap tm_sb,
                 const __grid_constant__ CUtensorMap tm_y, const PairParams p)
@@ -79,6 +79,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
     const int cluster = static_cast<int>(ptx::cluster_id_x()), clusters = static_cast<int>(ptx::cluster_count_x());
     const int tiles = p.m_tiles * p.n_tiles;
 
+    if (threadIdx.x < 4) ptx::prefetch_tensormap(threadIdx.x == 0 ? &tm_a : threadIdx.x == 1 ? &tm_b : threadIdx.x == 2 ? &tm_sa : &tm_sb);
     if (threadIdx.x == 0) {
         for (int i = 0; i < W_STAGES; ++i) {
             ptx::mbar_init(&full[i], 1);
@@ -98,6 +99,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(W_THREADS, 1)
     ptx::cluster_sync();
     ptx::tc_fence_after();
     const uint32_t acc = *tmem_slot, sf = acc + W_TILE;
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
 
     if (warp == 0 && lane == 0) {
         const uint32_t full0 = ptx::mapa_shared(ptx::smem_addr(full), 0);

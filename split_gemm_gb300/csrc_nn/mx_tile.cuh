@@ -72,6 +72,23 @@ struct TileConfig {
     static constexpr int SMEM = RING + 1024 + 256;                // + alignment, barriers
 };
 
+// The sum of four values over the S CTAs of the cluster, in their order; the loads are on their way together.
+template <int S>
+__device__ __forceinline__ float4 joined(uint32_t at)
+{
+    float4 v[S];
+#pragma unroll
+    for (int k = 0; k < S; ++k) v[k] = ptx::ld_cluster_v4(ptx::mapa_shared(at, k));
+#pragma unroll
+    for (int k = 1; k < S; ++k) {
+        v[0].x += v[k].x;
+        v[0].y += v[k].y;
+        v[0].z += v[k].z;
+        v[0].w += v[k].w;
+    }
+    return v[0];
+}
+
 template <int BN, bool SWAP, typename T>
 __global__ void __launch_bounds__(T_THREADS) tile_kernel(const __grid_constant__ CUtensorMap tm_p,
                                                          const __grid_constant__ CUtensorMap tm_q, const TileParams p)
@@ -91,6 +108,7 @@ __global__ void __launch_bounds__(T_THREADS) tile_kernel(const __grid_constant__
     const int s0 = static_cast<int>(static_cast<int64_t>(rank) * p.stages / p.splits);
     const int s1 = static_cast<int>(static_cast<int64_t>(rank + 1) * p.stages / p.splits);
 
+    if (threadIdx.x < 2) ptx::prefetch_tensormap(threadIdx.x ? &tm_q : &tm_p);
     if (threadIdx.x == 0) {
         for (int i = 0; i < C::STAGES; ++i) {
             ptx::mbar_init(&full[i], 1);
@@ -108,6 +126,8 @@ __global__ void __launch_bounds__(T_THREADS) tile_kernel(const __grid_constant__
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t acc = *tmem_slot, sf = acc + (BN < 32 ? 32 : BN);
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
 
     if (warp == 4 && lane == 0) {
         int it = 0;
@@ -198,15 +218,10 @@ __global__ void __launch_bounds__(T_THREADS) tile_kernel(const __grid_constant__
             const int rows = SWAP ? p.q_rows : p.p_rows, cols = SWAP ? p.p_rows : p.q_rows;
             if (row >= rows || col >= cols) continue;
             const uint32_t at = base + static_cast<uint32_t>(sr * C::PITCH + sc) * 4u;
-            float4 s = ptx::ld_cluster_v4(ptx::mapa_shared(at, 0));
-#pragma unroll 7
-            for (int k = 1; k < p.splits; ++k) {
-                const float4 t = ptx::ld_cluster_v4(ptx::mapa_shared(at, k));
-                s.x += t.x;
-                s.y += t.y;
-                s.z += t.z;
-                s.w += t.w;
-            }
+            const float4 s = p.splits == 1   ? *reinterpret_cast<const float4*>(staged + sr * C::PITCH + sc)
+                             : p.splits == 2 ? joined<2>(at)
+                             : p.splits == 4 ? joined<4>(at)
+                                             : joined<8>(at);
             float v[4] = {s.x, s.y, s.z, s.w};
             const bool whole = col + 4 <= cols;
 #pragma unroll

@@ -2,6 +2,7 @@
 #include "mxfp4.h"
 
 #include "mx_common.cuh"
+#include "ptx.cuh"
 
 namespace sgb {
 namespace mx {
@@ -49,6 +50,8 @@ __global__ void __launch_bounds__(Q_THREADS) quantize_kernel(const T* __restrict
     const int rows = static_cast<int>(p.rows - r0 < Q_TILE ? p.rows - r0 : Q_TILE);
     const int cols = static_cast<int>(p.cols - c0 < Q_TILE ? p.cols - c0 : Q_TILE);
     const T* src = x + r0 * p.x_stride + c0;
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
     if constexpr (VEC) {
         constexpr int V = 16 / sizeof(T), PER = Q_TILE / V, STEP = Q_THREADS / PER;
         const int c = threadIdx.x % PER * V;
@@ -168,6 +171,8 @@ __global__ void __launch_bounds__(D_THREADS) dequantize_kernel(const uint8_t* __
     const int64_t i0 = int64_t(blockIdx.x) * D_THREADS + threadIdx.x;
     int64_t r = i0 / words, w = i0 - r * words;
     const int lane = threadIdx.x & 31;
+    ptx::grid_dependency_wait();
+    ptx::grid_launch_dependents();
     for (int64_t i = i0; i - lane < n; i += step) {  // a warp's lanes stay together
         float2 v[4];
         if (i < n) {
@@ -219,15 +224,14 @@ __global__ void __launch_bounds__(D_THREADS) dequantize_kernel(const uint8_t* __
     }
 }
 
-// Sets the kernel's shared-memory limit and launches one block to a tile.
+// One block to a tile.
 template <typename T, bool VEC>
 int launch_quantize(const T* x, const QuantParams& p, cudaStream_t stream)
 {
+    static std::atomic<uint64_t> done{0};
     constexpr int smem = sizeof(QuantTile<T>);
-    if (smem > 48 * 1024 && cudaFuncSetAttribute(quantize_kernel<T, VEC>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess)
-        return CONV2D_ERR_CUDA;
-    quantize_kernel<T, VEC><<<static_cast<unsigned>(p.row_tiles * p.col_tiles), Q_THREADS, smem, stream>>>(x, p);
-    return cudaGetLastError() == cudaSuccess ? CONV2D_OK : CONV2D_ERR_CUDA;
+    if (!allow_smem(quantize_kernel<T, VEC>, smem, done)) return CONV2D_ERR_CUDA;
+    return launch(quantize_kernel<T, VEC>, p.row_tiles * p.col_tiles, Q_THREADS, smem, stream, 1, x, p) == cudaSuccess ? CONV2D_OK : CONV2D_ERR_CUDA;
 }
 
 template <typename T>
@@ -243,12 +247,9 @@ int dequantize(const uint8_t* data, const uint8_t* scales, void* y, int64_t rows
 {
     // Eight blocks to an SM at most: they stay, and take one group after another.
     const int64_t need = cdiv<int64_t>(rows * cdiv<int64_t>(cols, BLOCK) * 4, D_THREADS);
-    const unsigned grid = static_cast<unsigned>(need < SMS * 8 ? need : SMS * 8);
-    if (cols % 8 == 0)
-        dequantize_kernel<T, true><<<grid, D_THREADS, 0, stream>>>(data, scales, static_cast<T*>(y), rows, cols);
-    else
-        dequantize_kernel<T, false><<<grid, D_THREADS, 0, stream>>>(data, scales, static_cast<T*>(y), rows, cols);
-    return cudaGetLastError() == cudaSuccess ? CONV2D_OK : CONV2D_ERR_CUDA;
+    const int64_t grid = need < SMS * 8 ? need : SMS * 8;
+    const auto kernel = cols % 8 == 0 ? dequantize_kernel<T, true> : dequantize_kernel<T, false>;
+    return launch(kernel, grid, D_THREADS, 0, stream, 1, data, scales, static_cast<T*>(y), rows, cols) == cudaSuccess ? CONV2D_OK : CONV2D_ERR_CUDA;
 }
 
 }  // namespace mx

@@ -48,19 +48,6 @@ struct Operand {
     int64_t rows;
 };
 
-// Sets the kernel's shared-memory limit once per device.
-template <typename K>
-bool allow_smem(K kernel, int bytes, std::atomic<uint64_t>& done)
-{
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return false;
-    const uint64_t bit = uint64_t(1) << (dev & 63);
-    if (dev < 64 && (done.load(std::memory_order_acquire) & bit)) return true;
-    if (cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) return false;
-    if (dev < 64) done.fetch_or(bit, std::memory_order_release);
-    return true;
-}
-
 template <int BN, bool SWAP, typename T>
 int launch_tile(const Operand& P, const Operand& Q, TileParams& k, cudaStream_t stream)
 {
@@ -75,18 +62,8 @@ int launch_tile(const Operand& P, const Operand& Q, TileParams& k, cudaStream_t 
     k.splits = 1;
     while (k.splits < 8 && tiles * k.splits * 2 <= SMS && k.stages >= 4 * k.splits) k.splits *= 2;
     if (tiles * k.splits > INT32_MAX) return CONV2D_ERR_UNSUPPORTED;
-    cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(tiles * k.splits));
-    cfg.blockDim = dim3(T_THREADS);
-    cfg.dynamicSmemBytes = C::SMEM;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr{};
-    attr.id = cudaLaunchAttributeClusterDimension;
-    attr.val.clusterDim.x = static_cast<unsigned>(k.splits);
-    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, tile_kernel<BN, SWAP, T>, tm_p, tm_q, k) == cudaSuccess ? CONV2D_OK : CONV2D_ERR_CUDA;
+    return launch(tile_kernel<BN, SWAP, T>, tiles * k.splits, T_THREADS, C::SMEM, stream, k.splits, tm_p, tm_q, k) == cudaSuccess ? CONV2D_OK
+                                                                                                                           : CONV2D_ERR_CUDA;
 }
 
 // Map of an operand's scales: tiles of 128 words, `tiles` of them to a row of tiles; boxes of 2 x box_rows tiles.
@@ -136,9 +113,8 @@ int launch_pair(const Operand& a, const Operand& b, const TileParams& k, cudaStr
         (p.tma_store && !encode_y(&tm_y, k.y, a.rows, b.rows, sizeof(T))))
         return CONV2D_ERR_CUDA;
     if (!allow_smem(pair_kernel<T>, W_SMEM, done)) return CONV2D_ERR_CUDA;
-    const unsigned grid = 2 * static_cast<unsigned>(tiles < SMS / 2 ? tiles : SMS / 2);
-    pair_kernel<T><<<grid, W_THREADS, W_SMEM, stream>>>(tm_a, tm_b, tm_sa, tm_sb, tm_y, p);
-    return cudaGetLastError() == cudaSuccess ? CONV2D_OK : CONV2D_ERR_CUDA;
+    const int64_t grid = 2 * (tiles < SMS / 2 ? tiles : SMS / 2);
+    return launch(pair_kernel<T>, grid, W_THREADS, W_SMEM, stream, 2, tm_a, tm_b, tm_sa, tm_sb, tm_y, p) == cudaSuccess ? CONV2D_OK : CONV2D_ERR_CUDA;
 }
 
 template <typename T>
