@@ -39,7 +39,7 @@ def rows_of(t, name) -> Tuple[int, int, int]:
     if cols < 1:
         raise ValueError(f"{name} must have at least one column")
     if t.is_contiguous():
-        return t.numel() // cols, cols, cols
+        return (shape[0] if len(shape) == 2 else t.numel() // cols), cols, cols
     strides = t.stride()
     if strides[-1] != 1 and cols > 1:
         raise ValueError(f"{name}'s last dimension must be dense")
@@ -62,15 +62,16 @@ def check_vector(t, name, n, like) -> Optional[int]:
     """Device pointer of an optional dense fp32 [n] tensor on the device of ``like``."""
     if t is None:
         return None
+    if isinstance(t, torch.Tensor) and t.dtype is torch.float32 and t.numel() == n and t.get_device() == like.get_device() \
+            and t.is_contiguous():
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.get_device() != like.get_device():
         raise ValueError(f"{name} must be a CUDA tensor on {like.device}")
     if t.dtype != torch.float32:
         raise TypeError(f"{name} must be torch.float32, got {t.dtype}")
-    if t.numel() != n or not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous with {n} elements")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous with {n} elements")
 
 
 def same_device(t, name, like) -> None:

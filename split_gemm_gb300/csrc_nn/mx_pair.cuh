@@ -100,7 +100,6 @@ __global__ void __launch_bounds__(W_THREADS, 1)
     ptx::tc_fence_after();
     const uint32_t acc = *tmem_slot, sf = acc + W_TILE;
     ptx::grid_dependency_wait();
-    ptx::grid_launch_dependents();
 
     if (warp == 0 && lane == 0) {
         const uint32_t full0 = ptx::mapa_shared(ptx::smem_addr(full), 0);

@@ -127,7 +127,6 @@ __global__ void __launch_bounds__(T_THREADS) tile_kernel(const __grid_constant__
     ptx::tc_fence_after();
     const uint32_t acc = *tmem_slot, sf = acc + (BN < 32 ? 32 : BN);
     ptx::grid_dependency_wait();
-    ptx::grid_launch_dependents();
 
     if (warp == 4 && lane == 0) {
         int it = 0;

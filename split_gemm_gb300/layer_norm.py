@@ -44,12 +44,18 @@ def layer_norm_fwd(x, weight=None, bias=None, eps: float = 1e-5, *, out_dtype=No
     """Returns (y, mean, rstd): y of x's shape and ``out_dtype`` (default: x's type), and the fp32 statistics
     of each row (the shape of x without its last dimension) that the backward pass takes."""
     rows, cols, x_stride = rows_of(x, "x")
-    out_dtype = x.dtype if out_dtype is None else out_dtype
-    check_out_dtype(out_dtype)
+    if out_dtype is None:
+        out_dtype = x.dtype
+    else:
+        check_out_dtype(out_dtype)
     shape, device = x.shape, x.device
-    y = empty_on(stream, shape, out_dtype, device)
-    mean = empty_on(stream, shape[:-1], torch.float32, device)
-    rstd = empty_on(stream, shape[:-1], torch.float32, device)
+    if stream is None:
+        y = torch.empty(shape, dtype=out_dtype, device=device)
+        mean = torch.empty(shape[:-1], dtype=torch.float32, device=device)
+        rstd = torch.empty(shape[:-1], dtype=torch.float32, device=device)
+    else:
+        y, mean, rstd = (empty_on(stream, s, t, device) for s, t in
+                         ((shape, out_dtype), (shape[:-1], torch.float32), (shape[:-1], torch.float32)))
     _fwd(y, x, (rows, cols, x_stride, cols), weight, bias, eps, mean.data_ptr(), rstd.data_ptr(), stream)
     return y, mean, rstd
 

@@ -38,9 +38,11 @@ class Mxfp4(NamedTuple):
 def mxfp4_empty(rows: int, cols: int, device, *, stream=None) -> Mxfp4:
     """An unwritten quantised matrix, for mxfp4_quantize_into."""
     blocks = (cols + 31) // 32
-    data = empty_on(stream, (rows, 16 * blocks), torch.uint8, device)
-    scales = empty_on(stream, ((rows + 127) // 128 * ((blocks + 3) // 4) * 512,), torch.uint8, device)
-    return Mxfp4(data, scales, rows, cols)
+    scales = (rows + 127) // 128 * ((blocks + 3) // 4) * 512
+    if stream is None:
+        return Mxfp4(torch.empty((rows, 16 * blocks), dtype=torch.uint8, device=device),
+                     torch.empty((scales,), dtype=torch.uint8, device=device), rows, cols)
+    return Mxfp4(empty_on(stream, (rows, 16 * blocks), torch.uint8, device), empty_on(stream, (scales,), torch.uint8, device), rows, cols)
 
 
 def _check_mx(q, name) -> Tuple[int, int]:
@@ -48,16 +50,18 @@ def _check_mx(q, name) -> Tuple[int, int]:
     if not isinstance(q, Mxfp4):
         raise TypeError(f"{name} must be an Mxfp4")
     data, scales, rows, cols = q
+    blocks = (cols + 31) // 32
+    if data.dtype is torch.uint8 and scales.dtype is torch.uint8 and data.is_cuda and scales.get_device() == data.get_device() \
+            and data.numel() == rows * 16 * blocks and scales.numel() == (rows + 127) // 128 * ((blocks + 3) // 4) * 512 \
+            and data.is_contiguous() and scales.is_contiguous():
+        return data.data_ptr(), scales.data_ptr()
     if data.dtype != torch.uint8 or scales.dtype != torch.uint8:
         raise TypeError(f"{name}.data and {name}.scales must be torch.uint8")
     if not data.is_cuda or scales.get_device() != data.get_device():
         raise ValueError(f"{name}.data and {name}.scales must be CUDA tensors of one device")
-    blocks = (cols + 31) // 32
-    if data.numel() != rows * 16 * blocks or scales.numel() != (rows + 127) // 128 * ((blocks + 3) // 4) * 512:
-        raise ValueError(f"{name}.data or {name}.scales has the wrong size for {rows} x {cols}")
     if not data.is_contiguous() or not scales.is_contiguous():
         raise ValueError(f"{name}.data and {name}.scales must be contiguous")
-    return data.data_ptr(), scales.data_ptr()
+    raise ValueError(f"{name}.data or {name}.scales has the wrong size for {rows} x {cols}")
 
 
 def _quantize(x, layout, ptr, ptr_t, stream) -> None:
@@ -91,7 +95,7 @@ def mxfp4_quantize_into(q, x, q_t=None, *, stream=None) -> None:
 
 def _new(rows, cols, device, stream):
     q = mxfp4_empty(rows, cols, device, stream=stream)
-    return q, (q.data.data_ptr(), q.scales.data_ptr())
+    return q, (q[0].data_ptr(), q[1].data_ptr())
 
 
 def mxfp4_quantize(x, *, transpose: bool = False, stream=None) -> Mxfp4:
@@ -161,7 +165,8 @@ def mxfp4_matmul(a: Mxfp4, b: Mxfp4, bias=None, *, relu: bool = False, out_dtype
     """Returns a b^T + bias as a new [a.rows, b.rows] tensor of ``out_dtype`` (asynchronous)."""
     ptrs = _operands(a, b)
     check_out_dtype(out_dtype)
-    y = empty_on(stream, (a.rows, b.rows), out_dtype, a.data.device)
+    shape, device = (a.rows, b.rows), a.data.device
+    y = torch.empty(shape, dtype=out_dtype, device=device) if stream is None else empty_on(stream, shape, out_dtype, device)
     _matmul(y, ptrs, a, b, bias, relu, stream)
     return y
 
