@@ -236,12 +236,25 @@ __global__ void __launch_bounds__(W_THREADS, 1)
                     }
                 } else {
                     __syncwarp();
+                    // rows of y that begin anywhere: 16-byte stores from the first aligned place on, the rest one by one
+                    constexpr int EV = 16 / sizeof(T);  // eight lanes to a row of the box
                     T* y = static_cast<T*>(p.y);
-                    for (int e = lane; e < 32 * COLS; e += 32) {
-                        const int r = e / COLS, c = e % COLS;
-                        const int byte = r * 128 + ((c * static_cast<int>(sizeof(T))) ^ ((r & 7) << 4));
-                        if (row0 + r < p.m && col0 + b * COLS + c < p.n)
-                            y[static_cast<int64_t>(row0 + r) * p.ldy + col0 + b * COLS + c] = *reinterpret_cast<const T*>(box + byte);
+                    const int c0 = col0 + b * COLS, left_c = p.n - c0, valid = left_c < COLS ? left_c : COLS;
+                    auto value = [&](int r, int c) {
+                        return *reinterpret_cast<const T*>(box + r * 128 + ((c * static_cast<int>(sizeof(T))) ^ ((r & 7) << 4)));
+                    };
+                    for (int r = lane / 8; r < 32 && row0 + r < p.m; r += 4) {
+                        const int64_t g = static_cast<int64_t>(row0 + r) * p.ldy + c0;  // y is aligned to 16 bytes
+                        const int head = static_cast<int>(-g & (EV - 1)), at_c = head + lane % 8 * EV;
+                        if (at_c + EV <= valid) {
+                            alignas(16) T o[EV];
+#pragma unroll
+                            for (int i = 0; i < EV; ++i) o[i] = value(r, at_c + i);
+                            *reinterpret_cast<uint4*>(y + g + at_c) = *reinterpret_cast<const uint4*>(o);
+                        }
+                        if (lane % 8 < head && lane % 8 < valid) y[g + lane % 8] = value(r, lane % 8);
+                        const int tail = valid > head ? head + (valid - head) / EV * EV : valid;
+                        if (tail + lane % 8 < valid) y[g + tail + lane % 8] = value(r, tail + lane % 8);
                     }
                     __syncwarp();
                 }

@@ -21,19 +21,22 @@ __host__ __device__ constexpr uint32_t idesc_mxf4(int m, int n, int sf_id)
 // One stage of one CTA, up to 256 reduction elements, executed by a whole warp in uniform control flow: one elected
 // lane copies the scales to tensor memory and issues the MMAs (128 x N x 64, N <= 128).  `mmas` is 1 .. 4; the scale
 // tiles of 512 bytes lie at `sf_desc`, a's two in order of the reduction, then b's two, and go to the 16 columns
-// from sfa in the same order; the second ones are read for more than two MMAs only.  In one block, so that the election and the operands' moves to uniform registers are paid once.
+// from sfa in the same order; the second ones are read for more than two MMAs only.  b's rows begin at the 32 rows of
+// column `sfb_from` of a tile.  In one block, so that the election and the operands' moves to uniform registers are paid once.
 __device__ __forceinline__ void mma_mxf4_stage(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint64_t sf_desc, uint32_t sfa,
-                                               uint32_t idesc_lo, uint32_t idesc_hi, uint32_t accumulate, uint32_t mmas)
+                                               uint32_t sfb_from, uint32_t idesc_lo, uint32_t idesc_hi, uint32_t accumulate,
+                                               uint32_t mmas)
 {
     asm volatile(
         "{\n\t.reg .pred p, e, t, m1, m2, m3;\n\t.reg .b64 a1, a2, a3, b1, b2, b3, s1, s2, s3;\n\t"
-        ".reg .b32 f4, f8, f12;\n\t"
+        ".reg .b32 f4, f8, f12, q8, q12;\n\t"
         "setp.ne.b32 p, %7, 0;\n\t"
         "setp.eq.b32 t, 0, 0;\n\t"
         "add.s64 a1, %1, 2;\n\tadd.s64 a2, %1, 4;\n\tadd.s64 a3, %1, 6;\n\t"
         "add.s64 b1, %2, 2;\n\tadd.s64 b2, %2, 4;\n\tadd.s64 b3, %2, 6;\n\t"
         "add.s64 s1, %3, 32;\n\tadd.s64 s2, %3, 64;\n\tadd.s64 s3, %3, 96;\n\t"
         "add.s32 f4, %4, 4;\n\tadd.s32 f8, %4, 8;\n\tadd.s32 f12, %4, 12;\n\t"
+        "add.s32 q8, f8, %9;\n\tadd.s32 q12, f12, %9;\n\t"
         "elect.sync _|e, 0xffffffff;\n\t"
         "setp.gt.and.u32 m1, %8, 1, e;\n\t"
         "setp.gt.and.u32 m2, %8, 2, e;\n\t"
@@ -42,11 +45,11 @@ __device__ __forceinline__ void mma_mxf4_stage(uint32_t d_tmem, uint64_t a_desc,
         "@e tcgen05.cp.cta_group::1.32x128b.warpx4 [f8], s2;\n\t"
         "@m2 tcgen05.cp.cta_group::1.32x128b.warpx4 [f4], s1;\n\t"
         "@m2 tcgen05.cp.cta_group::1.32x128b.warpx4 [f12], s3;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %5, [%4], [f8], p;\n\t"
-        "@m1 tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], a1, b1, %6, [%4], [f8], t;\n\t"
-        "@m2 tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], a2, b2, %5, [f4], [f12], t;\n\t"
-        "@m3 tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], a3, b3, %6, [f4], [f12], t;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "l"(sf_desc), "r"(sfa), "r"(idesc_lo), "r"(idesc_hi), "r"(accumulate), "r"(mmas)
+        "@e tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], %1, %2, %5, [%4], [q8], p;\n\t"
+        "@m1 tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], a1, b1, %6, [%4], [q8], t;\n\t"
+        "@m2 tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], a2, b2, %5, [f4], [q12], t;\n\t"
+        "@m3 tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X [%0], a3, b3, %6, [f4], [q12], t;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "l"(sf_desc), "r"(sfa), "r"(idesc_lo), "r"(idesc_hi), "r"(accumulate), "r"(mmas), "r"(sfb_from)
         : "memory");
 }
 
@@ -121,6 +124,13 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const void* map, uin
         " [%0], [%1, {%3, %4}], [%2];" ::"r"(smem_addr(dst)),
         "l"(reinterpret_cast<uint64_t>(map)), "r"(bar_cl), "r"(c0), "r"(c1)
         : "memory");
+}
+
+__device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr)
+{
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
+    return v;
 }
 
 __device__ __forceinline__ float4 ld_cluster_v4(uint32_t cluster_addr)

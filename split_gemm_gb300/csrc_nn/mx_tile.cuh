@@ -72,25 +72,110 @@ struct TileConfig {
     static constexpr int SMEM = RING + 1024 + 256;                // + alignment, barriers
 };
 
-// The sum of four values over the S CTAs of the cluster, in their order; the loads are on their way together.
+// The sum of four values, or of one, over the S CTAs of the cluster, in their order; the loads are on their way together.
 template <int S>
-__device__ __forceinline__ float4 joined(uint32_t at)
+__device__ __forceinline__ float4 joined4(const float* at)
 {
-    float4 v[S];
+    if constexpr (S == 1) {
+        return *reinterpret_cast<const float4*>(at);
+    } else {
+        float4 v[S];
 #pragma unroll
-    for (int k = 0; k < S; ++k) v[k] = ptx::ld_cluster_v4(ptx::mapa_shared(at, k));
+        for (int k = 0; k < S; ++k) v[k] = ptx::ld_cluster_v4(ptx::mapa_shared(ptx::smem_addr(at), k));
 #pragma unroll
-    for (int k = 1; k < S; ++k) {
-        v[0].x += v[k].x;
-        v[0].y += v[k].y;
-        v[0].z += v[k].z;
-        v[0].w += v[k].w;
+        for (int k = 1; k < S; ++k) {
+            v[0].x += v[k].x;
+            v[0].y += v[k].y;
+            v[0].z += v[k].z;
+            v[0].w += v[k].w;
+        }
+        return v[0];
     }
-    return v[0];
+}
+template <int S>
+__device__ __forceinline__ float joined1(const float* at)
+{
+    if constexpr (S == 1) {
+        return *at;
+    } else {
+        float v[S];
+#pragma unroll
+        for (int k = 0; k < S; ++k) v[k] = ptx::ld_cluster_f32(ptx::mapa_shared(ptx::smem_addr(at), k));
+#pragma unroll
+        for (int k = 1; k < S; ++k) v[0] += v[k];
+        return v[0];
+    }
+}
+
+// Joins and writes this CTA's share of the tile, 128/S of P's rows, four elements of a row of y to a thread.
+template <int S, int BN, bool SWAP, typename T>
+__device__ __forceinline__ void write_share(float* staged, int rank, int p0, int q0, int q_valid, const TileParams& p)
+{
+    constexpr int SHARE = T_ROWS / S, PITCH = TileConfig<BN, SWAP>::PITCH;
+    constexpr int WIDTH = SWAP ? SHARE : BN;  // of a row of the share
+    static_assert(T_THREADS % (WIDTH / 4) == 0, "a thread keeps its columns");
+    // A thread keeps its four columns and goes down the rows.
+    const int r0 = rank * SHARE;
+    const int height = SWAP ? q_valid : SHARE;
+    const int rows = SWAP ? p.q_rows : p.p_rows, cols = SWAP ? p.p_rows : p.q_rows;  // of y
+    // rows and columns of the staged tile, and where they are in y
+    const int first_row = SWAP ? 0 : r0, first_col = SWAP ? r0 : 0, y_row = SWAP ? q0 : p0, y_col = SWAP ? p0 : q0;
+    const int left = rows - (y_row + first_row), n_rows = left < height ? left : height;
+    T* y = static_cast<T*>(p.y);
+    constexpr int LANES = WIDTH / 4;
+    const int c = first_col + threadIdx.x % LANES * 4, col = y_col + c;
+    if (col < cols) {
+        float bias[4] = {0.f, 0.f, 0.f, 0.f};
+        if (p.bias)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (col + i < cols) bias[i] = __ldg(p.bias + col + i);
+#pragma unroll 2
+        for (int r = threadIdx.x / LANES; r < n_rows; r += T_THREADS / LANES) {
+            float* at = staged + (first_row + r) * PITCH + c;
+            const float4 s = joined4<S>(at);
+            float v[4] = {s.x + bias[0], s.y + bias[1], s.z + bias[2], s.w + bias[3]};
+            if (p.relu)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (v[i] < 0.f) v[i] = 0.f;
+            T* out = y + static_cast<int64_t>(y_row + first_row + r) * p.ldy + col;
+            if (!p.vec_y) {
+                *reinterpret_cast<float4*>(at) = make_float4(v[0], v[1], v[2], v[3]);
+            } else if constexpr (sizeof(T) == 4) {
+                *reinterpret_cast<float4*>(out) = make_float4(v[0], v[1], v[2], v[3]);
+            } else {
+                const __nv_bfloat162 lo = __floats2bfloat162_rn(v[0], v[1]), hi = __floats2bfloat162_rn(v[2], v[3]);
+                *reinterpret_cast<uint2*>(out) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+            }
+        }
+    }
+    if (p.vec_y) return;
+    // Rows of y that begin anywhere: the finished values went back to where they lay (no other CTA reads this share), and
+    // leave in 16-byte stores from the first aligned place of each row on, the few before and after one by one.
+    __syncthreads();
+    constexpr int EV = 16 / sizeof(T), ROW_LANES = WIDTH / EV;
+    const int lane = threadIdx.x % ROW_LANES;
+    const int valid = cols - (y_col + first_col) < WIDTH ? cols - (y_col + first_col) : WIDTH;
+    for (int r = threadIdx.x / ROW_LANES; r < n_rows; r += T_THREADS / ROW_LANES) {
+        const float* from = staged + (first_row + r) * PITCH + first_col;
+        const int64_t g = static_cast<int64_t>(y_row + first_row + r) * p.ldy + y_col + first_col;  // y is aligned to 16 bytes
+        const int head = static_cast<int>(-g & (EV - 1));
+        const int at = head + lane * EV;
+        if (at + EV <= valid) {
+            alignas(16) T v[EV];
+#pragma unroll
+            for (int i = 0; i < EV; ++i) from_float(v[i], from[at + i]);
+            *reinterpret_cast<uint4*>(y + g + at) = *reinterpret_cast<const uint4*>(v);
+        }
+        for (int e = lane; e < head && e < valid; e += ROW_LANES) from_float(y[g + e], from[e]);
+        const int tail = valid > head ? head + (valid - head) / EV * EV : valid;
+        for (int e = tail + lane; e < valid; e += ROW_LANES) from_float(y[g + e], from[e]);
+    }
 }
 
 template <int BN, bool SWAP, typename T>
-__global__ void __launch_bounds__(T_THREADS) tile_kernel(const __grid_constant__ CUtensorMap tm_p,
+__global__ void __launch_bounds__(T_THREADS, 1) tile_kernel(const __grid_constant__ CUtensorMap tm_p,
                                                          const __grid_constant__ CUtensorMap tm_q, const TileParams p)
 {
     using C = TileConfig<BN, SWAP>;
@@ -162,7 +247,7 @@ __global__ void __launch_bounds__(T_THREADS) tile_kernel(const __grid_constant__
             const uint32_t st = ptx::smem_addr(ring + slot * C::STAGE);
             const int left = p.blocks - s * T_STAGE_BLOCKS;
             ptx::mma_mxf4_stage(acc, ptx::sw128_kmajor_desc(st), ptx::sw128_kmajor_desc(st + C::P_BYTES),
-                                ptx::plain_kmajor_desc(st + C::P_BYTES + C::Q_BYTES, 128, 128), sf + slot * C::SF_COLS,
+                                ptx::plain_kmajor_desc(st + C::P_BYTES + C::Q_BYTES, 128, 128), sf + slot * C::SF_COLS, q0 % TILE_ROWS / 32,
                                 ptx::idesc_mxf4(T_ROWS, BN, 0), ptx::idesc_mxf4(T_ROWS, BN, 2), it > 0,
                                 left >= T_STAGE_BLOCKS ? 4 : (left + 1) / 2);
             ptx::mma_commit_elect(&empty[slot]);
@@ -180,18 +265,23 @@ __global__ void __launch_bounds__(T_THREADS) tile_kernel(const __grid_constant__
     __syncthreads();  // also: the copies' thread has seen its last copy land
     if (warp < 4) {
         ptx::tc_fence_after();
-        for (int c = 0; c < q_valid; c += 16) {
-            uint32_t v[16];
-            ptx::tmem_ld_32x32b_x16(acc + (static_cast<uint32_t>(warp * 32) << 16) + c, v);
+        constexpr int STEP = BN < 64 ? 16 : 64;  // columns on their way at once
+        const int row = warp * 32 + lane;
+        for (int c = 0; c < q_valid; c += STEP) {
+            uint32_t v[STEP / 16][16];
+#pragma unroll
+            for (int k = 0; k < STEP / 16; ++k) ptx::tmem_ld_32x32b_x16(acc + (static_cast<uint32_t>(warp * 32) << 16) + c + 16 * k, v[k]);
             ptx::tmem_ld_wait();
-            const int row = warp * 32 + lane;
-            if constexpr (SWAP) {
 #pragma unroll
-                for (int i = 0; i < 16; ++i) staged[(c + i) * C::PITCH + row] = __uint_as_float(v[i]);
-            } else {
-                const uint32_t at = ptx::smem_addr(staged + row * C::PITCH + c);
+            for (int k = 0; k < STEP / 16; ++k) {
+                if constexpr (SWAP) {
 #pragma unroll
-                for (int i = 0; i < 4; ++i) ptx::st_shared_v4(at + 16 * i, v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                    for (int i = 0; i < 16; ++i) staged[(c + 16 * k + i) * C::PITCH + row] = __uint_as_float(v[k][i]);
+                } else {
+                    const uint32_t at = ptx::smem_addr(staged + row * C::PITCH + c + 16 * k);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) ptx::st_shared_v4(at + 16 * i, v[k][4 * i], v[k][4 * i + 1], v[k][4 * i + 2], v[k][4 * i + 3]);
+                }
             }
         }
         ptx::tc_fence_before();
@@ -204,44 +294,11 @@ __global__ void __launch_bounds__(T_THREADS) tile_kernel(const __grid_constant__
     if (failed) {
         if (threadIdx.x == 0 && p.status) atomicMax(p.status, 6u);
     } else {
-        // This CTA's share of the tile, four elements of a row of y at a time: 128/S of P's rows.
-        const int share = T_ROWS / p.splits, r0 = rank * share;
-        const int width = (SWAP ? share : BN) / 4, height = SWAP ? q_valid : share;
-        const uint32_t base = ptx::smem_addr(staged);
-        T* y = static_cast<T*>(p.y);
-        for (int e = threadIdx.x; e < width * height; e += T_THREADS) {
-            const int h = e / width, w = 4 * (e - h * width);
-            const int sr = SWAP ? h : r0 + h, sc = SWAP ? r0 + w : w;  // row and column of the staged tile
-            const int64_t row = (SWAP ? q0 : p0) + sr;
-            const int col = (SWAP ? p0 : q0) + sc;
-            const int rows = SWAP ? p.q_rows : p.p_rows, cols = SWAP ? p.p_rows : p.q_rows;
-            if (row >= rows || col >= cols) continue;
-            const uint32_t at = base + static_cast<uint32_t>(sr * C::PITCH + sc) * 4u;
-            const float4 s = p.splits == 1   ? *reinterpret_cast<const float4*>(staged + sr * C::PITCH + sc)
-                             : p.splits == 2 ? joined<2>(at)
-                             : p.splits == 4 ? joined<4>(at)
-                                             : joined<8>(at);
-            float v[4] = {s.x, s.y, s.z, s.w};
-            const bool whole = col + 4 <= cols;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (p.bias && (whole || col + i < cols)) v[i] += __ldg(p.bias + col + i);
-                if (p.relu && v[i] < 0.f) v[i] = 0.f;
-            }
-            T* out = y + row * p.ldy + col;
-            if (whole && p.vec_y) {
-                if constexpr (sizeof(T) == 4) {
-                    *reinterpret_cast<float4*>(out) = make_float4(v[0], v[1], v[2], v[3]);
-                } else {
-                    const __nv_bfloat162 lo = __floats2bfloat162_rn(v[0], v[1]), hi = __floats2bfloat162_rn(v[2], v[3]);
-                    *reinterpret_cast<uint2*>(out) =
-                        make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (col + i < cols) from_float(out[i], v[i]);
-            }
+        switch (p.splits) {
+            case 1: write_share<1, BN, SWAP, T>(staged, 0, p0, q0, q_valid, p); break;
+            case 2: write_share<2, BN, SWAP, T>(staged, rank, p0, q0, q_valid, p); break;
+            case 4: write_share<4, BN, SWAP, T>(staged, rank, p0, q0, q_valid, p); break;
+            default: write_share<8, BN, SWAP, T>(staged, rank, p0, q0, q_valid, p); break;
         }
     }
     if (p.splits > 1) ptx::cluster_sync();  // the others have read this CTA's part

@@ -48,6 +48,28 @@ struct Operand {
     int64_t rows;
 };
 
+// How the sum of `tiles` tiles is split: over clusters of 1, 2, 4 or 8 CTAs, of which the SMs hold 152, 76, 36 and 15 at
+// once (one CTA to an SM).  A wave costs some 3 us of start and end, 0.7 us more where partial tiles are joined, and each stage its
+// bytes at 55 bytes a clock, what an SM takes from L2.
+struct Split {
+    int splits;
+    double us;
+};
+
+Split best_split(int64_t tiles, int stages, int bn)
+{
+    constexpr int held[4] = {152, 76, 36, 15};
+    Split best{1, 1e30};
+    for (int i = 0; i < 4; ++i) {
+        const int s = 1 << i;
+        if (s > stages) break;
+        const double us = static_cast<double>(cdiv<int64_t>(tiles, held[i])) *
+                          (3.0 + (s > 1 ? 0.7 : 0.0) + cdiv(stages, s) * (128.0 + bn + 16.0) * 128.0 / (55.0 * 1900.0));
+        if (us < best.us) best = {s, us};
+    }
+    return best;
+}
+
 template <int BN, bool SWAP, typename T>
 int launch_tile(const Operand& P, const Operand& Q, TileParams& k, cudaStream_t stream)
 {
@@ -58,9 +80,7 @@ int launch_tile(const Operand& P, const Operand& Q, TileParams& k, cudaStream_t 
     if (!allow_smem(tile_kernel<BN, SWAP, T>, C::SMEM, done)) return CONV2D_ERR_CUDA;
     k.q_tiles = cdiv(k.q_rows, BN);
     const int64_t tiles = cdiv<int64_t>(k.p_rows, T_ROWS) * k.q_tiles;
-    // The sum is split while that still gives every SM at most one CTA and every CTA two stages.
-    k.splits = 1;
-    while (k.splits < 8 && tiles * k.splits * 2 <= SMS && k.stages >= 4 * k.splits) k.splits *= 2;
+    k.splits = best_split(tiles, k.stages, BN).splits;
     if (tiles * k.splits > INT32_MAX) return CONV2D_ERR_UNSUPPORTED;
     return launch(tile_kernel<BN, SWAP, T>, tiles * k.splits, T_THREADS, C::SMEM, stream, k.splits, tm_p, tm_q, k) == cudaSuccess ? CONV2D_OK
                                                                                                                            : CONV2D_ERR_CUDA;
@@ -130,7 +150,11 @@ int product(const Operand& a, const Operand& b, TileParams& k, cudaStream_t stre
     k.q_scales = static_cast<const uint8_t*>(Q.scales);
     k.p_rows = static_cast<int>(P.rows);
     k.q_rows = static_cast<int>(Q.rows);
-    const int bn = Q.rows <= 16 ? 16 : Q.rows <= 32 ? 32 : Q.rows <= 64 ? 64 : 128;
+    int bn = Q.rows <= 16 ? 16 : Q.rows <= 32 ? 32 : Q.rows <= 64 ? 64 : 128;
+    if (bn == 128) {  // narrower tiles where more SMs are worth more than reading P twice
+        const int64_t p_tiles = cdiv<int64_t>(P.rows, T_ROWS);
+        if (best_split(p_tiles * cdiv<int64_t>(Q.rows, 64), k.stages, 64).us < best_split(p_tiles * cdiv<int64_t>(Q.rows, 128), k.stages, 128).us) bn = 64;
+    }
     if (swap) {
         switch (bn) {
             case 16: return launch_tile<16, true, T>(P, Q, k, stream);
