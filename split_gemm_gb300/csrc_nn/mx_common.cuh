@@ -50,6 +50,28 @@ __device__ __forceinline__ float scale_value(uint32_t byte)
     return byte == 255u ? __uint_as_float(0x7fffffffu) : __uint_as_float(byte == 0u ? 0x00400000u : byte << 23);
 }
 
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 add2(float2 a, float2 b)
+{
+    float2 d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(reinterpret_cast<uint64_t&>(d)) : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+    return d;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b)
+{
+    float2 d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(reinterpret_cast<uint64_t&>(d)) : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)));
+    return d;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
+{
+    float2 d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;"
+        : "=l"(reinterpret_cast<uint64_t&>(d))
+        : "l"(reinterpret_cast<uint64_t&>(a)), "l"(reinterpret_cast<uint64_t&>(b)), "l"(reinterpret_cast<uint64_t&>(c)));
+    return d;
+}
+
 // Eight fp32 values to E2M1 (nearest even, saturating), the first in the lowest four bits.
 __device__ __forceinline__ uint32_t pack_e2m1x8(const float (&v)[8])
 {
@@ -91,10 +113,10 @@ __device__ __forceinline__ uint32_t abs_bits(float v) { return __float_as_uint(v
 // Launches a kernel that may get ready while the one before it on the stream ends; it waits for that one itself
 // (griddepcontrol.wait) before it touches global memory.  cluster > 1: in clusters of so many blocks.
 template <typename... P, typename... A>
-cudaError_t launch(void (*kernel)(P...), int64_t grid, int threads, int smem, cudaStream_t stream, int cluster, A... args)
+cudaError_t launch(void (*kernel)(P...), dim3 grid, int threads, int smem, cudaStream_t stream, int cluster, A... args)
 {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.gridDim = grid;
     cfg.blockDim = dim3(static_cast<unsigned>(threads));
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = stream;
@@ -107,6 +129,12 @@ cudaError_t launch(void (*kernel)(P...), int64_t grid, int threads, int smem, cu
     cfg.attrs = attr;
     cfg.numAttrs = cluster > 1 ? 2 : 1;
     return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <typename... P, typename... A>
+cudaError_t launch(void (*kernel)(P...), int64_t grid, int threads, int smem, cudaStream_t stream, int cluster, A... args)
+{
+    return launch(kernel, dim3(static_cast<unsigned>(grid)), threads, smem, stream, cluster, args...);
 }
 
 // Lets a kernel have `bytes` of dynamic shared memory; asked of the driver once per device.

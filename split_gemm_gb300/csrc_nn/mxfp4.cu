@@ -36,9 +36,14 @@ struct alignas(16) QuantTile {
 // line so that threads with lines in turn write to different banks.
 __device__ __forceinline__ int out_at(int l, int q) { return (l >> 1) * 128 + ((((l & 1) * 4 + q) ^ ((l >> 1) & 7)) << 4); }
 
-// Largest absolute value's bits of 32 values in a register, as fp32 bits; bf16 pairs are compared as pairs.
+// The larger absolute value, as bits; bf16 values come in pairs and are compared as pairs.  A NaN stays (its bits
+// are above every number's).
 __device__ __forceinline__ uint32_t join_max(uint32_t m, uint32_t v, float) { return max(m, v & 0x7fffffffu); }
-__device__ __forceinline__ uint32_t join_max(uint32_t m, uint32_t v, __nv_bfloat16) { return __vmaxu2(m, v & 0x7fff7fffu); }
+__device__ __forceinline__ uint32_t join_max(uint32_t m, uint32_t v, __nv_bfloat16)
+{
+    const __nv_bfloat162 r = __hmax2_nan(*reinterpret_cast<const __nv_bfloat162*>(&m), __habs2(*reinterpret_cast<const __nv_bfloat162*>(&v)));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
 
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(Q_THREADS) quantize_kernel(const T* __restrict__ x, const QuantParams p)
@@ -113,7 +118,11 @@ __global__ void __launch_bounds__(Q_THREADS) quantize_kernel(const T* __restrict
             const uint32_t byte = scale_byte(m);
             const float inv = inverse_scale(byte);
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] *= inv;
+            for (int j = 0; j < 8; j += 2) {
+                const float2 w = mul2(make_float2(v[j], v[j + 1]), make_float2(inv, inv));
+                v[j] = w.x;
+                v[j + 1] = w.y;
+            }
             *reinterpret_cast<uint32_t*>(s.out + out_at(r, lane / 4) + 4 * (lane % 4)) = pack_e2m1x8(v);
             if (lane % 4 == 0) s.scales[(r % 32) * 16 + r / 32 * 4 + lane / 4] = static_cast<uint8_t>(byte);
         }
@@ -141,9 +150,13 @@ __global__ void __launch_bounds__(Q_THREADS) quantize_kernel(const T* __restrict
                 for (int q = 0; q < 4; ++q) {
                     float f[8];
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const uint32_t b = v[8 * q + j];
-                        f[j] = __uint_as_float(PAIR == 1 ? b : h ? b & 0xffff0000u : b << 16) * inv;
+                    for (int j = 0; j < 8; j += 2) {
+                        const uint32_t b0 = v[8 * q + j], b1 = v[8 * q + j + 1];
+                        const float2 w = mul2(make_float2(__uint_as_float(PAIR == 1 ? b0 : h ? b0 & 0xffff0000u : b0 << 16),
+                                                          __uint_as_float(PAIR == 1 ? b1 : h ? b1 & 0xffff0000u : b1 << 16)),
+                                              make_float2(inv, inv));
+                        f[j] = w.x;
+                        f[j + 1] = w.y;
                     }
                     o[q] = pack_e2m1x8(f);
                 }
@@ -161,33 +174,43 @@ constexpr int D_THREADS = 256;
 
 template <typename T, bool VEC>
 __global__ void __launch_bounds__(D_THREADS) dequantize_kernel(const uint8_t* __restrict__ data, const uint8_t* __restrict__ scales, T* y,
-                                                               int64_t rows, int64_t cols)
+                                                               int64_t rows, int64_t cols, int lanes_log2)
 {
+    // a thread keeps its 8 columns, 1 << lanes_log2 threads side by side, and goes down the rows
     __shared__ float gather[VEC ? 1 : D_THREADS][9];
     const int64_t blocks = cdiv<int64_t>(cols, BLOCK), btiles = cdiv<int64_t>(blocks, TILE_BLOCKS);
-    const int64_t words = blocks * 4, n = rows * words;
-    const int64_t step = int64_t(gridDim.x) * D_THREADS;
-    const int64_t step_r = step / words, step_w = step - step_r * words;
-    const int64_t i0 = int64_t(blockIdx.x) * D_THREADS + threadIdx.x;
-    int64_t r = i0 / words, w = i0 - r * words;
+    const int64_t words = blocks * 4;
+    const int64_t w = (static_cast<int64_t>(blockIdx.x) << lanes_log2) + (threadIdx.x & ((1 << lanes_log2) - 1));
+    const int64_t per = D_THREADS >> lanes_log2, step = gridDim.y * per;
+    const int64_t r0 = blockIdx.y * per + (threadIdx.x >> lanes_log2);
+    const int64_t lead = blockIdx.y * per + ((threadIdx.x & ~31) >> lanes_log2);  // of the warp, whose lanes stay together
+    const uint8_t* scale_col = scales + (w >> 4) * TILE_BYTES + ((w >> 2) & 3);
     const int lane = threadIdx.x & 31;
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
-    for (int64_t i = i0; i - lane < n; i += step) {  // a warp's lanes stay together
-        float2 v[4];
-        if (i < n) {
-            const uint32_t word = __ldg(reinterpret_cast<const uint32_t*>(data) + i);
-            const float s = scale_value(__ldg(scales + scale_at(r, w >> 2, btiles)));
+#pragma unroll 4
+    for (int64_t k = 0; lead + k < rows; k += step) {
+        const int64_t r = r0 + k;
+        float2 v[4] = {};
+        if (r < rows && w < words) {
+            const uint32_t word = __ldg(reinterpret_cast<const uint32_t*>(data) + r * words + w);
+            const float s = scale_value(__ldg(scale_col + scale_at(r, 0, btiles)));
             unpack_e2m1x8(v, word);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = make_float2(v[j].x * s, v[j].y * s);
+            for (int j = 0; j < 4; ++j) v[j] = mul2(v[j], make_float2(s, s));
         }
         if constexpr (VEC) {
-            if (i < n && w * 8 < cols) {
+            if (r < rows && w * 8 < cols) {
                 T* out = y + r * cols + w * 8;
                 if constexpr (sizeof(T) == 4) {
-                    reinterpret_cast<float4*>(out)[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
-                    reinterpret_cast<float4*>(out)[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+                    if (reinterpret_cast<uintptr_t>(out) % 32 == 0) {  // a whole sector to a thread
+                        asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out), "f"(v[0].x), "f"(v[0].y),
+                                     "f"(v[1].x), "f"(v[1].y), "f"(v[2].x), "f"(v[2].y), "f"(v[3].x), "f"(v[3].y)
+                                     : "memory");
+                    } else {
+                        reinterpret_cast<float4*>(out)[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+                        reinterpret_cast<float4*>(out)[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+                    }
                 } else {
                     uint32_t o[4];
 #pragma unroll
@@ -208,18 +231,12 @@ __global__ void __launch_bounds__(D_THREADS) dequantize_kernel(const uint8_t* __
             }
             __syncwarp();
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const int from = 4 * k + lane / 8;  // the thread whose element this is
+            for (int e = 0; e < 8; ++e) {
+                const int from = 4 * e + lane / 8;  // the thread whose element this is
                 const int64_t fr = __shfl_sync(0xffffffffu, r, from), fw = __shfl_sync(0xffffffffu, w, from);
                 const int64_t c = fw * 8 + lane % 8;
                 if (fr < rows && c < cols) from_float(y[fr * cols + c], mine[from][lane % 8]);
             }
-        }
-        r += step_r;
-        w += step_w;
-        if (w >= words) {
-            w -= words;
-            ++r;
         }
     }
 }
@@ -245,11 +262,17 @@ int quantize(const void* x, const QuantParams& p, cudaStream_t stream)
 template <typename T>
 int dequantize(const uint8_t* data, const uint8_t* scales, void* y, int64_t rows, int64_t cols, cudaStream_t stream)
 {
-    // Eight blocks to an SM at most: they stay, and take one group after another.
-    const int64_t need = cdiv<int64_t>(rows * cdiv<int64_t>(cols, BLOCK) * 4, D_THREADS);
-    const int64_t grid = need < SMS * 8 ? need : SMS * 8;
+    const int64_t words = cdiv<int64_t>(cols, BLOCK) * 4;
+    int lanes_log2 = 2;
+    while (lanes_log2 < 8 && (int64_t(1) << lanes_log2) < words) ++lanes_log2;
+    // Eight blocks to an SM at most: they stay, and go down the rows.
+    const int64_t across = cdiv<int64_t>(words, int64_t(1) << lanes_log2), down = cdiv<int64_t>(rows, D_THREADS >> lanes_log2);
+    const int64_t most = cdiv<int64_t>(SMS * 8, across) < 65535 ? cdiv<int64_t>(SMS * 8, across) : 65535;
+    if (across > INT32_MAX) return CONV2D_ERR_UNSUPPORTED;
+    const dim3 grid(static_cast<unsigned>(across), static_cast<unsigned>(down < most ? down : most));
     const auto kernel = cols % 8 == 0 ? dequantize_kernel<T, true> : dequantize_kernel<T, false>;
-    return launch(kernel, grid, D_THREADS, 0, stream, 1, data, scales, static_cast<T*>(y), rows, cols) == cudaSuccess ? CONV2D_OK : CONV2D_ERR_CUDA;
+    return launch(kernel, grid, D_THREADS, 0, stream, 1, data, scales, static_cast<T*>(y), rows, cols, lanes_log2) == cudaSuccess ? CONV2D_OK
+                                                                                                                                : CONV2D_ERR_CUDA;
 }
 
 }  // namespace mx
