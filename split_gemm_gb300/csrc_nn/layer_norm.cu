@@ -74,7 +74,7 @@ bool sums_in_rows(RowShape s) { return s.elems == 8 || s.elems == 16; }
 
 int64_t bwd_parts(const layer_norm_params* p)
 {
-    const RowShape s = bwd_shape(p->rows, span_of(p), static_cast<int>(dtype_size(p->x_dtype)));
+    const RowShape s = bwd_shape(p->rows, span_of(p), static_cast<int>(dtype_size(p->x_dtype)), span_of(p) == p->cols);
     if (!sums_in_rows(s)) {
         const int64_t n = mx::cdiv(p->rows, PART_ROWS);
         return n < PART_CHUNKS ? n : PART_CHUNKS;
@@ -204,7 +204,7 @@ extern "C" int layer_norm_bwd(const layer_norm_params* params, const void* dy_de
             using TY = std::remove_pointer_t<decltype(ty)>;
             rc = ln::launch_bwd_rows<TX, TY>(k, vec, k.chunks, stream);
             if (rc != CONV2D_OK && rc != CONV2D_ERR_UNSUPPORTED) return;
-            if (rc == CONV2D_OK && ln::sums_in_rows(ln::bwd_shape(k.rows, k.span, sizeof(TX)))) return;
+            if (rc == CONV2D_OK && ln::sums_in_rows(ln::bwd_shape(k.rows, k.span, sizeof(TX), k.span == k.cols))) return;
             const TX* x = static_cast<const TX*>(x_dev);
             const TY* dy = static_cast<const TY*>(dy_dev);
             if (rc == CONV2D_ERR_UNSUPPORTED)

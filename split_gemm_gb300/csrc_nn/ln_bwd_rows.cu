@@ -33,13 +33,16 @@ int start_bwd(const BwdParams& p, RowShape s, int grid, cudaStream_t stream)
 template <typename TX, typename TY, int VEC>
 int bwd_by_shape(const BwdParams& p, int grid, cudaStream_t stream)
 {
-    const RowShape s = bwd_shape(p.rows, p.span, sizeof(TX));
+    constexpr bool B16 = sizeof(TX) == 2;  // shapes of many elements to a thread are for 16-bit rows
+    const RowShape s = bwd_shape(p.rows, p.span, sizeof(TX), p.span == p.cols);
     if (s.threads == 0) return CONV2D_ERR_UNSUPPORTED;
-    if (s.threads == 4) return start_bwd<TX, TY, VEC, 16, 4, 256, true>(p, s, grid, stream);
-    if (s.threads == 8)
-        return s.elems == 8 ? start_bwd<TX, TY, VEC, 8, 8, 256, true>(p, s, grid, stream) : start_bwd<TX, TY, VEC, 16, 8, 256, true>(p, s, grid, stream);
-    if (s.threads == 16)
-        return s.elems == 8 ? start_bwd<TX, TY, VEC, 8, 16, 256, true>(p, s, grid, stream) : start_bwd<TX, TY, VEC, 16, 16, 256, true>(p, s, grid, stream);
+    if constexpr (B16) {
+        if (s.threads == 4) return start_bwd<TX, TY, VEC, 16, 4, 256, true>(p, s, grid, stream);
+        if (s.threads == 8 && s.elems == 16) return start_bwd<TX, TY, VEC, 16, 8, 256, true>(p, s, grid, stream);
+        if (s.threads == 16 && s.elems == 16) return start_bwd<TX, TY, VEC, 16, 16, 256, true>(p, s, grid, stream);
+    }
+    if (s.threads == 8) return start_bwd<TX, TY, VEC, 8, 8, 256, true>(p, s, grid, stream);
+    if (s.threads == 16) return start_bwd<TX, TY, VEC, 8, 16, 256, true>(p, s, grid, stream);
     if (s.threads == 32)
         return s.elems == 8 ? start_bwd<TX, TY, VEC, 8, 32, 256, true>(p, s, grid, stream) : start_bwd<TX, TY, VEC, 16, 32, 256, true>(p, s, grid, stream);
     if (s.elems == 8) return start_bwd<TX, TY, VEC, 8, 0, 256, true>(p, s, grid, stream);

@@ -35,21 +35,27 @@ int fwd_by_shape(const FwdParams& p, cudaStream_t stream)
     // a quantised row needs the 128 columns of a scale tile in one vector of its group, single elements a whole warp
     constexpr bool MX = std::is_same_v<TY, void>;
     constexpr int LEAST = !MX ? 4 : VEC == 8 ? 16 : 32;
-    RowShape s = fwd_shape(p.rows, p.span, sizeof(TX));
+    constexpr bool B16 = sizeof(TX) == 2;  // shapes of many elements to a thread are for 16-bit rows
+    RowShape s = fwd_shape(p.rows, p.span, sizeof(TX), VEC > 1 && p.span == p.cols);
     if (s.threads == 0) return CONV2D_ERR_UNSUPPORTED;
     if (s.threads < LEAST) s = RowShape{LEAST, 8, 256};
-    if constexpr (LEAST <= 4)
+    if constexpr (LEAST <= 4 && B16)
         if (s.threads == 4) return start_fwd<TX, TY, VEC, 16, 4, 256>(p, s, stream);
+    if constexpr (LEAST <= 8 && B16)
+        if (s.threads == 8 && s.elems == 16) return start_fwd<TX, TY, VEC, 16, 8, 256>(p, s, stream);
     if constexpr (LEAST <= 8)
-        if (s.threads == 8) return s.elems == 8 ? start_fwd<TX, TY, VEC, 8, 8, 256>(p, s, stream) : start_fwd<TX, TY, VEC, 16, 8, 256>(p, s, stream);
+        if (s.threads == 8) return start_fwd<TX, TY, VEC, 8, 8, 256>(p, s, stream);
+    if constexpr (LEAST <= 16 && B16)
+        if (s.threads == 16 && s.elems == 16) return start_fwd<TX, TY, VEC, 16, 16, 256>(p, s, stream);
     if constexpr (LEAST <= 16)
-        if (s.threads == 16) return s.elems == 8 ? start_fwd<TX, TY, VEC, 8, 16, 256>(p, s, stream) : start_fwd<TX, TY, VEC, 16, 16, 256>(p, s, stream);
+        if (s.threads == 16) return start_fwd<TX, TY, VEC, 8, 16, 256>(p, s, stream);
+    if constexpr (B16 && VEC > 1)
+        if (s.threads == 32 && s.elems == 32 && s.most == 256) return start_fwd_as<TX, TY, VEC, 32, 32, 256, true>(p, s, stream);
     if (s.threads == 32 && s.most == 256)
-        return s.elems == 8    ? start_fwd<TX, TY, VEC, 8, 32, 256>(p, s, stream)
-               : s.elems == 16 ? start_fwd<TX, TY, VEC, 16, 32, 256>(p, s, stream)
-                               : start_fwd<TX, TY, VEC, 32, 32, 256>(p, s, stream);
+        return s.elems == 8 ? start_fwd<TX, TY, VEC, 8, 32, 256>(p, s, stream) : start_fwd<TX, TY, VEC, 16, 32, 256>(p, s, stream);
     if (s.elems == 8) return start_fwd<TX, TY, VEC, 8, 0, 256>(p, s, stream);
-    if (s.elems == 16) return s.most == 256 ? start_fwd<TX, TY, VEC, 16, 0, 256>(p, s, stream) : start_fwd<TX, TY, VEC, 16, 0, 512>(p, s, stream);
+    if (s.elems == 16 && s.most == 256) return start_fwd<TX, TY, VEC, 16, 0, 256>(p, s, stream);
+    if (s.elems == 16) return start_fwd_as<TX, TY, VEC, 16, 0, 512, false>(p, s, stream);
     return start_fwd<TX, TY, VEC, 32, 0, 512>(p, s, stream);
 }
 

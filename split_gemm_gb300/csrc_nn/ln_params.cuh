@@ -55,26 +55,26 @@ __host__ __device__ constexpr RowShape group_shape(int n, bool many)
                                                   : (n <= 64 ? RowShape{8, 8, 256} : n <= 128 ? RowShape{16, 8, 256} : RowShape{32, 8, 256});
 }
 
-// Forward: a warp to a row of up to 1024 columns where there are many rows and those fill it, else blocks of 8, 16 or 32
-// elements to a thread.
-__host__ __device__ constexpr RowShape fwd_shape(int64_t rows, int64_t cols, int x_bytes)
+// Forward: a warp to a row of up to 1024 columns where there are many rows and those nearly fill it, else blocks of 8, 16 or 32
+// elements to a thread.  `whole`: rows are whole vectors (others need registers for masks).
+__host__ __device__ constexpr RowShape fwd_shape(int64_t rows, int64_t cols, int x_bytes, bool whole)
 {
     if (cols > 16384) return RowShape{0, 0, 0};
     const int n = static_cast<int>(cols);
     if (n <= 512) return group_shape(n, many_rows(rows, x_bytes, 16));
-    if (n > 768 && n <= 1024 && n % 8 == 0 && many_rows(rows, x_bytes, 32)) return RowShape{32, 32, 256};
+    if (n > 768 && n <= 1024 && whole && many_rows(rows, x_bytes, 32)) return RowShape{32, 32, 256};
     return n <= (many_rows(rows, x_bytes, 64) ? 1024 : 2048) ? warps_of(n, 8, 256) : n <= 4096 ? warps_of(n, 16, 256)
-         : n <= 8192 && n % 8                                ? warps_of(n, 16, 512) : warps_of(n, 32, 512);
+         : n <= 8192 && !whole                               ? warps_of(n, 16, 512) : warps_of(n, 32, 512);
 }
 
 // Backward: the sums of dweight and dbias leave registers for 16 elements; above 8192 columns dx alone takes 32.
-__host__ __device__ constexpr RowShape bwd_shape(int64_t rows, int64_t cols, int x_bytes)
+__host__ __device__ constexpr RowShape bwd_shape(int64_t rows, int64_t cols, int x_bytes, bool whole)
 {
     if (cols > 16384) return RowShape{0, 0, 0};
     const int n = static_cast<int>(cols);
     if (n <= 512) return group_shape(n, many_rows(rows, x_bytes, 16));
     if (n > 8192) return warps_of(n, 32, 512);
-    const bool wide = n > 2048 || (many_rows(rows, x_bytes, 64) && n % 8 == 0 && (n + 511) / 512 * 512 <= n + n / 4);
+    const bool wide = n > 2048 || (many_rows(rows, x_bytes, 64) && whole && (n + 511) / 512 * 512 <= n + n / 4);
     return wide ? warps_of(n, 16, n <= 4096 ? 256 : 512) : warps_of(n, 8, 256);
 }
 
