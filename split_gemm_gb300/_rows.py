@@ -5,6 +5,7 @@ decided by few attribute reads and what is wrong is named only once something is
 """
 from __future__ import annotations
 
+import importlib.util
 from typing import Optional, Tuple
 
 import torch
@@ -13,6 +14,22 @@ from . import OUT_BF16, OUT_F32, load_library
 
 DTYPE_CODES = {torch.float32: OUT_F32, torch.bfloat16: OUT_BF16}
 _lib = None
+_calls = None
+
+
+def calls():
+    """The compiled calls (csrc_nn/torch_calls.cpp): they take the usual case and return None for any other."""
+    global _calls
+    if _calls is None:
+        library()  # builds what is stale
+        from . import _build
+        from .mxfp4 import Mxfp4
+        spec = importlib.util.spec_from_file_location("split_gemm_gb300._calls", _build.CALLS_PATH)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        module.use(Mxfp4)
+        _calls = module
+    return _calls
 
 
 def library():

@@ -14,7 +14,7 @@ import ctypes
 import torch
 
 from . import Conv2dError, LayerNormParams
-from ._rows import DTYPE_CODES, check_out_dtype, check_vector, empty_on, library, rows_of, same_device, stream_handle
+from ._rows import DTYPE_CODES, calls, check_out_dtype, check_vector, empty_on, library, rows_of, same_device, stream_handle
 from .mxfp4 import Mxfp4, mxfp4_empty
 
 
@@ -43,19 +43,15 @@ def layer_norm_fwd_into(y, x, weight=None, bias=None, eps: float = 1e-5, *, mean
 def layer_norm_fwd(x, weight=None, bias=None, eps: float = 1e-5, *, out_dtype=None, stream=None):
     """Returns (y, mean, rstd): y of x's shape and ``out_dtype`` (default: x's type), and the fp32 statistics
     of each row (the shape of x without its last dimension) that the backward pass takes."""
+    if stream is None and (made := calls().layer_norm_fwd(x, weight, bias, eps, out_dtype)) is not None:
+        return made
     rows, cols, x_stride = rows_of(x, "x")
-    if out_dtype is None:
-        out_dtype = x.dtype
-    else:
-        check_out_dtype(out_dtype)
+    out_dtype = x.dtype if out_dtype is None else out_dtype
+    check_out_dtype(out_dtype)
     shape, device = x.shape, x.device
-    if stream is None:
-        y = torch.empty(shape, dtype=out_dtype, device=device)
-        mean = torch.empty(shape[:-1], dtype=torch.float32, device=device)
-        rstd = torch.empty(shape[:-1], dtype=torch.float32, device=device)
-    else:
-        y, mean, rstd = (empty_on(stream, s, t, device) for s, t in
-                         ((shape, out_dtype), (shape[:-1], torch.float32), (shape[:-1], torch.float32)))
+    y = empty_on(stream, shape, out_dtype, device)
+    mean = empty_on(stream, shape[:-1], torch.float32, device)
+    rstd = empty_on(stream, shape[:-1], torch.float32, device)
     _fwd(y, x, (rows, cols, x_stride, cols), weight, bias, eps, mean.data_ptr(), rstd.data_ptr(), stream)
     return y, mean, rstd
 
@@ -106,6 +102,8 @@ def layer_norm_bwd_into(dx, dweight, dbias, dy, x, mean, rstd, weight=None, *, w
 def layer_norm_bwd(dy, x, mean, rstd, weight=None, *, workspace=None, stream=None):
     """Returns (dx, dweight, dbias) for y = layer_norm_fwd(x, weight, bias): dx of x's shape and type, dweight and
     dbias [C] fp32, summed over all rows in a fixed order."""
+    if stream is None and workspace is None and (made := calls().layer_norm_bwd(dy, x, mean, rstd, weight)) is not None:
+        return made
     layout = rows_of(x, "x")
     device = x.device
     dx = empty_on(stream, x.shape, x.dtype, device)
@@ -118,6 +116,8 @@ def layer_norm_bwd(dy, x, mean, rstd, weight=None, *, workspace=None, stream=Non
 def layer_norm_mxfp4(x, weight=None, bias=None, eps: float = 1e-5, *, mean=None, rstd=None, stream=None) -> Mxfp4:
     """layer_norm_fwd's fp32 result quantised at once, as the [rows, C] operand of mxfp4_matmul; ``mean`` and
     ``rstd`` (fp32, one to a row), where given, are written too."""
+    if stream is None and mean is None and rstd is None and (made := calls().layer_norm_mxfp4(x, weight, bias, eps)) is not None:
+        return Mxfp4(*made)
     rows, cols, x_stride = rows_of(x, "x")
     params = LayerNormParams(rows, cols, x_stride, cols, DTYPE_CODES[x.dtype], 0, eps)
     q = mxfp4_empty(rows, cols, x.device, stream=stream)

@@ -19,7 +19,7 @@ from typing import NamedTuple, Tuple
 import torch
 
 from . import ACT_NONE, ACT_RELU, Conv2dError, Epilogue, Mxfp4MatmulParams
-from ._rows import DTYPE_CODES, check_out_dtype, check_vector, empty_on, library, rows_of, same_device, stream_handle
+from ._rows import DTYPE_CODES, calls, check_out_dtype, check_vector, empty_on, library, rows_of, same_device, stream_handle
 
 
 class Mxfp4(NamedTuple):
@@ -38,11 +38,9 @@ class Mxfp4(NamedTuple):
 def mxfp4_empty(rows: int, cols: int, device, *, stream=None) -> Mxfp4:
     """An unwritten quantised matrix, for mxfp4_quantize_into."""
     blocks = (cols + 31) // 32
-    scales = (rows + 127) // 128 * ((blocks + 3) // 4) * 512
-    if stream is None:
-        return Mxfp4(torch.empty((rows, 16 * blocks), dtype=torch.uint8, device=device),
-                     torch.empty((scales,), dtype=torch.uint8, device=device), rows, cols)
-    return Mxfp4(empty_on(stream, (rows, 16 * blocks), torch.uint8, device), empty_on(stream, (scales,), torch.uint8, device), rows, cols)
+    data = empty_on(stream, (rows, 16 * blocks), torch.uint8, device)
+    scales = empty_on(stream, ((rows + 127) // 128 * ((blocks + 3) // 4) * 512,), torch.uint8, device)
+    return Mxfp4(data, scales, rows, cols)
 
 
 def _check_mx(q, name) -> Tuple[int, int]:
@@ -101,6 +99,8 @@ def _new(rows, cols, device, stream):
 def mxfp4_quantize(x, *, transpose: bool = False, stream=None) -> Mxfp4:
     """Quantises x [..., C] (bf16 or fp32), seen as [rows, C]; with ``transpose`` the result is [C, rows], in blocks
     along x's columns."""
+    if stream is None and (made := calls().quantize(x, not transpose, bool(transpose))) is not None:
+        return Mxfp4(*made[1 if transpose else 0])
     rows, cols, x_stride = rows_of(x, "x")
     if transpose:
         q, ptr_t = _new(cols, rows, x.device, stream)
@@ -113,6 +113,8 @@ def mxfp4_quantize(x, *, transpose: bool = False, stream=None) -> Mxfp4:
 
 def mxfp4_quantize_both(x, *, stream=None) -> Tuple[Mxfp4, Mxfp4]:
     """(mxfp4_quantize(x), mxfp4_quantize(x, transpose=True)) from one reading of x."""
+    if stream is None and (made := calls().quantize(x, True, True)) is not None:
+        return Mxfp4(*made[0]), Mxfp4(*made[1])
     rows, cols, x_stride = rows_of(x, "x")
     q, ptr = _new(rows, cols, x.device, stream)
     q_t, ptr_t = _new(cols, rows, x.device, stream)
@@ -122,6 +124,8 @@ def mxfp4_quantize_both(x, *, stream=None) -> Tuple[Mxfp4, Mxfp4]:
 
 def mxfp4_dequantize(q: Mxfp4, *, out_dtype=torch.bfloat16, stream=None):
     """The values that q stands for, [rows, cols] bf16 or fp32 (exact in either)."""
+    if stream is None and (made := calls().dequantize(q, out_dtype)) is not None:
+        return made
     data, scales = _check_mx(q, "q")
     code = check_out_dtype(out_dtype)
     y = empty_on(stream, (q.rows, q.cols), out_dtype, q.data.device)
@@ -163,10 +167,11 @@ def mxfp4_matmul_into(y, a: Mxfp4, b: Mxfp4, bias=None, *, relu: bool = False, s
 
 def mxfp4_matmul(a: Mxfp4, b: Mxfp4, bias=None, *, relu: bool = False, out_dtype=torch.float32, stream=None):
     """Returns a b^T + bias as a new [a.rows, b.rows] tensor of ``out_dtype`` (asynchronous)."""
+    if stream is None and (made := calls().matmul(a, b, bias, relu, out_dtype)) is not None:
+        return made
     ptrs = _operands(a, b)
     check_out_dtype(out_dtype)
-    shape, device = (a.rows, b.rows), a.data.device
-    y = torch.empty(shape, dtype=out_dtype, device=device) if stream is None else empty_on(stream, shape, out_dtype, device)
+    y = empty_on(stream, (a.rows, b.rows), out_dtype, a.data.device)
     _matmul(y, ptrs, a, b, bias, relu, stream)
     return y
 
