@@ -192,18 +192,19 @@ __global__ void __launch_bounds__(W_THREADS, 1)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const float4 b = mine[c * 8 + i];
-                        v[c][4 * i] = __float_as_uint(__uint_as_float(v[c][4 * i]) + b.x);
-                        v[c][4 * i + 1] = __float_as_uint(__uint_as_float(v[c][4 * i + 1]) + b.y);
-                        v[c][4 * i + 2] = __float_as_uint(__uint_as_float(v[c][4 * i + 2]) + b.z);
-                        v[c][4 * i + 3] = __float_as_uint(__uint_as_float(v[c][4 * i + 3]) + b.w);
+                        const float2 lo = add2(make_float2(__uint_as_float(v[c][4 * i]), __uint_as_float(v[c][4 * i + 1])), make_float2(b.x, b.y));
+                        const float2 hi = add2(make_float2(__uint_as_float(v[c][4 * i + 2]), __uint_as_float(v[c][4 * i + 3])), make_float2(b.z, b.w));
+                        v[c][4 * i] = __float_as_uint(lo.x);
+                        v[c][4 * i + 1] = __float_as_uint(lo.y);
+                        v[c][4 * i + 2] = __float_as_uint(hi.x);
+                        v[c][4 * i + 3] = __float_as_uint(hi.y);
                     }
             }
-            if (p.relu) {
+            if (sizeof(T) == 4 && p.relu) {  // bf16 values are clamped by pairs after rounding, which is the same
 #pragma unroll
                 for (int c = 0; c < 4; ++c)
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (__uint_as_float(v[c][i]) < 0.f) v[c][i] = 0u;
+                    for (int i = 0; i < 32; ++i) v[c][i] = ptx::relu_nan(v[c][i]);
             }
 #pragma unroll
             for (int b = 0; b < 128 / COLS; ++b) {
@@ -221,7 +222,8 @@ __global__ void __launch_bounds__(W_THREADS, 1)
                             w[i] = v[b][4 * q + i];
                         } else {
                             const int e = b * 64 + q * 8 + 2 * i;
-                            const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(v[e / 32][e % 32]), __uint_as_float(v[e / 32][e % 32 + 1]));
+                            __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(v[e / 32][e % 32]), __uint_as_float(v[e / 32][e % 32 + 1]));
+                            if (p.relu) h = __hmax2_nan(h, __nv_bfloat162(__float2bfloat16_rn(0.f), __float2bfloat16_rn(0.f)));
                             w[i] = *reinterpret_cast<const uint32_t*>(&h);
                         }
                     }

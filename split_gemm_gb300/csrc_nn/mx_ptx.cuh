@@ -126,6 +126,14 @@ __device__ __forceinline__ void tma_load_2d_pair(void* dst, const void* map, uin
         : "memory");
 }
 
+// max(v, 0) of fp32 bits; NaN stays.
+__device__ __forceinline__ uint32_t relu_nan(uint32_t v)
+{
+    float d;
+    asm("max.NaN.f32 %0, %1, 0f00000000;" : "=f"(d) : "f"(__uint_as_float(v)));
+    return __float_as_uint(d);
+}
+
 __device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr)
 {
     float v;
