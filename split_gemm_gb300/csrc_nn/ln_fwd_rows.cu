@@ -32,9 +32,9 @@ int start_fwd(const FwdParams& p, RowShape s, cudaStream_t stream)
 template <typename TX, typename TY, int VEC>
 int fwd_by_shape(const FwdParams& p, cudaStream_t stream)
 {
-    // a quantised row needs the 128 columns of a scale tile in one vector of its group, single elements a whole warp
+    // a quantised row needs a block's 32 columns in one vector of its group, and its group over whole scale tiles
     constexpr bool MX = std::is_same_v<TY, void>;
-    constexpr int LEAST = !MX ? 4 : VEC == 8 ? 16 : 32;
+    constexpr int LEAST = !MX ? 4 : VEC > 1 ? 16 : 32;
     constexpr bool B16 = sizeof(TX) == 2;  // shapes of many elements to a thread are for 16-bit rows
     RowShape s = fwd_shape(p.rows, p.span, sizeof(TX), VEC > 1 && p.span == p.cols);
     if (s.threads == 0) return CONV2D_ERR_UNSUPPORTED;

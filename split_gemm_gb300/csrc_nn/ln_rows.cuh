@@ -222,9 +222,11 @@ __device__ __forceinline__ void store_mx(const float2 (&v)[(VEC + 1) / 2], int c
 {
     constexpr int LANES = mx::BLOCK / VEC;
     const int lane = threadIdx.x & 31;
-    uint32_t m = mx::abs_bits(v[0].x);
+    float largest = fabsf(v[0].x);
+    if constexpr (VEC > 1)
 #pragma unroll
-    for (int i = 1; i < VEC; ++i) m = max(m, mx::abs_bits(i % 2 ? v[i / 2].y : v[i / 2].x));
+        for (int i = 0; i < VEC / 2; ++i) largest = mx::max_abs3(largest, v[i].x, v[i].y);
+    uint32_t m = mx::abs_bits(largest);
 #pragma unroll
     for (int o = LANES / 2; o; o >>= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
     const uint32_t byte = mx::scale_byte(m);
@@ -249,15 +251,7 @@ __device__ __forceinline__ void store_mx(const float2 (&v)[(VEC + 1) / 2], int c
         word |= __shfl_xor_sync(0xffffffffu, word, 4) << 16;
         if (in_data && lane % 8 == 0) *reinterpret_cast<uint32_t*>(data + col / 2) = word;
     }
-    uint8_t* at = scales + b / 4 * mx::TILE_BYTES;
-    if constexpr (VEC == 1) {
-        if (in_tile && lane == 0) at[b & 3] = static_cast<uint8_t>(byte);
-    } else {  // four blocks' bytes side by side
-        uint32_t w = byte << (8 * (b & 3));
-        w |= __shfl_xor_sync(0xffffffffu, w, LANES);
-        w |= __shfl_xor_sync(0xffffffffu, w, 2 * LANES);
-        if (in_tile && lane % (4 * LANES) == 0) *reinterpret_cast<uint32_t*>(at) = w;
-    }
+    if (in_tile && lane % LANES == 0) scales[b / 4 * mx::TILE_BYTES + (b & 3)] = static_cast<uint8_t>(byte);
 }
 
 // Forward.  TY = void: the result quantised; rows from p.rows to p.padded_rows are the scale tiles' padding (and `off` is 0).
@@ -266,7 +260,7 @@ __global__ void __launch_bounds__(MOST, FWD_RESIDENT<G, E, MOST>) fwd_rows(const
 {
     constexpr bool MX = std::is_same_v<TY, void>;
     constexpr int ROWS = G ? MOST / G : 1, DEPTH = ring_depth(RowShape{G ? G : MOST, E, MOST}, sizeof(TX), 0);
-    static_assert(!MX || G == 0 || (VEC == 1 ? G >= 32 : G * VEC >= 128), "four blocks' scales are joined within a row's lanes");
+    static_assert(!MX || G == 0 || (G * VEC >= mx::BLOCK && G * E >= mx::BLOCK * mx::TILE_BLOCKS), "a block's lanes lie in one group, which covers whole scale tiles");
     using Un = Units<VEC, E, WHOLE>;
     constexpr int U = Un::U, H = Un::H;
     extern __shared__ __align__(16) uint8_t ring_mem[];

@@ -72,6 +72,14 @@ __device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c)
     return d;
 }
 
+// The largest of three absolute values; NaN if one is.
+__device__ __forceinline__ float max_abs3(float a, float b, float c)
+{
+    float d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 // Eight fp32 values to E2M1 (nearest even, saturating), the first in the lowest four bits.
 __device__ __forceinline__ uint32_t pack_e2m1x8(const float (&v)[8])
 {

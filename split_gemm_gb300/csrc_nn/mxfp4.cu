@@ -107,11 +107,14 @@ __global__ void __launch_bounds__(Q_THREADS) quantize_kernel(const T* __restrict
                 }
                 m = max(m << 16, m & 0xffff0000u);
             } else {
+                float largest = 0.f;
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
+                for (int j = 0; j < 8; j += 2) {
                     v[j] = s.x[r][c + j];
-                    m = max(m, abs_bits(v[j]));
+                    v[j + 1] = s.x[r][c + j + 1];
+                    largest = max_abs3(largest, v[j], v[j + 1]);
                 }
+                m = __float_as_uint(largest);
             }
             m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
             m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
