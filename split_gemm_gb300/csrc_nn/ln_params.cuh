@@ -88,12 +88,12 @@ __host__ __device__ constexpr int bwd_threads(RowShape s) { return s.elems == 8 
 __host__ __device__ constexpr int fwd_resident(RowShape s) { return fwd_threads(s) / block_threads(s); }
 __host__ __device__ constexpr int bwd_resident(RowShape s) { return bwd_threads(s) / block_threads(s); }
 
-// Rows of a block's ring.  Forward some 72 KB of them on an SM, as more in flight slows HBM down (bf16, 32768 x 4096, rows of
-// all blocks 24 KB: two 89.5 us, three 88.4, four 93.3); backward 128 KB (four rows of 32 KB 141 us, two 173).
+// Rows of a block's ring: some 72 KB of them on an SM, as more in flight slows HBM down (bf16, 32768 x 4096 forward, rows of all
+// blocks 24 KB: two 89.5 us, three 88.4, four 93.3; backward, 32 KB: two to five 141 to 142), but two at least where they fit.
 __host__ __device__ constexpr int ring_depth(RowShape s, int x_bytes, int y_bytes)
 {
     const int row = (y_bytes ? bwd_threads(s) : fwd_threads(s)) * s.elems * (x_bytes + y_bytes);
-    const int n = (y_bytes ? 128 : 72) * 1024 / row;
+    const int n = 72 * 1024 / row;
     return n > 4 ? 4 : n >= 2 ? n : 2 * row <= 200 * 1024 ? 2 : 1;
 }
 

@@ -79,9 +79,9 @@ struct Ring {
 };
 
 // A thread's E elements of a row as units of H pairs for two-wide arithmetic: a unit is a vector, or (VEC = 1) two
-// single elements a group apart.  WHOLE: rows are whole vectors, so that a unit lies in the row or beyond its end.  Else a bit
-// mask for each element zeroes what lies outside (a mask and not a factor, as the row before may hold NaN; kept in
-// registers, as branches around the few edge vectors cost more).
+// single elements a group apart.  WHOLE: rows are whole vectors, so that a unit lies in the row or beyond its end.  Else the
+// row's first and last vector may lie partly outside it; the thread that has one (`edge`) zeroes that part in a
+// branch of its own, once for all units (a branch or a mask for each unit cost all threads more).
 template <int VEC, int E, bool WHOLE>
 struct Units {
     static constexpr int U = VEC > 1 ? E / VEC : E / 2;
@@ -89,16 +89,11 @@ struct Units {
     static constexpr int NV = E / VEC;
     int t, g, off, cols;  // thread of its group of g
     bool edge = false;    // a unit lies partly in the row
-    uint32_t mask[WHOLE ? 1 : U][2 * H];
     __device__ __forceinline__ Units(int t, int g, int off, int cols) : t(t), g(g), off(off), cols(cols)
     {
         if constexpr (!WHOLE)
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                edge |= !none(u) && !whole(u);
-#pragma unroll
-                for (int i = 0; i < 2 * H; ++i) mask[u][i] = in(u, i) ? 0xffffffffu : 0u;
-            }
+            for (int u = 0; u < U; ++u) edge |= !none(u) && !whole(u);
     }
     // column of element i of unit u: below 0 or past the end outside the row
     __device__ __forceinline__ int col(int u, int i) const { return VEC > 1 ? (u * g + t) * VEC + i - off : (2 * u + i) * g + t; }
@@ -108,14 +103,20 @@ struct Units {
     }
     __device__ __forceinline__ bool none(int u) const { return col(u, 0) >= cols; }
     __device__ __forceinline__ bool whole(int u) const { return WHOLE || (VEC > 1 ? col(u, 0) >= 0 && col(u, 2 * H - 1) < cols : in(u, 1)); }
-    // Zeroes what lies outside the row.
-    __device__ __forceinline__ void cut(float2 (&d)[H], int u) const
+    // Zeroes the part of a partial unit that lies outside the row.
+    __device__ __forceinline__ void cut(float2 (&d)[U][H]) const
     {
         if constexpr (!WHOLE) {
+            if (edge) {
 #pragma unroll
-            for (int i = 0; i < H; ++i) {
-                d[i].x = __uint_as_float(__float_as_uint(d[i].x) & mask[u][2 * i]);
-                d[i].y = __uint_as_float(__float_as_uint(d[i].y) & mask[u][2 * i + 1]);
+                for (int u = 0; u < U; ++u)
+                    if (!none(u) && !whole(u)) {
+#pragma unroll
+                        for (int i = 0; i < H; ++i) {
+                            if (!in(u, 2 * i)) d[u][i].x = 0.f;
+                            if (!in(u, 2 * i + 1)) d[u][i].y = 0.f;
+                        }
+                    }
             }
         }
     }
@@ -131,7 +132,7 @@ struct Units {
             for (int i = 0; i < H; ++i) d[i] = make_float2(v.v[2 * i], v.v[2 * i + 1]);
         }
     }
-    // The unit's values, zero outside the row.
+    // The unit's values, zero beyond the row's end (before its beginning the row before, see cut).
     template <typename T, typename R>
     __device__ __forceinline__ void take(float2 (&d)[H], const R& ring, int slot, const T* row, int u, bool live) const
     {
@@ -141,7 +142,6 @@ struct Units {
             Pack<T, VEC> v;
             ring.get(v, slot, u);
             widen(d, v);
-            cut(d, u);
         }
     }
     // Stores the values that lie in the row.  A vector is made before anything is asked, so that its store is one predicated
@@ -299,11 +299,12 @@ __global__ void __launch_bounds__(MOST, FWD_RESIDENT<G, E, MOST>) fwd_rows(const
         float2 d[U][H];
         float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            un.take(d[u], ring, slot, x + r * p.x_stride, u, live);
+        for (int u = 0; u < U; ++u) un.take(d[u], ring, slot, x + r * p.x_stride, u, live);
+        un.cut(d);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int i = 0; i < H; ++i) s2 = add2(s2, d[u][i]);
-        }
         float s[1] = {s2.x + s2.y};
         row_sum<G>(s, sums[0]);
         ask(slot, r + DEPTH * step);  // what the slot held is in registers
@@ -313,13 +314,15 @@ __global__ void __launch_bounds__(MOST, FWD_RESIDENT<G, E, MOST>) fwd_rows(const
         s2 = make_float2(0.f, 0.f);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const float2 m = WHOLE && un.none(u) ? make_float2(0.f, 0.f) : minus;  // zeros beyond the row stay
+            const float2 m = un.none(u) ? make_float2(0.f, 0.f) : minus;  // zeros beyond the row stay
 #pragma unroll
             for (int i = 0; i < H; ++i) d[u][i] = add2(d[u][i], m);
-            un.cut(d[u], u);
+        }
+        un.cut(d);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
 #pragma unroll
             for (int i = 0; i < H; ++i) s2 = fma2(d[u][i], d[u][i], s2);
-        }
         s[0] = s2.x + s2.y;
         row_sum<G>(s, sums[1]);
         const float rstd = rsqrtf(s[0] * p.inv_cols + p.eps);
@@ -413,6 +416,11 @@ __global__ void __launch_bounds__(MOST, BWD_RESIDENT<G, E, MOST>) bwd_rows(const
         for (int u = 0; u < U; ++u) {
             un.take(xh[u], ring_x, slot, x + r * p.x_stride, u, live);
             un.take(g[u], ring_g, slot, dy + r * p.dy_stride, u, live);
+        }
+        un.cut(xh);
+        un.cut(g);
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
 #pragma unroll
             for (int i = 0; i < H; ++i) {  // outside the row dy is zero and the normalised value finite where mean and rstd are
                 xh[u][i] = mul2(add2(xh[u][i], minus), scale);
