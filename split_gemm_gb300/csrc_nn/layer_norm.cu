@@ -59,8 +59,9 @@ void by_types(int32_t x, int32_t y, F&& f)
 }
 
 // Parts that the sums over the rows are made in: one for each block of the kernel that takes them.
-constexpr int64_t PART_ROWS = 64;     // rows too wide for registers: of one part, at least
-constexpr int64_t PART_CHUNKS = 512;  // and parts, at most
+// Parts that the sums over the rows are made in: one for each block of the kernel that takes them, or, for rows too wide
+// for that, a multiple of 8 of some 32 rows each, at most so many.
+constexpr int64_t PART_ROWS = 32, PARTS = 128;
 
 // Columns that the threads of a row have to hold: where rows do not start at whole vectors, up to 7 elements
 // stand in front of them.
@@ -76,8 +77,8 @@ int64_t bwd_parts(const layer_norm_params* p)
 {
     const RowShape s = bwd_shape(p->rows, span_of(p), static_cast<int>(dtype_size(p->x_dtype)), span_of(p) == p->cols);
     if (!sums_in_rows(s)) {
-        const int64_t n = mx::cdiv(p->rows, PART_ROWS);
-        return n < PART_CHUNKS ? n : PART_CHUNKS;
+        const int64_t n = mx::cdiv(p->rows, 8 * PART_ROWS) * 8;
+        return n < PARTS ? n : PARTS;
     }
     return bwd_blocks(p->rows, s);
 }
@@ -191,7 +192,6 @@ extern "C" int layer_norm_bwd(const layer_norm_params* params, const void* dy_de
     k.dx = dx_dev;
     k.part = sums ? static_cast<float*>(workspace_dev) : nullptr;
     k.chunks = static_cast<int>(ln::bwd_parts(params));
-    k.chunk = k.chunks ? mx::cdiv<int64_t>(params->rows, k.chunks) : 0;
     const int64_t v = ln::vector_of(params->x_dtype);
     const size_t sx = ln::dtype_size(params->x_dtype);
     const bool vec = ln::in_vectors(x_dev, k.x_stride, k.x_stride, sx, v) && ln::in_vectors(dx_dev, k.cols, k.x_stride, sx, v) &&
@@ -209,8 +209,14 @@ extern "C" int layer_norm_bwd(const layer_norm_params* params, const void* dy_de
             const TY* dy = static_cast<const TY*>(dy_dev);
             if (rc == CONV2D_ERR_UNSUPPORTED)
                 ln::bwd_dx_any<<<ln::row_grid(k.rows), ln::THREADS, 0, stream>>>(dy, x, static_cast<TX*>(dx_dev), k);
-            const dim3 grid(static_cast<unsigned>(mx::cdiv(k.cols, ln::THREADS)), static_cast<unsigned>(k.chunks));
-            if (sums) ln::bwd_part_any<<<grid, ln::THREADS, 0, stream>>>(dy, x, k);
+            constexpr int VEC = 16 / sizeof(TX);
+            const auto columns = [&](int vec) {  // with what may stand in front of an unaligned row
+                return dim3(static_cast<unsigned>(mx::cdiv<int64_t>(int64_t(k.cols) + vec - 1, ln::THREADS * vec)), static_cast<unsigned>(k.chunks));
+            };
+            if (sums && vec)
+                ln::bwd_part_any<TX, TY, VEC><<<columns(VEC), ln::THREADS, 0, stream>>>(dy, x, k);
+            else if (sums)
+                ln::bwd_part_any<TX, TY, 1><<<columns(1), ln::THREADS, 0, stream>>>(dy, x, k);
             rc = ln::launched();
         });
     if (rc) return rc;

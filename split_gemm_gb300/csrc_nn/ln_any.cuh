@@ -124,23 +124,50 @@ __global__ void __launch_bounds__(THREADS) bwd_dx_any(const TY* dy, const TX* x,
     }
 }
 
-// Partial sums of dweight and dbias over one chunk of rows, a thread to a column.
-template <typename TX, typename TY>
-__global__ void __launch_bounds__(THREADS) bwd_part_any(const TY* dy, const TX* x, const BwdParams p)
+// Partial sums of dweight and dbias for rows too wide for registers: a thread keeps VEC columns and takes every
+// p.chunks-th row.  Rows of one part lie a multiple of 8 rows apart, so they begin at the same place within 16 bytes, and vectors
+// are whole from there: what stands in front of a row (the row before) adds to sums that are not written.  Bound by HBM.
+template <typename TX, typename TY, int VEC>
+__global__ void __launch_bounds__(THREADS) bwd_part_any(const TY* __restrict__ dy, const TX* __restrict__ x, const BwdParams p)
 {
-    const int c = blockIdx.x * THREADS + threadIdx.x;
-    if (c >= p.cols) return;
-    for (int k = blockIdx.y; k < p.chunks; k += gridDim.y) {
-        const int64_t r0 = k * p.chunk, r1 = r0 + p.chunk < p.rows ? r0 + p.chunk : p.rows;
-        float dw = 0.f, db = 0.f;
-        for (int64_t r = r0; r < r1; ++r) {
-            const float g = mx::to_float(dy[r * p.dy_stride + c]);
-            dw = fmaf(g, (mx::to_float(x[r * p.x_stride + c]) - p.mean[r]) * p.rstd[r], dw);
-            db += g;
+    const int k = blockIdx.y;
+    const int off = VEC > 1 ? static_cast<int>(k * p.x_stride % VEC) : 0;
+    const int c0 = (blockIdx.x * THREADS + threadIdx.x) * VEC - off;
+    if (c0 >= p.cols) return;
+    const bool tail = c0 + VEC > p.cols;  // the last row's end may be the tensor's
+    float dw[VEC] = {}, db[VEC] = {};
+#pragma unroll 4
+    for (int64_t r = k; r < p.rows; r += p.chunks) {
+        const float mean = __ldg(p.mean + r), rstd = __ldg(p.rstd + r);
+        const TX* xr = x + r * p.x_stride + c0;
+        const TY* gr = dy + r * p.dy_stride + c0;
+        struct alignas(sizeof(TX) * VEC < 16 ? sizeof(TX) * VEC : 16) X { TX v[VEC]; } xv;
+        struct alignas(sizeof(TY) * VEC < 16 ? sizeof(TY) * VEC : 16) G { TY v[VEC]; } gv;
+        if (!tail) {
+            xv = *reinterpret_cast<const X*>(xr);
+            gv = *reinterpret_cast<const G*>(gr);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VEC; ++i) {
+                const bool in = c0 + i >= 0 && c0 + i < p.cols;
+                xv.v[i] = in ? xr[i] : TX(0.f);
+                gv.v[i] = in ? gr[i] : TY(0.f);
+            }
         }
-        p.part[(2 * static_cast<int64_t>(k)) * p.cols + c] = dw;
-        p.part[(2 * static_cast<int64_t>(k) + 1) * p.cols + c] = db;
+#pragma unroll
+        for (int i = 0; i < VEC; ++i) {
+            const float g = mx::to_float(gv.v[i]);
+            dw[i] = fmaf(g, (mx::to_float(xv.v[i]) - mean) * rstd, dw[i]);
+            db[i] += g;
+        }
     }
+    float* part = p.part + 2 * static_cast<int64_t>(k) * p.cols;
+#pragma unroll
+    for (int i = 0; i < VEC; ++i)
+        if (c0 + i >= 0 && c0 + i < p.cols) {
+            part[c0 + i] = dw[i];
+            part[p.cols + c0 + i] = db[i];
+        }
 }
 
 // Joins the partial sums in a fixed order: a block has 32 columns and 32 sums of every 32nd part.

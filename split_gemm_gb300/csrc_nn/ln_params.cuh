@@ -20,7 +20,7 @@ struct FwdParams {
 struct BwdParams {
     const void *x, *dy;
     void* dx;
-    int64_t rows, x_stride, dy_stride, chunk;
+    int64_t rows, x_stride, dy_stride;
     int cols, span;
     float inv_cols;
     const float *mean, *rstd, *weight;
