@@ -184,61 +184,70 @@ __global__ void __launch_bounds__(D_THREADS) dequantize_kernel(const uint8_t* __
     const int64_t blocks = cdiv<int64_t>(cols, BLOCK), btiles = cdiv<int64_t>(blocks, TILE_BLOCKS);
     const int64_t words = blocks * 4;
     const int64_t w = (static_cast<int64_t>(blockIdx.x) << lanes_log2) + (threadIdx.x & ((1 << lanes_log2) - 1));
-    const int64_t per = D_THREADS >> lanes_log2, step = gridDim.y * per;
-    const int64_t r0 = blockIdx.y * per + (threadIdx.x >> lanes_log2);
-    const int64_t lead = blockIdx.y * per + ((threadIdx.x & ~31) >> lanes_log2);  // of the warp, whose lanes stay together
+    constexpr int DEPTH = 4;  // neighbouring rows, on their way at once
+    const int64_t per = (D_THREADS >> lanes_log2) * DEPTH, step = gridDim.y * per;
+    const int64_t r0 = blockIdx.y * per + (threadIdx.x >> lanes_log2) * DEPTH;
+    const int64_t lead = blockIdx.y * per + ((threadIdx.x & ~31) >> lanes_log2) * DEPTH;  // of the warp, whose lanes stay together
     const uint8_t* scale_col = scales + (w >> 4) * TILE_BYTES + ((w >> 2) & 3);
     const int lane = threadIdx.x & 31;
     ptx::grid_dependency_wait();
     ptx::grid_launch_dependents();
-#pragma unroll 4
-    for (int64_t k = 0; lead + k < rows; k += step) {
-        const int64_t r = r0 + k;
-        float2 v[4] = {};
-        if (r < rows && w < words) {
-            const uint32_t word = __ldg(reinterpret_cast<const uint32_t*>(data) + r * words + w);
-            const float s = scale_value(__ldg(scale_col + scale_at(r, 0, btiles)));
-            unpack_e2m1x8(v, word);
+    for (int64_t k0 = 0; lead + k0 < rows; k0 += step) {
+        uint32_t words_of[DEPTH] = {}, scale_of[DEPTH] = {};
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d) {
+            const int64_t r = r0 + k0 + d;
+            if (r < rows && w < words) {
+                words_of[d] = __ldg(reinterpret_cast<const uint32_t*>(data) + r * words + w);
+                scale_of[d] = __ldg(scale_col + scale_at(r, 0, btiles));
+            }
+        }
+#pragma unroll
+        for (int d = 0; d < DEPTH; ++d) {
+            const int64_t r = r0 + k0 + d;
+            float2 v[4];
+            unpack_e2m1x8(v, words_of[d]);
+            const float s = scale_value(scale_of[d]);
 #pragma unroll
             for (int j = 0; j < 4; ++j) v[j] = mul2(v[j], make_float2(s, s));
-        }
-        if constexpr (VEC) {
-            if (r < rows && w * 8 < cols) {
-                T* out = y + r * cols + w * 8;
-                if constexpr (sizeof(T) == 4) {
-                    if (reinterpret_cast<uintptr_t>(out) % 32 == 0) {  // a whole sector to a thread
-                        asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out), "f"(v[0].x), "f"(v[0].y),
-                                     "f"(v[1].x), "f"(v[1].y), "f"(v[2].x), "f"(v[2].y), "f"(v[3].x), "f"(v[3].y)
-                                     : "memory");
+            if constexpr (VEC) {
+                if (r < rows && w * 8 < cols) {
+                    T* out = y + r * cols + w * 8;
+                    if constexpr (sizeof(T) == 4) {
+                        if (reinterpret_cast<uintptr_t>(out) % 32 == 0) {  // a whole sector to a thread
+                            asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out), "f"(v[0].x), "f"(v[0].y),
+                                         "f"(v[1].x), "f"(v[1].y), "f"(v[2].x), "f"(v[2].y), "f"(v[3].x), "f"(v[3].y)
+                                         : "memory");
+                        } else {
+                            reinterpret_cast<float4*>(out)[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+                            reinterpret_cast<float4*>(out)[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+                        }
                     } else {
-                        reinterpret_cast<float4*>(out)[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
-                        reinterpret_cast<float4*>(out)[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
-                    }
-                } else {
-                    uint32_t o[4];
+                        uint32_t o[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const __nv_bfloat162 h = __floats2bfloat162_rn(v[j].x, v[j].y);
-                        o[j] = *reinterpret_cast<const uint32_t*>(&h);
+                        for (int j = 0; j < 4; ++j) {
+                            const __nv_bfloat162 h = __floats2bfloat162_rn(v[j].x, v[j].y);
+                            o[j] = *reinterpret_cast<const uint32_t*>(&h);
+                        }
+                        *reinterpret_cast<uint4*>(out) = make_uint4(o[0], o[1], o[2], o[3]);
                     }
-                    *reinterpret_cast<uint4*>(out) = make_uint4(o[0], o[1], o[2], o[3]);
                 }
-            }
-        } else {
-            float(*mine)[9] = gather + (threadIdx.x & ~31);
-            __syncwarp();
+            } else {
+                float(*mine)[9] = gather + (threadIdx.x & ~31);
+                __syncwarp();
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                mine[lane][2 * j] = v[j].x;
-                mine[lane][2 * j + 1] = v[j].y;
-            }
-            __syncwarp();
+                for (int j = 0; j < 4; ++j) {
+                    mine[lane][2 * j] = v[j].x;
+                    mine[lane][2 * j + 1] = v[j].y;
+                }
+                __syncwarp();
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int from = 4 * e + lane / 8;  // the thread whose element this is
-                const int64_t fr = __shfl_sync(0xffffffffu, r, from), fw = __shfl_sync(0xffffffffu, w, from);
-                const int64_t c = fw * 8 + lane % 8;
-                if (fr < rows && c < cols) from_float(y[fr * cols + c], mine[from][lane % 8]);
+                for (int e = 0; e < 8; ++e) {
+                    const int from = 4 * e + lane / 8;  // the thread whose element this is
+                    const int64_t fr = __shfl_sync(0xffffffffu, r, from), fw = __shfl_sync(0xffffffffu, w, from);
+                    const int64_t c = fw * 8 + lane % 8;
+                    if (fr < rows && c < cols) from_float(y[fr * cols + c], mine[from][lane % 8]);
+                }
             }
         }
     }
@@ -269,7 +278,7 @@ int dequantize(const uint8_t* data, const uint8_t* scales, void* y, int64_t rows
     int lanes_log2 = 2;
     while (lanes_log2 < 8 && (int64_t(1) << lanes_log2) < words) ++lanes_log2;
     // Eight blocks to an SM at most: they stay, and go down the rows.
-    const int64_t across = cdiv<int64_t>(words, int64_t(1) << lanes_log2), down = cdiv<int64_t>(rows, D_THREADS >> lanes_log2);
+    const int64_t across = cdiv<int64_t>(words, int64_t(1) << lanes_log2), down = cdiv<int64_t>(rows, (D_THREADS >> lanes_log2) * 4);
     const int64_t most = cdiv<int64_t>(SMS * 8, across) < 65535 ? cdiv<int64_t>(SMS * 8, across) : 65535;
     if (across > INT32_MAX) return CONV2D_ERR_UNSUPPORTED;
     const dim3 grid(static_cast<unsigned>(across), static_cast<unsigned>(down < most ? down : most));
