@@ -58,24 +58,37 @@ void by_types(int32_t x, int32_t y, F&& f)
         y == CONV2D_OUT_BF16 ? f(f32, b16) : f(f32, f32);
 }
 
-// Parts that the sums over the rows are made in: one for each block of the kernel that takes them.
 // Parts that the sums over the rows are made in: one for each block of the kernel that takes them, or, for rows too wide
 // for that, a multiple of 8 of some 32 rows each, at most so many.
 constexpr int64_t PART_ROWS = 32, PARTS = 128;
 
 // Columns that the threads of a row have to hold: where rows do not start at whole vectors, up to 7 elements
-// stand in front of them.
-int64_t span_of(const layer_norm_params* p)
+// stand in front of them.  A row that fits its kernel (`most` columns) only without those is read by elements instead,
+// where that is the faster way.
+bool whole_rows(const layer_norm_params* p) { return (p->cols | p->x_stride | p->y_stride) % 8 == 0; }
+
+int64_t span_of(const layer_norm_params* p, int64_t most)
 {
-    return (p->cols | p->x_stride | p->y_stride) % 8 == 0 ? p->cols : p->cols + 7;
+    return whole_rows(p) || (p->cols <= most && p->cols + 7 > most) ? p->cols : p->cols + 7;
 }
+
+// 16384 columns: else the kernels for any width (8192 x 16383: fp32 forward 245 us against 379, backward 437 against 655; but
+// bf16 forward 327 against 212, backward 456 against 442; bf16, 64 rows: 6.6 against 16.7 and 14.4 against 22.4).
+int64_t most_columns(const layer_norm_params* p) { return p->x_dtype == CONV2D_OUT_F32 || p->rows <= SMS ? 16384 : 0; }
+int64_t fwd_span(const layer_norm_params* p) { return span_of(p, most_columns(p)); }
+// 8192 columns: else the sums take a kernel of their own (16384 x 8191: bf16 284 us against 354, fp32 337 against 588).
+int64_t bwd_span(const layer_norm_params* p) { return span_of(p, p->cols <= 8192 ? 8192 : most_columns(p)); }
+
+// Whether the kernels that hold rows read them in vectors, `vec` telling of their alignment to each other.
+bool rows_in_vectors(const layer_norm_params* p, int64_t span, bool vec) { return vec && (span != p->cols || whole_rows(p)); }
 
 // Whether the kernel that computes dx holds the sums over its rows as well.
 bool sums_in_rows(RowShape s) { return s.elems == 8 || s.elems == 16; }
 
 int64_t bwd_parts(const layer_norm_params* p)
 {
-    const RowShape s = bwd_shape(p->rows, span_of(p), static_cast<int>(dtype_size(p->x_dtype)), span_of(p) == p->cols);
+    const int64_t span = bwd_span(p);
+    const RowShape s = bwd_shape(p->rows, span, static_cast<int>(dtype_size(p->x_dtype)), span == p->cols);
     if (!sums_in_rows(s)) {
         const int64_t n = mx::cdiv(p->rows, 8 * PART_ROWS) * 8;
         return n < PARTS ? n : PARTS;
@@ -114,12 +127,13 @@ extern "C" int layer_norm_fwd(const layer_norm_params* params, const void* x_dev
     const int64_t v = ln::vector_of(params->x_dtype);
     const bool vec = ln::in_vectors(x_dev, k.x_stride, k.x_stride, ln::dtype_size(params->x_dtype), v) &&
                      ln::in_vectors(y_dev, k.y_stride, k.x_stride, ln::dtype_size(params->y_dtype), v);
-    k.span = static_cast<int>(ln::span_of(params));
+    k.span = static_cast<int>(ln::fwd_span(params));
+    const bool rows_vec = ln::rows_in_vectors(params, k.span, vec);
     int rc = CONV2D_OK;
     ln::by_types(params->x_dtype, params->y_dtype, [&](auto* tx, auto* ty) {
         using TX = std::remove_pointer_t<decltype(tx)>;
         using TY = std::remove_pointer_t<decltype(ty)>;
-        rc = ln::launch_fwd_rows<TX, TY>(k, vec, stream);
+        rc = ln::launch_fwd_rows<TX, TY>(k, rows_vec, stream);
         if (rc != CONV2D_ERR_UNSUPPORTED) return;
         ln::fwd_any<<<ln::row_grid(k.rows), ln::THREADS, 0, stream>>>(static_cast<const TX*>(x_dev), static_cast<TY*>(y_dev), k);
         rc = ln::launched();
@@ -196,13 +210,14 @@ extern "C" int layer_norm_bwd(const layer_norm_params* params, const void* dy_de
     const size_t sx = ln::dtype_size(params->x_dtype);
     const bool vec = ln::in_vectors(x_dev, k.x_stride, k.x_stride, sx, v) && ln::in_vectors(dx_dev, k.cols, k.x_stride, sx, v) &&
                      ln::in_vectors(dy_dev, k.dy_stride, k.x_stride, ln::dtype_size(params->y_dtype), v);
-    k.span = static_cast<int>(ln::span_of(params));
+    k.span = static_cast<int>(ln::bwd_span(params));
+    const bool rows_vec = ln::rows_in_vectors(params, k.span, vec);
     int rc = CONV2D_OK;
     if (params->rows > 0)
         ln::by_types(params->x_dtype, params->y_dtype, [&](auto* tx, auto* ty) {
             using TX = std::remove_pointer_t<decltype(tx)>;
             using TY = std::remove_pointer_t<decltype(ty)>;
-            rc = ln::launch_bwd_rows<TX, TY>(k, vec, k.chunks, stream);
+            rc = ln::launch_bwd_rows<TX, TY>(k, rows_vec, k.chunks, stream);
             if (rc != CONV2D_OK && rc != CONV2D_ERR_UNSUPPORTED) return;
             if (rc == CONV2D_OK && ln::sums_in_rows(ln::bwd_shape(k.rows, k.span, sizeof(TX), k.span == k.cols))) return;
             const TX* x = static_cast<const TX*>(x_dev);

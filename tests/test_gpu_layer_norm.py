@@ -153,6 +153,17 @@ def test_backward(sg, rows, cols, xt, dt):
     assert all(torch.equal(a, b) for a, b in zip(got, again))  # fixed order
 
 
+@pytest.mark.parametrize("rows", [9, 160])
+@pytest.mark.parametrize("cols", [1017, 2041, 4095, 4097, 8184, 8185, 8191, 8193, 16377, 16383, 16385])
+@pytest.mark.parametrize("xt,yt", [(F32, F32), (BF16, BF16), (F32, BF16), (BF16, F32)])
+def test_widths_at_the_limits_of_the_shapes(sg, rows, cols, xt, yt):
+    """Rows that fill a block's registers, with and without room for what stands in front of an unaligned one."""
+    w, b = _params(cols)
+    _check_fwd(sg, _rows(rows, cols, xt), w, b, yt)
+    x, dy, w, mean, rstd = _grad_inputs(sg, rows, cols, xt, yt)
+    _check_bwd(sg.layer_norm_bwd(dy.cuda(), x.cuda(), mean, rstd, w.cuda()), dy, x, mean, rstd, w, xt)
+
+
 @pytest.mark.parametrize("cols", [24, 256, 4096])
 def test_backward_without_weight_and_partial_outputs(sg, cols):
     x, dy, w, mean, rstd = _grad_inputs(sg, 50, cols, BF16, BF16)
