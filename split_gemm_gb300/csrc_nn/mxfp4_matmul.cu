@@ -143,7 +143,8 @@ int product(const Operand& a, const Operand& b, TileParams& k, cudaStream_t stre
     // Up to 128 rows of y: the weight's rows in the accumulator's lanes, y's rows in
     // its columns, as few as cover them.
     const bool swap = a.rows <= 128;
-    // 256 x 256 tiles where they fill half of the SM pairs.
+    // 256 x 256 tiles where they fill half of the SM pairs (bf16 y; 32 tiles, 512 x 4096 x 4096: pairs 10.4 us, single CTAs 9.6;
+    // 40 tiles, 1280 x 2048 x 1024: 6.9 and 10.9; 64 tiles, 1024 x 4096 x 4096: 10.7 and 18.5).
     if (!swap && cdiv<int64_t>(a.rows, W_TILE) * cdiv<int64_t>(b.rows, W_TILE) * 4 >= SMS) return launch_pair<T>(a, b, k, stream);
     const Operand &P = swap ? b : a, &Q = swap ? a : b;
     k.p_scales = static_cast<const uint8_t*>(P.scales);
