@@ -19,7 +19,7 @@ constexpr int TILE_BLOCKS = 4;
 constexpr int TILE_BYTES = 512;
 
 template <typename T>
-__host__ __device__ constexpr T cdiv(T a, T b) { return (a + b - 1) / b; }
+__host__ __device__ constexpr T cdiv(T a, T b) { return a / b + (a % b != 0); }  // a up to the type's largest
 
 // Byte of row r, block b within the scales of a matrix with `btiles` tiles to a row of tiles.
 __host__ __device__ __forceinline__ int64_t scale_at(int64_t r, int64_t b, int64_t btiles)

@@ -211,6 +211,37 @@ def test_backward_is_the_forward_s_difference_quotient(sg):
         assert abs(((hi - lo) * _np(dy)).sum() / (2 * h) - dx[i]) < 5e-3
 
 
+@pytest.mark.parametrize("cols,extra", [(1000, 8), (1001, 9), (17000, 8)])
+def test_rows_beyond_32_bit_offsets(sg, cols, extra):
+    """Rows more than 2^31 elements apart: the last row's neighbours in the low 32 bits are another's."""
+    stride = (1 << 30) + extra
+    small = _rows(3, cols, BF16)
+    buf = torch.zeros(2 * stride + cols + 8, device="cuda", dtype=BF16)
+    xd = buf.as_strided((3, cols), (stride, 1))
+    xd.copy_(small)
+    w, b = _params(cols)
+    y, mean, rstd = sg.layer_norm_fwd(xd, w.cuda(), b.cuda())
+    want = sg.layer_norm_fwd(small.cuda(), w.cuda(), b.cuda())
+    assert all(torch.allclose(g.float(), h.float(), rtol=2 ** -7, atol=2 ** -7) for g, h in zip((y, mean, rstd), want))
+    dy = _rows(3, cols, BF16, seed=2)
+    got = sg.layer_norm_bwd(dy.cuda(), xd, mean, rstd, w.cuda())
+    _check_bwd(got, dy, small, mean, rstd, w, BF16)
+
+
+def test_results_beyond_32_bit_offsets(sg):
+    """More than 2^31 elements in x, y, dy and dx: the last rows come out as they do on their own."""
+    rows, cols, last = (1 << 21) + 37, 1024, 5
+    x = torch.randn(rows, cols, device="cuda", dtype=BF16)
+    tail = x[-last:].cpu()
+    y, mean, rstd = sg.layer_norm_fwd(x)
+    ones = torch.ones(cols)
+    want = sg.layer_norm_fwd(tail.cuda())
+    assert torch.allclose(y[-last:].float(), want[0].float(), rtol=2 ** -7, atol=2 ** -7)
+    dx = sg.layer_norm_bwd(y, x, mean, rstd)[0]
+    alone = sg.layer_norm_bwd(y[-last:], x[-last:], mean[-last:], rstd[-last:], ones.cuda())[0]
+    assert torch.allclose(dx[-last:].float(), alone.float(), rtol=2 ** -7, atol=2 ** -7)
+
+
 @pytest.mark.parametrize("rows,cols", [(1, 1), (1, 4096), (3, 40), (785, 1001), (130, 96), (257, 8192), (5, 20000), (64, 256), (300, 1000)])
 @pytest.mark.parametrize("xt", [F32, BF16])
 def test_forward_into_4_bits(sg, rows, cols, xt):

@@ -190,6 +190,29 @@ def test_matmul_empty_and_other_stream(sg):
     assert torch.equal(v, sg.mxfp4_dequantize(sg.mxfp4_quantize(x)))
 
 
+def test_matrices_beyond_32_bit_offsets(sg):
+    """More than 2^31 elements: the last rows and columns are quantised, and come back, as they do on their own."""
+    rows, cols = 1 << 16, (1 << 15) + 128
+    x = torch.randn(rows, cols, device="cuda", dtype=BF16)
+    q, q_t = sg.mxfp4_quantize_both(x)
+    alone, alone_t = sg.mxfp4_quantize(x[-128:]), sg.mxfp4_quantize(x[:, -128:], transpose=True)
+    assert torch.equal(q.data.view(-1)[-alone.data.numel():], alone.data.view(-1))
+    assert torch.equal(q.scales.view(-1)[-alone.scales.numel():], alone.scales.view(-1))
+    assert torch.equal(q_t.data.view(-1)[-alone_t.data.numel():], alone_t.data.view(-1))
+    assert torch.equal(q_t.scales.view(-1)[-alone_t.scales.numel():], alone_t.scales.view(-1))
+    assert torch.equal(sg.mxfp4_dequantize(q)[-128:], sg.mxfp4_dequantize(alone))
+
+
+@pytest.mark.parametrize("n", [(1 << 14) + 16, (1 << 14) + 5])
+def test_results_beyond_32_bit_offsets(sg, n):
+    """More than 2^31 elements of y, stored by boxes and element by element: the last rows come out as they do on their own."""
+    m, k = (1 << 17) + 37, 64
+    a, b = torch.randn(m, k, device="cuda"), torch.randn(n, k, device="cuda")
+    qb = sg.mxfp4_quantize(b)
+    y = sg.mxfp4_matmul(sg.mxfp4_quantize(a), qb, out_dtype=BF16)
+    assert torch.equal(y[-300:], sg.mxfp4_matmul(sg.mxfp4_quantize(a[-300:]), qb, out_dtype=BF16))
+
+
 def test_gradients_of_the_product(sg):
     """dx and dw of y = x w^T from the quantised operands are the oracle's products of the oracle's quantisations."""
     m, n, k = 200, 96, 160
