@@ -153,10 +153,10 @@ extern "C" int layer_norm_mxfp4(const layer_norm_params* params, const void* x_d
         return CONV2D_ERR_ALIGNMENT;
     ln::FwdParams k = ln::fwd_params(params, weight_dev, bias_dev, mean_dev, rstd_dev);
     k.x = x_dev;
-    // the format's blocks start with the row: whole vectors only
     const int64_t v = ln::vector_of(params->x_dtype);
-    const bool vec = k.cols % v == 0 && k.x_stride % v == 0 && ln::aligned(x_dev, 16);
-    k.span = k.cols;
+    const bool whole = k.cols % v == 0 && k.x_stride % v == 0;
+    k.span = static_cast<int>(whole ? k.cols : ln::fwd_span(params));
+    const bool vec = ln::aligned(x_dev, 16) && (whole || k.span != k.cols);
     k.data = static_cast<uint8_t*>(data_dev);
     k.scales = static_cast<uint8_t*>(scales_dev);
     int rc = CONV2D_OK;

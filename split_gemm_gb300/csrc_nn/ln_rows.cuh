@@ -145,6 +145,31 @@ struct Units {
             widen(d, v);
         }
     }
+    // The same where the row begins `shift` elements behind the ring's first vector but columns begin with the row: a
+    // vector's values lie in two of the ring's, the second another thread's (of the last vector of all nothing lies there).
+    template <typename T, typename R>
+    __device__ __forceinline__ void take_shifted(float2 (&d)[H], const R& ring, int slot, int u, int shift) const
+    {
+        static_assert(sizeof(T) * VEC == 16, "a vector to a copy");
+        const uint8_t* at = ring.at(slot, u, 0);
+        const uint4 lo = *reinterpret_cast<const uint4*>(at);
+        uint4 hi = make_uint4(0, 0, 0, 0);
+        if (t + 1 < g)
+            hi = *reinterpret_cast<const uint4*>(at + 16);
+        else if (u + 1 < U)
+            hi = *reinterpret_cast<const uint4*>(ring.at(slot, u + 1, 0) - (g - 1) * 16);
+        uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        constexpr int PER = 4 / sizeof(T);  // elements of a word
+#pragma unroll
+        for (int i = 0; i < 6; ++i) w[i] = shift & (2 * PER) ? w[i + 2] : w[i];
+#pragma unroll
+        for (int i = 0; i < 5; ++i) w[i] = shift & PER ? w[i + 1] : w[i];
+        Pack<T, VEC> v;
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            reinterpret_cast<uint32_t*>(&v)[i] = PER == 2 ? __funnelshift_r(w[i], w[i + 1], 16 * (shift & 1)) : w[i];
+        widen(d, v);
+    }
     // Stores the values that lie in the row.  A vector is made before anything is asked, so that its store is one predicated
     // instruction (a branch around both cost the backward pass a quarter of its time), and a row's first and last vector wait for one branch at the end.
     template <typename T>
@@ -255,7 +280,9 @@ __device__ __forceinline__ void store_mx(const float2 (&v)[(VEC + 1) / 2], int c
     if (in_tile && lane % LANES == 0) scales[b / 4 * mx::TILE_BYTES + (b & 3)] = static_cast<uint8_t>(byte);
 }
 
-// Forward.  TY = void: the result quantised; rows from p.rows to p.padded_rows are the scale tiles' padding (and `off` is 0).
+// Forward.  TY = void: the result quantised; rows from p.rows to p.padded_rows are the scale tiles' padding.  The format's blocks
+// begin with the row, so `off` is 0 there, and vectors of rows that do not start at 16 bytes are put together from the ring's,
+// which takes one barrier more to a row.
 template <typename TX, typename TY, int VEC, int E, int G, int MOST, bool WHOLE>
 __global__ void __launch_bounds__(MOST, FWD_RESIDENT<G, E, MOST>) fwd_rows(const TX* __restrict__ x, TY* y, const FwdParams p)
 {
@@ -272,13 +299,15 @@ __global__ void __launch_bounds__(MOST, FWD_RESIDENT<G, E, MOST>) fwd_rows(const
     const int g = G ? G : blockDim.x;
     const int64_t first = static_cast<int64_t>(blockIdx.x) * ROWS + (G ? threadIdx.x / (G ? G : 1) : 0);
     const int64_t lead = G && G < 32 ? static_cast<int64_t>(blockIdx.x) * ROWS + (threadIdx.x & ~31) / (G ? G : 1) : first;
-    const Un un(G ? threadIdx.x % (G ? G : 1) : threadIdx.x, g, WHOLE || VEC == 1 ? 0 : static_cast<int>(first * p.x_stride % VEC), p.cols);
+    constexpr bool SHIFTED = MX && VEC > 1 && !WHOLE;
+    const int before = WHOLE || VEC == 1 ? 0 : static_cast<int>(first * p.x_stride % VEC);  // elements in front of a row
+    const Un un(G ? threadIdx.x % (G ? G : 1) : threadIdx.x, g, SHIFTED ? 0 : before, p.cols);
     const int blocks = MX ? mx::cdiv(p.cols, mx::BLOCK) : 0, btiles = MX ? mx::cdiv(blocks, mx::TILE_BLOCKS) : 0;
 
     const Ring<TX, VEC == 1 ? 8 : VEC, VEC == 1 ? 1 : Un::NV, DEPTH> ring(ring_mem, blockDim.x);
     auto ask = [&](int slot, int64_t r) {
         if constexpr (VEC > 1) {
-            ring.ask(slot, x + (r < p.rows ? r * p.x_stride : 0), un.t * VEC - un.off, g * VEC, r < p.rows ? p.cols : 0);
+            ring.ask(slot, x + (r < p.rows ? r * p.x_stride : 0), un.t * VEC - before, g * VEC, r < p.rows ? p.cols : 0);
             ptx::cp_async_commit();
         }
     };
@@ -299,8 +328,14 @@ __global__ void __launch_bounds__(MOST, FWD_RESIDENT<G, E, MOST>) fwd_rows(const
         if constexpr (VEC > 1) ptx::cp_async_wait<DEPTH - 1>();
         float2 d[U][H];
         float2 s2 = make_float2(0.f, 0.f);
+        if constexpr (SHIFTED) G ? __syncwarp() : __syncthreads();  // the others' copies have landed as well
 #pragma unroll
-        for (int u = 0; u < U; ++u) un.take(d[u], ring, slot, x + r * p.x_stride, u, live);
+        for (int u = 0; u < U; ++u) {
+            if constexpr (SHIFTED)
+                un.template take_shifted<TX>(d[u], ring, slot, u, before);
+            else
+                un.take(d[u], ring, slot, x + r * p.x_stride, u, live);
+        }
         un.cut(d);
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -308,6 +343,7 @@ __global__ void __launch_bounds__(MOST, FWD_RESIDENT<G, E, MOST>) fwd_rows(const
             for (int i = 0; i < H; ++i) s2 = add2(s2, d[u][i]);
         float s[1] = {s2.x + s2.y};
         row_sum<G>(s, sums[0]);
+        if constexpr (SHIFTED && G) __syncwarp();  // (a block's threads met in the sum)
         ask(slot, r + DEPTH * step);  // what the slot held is in registers
         slot = slot + 1 == DEPTH ? 0 : slot + 1;
         const float mean = s[0] * p.inv_cols;

@@ -269,6 +269,26 @@ def test_forward_into_4_bits(sg, rows, cols, xt):
     assert not codes[:, cols:].any()
 
 
+@pytest.mark.parametrize("xt", [F32, BF16])
+@pytest.mark.parametrize("cols", [31, 33, 57, 63, 121, 127, 129, 250, 255, 505, 511, 513, 767, 1001, 2047, 4097, 8187, 12001, 16377, 16383])
+def test_forward_into_4_bits_at_odd_widths(sg, cols, xt):
+    """Rows that do not begin at whole vectors: the same codes and scales as of rows that do, at a stride of whole ones."""
+    rows = 137
+    wide = torch.zeros(rows, (cols + 7) // 8 * 8 + 8, dtype=xt)
+    wide[:, :cols] = _rows(rows, cols, xt)
+    x = wide[:, :cols].contiguous().cuda()
+    w, b = (t.cuda() for t in _params(cols))
+    q = sg.layer_norm_mxfp4(x, w, b)
+    y = sg.layer_norm_fwd(x, w, b, out_dtype=F32)[0]
+    want = sg.mxfp4_quantize(y)
+    got, full = sg.mxfp4_dequantize(q, out_dtype=F32), sg.mxfp4_dequantize(want, out_dtype=F32)
+    # rounding in fp32 may put a value on the other side of a step, or a block's largest past a power of two
+    same = (got == full).float().mean().item()
+    assert same > 0.999, same
+    # between neighbours of E2M1 lie at most 2 units of the scale, twice that where the scales are a factor of two apart
+    assert ((got - full).abs() <= 0.5 * torch.maximum(got.abs(), full.abs()) + 1e-30).float().mean().item() > 0.9999
+
+
 def test_other_stream_and_device_checks(sg):
     x = _rows(500, 512, BF16).cuda()
     w, b = (v.cuda() for v in _params(512))
