@@ -55,6 +55,7 @@ int fwd_by_shape(const FwdParams& p, cudaStream_t stream)
         return s.elems == 8 ? start_fwd<TX, TY, VEC, 8, 32, 256>(p, s, stream) : start_fwd<TX, TY, VEC, 16, 32, 256>(p, s, stream);
     if (s.elems == 8) return start_fwd<TX, TY, VEC, 8, 0, 256>(p, s, stream);
     if (s.elems == 16 && s.most == 256) return start_fwd<TX, TY, VEC, 16, 0, 256>(p, s, stream);
+    if (s.elems == 16 && s.most == 384) return start_fwd_as<TX, TY, VEC, 16, 0, 384, false>(p, s, stream);
     if (s.elems == 16) return start_fwd_as<TX, TY, VEC, 16, 0, 512, false>(p, s, stream);
     return start_fwd<TX, TY, VEC, 32, 0, 512>(p, s, stream);
 }
