@@ -21,6 +21,7 @@
 
 #include "ln_params.cuh"
 #include "ptx.cuh"
+#include "row_copy.h"
 
 namespace sgb {
 namespace ln {
@@ -50,16 +51,17 @@ struct Ring {
     int pitch;  // bytes between a thread's chunks: a chunk of every thread
     __device__ __forceinline__ Ring(uint8_t* base, int threads) : mine(base + threadIdx.x * CHUNK), pitch(threads * CHUNK) {}
     __device__ __forceinline__ uint8_t* at(int slot, int k, int j) const { return mine + ((slot * NV + k) * CHUNKS + j) * pitch; }
-    // Asks for the vectors at columns c0 + k*step of `row`; `cols` is 0 for no row.
-    __device__ __forceinline__ void ask(int slot, const T* row, int c0, int step, int cols) const
+    // Asks for the vectors at columns c0 + k*step of `row`, which begins `front` elements behind a whole vector's start; for no
+    // row, `cols` and `front` are 0 and `row` is any aligned address.
+    __device__ __forceinline__ void ask(int slot, const T* row, int c0, int step, int cols, int front) const
     {
 #pragma unroll
         for (int k = 0; k < NV; ++k)
 #pragma unroll
             for (int j = 0; j < CHUNKS; ++j) {
-                const int c = c0 + k * step + j * PER, left = cols - c;
-                const int bytes = cols == 0 || left <= 0 ? 0 : left < PER ? left * static_cast<int>(sizeof(T)) : CHUNK;
-                const T* src = bytes ? row + c : row;
+                const RowCopy copy = row_copy(c0 + k * step + j * PER, PER, cols, front);
+                const int bytes = copy.count * static_cast<int>(sizeof(T));
+                const T* src = row + copy.at;
                 if constexpr (CHUNK == 16)
                     ptx::cp_async_16(at(slot, k, j), src, bytes);
                 else
@@ -307,7 +309,8 @@ __global__ void __launch_bounds__(MOST, FWD_RESIDENT<G, E, MOST>) fwd_rows(const
     const Ring<TX, VEC == 1 ? 8 : VEC, VEC == 1 ? 1 : Un::NV, DEPTH> ring(ring_mem, blockDim.x);
     auto ask = [&](int slot, int64_t r) {
         if constexpr (VEC > 1) {
-            ring.ask(slot, x + (r < p.rows ? r * p.x_stride : 0), un.t * VEC - before, g * VEC, r < p.rows ? p.cols : 0);
+            const int front = r < p.rows ? before : 0;
+            ring.ask(slot, x + (r < p.rows ? r * p.x_stride : 0), un.t * VEC - front, g * VEC, r < p.rows ? p.cols : 0, front);
             ptx::cp_async_commit();
         }
     };
@@ -420,8 +423,9 @@ __global__ void __launch_bounds__(MOST, BWD_RESIDENT<G, E, MOST>) bwd_rows(const
     auto ask = [&](int slot, int64_t r) {
         if constexpr (VEC > 1) {
             const bool live = r < p.rows;
-            ring_x.ask(slot, x + (live ? r * p.x_stride : 0), un.t * VEC - un.off, group * VEC, live ? p.cols : 0);
-            ring_g.ask(slot, dy + (live ? r * p.dy_stride : 0), un.t * VEC - un.off, group * VEC, live ? p.cols : 0);
+            const int front = live ? un.off : 0;
+            ring_x.ask(slot, x + (live ? r * p.x_stride : 0), un.t * VEC - front, group * VEC, live ? p.cols : 0, front);
+            ring_g.ask(slot, dy + (live ? r * p.dy_stride : 0), un.t * VEC - front, group * VEC, live ? p.cols : 0, front);
             ptx::cp_async_commit();
         }
     };
