@@ -96,6 +96,16 @@ def same_device(t, name, like) -> None:
         raise ValueError(f"{name} must be a CUDA tensor on {like.device}")
 
 
+def check_workspace(t, like) -> Tuple[int, int]:
+    """(device pointer, bytes) of a workspace, a contiguous tensor of any type on the device of ``like``: what it spans is written."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError("workspace must be a torch.Tensor")
+    same_device(t, "workspace", like)
+    if not t.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
 def check_out_dtype(dtype) -> int:
     code = DTYPE_CODES.get(dtype)
     if code is None:

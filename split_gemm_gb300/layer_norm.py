@@ -14,7 +14,7 @@ import ctypes
 import torch
 
 from . import Conv2dError, LayerNormParams
-from ._rows import DTYPE_CODES, calls, check_out_dtype, check_vector, empty_on, library, rows_of, same_device, stream_handle
+from ._rows import DTYPE_CODES, calls, check_out_dtype, check_vector, check_workspace, empty_on, library, rows_of, same_device, stream_handle
 from .mxfp4 import Mxfp4, mxfp4_empty
 
 
@@ -76,7 +76,7 @@ def _bwd(dx, dw_ptr, db_ptr, dy, x, layout, mean, rstd, weight, workspace, strea
     lib = library()
     ws_ptr, ws_len = None, 0
     if workspace is not None:
-        ws_ptr, ws_len = workspace.data_ptr(), workspace.numel() * workspace.element_size()
+        ws_ptr, ws_len = check_workspace(workspace, x)
     elif dw_ptr or db_ptr:
         ws_len = lib.layer_norm_bwd_workspace_bytes(params)
         workspace = empty_on(stream, (ws_len,), torch.uint8, x.device)
@@ -90,7 +90,8 @@ def _bwd(dx, dw_ptr, db_ptr, dy, x, layout, mean, rstd, weight, workspace, strea
 
 def layer_norm_bwd_into(dx, dweight, dbias, dy, x, mean, rstd, weight=None, *, workspace=None, stream=None) -> None:
     """Writes the gradients for the output gradient ``dy`` (x's shape): ``dx`` (x's shape and type, dense) and the
-    fp32 ``dweight`` and ``dbias`` [C] (either may be None: not computed).  Asynchronous."""
+    fp32 ``dweight`` and ``dbias`` [C] (either may be None: not computed).  ``workspace``: contiguous, on x's device, of
+    layer_norm_bwd_workspace_bytes (None: taken from torch).  Asynchronous."""
     layout = rows_of(x, "x")
     if dx.shape != x.shape or dx.dtype != x.dtype or not dx.is_cuda or not dx.is_contiguous():
         raise ValueError(f"dx must be a contiguous CUDA tensor of {list(x.shape)}, {x.dtype}")
