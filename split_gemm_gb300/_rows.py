@@ -5,6 +5,7 @@ decided by few attribute reads and what is wrong is named only once something is
 """
 from __future__ import annotations
 
+import contextlib
 import importlib.util
 from typing import Optional, Tuple
 
@@ -13,6 +14,7 @@ import torch
 from . import OUT_BF16, OUT_F32, load_library
 
 DTYPE_CODES = {torch.float32: OUT_F32, torch.bfloat16: OUT_BF16}
+_HERE = contextlib.nullcontext()
 _lib = None
 _calls = None
 
@@ -113,9 +115,20 @@ def check_out_dtype(dtype) -> int:
     return code
 
 
+def on_device_of(t):
+    """A context in which the device of ``t`` is the current one: kernels start there, and the library's own device memory and
+    kernel attributes are that device's."""
+    index = t.get_device()
+    return _HERE if index == torch.cuda.current_device() else torch.cuda.device(index)
+
+
 def stream_handle(t, stream) -> int:
     """cudaStream_t of ``stream`` (None: the current stream of t's device)."""
-    return torch._C._cuda_getCurrentRawStream(t.get_device()) if stream is None else stream.cuda_stream
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
+    if stream.device_index != t.get_device():
+        raise ValueError(f"stream must belong to {t.device}, got one of cuda:{stream.device_index}")
+    return stream.cuda_stream
 
 
 def empty_on(stream, shape, dtype, device):

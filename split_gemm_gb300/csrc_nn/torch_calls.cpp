@@ -1,14 +1,15 @@
 // The row operators' calls on ordinary torch tensors, without Python between the arguments and the C ABI.
 //
 // A one-token call spends a few microseconds on the GPU; checking its arguments and allocating its results in Python took
-// 11 to 23 us on a Grace core.  These functions take the usual case (dense CUDA tensors of the expected types, results on
-// the current stream) and return None for everything else: the Python functions that call them then check
+// 11 to 23 us on a Grace core.  These functions take the usual case (dense tensors of the expected types on the current
+// device, results on its current stream) and return None for everything else: the Python functions that call them then check
 // one thing after another and raise what is wrong, or take the strided and streamed cases.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
 #include <ATen/ops/empty.h>
+#include <c10/cuda/CUDAFunctions.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
 #include <torch/csrc/Exceptions.h>
@@ -30,6 +31,9 @@ const at::Tensor* tensor(PyObject* o)
 // conv2d_out_dtype of a type, or -1.
 int code_of(at::ScalarType t) { return t == at::kFloat ? CONV2D_OUT_F32 : t == at::kBFloat16 ? CONV2D_OUT_BF16 : -1; }
 
+// Whether kernels that are started now can take the tensor: they start on the current device.
+bool here(const at::Tensor& t) { return t.is_cuda() && t.get_device() == c10::cuda::current_device(); }
+
 // A dense CUDA tensor of rows; rows, cols and its type's code are filled in.
 struct Rows {
     const at::Tensor* t = nullptr;
@@ -38,7 +42,7 @@ struct Rows {
     explicit Rows(PyObject* o)
     {
         const at::Tensor* x = tensor(o);
-        if (!x || !x->is_cuda() || x->dim() < 1 || !x->is_contiguous()) return;
+        if (!x || !here(*x) || x->dim() < 1 || !x->is_contiguous()) return;
         code = code_of(x->scalar_type());
         cols = x->size(-1);
         if (code < 0 || cols < 1) return;
@@ -72,7 +76,7 @@ struct Mx {
         rows = PyLong_AsLongLongAndOverflow(r, &over);
         if (over) return;
         cols = PyLong_AsLongLongAndOverflow(c, &over);
-        if (over || !d->is_cuda() || d->device() != s->device() || d->scalar_type() != at::kByte || s->scalar_type() != at::kByte ||
+        if (over || !here(*d) || d->device() != s->device() || d->scalar_type() != at::kByte || s->scalar_type() != at::kByte ||
             !d->is_contiguous() || !s->is_contiguous() || rows < 1 || cols < 1 ||
             static_cast<size_t>(d->numel()) != mxfp4_data_bytes(rows, cols) || static_cast<size_t>(s->numel()) != mxfp4_scale_bytes(rows, cols))
             return;

@@ -14,16 +14,17 @@ import ctypes
 import torch
 
 from . import Conv2dError, LayerNormParams
-from ._rows import DTYPE_CODES, calls, check_out_dtype, check_vector, check_workspace, empty_on, library, rows_of, same_device, stream_handle
+from ._rows import DTYPE_CODES, calls, check_out_dtype, check_vector, check_workspace, empty_on, library, on_device_of, rows_of, same_device, stream_handle
 from .mxfp4 import Mxfp4, mxfp4_empty
 
 
 def _fwd(y, x, layout, weight, bias, eps, mean_ptr, rstd_ptr, stream) -> None:
     rows, cols, x_stride, y_stride = layout
     params = LayerNormParams(rows, cols, x_stride, y_stride, DTYPE_CODES[x.dtype], DTYPE_CODES[y.dtype], eps)
-    rc = library().layer_norm_fwd(
-        ctypes.byref(params), x.data_ptr(), check_vector(weight, "weight", cols, x), check_vector(bias, "bias", cols, x),
-        y.data_ptr(), mean_ptr, rstd_ptr, stream_handle(x, stream))
+    with on_device_of(x):
+        rc = library().layer_norm_fwd(
+            ctypes.byref(params), x.data_ptr(), check_vector(weight, "weight", cols, x), check_vector(bias, "bias", cols, x),
+            y.data_ptr(), mean_ptr, rstd_ptr, stream_handle(x, stream))
     if rc:
         raise Conv2dError(rc, "layer_norm_fwd")
 
@@ -81,9 +82,10 @@ def _bwd(dx, dw_ptr, db_ptr, dy, x, layout, mean, rstd, weight, workspace, strea
         ws_len = lib.layer_norm_bwd_workspace_bytes(params)
         workspace = empty_on(stream, (ws_len,), torch.uint8, x.device)
         ws_ptr = workspace.data_ptr()
-    rc = lib.layer_norm_bwd(
-        params, dy.data_ptr(), x.data_ptr(), check_vector(mean, "mean", rows, x), check_vector(rstd, "rstd", rows, x),
-        check_vector(weight, "weight", cols, x), dx.data_ptr(), dw_ptr, db_ptr, ws_ptr, ws_len, stream_handle(x, stream))
+    with on_device_of(x):
+        rc = lib.layer_norm_bwd(
+            params, dy.data_ptr(), x.data_ptr(), check_vector(mean, "mean", rows, x), check_vector(rstd, "rstd", rows, x),
+            check_vector(weight, "weight", cols, x), dx.data_ptr(), dw_ptr, db_ptr, ws_ptr, ws_len, stream_handle(x, stream))
     if rc:
         raise Conv2dError(rc, "layer_norm_bwd")
 
@@ -122,10 +124,11 @@ def layer_norm_mxfp4(x, weight=None, bias=None, eps: float = 1e-5, *, mean=None,
     rows, cols, x_stride = rows_of(x, "x")
     params = LayerNormParams(rows, cols, x_stride, cols, DTYPE_CODES[x.dtype], 0, eps)
     q = mxfp4_empty(rows, cols, x.device, stream=stream)
-    rc = library().layer_norm_mxfp4(
-        ctypes.byref(params), x.data_ptr(), check_vector(weight, "weight", cols, x), check_vector(bias, "bias", cols, x),
-        q.data.data_ptr(), q.scales.data_ptr(), check_vector(mean, "mean", rows, x), check_vector(rstd, "rstd", rows, x),
-        stream_handle(x, stream))
+    with on_device_of(x):
+        rc = library().layer_norm_mxfp4(
+            ctypes.byref(params), x.data_ptr(), check_vector(weight, "weight", cols, x), check_vector(bias, "bias", cols, x),
+            q.data.data_ptr(), q.scales.data_ptr(), check_vector(mean, "mean", rows, x), check_vector(rstd, "rstd", rows, x),
+            stream_handle(x, stream))
     if rc:
         raise Conv2dError(rc, "layer_norm_mxfp4")
     return q

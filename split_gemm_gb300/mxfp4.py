@@ -19,7 +19,7 @@ from typing import NamedTuple, Tuple
 import torch
 
 from . import ACT_NONE, ACT_RELU, Conv2dError, Epilogue, Mxfp4MatmulParams
-from ._rows import DTYPE_CODES, calls, check_out_dtype, check_vector, empty_on, library, rows_of, same_device, stream_handle
+from ._rows import DTYPE_CODES, calls, check_out_dtype, check_vector, empty_on, library, on_device_of, rows_of, same_device, stream_handle
 
 
 class Mxfp4(NamedTuple):
@@ -66,7 +66,8 @@ def _quantize(x, layout, ptr, ptr_t, stream) -> None:
     rows, cols, x_stride = layout
     if rows == 0:
         return
-    rc = library().mxfp4_quantize(rows, cols, x.data_ptr(), DTYPE_CODES[x.dtype], x_stride, *ptr, *ptr_t, stream_handle(x, stream))
+    with on_device_of(x):
+        rc = library().mxfp4_quantize(rows, cols, x.data_ptr(), DTYPE_CODES[x.dtype], x_stride, *ptr, *ptr_t, stream_handle(x, stream))
     if rc:
         raise Conv2dError(rc, "mxfp4_quantize")
 
@@ -131,7 +132,8 @@ def mxfp4_dequantize(q: Mxfp4, *, out_dtype=torch.bfloat16, stream=None):
     y = empty_on(stream, (q.rows, q.cols), out_dtype, q.data.device)
     if q.rows == 0:
         return y
-    rc = library().mxfp4_dequantize(q.rows, q.cols, data, scales, y.data_ptr(), code, stream_handle(q.data, stream))
+    with on_device_of(q.data):
+        rc = library().mxfp4_dequantize(q.rows, q.cols, data, scales, y.data_ptr(), code, stream_handle(q.data, stream))
     if rc:
         raise Conv2dError(rc, "mxfp4_dequantize")
     return y
@@ -148,8 +150,9 @@ def _operands(a, b):
 def _matmul(y, ptrs, a, b, bias, relu, stream) -> None:
     epi = Epilogue(ACT_RELU if relu else ACT_NONE, DTYPE_CODES[y.dtype])
     params = Mxfp4MatmulParams(a.rows, b.rows, a.cols)
-    rc = library().mxfp4_matmul(ctypes.byref(params), *ptrs, check_vector(bias, "bias", b.rows, a.data), y.data_ptr(),
-                                ctypes.byref(epi), stream_handle(a.data, stream))
+    with on_device_of(a.data):
+        rc = library().mxfp4_matmul(ctypes.byref(params), *ptrs, check_vector(bias, "bias", b.rows, a.data), y.data_ptr(),
+                                    ctypes.byref(epi), stream_handle(a.data, stream))
     if rc:
         raise Conv2dError(rc, "mxfp4_matmul")
 
@@ -179,4 +182,5 @@ def mxfp4_matmul(a: Mxfp4, b: Mxfp4, bias=None, *, relu: bool = False, out_dtype
 def mxfp4_matmul_status(stream=None) -> int:
     """Synchronises the stream; 0, or CONV2D_ERR_TIMEOUT if a device-side wait of a product ran out since last asked."""
     st = torch.cuda.current_stream() if stream is None else stream
-    return int(library().mxfp4_matmul_status(st.cuda_stream))
+    with torch.cuda.device(st.device_index):
+        return int(library().mxfp4_matmul_status(st.cuda_stream))
