@@ -1,0 +1,51 @@
+"""Rows at the edges of the row operators' number range and shapes, against the 64-bit oracles."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import mxfp4 as mx_oracle
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def sg():
+    if not torch.cuda.is_available():
+        pytest.fail("GPU tests need a CUDA device")
+    import split_gemm_gb300
+    return split_gemm_gb300
+
+
+def _np(t):
+    return t.detach().cpu().double().numpy()
+
+
+def _rows(rows, cols, dtype, seed=0):
+    g = torch.Generator().manual_seed(seed + rows + cols)
+    return torch.randn(rows, cols, generator=g).to(dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("cols", [1, 40, 64, 200, 300, 520, 1000, 1001, 2500, 4097, 8200, 16383, 16500])
+def test_bad_rows_into_4_bits_leave_the_padding_zero(sg, cols, dtype):
+    """A row without a finite rstd is NaN in each of its blocks and nowhere else: scale bytes of blocks past the row's last and
+    elements past its end are zero as the format has them, and the other rows come out as they do without it."""
+    rows = 9
+    x = _rows(rows, cols, dtype)
+    clean = sg.layer_norm_mxfp4(x.cuda(), eps=0.0)
+    x[1, cols // 2], x[3, cols - 1], x[4, 0] = float("nan"), float("inf"), -float("inf")
+    x[6] = 0.5  # no spread: rstd is infinite for eps = 0
+    q = sg.layer_norm_mxfp4(x.cuda(), eps=0.0)
+    nb = mx_oracle.blocks_of(cols)
+    flat = q.scales.cpu().numpy()
+    scales = mx_oracle.untile_scales(flat, rows, cols)
+    assert np.array_equal(mx_oracle.tile_scales(scales), flat)
+    codes = mx_oracle.unpack(q.data.cpu().numpy())
+    assert codes.shape == (rows, 32 * nb) and not codes[:, cols:].any()
+    bad = [1, 3, 4, 6] if cols > 1 else list(range(rows))
+    assert (scales[bad] == 255).all()
+    good = [r for r in range(rows) if r not in bad]
+    assert torch.equal(q.data[good].cpu(), clean.data[good].cpu())
+    assert np.array_equal(scales[good], mx_oracle.untile_scales(clean.scales.cpu().numpy(), rows, cols)[good])
