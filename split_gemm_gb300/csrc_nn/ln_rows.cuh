@@ -476,10 +476,12 @@ __global__ void __launch_bounds__(MOST, BWD_RESIDENT<G, E, MOST>) bwd_rows(const
         }
         un.cut(xh);
         un.cut(g);
+        // Outside the row dy is zero, but a normalised zero may be past fp32 where the row's values are not: there the mean takes its place.
+        if (__any_sync(0xffffffffu, !(fabsf(minus.x * scale.x) <= FLT_MAX))) un.fill(xh, -minus.x);
 #pragma unroll
         for (int u = 0; u < U; ++u) {
 #pragma unroll
-            for (int i = 0; i < H; ++i) {  // outside the row dy is zero and the normalised value finite where mean and rstd are
+            for (int i = 0; i < H; ++i) {
                 xh[u][i] = mul2(add2(xh[u][i], minus), scale);
                 if constexpr (SUMS) {
                     dw[u][i] = fma2(g[u][i], xh[u][i], dw[u][i]);
