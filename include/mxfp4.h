@@ -67,7 +67,10 @@ int mxfp4_matmul(const mxfp4_matmul_params* params, const void* a_data_dev, cons
 
 /* Synchronises `stream` and returns CONV2D_OK, or CONV2D_ERR_TIMEOUT if a
  * device-side wait (each is bounded, by seconds) ran out in any mxfp4_matmul on
- * the current device since the last time this was asked; that call's y is undefined then. */
+ * the current device since the last time this was asked; that call's y is undefined then.
+ * The device has one such word for all streams and threads: each report is told
+ * once, to whoever asks first, so a program asks in one place and holds all of
+ * its products since the last answer for undefined.  Threads may ask at the same time. */
 int mxfp4_matmul_status(conv2d_stream_t stream);
 
 #ifdef __cplusplus

@@ -39,8 +39,13 @@ bool encode(CUtensorMap* map, const void* data, int64_t rows, int64_t blocks, in
                         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Device status word of this library's product kernels; read and cleared by mxfp4_matmul_status.
-__device__ uint32_t product_status;
+// Device status word of this library's product kernels, and what mxfp4_matmul_status last took out of it: read and cleared in
+// one step, so that no report falls between the two.
+__device__ uint32_t product_status, taken_status;
+
+__global__ void take_status() { taken_status = atomicExch(&product_status, 0u); }
+
+std::mutex asking;  // taken_status is one question's at a time
 
 struct Operand {
     const void* data;
@@ -212,10 +217,10 @@ extern "C" int mxfp4_matmul(const mxfp4_matmul_params* params, const void* a_dat
 extern "C" int mxfp4_matmul_status(conv2d_stream_t stream)
 {
     uint32_t word = 0;
+    std::lock_guard<std::mutex> one(mx::asking);
+    mx::take_status<<<1, 1, 0, stream>>>();
+    if (cudaGetLastError() != cudaSuccess) return CONV2D_ERR_CUDA;
+    if (cudaMemcpyFromSymbolAsync(&word, mx::taken_status, sizeof word, 0, cudaMemcpyDeviceToHost, stream) != cudaSuccess) return CONV2D_ERR_CUDA;
     if (cudaStreamSynchronize(stream) != cudaSuccess) return CONV2D_ERR_CUDA;
-    if (cudaMemcpyFromSymbol(&word, mx::product_status, sizeof word) != cudaSuccess) return CONV2D_ERR_CUDA;
-    if (word == 0) return CONV2D_OK;
-    word = 0;
-    if (cudaMemcpyToSymbol(mx::product_status, &word, sizeof word) != cudaSuccess) return CONV2D_ERR_CUDA;
-    return CONV2D_ERR_TIMEOUT;
+    return word == 0 ? CONV2D_OK : CONV2D_ERR_TIMEOUT;
 }

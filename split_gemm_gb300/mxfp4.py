@@ -180,7 +180,8 @@ def mxfp4_matmul(a: Mxfp4, b: Mxfp4, bias=None, *, relu: bool = False, out_dtype
 
 
 def mxfp4_matmul_status(stream=None) -> int:
-    """Synchronises the stream; 0, or CONV2D_ERR_TIMEOUT if a device-side wait of a product ran out since last asked."""
+    """Synchronises the stream; 0, or CONV2D_ERR_TIMEOUT if a device-side wait of a product, of any stream of its device, ran out
+    since last asked (each report is told once, to whoever asks first)."""
     st = torch.cuda.current_stream() if stream is None else stream
     with torch.cuda.device(st.device_index):
         return int(library().mxfp4_matmul_status(st.cuda_stream))
