@@ -21,6 +21,7 @@ Between convolutions: ``layer_norm_fwd`` / ``layer_norm_bwd`` over the channels
 from __future__ import annotations
 
 import ctypes
+import importlib
 import os
 import threading
 from typing import Optional, Tuple
@@ -506,7 +507,24 @@ def status(workspace, stream=None) -> int:
                                                 workspace.numel() * workspace.element_size(), st.cuda_stream))
 
 
-from .mxfp4 import (Mxfp4, mxfp4_dequantize, mxfp4_empty, mxfp4_matmul, mxfp4_matmul_into, mxfp4_matmul_status,  # noqa: E402
-                    mxfp4_quantize, mxfp4_quantize_both, mxfp4_quantize_into)
-from .layer_norm import (layer_norm_bwd, layer_norm_bwd_into, layer_norm_bwd_workspace_bytes,  # noqa: E402
-                         layer_norm_fwd, layer_norm_fwd_into, layer_norm_mxfp4)
+# The row operators work on torch tensors and import torch with their modules; the package itself does not need it.
+_ROW_OPERATORS = {
+    "layer_norm": ("layer_norm_bwd", "layer_norm_bwd_into", "layer_norm_bwd_workspace_bytes", "layer_norm_fwd", "layer_norm_fwd_into",
+                   "layer_norm_mxfp4"),
+    "mxfp4": ("Mxfp4", "mxfp4_dequantize", "mxfp4_empty", "mxfp4_matmul", "mxfp4_matmul_into", "mxfp4_matmul_status", "mxfp4_quantize",
+              "mxfp4_quantize_both", "mxfp4_quantize_into"),
+}
+_MODULE_OF = {name: module for module, names in _ROW_OPERATORS.items() for name in (module, *names)}
+
+
+def __getattr__(name):
+    if name not in _MODULE_OF:
+        raise AttributeError(f"module {__name__!r} has no attribute {name!r}")
+    module = importlib.import_module("." + _MODULE_OF[name], __name__)
+    for each in _ROW_OPERATORS[_MODULE_OF[name]]:  # found at once from now on
+        globals()[each] = getattr(module, each)
+    return module if name == _MODULE_OF[name] else globals()[name]
+
+
+def __dir__():
+    return sorted({*globals(), *_MODULE_OF})
