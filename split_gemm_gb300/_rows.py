@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import contextlib
 import importlib.util
+import os
 from typing import Optional, Tuple
 
 import torch
@@ -19,6 +20,16 @@ _lib = None
 _calls = None
 
 
+class _NoCalls:
+    """In the place of the compiled calls where they cannot be built: none takes any case."""
+
+    @staticmethod
+    def _none(*args):
+        return None
+
+    layer_norm_fwd = layer_norm_bwd = layer_norm_mxfp4 = quantize = dequantize = matmul = _none
+
+
 def calls():
     """The compiled calls (csrc_nn/torch_calls.cpp): they take the usual case and return None for any other."""
     global _calls
@@ -26,6 +37,9 @@ def calls():
         library()  # builds what is stale
         from . import _build
         from .mxfp4 import Mxfp4
+        if not os.path.exists(_build.CALLS_PATH):
+            _calls = _NoCalls
+            return _calls
         spec = importlib.util.spec_from_file_location("split_gemm_gb300._calls", _build.CALLS_PATH)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
