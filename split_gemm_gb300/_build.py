@@ -11,6 +11,7 @@ from __future__ import annotations
 import concurrent.futures as cf
 import importlib.util
 import os
+import re
 import shutil
 import subprocess
 import sys
@@ -27,7 +28,7 @@ LIB_PATH = os.path.join(LIB_DIR, "libconv2d.so")
 CALLS_PATH = os.path.join(LIB_DIR, "_calls.so")  # the row operators' calls on torch tensors (needs torch's headers)
 CALLS_SOURCE = os.path.join(CSRC_NN, "torch_calls.cpp")
 OBJ_DIR = os.path.join(PKG, "_build")
-CALLS_NOTE = os.path.join(OBJ_DIR, "calls.txt")  # "built", "lacks: " what, or "failed: " why; written last
+CALLS_NOTE = os.path.join(OBJ_DIR, "calls.txt")  # calls_for(), then "built", "lacks: " what, or "failed: " why; written last
 
 SOURCES = ["conv2d_api.cu", "conv2d_bn64.cu", "conv2d_bn128.cu", "conv2d_bn256.cu", "conv2d_rowwin.cu", "conv2d_direct.cu",
            "conv2d_noalloc.cu", "conv2d_pair_kb1.cu", "conv2d_pair_kb2.cu"]
@@ -60,12 +61,25 @@ def library_up_to_date() -> bool:
     return _newer(LIB_PATH, _deps())
 
 
+def calls_for() -> str:
+    """What the compiled calls are bound to beside their sources: torch's C++ interface and Python's, of one version each."""
+    torch_dir = _torch_folder()
+    version = os.path.join(torch_dir, "version.py") if torch_dir else ""  # with the local part, which an installer's records may lack
+    torch = ""
+    if os.path.exists(version):
+        with open(version) as f:
+            torch = ", ".join(re.findall(r"'([^']+)'", f.read()))
+    return f"torch {torch} in {torch_dir}; Python {sysconfig.get_config_var('SOABI')}"
+
+
 def calls_up_to_date() -> bool:
-    """The compiled calls are those of the sources, or cannot be built here."""
+    """The compiled calls are those of the sources and of this torch and Python, or cannot be built here."""
     if not _newer(CALLS_NOTE, _deps() + [CALLS_SOURCE, LIB_PATH]):
         return False
     with open(CALLS_NOTE) as f:
-        note = f.read()
+        built_for, _, note = f.read().partition("\n")
+    if built_for != calls_for():
+        return False
     return os.path.exists(CALLS_PATH) if note == "built" else note.startswith("failed: ") or note == f"lacks: {_calls_missing()}"
 
 
@@ -159,7 +173,7 @@ def _build_calls(compiled: "cf.Future[str]") -> None:
             os.remove(CALLS_PATH)
     tmp = CALLS_NOTE + f".tmp{os.getpid()}"
     with open(tmp, "w") as f:
-        f.write(note)
+        f.write(f"{calls_for()}\n{note}")
     os.replace(tmp, CALLS_NOTE)
 
 

@@ -65,6 +65,24 @@ def test_torch_that_comes_later(sandbox, monkeypatch):
     assert sandbox == ["g++ for torch_calls.cpp", "linking _calls.so"] and _build.up_to_date()
 
 
+def test_another_torch_has_the_calls_rebuilt(sandbox, monkeypatch, tmp_path):
+    other = tmp_path / "torch"
+    (other / "include" / "ATen" / "core").mkdir(parents=True)
+    (other / "include" / "ATen" / "core" / "Tensor.h").write_text("")
+    (other / "version.py").write_text("__version__ = '99.0+cu130'\n")
+    _build.build()
+    assert _build.up_to_date()
+    monkeypatch.setattr(_build, "_torch_folder", lambda: str(other))
+    assert not _build.up_to_date()
+    _build.build()
+    assert _build.up_to_date()
+    (other / "version.py").write_text("__version__ = '99.0+cu131'\n")
+    assert _build.library_up_to_date() and not _build.up_to_date()
+    del sandbox[:]
+    _build.build()
+    assert sandbox == ["g++ for torch_calls.cpp", "linking _calls.so"] and _build.up_to_date()
+
+
 def test_headers_that_do_not_compile_leave_the_library(sandbox, monkeypatch, capsys):
     def fails():
         raise RuntimeError("no such member")
