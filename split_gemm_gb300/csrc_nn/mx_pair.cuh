@@ -46,7 +46,7 @@ struct PairParams {
     uint32_t* status;
     int64_t ldy;
     int m, n;
-    int blocks, stages;
+    int stages;
     int m_tiles, n_tiles;
     int relu, tma_store;
 };

@@ -134,13 +134,6 @@ __device__ __forceinline__ uint32_t relu_nan(uint32_t v)
     return __float_as_uint(d);
 }
 
-__device__ __forceinline__ float ld_cluster_f32(uint32_t cluster_addr)
-{
-    float v;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(cluster_addr) : "memory");
-    return v;
-}
-
 __device__ __forceinline__ float4 ld_cluster_v4(uint32_t cluster_addr)
 {
     float4 v;

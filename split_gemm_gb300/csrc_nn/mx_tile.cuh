@@ -76,7 +76,7 @@ struct TileConfig {
     static constexpr int SMEM = RING + 1024 + 256;                // + alignment, barriers
 };
 
-// The sum of four values, or of one, over the S CTAs of the cluster, in their order; the loads are on their way together.
+// The sum of four values over the S CTAs of the cluster, in their order; the loads are on their way together.
 template <int S>
 __device__ __forceinline__ float4 joined4(const float* at)
 {
@@ -93,20 +93,6 @@ __device__ __forceinline__ float4 joined4(const float* at)
             v[0].z += v[k].z;
             v[0].w += v[k].w;
         }
-        return v[0];
-    }
-}
-template <int S>
-__device__ __forceinline__ float joined1(const float* at)
-{
-    if constexpr (S == 1) {
-        return *at;
-    } else {
-        float v[S];
-#pragma unroll
-        for (int k = 0; k < S; ++k) v[k] = ptx::ld_cluster_f32(ptx::mapa_shared(ptx::smem_addr(at), k));
-#pragma unroll
-        for (int k = 1; k < S; ++k) v[0] += v[k];
         return v[0];
     }
 }

@@ -11,7 +11,6 @@
 namespace sgb {
 namespace mx {
 
-
 std::once_flag encode_once;
 PFN_cuTensorMapEncodeTiled_v12000 encode_tiled = nullptr;
 
@@ -124,7 +123,6 @@ int launch_pair(const Operand& a, const Operand& b, const TileParams& k, cudaStr
     p.ldy = k.ldy;
     p.m = static_cast<int>(a.rows);
     p.n = static_cast<int>(b.rows);
-    p.blocks = k.blocks;
     p.stages = k.stages;
     p.m_tiles = cdiv(p.m, W_TILE);
     p.n_tiles = cdiv(p.n, W_TILE);
