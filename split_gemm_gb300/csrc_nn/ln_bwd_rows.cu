@@ -10,7 +10,7 @@ int start_bwd_as(const BwdParams& p, RowShape s, int grid, cudaStream_t stream)
 {
     static std::atomic<uint64_t> done{0};
     constexpr int DEPTH = ring_depth(RowShape{G ? G : MOST, E, MOST}, sizeof(TX), sizeof(TY)), V = VEC == 1 ? 8 : VEC;
-    constexpr int ring = VEC > 1 ? Ring<TX, V, E / V, DEPTH>::THREAD_BYTES + Ring<TY, V, E / V, DEPTH>::THREAD_BYTES : 0;
+    constexpr int ring = VEC > 1 ? Ring<TX, V, E / V, DEPTH, WHOLE>::THREAD_BYTES + Ring<TY, V, E / V, DEPTH, WHOLE>::THREAD_BYTES : 0;
     constexpr int join = G ? 2 * E * 4 : 0;  // a block's sums by row and column
     constexpr int per_thread = ring > join ? ring : join;
     const auto kernel = bwd_rows<TX, TY, VEC, E, G, MOST, SUMS, WHOLE>;

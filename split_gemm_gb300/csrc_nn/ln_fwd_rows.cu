@@ -10,7 +10,7 @@ int start_fwd_as(const FwdParams& p, RowShape s, cudaStream_t stream)
 {
     static std::atomic<uint64_t> done{0};
     constexpr int V = VEC == 1 ? 8 : VEC;
-    constexpr int per_thread = VEC > 1 ? Ring<TX, V, E / V, ring_depth(RowShape{G ? G : MOST, E, MOST}, sizeof(TX), 0)>::THREAD_BYTES : 0;
+    constexpr int per_thread = VEC > 1 ? Ring<TX, V, E / V, ring_depth(RowShape{G ? G : MOST, E, MOST}, sizeof(TX), 0), WHOLE>::THREAD_BYTES : 0;
     const auto kernel = fwd_rows<TX, TY, VEC, E, G, MOST, WHOLE>;
     if (!mx::allow_smem(kernel, per_thread * MOST, done)) return CONV2D_ERR_CUDA;
     const int64_t grid = row_blocks(std::is_same_v<TY, void> ? p.padded_rows : p.rows, s, fwd_resident(s));

@@ -34,7 +34,7 @@ int main()
                             for (int u = 0; u < elems / k.vec; ++u)
                                 for (int j = 0; j < k.vec / k.per; ++j) {
                                     const int c = t * k.vec - front + u * group * k.vec + j * k.per;
-                                    const sgb::ln::RowCopy copy = sgb::ln::row_copy(c, k.per, live ? cols : 0, front);
+                                    const sgb::ln::RowCopy copy = sgb::ln::row_copy(c, k.per, live ? cols : 0, front, whole);
                                     const int64_t at = row + copy.at;
                                     want(at % k.per == 0, "unaligned", cols, stride, r, c);
                                     want(copy.count >= 0 && copy.count <= k.per, "count", cols, stride, r, c);
