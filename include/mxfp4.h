@@ -46,8 +46,10 @@ int mxfp4_quantize(int64_t rows, int64_t cols, const void* x_dev, int32_t x_dtyp
                    void* data_dev, void* scales_dev, void* data_t_dev, void* scales_t_dev,
                    conv2d_stream_t stream);
 
-/* y [rows][cols], dense, of y_dtype: the values that data and scales stand for
- * (exact in fp32; exact in bf16). */
+/* y [rows][cols], dense, of y_dtype: the values that data and scales stand for,
+ * exact in fp32 and in bf16.  The quantiser's scale bytes are at most 252 (or
+ * 255, NaN); with 253 and 254 from elsewhere the largest elements are past
+ * either type and read as infinities. */
 int mxfp4_dequantize(int64_t rows, int64_t cols, const void* data_dev, const void* scales_dev, void* y_dev,
                      int32_t y_dtype, conv2d_stream_t stream);
 

@@ -72,11 +72,11 @@ int64_t span_of(const layer_norm_params* p, int64_t most)
     return whole_rows(p) || (p->cols <= most && p->cols + 7 > most) ? p->cols : p->cols + 7;
 }
 
-// 16384 columns: else the kernels for any width (8192 x 16383: fp32 forward 245 us against 379, backward 437 against 655; but
-// bf16 forward 327 against 212, backward 456 against 442; bf16, 64 rows: 6.6 against 16.7 and 14.4 against 22.4).
+// 16384 columns: else the kernels for any width (8192 x 16383: fp32 forward 244 us against 405, backward 476 against 778; but
+// bf16 forward 317 against 209, though backward 454 against 501; bf16, 64 rows: 6.2 against 16.4 and 13.8 against 22.0).
 int64_t most_columns(const layer_norm_params* p) { return p->x_dtype == CONV2D_OUT_F32 || p->rows <= SMS ? 16384 : 0; }
 int64_t fwd_span(const layer_norm_params* p) { return span_of(p, most_columns(p)); }
-// 8192 columns: else the sums take a kernel of their own (16384 x 8191: bf16 284 us against 354, fp32 337 against 588).
+// 8192 columns: else the sums take a kernel of their own (16384 x 8191: bf16 303 us against 386, fp32 322 against 640).
 int64_t bwd_span(const layer_norm_params* p) { return span_of(p, p->cols <= 8192 ? 8192 : most_columns(p)); }
 
 // Whether the kernels that hold rows read them in vectors, `vec` telling of their alignment to each other.

@@ -57,8 +57,8 @@ __host__ __device__ constexpr RowShape group_shape(int n, bool many)
 
 // Forward: a warp to a row of up to 1024 columns where there are many rows and those nearly fill it, else blocks of 8, 16 or 32
 // elements to a thread.  `whole`: rows are whole vectors (others need registers for masks; of 4097 to 6144
-// columns two blocks of at most 384 threads stay on an SM instead of one: 16380 x 4097, forward bf16 66 us against 97, fp32 87 against
-// 113, quantised bf16 94 against 125).
+// columns two blocks of at most 384 threads stay on an SM instead of one: 16380 x 4097, forward bf16 65 us against 97, fp32 89 against
+// 113, quantised bf16 95 against 125).
 __host__ __device__ constexpr RowShape fwd_shape(int64_t rows, int64_t cols, int x_bytes, bool whole)
 {
     if (cols > 16384) return RowShape{0, 0, 0};

@@ -13,8 +13,11 @@
 // stand in front of the first one, and are left out.  A group's rows lie a multiple of VEC rows apart, so `off`, and with it a thread's
 // columns, is the same in all of them.  A row's end is cut off by the copy itself.
 //
-// All of them are bound by HBM: per element the forward pass moves sizeof(x) + sizeof(y) bytes for about 8 operations.
-// Measured, 32768 x 4096 bf16: forward 90 us, 6.0 TB/s; backward 140 us, 5.7 TB/s.
+// Rows of whole vectors are bound by HBM, forward and (up to 8192 columns) backward: per element the forward pass moves
+// sizeof(x) + sizeof(y) bytes for about 8 operations.  32768 x 4096 bf16: forward 90 us, 6.0 TB/s; backward 141 us, 5.7 TB/s.  Others are not:
+// unaligned rows wait for their barriers and edges (16384 x 8191 bf16 142 us forward, 3.8 TB/s), and the quantised norm, which
+// writes a quarter of the bytes, takes longer than the norm (16384 x 4096 bf16 53 us, 3.2 TB/s, against 44): for the instructions
+// after the norm or for its scale bytes, each stored alone into sectors that rows of other blocks share; which was not told apart.
 #pragma once
 
 #include <cfloat>

@@ -15,7 +15,7 @@
 // Warps: 0 copies (one thread), 1 MMAs (one thread of the leader), 2..9 accumulator to y.  y goes out by TMA
 // stores of 32-row boxes, or element by element where its rows are not a multiple of 16 bytes.
 //
-// Measured: 8192 x 8192 x 8192 to bf16 162 us, 6.8 PFLOP/s; 1024 x 4096 x 4096 10.7 us.  Of the 8192 cube the MMAs alone are
+// Measured: 8192 x 8192 x 8192 to bf16 163 us, 6.8 PFLOP/s; 1024 x 4096 x 4096 11 us.  Of the 8192 cube the MMAs alone are
 // 119 us; without loads it would take 135, without stores 155, so most of the rest is the operands' way from L2.  Five stages, as four
 // cost 181 us and three 215.
 #pragma once
@@ -244,7 +244,8 @@ __global__ void __launch_bounds__(W_THREADS, 1)
                     __syncwarp();
                     // Rows of y that begin anywhere.  fp32: the warp stores a row of the box at a time, a word to a lane.  bf16, where
                     // that would be half words: eight lanes to a row, 16-byte stores from the first aligned place on, the rest one by
-                    // one.  (13567 x 10797 x 128: fp32 249 us, the other way 275; bf16 177, the other way 213.)
+                    // one.  (13567 x 10797 x 128: fp32 249 us, the other way 275; bf16 177, the other way 213; in a graph
+                    // 234 and 155, with 10800 columns, which go by boxes, 103 and 75.)
                     T* y = static_cast<T*>(p.y);
                     const int c0 = col0 + b * COLS, left_c = p.n - c0, valid = left_c < COLS ? left_c : COLS;
                     if constexpr (sizeof(T) == 4) {

@@ -23,9 +23,11 @@
 // six write the result.  Every wait is bounded: on running out the status word is set and
 // the CTA goes through its remaining barriers without waiting or storing.
 //
-// Measured: one token, 1 x 16384 x 4096 to bf16, 8.1 us, 4.4 TB/s of weight (the MMAs of a stage take 0.18 us however few
-// rows there are, which nears the weight's time from HBM); 1024 x 256 x 12544 to fp32, 9.4 us, bound by what an SM
-// takes from L2 and by start and join.
+// Measured: one token, 1 x 16384 x 4096 to bf16, 8.0 us, 4.5 TB/s of weight; 1 x 65536 x 8192, 54 us, 5.3 TB/s.  The MMAs do not
+// bind there: a stage's take 0.18 us however few rows there are, but an SM has 16 to 32 stages to a tile, 3 us of those 8, and in the
+// second case the tensor pipe is at 4%.  What does was not measured; a CTA takes one tile and fills an SM, so that each tile pays for its
+// barriers, an empty ring and a drain with nothing beside it, and 128 tiles leave 24 SMs idle.  1024 x 256 x 12544 to fp32, 9.5 us, bound by what
+// an SM takes from L2 and by start and join.
 #pragma once
 
 #include <cuda.h>

@@ -22,7 +22,7 @@ struct QuantParams {
 // a block's 32), or 32 elements of one column (two columns where x is bf16, which come as one word); what it makes is
 // gathered in shared memory and leaves in whole rows: 64 bytes of data, 512 bytes of scales.  x is read once and 17/32 of a byte
 // written for each element of each form; bound by issue, some 17 instructions an element for both forms (16384 x 4096 bf16: rows
-// 37 us, columns 34, both 50, 4.1 TB/s).
+// 38 us, columns 34, both 50, 4.1 TB/s; fp32: rows 67, columns 61, both 79, 4.3 TB/s).
 constexpr int Q_TILE = 128;
 constexpr int Q_THREADS = 256;
 
@@ -175,6 +175,8 @@ __global__ void __launch_bounds__(Q_THREADS) quantize_kernel(const T* __restrict
 // A thread takes 8 elements: 4 bytes in, 16 or 32 out (in one or two 16-byte stores where rows are whole vectors; else a
 // warp's 256 elements go through shared memory and leave element by element in order).
 // Bound by HBM once four rows' loads are in flight: 16384 x 4096 to bf16 31 us, 5.5 TB/s (one row at a time 34), to fp32 51 us, 6.0 TB/s (57).
+// Other widths are bound by their way through shared memory: 16384 x 4093 79 us to bf16 and 78 to fp32; 4097 columns, whose third block
+// of 256 threads across has 4 at work, 123 and 121.
 constexpr int D_THREADS = 256;
 
 template <typename T, bool VEC>

@@ -124,7 +124,7 @@ def mxfp4_quantize_both(x, *, stream=None) -> Tuple[Mxfp4, Mxfp4]:
 
 
 def mxfp4_dequantize(q: Mxfp4, *, out_dtype=torch.bfloat16, stream=None):
-    """The values that q stands for, [rows, cols] bf16 or fp32 (exact in either)."""
+    """The values that q stands for, [rows, cols] bf16 or fp32 (exact in either, but infinite past it: ``include/mxfp4.h``)."""
     if stream is None and (made := calls().dequantize(q, out_dtype)) is not None:
         return made
     data, scales = _check_mx(q, "q")
