@@ -8,7 +8,7 @@ The operators, as a user reaches them in ``split_gemm_gb300``:
                    each adapter; x in 16 bits or as an 8-bit checkpoint
   mxint8_quantize  8-bit integers in blocks of 32 with a shared power-of-two scale (MXINT8 of the OCP Microscaling
                    Formats specification), and mxint8_dequantize
-  layer_norm_bwd_mxint8   the norm's gradient with x as such a checkpoint
+  mxint8_layer_norm_bwd  the norm's gradient with x as such a checkpoint
 
 ``run`` computes them in elementary torch operations where ``own`` is false and through the package where it is
 true.  A checkpoint of [rows, cols] is ``data`` int8 [rows, 32*ceil(cols/32)], zero past cols, and ``scales`` uint8
@@ -254,7 +254,7 @@ def _own(s):
     if op == "checkpoint":
         return {"x": sg.mxint8_dequantize(sg.mxint8_quantize(s["x"]), out_dtype=s["x"].dtype)}
     if op == "norm_grad":
-        dx, dw, db = sg.layer_norm_bwd_mxint8(s["dy"], sg.Mxint8(**s["x"]), s["mean"], s["rstd"], s["weight"])
+        dx, dw, db = sg.mxint8_layer_norm_bwd(s["dy"], sg.Mxint8(**s["x"]), s["mean"], s["rstd"], s["weight"])
         return {"dx": dx, "dweight": dw, "dbias": db}
     plan = s["plan"] if "plan" in s else sg.adapter_plan(s["index"], case["adapters"])
     if op == "adapter":
