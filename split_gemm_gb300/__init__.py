@@ -17,6 +17,9 @@ Between convolutions: ``layer_norm_fwd`` / ``layer_norm_bwd`` over the channels
 (``layer_norm.py``), and 4-bit microscaled matrices (``mxfp4.py``):
 ``mxfp4_quantize``, ``mxfp4_quantize_both``, ``mxfp4_dequantize``,
 ``mxfp4_matmul`` (a pointwise convolution of NHWC rows) and ``layer_norm_mxfp4``.
+Beside them: low-rank adapters of many requests (``adapter.py``: ``adapter_plan``,
+``adapter_fwd``, ``adapter_bwd``) and activation checkpoints in 8 bits (``mxint8.py``:
+``mxint8_quantize``, ``mxint8_dequantize``, ``mxint8_layer_norm_bwd``).
 """
 from __future__ import annotations
 
@@ -40,6 +43,10 @@ __all__ = [
     "layer_norm_fwd", "layer_norm_fwd_into", "layer_norm_bwd", "layer_norm_bwd_into", "layer_norm_mxfp4",
     "layer_norm_bwd_workspace_bytes", "LayerNormParams", "Mxfp4", "mxfp4_empty", "mxfp4_quantize", "mxfp4_quantize_both", "mxfp4_quantize_into",
     "mxfp4_dequantize", "mxfp4_matmul", "mxfp4_matmul_into", "mxfp4_matmul_status", "Mxfp4MatmulParams",
+    "Mxint8", "mxint8_empty", "mxint8_quantize", "mxint8_quantize_into", "mxint8_dequantize", "mxint8_layer_norm_bwd",
+    "mxint8_layer_norm_bwd_into", "mxint8_layer_norm_bwd_workspace_bytes",
+    "AdapterPlan", "adapter_plan", "adapter_fwd", "adapter_fwd_into", "adapter_bwd", "adapter_bwd_into", "adapter_bwd_workspace_bytes",
+    "adapter_status", "AdapterFwdParams", "AdapterBwdParams",
 ]
 
 LOADER_AUTO, LOADER_TMA_IM2COL, LOADER_CPASYNC, LOADER_SCALAR, LOADER_HYBRID, LOADER_ROW_WINDOW = 0, 1, 2, 3, 4, 5
@@ -68,6 +75,9 @@ EXPORTED_SYMBOLS = [
     "conv2d_bwd_data_query_algo",
     "layer_norm_fwd", "layer_norm_bwd_workspace_bytes", "layer_norm_bwd", "layer_norm_mxfp4",
     "mxfp4_data_bytes", "mxfp4_scale_bytes", "mxfp4_quantize", "mxfp4_dequantize", "mxfp4_matmul", "mxfp4_matmul_status",
+    "mxint8_data_bytes", "mxint8_scale_bytes", "mxint8_quantize", "mxint8_dequantize", "mxint8_layer_norm_bwd_workspace_bytes",
+    "mxint8_layer_norm_bwd",
+    "adapter_plan_bytes", "adapter_plan", "adapter_fwd", "adapter_bwd_workspace_bytes", "adapter_bwd", "adapter_status",
 ]
 
 
@@ -107,6 +117,18 @@ class LayerNormParams(ctypes.Structure):
 
 class Mxfp4MatmulParams(ctypes.Structure):
     _fields_ = [("m", ctypes.c_int64), ("n", ctypes.c_int64), ("k", ctypes.c_int64)]
+
+
+class AdapterFwdParams(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("outs", ctypes.c_int64), ("rank", ctypes.c_int64),
+                ("adapters", ctypes.c_int64), ("x_stride", ctypes.c_int64), ("y_stride", ctypes.c_int64), ("out_stride", ctypes.c_int64),
+                ("y_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32), ("activation", ctypes.c_int32)]
+
+
+class AdapterBwdParams(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("cols", ctypes.c_int64), ("outs", ctypes.c_int64), ("rank", ctypes.c_int64),
+                ("adapters", ctypes.c_int64), ("dy_stride", ctypes.c_int64), ("x_stride", ctypes.c_int64), ("dx0_stride", ctypes.c_int64),
+                ("dx_stride", ctypes.c_int64), ("x_type", ctypes.c_int32), ("dx0_dtype", ctypes.c_int32), ("dx_dtype", ctypes.c_int32)]
 
 
 _lock = threading.Lock()
@@ -178,6 +200,21 @@ def _bind(lib):
     lib.mxfp4_dequantize.argtypes = [i64, i64, vp, vp, vp, i32, vp]
     lib.mxfp4_matmul.argtypes = [ctypes.POINTER(Mxfp4MatmulParams), vp, vp, vp, vp, vp, vp, ctypes.POINTER(Epilogue), vp]
     lib.mxfp4_matmul_status.argtypes = [vp]
+    lib.mxint8_data_bytes.argtypes = lib.mxint8_scale_bytes.argtypes = [i64, i64]
+    lib.mxint8_data_bytes.restype = lib.mxint8_scale_bytes.restype = sz
+    lib.mxint8_quantize.argtypes = [i64, i64, vp, i32, i64, vp, vp, vp]
+    lib.mxint8_dequantize.argtypes = [i64, i64, vp, vp, vp, i32, vp]
+    lib.mxint8_layer_norm_bwd_workspace_bytes.argtypes = [L]
+    lib.mxint8_layer_norm_bwd_workspace_bytes.restype = sz
+    lib.mxint8_layer_norm_bwd.argtypes = [L, vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    lib.adapter_plan_bytes.argtypes = [i64, i64]
+    lib.adapter_plan_bytes.restype = sz
+    lib.adapter_plan.argtypes = [i64, i64, vp, vp, vp]
+    lib.adapter_fwd.argtypes = [ctypes.POINTER(AdapterFwdParams), vp, vp, vp, vp, vp, vp, vp, vp, vp]
+    lib.adapter_bwd_workspace_bytes.argtypes = [ctypes.POINTER(AdapterBwdParams)]
+    lib.adapter_bwd_workspace_bytes.restype = sz
+    lib.adapter_bwd.argtypes = [ctypes.POINTER(AdapterBwdParams)] + [vp] * 13 + [sz, vp]
+    lib.adapter_status.argtypes = [vp]
     return lib
 
 
@@ -513,6 +550,10 @@ _ROW_OPERATORS = {
                    "layer_norm_mxfp4"),
     "mxfp4": ("Mxfp4", "mxfp4_dequantize", "mxfp4_empty", "mxfp4_matmul", "mxfp4_matmul_into", "mxfp4_matmul_status", "mxfp4_quantize",
               "mxfp4_quantize_both", "mxfp4_quantize_into"),
+    "mxint8": ("Mxint8", "mxint8_layer_norm_bwd", "mxint8_layer_norm_bwd_into", "mxint8_layer_norm_bwd_workspace_bytes", "mxint8_dequantize",
+               "mxint8_empty", "mxint8_quantize", "mxint8_quantize_into"),
+    "adapter": ("AdapterPlan", "adapter_bwd", "adapter_bwd_into", "adapter_bwd_workspace_bytes", "adapter_fwd", "adapter_fwd_into",
+                "adapter_plan", "adapter_status"),
 }
 _MODULE_OF = {name: module for module, names in _ROW_OPERATORS.items() for name in (module, *names)}
 

@@ -21,7 +21,7 @@ from typing import List, Optional
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
-CSRC_NN = os.path.join(PKG, "csrc_nn")  # layer normalisation and 4-bit products
+CSRC_NN = os.path.join(PKG, "csrc_nn")  # layer normalisation, 4-bit products, checkpoints and adapters
 INCLUDE = os.path.join(ROOT, "include")
 LIB_DIR = os.path.join(PKG, "_lib")
 LIB_PATH = os.path.join(LIB_DIR, "libconv2d.so")
@@ -32,7 +32,8 @@ CALLS_NOTE = os.path.join(OBJ_DIR, "calls.txt")  # calls_for(), then "built", "l
 
 SOURCES = ["conv2d_api.cu", "conv2d_bn64.cu", "conv2d_bn128.cu", "conv2d_bn256.cu", "conv2d_rowwin.cu", "conv2d_direct.cu",
            "conv2d_noalloc.cu", "conv2d_pair_kb1.cu", "conv2d_pair_kb2.cu"]
-SOURCES_NN = ["layer_norm.cu", "ln_fwd_rows.cu", "ln_bwd_rows.cu", "mxfp4.cu", "mxfp4_matmul.cu"]
+SOURCES_NN = ["layer_norm.cu", "ln_fwd_rows.cu", "ln_bwd_rows.cu", "mxfp4.cu", "mxfp4_matmul.cu", "mxint8.cu", "ln_bwd_mxint8.cu",
+              "adapter_plan.cu", "adapter.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-I", INCLUDE, "-I", CSRC]

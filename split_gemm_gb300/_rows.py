@@ -1,4 +1,4 @@
-"""What the row operators (layer normalisation, 4-bit matrices) share: argument checks, streams and the library.
+"""What the row operators (layer normalisation, 4-bit matrices, checkpoints, adapters) share: argument checks, streams and the library.
 
 The checks are written for their cost: a decoding step's calls take a few microseconds each, so the usual case is
 decided by few attribute reads and what is wrong is named only once something is.
@@ -28,6 +28,7 @@ class _NoCalls:
         return None
 
     layer_norm_fwd = layer_norm_bwd = layer_norm_mxfp4 = quantize = dequantize = matmul = _none
+    quantize_int8 = dequantize_int8 = mxint8_layer_norm_bwd = adapter_fwd = adapter_bwd = _none
 
 
 def calls():
@@ -36,14 +37,16 @@ def calls():
     if _calls is None:
         library()  # builds what is stale
         from . import _build
+        from .adapter import AdapterPlan
         from .mxfp4 import Mxfp4
+        from .mxint8 import Mxint8
         if not os.path.exists(_build.CALLS_PATH):
             _calls = _NoCalls
             return _calls
         spec = importlib.util.spec_from_file_location("split_gemm_gb300._calls", _build.CALLS_PATH)
         module = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(module)
-        module.use(Mxfp4)
+        module.use(Mxfp4, Mxint8, AdapterPlan)
         _calls = module
     return _calls
 

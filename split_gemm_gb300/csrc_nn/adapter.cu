@@ -1,0 +1,285 @@
+// Low-rank adapters: the C entry points and the kernels of any size.
+#include "adapter.h"
+
+#include <atomic>
+#include <mutex>
+#include <type_traits>
+
+#include "adapter_plan.cuh"
+#include "mxint8.cuh"
+
+namespace sgb {
+namespace ad {
+
+__device__ uint32_t adapter_word, adapter_taken;  // as the product's status words
+
+__global__ void take_adapter_status() { adapter_taken = atomicExch(&adapter_word, 0u); }
+
+std::mutex asking;
+
+constexpr int MOST_RANK = 128;
+constexpr int64_t MOST_COLS = int64_t(1) << 30;
+
+// One direction through the adapters: in [rows][from] -> mid [rows][rank] -> out [rows][to].
+struct PassParams {
+    Plan plan;
+    const __nv_bfloat16 *in, *w1, *w2;
+    const float* scale;
+    const void* base;  // y or dx0
+    void* out;
+    float* mid;
+    int64_t in_stride, base_stride, out_stride;
+    int adapters, rank, from, to;
+    int64_t w1_rank, w1_from, w2_rank, w2_to;  // strides of the weights along each of their axes
+    int relu;
+};
+
+template <typename TB, typename TO>
+__global__ void __launch_bounds__(256) pass_simple(const PassParams p)
+{
+    __shared__ float mid[MOST_RANK];
+    const Piece piece = p.plan.tiles[blockIdx.x];
+    const bool has = piece.adapter < p.adapters;
+    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+    const int64_t size = static_cast<int64_t>(p.rank);
+    const __nv_bfloat16 *w1 = p.w1 + piece.adapter * size * p.from, *w2 = p.w2 + piece.adapter * size * p.to;
+    for (int i = 0; i < piece.rows; ++i) {
+        const int64_t t = p.plan.order[piece.first + i];
+        const __nv_bfloat16* x = p.in + t * p.in_stride;
+        for (int r = warp; r < p.rank; r += 8) {
+            float s = 0.f;
+            if (has)
+                for (int c = lane; c < p.from; c += 32) s = fmaf(mx::to_float(x[c]), mx::to_float(w1[r * p.w1_rank + c * p.w1_from]), s);
+            for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+            if (has && p.scale) s *= p.scale[piece.adapter];
+            if (lane == 0) {
+                mid[r] = s;
+                if (p.mid) p.mid[t * p.rank + r] = s;
+            }
+        }
+        __syncthreads();
+        if (p.out)
+            for (int k = threadIdx.x; k < p.to; k += 256) {
+                float v = p.base ? mx::to_float(static_cast<const TB*>(p.base)[t * p.base_stride + k]) : 0.f;
+                if (has) {
+                    float s = 0.f;
+                    for (int r = 0; r < p.rank; ++r) s = fmaf(mid[r], mx::to_float(w2[r * p.w2_rank + k * p.w2_to]), s);
+                    v += s;
+                }
+                if (p.relu && v < 0.f) v = 0.f;
+                mx::from_float(static_cast<TO*>(p.out)[t * p.out_stride + k], v);
+            }
+        __syncthreads();
+    }
+}
+
+// Sums over an adapter's rows: out[e] (r, c) = sum of mid[t][r] * in[t][c].
+struct SumParams {
+    Plan plan;
+    const __nv_bfloat16* in;
+    const uint8_t *data, *scales;  // or a checkpoint
+    const float* mid;
+    float* out;
+    int64_t in_stride, blocks;
+    int rank, cols;
+    int64_t out_rank, out_col;
+};
+
+__global__ void __launch_bounds__(256) sum_simple(const SumParams p)
+{
+    const int c = blockIdx.x * 256 + threadIdx.x, r = blockIdx.y;
+    if (c >= p.cols) return;
+    const int e = blockIdx.z, first = p.plan.starts[e], last = p.plan.starts[e + 1];
+    float s = 0.f;
+    for (int i = first; i < last; ++i) {
+        const int64_t t = p.plan.order[i];
+        float v;
+        if (p.data) {
+            const int q = static_cast<int8_t>(p.data[t * (p.blocks * 32) + c]);
+            v = static_cast<float>(q) * 0.015625f * mx::scale_value(p.scales[t * p.blocks + c / 32]);
+        } else {
+            v = mx::to_float(p.in[t * p.in_stride + c]);
+        }
+        s = fmaf(p.mid[t * p.rank + r], v, s);
+    }
+    p.out[static_cast<int64_t>(e) * p.rank * p.cols + r * p.out_rank + c * p.out_col] = s;
+}
+
+// Calls f with null pointers of the two element types.
+template <typename F>
+void by_types(int32_t x, int32_t y, F&& f)
+{
+    float* f32 = nullptr;
+    __nv_bfloat16* b16 = nullptr;
+    if (x == CONV2D_OUT_BF16)
+        y == CONV2D_OUT_BF16 ? f(b16, b16) : f(b16, f32);
+    else
+        y == CONV2D_OUT_BF16 ? f(f32, b16) : f(f32, f32);
+}
+
+int launch_pass(const PassParams& p, int32_t base_dtype, int32_t out_dtype, cudaStream_t stream)
+{
+    by_types(base_dtype, out_dtype, [&](auto* tb, auto* to) {
+        pass_simple<std::remove_pointer_t<decltype(tb)>, std::remove_pointer_t<decltype(to)>><<<p.plan.n_tiles, 256, 0, stream>>>(p);
+    });
+    return cudaGetLastError() == cudaSuccess ? CONV2D_OK : CONV2D_ERR_CUDA;
+}
+
+int launch_sum(const SumParams& p, int adapters, cudaStream_t stream)
+{
+    sum_simple<<<dim3(mx::cdiv(p.cols, 256), p.rank, adapters), 256, 0, stream>>>(p);
+    return cudaGetLastError() == cudaSuccess ? CONV2D_OK : CONV2D_ERR_CUDA;
+}
+
+bool dtype_ok(int32_t t) { return t == CONV2D_OUT_F32 || t == CONV2D_OUT_BF16; }
+bool aligned(const void* p, int32_t t) { return reinterpret_cast<uintptr_t>(p) % (t == CONV2D_OUT_BF16 ? 2 : 4) == 0; }
+
+int check(int64_t rows, int64_t cols, int64_t outs, int64_t rank, int64_t adapters)
+{
+    if (rows < 0 || cols < 1 || outs < 1 || rank < 1 || adapters < 1) return CONV2D_ERR_INVALID;
+    if (rows > MOST_ROWS || cols > MOST_COLS || outs > MOST_COLS || rank > MOST_RANK || adapters > MOST_ADAPTERS) return CONV2D_ERR_UNSUPPORTED;
+    return CONV2D_OK;
+}
+
+}  // namespace ad
+}  // namespace sgb
+
+using namespace sgb;
+
+extern "C" int adapter_fwd(const adapter_fwd_params* params, const void* plan_dev, const void* y_dev, const void* x_dev,
+                           const void* a_dev, const void* b_dev, const float* scale_dev, void* out_dev, float* h_dev,
+                           conv2d_stream_t stream)
+{
+    if (!params) return CONV2D_ERR_INVALID;
+    const adapter_fwd_params& q = *params;
+    if (int rc = ad::check(q.rows, q.cols, q.outs, q.rank, q.adapters)) return rc;
+    if (!ad::dtype_ok(q.y_dtype) || !ad::dtype_ok(q.out_dtype) || (q.activation != CONV2D_ACT_NONE && q.activation != CONV2D_ACT_RELU) ||
+        q.x_stride < q.cols || q.y_stride < q.outs || q.out_stride < q.outs)
+        return CONV2D_ERR_INVALID;
+    if (q.rows == 0) return CONV2D_OK;
+    if (!plan_dev || !y_dev || !x_dev || !a_dev || !b_dev || !out_dev) return CONV2D_ERR_INVALID;
+    if (reinterpret_cast<uintptr_t>(plan_dev) % 16 || !ad::aligned(x_dev, CONV2D_OUT_BF16) || !ad::aligned(a_dev, CONV2D_OUT_BF16) ||
+        !ad::aligned(b_dev, CONV2D_OUT_BF16) || !ad::aligned(scale_dev, CONV2D_OUT_F32) || !ad::aligned(h_dev, CONV2D_OUT_F32) ||
+        !ad::aligned(y_dev, q.y_dtype) || !ad::aligned(out_dev, q.out_dtype))
+        return CONV2D_ERR_ALIGNMENT;
+    ad::PassParams p{};
+    p.plan = ad::plan_of(plan_dev, q.rows, q.adapters);
+    p.in = static_cast<const __nv_bfloat16*>(x_dev);
+    p.w1 = static_cast<const __nv_bfloat16*>(a_dev);
+    p.w2 = static_cast<const __nv_bfloat16*>(b_dev);
+    p.scale = scale_dev;
+    p.base = y_dev;
+    p.out = out_dev;
+    p.mid = h_dev;
+    p.in_stride = q.x_stride;
+    p.base_stride = q.y_stride;
+    p.out_stride = q.out_stride;
+    p.adapters = static_cast<int>(q.adapters);
+    p.rank = static_cast<int>(q.rank);
+    p.from = static_cast<int>(q.cols);
+    p.to = static_cast<int>(q.outs);
+    p.w1_rank = q.cols;
+    p.w1_from = 1;
+    p.w2_rank = 1;
+    p.w2_to = q.rank;
+    p.relu = q.activation == CONV2D_ACT_RELU;
+    return ad::launch_pass(p, q.y_dtype, q.out_dtype, stream);
+}
+
+extern "C" size_t adapter_bwd_workspace_bytes(const adapter_bwd_params* params)
+{
+    if (!params || ad::check(params->rows, params->cols, params->outs, params->rank, params->adapters)) return 0;
+    return static_cast<size_t>(params->rows) * static_cast<size_t>(params->rank) * 4;
+}
+
+extern "C" int adapter_bwd(const adapter_bwd_params* params, const void* plan_dev, const void* dy_dev, const void* x_dev,
+                           const void* x_scales_dev, const float* h_dev, const void* a_dev, const void* b_dev,
+                           const float* scale_dev, const void* dx0_dev, void* dx_dev, float* da_dev, float* db_dev,
+                           void* workspace_dev, size_t workspace_bytes, conv2d_stream_t stream)
+{
+    if (!params) return CONV2D_ERR_INVALID;
+    const adapter_bwd_params& q = *params;
+    if (int rc = ad::check(q.rows, q.cols, q.outs, q.rank, q.adapters)) return rc;
+    const bool eight = q.x_type == ADAPTER_X_MXINT8;
+    if ((!eight && q.x_type != ADAPTER_X_BF16) || !ad::dtype_ok(q.dx0_dtype) || !ad::dtype_ok(q.dx_dtype) || q.dy_stride < q.outs ||
+        (dx_dev && q.dx_stride < q.cols) || (dx0_dev && q.dx0_stride < q.cols) || (!eight && da_dev && q.x_stride < q.cols))
+        return CONV2D_ERR_INVALID;
+    if (!ad::aligned(da_dev, CONV2D_OUT_F32) || !ad::aligned(db_dev, CONV2D_OUT_F32)) return CONV2D_ERR_ALIGNMENT;
+    if (q.rows > 0) {
+        if (!plan_dev || !dy_dev || !a_dev || !b_dev || (da_dev && (!x_dev || (eight && !x_scales_dev))) || (db_dev && !h_dev))
+            return CONV2D_ERR_INVALID;
+        if (reinterpret_cast<uintptr_t>(plan_dev) % 16 || reinterpret_cast<uintptr_t>(workspace_dev) % 16 || !ad::aligned(dy_dev, CONV2D_OUT_BF16) ||
+            (eight ? reinterpret_cast<uintptr_t>(x_dev) % 16 != 0 : !ad::aligned(x_dev, CONV2D_OUT_BF16)) || !ad::aligned(h_dev, CONV2D_OUT_F32) ||
+            !ad::aligned(a_dev, CONV2D_OUT_BF16) || !ad::aligned(b_dev, CONV2D_OUT_BF16) || !ad::aligned(scale_dev, CONV2D_OUT_F32) ||
+            !ad::aligned(dx0_dev, q.dx0_dtype) || !ad::aligned(dx_dev, q.dx_dtype))
+            return CONV2D_ERR_ALIGNMENT;
+        const size_t need = adapter_bwd_workspace_bytes(params);
+        if (need && (!workspace_dev || workspace_bytes < need)) return CONV2D_ERR_WORKSPACE;
+    } else {
+        const size_t grads = static_cast<size_t>(q.adapters) * q.rank * 4;
+        if (da_dev && cudaMemsetAsync(da_dev, 0, grads * q.cols, stream) != cudaSuccess) return CONV2D_ERR_CUDA;
+        if (db_dev && cudaMemsetAsync(db_dev, 0, grads * q.outs, stream) != cudaSuccess) return CONV2D_ERR_CUDA;
+        return CONV2D_OK;
+    }
+    ad::PassParams p{};
+    p.plan = ad::plan_of(plan_dev, q.rows, q.adapters);
+    p.in = static_cast<const __nv_bfloat16*>(dy_dev);
+    p.w1 = static_cast<const __nv_bfloat16*>(b_dev);
+    p.w2 = static_cast<const __nv_bfloat16*>(a_dev);
+    p.scale = scale_dev;
+    p.base = dx0_dev;
+    p.out = dx_dev;
+    p.mid = static_cast<float*>(workspace_dev);
+    p.in_stride = q.dy_stride;
+    p.base_stride = q.dx0_stride;
+    p.out_stride = q.dx_stride;
+    p.adapters = static_cast<int>(q.adapters);
+    p.rank = static_cast<int>(q.rank);
+    p.from = static_cast<int>(q.outs);
+    p.to = static_cast<int>(q.cols);
+    p.w1_rank = 1;
+    p.w1_from = q.rank;
+    p.w2_rank = q.cols;
+    p.w2_to = 1;
+    if (dx_dev || da_dev)
+        if (int rc = ad::launch_pass(p, q.dx0_dtype, q.dx_dtype, stream)) return rc;
+    ad::SumParams s{};
+    s.plan = p.plan;
+    s.rank = p.rank;
+    if (da_dev) {
+        s.in = eight ? nullptr : static_cast<const __nv_bfloat16*>(x_dev);
+        s.data = eight ? static_cast<const uint8_t*>(x_dev) : nullptr;
+        s.scales = static_cast<const uint8_t*>(x_scales_dev);
+        s.mid = p.mid;
+        s.out = da_dev;
+        s.in_stride = q.x_stride;
+        s.blocks = mx::cdiv<int64_t>(q.cols, 32);
+        s.cols = static_cast<int>(q.cols);
+        s.out_rank = q.cols;
+        s.out_col = 1;
+        if (int rc = ad::launch_sum(s, p.adapters, stream)) return rc;
+    }
+    if (db_dev) {
+        s.in = static_cast<const __nv_bfloat16*>(dy_dev);
+        s.data = nullptr;
+        s.mid = h_dev;
+        s.out = db_dev;
+        s.in_stride = q.dy_stride;
+        s.cols = static_cast<int>(q.outs);
+        s.out_rank = 1;
+        s.out_col = q.rank;
+        if (int rc = ad::launch_sum(s, p.adapters, stream)) return rc;
+    }
+    return CONV2D_OK;
+}
+
+extern "C" int adapter_status(conv2d_stream_t stream)
+{
+    uint32_t word = 0;
+    std::lock_guard<std::mutex> one(ad::asking);
+    ad::take_adapter_status<<<1, 1, 0, stream>>>();
+    if (cudaGetLastError() != cudaSuccess) return CONV2D_ERR_CUDA;
+    if (cudaMemcpyFromSymbolAsync(&word, ad::adapter_taken, sizeof word, 0, cudaMemcpyDeviceToHost, stream) != cudaSuccess) return CONV2D_ERR_CUDA;
+    if (cudaStreamSynchronize(stream) != cudaSuccess) return CONV2D_ERR_CUDA;
+    return word == 0 ? CONV2D_OK : CONV2D_ERR_TIMEOUT;
+}

@@ -236,5 +236,5 @@ extern "C" int layer_norm_bwd(const layer_norm_params* params, const void* dy_de
         });
     if (rc) return rc;
     if (!sums) return CONV2D_OK;
-    return mx::launch(ln::bwd_join, mx::cdiv(k.cols, 32), 1024, 0, stream, 1, k) == cudaSuccess ? CONV2D_OK : CONV2D_ERR_CUDA;
+    return ln::join_parts(k, stream);
 }

@@ -172,7 +172,7 @@ __global__ void __launch_bounds__(THREADS) bwd_part_any(const TY* __restrict__ d
 }
 
 // Joins the partial sums in a fixed order: a block has 32 columns and 32 sums of every 32nd part.
-__global__ void __launch_bounds__(1024) bwd_join(const BwdParams p)
+static __global__ void __launch_bounds__(1024) bwd_join(const BwdParams p)
 {
     __shared__ float sums[2][32][33];
     const int tx = threadIdx.x & 31, ty = threadIdx.x >> 5;
@@ -200,6 +200,11 @@ __global__ void __launch_bounds__(1024) bwd_join(const BwdParams p)
         if (p.dweight) p.dweight[out] = dw;
         if (p.dbias) p.dbias[out] = db;
     }
+}
+
+inline int join_parts(const BwdParams& p, cudaStream_t stream)
+{
+    return mx::launch(bwd_join, mx::cdiv(p.cols, 32), 1024, 0, stream, 1, p) == cudaSuccess ? CONV2D_OK : CONV2D_ERR_CUDA;
 }
 
 }  // namespace ln

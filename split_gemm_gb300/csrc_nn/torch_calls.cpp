@@ -15,12 +15,16 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include "adapter.h"
 #include "layer_norm.h"
 #include "mxfp4.h"
+#include "mxint8.h"
 
 namespace {
 
-PyObject* g_mxfp4 = nullptr;  // the Mxfp4 type, a named tuple (data, scales, rows, cols)
+PyObject* g_mxfp4 = nullptr;   // the Mxfp4 type, a named tuple (data, scales, rows, cols)
+PyObject* g_mxint8 = nullptr;  // the Mxint8 type, the same
+PyObject* g_plan = nullptr;    // the AdapterPlan type, a named tuple (data, rows, adapters)
 
 // The tensor, or nullptr if the object is none (a subclass goes the general way).
 const at::Tensor* tensor(PyObject* o)
@@ -63,28 +67,72 @@ bool vector(PyObject* o, int64_t n, const at::Tensor& x, const float** p)
     return true;
 }
 
-struct Mx {
+// A non-negative int of a named tuple, or -1.
+int64_t extent(PyObject* o)
+{
+    int over = 0;
+    if (!PyLong_CheckExact(o)) return -1;
+    const int64_t n = PyLong_AsLongLongAndOverflow(o, &over);
+    return over || n < 0 ? -1 : n;
+}
+
+// A quantised matrix of the named tuple type `type`.
+struct Quantised {
     const at::Tensor *data = nullptr, *scales = nullptr;
     int64_t rows = 0, cols = 0;
-    explicit Mx(PyObject* o)
+    explicit operator bool() const { return data != nullptr; }
+
+protected:
+    Quantised(PyObject* o, PyObject* type, at::ScalarType element, size_t (*data_bytes)(int64_t, int64_t), size_t (*scale_bytes)(int64_t, int64_t))
     {
-        if (reinterpret_cast<PyObject*>(Py_TYPE(o)) != g_mxfp4) return;
+        if (reinterpret_cast<PyObject*>(Py_TYPE(o)) != type) return;
         const at::Tensor *d = tensor(PyTuple_GET_ITEM(o, 0)), *s = tensor(PyTuple_GET_ITEM(o, 1));
-        PyObject *r = PyTuple_GET_ITEM(o, 2), *c = PyTuple_GET_ITEM(o, 3);
-        if (!d || !s || !PyLong_CheckExact(r) || !PyLong_CheckExact(c)) return;
-        int over = 0;
-        rows = PyLong_AsLongLongAndOverflow(r, &over);
-        if (over) return;
-        cols = PyLong_AsLongLongAndOverflow(c, &over);
-        if (over || !here(*d) || d->device() != s->device() || d->scalar_type() != at::kByte || s->scalar_type() != at::kByte ||
-            !d->is_contiguous() || !s->is_contiguous() || rows < 1 || cols < 1 ||
-            static_cast<size_t>(d->numel()) != mxfp4_data_bytes(rows, cols) || static_cast<size_t>(s->numel()) != mxfp4_scale_bytes(rows, cols))
+        if (!d || !s) return;
+        rows = extent(PyTuple_GET_ITEM(o, 2));
+        cols = extent(PyTuple_GET_ITEM(o, 3));
+        if (rows < 1 || cols < 1 || !here(*d) || d->device() != s->device() || d->scalar_type() != element || s->scalar_type() != at::kByte ||
+            !d->is_contiguous() || !s->is_contiguous() || static_cast<size_t>(d->numel()) != data_bytes(rows, cols) ||
+            static_cast<size_t>(s->numel()) != scale_bytes(rows, cols))
             return;
         data = d;
         scales = s;
     }
+};
+
+struct Mx : Quantised {
+    explicit Mx(PyObject* o) : Quantised(o, g_mxfp4, at::kByte, mxfp4_data_bytes, mxfp4_scale_bytes) {}
+};
+
+struct Mx8 : Quantised {
+    explicit Mx8(PyObject* o) : Quantised(o, g_mxint8, at::kChar, mxint8_data_bytes, mxint8_scale_bytes) {}
+};
+
+// A plan for `rows` rows beside `like`.
+struct Plan {
+    const at::Tensor* data = nullptr;
+    int64_t adapters = 0;
+    Plan(PyObject* o, int64_t rows, const at::Tensor& like)
+    {
+        if (reinterpret_cast<PyObject*>(Py_TYPE(o)) != g_plan) return;
+        const at::Tensor* d = tensor(PyTuple_GET_ITEM(o, 0));
+        adapters = extent(PyTuple_GET_ITEM(o, 2));
+        if (!d || extent(PyTuple_GET_ITEM(o, 1)) != rows || adapters < 1 || d->device() != like.device() || d->scalar_type() != at::kInt ||
+            !d->is_contiguous() || static_cast<size_t>(d->numel()) * 4 != adapter_plan_bytes(rows, adapters))
+            return;
+        data = d;
+    }
     explicit operator bool() const { return data != nullptr; }
 };
+
+// The adapters' weights, dense bf16 of [adapters][rank][cols] and [adapters][outs][rank] beside `like`; the rank, or 0.
+int64_t rank_of(const at::Tensor* a, const at::Tensor* b, int64_t adapters, int64_t cols, int64_t outs, const at::Tensor& like)
+{
+    if (!a || !b || a->scalar_type() != at::kBFloat16 || b->scalar_type() != at::kBFloat16 || a->device() != like.device() ||
+        b->device() != like.device() || !a->is_contiguous() || !b->is_contiguous() || a->dim() != 3 || b->dim() != 3 || a->size(0) != adapters ||
+        a->size(2) != cols || b->size(0) != adapters || b->size(1) != outs || a->size(1) != b->size(2))
+        return 0;
+    return a->size(1);
+}
 
 at::Tensor empty(at::IntArrayRef shape, at::ScalarType t, const at::Tensor& like)
 {
@@ -244,22 +292,150 @@ PyObject* matmul(PyObject*, PyObject* const* v, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
-// (Mxfp4): the type that dequantize and matmul take.
-PyObject* use(PyObject*, PyObject* type)
+// (x) -> (data, scales, rows, cols)
+PyObject* quantize_int8(PyObject*, PyObject* const* a, Py_ssize_t n)
 {
-    Py_INCREF(type);
-    Py_XSETREF(g_mxfp4, type);
+    HANDLE_TH_ERRORS
+    if (n != 1) Py_RETURN_NONE;
+    const Rows x(a[0]);
+    if (!x || x.rows < 1) Py_RETURN_NONE;
+    const int64_t blocks = (x.cols + 31) / 32;
+    at::Tensor data = empty({x.rows, 32 * blocks}, at::kChar, *x.t), scales = empty({x.rows, blocks}, at::kByte, *x.t);
+    if (mxint8_quantize(x.rows, x.cols, x.t->data_ptr(), x.code, x.cols, data.data_ptr(), scales.data_ptr(), stream_of(*x.t))) Py_RETURN_NONE;
+    return mx_tuple(std::move(data), std::move(scales), x.rows, x.cols);
+    END_HANDLE_TH_ERRORS
+}
+
+// (q, out_dtype) -> y
+PyObject* dequantize_int8(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    if (n != 2) Py_RETURN_NONE;
+    const Mx8 q(a[0]);
+    const int code = out_code(a[1], -1);
+    if (!q || code < 0) Py_RETURN_NONE;
+    at::Tensor y = empty({q.rows, q.cols}, type_of(code), *q.data);
+    if (mxint8_dequantize(q.rows, q.cols, q.data->data_ptr(), q.scales->data_ptr(), y.data_ptr(), code, stream_of(*q.data))) Py_RETURN_NONE;
+    return wrap(std::move(y));
+    END_HANDLE_TH_ERRORS
+}
+
+// (dy, x, mean, rstd, weight) -> (dx, dweight, dbias)
+PyObject* norm_bwd_int8(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    if (n != 5) Py_RETURN_NONE;
+    const Rows dy(a[0]);
+    const Mx8 x(a[1]);
+    if (!dy || !x || dy.t->device() != x.data->device() || dy.rows != x.rows || dy.cols != x.cols || a[2] == Py_None || a[3] == Py_None)
+        Py_RETURN_NONE;
+    const float *mean, *rstd, *w;
+    if (!vector(a[2], x.rows, *dy.t, &mean) || !vector(a[3], x.rows, *dy.t, &rstd) || !vector(a[4], x.cols, *dy.t, &w)) Py_RETURN_NONE;
+    const layer_norm_params p{dy.rows, dy.cols, dy.cols, dy.cols, CONV2D_OUT_F32, dy.code, 0.f};
+    const int64_t need = static_cast<int64_t>(mxint8_layer_norm_bwd_workspace_bytes(&p));
+    at::Tensor dx = empty(dy.t->sizes(), dy.t->scalar_type(), *dy.t);
+    at::Tensor dw = empty({dy.cols}, at::kFloat, *dy.t), db = empty({dy.cols}, at::kFloat, *dy.t), ws = empty({need}, at::kByte, *dy.t);
+    if (mxint8_layer_norm_bwd(&p, dy.t->data_ptr(), x.data->data_ptr(), x.scales->data_ptr(), mean, rstd, w, dx.data_ptr(),
+                              static_cast<float*>(dw.data_ptr()), static_cast<float*>(db.data_ptr()), ws.data_ptr(), static_cast<size_t>(need),
+                              stream_of(*dy.t)))
+        Py_RETURN_NONE;
+    return tuple_of(std::move(dx), std::move(dw), std::move(db));
+    END_HANDLE_TH_ERRORS
+}
+
+// (y, x, a, b, plan, scale, relu, out_dtype) -> (out, h)
+PyObject* adapter_forward(PyObject*, PyObject* const* v, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    if (n != 8) Py_RETURN_NONE;
+    const Rows y(v[0]), x(v[1]);
+    if (!y || !x || x.code != CONV2D_OUT_BF16 || y.rows != x.rows || x.rows < 1 || y.t->device() != x.t->device() || !PyBool_Check(v[6]))
+        Py_RETURN_NONE;
+    const Plan plan(v[4], x.rows, *x.t);
+    const int code = out_code(v[7], y.code);
+    if (!plan || code < 0) Py_RETURN_NONE;
+    const at::Tensor *a = tensor(v[2]), *b = tensor(v[3]);
+    const int64_t rank = rank_of(a, b, plan.adapters, x.cols, y.cols, *x.t);
+    const float* scale;
+    if (rank < 1 || !vector(v[5], plan.adapters, *x.t, &scale)) Py_RETURN_NONE;
+    at::Tensor out = empty(y.t->sizes(), type_of(code), *x.t), h = empty({x.rows, rank}, at::kFloat, *x.t);
+    const adapter_fwd_params p{x.rows, x.cols, y.cols, rank, plan.adapters, x.cols, y.cols, y.cols, y.code, code,
+                               v[6] == Py_True ? CONV2D_ACT_RELU : CONV2D_ACT_NONE};
+    if (adapter_fwd(&p, plan.data->data_ptr(), y.t->data_ptr(), x.t->data_ptr(), a->data_ptr(), b->data_ptr(), scale, out.data_ptr(),
+                    static_cast<float*>(h.data_ptr()), stream_of(*x.t)))
+        Py_RETURN_NONE;
+    PyObject* r = PyTuple_New(2);
+    if (!r) return nullptr;
+    PyTuple_SET_ITEM(r, 0, wrap(std::move(out)));
+    PyTuple_SET_ITEM(r, 1, wrap(std::move(h)));
+    return r;
+    END_HANDLE_TH_ERRORS
+}
+
+// (dy, x, h, a, b, plan, scale, dx, out_dtype) -> (dx, da, db)
+PyObject* adapter_backward(PyObject*, PyObject* const* v, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    if (n != 9) Py_RETURN_NONE;
+    const Rows dy(v[0]), x16(v[1]);
+    const Mx8 x8(v[1]);
+    if (!dy || dy.code != CONV2D_OUT_BF16 || (!x8 && (!x16 || x16.code != CONV2D_OUT_BF16)) || dy.rows < 1) Py_RETURN_NONE;
+    const int64_t cols = x8 ? x8.cols : x16.cols;
+    if ((x8 ? x8.rows : x16.rows) != dy.rows || (x8 ? x8.data : x16.t)->device() != dy.t->device() || v[2] == Py_None) Py_RETURN_NONE;
+    const Plan plan(v[5], dy.rows, *dy.t);
+    if (!plan) Py_RETURN_NONE;
+    const at::Tensor *a = tensor(v[3]), *b = tensor(v[4]), *dx0 = nullptr;
+    const int64_t rank = rank_of(a, b, plan.adapters, cols, dy.cols, *dy.t);
+    const float *scale, *h;
+    if (rank < 1 || !vector(v[2], dy.rows * rank, *dy.t, &h) || !vector(v[6], plan.adapters, *dy.t, &scale)) Py_RETURN_NONE;
+    int dx0_code = CONV2D_OUT_BF16;
+    if (v[7] != Py_None) {
+        const Rows base(v[7]);
+        if (!base || base.rows != dy.rows || base.cols != cols || base.t->device() != dy.t->device()) Py_RETURN_NONE;
+        dx0 = base.t;
+        dx0_code = base.code;
+    }
+    const int code = out_code(v[8], dx0_code);
+    if (code < 0) Py_RETURN_NONE;
+    const adapter_bwd_params p{dy.rows, cols, dy.cols, rank, plan.adapters, dy.cols, cols, cols, cols, x8 ? ADAPTER_X_MXINT8 : ADAPTER_X_BF16,
+                               dx0_code, code};
+    const int64_t need = static_cast<int64_t>(adapter_bwd_workspace_bytes(&p));
+    at::Tensor dx = dx0 ? empty(dx0->sizes(), type_of(code), *dy.t) : x8 ? empty({dy.rows, cols}, type_of(code), *dy.t) : empty(x16.t->sizes(), type_of(code), *dy.t);
+    at::Tensor da = empty(a->sizes(), at::kFloat, *dy.t), db = empty(b->sizes(), at::kFloat, *dy.t), ws = empty({need}, at::kByte, *dy.t);
+    if (adapter_bwd(&p, plan.data->data_ptr(), dy.t->data_ptr(), x8 ? x8.data->data_ptr() : x16.t->data_ptr(),
+                    x8 ? x8.scales->data_ptr() : nullptr, h, a->data_ptr(), b->data_ptr(), scale, dx0 ? dx0->data_ptr() : nullptr, dx.data_ptr(),
+                    static_cast<float*>(da.data_ptr()), static_cast<float*>(db.data_ptr()), ws.data_ptr(), static_cast<size_t>(need),
+                    stream_of(*dy.t)))
+        Py_RETURN_NONE;
+    return tuple_of(std::move(dx), std::move(da), std::move(db));
+    END_HANDLE_TH_ERRORS
+}
+
+// (Mxfp4, Mxint8, AdapterPlan): the types that these functions take.
+PyObject* use(PyObject*, PyObject* const* types, Py_ssize_t n)
+{
+    PyObject** const known[3] = {&g_mxfp4, &g_mxint8, &g_plan};
+    for (Py_ssize_t i = 0; i < n && i < 3; ++i) {
+        Py_INCREF(types[i]);
+        Py_XSETREF(*known[i], types[i]);
+    }
     Py_RETURN_NONE;
 }
 
+#define FAST(name, fn) {name, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(fn)), METH_FASTCALL, nullptr}
 PyMethodDef methods[] = {
-    {"layer_norm_fwd", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(norm_fwd)), METH_FASTCALL, nullptr},
-    {"layer_norm_bwd", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(norm_bwd)), METH_FASTCALL, nullptr},
-    {"layer_norm_mxfp4", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(norm_mxfp4)), METH_FASTCALL, nullptr},
-    {"quantize", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(quantize)), METH_FASTCALL, nullptr},
-    {"dequantize", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(dequantize)), METH_FASTCALL, nullptr},
-    {"matmul", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(matmul)), METH_FASTCALL, nullptr},
-    {"use", use, METH_O, nullptr},
+    FAST("layer_norm_fwd", norm_fwd),
+    FAST("layer_norm_bwd", norm_bwd),
+    FAST("layer_norm_mxfp4", norm_mxfp4),
+    FAST("quantize", quantize),
+    FAST("dequantize", dequantize),
+    FAST("matmul", matmul),
+    FAST("quantize_int8", quantize_int8),
+    FAST("dequantize_int8", dequantize_int8),
+    FAST("mxint8_layer_norm_bwd", norm_bwd_int8),
+    FAST("adapter_fwd", adapter_forward),
+    FAST("adapter_bwd", adapter_backward),
+    FAST("use", use),
     {nullptr, nullptr, 0, nullptr},
 };
 
