@@ -1,11 +1,10 @@
-// Low-rank adapters: the C entry points and the kernels of any size.
+// Low-rank adapters: the C entry points and the rules by which kernels are chosen.
 #include "adapter.h"
 
 #include <atomic>
 #include <mutex>
-#include <type_traits>
 
-#include "adapter_plan.cuh"
+#include "adapter_params.cuh"
 #include "mxint8.cuh"
 
 namespace sgb {
@@ -17,61 +16,7 @@ __global__ void take_adapter_status() { adapter_taken = atomicExch(&adapter_word
 
 std::mutex asking;
 
-constexpr int MOST_RANK = 128;
 constexpr int64_t MOST_COLS = int64_t(1) << 30;
-
-// One direction through the adapters: in [rows][from] -> mid [rows][rank] -> out [rows][to].
-struct PassParams {
-    Plan plan;
-    const __nv_bfloat16 *in, *w1, *w2;
-    const float* scale;
-    const void* base;  // y or dx0
-    void* out;
-    float* mid;
-    int64_t in_stride, base_stride, out_stride;
-    int adapters, rank, from, to;
-    int64_t w1_rank, w1_from, w2_rank, w2_to;  // strides of the weights along each of their axes
-    int relu;
-};
-
-template <typename TB, typename TO>
-__global__ void __launch_bounds__(256) pass_simple(const PassParams p)
-{
-    __shared__ float mid[MOST_RANK];
-    const Piece piece = p.plan.tiles[blockIdx.x];
-    const bool has = piece.adapter < p.adapters;
-    const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
-    const int64_t size = static_cast<int64_t>(p.rank);
-    const __nv_bfloat16 *w1 = p.w1 + piece.adapter * size * p.from, *w2 = p.w2 + piece.adapter * size * p.to;
-    for (int i = 0; i < piece.rows; ++i) {
-        const int64_t t = p.plan.order[piece.first + i];
-        const __nv_bfloat16* x = p.in + t * p.in_stride;
-        for (int r = warp; r < p.rank; r += 8) {
-            float s = 0.f;
-            if (has)
-                for (int c = lane; c < p.from; c += 32) s = fmaf(mx::to_float(x[c]), mx::to_float(w1[r * p.w1_rank + c * p.w1_from]), s);
-            for (int o = 16; o; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-            if (has && p.scale) s *= p.scale[piece.adapter];
-            if (lane == 0) {
-                mid[r] = s;
-                if (p.mid) p.mid[t * p.rank + r] = s;
-            }
-        }
-        __syncthreads();
-        if (p.out)
-            for (int k = threadIdx.x; k < p.to; k += 256) {
-                float v = p.base ? mx::to_float(static_cast<const TB*>(p.base)[t * p.base_stride + k]) : 0.f;
-                if (has) {
-                    float s = 0.f;
-                    for (int r = 0; r < p.rank; ++r) s = fmaf(mid[r], mx::to_float(w2[r * p.w2_rank + k * p.w2_to]), s);
-                    v += s;
-                }
-                if (p.relu && v < 0.f) v = 0.f;
-                mx::from_float(static_cast<TO*>(p.out)[t * p.out_stride + k], v);
-            }
-        __syncthreads();
-    }
-}
 
 // Sums over an adapter's rows: out[e] (r, c) = sum of mid[t][r] * in[t][c].
 struct SumParams {
@@ -105,24 +50,41 @@ __global__ void __launch_bounds__(256) sum_simple(const SumParams p)
     p.out[static_cast<int64_t>(e) * p.rank * p.cols + r * p.out_rank + c * p.out_col] = s;
 }
 
-// Calls f with null pointers of the two element types.
-template <typename F>
-void by_types(int32_t x, int32_t y, F&& f)
+// The number of CTAs that share a tile and of stages in their rings.
+void shape_pass(PassParams& p, int64_t rows)
 {
-    float* f32 = nullptr;
-    __nv_bfloat16* b16 = nullptr;
-    if (x == CONV2D_OUT_BF16)
-        y == CONV2D_OUT_BF16 ? f(b16, b16) : f(b16, f32);
-    else
-        y == CONV2D_OUT_BF16 ? f(f32, b16) : f(f32, f32);
+    // two CTAs to an SM where two stages of the ring fit, else one
+    int per_sm = 2;
+    p.stages = 2;
+    int room = 113 * 1024;
+    if (PassSmem(p.rank, 2).bytes() > room) {
+        per_sm = 1;
+        room = 227 * 1024;
+    }
+    while (p.stages < P_MOST_STAGES && PassSmem(p.rank, p.stages + 1).bytes() <= room) ++p.stages;
+    const int64_t tiles = mx::cdiv<int64_t>(rows, TILE);
+    const int steps = mx::cdiv(p.from, P_STEP);
+    p.splits = 1;
+    while (p.splits < 8 && tiles * p.splits < mx::SMS * per_sm && 2 * p.splits <= steps) p.splits *= 2;
 }
 
-int launch_pass(const PassParams& p, int32_t base_dtype, int32_t out_dtype, cudaStream_t stream)
+size_t size_of(int32_t t) { return t == CONV2D_OUT_BF16 ? 2 : 4; }
+
+bool vectors(const void* p, int64_t stride, size_t elem) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride * elem % 16 == 0; }
+
+// Whether every row that the pass touches is whole 16-byte vectors.
+bool in_vectors(const PassParams& p, int32_t base, int32_t out)
 {
-    by_types(base_dtype, out_dtype, [&](auto* tb, auto* to) {
-        pass_simple<std::remove_pointer_t<decltype(tb)>, std::remove_pointer_t<decltype(to)>><<<p.plan.n_tiles, 256, 0, stream>>>(p);
-    });
-    return cudaGetLastError() == cudaSuccess ? CONV2D_OK : CONV2D_ERR_CUDA;
+    return (p.rank | p.from | p.to) % 8 == 0 && vectors(p.in, p.in_stride, 2) && vectors(p.w1, 8, 2) && vectors(p.w2, 8, 2) &&
+           vectors(p.base, p.base ? p.base_stride : 8, size_of(base)) && vectors(p.out, p.out ? p.out_stride : 8, size_of(out));
+}
+
+bool status_word(uint32_t** word)
+{
+    void* at = nullptr;
+    if (cudaGetSymbolAddress(&at, adapter_word) != cudaSuccess) return false;
+    *word = static_cast<uint32_t*>(at);
+    return true;
 }
 
 int launch_sum(const SumParams& p, int adapters, cudaStream_t stream)
@@ -164,6 +126,7 @@ extern "C" int adapter_fwd(const adapter_fwd_params* params, const void* plan_de
         return CONV2D_ERR_ALIGNMENT;
     ad::PassParams p{};
     p.plan = ad::plan_of(plan_dev, q.rows, q.adapters);
+    if (!ad::status_word(&p.status)) return CONV2D_ERR_CUDA;
     p.in = static_cast<const __nv_bfloat16*>(x_dev);
     p.w1 = static_cast<const __nv_bfloat16*>(a_dev);
     p.w2 = static_cast<const __nv_bfloat16*>(b_dev);
@@ -178,12 +141,9 @@ extern "C" int adapter_fwd(const adapter_fwd_params* params, const void* plan_de
     p.rank = static_cast<int>(q.rank);
     p.from = static_cast<int>(q.cols);
     p.to = static_cast<int>(q.outs);
-    p.w1_rank = q.cols;
-    p.w1_from = 1;
-    p.w2_rank = 1;
-    p.w2_to = q.rank;
     p.relu = q.activation == CONV2D_ACT_RELU;
-    return ad::launch_pass(p, q.y_dtype, q.out_dtype, stream);
+    ad::shape_pass(p, q.rows);
+    return ad::launch_pass_fwd(p, q.y_dtype, q.out_dtype, ad::in_vectors(p, q.y_dtype, q.out_dtype), stream);
 }
 
 extern "C" size_t adapter_bwd_workspace_bytes(const adapter_bwd_params* params)
@@ -237,12 +197,10 @@ extern "C" int adapter_bwd(const adapter_bwd_params* params, const void* plan_de
     p.rank = static_cast<int>(q.rank);
     p.from = static_cast<int>(q.outs);
     p.to = static_cast<int>(q.cols);
-    p.w1_rank = 1;
-    p.w1_from = q.rank;
-    p.w2_rank = q.cols;
-    p.w2_to = 1;
+    if (!ad::status_word(&p.status)) return CONV2D_ERR_CUDA;
+    ad::shape_pass(p, q.rows);
     if (dx_dev || da_dev)
-        if (int rc = ad::launch_pass(p, q.dx0_dtype, q.dx_dtype, stream)) return rc;
+        if (int rc = ad::launch_pass_bwd(p, q.dx0_dtype, q.dx_dtype, ad::in_vectors(p, q.dx0_dtype, q.dx_dtype), stream)) return rc;
     ad::SumParams s{};
     s.plan = p.plan;
     s.rank = p.rank;

@@ -1,0 +1,50 @@
+// Kernel parameters of the adapter kernels and their shared memory.
+#pragma once
+
+#include <atomic>
+
+#include "adapter_plan.cuh"
+
+namespace sgb {
+namespace ad {
+
+constexpr int MOST_RANK = 128;
+
+struct PassParams {
+    Plan plan;
+    const __nv_bfloat16 *in, *w1, *w2;
+    const float* scale;
+    const void* base;  // y or dx0
+    void* out;
+    float* mid;
+    uint32_t* status;
+    int64_t in_stride, base_stride, out_stride;
+    int adapters, rank, from, to;
+    int relu;
+    int splits, stages;  // CTAs of a cluster, stages of the ring
+};
+
+constexpr int P_STEP = 64;  // of `from`, in a stage
+constexpr int P_COLS = 64;  // of `to`, in a chunk
+constexpr int P_MOST_STAGES = 6;
+
+// Shared memory by the rank padded to 16.  A chunk of w2: core matrices 144 bytes apart along the columns, so that the pairs that the
+// backward pass places one by one fall into different banks.
+struct PassSmem {
+    int rp, stages;
+    __host__ __device__ constexpr PassSmem(int rank, int stages) : rp((rank + 15) / 16 * 16), stages(stages) {}
+    __host__ __device__ constexpr int stage() const { return TILE * P_STEP * 2 + rp * P_STEP * 2; }
+    __host__ __device__ constexpr int pitch() const { return rp + 4; }                     // of the joined sums' rows, in words
+    __host__ __device__ constexpr int sums() const { return TILE * pitch() * 4; }
+    __host__ __device__ constexpr int chunk() const { return rp / 8 * 1152; }
+    // the ring; after it the sums and w2's second buffer
+    __host__ __device__ constexpr int ring() const { return stages * stage() > sums() + chunk() ? stages * stage() : sums() + chunk(); }
+    __host__ __device__ constexpr int parts() const { return TILE * 3 * rp * 2; }
+    __host__ __device__ constexpr int bytes() const { return ring() + parts() + chunk() + 256; }
+};
+
+int launch_pass_fwd(const PassParams& p, int32_t base_dtype, int32_t out_dtype, bool vec, cudaStream_t stream);
+int launch_pass_bwd(const PassParams& p, int32_t base_dtype, int32_t out_dtype, bool vec, cudaStream_t stream);
+
+}  // namespace ad
+}  // namespace sgb

@@ -1,0 +1,76 @@
+// Inline-PTX wrappers of the adapter kernels, written from the PTX ISA's instruction descriptions; the others are in ptx.cuh and mx_ptx.cuh.
+#pragma once
+
+#include "mx_ptx.cuh"
+
+namespace sgb {
+namespace ptx {
+
+// 16 lanes x 32 consecutive 32-bit columns of tensor memory: of column group j of 8, thread t gets columns 8j + 2(t%4) and the next, of
+// lane t/4 in v[4j], v[4j+1] and of lane t/4 + 8 in v[4j+2], v[4j+3].
+__device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&v)[16])
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+          "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+        : "r"(taddr)
+        : "memory");
+}
+
+// The same descriptor as plain_kmajor_desc for an MN-major operand without swizzle: core matrices of 8 reduction indices x 16 bytes of M (or N),
+// the 8 indices 16 B apart; `sbo` is the distance of core matrices adjacent along M/N and `lbo` along the reduction.
+__device__ __forceinline__ uint64_t plain_mnmajor_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) { return plain_kmajor_desc(saddr, lbo, sbo); }
+
+// One MMA from one elected lane of a warp in uniform control flow.
+__device__ __forceinline__ void mma_bf16_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, e;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// Four bytes, zero where `src_bytes` is 0 (the address need only be valid for 4 bytes).
+__device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src, uint32_t src_bytes)
+{
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+}
+
+__device__ __forceinline__ void cp_async_16s(uint32_t dst, const void* src, uint32_t src_bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
+}
+
+// Orders this thread's generic-proxy writes, to any CTA's shared memory, before later async-proxy accesses.
+__device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
+
+__device__ __forceinline__ void st_cluster_v2(uint32_t cluster_addr, uint32_t a, uint32_t b)
+{
+    asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(cluster_addr), "r"(a), "r"(b) : "memory");
+}
+
+}  // namespace ptx
+
+namespace ad {
+
+// A 32-bit value as three bf16 parts that add up to it exactly: its first 8 significant bits, the next 8 and the rest (each cut off, so
+// that no part is larger than the value); what is not finite stays in the first alone.
+__device__ __forceinline__ void split3(float v, uint32_t& hi, uint32_t& mid, uint32_t& lo)
+{
+    const uint32_t b = __float_as_uint(v);
+    const bool finite = (b & 0x7f800000u) != 0x7f800000u;
+    const float r = v - __uint_as_float(b & 0xffff0000u);
+    const uint32_t rb = __float_as_uint(r);
+    const float q = r - __uint_as_float(rb & 0xffff0000u);
+    hi = finite ? b >> 16 : (b >> 16) | ((b & 0x7fffffu) ? 0x40u : 0u);  // a NaN stays one
+    mid = finite ? rb >> 16 : 0u;
+    lo = finite ? __float_as_uint(q) >> 16 : 0u;
+}
+
+}  // namespace ad
+}  // namespace sgb
