@@ -18,38 +18,6 @@ std::mutex asking;
 
 constexpr int64_t MOST_COLS = int64_t(1) << 30;
 
-// Sums over an adapter's rows: out[e] (r, c) = sum of mid[t][r] * in[t][c].
-struct SumParams {
-    Plan plan;
-    const __nv_bfloat16* in;
-    const uint8_t *data, *scales;  // or a checkpoint
-    const float* mid;
-    float* out;
-    int64_t in_stride, blocks;
-    int rank, cols;
-    int64_t out_rank, out_col;
-};
-
-__global__ void __launch_bounds__(256) sum_simple(const SumParams p)
-{
-    const int c = blockIdx.x * 256 + threadIdx.x, r = blockIdx.y;
-    if (c >= p.cols) return;
-    const int e = blockIdx.z, first = p.plan.starts[e], last = p.plan.starts[e + 1];
-    float s = 0.f;
-    for (int i = first; i < last; ++i) {
-        const int64_t t = p.plan.order[i];
-        float v;
-        if (p.data) {
-            const int q = static_cast<int8_t>(p.data[t * (p.blocks * 32) + c]);
-            v = static_cast<float>(q) * 0.015625f * mx::scale_value(p.scales[t * p.blocks + c / 32]);
-        } else {
-            v = mx::to_float(p.in[t * p.in_stride + c]);
-        }
-        s = fmaf(p.mid[t * p.rank + r], v, s);
-    }
-    p.out[static_cast<int64_t>(e) * p.rank * p.cols + r * p.out_rank + c * p.out_col] = s;
-}
-
 // The number of CTAs that share a tile and of stages in their rings.
 void shape_pass(PassParams& p, int64_t rows)
 {
@@ -79,18 +47,15 @@ bool in_vectors(const PassParams& p, int32_t base, int32_t out)
            vectors(p.base, p.base ? p.base_stride : 8, size_of(base)) && vectors(p.out, p.out ? p.out_stride : 8, size_of(out));
 }
 
+// dh's bytes in the workspace, to whole vectors.
+size_t dh_bytes(int64_t rows, int64_t rank) { return (static_cast<size_t>(rows) * static_cast<size_t>(rank) * 4 + 15) / 16 * 16; }
+
 bool status_word(uint32_t** word)
 {
     void* at = nullptr;
     if (cudaGetSymbolAddress(&at, adapter_word) != cudaSuccess) return false;
     *word = static_cast<uint32_t*>(at);
     return true;
-}
-
-int launch_sum(const SumParams& p, int adapters, cudaStream_t stream)
-{
-    sum_simple<<<dim3(mx::cdiv(p.cols, 256), p.rank, adapters), 256, 0, stream>>>(p);
-    return cudaGetLastError() == cudaSuccess ? CONV2D_OK : CONV2D_ERR_CUDA;
 }
 
 bool dtype_ok(int32_t t) { return t == CONV2D_OUT_F32 || t == CONV2D_OUT_BF16; }
@@ -149,7 +114,10 @@ extern "C" int adapter_fwd(const adapter_fwd_params* params, const void* plan_de
 extern "C" size_t adapter_bwd_workspace_bytes(const adapter_bwd_params* params)
 {
     if (!params || ad::check(params->rows, params->cols, params->outs, params->rank, params->adapters)) return 0;
-    return static_cast<size_t>(params->rows) * static_cast<size_t>(params->rank) * 4;
+    // dh, and two parts of each gradient to a piece
+    const int each = ad::sum_tiles_each(params->rows, params->adapters, static_cast<int>(params->rank), params->cols, params->outs);
+    const size_t pieces = static_cast<size_t>(ad::sum_pieces(ad::PlanLayout(params->rows, params->adapters), each));
+    return ad::dh_bytes(params->rows, params->rank) + 2 * pieces * params->rank * static_cast<size_t>(params->cols + params->outs) * 4;
 }
 
 extern "C" int adapter_bwd(const adapter_bwd_params* params, const void* plan_dev, const void* dy_dev, const void* x_dev,
@@ -203,32 +171,38 @@ extern "C" int adapter_bwd(const adapter_bwd_params* params, const void* plan_de
         if (int rc = ad::launch_pass_bwd(p, q.dx0_dtype, q.dx_dtype, ad::in_vectors(p, q.dx0_dtype, q.dx_dtype), stream)) return rc;
     ad::SumParams s{};
     s.plan = p.plan;
+    s.status = p.status;
+    s.adapters = p.adapters;
     s.rank = p.rank;
+    s.tiles_each = ad::sum_tiles_each(q.rows, q.adapters, p.rank, q.cols, q.outs);
+    const int64_t pieces = ad::sum_pieces(ad::PlanLayout(q.rows, q.adapters), s.tiles_each);
+    float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace_dev) + ad::dh_bytes(q.rows, q.rank));
     if (da_dev) {
-        s.in = eight ? nullptr : static_cast<const __nv_bfloat16*>(x_dev);
-        s.data = eight ? static_cast<const uint8_t*>(x_dev) : nullptr;
-        s.scales = static_cast<const uint8_t*>(x_scales_dev);
-        s.mid = p.mid;
-        s.out = da_dev;
-        s.in_stride = q.x_stride;
-        s.blocks = mx::cdiv<int64_t>(q.cols, 32);
-        s.cols = static_cast<int>(q.cols);
-        s.out_rank = q.cols;
-        s.out_col = 1;
-        if (int rc = ad::launch_sum(s, p.adapters, stream)) return rc;
+        ad::SumJob& job = s.jobs[0];
+        job.in = static_cast<const __nv_bfloat16*>(x_dev);
+        job.data = static_cast<const uint8_t*>(x_dev);
+        job.scales = static_cast<const uint8_t*>(x_scales_dev);
+        job.mid = p.mid;
+        job.out = da_dev;
+        job.part = part;
+        job.in_stride = q.x_stride;
+        job.blocks = mx::cdiv<int64_t>(q.cols, 32);
+        job.cols = static_cast<int>(q.cols);
+        job.mode = eight ? 2 : q.cols % 8 == 0 && ad::vectors(x_dev, q.x_stride, 2) ? 0 : 1;
+        job.out_col = 1;
     }
     if (db_dev) {
-        s.in = static_cast<const __nv_bfloat16*>(dy_dev);
-        s.data = nullptr;
-        s.mid = h_dev;
-        s.out = db_dev;
-        s.in_stride = q.dy_stride;
-        s.cols = static_cast<int>(q.outs);
-        s.out_rank = 1;
-        s.out_col = q.rank;
-        if (int rc = ad::launch_sum(s, p.adapters, stream)) return rc;
+        ad::SumJob& job = s.jobs[1];
+        job.in = static_cast<const __nv_bfloat16*>(dy_dev);
+        job.mid = h_dev;
+        job.out = db_dev;
+        job.part = part + 2 * pieces * q.rank * q.cols;
+        job.in_stride = q.dy_stride;
+        job.cols = static_cast<int>(q.outs);
+        job.mode = q.outs % 8 == 0 && ad::vectors(dy_dev, q.dy_stride, 2) ? 0 : 1;
+        job.out_col = 0;
     }
-    return CONV2D_OK;
+    return ad::launch_sums(s, pieces, stream);
 }
 
 extern "C" int adapter_status(conv2d_stream_t stream)

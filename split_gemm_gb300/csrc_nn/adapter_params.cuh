@@ -43,6 +43,32 @@ struct PassSmem {
     __host__ __device__ constexpr int bytes() const { return ring() + parts() + chunk() + 256; }
 };
 
+// Sums over the adapters' rows: out[e] (r, c) = sum of mid[t][r] * in[t][c].
+struct SumJob {
+    const __nv_bfloat16* in;
+    const uint8_t *data, *scales;  // or a checkpoint
+    const float* mid;
+    float *out, *part;             // part: [2 * pieces][rank * cols], in out's order
+    int64_t in_stride, blocks;     // blocks of 32 to a checkpoint's row
+    int cols, col_blocks;
+    int mode;                      // 0: bf16 rows of whole vectors, 1: bf16, 2: a checkpoint
+    int out_col;                   // 1: out[r][c]; else out[c][r]
+    int mid_vec, out_vec, join_vec;
+};
+
+struct SumParams {
+    Plan plan;
+    SumJob jobs[2];  // without a result: not wanted
+    uint32_t* status;
+    int adapters, rank, tiles_each, per_piece;
+};
+
+constexpr int SUM_TILES = 32;  // of a piece, at most
+
+int sum_tiles_each(int64_t rows, int64_t adapters, int rank, int64_t cols, int64_t outs);
+int64_t sum_pieces(const PlanLayout& l, int tiles_each);
+int launch_sums(SumParams& p, int64_t pieces, cudaStream_t stream);
+
 int launch_pass_fwd(const PassParams& p, int32_t base_dtype, int32_t out_dtype, bool vec, cudaStream_t stream);
 int launch_pass_bwd(const PassParams& p, int32_t base_dtype, int32_t out_dtype, bool vec, cudaStream_t stream);
 

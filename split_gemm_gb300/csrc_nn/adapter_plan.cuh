@@ -52,6 +52,7 @@ struct PlanLayout {
 struct Plan {
     const int *starts, *order;
     const Piece *tiles, *small;
+    const int* tile_starts;  // [adapters + 2]: number of each adapter's first tile
     int n_tiles, n_small;
 };
 
@@ -60,7 +61,7 @@ inline Plan plan_of(const void* plan, int64_t rows, int64_t adapters)
     const PlanLayout l(rows, adapters);
     const int* w = static_cast<const int*>(plan);
     return Plan{w, w + l.order(), reinterpret_cast<const Piece*>(w + l.table()), reinterpret_cast<const Piece*>(w + l.small_table()),
-                static_cast<int>(l.tiles), static_cast<int>(l.small)};
+                w + l.tile_starts(), static_cast<int>(l.tiles), static_cast<int>(l.small)};
 }
 
 }  // namespace ad
