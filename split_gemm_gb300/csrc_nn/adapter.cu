@@ -43,7 +43,7 @@ bool vectors(const void* p, int64_t stride, size_t elem) { return reinterpret_ca
 // Whether every row that the pass touches is whole 16-byte vectors.
 bool in_vectors(const PassParams& p, int32_t base, int32_t out)
 {
-    return (p.rank | p.from | p.to) % 8 == 0 && vectors(p.in, p.in_stride, 2) && vectors(p.w1, 8, 2) && vectors(p.w2, 8, 2) &&
+    return (p.rank | p.from | p.to) % 8 == 0 && vectors(p.in, p.in_stride, 2) && vectors(p.w1, 8, 2) && vectors(p.w2, 8, 2) && vectors(p.mid, 8, 4) &&
            vectors(p.base, p.base ? p.base_stride : 8, size_of(base)) && vectors(p.out, p.out ? p.out_stride : 8, size_of(out));
 }
 

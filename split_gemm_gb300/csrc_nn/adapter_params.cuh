@@ -28,12 +28,15 @@ constexpr int P_STEP = 64;  // of `from`, in a stage
 constexpr int P_COLS = 64;  // of `to`, in a chunk
 constexpr int P_MOST_STAGES = 6;
 
+// Bytes between the 16-byte columns of an MN-major stage of w1: 16 more than they need, so that neighbours fall into different banks.
+constexpr int W1_COLUMN = P_STEP * 16 + 16;
+
 // Shared memory by the rank padded to 16.  A chunk of w2: core matrices 144 bytes apart along the columns, so that the pairs that the
 // backward pass places one by one fall into different banks.
 struct PassSmem {
     int rp, stages;
     __host__ __device__ constexpr PassSmem(int rank, int stages) : rp((rank + 15) / 16 * 16), stages(stages) {}
-    __host__ __device__ constexpr int stage() const { return TILE * P_STEP * 2 + rp * P_STEP * 2; }
+    __host__ __device__ constexpr int stage() const { return TILE * P_STEP * 2 + (rp / 8 * W1_COLUMN + 1023) / 1024 * 1024; }
     __host__ __device__ constexpr int pitch() const { return rp + 4; }                     // of the joined sums' rows, in words
     __host__ __device__ constexpr int sums() const { return TILE * pitch() * 4; }
     __host__ __device__ constexpr int chunk() const { return rp / 8 * 1152; }

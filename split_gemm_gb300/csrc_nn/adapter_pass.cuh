@@ -6,12 +6,10 @@
 //
 // in, base and out each pass once over HBM and bind it: with rank r the matrix units have 2r flops to some 4 bytes.  A cluster
 // of S CTAs shares a tile: each takes a part of `from` for the first product, 128/S rows of the join and a part of `to` for the
-// second, so that few tiles fill the SMs and the smaller the parts, the more tiles are at different phases at once on an SM (two CTAs stay there up
-// to rank 64).  mid never leaves the chip but for the copy that the gradients need.
+// second.  Two CTAs stay on an SM up to rank 64, each at a phase of its own.  mid never leaves the chip but for the copy that the gradients need.
 //
-// First product: rows of `in` are gathered by the plan's order with cp.async into core matrices of 8 rows x 16 bytes (no
-// swizzle); a quarter warp copies one 16-byte column of 8 rows, which is conflict-free in shared memory, a warp 64 bytes of each row.  128 x rank
-// x 64 a stage.  The sums over the parts meet in shared memory as fp32, are joined in the CTAs' order and cut into three bf16 parts that
+// First product: rows of `in` are gathered by the plan's order with cp.async, 128 bytes of a row at a time, 128 x rank x 64 a stage.  The sums over
+// the parts meet in shared memory as fp32, are joined in the CTAs' order and cut into three bf16 parts that
 // hold all 24 bits: the second product, K = 3 * rank, is that of an fp32 mid.
 //
 // Second product: 64 columns of `to` at a time, two accumulators in turn.  A thread reads the accumulator in the 16 x 256-bit layout, 2
@@ -91,29 +89,58 @@ struct Pass {
         }
     }
 
-    // Columns f0 .. f0+63 of the tile's rows and of w1.
-    __device__ __forceinline__ void load_stage(uint8_t* st, int f0, const __nv_bfloat16* const (&rows)[2]) const
+    // Where a loader's copies of an MN-major w1 or a K-major w2 go: 64 rows of rank/8 16-byte columns, one after another in memory.
+    // (Addresses are kept in registers: computed for each copy they cost the loaders more time than the copies.)
+    uint32_t place[4];
+    __device__ __forceinline__ void make_places()
     {
-        const uint32_t at = ptx::smem_addr(st);
+        const int per = p.rank >> 3;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int row = (lane & 7) + 8 * warp + 64 * (i & 1), c8 = (lane >> 3) + 4 * (i >> 1);
-            if (row < piece.rows) copy8(at + (row & 7) * 16 + (row >> 3) * 128 + c8 * 2048, rows[i & 1] + f0 + 8 * c8, p.from - f0 - 8 * c8);
+        for (int j = 0; j < 4; ++j) {
+            const int i = tid + P_LOADERS * j, row = i / per, c8 = i - row * per;
+            const int n = (row & 32) + 8 * ((row >> 1) & 3) + 2 * ((row >> 3) & 3) + (row & 1);  // of w2, as below
+            place[j] = row >= 64 ? 0xffffffffu : TRANS ? (row & 7) * 16 + (row >> 3) * 128 + c8 * W1_COLUMN : (n & 7) * 16 + (n >> 3) * 144 + c8 * 1152;
         }
-        const uint32_t w_at = at + TILE * P_STEP * 2;
+    }
+
+    // Columns f0 .. f0+63 of the tile's rows and of w1.  rows: at this thread's 16-byte column of every 32nd row.
+    __device__ __forceinline__ void load_stage(uint8_t* st, int f0, const __nv_bfloat16* const (&rows)[4]) const
+    {
+        const uint32_t at = ptx::smem_addr(st), w_at = at + TILE * P_STEP * 2;
         const int64_t size = static_cast<int64_t>(p.rank) * p.from;
         const __nv_bfloat16* w = p.w1 + e * size;
-        if constexpr (!TRANS) {
-            for (int i = tid; i < s.rp * 8; i += P_LOADERS) {  // rows of 8 16-byte columns
-                const int group = i >> 5, groups = s.rp >> 3, half = group >= groups;
-                const int r = (i & 7) + 8 * (group - half * groups), c8 = ((i >> 3) & 3) + 4 * half;
-                if (r < p.rank) copy8(w_at + (r & 7) * 16 + (r >> 3) * 128 + c8 * (s.rp * 16), w + static_cast<int64_t>(r) * p.from + f0 + 8 * c8, p.from - f0 - 8 * c8);
+        const int row = tid >> 3, c8 = tid & 7;
+        const uint32_t mine = row * 128 + ((c8 ^ (row & 7)) << 4);  // 128-byte swizzle
+        if (VEC && f0 + P_STEP <= p.from) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                if (row + 32 * i < piece.rows) ptx::cp_async_16s(at + mine + 4096 * i, rows[i] + f0, 16);
+            if constexpr (!TRANS) {
+                const __nv_bfloat16* src = w + static_cast<int64_t>(row) * p.from + f0 + 8 * c8;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    if (row + 32 * i < p.rank) ptx::cp_async_16s(w_at + mine + 4096 * i, src, 16);
+                    src += 32 * static_cast<int64_t>(p.from);
+                }
+            } else {
+                const __nv_bfloat16* src = w + static_cast<int64_t>(f0) * p.rank + 8 * tid;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (place[i] != 0xffffffffu) ptx::cp_async_16s(w_at + place[i], src + 8 * P_LOADERS * i, 16);
             }
+            return;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (row + 32 * i < piece.rows) copy8(at + mine + 4096 * i, rows[i] + f0, p.from - f0 - 8 * c8);
+        if constexpr (!TRANS) {
+            for (int r = row; r < p.rank; r += 32)
+                copy8(w_at + r * 128 + ((c8 ^ (r & 7)) << 4), w + static_cast<int64_t>(r) * p.from + f0 + 8 * c8, p.from - f0 - 8 * c8);
         } else {
             for (int i = tid; i < s.rp * 8; i += P_LOADERS) {  // 64 rows of rp/8 16-byte columns
                 const int k = (i >> 1) & 63, n8 = 2 * (i >> 7) + (i & 1);
                 const int left = f0 + k < p.from ? p.rank - 8 * n8 : 0;
-                copy8(w_at + (k & 7) * 16 + n8 * 1024 + (k >> 3) * 128, w + static_cast<int64_t>(f0 + k) * p.rank + 8 * n8, left);
+                copy8(w_at + (k & 7) * 16 + n8 * W1_COLUMN + (k >> 3) * 128, w + static_cast<int64_t>(f0 + k) * p.rank + 8 * n8, left);
             }
         }
     }
@@ -124,6 +151,20 @@ struct Pass {
         const uint32_t at = ptx::smem_addr(buf);
         const int64_t size = static_cast<int64_t>(p.rank) * p.to;
         const __nv_bfloat16* w = p.w2 + e * size;
+        if (VEC && c0 + P_COLS <= p.to) {
+            if constexpr (!TRANS) {
+                const __nv_bfloat16* src = w + static_cast<int64_t>(c0) * p.rank + 8 * tid;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (place[i] != 0xffffffffu) ptx::cp_async_16s(at + place[i], src + 8 * P_LOADERS * i, 16);
+            } else {
+                const int c = 2 * lane;
+                uint32_t dst = at + warp * 16 + ((c >> 3) & 3) * 4 + (((c >> 1) & 3) + 4 * (c >> 5)) * 144;
+                const __nv_bfloat16* src = w + static_cast<int64_t>(warp) * p.to + c0 + c;
+                for (int k = warp; k < p.rank; k += 8, dst += 1152, src += 8 * static_cast<int64_t>(p.to)) ptx::cp_async_4(dst, src, 4);
+            }
+            return;
+        }
         if constexpr (!TRANS) {
             for (int i = tid; i < s.rp * 8; i += P_LOADERS) {
                 const int n = (i >> 1) & 63, k8 = 2 * (i >> 7) + (i & 1);
@@ -145,128 +186,157 @@ struct Pass {
             }
         }
     }
+    // The part of a chunk of w2 that pads an odd number of 8 ranks; whole copies do not reach it.
+    __device__ __forceinline__ void clear_pad(uint8_t* buf) const
+    {
+        if (VEC && (p.rank & 8) && tid < 64) ptx::st_shared_v4(ptx::smem_addr(buf) + (tid & 7) * 16 + (tid >> 3) * 144 + (p.rank >> 3) * 1152, 0u, 0u, 0u, 0u);
+        if (VEC) ptx::fence_proxy_async_smem();
+    }
 
     // This CTA's rows of the sums over the cluster: scaled, to mid, and in three parts to every CTA.
     template <int S>
     __device__ __forceinline__ void join(const float* sums, float scale) const
     {
         constexpr int SHARE = TILE / S;
-        const int quads = s.rp >> 2;
-        for (int i = tid; i < SHARE * quads; i += P_THREADS) {
-            const int row = rank_in * SHARE + i % SHARE, r = 4 * (i / SHARE);
+        const int eighths = s.rp >> 3;
+        for (int i = tid; i < SHARE * eighths; i += P_THREADS) {
+            const int row = rank_in * SHARE + i % SHARE, r = 8 * (i / SHARE);
             const float* at = sums + row * s.pitch() + r;
-            float v[4] = {0.f, 0.f, 0.f, 0.f};
+            float v[8] = {};
             if (row < piece.rows) {
-                if constexpr (S == 1) {
-                    *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(at);
-                } else {
+#pragma unroll
+                for (int h = 0; h < 8; h += 4) {
                     float4 u[S];
 #pragma unroll
-                    for (int k = 0; k < S; ++k) u[k] = ptx::ld_cluster_v4(ptx::mapa_shared(ptx::smem_addr(at), k));
+                    for (int k = 0; k < S; ++k) {
+                        if constexpr (S == 1)
+                            u[k] = *reinterpret_cast<const float4*>(at + h);
+                        else
+                            u[k] = ptx::ld_cluster_v4(ptx::mapa_shared(ptx::smem_addr(at + h), k));
+                    }
 #pragma unroll
                     for (int k = 0; k < S; ++k) {
-                        v[0] += u[k].x;
-                        v[1] += u[k].y;
-                        v[2] += u[k].z;
-                        v[3] += u[k].w;
+                        v[h] += u[k].x;
+                        v[h + 1] += u[k].y;
+                        v[h + 2] += u[k].z;
+                        v[h + 3] += u[k].w;
                     }
                 }
 #pragma unroll
-                for (int j = 0; j < 4; ++j) v[j] = r + j < p.rank ? v[j] * scale : 0.f;
+                for (int j = 0; j < 8; ++j) v[j] = r + j < p.rank ? v[j] * scale : 0.f;
                 if (p.mid) {
                     float* mid = p.mid + static_cast<int64_t>(p.plan.order[piece.first + row]) * p.rank + r;
+                    if (VEC && r < p.rank) {
+                        reinterpret_cast<float4*>(mid)[0] = make_float4(v[0], v[1], v[2], v[3]);
+                        reinterpret_cast<float4*>(mid)[1] = make_float4(v[4], v[5], v[6], v[7]);
+                    } else {
 #pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (r + j < p.rank) mid[j] = v[j];
+                        for (int j = 0; j < 8; ++j)
+                            if (r + j < p.rank) mid[j] = v[j];
+                    }
                 }
             }
             uint32_t part[3][4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j) split3(v[j], part[0][j], part[1][j], part[2][j]);
-            const uint32_t to = ptx::smem_addr(parts()) + (row & 7) * 16 + (row >> 3) * 128 + (r & 4) * 2;
+            for (int j = 0; j < 4; ++j) {
+                uint32_t a[3], b[3];
+                split3(v[2 * j], a[0], a[1], a[2]);
+                split3(v[2 * j + 1], b[0], b[1], b[2]);
+#pragma unroll
+                for (int q = 0; q < 3; ++q) part[q][j] = a[q] | b[q] << 16;
+            }
+            const uint32_t to = ptx::smem_addr(parts()) + (row & 7) * 16 + (row >> 3) * 128;
 #pragma unroll
             for (int q = 0; q < 3; ++q) {
                 const uint32_t dst = to + ((q * s.rp + r) >> 3) * 2048;
-                const uint32_t lo = part[q][0] | part[q][1] << 16, hi = part[q][2] | part[q][3] << 16;
                 if constexpr (S == 1) {
-                    asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(dst), "r"(lo), "r"(hi) : "memory");
+                    ptx::st_shared_v4(dst, part[q][0], part[q][1], part[q][2], part[q][3]);
                 } else {
 #pragma unroll
-                    for (int k = 0; k < S; ++k) ptx::st_cluster_v2(ptx::mapa_shared(dst, k), lo, hi);
+                    for (int k = 0; k < S; ++k) ptx::st_cluster_v4(ptx::mapa_shared(dst, k), part[q][0], part[q][1], part[q][2], part[q][3]);
                 }
             }
         }
         ptx::fence_proxy_async_all();
     }
 
-    // 8 elements of a row from column c on, of which `left` exist.
-    template <typename T>
-    struct Eight {
-        static constexpr int N = sizeof(T) / 2;
-        uint4 u[N];
-        __device__ __forceinline__ void load(const T* row, int left)
-        {
+    // A thread's rows of a tile are every 8th of its warp's 32, their elements of a chunk of 64 columns 8 of the warp's 32.  It holds
+    // ROWS of those rows at a time: 64 bytes of base.
+    static constexpr int ROWS = sizeof(TB) == 2 ? 4 : 2, TURNS = 4 / ROWS, WORDS = 2 * sizeof(TB);
+    struct Held {
+        uint32_t u[ROWS][WORDS];
+    };
+    const TB* base_at[4];
+    TO* out_at[4];
+    __device__ __forceinline__ int row_of(int i) const { return 32 * (warp & 3) + (lane >> 2) + 8 * i; }
+    __device__ __forceinline__ int col_of(int c0) const { return c0 + 32 * (warp >> 2) + 8 * (lane & 3); }
+    __device__ __forceinline__ void make_rows()
+    {
 #pragma unroll
-            for (int i = 0; i < N; ++i) u[i] = make_uint4(0, 0, 0, 0);
-            if (left <= 0) return;
+        for (int i = 0; i < 4; ++i) {
+            const int64_t t = p.plan.order[piece.first + (row_of(i) < piece.rows ? row_of(i) : 0)];
+            base_at[i] = static_cast<const TB*>(p.base) + t * p.base_stride + col_of(0);
+            out_at[i] = static_cast<TO*>(p.out) + t * p.out_stride + col_of(0);
+        }
+    }
+    // Turn `turn` of the chunk at c0.
+    __device__ __forceinline__ void load_base(Held& b, int turn, int c0) const
+    {
+#pragma unroll
+        for (int k = 0; k < ROWS; ++k) {
+            const int i = turn * ROWS + k;
+            const TB* src = base_at[i] + c0;
+            const int left = p.base && row_of(i) < piece.rows ? p.to - col_of(c0) : 0;
             if constexpr (VEC) {
 #pragma unroll
-                for (int i = 0; i < N; ++i) u[i] = __ldcs(reinterpret_cast<const uint4*>(row) + i);
+                for (int j = 0; j < WORDS; j += 4) {
+                    uint4 q = make_uint4(0, 0, 0, 0);
+                    if (left > 0) q = __ldcs(reinterpret_cast<const uint4*>(src) + j / 4);
+                    b.u[k][j] = q.x, b.u[k][j + 1] = q.y, b.u[k][j + 2] = q.z, b.u[k][j + 3] = q.w;
+                }
             } else {
-                T* v = reinterpret_cast<T*>(u);
+                TB* v = reinterpret_cast<TB*>(b.u[k]);
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    if (i < left) v[i] = row[i];
+                for (int j = 0; j < WORDS; ++j) b.u[k][j] = 0u;
+#pragma unroll
+                for (int j = 0; j < 8; ++j)
+                    if (j < left) v[j] = src[j];
             }
         }
-        __device__ __forceinline__ float at(int i) const
-        {
-            if constexpr (sizeof(T) == 4) return reinterpret_cast<const float*>(u)[i];
-            const uint32_t w = reinterpret_cast<const uint32_t*>(u)[i / 2];
-            return __uint_as_float(i % 2 ? w & 0xffff0000u : w << 16);
-        }
-    };
-    __device__ __forceinline__ static void store8(TO* row, const float (&v)[8], int left)
+    }
+    // out = act(base + sum) for row i: `base` its base, `v` its sums as they come from tensor memory.
+    __device__ __forceinline__ void finish(const uint32_t (&base)[WORDS], float2 (&v)[4], int i, int c0, bool live) const
     {
-        if (left <= 0) return;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 b = sizeof(TB) == 2 ? make_float2(__uint_as_float(base[j] << 16), __uint_as_float(base[j] & 0xffff0000u))
+                                             : make_float2(__uint_as_float(base[2 * j % WORDS]), __uint_as_float(base[(2 * j + 1) % WORDS]));
+            v[j] = mx::add2(v[j], b);
+        }
+        if (p.relu)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = make_float2(v[j].x < 0.f ? 0.f : v[j].x, v[j].y < 0.f ? 0.f : v[j].y);
+        TO* row = out_at[i] + c0;
+        const int left = live && row_of(i) < piece.rows ? p.to - col_of(c0) : 0;
         if constexpr (VEC) {
+            if (left <= 0) return;
             if constexpr (sizeof(TO) == 4) {
-                __stcs(reinterpret_cast<float4*>(row), make_float4(v[0], v[1], v[2], v[3]));
-                __stcs(reinterpret_cast<float4*>(row) + 1, make_float4(v[4], v[5], v[6], v[7]));
+                __stcs(reinterpret_cast<float4*>(row), make_float4(v[0].x, v[0].y, v[1].x, v[1].y));
+                __stcs(reinterpret_cast<float4*>(row) + 1, make_float4(v[2].x, v[2].y, v[3].x, v[3].y));
             } else {
                 uint32_t o[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
-                    o[i] = *reinterpret_cast<const uint32_t*>(&h);
+                for (int j = 0; j < 4; ++j) {
+                    const __nv_bfloat162 h = __floats2bfloat162_rn(v[j].x, v[j].y);
+                    o[j] = *reinterpret_cast<const uint32_t*>(&h);
                 }
                 __stcs(reinterpret_cast<uint4*>(row), make_uint4(o[0], o[1], o[2], o[3]));
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i < left) mx::from_float(row[i], v[i]);
+            for (int j = 0; j < 8; ++j)
+                if (j < left) mx::from_float(row[j], j % 2 ? v[j / 2].y : v[j / 2].x);
         }
-    }
-
-    // A thread's rows of a tile (of its warp's 32 lanes, every 8th) and their elements of a chunk of 64 columns: 8 of the warp's 32.
-    int tokens[4];
-    __device__ __forceinline__ int row_of(int i) const { return 32 * (warp & 3) + (lane >> 2) + 8 * i; }
-    __device__ __forceinline__ int col_of(int c0) const { return c0 + 32 * (warp >> 2) + 8 * (lane & 3); }
-    __device__ __forceinline__ void load_base(Eight<TB> (&b)[4], int c0) const
-    {
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            b[i].load(static_cast<const TB*>(p.base) + tokens[i] * p.base_stride + col_of(c0), p.base && row_of(i) < piece.rows ? p.to - col_of(c0) : 0);
-    }
-    __device__ __forceinline__ void finish(const Eight<TB>& b, float (&v)[8], int i, int c0, bool live) const
-    {
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            v[j] += b.at(j);
-            if (p.relu && v[j] < 0.f) v[j] = 0.f;
-        }
-        store8(static_cast<TO*>(p.out) + tokens[i] * p.out_stride + col_of(c0), v, live && row_of(i) < piece.rows ? p.to - col_of(c0) : 0);
     }
 
     // Rows without an adapter: out = act(base), mid = 0.
@@ -276,15 +346,17 @@ struct Pass {
             for (int i = tid; i < piece.rows * p.rank; i += P_THREADS)
                 p.mid[static_cast<int64_t>(p.plan.order[piece.first + i / p.rank]) * p.rank + i % p.rank] = 0.f;
         if (!p.out || warp >= P_WARPS) return;
-        for (int c = chunk0; c < chunk1; ++c) {
-            Eight<TB> b[4];
-            load_base(b, c * P_COLS);
+        for (int c = chunk0; c < chunk1; ++c)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                float v[8] = {};
-                finish(b[i], v, i, c * P_COLS, true);
+            for (int turn = 0; turn < TURNS; ++turn) {
+                Held b;
+                load_base(b, turn, c * P_COLS);
+#pragma unroll
+                for (int k = 0; k < ROWS; ++k) {
+                    float2 v[4] = {};
+                    finish(b.u[k], v, turn * ROWS + k, c * P_COLS, true);
+                }
             }
-        }
     }
 
     __device__ __forceinline__ void run()
@@ -317,8 +389,7 @@ struct Pass {
         const int chunks = p.out ? (p.to + P_COLS - 1) / P_COLS : 0;
         const int chunk0 = static_cast<int>(static_cast<int64_t>(rank_in) * chunks / p.splits), chunk1 = static_cast<int>(static_cast<int64_t>(rank_in + 1) * chunks / p.splits);
         if (piece.rows > 0) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i) tokens[i] = p.plan.order[piece.first + (row_of(i) < piece.rows ? row_of(i) : 0)];
+            if (warp < P_WARPS) make_rows();
             if (e < p.adapters)
                 with(tmem, d2, chunk0, chunk1);
             else
@@ -338,18 +409,20 @@ struct Pass {
         const int s0 = static_cast<int>(static_cast<int64_t>(rank_in) * steps / p.splits), s1 = static_cast<int>(static_cast<int64_t>(rank_in + 1) * steps / p.splits);
         bool ok = true;
         if (warp < P_WARPS) {
-            const __nv_bfloat16* rows[2];
+            const __nv_bfloat16* rows[4];
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int row = (lane & 7) + 8 * warp + 64 * i;
-                rows[i] = p.in + p.plan.order[piece.first + (row < piece.rows ? row : 0)] * p.in_stride;
+            for (int i = 0; i < 4; ++i) {
+                const int row = (tid >> 3) + 32 * i;
+                rows[i] = p.in + p.plan.order[piece.first + (row < piece.rows ? row : 0)] * p.in_stride + 8 * (tid & 7);
             }
+            if (VEC) make_places();
             for (int f = s0; f < s1; ++f) {
                 const int it = f - s0, at = it % p.stages;
                 if (!wait(&empty[at], (static_cast<uint32_t>(it / p.stages) & 1u) ^ 1u, ok)) break;
                 load_stage(mem + at * s.stage(), f * P_STEP, rows);
                 arrive(&full[at]);
             }
+            clear_pad(w2_buf(0));
             if (chunk0 < chunk1) load_w2(w2_buf(0), chunk0 * P_COLS);
             arrive(&w2_full[0]);
         } else {
@@ -361,11 +434,8 @@ struct Pass {
                 ptx::fence_proxy_async_smem();
                 ptx::tc_fence_after();
                 const uint32_t a = ptx::smem_addr(mem + at * s.stage()), b = a + TILE * P_STEP * 2;
-#pragma unroll
-                for (int k = 0; k < P_STEP / 16; ++k)
-                    ptx::mma_bf16_elect(tmem, ptx::plain_kmajor_desc(a + k * 4096, 2048, 128),
-                                        TRANS ? ptx::plain_mnmajor_desc(b + k * 256, 128, 1024) : ptx::plain_kmajor_desc(b + k * 2 * s.rp * 16, s.rp * 16, 128),
-                                        TRANS ? ptx::idesc_bf16_f32_bmn(TILE, s.rp) : ptx::idesc_bf16_f32(TILE, s.rp), it > 0 || k > 0);
+                ptx::mma_bf16_elect_x4(tmem, ptx::sw128_kmajor_desc(a), TRANS ? ptx::plain_mnmajor_desc(b, 128, W1_COLUMN) : ptx::sw128_kmajor_desc(b),
+                                       32 / 16, (TRANS ? 256 : 32) / 16, TRANS ? ptx::idesc_bf16_f32_bmn(TILE, s.rp) : ptx::idesc_bf16_f32(TILE, s.rp), it > 0);
                 ptx::mma_commit_elect(&empty[at]);
             }
             ptx::mma_commit_elect(done);
@@ -393,6 +463,7 @@ struct Pass {
         else
             __syncthreads();
         if (warp < P_WARPS) {
+            clear_pad(w2_buf(1));
             if (chunk0 + 1 < chunk1) load_w2(w2_buf(1), (chunk0 + 1) * P_COLS);
             arrive(&w2_full[1]);
         }
@@ -421,41 +492,50 @@ struct Pass {
                 ptx::fence_proxy_async_smem();
                 ptx::tc_fence_after();
                 const uint32_t w = ptx::smem_addr(w2_buf(b));
-                for (int q = 0; q < 3; ++q)
-                    for (int k = 0; k < s.rp / 16; ++k)
-                        ptx::mma_bf16_elect(d2 + P_COLS * b, ptx::plain_kmajor_desc(a + ((q * s.rp >> 3) + 2 * k) * 2048, 2048, 128),
-                                            TRANS ? ptx::plain_mnmajor_desc(w + k * 2304, 1152, 144) : ptx::plain_kmajor_desc(w + k * 2304, 1152, 144),
-                                            TRANS ? ptx::idesc_bf16_f32_bmn(TILE, P_COLS) : ptx::idesc_bf16_f32(TILE, P_COLS), q > 0 || k > 0);
+                for (int k = 0; k < s.rp / 16; ++k)  // the three parts of 16 of mid's columns
+                    ptx::mma_bf16_elect_x3(d2 + P_COLS * b, ptx::plain_kmajor_desc(a + k * 4096, 2048, 128),
+                                           TRANS ? ptx::plain_mnmajor_desc(w + k * 2304, 1152, 144) : ptx::plain_kmajor_desc(w + k * 2304, 1152, 144),
+                                           s.rp / 8 * (2048 / 16), TRANS ? ptx::idesc_bf16_f32_bmn(TILE, P_COLS) : ptx::idesc_bf16_f32(TILE, P_COLS), k > 0);
                 ptx::mma_commit_elect(&d_full[b]);
             }
         } else if (n > 0) {
-            Eight<TB> now[4], next[4];
-            load_base(now, chunk0 * P_COLS);
-            for (int j = 0; j < n; ++j) {
-                const int b = j & 1, c0 = (chunk0 + j) * P_COLS;
-                if (j + 1 < n) load_base(next, c0 + P_COLS);
-                wait(&d_full[b], static_cast<uint32_t>(j >> 1) & 1u, ok);
-                __syncwarp();
-                ptx::tc_fence_after();
-                uint32_t v[2][16];
-                const uint32_t at = d2 + P_COLS * b + 32 * (warp >> 2) + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
-                ptx::tmem_ld_16x256b_x4(at, v[0]);
-                ptx::tmem_ld_16x256b_x4(at + (16u << 16), v[1]);
-                if (j + 2 < n) load_w2(w2_buf(b), c0 + 2 * P_COLS);
-                if (j + 2 < n) arrive(&w2_full[b]);
-                ptx::tmem_ld_wait();
-                ptx::tc_fence_before();
-                if (lane == 0) ptx::mbar_arrive(&d_empty[b]);
+            // base a turn ahead, in two sets of registers by turns (a copy between them would wait for what is on its way)
+            Held held[2];
+            load_base(held[0], 0, chunk0 * P_COLS);
+            for (int j0 = 0; j0 < n; j0 += 2 / TURNS)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    float f[8];
+                for (int jj = 0; jj < 2 / TURNS; ++jj) {
+                    const int j = j0 + jj;
+                    if (j >= n) break;
+                    const int b = j & 1, c0 = (chunk0 + j) * P_COLS;
+                    if (TURNS == 2 || j + 1 < n) load_base(held[TURNS == 2 ? 1 : (jj + 1) & 1], TURNS - 1, TURNS == 2 ? c0 : c0 + P_COLS);
+                    wait(&d_full[b], static_cast<uint32_t>(j >> 1) & 1u, ok);
+                    __syncwarp();
+                    ptx::tc_fence_after();
+                    uint32_t v[2][16];
+                    const uint32_t at = d2 + P_COLS * b + 32 * (warp >> 2) + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+                    ptx::tmem_ld_16x256b_x4(at, v[0]);
+                    ptx::tmem_ld_16x256b_x4(at + (16u << 16), v[1]);
+                    if (j + 2 < n) {
+                        load_w2(w2_buf(b), c0 + 2 * P_COLS);
+                        arrive(&w2_full[b]);
+                    }
+                    ptx::tmem_ld_wait();
+                    ptx::tc_fence_before();
+                    if (lane == 0) ptx::mbar_arrive(&d_empty[b]);
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) f[k] = __uint_as_float(v[i >> 1][4 * (k >> 1) + 2 * (i & 1) + (k & 1)]);
-                    finish(now[i], f, i, c0, ok);
+                    for (int turn = 0; turn < TURNS; ++turn) {
+                        if (turn == 1 && j + 1 < n) load_base(held[0], 0, c0 + P_COLS);
+#pragma unroll
+                        for (int k = 0; k < ROWS; ++k) {
+                            const int i = turn * ROWS + k;
+                            float2 f[4];
+#pragma unroll
+                            for (int g = 0; g < 4; ++g) f[g] = make_float2(__uint_as_float(v[i >> 1][4 * g + 2 * (i & 1)]), __uint_as_float(v[i >> 1][4 * g + 2 * (i & 1) + 1]));
+                            finish(held[TURNS == 1 ? jj & 1 : turn].u[k], f, i, c0, ok);
+                        }
+                    }
                 }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) now[i] = next[i];
-            }
         }
         __syncwarp();
         ptx::cp_async_wait_all();

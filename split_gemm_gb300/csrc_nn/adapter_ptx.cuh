@@ -23,15 +23,56 @@ __device__ __forceinline__ void tmem_ld_16x256b_x4(uint32_t taddr, uint32_t (&v)
 // the 8 indices 16 B apart; `sbo` is the distance of core matrices adjacent along M/N and `lbo` along the reduction.
 __device__ __forceinline__ uint64_t plain_mnmajor_desc(uint32_t saddr, uint32_t lbo, uint32_t sbo) { return plain_kmajor_desc(saddr, lbo, sbo); }
 
-// One MMA from one elected lane of a warp in uniform control flow.
-__device__ __forceinline__ void mma_bf16_elect(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint32_t idesc, uint32_t accumulate)
+// Four MMAs in turn into the same accumulator from one elected lane of a warp in uniform control flow, the descriptors `a_step` and
+// `b_step` (16-byte units) apart; the first accumulates when `accumulate` is nonzero, the others always.  In one block, so that the election and the
+// operands' moves to uniform registers are paid once: alone, an MMA costs its warp some 100 clocks, three times what a 128 x 64 x 16 takes.
+__device__ __forceinline__ void mma_bf16_elect_x4(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint64_t a_step, uint64_t b_step, uint32_t idesc,
+                                                  uint32_t accumulate)
 {
     asm volatile(
-        "{\n\t.reg .pred p, e;\n\t"
-        "setp.ne.b32 p, %4, 0;\n\t"
+        "{\n\t.reg .pred p, e, t;\n\t.reg .b64 a1, a2, a3, b1, b2, b3;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "setp.eq.b32 t, 0, 0;\n\t"
+        "add.s64 a1, %1, %3;\n\tadd.s64 a2, a1, %3;\n\tadd.s64 a3, a2, %3;\n\t"
+        "add.s64 b1, %2, %4;\n\tadd.s64 b2, b1, %4;\n\tadd.s64 b3, b2, %4;\n\t"
         "elect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %5, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %5, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, b2, %5, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b3, %5, t;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "l"(a_step), "l"(b_step), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// The same for two MMAs.
+__device__ __forceinline__ void mma_bf16_elect_x2(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint64_t a_step, uint64_t b_step, uint32_t idesc,
+                                                  uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, e, t;\n\t.reg .b64 a1, b1;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
+        "setp.eq.b32 t, 0, 0;\n\t"
+        "add.s64 a1, %1, %3;\n\tadd.s64 b1, %2, %4;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %5, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, b1, %5, t;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "l"(a_step), "l"(b_step), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// The same for three MMAs with one B: A's descriptors `a_step` apart.
+__device__ __forceinline__ void mma_bf16_elect_x3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint64_t a_step, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, e, t;\n\t.reg .b64 a1, a2;\n\t"
+        "setp.ne.b32 p, %5, 0;\n\t"
+        "setp.eq.b32 t, 0, 0;\n\t"
+        "add.s64 a1, %1, %3;\n\tadd.s64 a2, a1, %3;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %4, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, %2, %4, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, %2, %4, t;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "l"(a_step), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 
@@ -49,9 +90,9 @@ __device__ __forceinline__ void cp_async_16s(uint32_t dst, const void* src, uint
 // Orders this thread's generic-proxy writes, to any CTA's shared memory, before later async-proxy accesses.
 __device__ __forceinline__ void fence_proxy_async_all() { asm volatile("fence.proxy.async;" ::: "memory"); }
 
-__device__ __forceinline__ void st_cluster_v2(uint32_t cluster_addr, uint32_t a, uint32_t b)
+__device__ __forceinline__ void st_cluster_v4(uint32_t cluster_addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
 {
-    asm volatile("st.shared::cluster.v2.b32 [%0], {%1, %2};" ::"r"(cluster_addr), "r"(a), "r"(b) : "memory");
+    asm volatile("st.shared::cluster.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(cluster_addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
 }  // namespace ptx

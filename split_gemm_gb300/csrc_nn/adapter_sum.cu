@@ -319,17 +319,17 @@ struct Sum {
             ptx::fence_proxy_async_smem();
             ptx::tc_fence_after();
             const uint32_t a = ptx::smem_addr(mem + at * s.stage()), b = a + s.in_bytes();
-            const int narrow = 3 * s.rp <= 256;
-            for (int m = 0; m < s.blocks; ++m)
-                for (int q = 0; q < s.tokens / 16; ++q) {
-                    const uint64_t ad = ptx::plain_mnmajor_desc(a + 16 * m * s.column() + q * 256, 128, s.column());
-                    const uint32_t d = tmem + 3 * m * s.rp;
-                    const uint32_t acc = !begins || q > 0;
-                    ptx::mma_bf16_elect(d, ad, ptx::plain_mnmajor_desc(b + q * 256, 128, s.column()), ptx::idesc_bf16_f32_mn(128, narrow ? 3 * s.rp : 2 * s.rp), acc);
-                    if (!narrow)
-                        ptx::mma_bf16_elect(d + 2 * s.rp, ad, ptx::plain_mnmajor_desc(b + (s.rp >> 2) * s.column() + q * 256, 128, s.column()),
-                                            ptx::idesc_bf16_f32_mn(128, s.rp), acc);
+            const uint64_t bd = ptx::plain_mnmajor_desc(b, 128, s.column());
+            for (int m = 0; m < s.blocks; ++m) {
+                const uint64_t ad = ptx::plain_mnmajor_desc(a + 16 * m * s.column(), 128, s.column());
+                const uint32_t d = tmem + 3 * m * s.rp;
+                if (s.tokens == 64) {  // rank 64 and below: all three parts in one
+                    ptx::mma_bf16_elect_x4(d, ad, bd, 256 / 16, 256 / 16, ptx::idesc_bf16_f32_mn(128, 3 * s.rp), !begins);
+                } else {
+                    ptx::mma_bf16_elect_x2(d, ad, bd, 256 / 16, 256 / 16, ptx::idesc_bf16_f32_mn(128, 2 * s.rp), !begins);
+                    ptx::mma_bf16_elect_x2(d + 2 * s.rp, ad, bd + (s.rp >> 2) * s.column() / 16, 256 / 16, 256 / 16, ptx::idesc_bf16_f32_mn(128, s.rp), !begins);
                 }
+            }
             ptx::mma_commit_elect(&empty[at]);
             if (ends_run(k)) {
                 ptx::mma_commit_elect(done);
