@@ -18,25 +18,36 @@ std::mutex asking;
 
 constexpr int64_t MOST_COLS = int64_t(1) << 30;
 
-// The number of CTAs that share a tile and of stages in their rings.
-void shape_pass(PassParams& p, int64_t rows)
-{
-    // two CTAs to an SM where two stages of the ring fit, else one
-    int per_sm = 2;
-    p.stages = 2;
-    int room = 113 * 1024;
-    if (PassSmem(p.rank, 2).bytes() > room) {
-        per_sm = 1;
-        room = 227 * 1024;
-    }
-    while (p.stages < P_MOST_STAGES && PassSmem(p.rank, p.stages + 1).bytes() <= room) ++p.stages;
-    const int64_t tiles = mx::cdiv<int64_t>(rows, TILE);
-    const int steps = mx::cdiv(p.from, P_STEP);
-    p.splits = 1;
-    while (p.splits < 8 && tiles * p.splits < mx::SMS * per_sm && 2 * p.splits <= steps) p.splits *= 2;
-}
-
 size_t size_of(int32_t t) { return t == CONV2D_OUT_BF16 ? 2 : 4; }
+
+// How a pass is cut up: tiles of 128 or 64 rows, and the CTAs that share one, one CTA to an SM.  A CTA costs some 3 us beside its rows, 3 more where sums
+// are joined over a cluster, and takes its bytes at 60 a ns at best and at its share of HBM's 6600; weights come from L2.
+bool shape_pass(PassParams& p, int64_t rows, int base_bytes, int out_bytes)
+{
+    bool halved = false;
+    double best = 1e30;
+    const int64_t groups = p.adapters + 1 < rows ? p.adapters + 1 : rows;
+    for (int h = 0; h < 2; ++h)
+        for (int splits = 1; splits <= 8; splits *= 2) {
+            if (splits > 1 && splits * P_STEP > p.from) break;
+            const int tile = TILE >> h;
+            const int64_t ctas = (rows / tile + (groups + 1) / 2) * splits;
+            const double held = splits == 8 ? 120.0 : splits == 4 ? 144.0 : 152.0;  // CTAs of clusters that the SMs hold at once
+            const double waves = static_cast<double>(mx::cdiv<int64_t>(ctas, static_cast<int64_t>(held)));
+            const double on = static_cast<double>(ctas) < held ? static_cast<double>(ctas) : held;
+            const double bytes = tile * (2.0 * p.from + static_cast<double>(base_bytes + out_bytes) * p.to) / splits;
+            const double weights = 2.0 * p.rank * (static_cast<double>(p.from) + p.to) / splits;
+            const double rate = 6600.0 / on < 60.0 ? 6600.0 / on : 60.0;
+            const double own = (bytes + weights) / 60.0 / 1000.0, hbm = bytes / rate / 1000.0;
+            const double us = waves * (3.0 + (splits > 1 ? 3.0 : 0.0) + (own > hbm ? own : hbm));
+            if (us < best) {
+                best = us;
+                halved = h;
+                p.splits = splits;
+            }
+        }
+    return halved;
+}
 
 bool vectors(const void* p, int64_t stride, size_t elem) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride * elem % 16 == 0; }
 
@@ -107,8 +118,8 @@ extern "C" int adapter_fwd(const adapter_fwd_params* params, const void* plan_de
     p.from = static_cast<int>(q.cols);
     p.to = static_cast<int>(q.outs);
     p.relu = q.activation == CONV2D_ACT_RELU;
-    ad::shape_pass(p, q.rows);
-    return ad::launch_pass_fwd(p, q.y_dtype, q.out_dtype, ad::in_vectors(p, q.y_dtype, q.out_dtype), stream);
+    const bool halved = ad::shape_pass(p, q.rows, static_cast<int>(ad::size_of(q.y_dtype)), static_cast<int>(ad::size_of(q.out_dtype)));
+    return ad::launch_pass_fwd(p, q.y_dtype, q.out_dtype, ad::in_vectors(p, q.y_dtype, q.out_dtype), halved, stream);
 }
 
 extern "C" size_t adapter_bwd_workspace_bytes(const adapter_bwd_params* params)
@@ -166,9 +177,9 @@ extern "C" int adapter_bwd(const adapter_bwd_params* params, const void* plan_de
     p.from = static_cast<int>(q.outs);
     p.to = static_cast<int>(q.cols);
     if (!ad::status_word(&p.status)) return CONV2D_ERR_CUDA;
-    ad::shape_pass(p, q.rows);
+    const bool halved = ad::shape_pass(p, q.rows, dx0_dev ? static_cast<int>(ad::size_of(q.dx0_dtype)) : 0, dx_dev ? static_cast<int>(ad::size_of(q.dx_dtype)) : 0);
     if (dx_dev || da_dev)
-        if (int rc = ad::launch_pass_bwd(p, q.dx0_dtype, q.dx_dtype, ad::in_vectors(p, q.dx0_dtype, q.dx_dtype), stream)) return rc;
+        if (int rc = ad::launch_pass_bwd(p, q.dx0_dtype, q.dx_dtype, ad::in_vectors(p, q.dx0_dtype, q.dx_dtype), halved, stream)) return rc;
     ad::SumParams s{};
     s.plan = p.plan;
     s.status = p.status;

@@ -21,30 +21,41 @@ struct PassParams {
     int64_t in_stride, base_stride, out_stride;
     int adapters, rank, from, to;
     int relu;
-    int splits, stages;  // CTAs of a cluster, stages of the ring
+    int splits;  // CTAs of a cluster
 };
 
 constexpr int P_STEP = 64;  // of `from`, in a stage
-constexpr int P_COLS = 64;  // of `to`, in a chunk
-constexpr int P_MOST_STAGES = 6;
+constexpr int P_MOST_STAGES = 6, P_MOST_CHUNKS = 8;
+constexpr int P_ROOM = 227 * 1024;  // bytes of shared memory
 
 // Bytes between the 16-byte columns of an MN-major stage of w1: 16 more than they need, so that neighbours fall into different banks.
 constexpr int W1_COLUMN = P_STEP * 16 + 16;
 
-// Shared memory by the rank padded to 16.  A chunk of w2: core matrices 144 bytes apart along the columns, so that the pairs that the
-// backward pass places one by one fall into different banks.
+// Shared memory by the rank padded to 16 and the halving of tiles: an area that holds the first product's ring and, when that is over, the
+// sums (from its start), mid's parts (to its end) and w2's chunks (downwards from the parts; over the sums, once those are joined); beside it w2's first
+// chunk, barriers and lists.  A chunk of w2: core matrices 144 bytes apart along the columns, so that the pairs that the backward
+// pass places one by one fall into different banks.
 struct PassSmem {
-    int rp, stages;
-    __host__ __device__ constexpr PassSmem(int rank, int stages) : rp((rank + 15) / 16 * 16), stages(stages) {}
+    int rp, cols;  // cols: of `to`, in a chunk
+    __host__ __device__ constexpr PassSmem(int rank, int halved) : rp((rank + 15) / 16 * 16), cols(64 << halved) {}
     __host__ __device__ constexpr int stage() const { return TILE * P_STEP * 2 + (rp / 8 * W1_COLUMN + 1023) / 1024 * 1024; }
-    __host__ __device__ constexpr int pitch() const { return rp + 4; }                     // of the joined sums' rows, in words
+    __host__ __device__ constexpr int column() const { return cols / 8 * 144; }  // of a chunk: 8 ranks
+    __host__ __device__ constexpr int chunk() const { return rp / 8 * column(); }
+    __host__ __device__ constexpr int rest() const { return 512 + TILE * 4; }
+    __host__ __device__ constexpr int area() const { return (P_ROOM - chunk() - rest()) / 128 * 128; }
+    __host__ __device__ constexpr int stages() const { return area() / stage() < P_MOST_STAGES ? area() / stage() : P_MOST_STAGES; }
+    __host__ __device__ constexpr int pitch() const { return rp + 4; }  // of the sums' rows, in words
     __host__ __device__ constexpr int sums() const { return TILE * pitch() * 4; }
-    __host__ __device__ constexpr int chunk() const { return rp / 8 * 1152; }
-    // the ring; after it the sums and w2's second buffer
-    __host__ __device__ constexpr int ring() const { return stages * stage() > sums() + chunk() ? stages * stage() : sums() + chunk(); }
-    __host__ __device__ constexpr int parts() const { return TILE * 3 * rp * 2; }
-    __host__ __device__ constexpr int bytes() const { return ring() + parts() + chunk() + 256; }
+    __host__ __device__ constexpr int group() const { return 3 * rp / 8 * 128; }  // of parts: 8 rows
+    __host__ __device__ constexpr int parts() const { return TILE / 8 * group(); }
+    __host__ __device__ constexpr int chunks() const { return 1 + (area() - parts()) / chunk() < P_MOST_CHUNKS ? 1 + (area() - parts()) / chunk() : P_MOST_CHUNKS; }
+    __host__ __device__ constexpr int early_chunks() const  // that do not lie over the sums
+    {
+        const int n = 1 + (area() - parts() - sums()) / chunk();
+        return n < chunks() ? n : chunks();
+    }
 };
+static_assert(PassSmem(128, 1).area() >= PassSmem(128, 1).parts() + PassSmem(128, 1).sums() && PassSmem(128, 1).chunks() >= 3, "the widest rank fits");
 
 // Sums over the adapters' rows: out[e] (r, c) = sum of mid[t][r] * in[t][c].
 struct SumJob {
@@ -72,8 +83,9 @@ int sum_tiles_each(int64_t rows, int64_t adapters, int rank, int64_t cols, int64
 int64_t sum_pieces(const PlanLayout& l, int tiles_each);
 int launch_sums(SumParams& p, int64_t pieces, cudaStream_t stream);
 
-int launch_pass_fwd(const PassParams& p, int32_t base_dtype, int32_t out_dtype, bool vec, cudaStream_t stream);
-int launch_pass_bwd(const PassParams& p, int32_t base_dtype, int32_t out_dtype, bool vec, cudaStream_t stream);
+// halved: tiles of 64 rows, not 128.
+int launch_pass_fwd(const PassParams& p, int32_t base_dtype, int32_t out_dtype, bool vec, bool halved, cudaStream_t stream);
+int launch_pass_bwd(const PassParams& p, int32_t base_dtype, int32_t out_dtype, bool vec, bool halved, cudaStream_t stream);
 
 }  // namespace ad
 }  // namespace sgb

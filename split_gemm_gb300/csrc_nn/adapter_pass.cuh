@@ -26,35 +26,48 @@
 namespace sgb {
 namespace ad {
 
-constexpr int P_WARPS = 8, P_LOADERS = 32 * P_WARPS, P_THREADS = P_LOADERS + 32;
+constexpr int P_WARPS = 16, P_LOADERS = 32 * P_WARPS, P_THREADS = P_LOADERS + 32;
+constexpr int P_GROUP = P_LOADERS / 2;  // threads that finish a chunk
 constexpr uint64_t P_WAIT_NS = 1000000000ull;
-constexpr uint32_t P_TMEM = 256;  // rank and two chunks
+constexpr uint32_t P_TMEM = 512;  // four chunks of up to 128 columns; the first product's sums before them
 
-template <bool TRANS, bool VEC, typename TB, typename TO>
+template <bool TRANS, bool VEC, int HALVED, typename TB, typename TO>
 struct Pass {
+    static constexpr int ROWS = TILE >> HALVED, COLS = 64 << HALVED;  // of a tile; of `to`, in a chunk
+    static constexpr int LANES = 32 >> HALVED;                        // of a warp's 32 lanes of tensor memory that hold rows
+
     const PassParams& p;
     const PassSmem s;
     uint8_t* mem;
-    uint64_t *full, *empty, *done, *w2_full, *d_full, *d_empty;
+    uint64_t *full, *empty, *done, *w2_full, *d_full, *d_empty, *parts_full;
+    int* ids;  // numbers of the tile's rows
     uint32_t* slot;
     volatile uint32_t* abort_flag;
-    int tid, warp, lane, rank_in, e;
+    int tid, warp, lane, rank_in, e, n_stages, n_bufs;
+    int group, gtid;  // of two that finish chunks by turns, and the thread of it
+
     Piece piece;
 
-    __device__ __forceinline__ Pass(const PassParams& p, uint8_t* raw) : p(p), s(p.rank, p.stages), mem(raw)
+    __device__ __forceinline__ Pass(const PassParams& p, uint8_t* raw) : p(p), s(p.rank, HALVED), mem(raw)
     {
-        full = reinterpret_cast<uint64_t*>(raw + s.ring() + s.parts() + s.chunk());
+        n_stages = s.stages();
+        n_bufs = s.chunks();
+        full = reinterpret_cast<uint64_t*>(raw + s.area() + s.chunk());
         empty = full + P_MOST_STAGES;
         done = empty + P_MOST_STAGES;
         w2_full = done + 1;
-        d_full = w2_full + 2;
-        d_empty = d_full + 2;
-        slot = reinterpret_cast<uint32_t*>(d_empty + 2);
+        d_full = w2_full + P_MOST_CHUNKS;
+        d_empty = d_full + 4;
+        parts_full = d_empty + 4;
+        ids = reinterpret_cast<int*>(parts_full + 1);
+        slot = reinterpret_cast<uint32_t*>(ids + TILE);
         abort_flag = slot + 1;
         tid = threadIdx.x;
         warp = tid >> 5;
         lane = tid & 31;
         rank_in = blockIdx.x % p.splits;
+        group = warp >> 3;
+        gtid = tid & (P_GROUP - 1);
     }
     __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, bool& ok) const
     {
@@ -64,8 +77,8 @@ struct Pass {
         }
         return ok;
     }
-    __device__ __forceinline__ uint8_t* parts() const { return mem + s.ring(); }
-    __device__ __forceinline__ uint8_t* w2_buf(int i) const { return i ? mem + s.sums() : mem + s.ring() + s.parts(); }
+    __device__ __forceinline__ uint8_t* parts() const { return mem + s.area() - s.parts(); }
+    __device__ __forceinline__ uint8_t* w2_buf(int i) const { return i ? parts() - i * s.chunk() : mem + s.area(); }
 
     // 16 bytes of row elements from `src`, `valid` elements of them; aligned copies run by themselves, others go through registers.
     __device__ __forceinline__ void copy8(uint32_t dst, const __nv_bfloat16* src, int valid) const
@@ -89,53 +102,54 @@ struct Pass {
         }
     }
 
+    // The accumulator's lane of row i: a halved tile has 16 rows in each warp's 32 lanes, so that all warps finish chunks.
+    __device__ __forceinline__ static int lane_of(int i) { return HALVED ? (i >> 4) * 32 + (i & 15) : i; }
+
     // Where a loader's copies of an MN-major w1 or a K-major w2 go: 64 rows of rank/8 16-byte columns, one after another in memory.
     // (Addresses are kept in registers: computed for each copy they cost the loaders more time than the copies.)
-    uint32_t place[4];
+    static constexpr int PLACES = 64 * MOST_RANK / 8 / (TRANS ? P_LOADERS : P_GROUP);
+    uint32_t place[PLACES];
     __device__ __forceinline__ void make_places()
     {
         const int per = p.rank >> 3;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const int i = tid + P_LOADERS * j, row = i / per, c8 = i - row * per;
+        for (int j = 0; j < PLACES; ++j) {
+            const int i = TRANS ? tid + P_LOADERS * j : gtid + P_GROUP * j, row = i / per, c8 = i - row * per;
             const int n = (row & 32) + 8 * ((row >> 1) & 3) + 2 * ((row >> 3) & 3) + (row & 1);  // of w2, as below
-            place[j] = row >= 64 ? 0xffffffffu : TRANS ? (row & 7) * 16 + (row >> 3) * 128 + c8 * W1_COLUMN : (n & 7) * 16 + (n >> 3) * 144 + c8 * 1152;
+            place[j] = row >= 64 ? 0xffffffffu : TRANS ? (row & 7) * 16 + (row >> 3) * 128 + c8 * W1_COLUMN : (n & 7) * 16 + (n >> 3) * 144 + c8 * s.column();
         }
     }
 
-    // Columns f0 .. f0+63 of the tile's rows and of w1.  rows: at this thread's 16-byte column of every 32nd row.
-    __device__ __forceinline__ void load_stage(uint8_t* st, int f0, const __nv_bfloat16* const (&rows)[4]) const
+    // Columns f0 .. f0+63 of the tile's rows and of w1.  rows: at this thread's 16-byte column of every 64th row.
+    __device__ __forceinline__ void load_stage(uint8_t* st, int f0, const __nv_bfloat16* const (&rows)[ROWS / 64]) const
     {
         const uint32_t at = ptx::smem_addr(st), w_at = at + TILE * P_STEP * 2;
         const int64_t size = static_cast<int64_t>(p.rank) * p.from;
         const __nv_bfloat16* w = p.w1 + e * size;
-        const int row = tid >> 3, c8 = tid & 7;
-        const uint32_t mine = row * 128 + ((c8 ^ (row & 7)) << 4);  // 128-byte swizzle
+        const int row = tid >> 3, c8 = tid & 7, l = lane_of(row);
+        const uint32_t swizzled = (c8 ^ (row & 7)) << 4, mine = l * 128 + swizzled;  // 128-byte swizzle
         if (VEC && f0 + P_STEP <= p.from) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                if (row + 32 * i < piece.rows) ptx::cp_async_16s(at + mine + 4096 * i, rows[i] + f0, 16);
+            for (int i = 0; i < ROWS / 64; ++i)
+                if (row + 64 * i < piece.rows) ptx::cp_async_16s(at + mine + 8192 * i, rows[i] + f0, 16);
             if constexpr (!TRANS) {
                 const __nv_bfloat16* src = w + static_cast<int64_t>(row) * p.from + f0 + 8 * c8;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (row + 32 * i < p.rank) ptx::cp_async_16s(w_at + mine + 4096 * i, src, 16);
-                    src += 32 * static_cast<int64_t>(p.from);
-                }
+                if (row < p.rank) ptx::cp_async_16s(w_at + row * 128 + swizzled, src, 16);
+                if (row + 64 < p.rank) ptx::cp_async_16s(w_at + row * 128 + swizzled + 8192, src + 64 * static_cast<int64_t>(p.from), 16);
             } else {
                 const __nv_bfloat16* src = w + static_cast<int64_t>(f0) * p.rank + 8 * tid;
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
+                for (int i = 0; i < PLACES; ++i)
                     if (place[i] != 0xffffffffu) ptx::cp_async_16s(w_at + place[i], src + 8 * P_LOADERS * i, 16);
             }
             return;
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (row + 32 * i < piece.rows) copy8(at + mine + 4096 * i, rows[i] + f0, p.from - f0 - 8 * c8);
+        for (int i = 0; i < ROWS / 64; ++i)
+            if (row + 64 * i < piece.rows) copy8(at + mine + 8192 * i, rows[i] + f0, p.from - f0 - 8 * c8);
         if constexpr (!TRANS) {
-            for (int r = row; r < p.rank; r += 32)
-                copy8(w_at + r * 128 + ((c8 ^ (r & 7)) << 4), w + static_cast<int64_t>(r) * p.from + f0 + 8 * c8, p.from - f0 - 8 * c8);
+            for (int r = row; r < p.rank; r += 64)
+                copy8(w_at + r * 128 + swizzled, w + static_cast<int64_t>(r) * p.from + f0 + 8 * c8, p.from - f0 - 8 * c8);
         } else {
             for (int i = tid; i < s.rp * 8; i += P_LOADERS) {  // 64 rows of rp/8 16-byte columns
                 const int k = (i >> 1) & 63, n8 = 2 * (i >> 7) + (i & 1);
@@ -145,43 +159,44 @@ struct Pass {
         }
     }
 
-    // w2's 64 columns from c0 on: column c of 32 becomes row 8((c>>1)&3) + 2(c>>3) + (c&1) of the operand.
+    // w2's columns of a chunk from c0 on, by a group: column c of 32 becomes row 8((c>>1)&3) + 2(c>>3) + (c&1) of the operand.
     __device__ __forceinline__ void load_w2(uint8_t* buf, int c0) const
     {
-        const uint32_t at = ptx::smem_addr(buf);
         const int64_t size = static_cast<int64_t>(p.rank) * p.to;
         const __nv_bfloat16* w = p.w2 + e * size;
-        if (VEC && c0 + P_COLS <= p.to) {
-            if constexpr (!TRANS) {
-                const __nv_bfloat16* src = w + static_cast<int64_t>(c0) * p.rank + 8 * tid;
+        uint32_t at = ptx::smem_addr(buf);
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (place[i] != 0xffffffffu) ptx::cp_async_16s(at + place[i], src + 8 * P_LOADERS * i, 16);
-            } else {
-                const int c = 2 * lane;
-                uint32_t dst = at + warp * 16 + ((c >> 3) & 3) * 4 + (((c >> 1) & 3) + 4 * (c >> 5)) * 144;
-                const __nv_bfloat16* src = w + static_cast<int64_t>(warp) * p.to + c0 + c;
-                for (int k = warp; k < p.rank; k += 8, dst += 1152, src += 8 * static_cast<int64_t>(p.to)) ptx::cp_async_4(dst, src, 4);
-            }
-            return;
-        }
-        if constexpr (!TRANS) {
-            for (int i = tid; i < s.rp * 8; i += P_LOADERS) {
-                const int n = (i >> 1) & 63, k8 = 2 * (i >> 7) + (i & 1);
-                const int c = c0 + (n & 32) + 8 * ((n >> 1) & 3) + 2 * ((n >> 3) & 3) + (n & 1);
-                copy8(at + (n & 7) * 16 + (n >> 3) * 144 + k8 * 1152, w + static_cast<int64_t>(c) * p.rank + 8 * k8, c < p.to ? p.rank - 8 * k8 : 0);
-            }
-        } else {
-            for (int i = tid; i < s.rp * 32; i += P_LOADERS) {
-                const int k = i >> 5, c = 2 * (i & 31);
-                const uint32_t dst = at + (k & 7) * 16 + ((c >> 3) & 3) * 4 + (((c >> 1) & 3) + 4 * (c >> 5)) * 144 + (k >> 3) * 1152;
-                const __nv_bfloat16* src = w + static_cast<int64_t>(k) * p.to + c0 + c;
-                const int left = k < p.rank ? p.to - c0 - c : 0;
-                if constexpr (VEC) {
-                    ptx::cp_async_4(dst, left > 0 ? src : p.w1, left > 0 ? 4 : 0);
+        for (int half = 0; half < COLS / 64; ++half, at += 8 * 144, c0 += 64) {
+            if (VEC && c0 + 64 <= p.to) {
+                if constexpr (!TRANS) {
+                    const __nv_bfloat16* src = w + static_cast<int64_t>(c0) * p.rank + 8 * gtid;
+#pragma unroll
+                    for (int i = 0; i < PLACES; ++i)
+                        if (place[i] != 0xffffffffu) ptx::cp_async_16s(at + place[i], src + 8 * P_GROUP * i, 16);
                 } else {
-                    const uint32_t lo = left > 0 ? __bfloat16_as_ushort(__ldg(src)) : 0u, hi = left > 1 ? __bfloat16_as_ushort(__ldg(src + 1)) : 0u;
-                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(lo | hi << 16) : "memory");
+                    const int c = 2 * lane, gwarp = warp & 7;
+                    uint32_t dst = at + gwarp * 16 + ((c >> 3) & 3) * 4 + (((c >> 1) & 3) + 4 * (c >> 5)) * 144;
+                    const __nv_bfloat16* src = w + static_cast<int64_t>(gwarp) * p.to + c0 + c;
+                    for (int k = gwarp; k < p.rank; k += 8, dst += s.column(), src += 8 * static_cast<int64_t>(p.to)) ptx::cp_async_4(dst, src, 4);
+                }
+            } else if constexpr (!TRANS) {
+                for (int i = gtid; i < s.rp * 8; i += P_GROUP) {
+                    const int n = (i >> 1) & 63, k8 = 2 * (i >> 7) + (i & 1);
+                    const int c = c0 + (n & 32) + 8 * ((n >> 1) & 3) + 2 * ((n >> 3) & 3) + (n & 1);
+                    copy8(at + (n & 7) * 16 + (n >> 3) * 144 + k8 * s.column(), w + static_cast<int64_t>(c) * p.rank + 8 * k8, c < p.to ? p.rank - 8 * k8 : 0);
+                }
+            } else {
+                for (int i = gtid; i < s.rp * 32; i += P_GROUP) {
+                    const int k = i >> 5, c = 2 * (i & 31);
+                    const uint32_t dst = at + (k & 7) * 16 + ((c >> 3) & 3) * 4 + (((c >> 1) & 3) + 4 * (c >> 5)) * 144 + (k >> 3) * s.column();
+                    const __nv_bfloat16* src = w + static_cast<int64_t>(k) * p.to + c0 + c;
+                    const int left = k < p.rank ? p.to - c0 - c : 0;
+                    if constexpr (VEC) {
+                        ptx::cp_async_4(dst, left > 0 ? src : p.w1, left > 0 ? 4 : 0);
+                    } else {
+                        const uint32_t lo = left > 0 ? __bfloat16_as_ushort(__ldg(src)) : 0u, hi = left > 1 ? __bfloat16_as_ushort(__ldg(src + 1)) : 0u;
+                        asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(lo | hi << 16) : "memory");
+                    }
                 }
             }
         }
@@ -189,43 +204,45 @@ struct Pass {
     // The part of a chunk of w2 that pads an odd number of 8 ranks; whole copies do not reach it.
     __device__ __forceinline__ void clear_pad(uint8_t* buf) const
     {
-        if (VEC && (p.rank & 8) && tid < 64) ptx::st_shared_v4(ptx::smem_addr(buf) + (tid & 7) * 16 + (tid >> 3) * 144 + (p.rank >> 3) * 1152, 0u, 0u, 0u, 0u);
+        if (VEC && (p.rank & 8) && gtid < COLS)
+            ptx::st_shared_v4(ptx::smem_addr(buf) + (gtid & 7) * 16 + (gtid >> 3) * 144 + (p.rank >> 3) * s.column(), 0u, 0u, 0u, 0u);
         if (VEC) ptx::fence_proxy_async_smem();
     }
 
-    // This CTA's rows of the sums over the cluster: scaled, to mid, and in three parts to every CTA.
+    // This CTA's rows of the sums over the cluster: scaled, to mid, in three parts, and on to every CTA.
     template <int S>
     __device__ __forceinline__ void join(const float* sums, float scale) const
     {
-        constexpr int SHARE = TILE / S;
+        constexpr int SHARE = ROWS / S;
         const int eighths = s.rp >> 3;
-        for (int i = tid; i < SHARE * eighths; i += P_THREADS) {
-            const int row = rank_in * SHARE + i % SHARE, r = 8 * (i / SHARE);
+        for (int i = tid; i < SHARE * eighths; i += P_THREADS) {  // neighbouring lanes read neighbouring parts of a row
+            const int own = i / eighths, row = rank_in * SHARE + own, r = 8 * (i - own * eighths);
             const float* at = sums + row * s.pitch() + r;
             float v[8] = {};
             if (row < piece.rows) {
+                float4 u[S][2];
 #pragma unroll
-                for (int h = 0; h < 8; h += 4) {
-                    float4 u[S];
+                for (int k = 0; k < S; ++k)
 #pragma unroll
-                    for (int k = 0; k < S; ++k) {
+                    for (int h = 0; h < 2; ++h) {
                         if constexpr (S == 1)
-                            u[k] = *reinterpret_cast<const float4*>(at + h);
+                            u[k][h] = reinterpret_cast<const float4*>(at)[h];
                         else
-                            u[k] = ptx::ld_cluster_v4(ptx::mapa_shared(ptx::smem_addr(at + h), k));
+                            u[k][h] = ptx::ld_cluster_v4(ptx::mapa_shared(ptx::smem_addr(at + 4 * h), k));
                     }
 #pragma unroll
-                    for (int k = 0; k < S; ++k) {
-                        v[h] += u[k].x;
-                        v[h + 1] += u[k].y;
-                        v[h + 2] += u[k].z;
-                        v[h + 3] += u[k].w;
+                for (int k = 0; k < S; ++k)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        v[4 * h] += u[k][h].x;
+                        v[4 * h + 1] += u[k][h].y;
+                        v[4 * h + 2] += u[k][h].z;
+                        v[4 * h + 3] += u[k][h].w;
                     }
-                }
 #pragma unroll
                 for (int j = 0; j < 8; ++j) v[j] = r + j < p.rank ? v[j] * scale : 0.f;
                 if (p.mid) {
-                    float* mid = p.mid + static_cast<int64_t>(p.plan.order[piece.first + row]) * p.rank + r;
+                    float* mid = p.mid + static_cast<int64_t>(ids[row]) * p.rank + r;
                     if (VEC && r < p.rank) {
                         reinterpret_cast<float4*>(mid)[0] = make_float4(v[0], v[1], v[2], v[3]);
                         reinterpret_cast<float4*>(mid)[1] = make_float4(v[4], v[5], v[6], v[7]);
@@ -245,48 +262,50 @@ struct Pass {
 #pragma unroll
                 for (int q = 0; q < 3; ++q) part[q][j] = a[q] | b[q] << 16;
             }
-            const uint32_t to = ptx::smem_addr(parts()) + (row & 7) * 16 + (row >> 3) * 128;
+            const uint32_t to = ptx::smem_addr(parts()) + (row & 7) * 16 + (lane_of(row) >> 3) * s.group();
 #pragma unroll
-            for (int q = 0; q < 3; ++q) {
-                const uint32_t dst = to + ((q * s.rp + r) >> 3) * 2048;
-                if constexpr (S == 1) {
-                    ptx::st_shared_v4(dst, part[q][0], part[q][1], part[q][2], part[q][3]);
-                } else {
-#pragma unroll
-                    for (int k = 0; k < S; ++k) ptx::st_cluster_v4(ptx::mapa_shared(dst, k), part[q][0], part[q][1], part[q][2], part[q][3]);
-                }
-            }
+            for (int q = 0; q < 3; ++q) ptx::st_shared_v4(to + ((q * s.rp + r) >> 3) * 128, part[q][0], part[q][1], part[q][2], part[q][3]);
         }
-        ptx::fence_proxy_async_all();
+        ptx::fence_proxy_async_smem();
+        __syncthreads();
+        constexpr int GROUPS = SHARE / 8;  // of 8 rows, that this CTA hands on
+        const int to = tid / GROUPS;
+        if (S > 1 && to < S && to != rank_in) {
+            const uint32_t at = ptx::smem_addr(parts()) + (lane_of(rank_in * SHARE + tid % GROUPS * 8) >> 3) * s.group();
+            ptx::bulk_to_cluster(ptx::mapa_shared(at, to), at, s.group(), ptx::mapa_shared(ptx::smem_addr(parts_full), to));
+        }
     }
 
-    // A thread's rows of a tile are every 8th of its warp's 32, their elements of a chunk of 64 columns 8 of the warp's 32.  It holds
-    // ROWS of those rows at a time: 64 bytes of base.
-    static constexpr int ROWS = sizeof(TB) == 2 ? 4 : 2, TURNS = 4 / ROWS, WORDS = 2 * sizeof(TB);
+    // A thread finishes four times 8 neighbouring elements of a chunk, SIDES side by side at 32 columns' distance in each of 4 / SIDES rows, 8 rows
+    // apart.  It holds HOLD of them at a time: 64 bytes of base.
+    static constexpr int SIDES = 1 << HALVED;
+    static constexpr int HOLD = sizeof(TB) == 2 ? 4 : 2, TURNS = 4 / HOLD, WORDS = 2 * sizeof(TB);
     struct Held {
-        uint32_t u[ROWS][WORDS];
+        uint32_t u[HOLD][WORDS];
     };
-    const TB* base_at[4];
-    TO* out_at[4];
-    __device__ __forceinline__ int row_of(int i) const { return 32 * (warp & 3) + (lane >> 2) + 8 * i; }
-    __device__ __forceinline__ int col_of(int c0) const { return c0 + 32 * (warp >> 2) + 8 * (lane & 3); }
+    const TB* base_at[4 / SIDES];
+    TO* out_at[4 / SIDES];
+    __device__ __forceinline__ static constexpr int row_index(int i) { return HALVED ? i & 1 : i; }
+    __device__ __forceinline__ static constexpr int side_of(int i) { return HALVED ? i >> 1 : 0; }
+    __device__ __forceinline__ int row_of(int i) const { return LANES * (warp & 3) + (lane >> 2) + 8 * row_index(i); }
+    __device__ __forceinline__ int col_of(int i, int c0) const { return c0 + 32 * SIDES * ((warp >> 2) & 1) + 32 * side_of(i) + 8 * (lane & 3); }
     __device__ __forceinline__ void make_rows()
     {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int64_t t = p.plan.order[piece.first + (row_of(i) < piece.rows ? row_of(i) : 0)];
-            base_at[i] = static_cast<const TB*>(p.base) + t * p.base_stride + col_of(0);
-            out_at[i] = static_cast<TO*>(p.out) + t * p.out_stride + col_of(0);
+        for (int i = 0; i < 4 / SIDES; ++i) {
+            const int64_t t = ids[row_of(i)];
+            base_at[i] = static_cast<const TB*>(p.base) + t * p.base_stride + col_of(i, 0);
+            out_at[i] = static_cast<TO*>(p.out) + t * p.out_stride + col_of(i, 0);
         }
     }
     // Turn `turn` of the chunk at c0.
     __device__ __forceinline__ void load_base(Held& b, int turn, int c0) const
     {
 #pragma unroll
-        for (int k = 0; k < ROWS; ++k) {
-            const int i = turn * ROWS + k;
-            const TB* src = base_at[i] + c0;
-            const int left = p.base && row_of(i) < piece.rows ? p.to - col_of(c0) : 0;
+        for (int k = 0; k < HOLD; ++k) {
+            const int i = turn * HOLD + k;
+            const TB* src = base_at[row_index(i)] + c0 + 32 * side_of(i);
+            const int left = p.base && row_of(i) < piece.rows ? p.to - col_of(i, c0) : 0;
             if constexpr (VEC) {
 #pragma unroll
                 for (int j = 0; j < WORDS; j += 4) {
@@ -304,7 +323,7 @@ struct Pass {
             }
         }
     }
-    // out = act(base + sum) for row i: `base` its base, `v` its sums as they come from tensor memory.
+    // out = act(base + sum) for 8 elements: `base` theirs, `v` their sums as they come from tensor memory.
     __device__ __forceinline__ void finish(const uint32_t (&base)[WORDS], float2 (&v)[4], int i, int c0, bool live) const
     {
 #pragma unroll
@@ -316,8 +335,8 @@ struct Pass {
         if (p.relu)
 #pragma unroll
             for (int j = 0; j < 4; ++j) v[j] = make_float2(v[j].x < 0.f ? 0.f : v[j].x, v[j].y < 0.f ? 0.f : v[j].y);
-        TO* row = out_at[i] + c0;
-        const int left = live && row_of(i) < piece.rows ? p.to - col_of(c0) : 0;
+        TO* row = out_at[row_index(i)] + c0 + 32 * side_of(i);
+        const int left = live && row_of(i) < piece.rows ? p.to - col_of(i, c0) : 0;
         if constexpr (VEC) {
             if (left <= 0) return;
             if constexpr (sizeof(TO) == 4) {
@@ -339,22 +358,42 @@ struct Pass {
         }
     }
 
+    // Base's next chunks to L2, AHEAD of them from chunk c on: HBM works on them while the sums are joined and chunks wait for their products.
+    static constexpr int AHEAD = 4;
+    __device__ __forceinline__ void prefetch_base(int c, int chunk1) const
+    {
+        if (!VEC || !p.base || !p.out || tid >= piece.rows || c >= chunk1) return;
+        const int c0 = c * COLS, end = (c + AHEAD < chunk1 ? c + AHEAD : chunk1) * COLS;
+        ptx::bulk_prefetch(static_cast<const TB*>(p.base) + ids[tid] * p.base_stride + c0, ((end < p.to ? end : p.to) - c0) * static_cast<int>(sizeof(TB)));
+    }
+
+    // The first filling of w2's buffers i0 .. i1, each by the group whose chunk it is for.
+    __device__ __forceinline__ void fill(int i0, int i1, int chunk0, int chunk1) const
+    {
+        for (int i = i0; i < i1; ++i) {
+            if ((i & 1) != group) continue;
+            clear_pad(w2_buf(i));
+            if (chunk0 + i < chunk1) load_w2(w2_buf(i), (chunk0 + i) * COLS);
+            arrive(&w2_full[i]);
+        }
+    }
+
     // Rows without an adapter: out = act(base), mid = 0.
     __device__ __forceinline__ void without(int chunk0, int chunk1) const
     {
         if (p.mid && rank_in == 0)
             for (int i = tid; i < piece.rows * p.rank; i += P_THREADS)
-                p.mid[static_cast<int64_t>(p.plan.order[piece.first + i / p.rank]) * p.rank + i % p.rank] = 0.f;
+                p.mid[static_cast<int64_t>(ids[i / p.rank]) * p.rank + i % p.rank] = 0.f;
         if (!p.out || warp >= P_WARPS) return;
-        for (int c = chunk0; c < chunk1; ++c)
+        for (int c = chunk0 + group; c < chunk1; c += 2)
 #pragma unroll
             for (int turn = 0; turn < TURNS; ++turn) {
                 Held b;
-                load_base(b, turn, c * P_COLS);
+                load_base(b, turn, c * COLS);
 #pragma unroll
-                for (int k = 0; k < ROWS; ++k) {
+                for (int k = 0; k < HOLD; ++k) {
                     float2 v[4] = {};
-                    finish(b.u[k], v, turn * ROWS + k, c * P_COLS, true);
+                    finish(b.u[k], v, turn * HOLD + k, c * COLS, true);
                 }
             }
     }
@@ -362,16 +401,18 @@ struct Pass {
     __device__ __forceinline__ void run()
     {
         if (tid == 0) {
-            for (int i = 0; i < p.stages; ++i) {
+            for (int i = 0; i < n_stages; ++i) {
                 ptx::mbar_init(&full[i], P_LOADERS);
                 ptx::mbar_init(&empty[i], 1);
             }
             ptx::mbar_init(done, 1);
-            for (int i = 0; i < 2; ++i) {
-                ptx::mbar_init(&w2_full[i], P_LOADERS);
+            for (int i = 0; i < n_bufs; ++i) ptx::mbar_init(&w2_full[i], P_GROUP);
+            for (int i = 0; i < 4; ++i) {
                 ptx::mbar_init(&d_full[i], 1);
-                ptx::mbar_init(&d_empty[i], P_WARPS);
+                ptx::mbar_init(&d_empty[i], P_WARPS / 2);
             }
+            ptx::mbar_init(parts_full, 1);
+            if (p.splits > 1) ptx::mbar_arrive_expect_tx(parts_full, (ROWS - ROWS / p.splits) / 8 * s.group());
             *abort_flag = 0u;
             ptx::mbar_init_fence();
         }
@@ -382,16 +423,24 @@ struct Pass {
         ptx::tc_fence_before();
         __syncthreads();
         ptx::tc_fence_after();
-        const uint32_t tmem = *slot, d2 = tmem + MOST_RANK;
+        const uint32_t tmem = *slot;
         ptx::grid_dependency_wait();
-        piece = p.plan.tiles[blockIdx.x / p.splits];  // the same for the whole cluster
+        const int block = blockIdx.x / p.splits;
+        piece = p.plan.tiles[block >> HALVED];  // the same for the whole cluster
+        if constexpr (HALVED) {
+            piece.first += (block & 1) * ROWS;
+            piece.rows -= (block & 1) * ROWS;
+            if (piece.rows > ROWS) piece.rows = ROWS;
+        }
         e = piece.adapter;
-        const int chunks = p.out ? (p.to + P_COLS - 1) / P_COLS : 0;
+        const int chunks = p.out ? (p.to + COLS - 1) / COLS : 0;
         const int chunk0 = static_cast<int>(static_cast<int64_t>(rank_in) * chunks / p.splits), chunk1 = static_cast<int>(static_cast<int64_t>(rank_in + 1) * chunks / p.splits);
         if (piece.rows > 0) {
+            if (tid < TILE) ids[tid] = p.plan.order[piece.first + (tid < piece.rows ? tid : 0)];
+            __syncthreads();
             if (warp < P_WARPS) make_rows();
             if (e < p.adapters)
-                with(tmem, d2, chunk0, chunk1);
+                with(tmem, chunk0, chunk1);
             else
                 without(chunk0, chunk1);
         }
@@ -403,32 +452,29 @@ struct Pass {
         }
     }
 
-    __device__ __forceinline__ void with(uint32_t tmem, uint32_t d2, int chunk0, int chunk1)
+    __device__ __forceinline__ void with(uint32_t tmem, int chunk0, int chunk1)
     {
         const int steps = (p.from + P_STEP - 1) / P_STEP;
         const int s0 = static_cast<int>(static_cast<int64_t>(rank_in) * steps / p.splits), s1 = static_cast<int>(static_cast<int64_t>(rank_in + 1) * steps / p.splits);
         bool ok = true;
+        const float scale = p.scale ? __ldg(p.scale + e) : 1.f;
         if (warp < P_WARPS) {
-            const __nv_bfloat16* rows[4];
+            const __nv_bfloat16* rows[ROWS / 64];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int row = (tid >> 3) + 32 * i;
-                rows[i] = p.in + p.plan.order[piece.first + (row < piece.rows ? row : 0)] * p.in_stride + 8 * (tid & 7);
-            }
+            for (int i = 0; i < ROWS / 64; ++i) rows[i] = p.in + ids[(tid >> 3) + 64 * i] * p.in_stride + 8 * (tid & 7);
             if (VEC) make_places();
             for (int f = s0; f < s1; ++f) {
-                const int it = f - s0, at = it % p.stages;
-                if (!wait(&empty[at], (static_cast<uint32_t>(it / p.stages) & 1u) ^ 1u, ok)) break;
+                const int it = f - s0, at = it % n_stages;
+                if (!wait(&empty[at], (static_cast<uint32_t>(it / n_stages) & 1u) ^ 1u, ok)) break;
                 load_stage(mem + at * s.stage(), f * P_STEP, rows);
                 arrive(&full[at]);
             }
-            clear_pad(w2_buf(0));
-            if (chunk0 < chunk1) load_w2(w2_buf(0), chunk0 * P_COLS);
-            arrive(&w2_full[0]);
+            prefetch_base(chunk0, chunk1);
+            fill(0, 1, chunk0, chunk1);
         } else {
             for (int f = s0; f < s1; ++f) {
-                const int it = f - s0, at = it % p.stages;
-                wait(&full[at], static_cast<uint32_t>(it / p.stages) & 1u, ok);
+                const int it = f - s0, at = it % n_stages;
+                wait(&full[at], static_cast<uint32_t>(it / n_stages) & 1u, ok);
                 ok = __all_sync(0xffffffffu, ok);  // what follows is the whole warp's
                 if (!ok) break;
                 ptx::fence_proxy_async_smem();
@@ -445,16 +491,18 @@ struct Pass {
         __syncwarp();
         // The ring is free: the sums, and w2's second chunk.
         float* sums = reinterpret_cast<float*>(mem);
-        if (warp < 4) {
+        if (warp < P_WARPS) {
             ptx::tc_fence_after();
-            const int row = 32 * warp + lane;
-            for (int c = 0; c < s.rp; c += 16) {
+            const int row = LANES * (warp & 3) + lane;
+            for (int c = 16 * (warp >> 2); c < s.rp; c += 64) {
                 uint32_t v[16];
-                ptx::tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(32 * warp) << 16) + c, v);
+                ptx::tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + c, v);
                 ptx::tmem_ld_wait();
                 const uint32_t at = ptx::smem_addr(sums + row * s.pitch() + c);
+                if (lane < LANES)
 #pragma unroll
-                for (int i = 0; i < 4; ++i) ptx::st_shared_v4(at + 16 * i, v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                    for (int i = 0; i < 4; ++i) ptx::st_shared_v4(at + 16 * i, v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                __syncwarp();
             }
             ptx::tc_fence_before();
         }
@@ -462,73 +510,73 @@ struct Pass {
             ptx::cluster_sync();
         else
             __syncthreads();
-        if (warp < P_WARPS) {
-            clear_pad(w2_buf(1));
-            if (chunk0 + 1 < chunk1) load_w2(w2_buf(1), (chunk0 + 1) * P_COLS);
-            arrive(&w2_full[1]);
-        }
-        const float scale = p.scale ? __ldg(p.scale + e) : 1.f;
+        if (warp < P_WARPS) fill(1, s.early_chunks(), chunk0, chunk1);
         switch (p.splits) {
             case 1: join<1>(sums, scale); break;
             case 2: join<2>(sums, scale); break;
             case 4: join<4>(sums, scale); break;
             default: join<8>(sums, scale); break;
         }
-        if (p.splits > 1)
-            ptx::cluster_sync();
-        else
-            __syncthreads();
+        // All parts are here: none of this CTA's peers reads its sums any more, and what they sent has come.
+        if (p.splits > 1) {
+            wait(parts_full, 0, ok);
+            __syncwarp();
+            ptx::cluster_arrive_relaxed();
+        }
+        if (warp < P_WARPS) fill(s.early_chunks(), n_bufs, chunk0, chunk1);
         const int n = chunk1 - chunk0;
         if (warp == P_WARPS) {
+            ok = __all_sync(0xffffffffu, ok);
             ptx::fence_proxy_async_smem();
+            ptx::tc_fence_after();
             const uint32_t a = ptx::smem_addr(parts());
             for (int j = 0; j < n; ++j) {
-                const int b = j & 1;
-                const uint32_t phase = static_cast<uint32_t>(j >> 1) & 1u;
-                wait(&w2_full[b], phase, ok);
-                wait(&d_empty[b], phase ^ 1u, ok);
+                const int b = j & 3, buf = j % n_bufs;
+                wait(&w2_full[buf], static_cast<uint32_t>(j / n_bufs) & 1u, ok);
+                wait(&d_empty[b], (static_cast<uint32_t>(j >> 2) & 1u) ^ 1u, ok);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 ptx::fence_proxy_async_smem();
                 ptx::tc_fence_after();
-                const uint32_t w = ptx::smem_addr(w2_buf(b));
+                const uint32_t w = ptx::smem_addr(w2_buf(buf));
                 for (int k = 0; k < s.rp / 16; ++k)  // the three parts of 16 of mid's columns
-                    ptx::mma_bf16_elect_x3(d2 + P_COLS * b, ptx::plain_kmajor_desc(a + k * 4096, 2048, 128),
-                                           TRANS ? ptx::plain_mnmajor_desc(w + k * 2304, 1152, 144) : ptx::plain_kmajor_desc(w + k * 2304, 1152, 144),
-                                           s.rp / 8 * (2048 / 16), TRANS ? ptx::idesc_bf16_f32_bmn(TILE, P_COLS) : ptx::idesc_bf16_f32(TILE, P_COLS), k > 0);
+                    ptx::mma_bf16_elect_x3(tmem + COLS * b, ptx::plain_kmajor_desc(a + k * 256, 128, s.group()), ptx::plain_kmajor_desc(w + k * 2 * s.column(), s.column(), 144),
+                                           s.rp / 8 * (128 / 16), TRANS ? ptx::idesc_bf16_f32_bmn(TILE, COLS) : ptx::idesc_bf16_f32(TILE, COLS), k > 0);
                 ptx::mma_commit_elect(&d_full[b]);
             }
-        } else if (n > 0) {
-            // base a turn ahead, in two sets of registers by turns (a copy between them would wait for what is on its way)
+        } else if (group < n) {
+            // This group's chunks, every other one; base a turn ahead, in two sets of registers by turns (a copy between them would wait for what
+            // is on its way).
             Held held[2];
-            load_base(held[0], 0, chunk0 * P_COLS);
-            for (int j0 = 0; j0 < n; j0 += 2 / TURNS)
+            load_base(held[0], 0, (chunk0 + group) * COLS);
+            for (int j0 = group; j0 < n; j0 += 4 / TURNS)
 #pragma unroll
                 for (int jj = 0; jj < 2 / TURNS; ++jj) {
-                    const int j = j0 + jj;
+                    const int j = j0 + 2 * jj;
                     if (j >= n) break;
-                    const int b = j & 1, c0 = (chunk0 + j) * P_COLS;
-                    if (TURNS == 2 || j + 1 < n) load_base(held[TURNS == 2 ? 1 : (jj + 1) & 1], TURNS - 1, TURNS == 2 ? c0 : c0 + P_COLS);
-                    wait(&d_full[b], static_cast<uint32_t>(j >> 1) & 1u, ok);
+                    const int b = j & 3, c0 = (chunk0 + j) * COLS;
+                    if (TURNS == 2 || j + 2 < n) load_base(held[TURNS == 2 ? 1 : (jj + 1) & 1], TURNS - 1, TURNS == 2 ? c0 : c0 + 2 * COLS);
+                    wait(&d_full[b], static_cast<uint32_t>(j >> 2) & 1u, ok);
                     __syncwarp();
                     ptx::tc_fence_after();
                     uint32_t v[2][16];
-                    const uint32_t at = d2 + P_COLS * b + 32 * (warp >> 2) + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+                    const uint32_t at = tmem + COLS * b + 32 * SIDES * ((warp >> 2) & 1) + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
                     ptx::tmem_ld_16x256b_x4(at, v[0]);
-                    ptx::tmem_ld_16x256b_x4(at + (16u << 16), v[1]);
-                    if (j + 2 < n) {
-                        load_w2(w2_buf(b), c0 + 2 * P_COLS);
-                        arrive(&w2_full[b]);
+                    ptx::tmem_ld_16x256b_x4(at + (HALVED ? 32u : 16u << 16), v[1]);
+                    if (j + n_bufs < n) {
+                        load_w2(w2_buf(j % n_bufs), c0 + n_bufs * COLS);
+                        arrive(&w2_full[j % n_bufs]);
                     }
+                    if (j % AHEAD == 0) prefetch_base(chunk0 + j + AHEAD, chunk1);
                     ptx::tmem_ld_wait();
                     ptx::tc_fence_before();
                     if (lane == 0) ptx::mbar_arrive(&d_empty[b]);
 #pragma unroll
                     for (int turn = 0; turn < TURNS; ++turn) {
-                        if (turn == 1 && j + 1 < n) load_base(held[0], 0, c0 + P_COLS);
+                        if (turn == 1 && j + 2 < n) load_base(held[0], 0, c0 + 2 * COLS);
 #pragma unroll
-                        for (int k = 0; k < ROWS; ++k) {
-                            const int i = turn * ROWS + k;
+                        for (int k = 0; k < HOLD; ++k) {
+                            const int i = turn * HOLD + k;
                             float2 f[4];
 #pragma unroll
                             for (int g = 0; g < 4; ++g) f[g] = make_float2(__uint_as_float(v[i >> 1][4 * g + 2 * (i & 1)]), __uint_as_float(v[i >> 1][4 * g + 2 * (i & 1) + 1]));
@@ -540,41 +588,44 @@ struct Pass {
         __syncwarp();
         ptx::cp_async_wait_all();
         if (!ok && lane == 0 && p.status) atomicMax(p.status, 6u);
+        __syncwarp();
+        if (p.splits > 1) ptx::cluster_wait();  // what this CTA sent has been received
     }
 };
 
-template <bool TRANS, bool VEC, typename TB, typename TO>
-__global__ void __launch_bounds__(P_THREADS, 2) pass_tiles(const __grid_constant__ PassParams p)
+template <bool TRANS, bool VEC, int HALVED, typename TB, typename TO>
+__global__ void __launch_bounds__(P_THREADS, 1) pass_tiles(const __grid_constant__ PassParams p)
 {
     extern __shared__ __align__(1024) uint8_t raw[];
-    Pass<TRANS, VEC, TB, TO> pass(p, raw);
+    Pass<TRANS, VEC, HALVED, TB, TO> pass(p, raw);
     pass.run();
 }
 
-template <typename K>
-int start_pass(K kernel, const PassParams& p, std::atomic<uint64_t>& done, cudaStream_t stream)
-{
-    const int bytes = PassSmem(p.rank, p.stages).bytes();
-    if (!mx::allow_smem(kernel, 227 * 1024, done)) return CONV2D_ERR_CUDA;
-    const int64_t grid = static_cast<int64_t>(p.plan.n_tiles) * p.splits;
-    if (grid > INT32_MAX) return CONV2D_ERR_UNSUPPORTED;
-    return mx::launch(kernel, grid, P_THREADS, bytes, stream, p.splits, p) == cudaSuccess ? CONV2D_OK : CONV2D_ERR_CUDA;
-}
-
-template <bool TRANS, bool VEC, typename TB, typename TO>
+template <bool TRANS, bool VEC, int HALVED, typename TB, typename TO>
 int start_pass_as(const PassParams& p, cudaStream_t stream)
 {
     static std::atomic<uint64_t> done{0};
-    return start_pass(pass_tiles<TRANS, VEC, TB, TO>, p, done, stream);
+    const auto kernel = pass_tiles<TRANS, VEC, HALVED, TB, TO>;
+    if (!mx::allow_smem(kernel, P_ROOM, done)) return CONV2D_ERR_CUDA;
+    const int64_t grid = (static_cast<int64_t>(p.plan.n_tiles) << HALVED) * p.splits;
+    if (grid > INT32_MAX) return CONV2D_ERR_UNSUPPORTED;
+    return mx::launch(kernel, grid, P_THREADS, P_ROOM, stream, p.splits, p) == cudaSuccess ? CONV2D_OK : CONV2D_ERR_CUDA;
 }
 
-template <bool TRANS, bool VEC>
+template <bool TRANS, bool VEC, int HALVED>
 int start_pass_by_types(const PassParams& p, int32_t base, int32_t out, cudaStream_t stream)
 {
     using B = __nv_bfloat16;
     if (base == CONV2D_OUT_BF16)
-        return out == CONV2D_OUT_BF16 ? start_pass_as<TRANS, VEC, B, B>(p, stream) : start_pass_as<TRANS, VEC, B, float>(p, stream);
-    return out == CONV2D_OUT_BF16 ? start_pass_as<TRANS, VEC, float, B>(p, stream) : start_pass_as<TRANS, VEC, float, float>(p, stream);
+        return out == CONV2D_OUT_BF16 ? start_pass_as<TRANS, VEC, HALVED, B, B>(p, stream) : start_pass_as<TRANS, VEC, HALVED, B, float>(p, stream);
+    return out == CONV2D_OUT_BF16 ? start_pass_as<TRANS, VEC, HALVED, float, B>(p, stream) : start_pass_as<TRANS, VEC, HALVED, float, float>(p, stream);
+}
+
+template <bool TRANS>
+int start_pass(const PassParams& p, int32_t base, int32_t out, bool vec, bool halved, cudaStream_t stream)
+{
+    if (vec) return halved ? start_pass_by_types<TRANS, true, 1>(p, base, out, stream) : start_pass_by_types<TRANS, true, 0>(p, base, out, stream);
+    return halved ? start_pass_by_types<TRANS, false, 1>(p, base, out, stream) : start_pass_by_types<TRANS, false, 0>(p, base, out, stream);
 }
 
 }  // namespace ad

@@ -5,9 +5,9 @@
 namespace sgb {
 namespace ad {
 
-int launch_pass_bwd(const PassParams& p, int32_t base_dtype, int32_t out_dtype, bool vec, cudaStream_t stream)
+int launch_pass_bwd(const PassParams& p, int32_t base_dtype, int32_t out_dtype, bool vec, bool halved, cudaStream_t stream)
 {
-    return vec ? start_pass_by_types<true, true>(p, base_dtype, out_dtype, stream) : start_pass_by_types<true, false>(p, base_dtype, out_dtype, stream);
+    return start_pass<true>(p, base_dtype, out_dtype, vec, halved, stream);
 }
 
 }  // namespace ad
