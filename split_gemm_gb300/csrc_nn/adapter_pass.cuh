@@ -63,7 +63,7 @@ struct Pass {
         slot = reinterpret_cast<uint32_t*>(ids + TILE);
         abort_flag = slot + 1;
         tid = threadIdx.x;
-        warp = tid >> 5;
+        warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // the same in all lanes, as the compiler then knows
         lane = tid & 31;
         rank_in = blockIdx.x % p.splits;
         group = warp >> 3;
@@ -291,21 +291,24 @@ struct Pass {
     __device__ __forceinline__ int col_of(int i, int c0) const { return c0 + 32 * SIDES * ((warp >> 2) & 1) + 32 * side_of(i) + 8 * (lane & 3); }
     __device__ __forceinline__ void make_rows()
     {
+        rows_here = 0u;
 #pragma unroll
         for (int i = 0; i < 4 / SIDES; ++i) {
             const int64_t t = ids[row_of(i)];
+            if (row_of(i) < piece.rows) rows_here |= 1u << i;
             base_at[i] = static_cast<const TB*>(p.base) + t * p.base_stride + col_of(i, 0);
             out_at[i] = static_cast<TO*>(p.out) + t * p.out_stride + col_of(i, 0);
         }
     }
-    // Turn `turn` of the chunk at c0.
-    __device__ __forceinline__ void load_base(Held& b, int turn, int c0) const
+    uint32_t rows_here;  // bit i: row_index i of the thread's is one of the tile's
+    // Turn `turn` of the chunk at c0; `whole`: all its columns exist.
+    __device__ __forceinline__ void load_base(Held& b, int turn, int c0, bool whole) const
     {
 #pragma unroll
         for (int k = 0; k < HOLD; ++k) {
             const int i = turn * HOLD + k;
             const TB* src = base_at[row_index(i)] + c0 + 32 * side_of(i);
-            const int left = p.base && row_of(i) < piece.rows ? p.to - col_of(i, c0) : 0;
+            const int left = !(rows_here >> row_index(i) & 1u) || !p.base ? 0 : whole ? 8 : p.to - col_of(i, c0);
             if constexpr (VEC) {
 #pragma unroll
                 for (int j = 0; j < WORDS; j += 4) {
@@ -324,7 +327,7 @@ struct Pass {
         }
     }
     // out = act(base + sum) for 8 elements: `base` theirs, `v` their sums as they come from tensor memory.
-    __device__ __forceinline__ void finish(const uint32_t (&base)[WORDS], float2 (&v)[4], int i, int c0, bool live) const
+    __device__ __forceinline__ void finish(const uint32_t (&base)[WORDS], float2 (&v)[4], int i, int c0, bool whole, bool live) const
     {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -336,12 +339,12 @@ struct Pass {
 #pragma unroll
             for (int j = 0; j < 4; ++j) v[j] = make_float2(v[j].x < 0.f ? 0.f : v[j].x, v[j].y < 0.f ? 0.f : v[j].y);
         TO* row = out_at[row_index(i)] + c0 + 32 * side_of(i);
-        const int left = live && row_of(i) < piece.rows ? p.to - col_of(i, c0) : 0;
-        if constexpr (VEC) {
-            if (left <= 0) return;
+        const int left = !(rows_here >> row_index(i) & 1u) || !live ? 0 : whole ? 8 : p.to - col_of(i, c0);
+        if constexpr (VEC) {  // made first, so that the stores are predicated
             if constexpr (sizeof(TO) == 4) {
-                __stcs(reinterpret_cast<float4*>(row), make_float4(v[0].x, v[0].y, v[1].x, v[1].y));
-                __stcs(reinterpret_cast<float4*>(row) + 1, make_float4(v[2].x, v[2].y, v[3].x, v[3].y));
+                const float4 lo = make_float4(v[0].x, v[0].y, v[1].x, v[1].y), hi = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
+                if (left > 0) __stcs(reinterpret_cast<float4*>(row), lo);
+                if (left > 0) __stcs(reinterpret_cast<float4*>(row) + 1, hi);
             } else {
                 uint32_t o[4];
 #pragma unroll
@@ -349,7 +352,8 @@ struct Pass {
                     const __nv_bfloat162 h = __floats2bfloat162_rn(v[j].x, v[j].y);
                     o[j] = *reinterpret_cast<const uint32_t*>(&h);
                 }
-                __stcs(reinterpret_cast<uint4*>(row), make_uint4(o[0], o[1], o[2], o[3]));
+                const uint4 q = make_uint4(o[0], o[1], o[2], o[3]);
+                if (left > 0) __stcs(reinterpret_cast<uint4*>(row), q);
             }
         } else {
 #pragma unroll
@@ -358,13 +362,16 @@ struct Pass {
         }
     }
 
-    // Base's next chunks to L2, AHEAD of them from chunk c on: HBM works on them while the sums are joined and chunks wait for their products.
+    // Base's first chunks to L2, where HBM works on them while the sums are joined.
     static constexpr int AHEAD = 4;
-    __device__ __forceinline__ void prefetch_base(int c, int chunk1) const
+    __device__ __forceinline__ void prefetch_base(int chunk0, int chunk1) const
     {
-        if (!VEC || !p.base || !p.out || tid >= piece.rows || c >= chunk1) return;
-        const int c0 = c * COLS, end = (c + AHEAD < chunk1 ? c + AHEAD : chunk1) * COLS;
-        ptx::bulk_prefetch(static_cast<const TB*>(p.base) + ids[tid] * p.base_stride + c0, ((end < p.to ? end : p.to) - c0) * static_cast<int>(sizeof(TB)));
+        constexpr int LINES = AHEAD * COLS * sizeof(TB) / 128, EACH = 128 / sizeof(TB);
+        if (!p.base || !p.out) return;
+        for (int i = tid; i < piece.rows * LINES; i += P_LOADERS) {
+            const int row = i / LINES, c = chunk0 * COLS + (i - row * LINES) * EACH;
+            if (c < p.to && c < chunk1 * COLS) ptx::prefetch_l2(static_cast<const TB*>(p.base) + ids[row] * p.base_stride + c);
+        }
     }
 
     // The first filling of w2's buffers i0 .. i1, each by the group whose chunk it is for.
@@ -389,11 +396,11 @@ struct Pass {
 #pragma unroll
             for (int turn = 0; turn < TURNS; ++turn) {
                 Held b;
-                load_base(b, turn, c * COLS);
+                load_base(b, turn, c * COLS, false);
 #pragma unroll
                 for (int k = 0; k < HOLD; ++k) {
                     float2 v[4] = {};
-                    finish(b.u[k], v, turn * HOLD + k, c * COLS, true);
+                    finish(b.u[k], v, turn * HOLD + k, c * COLS, false, true);
                 }
             }
     }
@@ -510,13 +517,13 @@ struct Pass {
             ptx::cluster_sync();
         else
             __syncthreads();
-        if (warp < P_WARPS) fill(1, s.early_chunks(), chunk0, chunk1);
         switch (p.splits) {
             case 1: join<1>(sums, scale); break;
             case 2: join<2>(sums, scale); break;
             case 4: join<4>(sums, scale); break;
             default: join<8>(sums, scale); break;
         }
+        if (warp < P_WARPS) fill(1, s.early_chunks(), chunk0, chunk1);
         // All parts are here: none of this CTA's peers reads its sums any more, and what they sent has come.
         if (p.splits > 1) {
             wait(parts_full, 0, ok);
@@ -539,23 +546,32 @@ struct Pass {
                 ptx::fence_proxy_async_smem();
                 ptx::tc_fence_after();
                 const uint32_t w = ptx::smem_addr(w2_buf(buf));
-                for (int k = 0; k < s.rp / 16; ++k)  // the three parts of 16 of mid's columns
-                    ptx::mma_bf16_elect_x3(tmem + COLS * b, ptx::plain_kmajor_desc(a + k * 256, 128, s.group()), ptx::plain_kmajor_desc(w + k * 2 * s.column(), s.column(), 144),
-                                           s.rp / 8 * (128 / 16), TRANS ? ptx::idesc_bf16_f32_bmn(TILE, COLS) : ptx::idesc_bf16_f32(TILE, COLS), k > 0);
+                // the three parts of 32 of mid's columns at a time
+                const uint64_t ad = ptx::plain_kmajor_desc(a, 128, s.group()), wd = ptx::plain_kmajor_desc(w, s.column(), 144);
+                const uint32_t idesc = TRANS ? ptx::idesc_bf16_f32_bmn(TILE, COLS) : ptx::idesc_bf16_f32(TILE, COLS);
+                const uint64_t part = s.rp / 8 * (128 / 16), w_step = 2 * s.column() / 16;
+                const int whole = s.rp / 32;
+                for (int k = 0; k < whole; ++k)
+                    ptx::mma_bf16_elect_3x2(tmem + COLS * b, ad + k * 32, wd + 2 * k * w_step, part, 16, w_step, idesc, k > 0);
+                if (s.rp & 16) ptx::mma_bf16_elect_x3(tmem + COLS * b, ad + whole * 32, wd + 2 * whole * w_step, part, idesc, whole > 0);
                 ptx::mma_commit_elect(&d_full[b]);
             }
         } else if (group < n) {
             // This group's chunks, every other one; base a turn ahead, in two sets of registers by turns (a copy between them would wait for what
             // is on its way).
             Held held[2];
-            load_base(held[0], 0, (chunk0 + group) * COLS);
+            load_base(held[0], 0, (chunk0 + group) * COLS, false);
             for (int j0 = group; j0 < n; j0 += 4 / TURNS)
 #pragma unroll
                 for (int jj = 0; jj < 2 / TURNS; ++jj) {
                     const int j = j0 + 2 * jj;
                     if (j >= n) break;
                     const int b = j & 3, c0 = (chunk0 + j) * COLS;
-                    if (TURNS == 2 || j + 2 < n) load_base(held[TURNS == 2 ? 1 : (jj + 1) & 1], TURNS - 1, TURNS == 2 ? c0 : c0 + 2 * COLS);
+                    const bool whole = c0 + COLS <= p.to, next = c0 + 3 * COLS <= p.to;
+                    if (TURNS == 2)
+                        load_base(held[1], 1, c0, whole);
+                    else if (j + 2 < n)
+                        load_base(held[(jj + 1) & 1], 0, c0 + 2 * COLS, next);
                     wait(&d_full[b], static_cast<uint32_t>(j >> 2) & 1u, ok);
                     __syncwarp();
                     ptx::tc_fence_after();
@@ -567,20 +583,19 @@ struct Pass {
                         load_w2(w2_buf(j % n_bufs), c0 + n_bufs * COLS);
                         arrive(&w2_full[j % n_bufs]);
                     }
-                    if (j % AHEAD == 0) prefetch_base(chunk0 + j + AHEAD, chunk1);
                     ptx::tmem_ld_wait();
                     ptx::tc_fence_before();
                     if (lane == 0) ptx::mbar_arrive(&d_empty[b]);
 #pragma unroll
                     for (int turn = 0; turn < TURNS; ++turn) {
-                        if (turn == 1 && j + 2 < n) load_base(held[0], 0, c0 + 2 * COLS);
+                        if (turn == 1 && j + 2 < n) load_base(held[0], 0, c0 + 2 * COLS, next);
 #pragma unroll
                         for (int k = 0; k < HOLD; ++k) {
                             const int i = turn * HOLD + k;
                             float2 f[4];
 #pragma unroll
                             for (int g = 0; g < 4; ++g) f[g] = make_float2(__uint_as_float(v[i >> 1][4 * g + 2 * (i & 1)]), __uint_as_float(v[i >> 1][4 * g + 2 * (i & 1) + 1]));
-                            finish(held[TURNS == 1 ? jj & 1 : turn].u[k], f, i, c0, ok);
+                            finish(held[TURNS == 1 ? jj & 1 : turn].u[k], f, i, c0, whole, ok);
                         }
                     }
                 }

@@ -60,8 +60,29 @@ __device__ __forceinline__ void mma_bf16_elect_x2(uint32_t d_tmem, uint64_t a_de
         : "memory");
 }
 
-// The same for three MMAs with one B: A's descriptors `a_step` apart.
-__device__ __forceinline__ void mma_bf16_elect_x3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint64_t a_step, uint32_t idesc, uint32_t accumulate)
+// The same for pairs of three MMAs, A's descriptors `a_part` apart in a triple with one B; the pair's triples `a_step` and `b_step` apart.
+__device__ __forceinline__ void mma_bf16_elect_3x2(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint64_t a_part, uint64_t a_step, uint64_t b_step,
+                                                   uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n\t.reg .pred p, e, t;\n\t.reg .b64 a1, a2, a3, a4, a5, b1;\n\t"
+        "setp.ne.b32 p, %7, 0;\n\t"
+        "setp.eq.b32 t, 0, 0;\n\t"
+        "add.s64 a1, %1, %3;\n\tadd.s64 a2, a1, %3;\n\tadd.s64 a3, %1, %4;\n\tadd.s64 a4, a3, %3;\n\tadd.s64 a5, a4, %3;\n\t"
+        "add.s64 b1, %2, %5;\n\t"
+        "elect.sync _|e, 0xffffffff;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %6, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, %2, %6, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, %2, %6, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b1, %6, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a4, b1, %6, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a5, b1, %6, t;\n\t}" ::"r"(d_tmem),
+        "l"(a_desc), "l"(b_desc), "l"(a_part), "l"(a_step), "l"(b_step), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// One triple.
+__device__ __forceinline__ void mma_bf16_elect_x3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint64_t a_part, uint32_t idesc, uint32_t accumulate)
 {
     asm volatile(
         "{\n\t.reg .pred p, e, t;\n\t.reg .b64 a1, a2;\n\t"
@@ -72,7 +93,7 @@ __device__ __forceinline__ void mma_bf16_elect_x3(uint32_t d_tmem, uint64_t a_de
         "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %4, p;\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, %2, %4, t;\n\t"
         "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, %2, %4, t;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "l"(a_step), "r"(idesc), "r"(accumulate)
+        "l"(a_desc), "l"(b_desc), "l"(a_part), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 
@@ -82,11 +103,8 @@ __device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src, uint32
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
 }
 
-// Brings a multiple of 16 bytes at an aligned address to L2.
-__device__ __forceinline__ void bulk_prefetch(const void* src, uint32_t bytes)
-{
-    asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(src), "r"(bytes) : "memory");
-}
+// The line that holds an address, to L2.
+__device__ __forceinline__ void prefetch_l2(const void* src) { asm volatile("prefetch.global.L2 [%0];" ::"l"(src)); }
 
 __device__ __forceinline__ void cp_async_16s(uint32_t dst, const void* src, uint32_t src_bytes)
 {

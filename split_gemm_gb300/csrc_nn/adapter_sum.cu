@@ -352,7 +352,7 @@ __global__ void __launch_bounds__(U_THREADS, 1) sum_tiles(const __grid_constant_
     uint32_t* slot = reinterpret_cast<uint32_t*>(free_ + 1);
     volatile uint32_t* abort_flag = slot + 1;
     volatile int* count = reinterpret_cast<volatile int*>(slot + 2);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     const int piece = blockIdx.x / p.per_piece, block = blockIdx.x % p.per_piece;
     const SumJob& job = p.jobs[block >= p.jobs[0].col_blocks];
     const int c0 = (block - (block >= p.jobs[0].col_blocks ? p.jobs[0].col_blocks : 0)) * 128 * s.blocks;
