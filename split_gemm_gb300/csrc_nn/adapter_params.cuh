@@ -32,7 +32,7 @@ constexpr int P_ROOM = 227 * 1024;  // bytes of shared memory
 constexpr int W1_COLUMN = P_STEP * 16 + 16;
 
 // Shared memory by the rank padded to 16 and the halving of tiles: an area that holds the first product's ring and, when that is over, the
-// sums (from its start), mid's parts (to its end) and w2's chunks (downwards from the parts; over the sums, once those are joined); beside it w2's first
+// sums (from its start), mid (to its end) and w2's chunks (downwards from mid; over the sums, once those are joined); beside it w2's first
 // chunk, barriers and lists.  A chunk of w2: core matrices 144 bytes apart along the columns, so that the pairs that the backward
 // pass places one by one fall into different banks.
 struct PassSmem {
@@ -44,18 +44,16 @@ struct PassSmem {
     __host__ __device__ constexpr int rest() const { return 512 + TILE * 4; }
     __host__ __device__ constexpr int area() const { return (P_ROOM - chunk() - rest()) / 128 * 128; }
     __host__ __device__ constexpr int stages() const { return area() / stage() < P_MOST_STAGES ? area() / stage() : P_MOST_STAGES; }
-    __host__ __device__ constexpr int pitch() const { return rp + 4; }  // of the sums' rows, in words
-    __host__ __device__ constexpr int sums() const { return TILE * pitch() * 4; }
-    __host__ __device__ constexpr int group() const { return 3 * rp / 8 * 128; }  // of parts: 8 rows
-    __host__ __device__ constexpr int parts() const { return TILE / 8 * group(); }
-    __host__ __device__ constexpr int chunks() const { return 1 + (area() - parts()) / chunk() < P_MOST_CHUNKS ? 1 + (area() - parts()) / chunk() : P_MOST_CHUNKS; }
+    __host__ __device__ constexpr int pitch() const { return rp + 4; }  // of the rows of sums and mid, in words
+    __host__ __device__ constexpr int sums() const { return TILE * pitch() * 4; }  // and mid's bytes
+    __host__ __device__ constexpr int chunks() const { return 1 + (area() - sums()) / chunk() < P_MOST_CHUNKS ? 1 + (area() - sums()) / chunk() : P_MOST_CHUNKS; }
     __host__ __device__ constexpr int early_chunks() const  // that do not lie over the sums
     {
-        const int n = 1 + (area() - parts() - sums()) / chunk();
+        const int n = 1 + (area() - sums() - sums()) / chunk();
         return n < chunks() ? n : chunks();
     }
 };
-static_assert(PassSmem(128, 1).area() >= PassSmem(128, 1).parts() + PassSmem(128, 1).sums() && PassSmem(128, 1).chunks() >= 3, "the widest rank fits");
+static_assert(PassSmem(128, 1).area() >= 2 * PassSmem(128, 1).sums() && PassSmem(128, 1).chunks() >= 3, "the widest rank fits");
 
 // Sums over the adapters' rows: out[e] (r, c) = sum of mid[t][r] * in[t][c].
 struct SumJob {

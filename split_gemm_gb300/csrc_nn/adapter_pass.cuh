@@ -12,7 +12,8 @@
 // the parts meet in shared memory as fp32, are joined in the CTAs' order and cut into three bf16 parts that
 // hold all 24 bits: the second product, K = 3 * rank, is that of an fp32 mid.
 //
-// Second product: 64 columns of `to` at a time, two accumulators in turn.  A thread reads the accumulator in the 16 x 256-bit layout, 2
+// Second product: mid's parts are its A operand in tensor memory (from shared memory they would be read once for each chunk and take
+// most of its bandwidth), 64 columns of `to` (128 of tiles of 64 rows) its B.  Two groups of 8 warps finish chunks by turns.  A thread reads the accumulator in the 16 x 256-bit layout, 2
 // neighbouring columns of a lane in each group of 8; w2's rows are placed in shared memory in an order that makes these 8 neighbouring columns of out, so base and
 // out move in 16-byte vectors straight between registers and memory, base a chunk ahead.
 //
@@ -29,17 +30,18 @@ namespace ad {
 constexpr int P_WARPS = 16, P_LOADERS = 32 * P_WARPS, P_THREADS = P_LOADERS + 32;
 constexpr int P_GROUP = P_LOADERS / 2;  // threads that finish a chunk
 constexpr uint64_t P_WAIT_NS = 1000000000ull;
-constexpr uint32_t P_TMEM = 512;  // four chunks of up to 128 columns; the first product's sums before them
+constexpr uint32_t P_TMEM = 512;  // the first product's sums, then 256 columns of chunks; mid's parts at the end
 
 template <bool TRANS, bool VEC, int HALVED, typename TB, typename TO>
 struct Pass {
     static constexpr int ROWS = TILE >> HALVED, COLS = 64 << HALVED;  // of a tile; of `to`, in a chunk
+    static constexpr int BUFS = 4 >> HALVED;                           // accumulators of chunks
     static constexpr int LANES = 32 >> HALVED;                        // of a warp's 32 lanes of tensor memory that hold rows
 
     const PassParams& p;
     const PassSmem s;
     uint8_t* mem;
-    uint64_t *full, *empty, *done, *w2_full, *d_full, *d_empty, *parts_full;
+    uint64_t *full, *empty, *done, *w2_full, *d_full, *d_empty, *mid_full;
     int* ids;  // numbers of the tile's rows
     uint32_t* slot;
     volatile uint32_t* abort_flag;
@@ -58,8 +60,8 @@ struct Pass {
         w2_full = done + 1;
         d_full = w2_full + P_MOST_CHUNKS;
         d_empty = d_full + 4;
-        parts_full = d_empty + 4;
-        ids = reinterpret_cast<int*>(parts_full + 1);
+        mid_full = d_empty + 4;
+        ids = reinterpret_cast<int*>(mid_full + 1);
         slot = reinterpret_cast<uint32_t*>(ids + TILE);
         abort_flag = slot + 1;
         tid = threadIdx.x;
@@ -77,8 +79,8 @@ struct Pass {
         }
         return ok;
     }
-    __device__ __forceinline__ uint8_t* parts() const { return mem + s.area() - s.parts(); }
-    __device__ __forceinline__ uint8_t* w2_buf(int i) const { return i ? parts() - i * s.chunk() : mem + s.area(); }
+    __device__ __forceinline__ float* mids() const { return reinterpret_cast<float*>(mem + s.area() - s.sums()); }
+    __device__ __forceinline__ uint8_t* w2_buf(int i) const { return i ? mem + s.area() - s.sums() - i * s.chunk() : mem + s.area(); }
 
     // 16 bytes of row elements from `src`, `valid` elements of them; aligned copies run by themselves, others go through registers.
     __device__ __forceinline__ void copy8(uint32_t dst, const __nv_bfloat16* src, int valid) const
@@ -209,7 +211,7 @@ struct Pass {
         if (VEC) ptx::fence_proxy_async_smem();
     }
 
-    // This CTA's rows of the sums over the cluster: scaled, to mid, in three parts, and on to every CTA.
+    // This CTA's rows of the sums over the cluster: scaled, to mid, and on to every CTA.
     template <int S>
     __device__ __forceinline__ void join(const float* sums, float scale) const
     {
@@ -253,27 +255,42 @@ struct Pass {
                     }
                 }
             }
-            uint32_t part[3][4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                uint32_t a[3], b[3];
-                split3(v[2 * j], a[0], a[1], a[2]);
-                split3(v[2 * j + 1], b[0], b[1], b[2]);
-#pragma unroll
-                for (int q = 0; q < 3; ++q) part[q][j] = a[q] | b[q] << 16;
-            }
-            const uint32_t to = ptx::smem_addr(parts()) + (row & 7) * 16 + (lane_of(row) >> 3) * s.group();
-#pragma unroll
-            for (int q = 0; q < 3; ++q) ptx::st_shared_v4(to + ((q * s.rp + r) >> 3) * 128, part[q][0], part[q][1], part[q][2], part[q][3]);
+            float* mine = mids() + row * s.pitch() + r;
+            reinterpret_cast<float4*>(mine)[0] = make_float4(v[0], v[1], v[2], v[3]);
+            reinterpret_cast<float4*>(mine)[1] = make_float4(v[4], v[5], v[6], v[7]);
         }
         ptx::fence_proxy_async_smem();
         __syncthreads();
-        constexpr int GROUPS = SHARE / 8;  // of 8 rows, that this CTA hands on
-        const int to = tid / GROUPS;
-        if (S > 1 && to < S && to != rank_in) {
-            const uint32_t at = ptx::smem_addr(parts()) + (lane_of(rank_in * SHARE + tid % GROUPS * 8) >> 3) * s.group();
-            ptx::bulk_to_cluster(ptx::mapa_shared(at, to), at, s.group(), ptx::mapa_shared(ptx::smem_addr(parts_full), to));
+        if (S > 1 && tid < S && tid != rank_in) {
+            const uint32_t at = ptx::smem_addr(mids() + rank_in * SHARE * s.pitch());
+            ptx::bulk_to_cluster(ptx::mapa_shared(at, tid), at, SHARE * s.pitch() * 4, ptx::mapa_shared(ptx::smem_addr(mid_full), tid));
         }
+    }
+
+    // mid's three parts to tensor memory, two neighbouring ranks to a column.
+    __device__ __forceinline__ void store_parts(uint32_t to) const
+    {
+        const float* row = mids() + (LANES * (warp & 3) + (lane & (LANES - 1))) * s.pitch();
+        for (int r = 16 * (warp >> 2); r < s.rp; r += 64) {
+            uint32_t part[3][8];
+#pragma unroll
+            for (int j = 0; j < 8; j += 2) {
+                const float4 v = *reinterpret_cast<const float4*>(row + r + 2 * j);
+                uint32_t a[3], b[3], c[3], d[3];
+                split3(v.x, a[0], a[1], a[2]);
+                split3(v.y, b[0], b[1], b[2]);
+                split3(v.z, c[0], c[1], c[2]);
+                split3(v.w, d[0], d[1], d[2]);
+#pragma unroll
+                for (int q = 0; q < 3; ++q) {
+                    part[q][j] = a[q] | b[q] << 16;
+                    part[q][j + 1] = c[q] | d[q] << 16;
+                }
+            }
+#pragma unroll
+            for (int q = 0; q < 3; ++q) ptx::tmem_st_32x32b_x8(to + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + ((q * s.rp + r) >> 1), part[q]);
+        }
+        ptx::tmem_st_wait();
     }
 
     // A thread finishes four times 8 neighbouring elements of a chunk, SIDES side by side at 32 columns' distance in each of 4 / SIDES rows, 8 rows
@@ -414,12 +431,12 @@ struct Pass {
             }
             ptx::mbar_init(done, 1);
             for (int i = 0; i < n_bufs; ++i) ptx::mbar_init(&w2_full[i], P_GROUP);
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < BUFS; ++i) {
                 ptx::mbar_init(&d_full[i], 1);
                 ptx::mbar_init(&d_empty[i], P_WARPS / 2);
             }
-            ptx::mbar_init(parts_full, 1);
-            if (p.splits > 1) ptx::mbar_arrive_expect_tx(parts_full, (ROWS - ROWS / p.splits) / 8 * s.group());
+            ptx::mbar_init(mid_full, 1);
+            if (p.splits > 1) ptx::mbar_arrive_expect_tx(mid_full, (ROWS - ROWS / p.splits) * s.pitch() * 4);
             *abort_flag = 0u;
             ptx::mbar_init_fence();
         }
@@ -524,36 +541,37 @@ struct Pass {
             default: join<8>(sums, scale); break;
         }
         if (warp < P_WARPS) fill(1, s.early_chunks(), chunk0, chunk1);
-        // All parts are here: none of this CTA's peers reads its sums any more, and what they sent has come.
+        // All of mid is here: none of this CTA's peers reads its sums any more, and what they sent has come.
         if (p.splits > 1) {
-            wait(parts_full, 0, ok);
+            wait(mid_full, 0, ok);
             __syncwarp();
             ptx::cluster_arrive_relaxed();
         }
+        const uint32_t parts = tmem + P_TMEM - 3 * s.rp / 2;
+        if (warp < P_WARPS) {
+            store_parts(parts);
+            ptx::tc_fence_before();
+        }
+        __syncthreads();
         if (warp < P_WARPS) fill(s.early_chunks(), n_bufs, chunk0, chunk1);
         const int n = chunk1 - chunk0;
         if (warp == P_WARPS) {
             ok = __all_sync(0xffffffffu, ok);
-            ptx::fence_proxy_async_smem();
             ptx::tc_fence_after();
-            const uint32_t a = ptx::smem_addr(parts());
             for (int j = 0; j < n; ++j) {
-                const int b = j & 3, buf = j % n_bufs;
+                const int b = j & (BUFS - 1), buf = j % n_bufs;
                 wait(&w2_full[buf], static_cast<uint32_t>(j / n_bufs) & 1u, ok);
-                wait(&d_empty[b], (static_cast<uint32_t>(j >> 2) & 1u) ^ 1u, ok);
+                wait(&d_empty[b], (static_cast<uint32_t>(j / BUFS) & 1u) ^ 1u, ok);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 ptx::fence_proxy_async_smem();
                 ptx::tc_fence_after();
                 const uint32_t w = ptx::smem_addr(w2_buf(buf));
-                // the three parts of 32 of mid's columns at a time
-                const uint64_t ad = ptx::plain_kmajor_desc(a, 128, s.group()), wd = ptx::plain_kmajor_desc(w, s.column(), 144);
+                const uint64_t wd = ptx::plain_kmajor_desc(w, s.column(), 144), w_step = 2 * s.column() / 16;
                 const uint32_t idesc = TRANS ? ptx::idesc_bf16_f32_bmn(TILE, COLS) : ptx::idesc_bf16_f32(TILE, COLS);
-                const uint64_t part = s.rp / 8 * (128 / 16), w_step = 2 * s.column() / 16;
-                const int whole = s.rp / 32;
-                for (int k = 0; k < whole; ++k)
-                    ptx::mma_bf16_elect_3x2(tmem + COLS * b, ad + k * 32, wd + 2 * k * w_step, part, 16, w_step, idesc, k > 0);
-                if (s.rp & 16) ptx::mma_bf16_elect_x3(tmem + COLS * b, ad + whole * 32, wd + 2 * whole * w_step, part, idesc, whole > 0);
+                const int whole = s.rp / 32;  // of the reduction, in twice three MMAs
+                for (int k = 0; k < whole; ++k) ptx::mma_bf16_parts_x2(tmem + COLS * b, parts + 16 * k, wd + 2 * k * w_step, s.rp / 2, w_step, idesc, k > 0);
+                if (s.rp & 16) ptx::mma_bf16_parts(tmem + COLS * b, parts + 16 * whole, wd + 2 * whole * w_step, s.rp / 2, idesc, whole > 0);
                 ptx::mma_commit_elect(&d_full[b]);
             }
         } else if (group < n) {
@@ -566,13 +584,13 @@ struct Pass {
                 for (int jj = 0; jj < 2 / TURNS; ++jj) {
                     const int j = j0 + 2 * jj;
                     if (j >= n) break;
-                    const int b = j & 3, c0 = (chunk0 + j) * COLS;
+                    const int b = j & (BUFS - 1), c0 = (chunk0 + j) * COLS;
                     const bool whole = c0 + COLS <= p.to, next = c0 + 3 * COLS <= p.to;
                     if (TURNS == 2)
                         load_base(held[1], 1, c0, whole);
                     else if (j + 2 < n)
                         load_base(held[(jj + 1) & 1], 0, c0 + 2 * COLS, next);
-                    wait(&d_full[b], static_cast<uint32_t>(j >> 2) & 1u, ok);
+                    wait(&d_full[b], static_cast<uint32_t>(j / BUFS) & 1u, ok);
                     __syncwarp();
                     ptx::tc_fence_after();
                     uint32_t v[2][16];

@@ -60,42 +60,52 @@ __device__ __forceinline__ void mma_bf16_elect_x2(uint32_t d_tmem, uint64_t a_de
         : "memory");
 }
 
-// The same for pairs of three MMAs, A's descriptors `a_part` apart in a triple with one B; the pair's triples `a_step` and `b_step` apart.
-__device__ __forceinline__ void mma_bf16_elect_3x2(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint64_t a_part, uint64_t a_step, uint64_t b_step,
-                                                   uint32_t idesc, uint32_t accumulate)
+// The same for A in tensor memory, in three parts: three MMAs with one B, A's columns `a_part` apart, and three with the next, 8 columns (16 of
+// the reduction) and `b_step` on.
+__device__ __forceinline__ void mma_bf16_parts_x2(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t a_part, uint64_t b_step, uint32_t idesc,
+                                                  uint32_t accumulate)
 {
     asm volatile(
-        "{\n\t.reg .pred p, e, t;\n\t.reg .b64 a1, a2, a3, a4, a5, b1;\n\t"
-        "setp.ne.b32 p, %7, 0;\n\t"
+        "{\n\t.reg .pred p, e, t;\n\t.reg .b32 a1, a2, a3, a4, a5;\n\t.reg .b64 b1;\n\t"
+        "setp.ne.b32 p, %6, 0;\n\t"
         "setp.eq.b32 t, 0, 0;\n\t"
-        "add.s64 a1, %1, %3;\n\tadd.s64 a2, a1, %3;\n\tadd.s64 a3, %1, %4;\n\tadd.s64 a4, a3, %3;\n\tadd.s64 a5, a4, %3;\n\t"
-        "add.s64 b1, %2, %5;\n\t"
+        "add.s32 a1, %1, %3;\n\tadd.s32 a2, a1, %3;\n\tadd.s32 a3, %1, 8;\n\tadd.s32 a4, a1, 8;\n\tadd.s32 a5, a2, 8;\n\t"
+        "add.s64 b1, %2, %4;\n\t"
         "elect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %6, p;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, %2, %6, t;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, %2, %6, t;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a3, b1, %6, t;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a4, b1, %6, t;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a5, b1, %6, t;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "l"(a_part), "l"(a_step), "l"(b_step), "r"(idesc), "r"(accumulate)
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %5, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], %2, %5, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], %2, %5, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a3], b1, %5, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a4], b1, %5, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a5], b1, %5, t;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(a_part), "l"(b_step), "r"(idesc), "r"(accumulate)
         : "memory");
 }
 
-// One triple.
-__device__ __forceinline__ void mma_bf16_elect_x3(uint32_t d_tmem, uint64_t a_desc, uint64_t b_desc, uint64_t a_part, uint32_t idesc, uint32_t accumulate)
+// The first three alone.
+__device__ __forceinline__ void mma_bf16_parts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t a_part, uint32_t idesc, uint32_t accumulate)
 {
     asm volatile(
-        "{\n\t.reg .pred p, e, t;\n\t.reg .b64 a1, a2;\n\t"
+        "{\n\t.reg .pred p, e, t;\n\t.reg .b32 a1, a2;\n\t"
         "setp.ne.b32 p, %5, 0;\n\t"
         "setp.eq.b32 t, 0, 0;\n\t"
-        "add.s64 a1, %1, %3;\n\tadd.s64 a2, a1, %3;\n\t"
+        "add.s32 a1, %1, %3;\n\tadd.s32 a2, a1, %3;\n\t"
         "elect.sync _|e, 0xffffffff;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %4, p;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a1, %2, %4, t;\n\t"
-        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], a2, %2, %4, t;\n\t}" ::"r"(d_tmem),
-        "l"(a_desc), "l"(b_desc), "l"(a_part), "r"(idesc), "r"(accumulate)
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %4, p;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a1], %2, %4, t;\n\t"
+        "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [a2], %2, %4, t;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(a_part), "r"(idesc), "r"(accumulate)
         : "memory");
 }
+
+// 8 columns of the warp's 32 lanes from each thread's registers, and the wait for such stores.
+__device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t (&v)[8])
+{
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(taddr), "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]),
+                 "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Four bytes, zero where `src_bytes` is 0 (the address need only be valid for 4 bytes).
 __device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src, uint32_t src_bytes)
