@@ -34,13 +34,13 @@ constexpr int W1_COLUMN = P_STEP * 16 + 16;
 // Shared memory by the rank padded to 16 and the halving of tiles: an area that holds the first product's ring and, when that is over, the
 // sums (from its start), mid (to its end) and w2's chunks (downwards from mid; over the sums, once those are joined); beside it w2's first
 // chunk, barriers and lists.  A chunk of w2: core matrices 144 bytes apart along the columns, so that the pairs that the backward
-// pass places one by one fall into different banks.
+// pass places one by one fall into different banks, and 16 bytes more from one column of 8 ranks to the next, for the forward pass's vectors.
 struct PassSmem {
     int rp, cols;  // cols: of `to`, in a chunk
     __host__ __device__ constexpr PassSmem(int rank, int halved) : rp((rank + 15) / 16 * 16), cols(64 << halved) {}
     __host__ __device__ constexpr int stage() const { return TILE * P_STEP * 2 + (rp / 8 * W1_COLUMN + 1023) / 1024 * 1024; }
-    __host__ __device__ constexpr int column() const { return cols / 8 * 144; }  // of a chunk: 8 ranks
-    __host__ __device__ constexpr int chunk() const { return rp / 8 * column(); }
+    __host__ __device__ constexpr int column() const { return cols / 8 * 144 + 16; }  // of a chunk: 8 ranks
+    __host__ __device__ constexpr int chunk() const { return (rp / 8 * column() + 127) / 128 * 128; }
     __host__ __device__ constexpr int rest() const { return 512 + TILE * 4; }
     __host__ __device__ constexpr int area() const { return (P_ROOM - chunk() - rest()) / 128 * 128; }
     __host__ __device__ constexpr int stages() const { return area() / stage() < P_MOST_STAGES ? area() / stage() : P_MOST_STAGES; }

@@ -206,9 +206,9 @@ struct Pass {
     // The part of a chunk of w2 that pads an odd number of 8 ranks; whole copies do not reach it.
     __device__ __forceinline__ void clear_pad(uint8_t* buf) const
     {
-        if (VEC && (p.rank & 8) && gtid < COLS)
-            ptx::st_shared_v4(ptx::smem_addr(buf) + (gtid & 7) * 16 + (gtid >> 3) * 144 + (p.rank >> 3) * s.column(), 0u, 0u, 0u, 0u);
-        if (VEC) ptx::fence_proxy_async_smem();
+        if (!VEC || !(p.rank & 8)) return;
+        if (gtid < COLS) ptx::st_shared_v4(ptx::smem_addr(buf) + (gtid & 7) * 16 + (gtid >> 3) * 144 + (p.rank >> 3) * s.column(), 0u, 0u, 0u, 0u);
+        ptx::fence_proxy_async_smem();
     }
 
     // This CTA's rows of the sums over the cluster: scaled, to mid, and on to every CTA.
