@@ -53,7 +53,7 @@ struct PassSmem {
         return n < chunks() ? n : chunks();
     }
 };
-static_assert(PassSmem(128, 1).area() >= 2 * PassSmem(128, 1).sums() && PassSmem(128, 1).chunks() >= 3, "the widest rank fits");
+static_assert(PassSmem(128, 1).area() >= 2 * PassSmem(128, 1).sums() && PassSmem(128, 1).early_chunks() >= 2 && PassSmem(128, 1).stages() >= 4, "the widest rank fits");
 
 // Sums over the adapters' rows: out[e] (r, c) = sum of mid[t][r] * in[t][c].
 struct SumJob {

@@ -71,13 +71,13 @@ struct Pass {
         group = warp >> 3;
         gtid = tid & (P_GROUP - 1);
     }
-    __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, bool& ok) const
+    // Once a wait has run out, `ok` is false and the thread waits no more: it goes on through its barriers with whatever is in memory.
+    __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, bool& ok) const
     {
-        if (ok && !ptx::mbar_wait(bar, parity, P_WAIT_NS)) {
+        if (!ptx::mbar_try_wait(bar, parity) && ok && !ptx::mbar_wait(bar, parity, P_WAIT_NS)) {
             ok = false;
             *abort_flag = 1u;
         }
-        return ok;
     }
     __device__ __forceinline__ float* mids() const { return reinterpret_cast<float*>(mem + s.area() - s.sums()); }
     __device__ __forceinline__ uint8_t* w2_buf(int i) const { return i ? mem + s.area() - s.sums() - i * s.chunk() : mem + s.area(); }
@@ -93,15 +93,13 @@ struct Pass {
             ptx::st_shared_v4(dst, v[0], v[1], v[2], v[3]);
         }
     }
-    // This thread's part of what `bar` counts is there.
+    // This warp's part of what `bar` counts is there (its threads have waited for their copies).  One arrival to a warp: a barrier takes its
+    // arrivals one after another, and 512 of them cost as much as the stage.
     __device__ __forceinline__ void arrive(uint64_t* bar) const
     {
-        if constexpr (VEC) {
-            ptx::cp_async_arrive_noinc(bar);
-        } else {
-            ptx::fence_proxy_async_smem();
-            ptx::mbar_arrive(bar);
-        }
+        if (!VEC) ptx::fence_proxy_async_smem();
+        __syncwarp();
+        ptx::mbar_arrive_if(bar, lane == 0);
     }
 
     // The accumulator's lane of row i: a halved tile has 16 rows in each warp's 32 lanes, so that all warps finish chunks.
@@ -133,16 +131,16 @@ struct Pass {
         if (VEC && f0 + P_STEP <= p.from) {
 #pragma unroll
             for (int i = 0; i < ROWS / 64; ++i)
-                if (row + 64 * i < piece.rows) ptx::cp_async_16s(at + mine + 8192 * i, rows[i] + f0, 16);
+                ptx::cp_async_16_if(at + mine + 8192 * i, rows[i] + f0, row + 64 * i < piece.rows);
             if constexpr (!TRANS) {
                 const __nv_bfloat16* src = w + static_cast<int64_t>(row) * p.from + f0 + 8 * c8;
-                if (row < p.rank) ptx::cp_async_16s(w_at + row * 128 + swizzled, src, 16);
-                if (row + 64 < p.rank) ptx::cp_async_16s(w_at + row * 128 + swizzled + 8192, src + 64 * static_cast<int64_t>(p.from), 16);
+                ptx::cp_async_16_if(w_at + row * 128 + swizzled, src, row < p.rank);
+                ptx::cp_async_16_if(w_at + row * 128 + swizzled + 8192, src + 64 * static_cast<int64_t>(p.from), row + 64 < p.rank);
             } else {
                 const __nv_bfloat16* src = w + static_cast<int64_t>(f0) * p.rank + 8 * tid;
 #pragma unroll
                 for (int i = 0; i < PLACES; ++i)
-                    if (place[i] != 0xffffffffu) ptx::cp_async_16s(w_at + place[i], src + 8 * P_LOADERS * i, 16);
+                    ptx::cp_async_16_if(w_at + place[i], src + 8 * P_LOADERS * i, place[i] != 0xffffffffu);
             }
             return;
         }
@@ -174,12 +172,15 @@ struct Pass {
                     const __nv_bfloat16* src = w + static_cast<int64_t>(c0) * p.rank + 8 * gtid;
 #pragma unroll
                     for (int i = 0; i < PLACES; ++i)
-                        if (place[i] != 0xffffffffu) ptx::cp_async_16s(at + place[i], src + 8 * P_GROUP * i, 16);
+                        ptx::cp_async_16_if(at + place[i], src + 8 * P_GROUP * i, place[i] != 0xffffffffu);
                 } else {
                     const int c = 2 * lane, gwarp = warp & 7;
                     uint32_t dst = at + gwarp * 16 + ((c >> 3) & 3) * 4 + (((c >> 1) & 3) + 4 * (c >> 5)) * 144;
                     const __nv_bfloat16* src = w + static_cast<int64_t>(gwarp) * p.to + c0 + c;
-                    for (int k = gwarp; k < p.rank; k += 8, dst += s.column(), src += 8 * static_cast<int64_t>(p.to)) ptx::cp_async_4(dst, src, 4);
+                    for (int k = gwarp; k < s.rp; k += 16, dst += 2 * s.column(), src += 16 * static_cast<int64_t>(p.to)) {
+                        ptx::cp_async_4_if(dst, src, k < p.rank);
+                        ptx::cp_async_4_if(dst + s.column(), src + 8 * static_cast<int64_t>(p.to), k + 8 < p.rank);
+                    }
                 }
             } else if constexpr (!TRANS) {
                 for (int i = gtid; i < s.rp * 8; i += P_GROUP) {
@@ -308,32 +309,31 @@ struct Pass {
     __device__ __forceinline__ int col_of(int i, int c0) const { return c0 + 32 * SIDES * ((warp >> 2) & 1) + 32 * side_of(i) + 8 * (lane & 3); }
     __device__ __forceinline__ void make_rows()
     {
-        rows_here = 0u;
 #pragma unroll
         for (int i = 0; i < 4 / SIDES; ++i) {
             const int64_t t = ids[row_of(i)];
-            if (row_of(i) < piece.rows) rows_here |= 1u << i;
+            row_here[i] = row_of(i) < piece.rows;
+            base_here[i] = row_here[i] && p.base;
             base_at[i] = static_cast<const TB*>(p.base) + t * p.base_stride + col_of(i, 0);
             out_at[i] = static_cast<TO*>(p.out) + t * p.out_stride + col_of(i, 0);
         }
     }
-    uint32_t rows_here;  // bit i: row_index i of the thread's is one of the tile's
+    bool row_here[4 / SIDES], base_here[4 / SIDES];  // the thread's rows are of the tile; and there is a base
     // Turn `turn` of the chunk at c0; `whole`: all its columns exist.
-    __device__ __forceinline__ void load_base(Held& b, int turn, int c0, bool whole) const
+    __device__ __forceinline__ void load_base(Held& b, int turn, int c0, bool whole, bool wanted = true) const
     {
 #pragma unroll
         for (int k = 0; k < HOLD; ++k) {
             const int i = turn * HOLD + k;
             const TB* src = base_at[row_index(i)] + c0 + 32 * side_of(i);
-            const int left = !(rows_here >> row_index(i) & 1u) || !p.base ? 0 : whole ? 8 : p.to - col_of(i, c0);
             if constexpr (VEC) {
 #pragma unroll
                 for (int j = 0; j < WORDS; j += 4) {
-                    uint4 q = make_uint4(0, 0, 0, 0);
-                    if (left > 0) q = __ldcs(reinterpret_cast<const uint4*>(src) + j / 4);
+                    const uint4 q = ptx::ld_stream_v4_if(reinterpret_cast<const uint4*>(src) + j / 4, wanted && base_here[row_index(i)] && (whole || col_of(i, c0) < p.to));
                     b.u[k][j] = q.x, b.u[k][j + 1] = q.y, b.u[k][j + 2] = q.z, b.u[k][j + 3] = q.w;
                 }
             } else {
+                const int left = wanted && base_here[row_index(i)] ? p.to - col_of(i, c0) : 0;
                 TB* v = reinterpret_cast<TB*>(b.u[k]);
 #pragma unroll
                 for (int j = 0; j < WORDS; ++j) b.u[k][j] = 0u;
@@ -343,39 +343,53 @@ struct Pass {
             }
         }
     }
-    // out = act(base + sum) for 8 elements: `base` theirs, `v` their sums as they come from tensor memory.
-    __device__ __forceinline__ void finish(const uint32_t (&base)[WORDS], float2 (&v)[4], int i, int c0, bool whole, bool live) const
+    // out = act(base + sum) for a turn: `v` the chunk's sums as they come from tensor memory.
+    __device__ __forceinline__ void finish(const Held& b, const uint32_t (&v)[2][16], int turn, int c0, bool whole, bool live) const
     {
+        float2 f[HOLD][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float2 b = sizeof(TB) == 2 ? make_float2(__uint_as_float(base[j] << 16), __uint_as_float(base[j] & 0xffff0000u))
-                                             : make_float2(__uint_as_float(base[2 * j % WORDS]), __uint_as_float(base[(2 * j + 1) % WORDS]));
-            v[j] = mx::add2(v[j], b);
+        for (int k = 0; k < HOLD; ++k) {
+            const int i = turn * HOLD + k;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 sum = make_float2(__uint_as_float(v[i >> 1][4 * j + 2 * (i & 1)]), __uint_as_float(v[i >> 1][4 * j + 2 * (i & 1) + 1]));
+                const float2 base = sizeof(TB) == 2 ? make_float2(__uint_as_float(b.u[k][j] << 16), __uint_as_float(b.u[k][j] & 0xffff0000u))
+                                                    : make_float2(__uint_as_float(b.u[k][2 * j % WORDS]), __uint_as_float(b.u[k][(2 * j + 1) % WORDS]));
+                f[k][j] = mx::add2(sum, base);
+            }
         }
         if (p.relu)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) v[j] = make_float2(v[j].x < 0.f ? 0.f : v[j].x, v[j].y < 0.f ? 0.f : v[j].y);
-        TO* row = out_at[row_index(i)] + c0 + 32 * side_of(i);
-        const int left = !(rows_here >> row_index(i) & 1u) || !live ? 0 : whole ? 8 : p.to - col_of(i, c0);
-        if constexpr (VEC) {  // made first, so that the stores are predicated
-            if constexpr (sizeof(TO) == 4) {
-                const float4 lo = make_float4(v[0].x, v[0].y, v[1].x, v[1].y), hi = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
-                if (left > 0) __stcs(reinterpret_cast<float4*>(row), lo);
-                if (left > 0) __stcs(reinterpret_cast<float4*>(row) + 1, hi);
-            } else {
-                uint32_t o[4];
+            for (int k = 0; k < HOLD; ++k)
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const __nv_bfloat162 h = __floats2bfloat162_rn(v[j].x, v[j].y);
-                    o[j] = *reinterpret_cast<const uint32_t*>(&h);
+                for (int j = 0; j < 4; ++j)
+                    f[k][j] = make_float2(__uint_as_float(ptx::relu_nan(__float_as_uint(f[k][j].x))), __uint_as_float(ptx::relu_nan(__float_as_uint(f[k][j].y))));
+#pragma unroll
+        for (int k = 0; k < HOLD; ++k) {
+            const int i = turn * HOLD + k;
+            TO* row = out_at[row_index(i)] + c0 + 32 * side_of(i);
+            if constexpr (VEC) {
+                const bool here = live && row_here[row_index(i)] && (whole || col_of(i, c0) < p.to);
+                if constexpr (sizeof(TO) == 4) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        ptx::st_stream_v4_if(row + 4 * h, make_uint4(__float_as_uint(f[k][2 * h].x), __float_as_uint(f[k][2 * h].y), __float_as_uint(f[k][2 * h + 1].x),
+                                                                     __float_as_uint(f[k][2 * h + 1].y)), here);
+                } else {
+                    uint32_t o[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(f[k][j].x, f[k][j].y);
+                        o[j] = *reinterpret_cast<const uint32_t*>(&h);
+                    }
+                    ptx::st_stream_v4_if(row, make_uint4(o[0], o[1], o[2], o[3]), here);
                 }
-                const uint4 q = make_uint4(o[0], o[1], o[2], o[3]);
-                if (left > 0) __stcs(reinterpret_cast<uint4*>(row), q);
-            }
-        } else {
+            } else {
+                const int left = live && row_here[row_index(i)] ? p.to - col_of(i, c0) : 0;
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                if (j < left) mx::from_float(row[j], j % 2 ? v[j / 2].y : v[j / 2].x);
+                for (int j = 0; j < 8; ++j)
+                    if (j < left) mx::from_float(row[j], j % 2 ? f[k][j / 2].y : f[k][j / 2].x);
+            }
         }
     }
 
@@ -391,15 +405,18 @@ struct Pass {
         }
     }
 
-    // The first filling of w2's buffers i0 .. i1, each by the group whose chunk it is for.
+    // The first filling of w2's buffers i0 .. i1, each by the group whose chunk it is for, and the word that they are there.
     __device__ __forceinline__ void fill(int i0, int i1, int chunk0, int chunk1) const
     {
-        for (int i = i0; i < i1; ++i) {
-            if ((i & 1) != group) continue;
+        for (int i = i0 + ((i0 ^ group) & 1); i < i1; i += 2) {
             clear_pad(w2_buf(i));
             if (chunk0 + i < chunk1) load_w2(w2_buf(i), (chunk0 + i) * COLS);
-            arrive(&w2_full[i]);
         }
+        ptx::cp_async_commit();
+    }
+    __device__ __forceinline__ void filled(int i0, int i1) const
+    {
+        for (int i = i0 + ((i0 ^ group) & 1); i < i1; i += 2) arrive(&w2_full[i]);
     }
 
     // Rows without an adapter: out = act(base), mid = 0.
@@ -414,11 +431,8 @@ struct Pass {
             for (int turn = 0; turn < TURNS; ++turn) {
                 Held b;
                 load_base(b, turn, c * COLS, false);
-#pragma unroll
-                for (int k = 0; k < HOLD; ++k) {
-                    float2 v[4] = {};
-                    finish(b.u[k], v, turn * HOLD + k, c * COLS, false, true);
-                }
+                const uint32_t none[2][16] = {};
+                finish(b, none, turn, c * COLS, false, true);
             }
     }
 
@@ -426,11 +440,11 @@ struct Pass {
     {
         if (tid == 0) {
             for (int i = 0; i < n_stages; ++i) {
-                ptx::mbar_init(&full[i], P_LOADERS);
+                ptx::mbar_init(&full[i], P_WARPS);
                 ptx::mbar_init(&empty[i], 1);
             }
             ptx::mbar_init(done, 1);
-            for (int i = 0; i < n_bufs; ++i) ptx::mbar_init(&w2_full[i], P_GROUP);
+            for (int i = 0; i < n_bufs; ++i) ptx::mbar_init(&w2_full[i], P_WARPS / 2);
             for (int i = 0; i < BUFS; ++i) {
                 ptx::mbar_init(&d_full[i], 1);
                 ptx::mbar_init(&d_empty[i], P_WARPS / 2);
@@ -487,26 +501,45 @@ struct Pass {
 #pragma unroll
             for (int i = 0; i < ROWS / 64; ++i) rows[i] = p.in + ids[(tid >> 3) + 64 * i] * p.in_stride + 8 * (tid & 7);
             if (VEC) make_places();
-            for (int f = s0; f < s1; ++f) {
-                const int it = f - s0, at = it % n_stages;
-                if (!wait(&empty[at], (static_cast<uint32_t>(it / n_stages) & 1u) ^ 1u, ok)) break;
-                load_stage(mem + at * s.stage(), f * P_STEP, rows);
-                arrive(&full[at]);
+            constexpr int LAG = VEC ? 3 : 0;  // stages on their way behind the one that is asked for
+            int at = 0, told = 0;
+            uint32_t free_phase = 1u;
+            for (int it = 0; it < s1 - s0; ++it) {
+                wait(&empty[at], free_phase, ok);
+                load_stage(mem + at * s.stage(), (s0 + it) * P_STEP, rows);
+                at = at + 1 == n_stages ? 0 : at + 1;
+                free_phase = at ? free_phase : free_phase ^ 1u;
+                if (VEC) {
+                    ptx::cp_async_commit();
+                    ptx::cp_async_wait<LAG>();
+                }
+                if (it < LAG) continue;
+                arrive(&full[told]);
+                told = told + 1 == n_stages ? 0 : told + 1;
+            }
+            if (VEC) {
+                ptx::cp_async_wait_all();
+                for (int i = s1 - s0 < LAG ? s1 - s0 : LAG; i > 0; --i) {
+                    arrive(&full[told]);
+                    told = told + 1 == n_stages ? 0 : told + 1;
+                }
             }
             prefetch_base(chunk0, chunk1);
             fill(0, 1, chunk0, chunk1);
         } else {
-            for (int f = s0; f < s1; ++f) {
-                const int it = f - s0, at = it % n_stages;
-                wait(&full[at], static_cast<uint32_t>(it / n_stages) & 1u, ok);
-                ok = __all_sync(0xffffffffu, ok);  // what follows is the whole warp's
-                if (!ok) break;
+            int at = 0;
+            uint32_t phase = 0u;
+            for (int it = 0; it < s1 - s0; ++it) {
+                wait(&full[at], phase, ok);
+                __syncwarp();  // what follows is the whole warp's
                 ptx::fence_proxy_async_smem();
                 ptx::tc_fence_after();
                 const uint32_t a = ptx::smem_addr(mem + at * s.stage()), b = a + TILE * P_STEP * 2;
                 ptx::mma_bf16_elect_x4(tmem, ptx::sw128_kmajor_desc(a), TRANS ? ptx::plain_mnmajor_desc(b, 128, W1_COLUMN) : ptx::sw128_kmajor_desc(b),
                                        32 / 16, (TRANS ? 256 : 32) / 16, TRANS ? ptx::idesc_bf16_f32_bmn(TILE, s.rp) : ptx::idesc_bf16_f32(TILE, s.rp), it > 0);
                 ptx::mma_commit_elect(&empty[at]);
+                at = at + 1 == n_stages ? 0 : at + 1;
+                phase = at ? phase : phase ^ 1u;
             }
             ptx::mma_commit_elect(done);
         }
@@ -553,20 +586,26 @@ struct Pass {
             ptx::tc_fence_before();
         }
         __syncthreads();
-        if (warp < P_WARPS) fill(s.early_chunks(), n_bufs, chunk0, chunk1);
+        if (warp < P_WARPS) {
+            ptx::cp_async_wait_all();
+            filled(0, s.early_chunks());
+            fill(s.early_chunks(), n_bufs, chunk0, chunk1);
+        }
         const int n = chunk1 - chunk0;
         if (warp == P_WARPS) {
-            ok = __all_sync(0xffffffffu, ok);
             ptx::tc_fence_after();
+            int buf = 0;
+            uint32_t phase = 0u;
             for (int j = 0; j < n; ++j) {
-                const int b = j & (BUFS - 1), buf = j % n_bufs;
-                wait(&w2_full[buf], static_cast<uint32_t>(j / n_bufs) & 1u, ok);
+                const int b = j & (BUFS - 1);
+                wait(&w2_full[buf], phase, ok);
                 wait(&d_empty[b], (static_cast<uint32_t>(j / BUFS) & 1u) ^ 1u, ok);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
+                __syncwarp();
                 ptx::fence_proxy_async_smem();
                 ptx::tc_fence_after();
                 const uint32_t w = ptx::smem_addr(w2_buf(buf));
+                buf = buf + 1 == n_bufs ? 0 : buf + 1;
+                phase = buf ? phase : phase ^ 1u;
                 const uint64_t wd = ptx::plain_kmajor_desc(w, s.column(), 144), w_step = 2 * s.column() / 16;
                 const uint32_t idesc = TRANS ? ptx::idesc_bf16_f32_bmn(TILE, COLS) : ptx::idesc_bf16_f32(TILE, COLS);
                 const int whole = s.rp / 32;  // of the reduction, in twice three MMAs
@@ -579,6 +618,7 @@ struct Pass {
             // is on its way).
             Held held[2];
             load_base(held[0], 0, (chunk0 + group) * COLS, false);
+            int buf = group % n_bufs, before = 0;  // w2's buffer of this chunk and of the group's last one
             for (int j0 = group; j0 < n; j0 += 4 / TURNS)
 #pragma unroll
                 for (int jj = 0; jj < 2 / TURNS; ++jj) {
@@ -588,8 +628,8 @@ struct Pass {
                     const bool whole = c0 + COLS <= p.to, next = c0 + 3 * COLS <= p.to;
                     if (TURNS == 2)
                         load_base(held[1], 1, c0, whole);
-                    else if (j + 2 < n)
-                        load_base(held[(jj + 1) & 1], 0, c0 + 2 * COLS, next);
+                    else
+                        load_base(held[(jj + 1) & 1], 0, c0 + 2 * COLS, next, j + 2 < n);
                     wait(&d_full[b], static_cast<uint32_t>(j / BUFS) & 1u, ok);
                     __syncwarp();
                     ptx::tc_fence_after();
@@ -597,24 +637,24 @@ struct Pass {
                     const uint32_t at = tmem + COLS * b + 32 * SIDES * ((warp >> 2) & 1) + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
                     ptx::tmem_ld_16x256b_x4(at, v[0]);
                     ptx::tmem_ld_16x256b_x4(at + (HALVED ? 32u : 16u << 16), v[1]);
-                    if (j + n_bufs < n) {
-                        load_w2(w2_buf(j % n_bufs), c0 + n_bufs * COLS);
-                        arrive(&w2_full[j % n_bufs]);
-                    }
+                    // w2 for this buffer's next chunk, and word of what was asked for a turn ago
+                    if (j + n_bufs < n) load_w2(w2_buf(buf), c0 + n_bufs * COLS);
+                    ptx::cp_async_commit();
+                    ptx::cp_async_wait<1>();
+                    if (j < 2)
+                        filled(s.early_chunks(), n_bufs);
+                    else if (j - 2 + n_bufs < n)
+                        arrive(&w2_full[before]);
+                    before = buf;
+                    buf += 2;
+                    buf = buf >= n_bufs ? buf - n_bufs : buf;
                     ptx::tmem_ld_wait();
                     ptx::tc_fence_before();
-                    if (lane == 0) ptx::mbar_arrive(&d_empty[b]);
-#pragma unroll
-                    for (int turn = 0; turn < TURNS; ++turn) {
-                        if (turn == 1 && j + 2 < n) load_base(held[0], 0, c0 + 2 * COLS, next);
-#pragma unroll
-                        for (int k = 0; k < HOLD; ++k) {
-                            const int i = turn * HOLD + k;
-                            float2 f[4];
-#pragma unroll
-                            for (int g = 0; g < 4; ++g) f[g] = make_float2(__uint_as_float(v[i >> 1][4 * g + 2 * (i & 1)]), __uint_as_float(v[i >> 1][4 * g + 2 * (i & 1) + 1]));
-                            finish(held[TURNS == 1 ? jj & 1 : turn].u[k], f, i, c0, whole, ok);
-                        }
+                    ptx::mbar_arrive_if(&d_empty[b], lane == 0);
+                    finish(held[TURNS == 1 ? jj & 1 : 0], v, 0, c0, whole, ok);
+                    if constexpr (TURNS == 2) {
+                        load_base(held[0], 0, c0 + 2 * COLS, next, j + 2 < n);
+                        finish(held[1], v, 1, c0, whole, ok);
                     }
                 }
         }

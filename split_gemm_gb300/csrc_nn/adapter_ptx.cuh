@@ -107,6 +107,41 @@ __device__ __forceinline__ void tmem_st_32x32b_x8(uint32_t taddr, const uint32_t
 }
 __device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
+// Copies, loads and stores that a lane may skip, predicated: a branch costs a warp some 20 clocks.
+__device__ __forceinline__ void cp_async_16_if(uint32_t dst, const void* src, bool p)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p cp.async.cg.shared.global [%0], [%1], 16;\n\t}" ::"r"(dst), "l"(src), "r"(static_cast<uint32_t>(p))
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_4_if(uint32_t dst, const void* src, bool p)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p cp.async.ca.shared.global [%0], [%1], 4;\n\t}" ::"r"(dst), "l"(src), "r"(static_cast<uint32_t>(p))
+                 : "memory");
+}
+// Streaming: what is read or written once.
+__device__ __forceinline__ uint4 ld_stream_v4_if(const void* src, bool p)
+{
+    uint4 v;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+        "@p ld.global.cs.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+        : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+        : "l"(src), "r"(static_cast<uint32_t>(p))
+        : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_stream_v4_if(void* dst, uint4 v, bool p)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t@p st.global.cs.v4.b32 [%0], {%1, %2, %3, %4};\n\t}" ::"l"(dst), "r"(v.x), "r"(v.y), "r"(v.z),
+                 "r"(v.w), "r"(static_cast<uint32_t>(p))
+                 : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_if(uint64_t* bar, bool p)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %1, 0;\n\t@p mbarrier.arrive.shared::cta.b64 _, [%0];\n\t}" ::"r"(smem_addr(bar)), "r"(static_cast<uint32_t>(p))
+                 : "memory");
+}
+
 // Four bytes, zero where `src_bytes` is 0 (the address need only be valid for 4 bytes).
 __device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src, uint32_t src_bytes)
 {

@@ -272,7 +272,7 @@ struct Sum {
 #pragma unroll
         for (int i = 0; i < DEPTH; ++i)
             if (i < n) fetch(held[i], i);
-        int first = 0, runs = 0;
+        int first = 0, runs = 0, told = 0;  // told: stages before it have been told of
         for (int k0 = 0; k0 < n; k0 += DEPTH)
 #pragma unroll
             for (int i = 0; i < DEPTH; ++i) {
@@ -283,13 +283,26 @@ struct Sum {
                 wait(&empty[at], (static_cast<uint32_t>(k / s.stages()) & 1u) ^ 1u, ok);
                 if constexpr (MODE == 0) {
                     copy(st, k);
-                    ptx::cp_async_arrive_noinc(&full[at]);
+                    ptx::cp_async_commit();
                 }
                 store(held[i], st);
                 ptx::fence_proxy_async_smem();
-                ptx::mbar_arrive(&full[at]);
+                // One arrival to a warp (a barrier takes its arrivals one after another); copies' stages are told of a stage later.
+                const bool last = ends_run(k);
+                if constexpr (MODE == 0) {
+                    if (last)
+                        ptx::cp_async_wait<0>();
+                    else
+                        ptx::cp_async_wait<1>();
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    if (MODE == 0 && k > told) ptx::mbar_arrive(&full[(k - 1) % s.stages()]);
+                    if (MODE != 0 || last) ptx::mbar_arrive(&full[at]);
+                }
+                if (last) told = k + 1;
                 if (k + DEPTH < n) fetch(held[i], k + DEPTH);
-                if (ends_run(k)) {
+                if (last) {
                     wait(done, static_cast<uint32_t>(runs) & 1u, ok);
                     __syncwarp();
                     ptx::tc_fence_after();
@@ -358,7 +371,7 @@ __global__ void __launch_bounds__(U_THREADS, 1) sum_tiles(const __grid_constant_
     const int c0 = (block - (block >= p.jobs[0].col_blocks ? p.jobs[0].col_blocks : 0)) * 128 * s.blocks;
     if (tid == 0) {
         for (int i = 0; i < s.stages(); ++i) {
-            ptx::mbar_init(&full[i], job.mode == 0 ? 2 * U_LOADERS : U_LOADERS);
+            ptx::mbar_init(&full[i], U_WARPS);
             ptx::mbar_init(&empty[i], 1);
         }
         ptx::mbar_init(done, 1);
