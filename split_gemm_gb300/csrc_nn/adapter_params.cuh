@@ -24,36 +24,43 @@ struct PassParams {
     int splits;  // CTAs of a cluster
 };
 
-constexpr int P_STEP = 64;  // of `from`, in a stage
-constexpr int P_MOST_STAGES = 6, P_MOST_CHUNKS = 8;
+constexpr int P_BLOCK = 64, P_STEP = 2 * P_BLOCK;  // of `from`: in a block of operands, and in a stage
+constexpr int P_COLS = 128;                        // of `to`, in a chunk
+constexpr int P_MOST_STAGES = 4, P_MOST_CHUNKS = 8;
 constexpr int P_ROOM = 227 * 1024;  // bytes of shared memory
 
-// Bytes between the 16-byte columns of an MN-major stage of w1: 16 more than they need, so that neighbours fall into different banks.
-constexpr int W1_COLUMN = P_STEP * 16 + 16;
+// Bytes between the 16-byte columns of an MN-major block of w1: 16 more than they need, so that neighbours fall into different banks.
+constexpr int W1_COLUMN = P_BLOCK * 16 + 16;
 
-// Shared memory by the rank padded to 16 and the halving of tiles: an area that holds the first product's ring and, when that is over, the
-// sums (from its start), mid (to its end) and w2's chunks (downwards from mid; over the sums, once those are joined); beside it w2's first
-// chunk, barriers and lists.  A chunk of w2: core matrices 144 bytes apart along the columns, so that the pairs that the backward
-// pass places one by one fall into different banks, and 16 bytes more from one column of 8 ranks to the next, for the forward pass's vectors.
+// Threads that finish chunks, and turns of base (64 bytes of each of them) on their way to shared memory.
+constexpr int P_WARPS = 16, P_LOADERS = 32 * P_WARPS, P_DEPTH = 3;
+
+// Shared memory by the rank padded to 16: an area that holds the first product's ring and, when that is over, the sums (from its start) and mid
+// (to its end); when mid is in tensor memory, base's ring (to its end).  Before that lie w2's chunks, over the sums once those are joined; beside
+// the area w2's first chunk, barriers and lists.  A chunk of w2: core matrices 144 bytes apart along the columns, so that the pairs that the
+// backward pass places one by one fall into different banks, and 16 bytes more from one column of 8 ranks to the next, for the forward pass's vectors.
 struct PassSmem {
-    int rp, cols;  // cols: of `to`, in a chunk
-    __host__ __device__ constexpr PassSmem(int rank, int halved) : rp((rank + 15) / 16 * 16), cols(64 << halved) {}
-    __host__ __device__ constexpr int stage() const { return TILE * P_STEP * 2 + (rp / 8 * W1_COLUMN + 1023) / 1024 * 1024; }
-    __host__ __device__ constexpr int column() const { return cols / 8 * 144 + 16; }  // of a chunk: 8 ranks
+    int rp;
+    __host__ __device__ constexpr explicit PassSmem(int rank) : rp((rank + 15) / 16 * 16) {}
+    __host__ __device__ constexpr int block() const { return TILE * P_BLOCK * 2 + (rp / 8 * W1_COLUMN + 1023) / 1024 * 1024; }
+    __host__ __device__ constexpr int stage() const { return 2 * block(); }
+    __host__ __device__ constexpr int column() const { return P_COLS / 8 * 144 + 16; }  // of a chunk: 8 ranks
     __host__ __device__ constexpr int chunk() const { return (rp / 8 * column() + 127) / 128 * 128; }
     __host__ __device__ constexpr int rest() const { return 512 + TILE * 4; }
     __host__ __device__ constexpr int area() const { return (P_ROOM - chunk() - rest()) / 128 * 128; }
     __host__ __device__ constexpr int stages() const { return area() / stage() < P_MOST_STAGES ? area() / stage() : P_MOST_STAGES; }
     __host__ __device__ constexpr int pitch() const { return rp + 4; }  // of the rows of sums and mid, in words
     __host__ __device__ constexpr int sums() const { return TILE * pitch() * 4; }  // and mid's bytes
-    __host__ __device__ constexpr int chunks() const { return 1 + (area() - sums()) / chunk() < P_MOST_CHUNKS ? 1 + (area() - sums()) / chunk() : P_MOST_CHUNKS; }
-    __host__ __device__ constexpr int early_chunks() const  // that do not lie over the sums
+    __host__ __device__ constexpr int ring() const { return P_DEPTH * P_LOADERS * 64; }
+    __host__ __device__ constexpr int chunks() const { return 1 + (area() - ring()) / chunk() < P_MOST_CHUNKS ? 1 + (area() - ring()) / chunk() : P_MOST_CHUNKS; }
+    __host__ __device__ constexpr int early_chunks() const  // that lie neither over the sums nor over mid
     {
-        const int n = 1 + (area() - sums() - sums()) / chunk();
+        const int top = area() - ring() < area() - sums() ? area() - ring() : area() - sums(), n = 1 + (top > sums() ? (top - sums()) / chunk() : 0);
         return n < chunks() ? n : chunks();
     }
 };
-static_assert(PassSmem(128, 1).area() >= 2 * PassSmem(128, 1).sums() && PassSmem(128, 1).early_chunks() >= 2 && PassSmem(128, 1).stages() >= 4, "the widest rank fits");
+static_assert(PassSmem(128).area() >= 2 * PassSmem(128).sums() && PassSmem(128).chunks() >= 2 && PassSmem(128).stages() >= 2 && PassSmem(128).ring() >= PassSmem(128).sums(),
+              "the widest rank fits");
 
 // Sums over the adapters' rows: out[e] (r, c) = sum of mid[t][r] * in[t][c].
 struct SumJob {

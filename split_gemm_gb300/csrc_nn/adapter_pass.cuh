@@ -8,12 +8,13 @@
 // of S CTAs shares a tile: each takes a part of `from` for the first product, 128/S rows of the join and a part of `to` for the
 // second.  Two CTAs stay on an SM up to rank 64, each at a phase of its own.  mid never leaves the chip but for the copy that the gradients need.
 //
-// First product: rows of `in` are gathered by the plan's order with cp.async, 128 bytes of a row at a time, 128 x rank x 64 a stage.  The sums over
+// First product: rows of `in` are gathered by the plan's order with cp.async, 128 bytes of a row at a time, 128 x rank x 128 a stage (the loop around a stage costs its warps some
+// 600 clocks, more than its copies of half the size).  The sums over
 // the parts meet in shared memory as fp32, are joined in the CTAs' order and cut into three bf16 parts that
 // hold all 24 bits: the second product, K = 3 * rank, is that of an fp32 mid.
 //
 // Second product: mid's parts are its A operand in tensor memory (from shared memory they would be read once for each chunk and take
-// most of its bandwidth), 64 columns of `to` (128 of tiles of 64 rows) its B.  Two groups of 8 warps finish chunks by turns.  A thread reads the accumulator in the 16 x 256-bit layout, 2
+// most of its bandwidth), 128 columns of `to` its B.  Two groups of 8 warps finish chunks by turns, each with an accumulator of its own.  A thread reads the accumulator in the 16 x 256-bit layout, 2
 // neighbouring columns of a lane in each group of 8; w2's rows are placed in shared memory in an order that makes these 8 neighbouring columns of out, so base and
 // out move in 16-byte vectors straight between registers and memory, base a chunk ahead.
 //
@@ -27,30 +28,30 @@
 namespace sgb {
 namespace ad {
 
-constexpr int P_WARPS = 16, P_LOADERS = 32 * P_WARPS, P_THREADS = P_LOADERS + 32;
-constexpr int P_GROUP = P_LOADERS / 2;  // threads that finish a chunk
+constexpr int P_W2_WARPS = 3, P_W2_THREADS = 32 * P_W2_WARPS;  // that bring w2's chunks
+constexpr int P_THREADS = P_LOADERS + 32 + P_W2_THREADS;
 constexpr uint64_t P_WAIT_NS = 1000000000ull;
 constexpr uint32_t P_TMEM = 512;  // the first product's sums, then 256 columns of chunks; mid's parts at the end
 
 template <bool TRANS, bool VEC, int HALVED, typename TB, typename TO>
 struct Pass {
-    static constexpr int ROWS = TILE >> HALVED, COLS = 64 << HALVED;  // of a tile; of `to`, in a chunk
-    static constexpr int BUFS = 4 >> HALVED;                           // accumulators of chunks
-    static constexpr int LANES = 32 >> HALVED;                        // of a warp's 32 lanes of tensor memory that hold rows
+    static constexpr int ROWS = TILE >> HALVED;  // of a tile
+    static constexpr int COLS = P_COLS, BUFS = 2;  // of `to`, in a chunk; accumulators of chunks, one to each group
+    static constexpr int LANES = 32 >> HALVED;   // of a warp's 32 lanes of tensor memory that hold rows
 
     const PassParams& p;
     const PassSmem s;
     uint8_t* mem;
-    uint64_t *full, *empty, *done, *w2_full, *d_full, *d_empty, *mid_full;
+    uint64_t *full, *empty, *done, *w2_full, *w2_empty, *d_full, *d_empty, *mid_full;
     int* ids;  // numbers of the tile's rows
     uint32_t* slot;
     volatile uint32_t* abort_flag;
     int tid, warp, lane, rank_in, e, n_stages, n_bufs;
-    int group, gtid;  // of two that finish chunks by turns, and the thread of it
+    int group;  // of two that finish chunks by turns
 
     Piece piece;
 
-    __device__ __forceinline__ Pass(const PassParams& p, uint8_t* raw) : p(p), s(p.rank, HALVED), mem(raw)
+    __device__ __forceinline__ Pass(const PassParams& p, uint8_t* raw) : p(p), s(p.rank), mem(raw)
     {
         n_stages = s.stages();
         n_bufs = s.chunks();
@@ -58,9 +59,10 @@ struct Pass {
         empty = full + P_MOST_STAGES;
         done = empty + P_MOST_STAGES;
         w2_full = done + 1;
-        d_full = w2_full + P_MOST_CHUNKS;
-        d_empty = d_full + 4;
-        mid_full = d_empty + 4;
+        w2_empty = w2_full + P_MOST_CHUNKS;
+        d_full = w2_empty + P_MOST_CHUNKS;
+        d_empty = d_full + BUFS;
+        mid_full = d_empty + BUFS;
         ids = reinterpret_cast<int*>(mid_full + 1);
         slot = reinterpret_cast<uint32_t*>(ids + TILE);
         abort_flag = slot + 1;
@@ -69,7 +71,6 @@ struct Pass {
         lane = tid & 31;
         rank_in = blockIdx.x % p.splits;
         group = warp >> 3;
-        gtid = tid & (P_GROUP - 1);
     }
     // Once a wait has run out, `ok` is false and the thread waits no more: it goes on through its barriers with whatever is in memory.
     __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, bool& ok) const
@@ -80,7 +81,8 @@ struct Pass {
         }
     }
     __device__ __forceinline__ float* mids() const { return reinterpret_cast<float*>(mem + s.area() - s.sums()); }
-    __device__ __forceinline__ uint8_t* w2_buf(int i) const { return i ? mem + s.area() - s.sums() - i * s.chunk() : mem + s.area(); }
+    __device__ __forceinline__ uint8_t* w2_buf(int i) const { return i ? mem + s.area() - s.ring() - i * s.chunk() : mem + s.area(); }
+    __device__ __forceinline__ uint32_t base_ring() const { return ptx::smem_addr(mem) + s.area() - s.ring() + 16 * tid; }
 
     // 16 bytes of row elements from `src`, `valid` elements of them; aligned copies run by themselves, others go through registers.
     __device__ __forceinline__ void copy8(uint32_t dst, const __nv_bfloat16* src, int valid) const
@@ -105,101 +107,104 @@ struct Pass {
     // The accumulator's lane of row i: a halved tile has 16 rows in each warp's 32 lanes, so that all warps finish chunks.
     __device__ __forceinline__ static int lane_of(int i) { return HALVED ? (i >> 4) * 32 + (i & 15) : i; }
 
-    // Where a loader's copies of an MN-major w1 or a K-major w2 go: 64 rows of rank/8 16-byte columns, one after another in memory.
+    // Where a loader's copies of an MN-major w1 go: 64 rows of rank/8 16-byte columns, one after another in memory.
     // (Addresses are kept in registers: computed for each copy they cost the loaders more time than the copies.)
-    static constexpr int PLACES = 64 * MOST_RANK / 8 / (TRANS ? P_LOADERS : P_GROUP);
+    static constexpr int PLACES = 64 * MOST_RANK / 8 / P_LOADERS;
     uint32_t place[PLACES];
     __device__ __forceinline__ void make_places()
     {
         const int per = p.rank >> 3;
 #pragma unroll
         for (int j = 0; j < PLACES; ++j) {
-            const int i = TRANS ? tid + P_LOADERS * j : gtid + P_GROUP * j, row = i / per, c8 = i - row * per;
-            const int n = (row & 32) + 8 * ((row >> 1) & 3) + 2 * ((row >> 3) & 3) + (row & 1);  // of w2, as below
-            place[j] = row >= 64 ? 0xffffffffu : TRANS ? (row & 7) * 16 + (row >> 3) * 128 + c8 * W1_COLUMN : (n & 7) * 16 + (n >> 3) * 144 + c8 * s.column();
+            const int i = tid + P_LOADERS * j, row = i / per, c8 = i - row * per;
+            place[j] = row >= 64 ? 0xffffffffu : (row & 7) * 16 + (row >> 3) * 128 + c8 * W1_COLUMN;
         }
     }
 
-    // Columns f0 .. f0+63 of the tile's rows and of w1.  rows: at this thread's 16-byte column of every 64th row.
-    __device__ __forceinline__ void load_stage(uint8_t* st, int f0, const __nv_bfloat16* const (&rows)[ROWS / 64]) const
+    // Columns f0 .. f0+63 of the tile's rows and of w1.  rows: at this thread's 16-byte column of every 64th row, w: where its copies of
+    // w1 begin, both at column f0.
+    __device__ __forceinline__ void load_block(uint32_t at, int f0, const __nv_bfloat16* const (&rows)[ROWS / 64], const __nv_bfloat16* w) const
     {
-        const uint32_t at = ptx::smem_addr(st), w_at = at + TILE * P_STEP * 2;
-        const int64_t size = static_cast<int64_t>(p.rank) * p.from;
-        const __nv_bfloat16* w = p.w1 + e * size;
-        const int row = tid >> 3, c8 = tid & 7, l = lane_of(row);
-        const uint32_t swizzled = (c8 ^ (row & 7)) << 4, mine = l * 128 + swizzled;  // 128-byte swizzle
-        if (VEC && f0 + P_STEP <= p.from) {
+        const uint32_t w_at = at + TILE * P_BLOCK * 2;
+        const int row = tid >> 3, c8 = tid & 7;
+        const uint32_t swizzled = (c8 ^ (row & 7)) << 4, mine = lane_of(row) * 128 + swizzled;  // 128-byte swizzle
+        if (VEC && f0 + P_BLOCK <= p.from) {
 #pragma unroll
             for (int i = 0; i < ROWS / 64; ++i)
-                ptx::cp_async_16_if(at + mine + 8192 * i, rows[i] + f0, row + 64 * i < piece.rows);
+                ptx::cp_async_16_if(at + mine + 8192 * i, rows[i], row + 64 * i < piece.rows);
             if constexpr (!TRANS) {
-                const __nv_bfloat16* src = w + static_cast<int64_t>(row) * p.from + f0 + 8 * c8;
-                ptx::cp_async_16_if(w_at + row * 128 + swizzled, src, row < p.rank);
-                ptx::cp_async_16_if(w_at + row * 128 + swizzled + 8192, src + 64 * static_cast<int64_t>(p.from), row + 64 < p.rank);
+                ptx::cp_async_16_if(w_at + row * 128 + swizzled, w, row < p.rank);
+                ptx::cp_async_16_if(w_at + row * 128 + swizzled + 8192, w + 64 * static_cast<int64_t>(p.from), row + 64 < p.rank);
             } else {
-                const __nv_bfloat16* src = w + static_cast<int64_t>(f0) * p.rank + 8 * tid;
 #pragma unroll
                 for (int i = 0; i < PLACES; ++i)
-                    ptx::cp_async_16_if(w_at + place[i], src + 8 * P_LOADERS * i, place[i] != 0xffffffffu);
+                    ptx::cp_async_16_if(w_at + place[i], w + 8 * P_LOADERS * i, place[i] != 0xffffffffu);
             }
             return;
         }
 #pragma unroll
         for (int i = 0; i < ROWS / 64; ++i)
-            if (row + 64 * i < piece.rows) copy8(at + mine + 8192 * i, rows[i] + f0, p.from - f0 - 8 * c8);
+            if (row + 64 * i < piece.rows) copy8(at + mine + 8192 * i, rows[i], p.from - f0 - 8 * c8);
+        const __nv_bfloat16* first = p.w1 + e * (static_cast<int64_t>(p.rank) * p.from);
         if constexpr (!TRANS) {
             for (int r = row; r < p.rank; r += 64)
-                copy8(w_at + r * 128 + swizzled, w + static_cast<int64_t>(r) * p.from + f0 + 8 * c8, p.from - f0 - 8 * c8);
+                copy8(w_at + r * 128 + swizzled, first + static_cast<int64_t>(r) * p.from + f0 + 8 * c8, p.from - f0 - 8 * c8);
         } else {
             for (int i = tid; i < s.rp * 8; i += P_LOADERS) {  // 64 rows of rp/8 16-byte columns
                 const int k = (i >> 1) & 63, n8 = 2 * (i >> 7) + (i & 1);
                 const int left = f0 + k < p.from ? p.rank - 8 * n8 : 0;
-                copy8(w_at + (k & 7) * 16 + n8 * W1_COLUMN + (k >> 3) * 128, w + static_cast<int64_t>(f0 + k) * p.rank + 8 * n8, left);
+                copy8(w_at + (k & 7) * 16 + n8 * W1_COLUMN + (k >> 3) * 128, first + static_cast<int64_t>(f0 + k) * p.rank + 8 * n8, left);
             }
         }
     }
 
-    // w2's columns of a chunk from c0 on, by a group: column c of 32 becomes row 8((c>>1)&3) + 2(c>>3) + (c&1) of the operand.
+    // w2's columns of a chunk from c0 on, by the warps that bring it: column c of 32 becomes row 8((c>>1)&3) + 2(c>>3) + (c&1) of the operand.
+    __device__ __forceinline__ static int place_of(int c) { return (c & ~31) + 8 * ((c >> 1) & 3) + 2 * ((c >> 3) & 3) + (c & 1); }
     __device__ __forceinline__ void load_w2(uint8_t* buf, int c0) const
     {
         const int64_t size = static_cast<int64_t>(p.rank) * p.to;
         const __nv_bfloat16* w = p.w2 + e * size;
-        uint32_t at = ptx::smem_addr(buf);
-#pragma unroll
-        for (int half = 0; half < COLS / 64; ++half, at += 8 * 144, c0 += 64) {
-            if (VEC && c0 + 64 <= p.to) {
-                if constexpr (!TRANS) {
-                    const __nv_bfloat16* src = w + static_cast<int64_t>(c0) * p.rank + 8 * gtid;
-#pragma unroll
-                    for (int i = 0; i < PLACES; ++i)
-                        ptx::cp_async_16_if(at + place[i], src + 8 * P_GROUP * i, place[i] != 0xffffffffu);
-                } else {
-                    const int c = 2 * lane, gwarp = warp & 7;
-                    uint32_t dst = at + gwarp * 16 + ((c >> 3) & 3) * 4 + (((c >> 1) & 3) + 4 * (c >> 5)) * 144;
-                    const __nv_bfloat16* src = w + static_cast<int64_t>(gwarp) * p.to + c0 + c;
-                    for (int k = gwarp; k < s.rp; k += 16, dst += 2 * s.column(), src += 16 * static_cast<int64_t>(p.to)) {
-                        ptx::cp_async_4_if(dst, src, k < p.rank);
-                        ptx::cp_async_4_if(dst + s.column(), src + 8 * static_cast<int64_t>(p.to), k + 8 < p.rank);
-                    }
-                }
-            } else if constexpr (!TRANS) {
-                for (int i = gtid; i < s.rp * 8; i += P_GROUP) {
-                    const int n = (i >> 1) & 63, k8 = 2 * (i >> 7) + (i & 1);
-                    const int c = c0 + (n & 32) + 8 * ((n >> 1) & 3) + 2 * ((n >> 3) & 3) + (n & 1);
-                    copy8(at + (n & 7) * 16 + (n >> 3) * 144 + k8 * s.column(), w + static_cast<int64_t>(c) * p.rank + 8 * k8, c < p.to ? p.rank - 8 * k8 : 0);
+        const uint32_t at = ptx::smem_addr(buf);
+        const int wt = tid - (P_LOADERS + 32), ww = warp - (P_WARPS + 1);
+        if (VEC && c0 + COLS <= p.to) {
+            if constexpr (!TRANS) {
+                // as many threads to a column's ranks as a power of two covers them
+                const int per = p.rank >> 3, shift = per <= 1 ? 0 : 32 - __clz(per - 1), step = P_W2_THREADS >> shift;
+                const int c8 = wt & ((1 << shift) - 1);
+                const uint32_t dst = at + c8 * s.column();
+                const __nv_bfloat16* src = w + static_cast<int64_t>(c0 + (wt >> shift)) * p.rank + 8 * c8;
+#pragma unroll 4
+                for (int c = wt >> shift; c < COLS; c += step, src += step * p.rank) {
+                    const int n = place_of(c);
+                    ptx::cp_async_16_if(dst + (n & 7) * 16 + (n >> 3) * 144, src, c8 < per);
                 }
             } else {
-                for (int i = gtid; i < s.rp * 32; i += P_GROUP) {
-                    const int k = i >> 5, c = 2 * (i & 31);
-                    const uint32_t dst = at + (k & 7) * 16 + ((c >> 3) & 3) * 4 + (((c >> 1) & 3) + 4 * (c >> 5)) * 144 + (k >> 3) * s.column();
-                    const __nv_bfloat16* src = w + static_cast<int64_t>(k) * p.to + c0 + c;
-                    const int left = k < p.rank ? p.to - c0 - c : 0;
-                    if constexpr (VEC) {
-                        ptx::cp_async_4(dst, left > 0 ? src : p.w1, left > 0 ? 4 : 0);
-                    } else {
-                        const uint32_t lo = left > 0 ? __bfloat16_as_ushort(__ldg(src)) : 0u, hi = left > 1 ? __bfloat16_as_ushort(__ldg(src + 1)) : 0u;
-                        asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(lo | hi << 16) : "memory");
-                    }
+                const int c = 2 * lane;
+                const uint32_t dst = at + ((c >> 3) & 3) * 4 + (((c >> 1) & 3) + 4 * (c >> 5)) * 144;
+                const __nv_bfloat16* src = w + static_cast<int64_t>(ww) * p.to + c0 + c;
+#pragma unroll 4
+                for (int k = ww; k < p.rank; k += P_W2_WARPS, src += P_W2_WARPS * static_cast<int64_t>(p.to)) {
+                    const uint32_t to = dst + (k & 7) * 16 + (k >> 3) * s.column();
+                    ptx::cp_async_4_if(to, src, true);
+                    ptx::cp_async_4_if(to + 8 * 144, src + 64, true);
+                }
+            }
+        } else if constexpr (!TRANS) {
+            for (int i = wt; i < s.rp * COLS / 8; i += P_W2_THREADS) {
+                const int per = s.rp >> 3, c = i / per, k8 = i - c * per, n = place_of(c);
+                copy8(at + (n & 7) * 16 + (n >> 3) * 144 + k8 * s.column(), w + static_cast<int64_t>(c0 + c) * p.rank + 8 * k8, c0 + c < p.to ? p.rank - 8 * k8 : 0);
+            }
+        } else {
+            for (int i = wt; i < s.rp * COLS / 2; i += P_W2_THREADS) {
+                const int k = i / (COLS / 2), c = 2 * (i % (COLS / 2)), n = place_of(c);
+                const uint32_t dst = at + (k & 7) * 16 + (n & 7) * 2 + (n >> 3) * 144 + (k >> 3) * s.column();
+                const __nv_bfloat16* src = w + static_cast<int64_t>(k) * p.to + c0 + c;
+                const int left = k < p.rank ? p.to - c0 - c : 0;
+                if constexpr (VEC) {
+                    ptx::cp_async_4(dst, left > 0 ? src : p.w1, left > 0 ? 4 : 0);
+                } else {
+                    const uint32_t lo = left > 0 ? __bfloat16_as_ushort(__ldg(src)) : 0u, hi = left > 1 ? __bfloat16_as_ushort(__ldg(src + 1)) : 0u;
+                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(lo | hi << 16) : "memory");
                 }
             }
         }
@@ -207,9 +212,32 @@ struct Pass {
     // The part of a chunk of w2 that pads an odd number of 8 ranks; whole copies do not reach it.
     __device__ __forceinline__ void clear_pad(uint8_t* buf) const
     {
-        if (!VEC || !(p.rank & 8)) return;
-        if (gtid < COLS) ptx::st_shared_v4(ptx::smem_addr(buf) + (gtid & 7) * 16 + (gtid >> 3) * 144 + (p.rank >> 3) * s.column(), 0u, 0u, 0u, 0u);
+        if constexpr (!VEC) return;
+        if (!(p.rank & 8)) return;
+        for (int i = tid - (P_LOADERS + 32); i < COLS; i += P_W2_THREADS)
+            ptx::st_shared_v4(ptx::smem_addr(buf) + (i & 7) * 16 + (i >> 3) * 144 + (p.rank >> 3) * s.column(), 0u, 0u, 0u, 0u);
         ptx::fence_proxy_async_smem();
+    }
+    // w2's chunks i0 .. i1 of the CTA's n from c0 on, one after another as buffers come free; the word of each a chunk later.
+    __device__ __forceinline__ void bring_w2(int i0, int i1, int c0, bool& ok) const
+    {
+        for (int j = i0; j < i1; ++j) {
+            const int buf = j % n_bufs;
+            wait(&w2_empty[buf], (static_cast<uint32_t>(j / n_bufs) & 1u) ^ 1u, ok);
+            if (j < n_bufs) clear_pad(w2_buf(buf));
+            load_w2(w2_buf(buf), c0 + j * COLS);
+            if (VEC) {
+                ptx::cp_async_commit();
+                ptx::cp_async_wait<1>();
+                if (j > i0) arrive(&w2_full[(j - 1) % n_bufs]);
+            } else {
+                arrive(&w2_full[buf]);
+            }
+        }
+        if (VEC && i1 > i0) {
+            ptx::cp_async_wait_all();
+            arrive(&w2_full[(i1 - 1) % n_bufs]);
+        }
     }
 
     // This CTA's rows of the sums over the cluster: scaled, to mid, and on to every CTA.
@@ -218,7 +246,7 @@ struct Pass {
     {
         constexpr int SHARE = ROWS / S;
         const int eighths = s.rp >> 3;
-        for (int i = tid; i < SHARE * eighths; i += P_THREADS) {  // neighbouring lanes read neighbouring parts of a row
+        for (int i = tid < P_LOADERS ? tid : SHARE * eighths; i < SHARE * eighths; i += P_LOADERS) {  // neighbouring lanes read neighbouring parts of a row
             const int own = i / eighths, row = rank_in * SHARE + own, r = 8 * (i - own * eighths);
             const float* at = sums + row * s.pitch() + r;
             float v[8] = {};
@@ -294,23 +322,23 @@ struct Pass {
         ptx::tmem_st_wait();
     }
 
-    // A thread finishes four times 8 neighbouring elements of a chunk, SIDES side by side at 32 columns' distance in each of 4 / SIDES rows, 8 rows
-    // apart.  It holds HOLD of them at a time: 64 bytes of base.
-    static constexpr int SIDES = 1 << HALVED;
-    static constexpr int HOLD = sizeof(TB) == 2 ? 4 : 2, TURNS = 4 / HOLD, WORDS = 2 * sizeof(TB);
+    // A thread finishes eight times (four of a halved tile) 8 neighbouring elements of a chunk, two side by side at 32 columns' distance in each of its
+    // rows, 8 rows apart.  It holds HOLD of them at a time, a turn: 64 bytes of base.
+    static constexpr int MINE = 4 >> HALVED, VECTORS = 2 * MINE;  // rows of a thread
+    static constexpr int HOLD = sizeof(TB) == 2 ? 4 : 2, TURNS = VECTORS / HOLD, WORDS = 2 * sizeof(TB);
     struct Held {
         uint32_t u[HOLD][WORDS];
     };
-    const TB* base_at[4 / SIDES];
-    TO* out_at[4 / SIDES];
-    __device__ __forceinline__ static constexpr int row_index(int i) { return HALVED ? i & 1 : i; }
-    __device__ __forceinline__ static constexpr int side_of(int i) { return HALVED ? i >> 1 : 0; }
+    const TB* base_at[MINE];
+    TO* out_at[MINE];
+    __device__ __forceinline__ static constexpr int row_index(int i) { return i % MINE; }
+    __device__ __forceinline__ static constexpr int side_of(int i) { return i / MINE; }
     __device__ __forceinline__ int row_of(int i) const { return LANES * (warp & 3) + (lane >> 2) + 8 * row_index(i); }
-    __device__ __forceinline__ int col_of(int i, int c0) const { return c0 + 32 * SIDES * ((warp >> 2) & 1) + 32 * side_of(i) + 8 * (lane & 3); }
+    __device__ __forceinline__ int col_of(int i, int c0) const { return c0 + 64 * ((warp >> 2) & 1) + 32 * side_of(i) + 8 * (lane & 3); }
     __device__ __forceinline__ void make_rows()
     {
 #pragma unroll
-        for (int i = 0; i < 4 / SIDES; ++i) {
+        for (int i = 0; i < MINE; ++i) {
             const int64_t t = ids[row_of(i)];
             row_here[i] = row_of(i) < piece.rows;
             base_here[i] = row_here[i] && p.base;
@@ -318,22 +346,53 @@ struct Pass {
             out_at[i] = static_cast<TO*>(p.out) + t * p.out_stride + col_of(i, 0);
         }
     }
-    bool row_here[4 / SIDES], base_here[4 / SIDES];  // the thread's rows are of the tile; and there is a base
-    // Turn `turn` of the chunk at c0; `whole`: all its columns exist.
-    __device__ __forceinline__ void load_base(Held& b, int turn, int c0, bool whole, bool wanted = true) const
+    bool row_here[MINE], base_here[MINE];  // the thread's rows are of the tile; and there is a base
+    // Turn `turn` of the chunk at c0, on its way to slot `slot` of the thread's ring (which no other thread reads: it has no barrier); `whole`: all
+    // the chunk's columns exist.
+    __device__ __forceinline__ void ask_base(int slot, int turn, int c0, bool whole, bool wanted) const
+    {
+        if constexpr (VEC) {
+            const uint32_t at = base_ring() + slot * (P_LOADERS * 64);
+#pragma unroll
+            for (int k = 0; k < HOLD; ++k) {
+                const int side = (turn * HOLD + k) / MINE;
+                const bool upper = HOLD < MINE && (turn & 1);  // rows 2 and 3 of four
+                const TB* src = (upper ? base_at[(k + HOLD) % MINE] : base_at[k % MINE]) + c0 + 32 * side;
+                const bool here = wanted && (upper ? base_here[(k + HOLD) % MINE] : base_here[k % MINE]) && (whole || col_of(0, c0) + 32 * side < p.to);
+#pragma unroll
+                for (int j = 0; j < WORDS / 4; ++j) ptx::cp_async_16_if(at + (k * (WORDS / 4) + j) * (P_LOADERS * 16), reinterpret_cast<const uint4*>(src) + j, here);
+            }
+        }
+    }
+    __device__ __forceinline__ void get_base(Held& b, int slot, int turn, int c0) const
+    {
+        if constexpr (VEC) {
+            const uint32_t at = base_ring() + slot * (P_LOADERS * 64);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const uint4 q = ptx::ld_shared_v4(at + i * (P_LOADERS * 16));
+                const int k = i / (WORDS / 4), j = i % (WORDS / 4) * 4;
+                b.u[k][j] = q.x, b.u[k][j + 1] = q.y, b.u[k][j + 2] = q.z, b.u[k][j + 3] = q.w;
+            }
+        } else {
+            load_base(b, turn, c0);
+        }
+    }
+    // The same straight from memory.
+    __device__ __forceinline__ void load_base(Held& b, int turn, int c0) const
     {
 #pragma unroll
         for (int k = 0; k < HOLD; ++k) {
             const int i = turn * HOLD + k;
             const TB* src = base_at[row_index(i)] + c0 + 32 * side_of(i);
+            const int left = base_here[row_index(i)] ? p.to - col_of(i, c0) : 0;
             if constexpr (VEC) {
 #pragma unroll
                 for (int j = 0; j < WORDS; j += 4) {
-                    const uint4 q = ptx::ld_stream_v4_if(reinterpret_cast<const uint4*>(src) + j / 4, wanted && base_here[row_index(i)] && (whole || col_of(i, c0) < p.to));
+                    const uint4 q = ptx::ld_stream_v4_if(reinterpret_cast<const uint4*>(src) + j / 4, left > 0);
                     b.u[k][j] = q.x, b.u[k][j + 1] = q.y, b.u[k][j + 2] = q.z, b.u[k][j + 3] = q.w;
                 }
             } else {
-                const int left = wanted && base_here[row_index(i)] ? p.to - col_of(i, c0) : 0;
                 TB* v = reinterpret_cast<TB*>(b.u[k]);
 #pragma unroll
                 for (int j = 0; j < WORDS; ++j) b.u[k][j] = 0u;
@@ -343,7 +402,7 @@ struct Pass {
             }
         }
     }
-    // out = act(base + sum) for a turn: `v` the chunk's sums as they come from tensor memory.
+    // out = act(base + sum) for a turn: `v` the sums of the four vectors that it belongs to, as they come from tensor memory.
     __device__ __forceinline__ void finish(const Held& b, const uint32_t (&v)[2][16], int turn, int c0, bool whole, bool live) const
     {
         float2 f[HOLD][4];
@@ -352,8 +411,8 @@ struct Pass {
             const int i = turn * HOLD + k;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float2 sum = make_float2(__uint_as_float(v[i >> 1][4 * j + 2 * (i & 1)]), __uint_as_float(v[i >> 1][4 * j + 2 * (i & 1) + 1]));
-                const float2 base = sizeof(TB) == 2 ? make_float2(__uint_as_float(b.u[k][j] << 16), __uint_as_float(b.u[k][j] & 0xffff0000u))
+                const float2 sum = make_float2(__uint_as_float(v[i >> 1 & 1][4 * j + 2 * (i & 1)]), __uint_as_float(v[i >> 1 & 1][4 * j + 2 * (i & 1) + 1]));
+                const float2 base = !p.base ? make_float2(0.f, 0.f) : sizeof(TB) == 2 ? make_float2(__uint_as_float(b.u[k][j] << 16), __uint_as_float(b.u[k][j] & 0xffff0000u))
                                                     : make_float2(__uint_as_float(b.u[k][2 * j % WORDS]), __uint_as_float(b.u[k][(2 * j + 1) % WORDS]));
                 f[k][j] = mx::add2(sum, base);
             }
@@ -394,7 +453,7 @@ struct Pass {
     }
 
     // Base's first chunks to L2, where HBM works on them while the sums are joined.
-    static constexpr int AHEAD = 4;
+    static constexpr int AHEAD = 2;
     __device__ __forceinline__ void prefetch_base(int chunk0, int chunk1) const
     {
         constexpr int LINES = AHEAD * COLS * sizeof(TB) / 128, EACH = 128 / sizeof(TB);
@@ -403,20 +462,6 @@ struct Pass {
             const int row = i / LINES, c = chunk0 * COLS + (i - row * LINES) * EACH;
             if (c < p.to && c < chunk1 * COLS) ptx::prefetch_l2(static_cast<const TB*>(p.base) + ids[row] * p.base_stride + c);
         }
-    }
-
-    // The first filling of w2's buffers i0 .. i1, each by the group whose chunk it is for, and the word that they are there.
-    __device__ __forceinline__ void fill(int i0, int i1, int chunk0, int chunk1) const
-    {
-        for (int i = i0 + ((i0 ^ group) & 1); i < i1; i += 2) {
-            clear_pad(w2_buf(i));
-            if (chunk0 + i < chunk1) load_w2(w2_buf(i), (chunk0 + i) * COLS);
-        }
-        ptx::cp_async_commit();
-    }
-    __device__ __forceinline__ void filled(int i0, int i1) const
-    {
-        for (int i = i0 + ((i0 ^ group) & 1); i < i1; i += 2) arrive(&w2_full[i]);
     }
 
     // Rows without an adapter: out = act(base), mid = 0.
@@ -430,7 +475,7 @@ struct Pass {
 #pragma unroll
             for (int turn = 0; turn < TURNS; ++turn) {
                 Held b;
-                load_base(b, turn, c * COLS, false);
+                load_base(b, turn, c * COLS);
                 const uint32_t none[2][16] = {};
                 finish(b, none, turn, c * COLS, false, true);
             }
@@ -444,7 +489,10 @@ struct Pass {
                 ptx::mbar_init(&empty[i], 1);
             }
             ptx::mbar_init(done, 1);
-            for (int i = 0; i < n_bufs; ++i) ptx::mbar_init(&w2_full[i], P_WARPS / 2);
+            for (int i = 0; i < n_bufs; ++i) {
+                ptx::mbar_init(&w2_full[i], P_W2_WARPS);
+                ptx::mbar_init(&w2_empty[i], 1);
+            }
             for (int i = 0; i < BUFS; ++i) {
                 ptx::mbar_init(&d_full[i], 1);
                 ptx::mbar_init(&d_empty[i], P_WARPS / 2);
@@ -494,19 +542,31 @@ struct Pass {
     {
         const int steps = (p.from + P_STEP - 1) / P_STEP;
         const int s0 = static_cast<int>(static_cast<int64_t>(rank_in) * steps / p.splits), s1 = static_cast<int>(static_cast<int64_t>(rank_in + 1) * steps / p.splits);
+        const int n = chunk1 - chunk0;
         bool ok = true;
         const float scale = p.scale ? __ldg(p.scale + e) : 1.f;
         if (warp < P_WARPS) {
             const __nv_bfloat16* rows[ROWS / 64];
 #pragma unroll
-            for (int i = 0; i < ROWS / 64; ++i) rows[i] = p.in + ids[(tid >> 3) + 64 * i] * p.in_stride + 8 * (tid & 7);
+            for (int i = 0; i < ROWS / 64; ++i) rows[i] = p.in + ids[(tid >> 3) + 64 * i] * p.in_stride + 8 * (tid & 7) + s0 * P_STEP;
+            const __nv_bfloat16* w = p.w1 + e * (static_cast<int64_t>(p.rank) * p.from) +
+                                     (TRANS ? static_cast<int64_t>(s0 * P_STEP) * p.rank + 8 * tid : static_cast<int64_t>(tid >> 3) * p.from + 8 * (tid & 7) + s0 * P_STEP);
+            const int64_t w_step = TRANS ? P_BLOCK * p.rank : P_BLOCK;
             if (VEC) make_places();
-            constexpr int LAG = VEC ? 3 : 0;  // stages on their way behind the one that is asked for
+            constexpr int LAG = VEC ? 1 : 0;  // stages on their way behind the one that is asked for
             int at = 0, told = 0;
             uint32_t free_phase = 1u;
             for (int it = 0; it < s1 - s0; ++it) {
                 wait(&empty[at], free_phase, ok);
-                load_stage(mem + at * s.stage(), (s0 + it) * P_STEP, rows);
+                const uint32_t st = ptx::smem_addr(mem) + at * s.stage();
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int f0 = (s0 + it) * P_STEP + h * P_BLOCK;
+                    if (f0 < p.from) load_block(st + h * s.block(), f0, rows, w);
+#pragma unroll
+                    for (int i = 0; i < ROWS / 64; ++i) rows[i] += P_BLOCK;
+                    w += w_step;
+                }
                 at = at + 1 == n_stages ? 0 : at + 1;
                 free_phase = at ? free_phase : free_phase ^ 1u;
                 if (VEC) {
@@ -525,8 +585,7 @@ struct Pass {
                 }
             }
             prefetch_base(chunk0, chunk1);
-            fill(0, 1, chunk0, chunk1);
-        } else {
+        } else if (warp == P_WARPS) {
             int at = 0;
             uint32_t phase = 0u;
             for (int it = 0; it < s1 - s0; ++it) {
@@ -534,19 +593,25 @@ struct Pass {
                 __syncwarp();  // what follows is the whole warp's
                 ptx::fence_proxy_async_smem();
                 ptx::tc_fence_after();
-                const uint32_t a = ptx::smem_addr(mem + at * s.stage()), b = a + TILE * P_STEP * 2;
-                ptx::mma_bf16_elect_x4(tmem, ptx::sw128_kmajor_desc(a), TRANS ? ptx::plain_mnmajor_desc(b, 128, W1_COLUMN) : ptx::sw128_kmajor_desc(b),
-                                       32 / 16, (TRANS ? 256 : 32) / 16, TRANS ? ptx::idesc_bf16_f32_bmn(TILE, s.rp) : ptx::idesc_bf16_f32(TILE, s.rp), it > 0);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    if ((s0 + it) * P_STEP + h * P_BLOCK >= p.from) break;
+                    const uint32_t a = ptx::smem_addr(mem) + at * s.stage() + h * s.block(), b = a + TILE * P_BLOCK * 2;
+                    ptx::mma_bf16_elect_x4(tmem, ptx::sw128_kmajor_desc(a), TRANS ? ptx::plain_mnmajor_desc(b, 128, W1_COLUMN) : ptx::sw128_kmajor_desc(b),
+                                           32 / 16, (TRANS ? 256 : 32) / 16, TRANS ? ptx::idesc_bf16_f32_bmn(TILE, s.rp) : ptx::idesc_bf16_f32(TILE, s.rp), it > 0 || h > 0);
+                }
                 ptx::mma_commit_elect(&empty[at]);
                 at = at + 1 == n_stages ? 0 : at + 1;
                 phase = at ? phase : phase ^ 1u;
             }
             ptx::mma_commit_elect(done);
+        } else if (n > 0) {
+            bring_w2(0, 1, chunk0 * COLS, ok);
         }
         __syncwarp();
         wait(done, 0, ok);
         __syncwarp();
-        // The ring is free: the sums, and w2's second chunk.
+        // The ring is free: the sums.
         float* sums = reinterpret_cast<float*>(mem);
         if (warp < P_WARPS) {
             ptx::tc_fence_after();
@@ -573,7 +638,8 @@ struct Pass {
             case 4: join<4>(sums, scale); break;
             default: join<8>(sums, scale); break;
         }
-        if (warp < P_WARPS) fill(1, s.early_chunks(), chunk0, chunk1);
+        const int early = s.early_chunks() >= 2 && n >= 2 ? 2 : 1;  // chunks of w2 that are brought before all meet again: one to a group
+        if (warp > P_WARPS) bring_w2(1, early, chunk0 * COLS, ok);
         // All of mid is here: none of this CTA's peers reads its sums any more, and what they sent has come.
         if (p.splits > 1) {
             wait(mid_full, 0, ok);
@@ -586,12 +652,6 @@ struct Pass {
             ptx::tc_fence_before();
         }
         __syncthreads();
-        if (warp < P_WARPS) {
-            ptx::cp_async_wait_all();
-            filled(0, s.early_chunks());
-            fill(s.early_chunks(), n_bufs, chunk0, chunk1);
-        }
-        const int n = chunk1 - chunk0;
         if (warp == P_WARPS) {
             ptx::tc_fence_after();
             int buf = 0;
@@ -604,59 +664,57 @@ struct Pass {
                 ptx::fence_proxy_async_smem();
                 ptx::tc_fence_after();
                 const uint32_t w = ptx::smem_addr(w2_buf(buf));
-                buf = buf + 1 == n_bufs ? 0 : buf + 1;
-                phase = buf ? phase : phase ^ 1u;
                 const uint64_t wd = ptx::plain_kmajor_desc(w, s.column(), 144), w_step = 2 * s.column() / 16;
                 const uint32_t idesc = TRANS ? ptx::idesc_bf16_f32_bmn(TILE, COLS) : ptx::idesc_bf16_f32(TILE, COLS);
                 const int whole = s.rp / 32;  // of the reduction, in twice three MMAs
                 for (int k = 0; k < whole; ++k) ptx::mma_bf16_parts_x2(tmem + COLS * b, parts + 16 * k, wd + 2 * k * w_step, s.rp / 2, w_step, idesc, k > 0);
                 if (s.rp & 16) ptx::mma_bf16_parts(tmem + COLS * b, parts + 16 * whole, wd + 2 * whole * w_step, s.rp / 2, idesc, whole > 0);
                 ptx::mma_commit_elect(&d_full[b]);
+                ptx::mma_commit_elect(&w2_empty[buf]);
+                buf = buf + 1 == n_bufs ? 0 : buf + 1;
+                phase = buf ? phase : phase ^ 1u;
             }
+        } else if (warp > P_WARPS) {
+            bring_w2(early, n, chunk0 * COLS, ok);
         } else if (group < n) {
-            // This group's chunks, every other one; base a turn ahead, in two sets of registers by turns (a copy between them would wait for what
-            // is on its way).
-            Held held[2];
-            load_base(held[0], 0, (chunk0 + group) * COLS, false);
-            int buf = group % n_bufs, before = 0;  // w2's buffer of this chunk and of the group's last one
-            for (int j0 = group; j0 < n; j0 += 4 / TURNS)
+            // This group's chunks, every other one; base P_DEPTH turns ahead.
+            const auto ask = [&](int slot, int j, int t) {  // turn t from chunk j's beginning on
+                const int c = j + 2 * (t / TURNS), c0 = (chunk0 + c) * COLS;
+                ask_base(slot, t % TURNS, c0, c0 + COLS <= p.to, c < n);
+                ptx::cp_async_commit();
+            };
 #pragma unroll
-                for (int jj = 0; jj < 2 / TURNS; ++jj) {
-                    const int j = j0 + 2 * jj;
-                    if (j >= n) break;
-                    const int b = j & (BUFS - 1), c0 = (chunk0 + j) * COLS;
-                    const bool whole = c0 + COLS <= p.to, next = c0 + 3 * COLS <= p.to;
-                    if (TURNS == 2)
-                        load_base(held[1], 1, c0, whole);
-                    else
-                        load_base(held[(jj + 1) & 1], 0, c0 + 2 * COLS, next, j + 2 < n);
-                    wait(&d_full[b], static_cast<uint32_t>(j / BUFS) & 1u, ok);
-                    __syncwarp();
-                    ptx::tc_fence_after();
+            for (int t = 0; t < P_DEPTH; ++t) ask(t, group, t);
+            int slot = 0;
+            for (int j = group; j < n; j += 2) {
+                const int c0 = (chunk0 + j) * COLS;
+                const bool whole = c0 + COLS <= p.to;
+                wait(&d_full[group], static_cast<uint32_t>(j >> 1) & 1u, ok);
+                __syncwarp();
+                ptx::tc_fence_after();
+                const uint32_t at = tmem + COLS * group + 64 * ((warp >> 2) & 1) + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
+#pragma unroll
+                for (int q = 0; q < VECTORS / 4; ++q) {
                     uint32_t v[2][16];
-                    const uint32_t at = tmem + COLS * b + 32 * SIDES * ((warp >> 2) & 1) + (static_cast<uint32_t>(32 * (warp & 3)) << 16);
-                    ptx::tmem_ld_16x256b_x4(at, v[0]);
-                    ptx::tmem_ld_16x256b_x4(at + (HALVED ? 32u : 16u << 16), v[1]);
-                    // w2 for this buffer's next chunk, and word of what was asked for a turn ago
-                    if (j + n_bufs < n) load_w2(w2_buf(buf), c0 + n_bufs * COLS);
-                    ptx::cp_async_commit();
-                    ptx::cp_async_wait<1>();
-                    if (j < 2)
-                        filled(s.early_chunks(), n_bufs);
-                    else if (j - 2 + n_bufs < n)
-                        arrive(&w2_full[before]);
-                    before = buf;
-                    buf += 2;
-                    buf = buf >= n_bufs ? buf - n_bufs : buf;
+                    ptx::tmem_ld_16x256b_x4(at + 32 * q, v[0]);
+                    ptx::tmem_ld_16x256b_x4(at + (HALVED ? 32u : 32 * q + (16u << 16)), v[1]);
                     ptx::tmem_ld_wait();
-                    ptx::tc_fence_before();
-                    ptx::mbar_arrive_if(&d_empty[b], lane == 0);
-                    finish(held[TURNS == 1 ? jj & 1 : 0], v, 0, c0, whole, ok);
-                    if constexpr (TURNS == 2) {
-                        load_base(held[0], 0, c0 + 2 * COLS, next, j + 2 < n);
-                        finish(held[1], v, 1, c0, whole, ok);
+                    if (q + 1 == VECTORS / 4) {
+                        ptx::tc_fence_before();
+                        ptx::mbar_arrive_if(&d_empty[group], lane == 0);
+                    }
+#pragma unroll
+                    for (int h = 0; h < 4 / HOLD; ++h) {
+                        const int t = q * (4 / HOLD) + h;
+                        ptx::cp_async_wait<P_DEPTH - 1>();
+                        Held held;
+                        get_base(held, slot, t, c0);
+                        finish(held, v, t, c0, whole, ok);
+                        ask(slot, j, t + P_DEPTH);  // what the slot held is in registers
+                        slot = slot + 1 == P_DEPTH ? 0 : slot + 1;
                     }
                 }
+            }
         }
         __syncwarp();
         ptx::cp_async_wait_all();
