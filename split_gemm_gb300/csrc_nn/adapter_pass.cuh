@@ -158,8 +158,15 @@ struct Pass {
         }
     }
 
-    // w2's columns of a chunk from c0 on, by the warps that bring it: column c of 32 becomes row 8((c>>1)&3) + 2(c>>3) + (c&1) of the operand.
-    __device__ __forceinline__ static int place_of(int c) { return (c & ~31) + 8 * ((c >> 1) & 3) + 2 * ((c >> 3) & 3) + (c & 1); }
+    // A thread finishes vectors of 8 elements: of 32 columns, one run of 8 or, where base or out has 32 bits, two of 4 at 16 columns' distance, so that
+    // four threads' runs are whole sectors.  It gets columns 8j + 2(lane%4) + {0, 1} of the accumulator, j = 0 .. 3; w2's column c becomes row
+    // place_of(c) of the operand for that.
+    static constexpr int RUN = sizeof(TB) == 2 && sizeof(TO) == 2 ? 8 : 4, RUNS = 8 / RUN;
+    __device__ __forceinline__ static int place_of(int c)
+    {
+        return (c & ~31) + (c & 1) + (RUN == 8 ? 8 * ((c >> 1) & 3) + 2 * ((c >> 3) & 3) : 8 * (2 * ((c >> 4) & 1) + ((c >> 1) & 1)) + 2 * ((c >> 2) & 3));
+    }
+    // w2's columns of a chunk from c0 on, by the warps that bring it.
     __device__ __forceinline__ void load_w2(uint8_t* buf, int c0) const
     {
         const int64_t size = static_cast<int64_t>(p.rank) * p.to;
@@ -179,8 +186,8 @@ struct Pass {
                     ptx::cp_async_16_if(dst + (n & 7) * 16 + (n >> 3) * 144, src, c8 < per);
                 }
             } else {
-                const int c = 2 * lane;
-                const uint32_t dst = at + ((c >> 3) & 3) * 4 + (((c >> 1) & 3) + 4 * (c >> 5)) * 144;
+                const int c = 2 * lane, n = place_of(c);
+                const uint32_t dst = at + (n & 7) * 2 + (n >> 3) * 144;
                 const __nv_bfloat16* src = w + static_cast<int64_t>(ww) * p.to + c0 + c;
 #pragma unroll 4
                 for (int k = ww; k < p.rank; k += P_W2_WARPS, src += P_W2_WARPS * static_cast<int64_t>(p.to)) {
@@ -322,8 +329,7 @@ struct Pass {
         ptx::tmem_st_wait();
     }
 
-    // A thread finishes eight times (four of a halved tile) 8 neighbouring elements of a chunk, two side by side at 32 columns' distance in each of its
-    // rows, 8 rows apart.  It holds HOLD of them at a time, a turn: 64 bytes of base.
+    // A thread finishes eight vectors (four of a halved tile) of a chunk, two side by side at 32 columns' distance in each of its rows, 8 rows apart.  It holds HOLD of them at a time, a turn: 64 bytes of base.
     static constexpr int MINE = 4 >> HALVED, VECTORS = 2 * MINE;  // rows of a thread
     static constexpr int HOLD = sizeof(TB) == 2 ? 4 : 2, TURNS = VECTORS / HOLD, WORDS = 2 * sizeof(TB);
     struct Held {
@@ -334,7 +340,7 @@ struct Pass {
     __device__ __forceinline__ static constexpr int row_index(int i) { return i % MINE; }
     __device__ __forceinline__ static constexpr int side_of(int i) { return i / MINE; }
     __device__ __forceinline__ int row_of(int i) const { return LANES * (warp & 3) + (lane >> 2) + 8 * row_index(i); }
-    __device__ __forceinline__ int col_of(int i, int c0) const { return c0 + 64 * ((warp >> 2) & 1) + 32 * side_of(i) + 8 * (lane & 3); }
+    __device__ __forceinline__ int col_of(int i, int c0) const { return c0 + 64 * ((warp >> 2) & 1) + 32 * side_of(i) + RUN * (lane & 3); }
     __device__ __forceinline__ void make_rows()
     {
 #pragma unroll
@@ -349,30 +355,44 @@ struct Pass {
     bool row_here[MINE], base_here[MINE];  // the thread's rows are of the tile; and there is a base
     // Turn `turn` of the chunk at c0, on its way to slot `slot` of the thread's ring (which no other thread reads: it has no barrier); `whole`: all
     // the chunk's columns exist.
+    static constexpr int PIECE = RUN * sizeof(TB);  // bytes of a run of base
     __device__ __forceinline__ void ask_base(int slot, int turn, int c0, bool whole, bool wanted) const
     {
         if constexpr (VEC) {
-            const uint32_t at = base_ring() + slot * (P_LOADERS * 64);
+            const uint32_t at = base_ring() + slot * (P_LOADERS * 64) - tid * (16 - PIECE);
 #pragma unroll
             for (int k = 0; k < HOLD; ++k) {
                 const int side = (turn * HOLD + k) / MINE;
                 const bool upper = HOLD < MINE && (turn & 1);  // rows 2 and 3 of four
                 const TB* src = (upper ? base_at[(k + HOLD) % MINE] : base_at[k % MINE]) + c0 + 32 * side;
-                const bool here = wanted && (upper ? base_here[(k + HOLD) % MINE] : base_here[k % MINE]) && (whole || col_of(0, c0) + 32 * side < p.to);
+                const bool here = wanted && (upper ? base_here[(k + HOLD) % MINE] : base_here[k % MINE]);
 #pragma unroll
-                for (int j = 0; j < WORDS / 4; ++j) ptx::cp_async_16_if(at + (k * (WORDS / 4) + j) * (P_LOADERS * 16), reinterpret_cast<const uint4*>(src) + j, here);
+                for (int r = 0; r < RUNS; ++r) {
+                    const bool in = here && (whole || col_of(0, c0) + 32 * side + 16 * r < p.to);
+                    const uint32_t dst = at + (k * RUNS + r) * (P_LOADERS * PIECE);
+                    if constexpr (PIECE == 16)
+                        ptx::cp_async_16_if(dst, src + 16 * r, in);
+                    else
+                        ptx::cp_async_8_if(dst, src + 16 * r, in);
+                }
             }
         }
     }
     __device__ __forceinline__ void get_base(Held& b, int slot, int turn, int c0) const
     {
         if constexpr (VEC) {
-            const uint32_t at = base_ring() + slot * (P_LOADERS * 64);
+            const uint32_t at = base_ring() + slot * (P_LOADERS * 64) - tid * (16 - PIECE);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const uint4 q = ptx::ld_shared_v4(at + i * (P_LOADERS * 16));
-                const int k = i / (WORDS / 4), j = i % (WORDS / 4) * 4;
-                b.u[k][j] = q.x, b.u[k][j + 1] = q.y, b.u[k][j + 2] = q.z, b.u[k][j + 3] = q.w;
+            for (int i = 0; i < HOLD * RUNS; ++i) {
+                constexpr int W = PIECE / 4;
+                uint32_t* to = b.u[i / RUNS] + i % RUNS * W;
+                if constexpr (PIECE == 16) {
+                    const uint4 q = ptx::ld_shared_v4(at + i * (P_LOADERS * 16));
+                    to[0] = q.x, to[1] = q.y, to[2] = q.z, to[3] = q.w;
+                } else {
+                    const uint2 q = ptx::ld_shared_v2(at + i * (P_LOADERS * 8));
+                    to[0] = q.x, to[1] = q.y;
+                }
             }
         } else {
             load_base(b, turn, c0);
@@ -384,21 +404,13 @@ struct Pass {
 #pragma unroll
         for (int k = 0; k < HOLD; ++k) {
             const int i = turn * HOLD + k;
-            const TB* src = base_at[row_index(i)] + c0 + 32 * side_of(i);
-            const int left = base_here[row_index(i)] ? p.to - col_of(i, c0) : 0;
-            if constexpr (VEC) {
+            TB* v = reinterpret_cast<TB*>(b.u[k]);
 #pragma unroll
-                for (int j = 0; j < WORDS; j += 4) {
-                    const uint4 q = ptx::ld_stream_v4_if(reinterpret_cast<const uint4*>(src) + j / 4, left > 0);
-                    b.u[k][j] = q.x, b.u[k][j + 1] = q.y, b.u[k][j + 2] = q.z, b.u[k][j + 3] = q.w;
-                }
-            } else {
-                TB* v = reinterpret_cast<TB*>(b.u[k]);
+            for (int r = 0; r < RUNS; ++r) {
+                const TB* src = base_at[row_index(i)] + c0 + 32 * side_of(i) + 16 * r;
+                const int left = base_here[row_index(i)] ? p.to - col_of(i, c0) - 16 * r : 0;
 #pragma unroll
-                for (int j = 0; j < WORDS; ++j) b.u[k][j] = 0u;
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (j < left) v[j] = src[j];
+                for (int j = 0; j < RUN; ++j) v[r * RUN + j] = j < left ? src[j] : TB(0.f);
             }
         }
     }
@@ -426,34 +438,37 @@ struct Pass {
 #pragma unroll
         for (int k = 0; k < HOLD; ++k) {
             const int i = turn * HOLD + k;
-            TO* row = out_at[row_index(i)] + c0 + 32 * side_of(i);
-            if constexpr (VEC) {
-                const bool here = live && row_here[row_index(i)] && (whole || col_of(i, c0) < p.to);
-                if constexpr (sizeof(TO) == 4) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        ptx::st_stream_v4_if(row + 4 * h, make_uint4(__float_as_uint(f[k][2 * h].x), __float_as_uint(f[k][2 * h].y), __float_as_uint(f[k][2 * h + 1].x),
-                                                                     __float_as_uint(f[k][2 * h + 1].y)), here);
+            for (int r = 0; r < RUNS; ++r) {
+                TO* row = out_at[row_index(i)] + c0 + 32 * side_of(i) + 16 * r;
+                const float2* from = f[k] + r * (RUN / 2);
+                const int col = col_of(i, c0) + 16 * r;
+                const bool here = live && row_here[row_index(i)];
+                if constexpr (!VEC) {
+#pragma unroll
+                    for (int j = 0; j < RUN; ++j)
+                        if (here && col + j < p.to) mx::from_float(row[j], j % 2 ? from[j / 2].y : from[j / 2].x);
+                } else if constexpr (sizeof(TO) == 4) {
+                    ptx::st_stream_v4_if(row, make_uint4(__float_as_uint(from[0].x), __float_as_uint(from[0].y), __float_as_uint(from[1].x), __float_as_uint(from[1].y)),
+                                         here && (whole || col < p.to));
                 } else {
-                    uint32_t o[4];
+                    uint32_t o[RUN / 2];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const __nv_bfloat162 h = __floats2bfloat162_rn(f[k][j].x, f[k][j].y);
+                    for (int j = 0; j < RUN / 2; ++j) {
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(from[j].x, from[j].y);
                         o[j] = *reinterpret_cast<const uint32_t*>(&h);
                     }
-                    ptx::st_stream_v4_if(row, make_uint4(o[0], o[1], o[2], o[3]), here);
+                    if constexpr (RUN == 8)
+                        ptx::st_stream_v4_if(row, make_uint4(o[0], o[1], o[2], o[3]), here && (whole || col < p.to));
+                    else
+                        ptx::st_stream_v2_if(row, make_uint2(o[0], o[1]), here && (whole || col < p.to));
                 }
-            } else {
-                const int left = live && row_here[row_index(i)] ? p.to - col_of(i, c0) : 0;
-#pragma unroll
-                for (int j = 0; j < 8; ++j)
-                    if (j < left) mx::from_float(row[j], j % 2 ? f[k][j / 2].y : f[k][j / 2].x);
             }
         }
     }
 
     // Base's first chunks to L2, where HBM works on them while the sums are joined.
-    static constexpr int AHEAD = 2;
+    static constexpr int AHEAD = sizeof(TB) == 4 ? 4 : 2;
     __device__ __forceinline__ void prefetch_base(int chunk0, int chunk1) const
     {
         constexpr int LINES = AHEAD * COLS * sizeof(TB) / 128, EACH = 128 / sizeof(TB);

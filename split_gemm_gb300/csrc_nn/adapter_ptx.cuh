@@ -118,6 +118,35 @@ __device__ __forceinline__ void cp_async_4_if(uint32_t dst, const void* src, boo
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p cp.async.ca.shared.global [%0], [%1], 4;\n\t}" ::"r"(dst), "l"(src), "r"(static_cast<uint32_t>(p))
                  : "memory");
 }
+__device__ __forceinline__ void cp_async_8_if(uint32_t dst, const void* src, bool p)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\t@p cp.async.ca.shared.global [%0], [%1], 8;\n\t}" ::"r"(dst), "l"(src), "r"(static_cast<uint32_t>(p))
+                 : "memory");
+}
+__device__ __forceinline__ void cp_async_16_fill_if(uint32_t dst, const void* src, uint32_t src_bytes, bool p)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\t@p cp.async.cg.shared.global [%0], [%1], 16, %2;\n\t}" ::"r"(dst), "l"(src), "r"(src_bytes),
+                 "r"(static_cast<uint32_t>(p))
+                 : "memory");
+}
+__device__ __forceinline__ uint4 ld_v4_if(const void* src, bool p)
+{
+    uint4 v;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\tmov.b32 %0, 0;\n\tmov.b32 %1, 0;\n\tmov.b32 %2, 0;\n\tmov.b32 %3, 0;\n\t"
+        "@p ld.global.v4.b32 {%0, %1, %2, %3}, [%4];\n\t}"
+        : "=&r"(v.x), "=&r"(v.y), "=&r"(v.z), "=&r"(v.w)
+        : "l"(src), "r"(static_cast<uint32_t>(p))
+        : "memory");
+    return v;
+}
+__device__ __forceinline__ uint32_t ld_u8_if(const void* src, bool p)
+{
+    uint32_t v;
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %2, 0;\n\tmov.b32 %0, 0;\n\t@p ld.global.u8 %0, [%1];\n\t}" : "=&r"(v) : "l"(src), "r"(static_cast<uint32_t>(p))
+                 : "memory");
+    return v;
+}
 // Streaming: what is read or written once.
 __device__ __forceinline__ uint4 ld_stream_v4_if(const void* src, bool p)
 {
@@ -135,6 +164,18 @@ __device__ __forceinline__ void st_stream_v4_if(void* dst, uint4 v, bool p)
     asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %5, 0;\n\t@p st.global.cs.v4.b32 [%0], {%1, %2, %3, %4};\n\t}" ::"l"(dst), "r"(v.x), "r"(v.y), "r"(v.z),
                  "r"(v.w), "r"(static_cast<uint32_t>(p))
                  : "memory");
+}
+__device__ __forceinline__ void st_stream_v2_if(void* dst, uint2 v, bool p)
+{
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %3, 0;\n\t@p st.global.cs.v2.b32 [%0], {%1, %2};\n\t}" ::"l"(dst), "r"(v.x), "r"(v.y),
+                 "r"(static_cast<uint32_t>(p))
+                 : "memory");
+}
+__device__ __forceinline__ uint2 ld_shared_v2(uint32_t addr)
+{
+    uint2 v;
+    asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
+    return v;
 }
 __device__ __forceinline__ void mbar_arrive_if(uint64_t* bar, bool p)
 {

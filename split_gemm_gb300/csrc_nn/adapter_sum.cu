@@ -34,8 +34,8 @@ struct SumSmem {
     __host__ __device__ constexpr int in_bytes() const { return 16 * blocks * column(); }
     __host__ __device__ constexpr int stage() const { return in_bytes() + 3 * rp / 8 * column(); }
     __host__ __device__ constexpr int stages() const { return 3; }
-    // the plan's part: rows' numbers, tiles, stages
-    __host__ __device__ constexpr int lists() const { return SUM_TILES * (TILE * 4 + 16) + SUM_TILES * 4 * 4; }
+    // the plan's part: rows' numbers and each stage's tile by stage, the tiles
+    __host__ __device__ constexpr int lists() const { return SUM_TILES * (TILE * 4 + 16) + SUM_TILES * 4 * 4 + 16; }
     __host__ __device__ constexpr int bytes() const { return stages() * stage() + lists() + 256; }
 };
 
@@ -45,22 +45,21 @@ struct Sum {
     const SumJob& job;
     const SumSmem s;
     uint8_t* mem;
-    int *ids, *steps;  // row numbers by tile (-1: none); stages: tile * 4 + part
-    Piece* tiles;
+    const int *ids, *steps;  // by stage: its rows' numbers (-1: none), its tile
+    const Piece* tiles;
     uint64_t *full, *empty, *done, *free_;
     volatile uint32_t* abort_flag;
     int tid, warp, lane, c0, n;
 
-    __device__ __forceinline__ bool wait(uint64_t* bar, uint32_t parity, bool& ok) const
+    // As in the pass: once a wait has run out, the thread waits no more.
+    __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, bool& ok) const
     {
-        if (ok && !ptx::mbar_wait(bar, parity, U_WAIT_NS)) {
+        if (!ptx::mbar_try_wait(bar, parity) && ok && !ptx::mbar_wait(bar, parity, U_WAIT_NS)) {
             ok = false;
             *abort_flag = 1u;
         }
-        return ok;
     }
-    __device__ __forceinline__ int row_at(int k, int t) const { return ids[(steps[k] >> 2) * TILE + (steps[k] & 3) * s.tokens + t]; }
-    __device__ __forceinline__ int adapter_at(int k) const { return tiles[steps[k] >> 2].adapter; }
+    __device__ __forceinline__ int adapter_at(int k) const { return tiles[steps[k]].adapter; }
     __device__ __forceinline__ bool ends_run(int k) const { return k + 1 == n || adapter_at(k + 1) != adapter_at(k); }
 
     // What a thread holds of a stage on its way.
@@ -70,58 +69,62 @@ struct Sum {
         float4 mid[2];
     };
 
-    // The thread's 16-byte columns of mid: token and 8 r's; whether there is one.
-    __device__ __forceinline__ bool mid_place(int& t, int& r8) const
+    // The thread's place in a stage: mid's token and 8 ranks, if it has any; in's columns and the four (two of a checkpoint) tokens from `row` on.
+    int mid_token, mid_rank, row, col;
+    bool has_mid, has_in;
+    __device__ __forceinline__ void find_place()
     {
         const int per = s.rp >> 3;
-        t = tid / per;
-        r8 = tid - t * per;
-        return t < s.tokens;
+        mid_token = tid / per;
+        mid_rank = tid - mid_token * per;
+        has_mid = mid_token < s.tokens;
+        if constexpr (MODE == 2) {  // 16 threads to two rows
+            row = 2 * (tid >> 4);
+            col = c0 + 16 * (tid & 15);
+            has_in = row < s.tokens && (s.blocks == 2 || (tid & 15) < 8) && col < job.blocks * 32;
+        } else {  // a warp to four
+            row = 4 * warp;
+            col = c0 + 8 * lane;
+            has_in = row < s.tokens && lane < 16 * s.blocks && col < job.cols;
+        }
+    }
+    // Whether the thread's part of in's place in a stage exists (it is zero where in has none).
+    __device__ __forceinline__ bool stores_in() const
+    {
+        return row < s.tokens && (MODE == 2 ? s.blocks == 2 || (tid & 15) < 8 : lane < 16 * s.blocks);
     }
 
     __device__ __forceinline__ void fetch(Held& h, int k) const
     {
+        const int* rows = ids + k * s.tokens;
         if constexpr (MODE == 2) {
+            const int2 t = has_in ? *reinterpret_cast<const int2*>(rows + row) : make_int2(-1, -1);
+            const int64_t pitch = job.blocks * 32;
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {  // 16 threads to a row
-                const int t = (tid >> 4) + 32 * i, c = c0 + 16 * (tid & 15);
-                h.x[i] = make_uint4(0, 0, 0, 0);
-                h.scale[i] = 0u;
-                if (t >= s.tokens || (s.blocks == 1 && (tid & 8))) continue;
-                const int64_t row = row_at(k, t);
-                if (row >= 0 && c < job.blocks * 32) {
-                    h.x[i] = __ldg(reinterpret_cast<const uint4*>(job.data + row * (job.blocks * 32) + c));
-                    h.scale[i] = __ldg(job.scales + row * job.blocks + (c >> 5));
-                }
+            for (int i = 0; i < 2; ++i) {
+                const int64_t r = i ? t.y : t.x;
+                h.x[i] = ptx::ld_stream_v4_if(job.data + r * pitch + col, r >= 0);
+                h.scale[i] = ptx::ld_u8_if(job.scales + r * job.blocks + (col >> 5), r >= 0);
             }
         } else if constexpr (MODE == 1) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {  // a warp to a row
-                const int t = warp + U_WARPS * i, c = c0 + 8 * lane;
+            for (int i = 0; i < 4; ++i) {
+                const int64_t r = has_in ? rows[row + i] : -1;
                 uint32_t v[4] = {0u, 0u, 0u, 0u};
-                if (t < s.tokens && lane < 16 * s.blocks) {
-                    const int64_t row = row_at(k, t);
-                    if (row >= 0 && c < job.cols) mx::load_any<4, 2>(v, job.in + row * job.in_stride + c, job.cols - c < 8 ? 2 * (job.cols - c) : 16);
-                }
+                if (r >= 0) mx::load_any<4, 2>(v, job.in + r * job.in_stride + col, job.cols - col < 8 ? 2 * (job.cols - col) : 16);
                 h.x[i] = make_uint4(v[0], v[1], v[2], v[3]);
             }
         }
-        int t, r8;
-        h.mid[0] = h.mid[1] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (mid_place(t, r8)) {
-            const int64_t row = row_at(k, t);
-            if (row >= 0) {
-                const float* m = job.mid + row * p.rank + 8 * r8;
-                if (job.mid_vec) {
-                    if (8 * r8 < p.rank) h.mid[0] = __ldg(reinterpret_cast<const float4*>(m));
-                    if (8 * r8 + 4 < p.rank) h.mid[1] = __ldg(reinterpret_cast<const float4*>(m) + 1);
-                } else {
-                    float* v = reinterpret_cast<float*>(h.mid);
+        const int64_t r = has_mid ? rows[mid_token] : -1;
+        const float* m = job.mid + r * p.rank + 8 * mid_rank;
+        if (job.mid_vec) {
+            const uint4 a = ptx::ld_v4_if(m, r >= 0 && 8 * mid_rank < p.rank), b = ptx::ld_v4_if(m + 4, r >= 0 && 8 * mid_rank + 4 < p.rank);
+            h.mid[0] = make_float4(__uint_as_float(a.x), __uint_as_float(a.y), __uint_as_float(a.z), __uint_as_float(a.w));
+            h.mid[1] = make_float4(__uint_as_float(b.x), __uint_as_float(b.y), __uint_as_float(b.z), __uint_as_float(b.w));
+        } else {
+            float* v = reinterpret_cast<float*>(h.mid);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        if (8 * r8 + i < p.rank) v[i] = __ldg(m + i);
-                }
-            }
+            for (int i = 0; i < 8; ++i) v[i] = r >= 0 && 8 * mid_rank + i < p.rank ? __ldg(m + i) : 0.f;
         }
     }
 
@@ -140,14 +143,12 @@ struct Sum {
         return make_uint2(o[0], o[1]);
     }
 
-    __device__ __forceinline__ void store(const Held& h, uint8_t* st) const
+    __device__ __forceinline__ void store(const Held& h, uint32_t at) const
     {
-        const uint32_t at = ptx::smem_addr(st);
         if constexpr (MODE == 2) {
+            if (stores_in())
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int t = (tid >> 4) + 32 * i;
-                if (t >= s.tokens || (s.blocks == 1 && (tid & 8))) continue;
                 const uint32_t w[4] = {h.x[i].x, h.x[i].y, h.x[i].z, h.x[i].w};
                 uint32_t o[8];
                 if (h.scale[i] <= 252u) {
@@ -171,19 +172,16 @@ struct Sum {
                         }
                     }
                 }
-                const uint32_t dst = at + t * 16 + 2 * (tid & 15) * s.column();
+                const uint32_t dst = at + (row + i) * 16 + 2 * (tid & 15) * s.column();
                 ptx::st_shared_v4(dst, o[0], o[1], o[2], o[3]);
                 ptx::st_shared_v4(dst + s.column(), o[4], o[5], o[6], o[7]);
             }
         } else if constexpr (MODE == 1) {
+            if (stores_in())
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int t = warp + U_WARPS * i;
-                if (t < s.tokens && lane < 16 * s.blocks) ptx::st_shared_v4(at + t * 16 + lane * s.column(), h.x[i].x, h.x[i].y, h.x[i].z, h.x[i].w);
-            }
+                for (int i = 0; i < 4; ++i) ptx::st_shared_v4(at + (row + i) * 16 + lane * s.column(), h.x[i].x, h.x[i].y, h.x[i].z, h.x[i].w);
         }
-        int t, r8;
-        if (mid_place(t, r8)) {
+        if (has_mid) {
             const float v[8] = {h.mid[0].x, h.mid[0].y, h.mid[0].z, h.mid[0].w, h.mid[1].x, h.mid[1].y, h.mid[1].z, h.mid[1].w};
             uint32_t o[3][4];
 #pragma unroll
@@ -200,24 +198,23 @@ struct Sum {
 #pragma unroll
                 for (int q = 0; q < 3; ++q) o[q][i] = __byte_perm(b[0][q], b[1][q], 0x7632);
             }
-            const uint32_t dst = at + s.in_bytes() + t * 16 + r8 * s.column();
+            const uint32_t dst = at + s.in_bytes() + mid_token * 16 + mid_rank * s.column();
 #pragma unroll
             for (int q = 0; q < 3; ++q) ptx::st_shared_v4(dst + q * (s.rp >> 3) * s.column(), o[q][0], o[q][1], o[q][2], o[q][3]);
         }
     }
 
-    // bf16 rows straight into their place.
-    __device__ __forceinline__ void copy(uint8_t* st, int k) const
+    // bf16 rows straight into their place; zeros for what is not there.
+    __device__ __forceinline__ void copy(uint32_t at, int k) const
     {
-        const uint32_t at = ptx::smem_addr(st);
+        const int4 t = row < s.tokens ? *reinterpret_cast<const int4*>(ids + k * s.tokens + row) : make_int4(-1, -1, -1, -1);
+        const uint32_t dst = at + row * 16 + lane * s.column();
+        const int rows[4] = {t.x, t.y, t.z, t.w};
+        const bool mine = stores_in();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int t = warp + U_WARPS * i, c = c0 + 8 * lane;
-            if (t < s.tokens && lane < 16 * s.blocks) {
-                const int64_t row = row_at(k, t);
-                const bool have = row >= 0 && c < job.cols;
-                ptx::cp_async_16s(at + t * 16 + lane * s.column(), have ? job.in + row * job.in_stride + c : job.in, have ? 16 : 0);
-            }
+            const bool have = has_in && rows[i] >= 0;
+            ptx::cp_async_16_fill_if(dst + 16 * i, have ? job.in + rows[i] * job.in_stride + col : job.in, have ? 16 : 0, mine);
         }
     }
 
@@ -225,7 +222,7 @@ struct Sum {
     __device__ __forceinline__ void flush(uint32_t tmem, int k, int first, bool ok) const
     {
         const int e = adapter_at(k), piece = blockIdx.x / p.per_piece;
-        const int t0 = piece * p.tiles_each + (steps[first] >> 2), t1 = piece * p.tiles_each + (steps[k] >> 2) + 1;
+        const int t0 = piece * p.tiles_each + steps[first], t1 = piece * p.tiles_each + steps[k] + 1;
         const bool before = p.plan.tile_starts[e] < t0, after = p.plan.tile_starts[e + 1] > t1;
         const int64_t size = static_cast<int64_t>(p.rank) * job.cols;
         float* out = before || after ? job.part + (2 * piece + !before) * size : job.out + e * size;
@@ -233,17 +230,19 @@ struct Sum {
         for (int item = warp >> 2; item < groups * s.blocks; item += U_WARPS / 4) {
             const int m = item / groups, r0 = (item - m * groups) * 16;
             const int c = c0 + 128 * m + 32 * (warp & 3) + lane;
-            uint32_t v[3][16];
+            float f[16];
 #pragma unroll
-            for (int q = 0; q < 3; ++q) ptx::tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + (3 * m + q) * s.rp + r0, v[q]);
-            ptx::tmem_ld_wait();
+            for (int q = 2; q >= 0; --q) {  // the smallest parts first
+                uint32_t v[16];
+                ptx::tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + (3 * m + q) * s.rp + r0, v);
+                ptx::tmem_ld_wait();
+#pragma unroll
+                for (int i = 0; i < 16; ++i) f[i] = q == 2 ? __uint_as_float(v[i]) : __uint_as_float(v[i]) + f[i];
+            }
             if (!ok || c >= job.cols) {
                 __syncwarp();
                 continue;
             }
-            float f[16];
-#pragma unroll
-            for (int i = 0; i < 16; ++i) f[i] = __uint_as_float(v[0][i]) + (__uint_as_float(v[1][i]) + __uint_as_float(v[2][i]));
             if (job.out_col == 1) {
 #pragma unroll
                 for (int i = 0; i < 16; ++i)
@@ -267,28 +266,31 @@ struct Sum {
     __device__ __forceinline__ void load(uint32_t tmem)
     {
         bool ok = true;
+        find_place();
         constexpr int DEPTH = MODE == 1 ? 1 : 2;
         Held held[DEPTH];
 #pragma unroll
         for (int i = 0; i < DEPTH; ++i)
             if (i < n) fetch(held[i], i);
         int first = 0, runs = 0, told = 0;  // told: stages before it have been told of
+        int at = 0, before = 0;  // slots of this stage and of the last one
+        uint32_t free_phase = 1u;
         for (int k0 = 0; k0 < n; k0 += DEPTH)
 #pragma unroll
             for (int i = 0; i < DEPTH; ++i) {
                 const int k = k0 + i;
                 if (k >= n) break;
-                const int at = k % s.stages();
-                uint8_t* st = mem + at * s.stage();
-                wait(&empty[at], (static_cast<uint32_t>(k / s.stages()) & 1u) ^ 1u, ok);
+                const uint32_t st = ptx::smem_addr(mem) + at * s.stage();
+                const bool last = ends_run(k);
+                wait(&empty[at], free_phase, ok);
                 if constexpr (MODE == 0) {
                     copy(st, k);
                     ptx::cp_async_commit();
                 }
                 store(held[i], st);
+                if (k + DEPTH < n) fetch(held[i], k + DEPTH);
                 ptx::fence_proxy_async_smem();
                 // One arrival to a warp (a barrier takes its arrivals one after another); copies' stages are told of a stage later.
-                const bool last = ends_run(k);
                 if constexpr (MODE == 0) {
                     if (last)
                         ptx::cp_async_wait<0>();
@@ -296,12 +298,12 @@ struct Sum {
                         ptx::cp_async_wait<1>();
                 }
                 __syncwarp();
-                if (lane == 0) {
-                    if (MODE == 0 && k > told) ptx::mbar_arrive(&full[(k - 1) % s.stages()]);
-                    if (MODE != 0 || last) ptx::mbar_arrive(&full[at]);
-                }
+                if (MODE == 0) ptx::mbar_arrive_if(&full[before], lane == 0 && k > told);
+                ptx::mbar_arrive_if(&full[at], lane == 0 && (MODE != 0 || last));
                 if (last) told = k + 1;
-                if (k + DEPTH < n) fetch(held[i], k + DEPTH);
+                before = at;
+                at = at + 1 == s.stages() ? 0 : at + 1;
+                free_phase = at ? free_phase : free_phase ^ 1u;
                 if (last) {
                     wait(done, static_cast<uint32_t>(runs) & 1u, ok);
                     __syncwarp();
@@ -321,14 +323,14 @@ struct Sum {
     __device__ __forceinline__ void multiply(uint32_t tmem)
     {
         bool ok = true;
-        int runs = 0;
+        int runs = 0, at = 0;
+        uint32_t phase = 0u;
+        bool begins = true;
         for (int k = 0; k < n; ++k) {
-            const int at = k % s.stages();
-            const bool begins = k == 0 || adapter_at(k - 1) != adapter_at(k);
             if (begins && runs > 0) wait(free_, static_cast<uint32_t>(runs - 1) & 1u, ok);
-            wait(&full[at], static_cast<uint32_t>(k / s.stages()) & 1u, ok);
-            ok = __all_sync(0xffffffffu, ok);  // what follows is the whole warp's
-            if (!ok) break;
+            const bool last = ends_run(k);
+            wait(&full[at], phase, ok);
+            __syncwarp();  // what follows is the whole warp's
             ptx::fence_proxy_async_smem();
             ptx::tc_fence_after();
             const uint32_t a = ptx::smem_addr(mem + at * s.stage()), b = a + s.in_bytes();
@@ -344,7 +346,10 @@ struct Sum {
                 }
             }
             ptx::mma_commit_elect(&empty[at]);
-            if (ends_run(k)) {
+            at = at + 1 == s.stages() ? 0 : at + 1;
+            phase = at ? phase : phase ^ 1u;
+            begins = last;
+            if (last) {
                 ptx::mma_commit_elect(done);
                 ++runs;
             }
@@ -398,12 +403,19 @@ __global__ void __launch_bounds__(U_THREADS, 1) sum_tiles(const __grid_constant_
         }
         if (lane == 31) *count = before;
         before -= parts;
-        for (int i = 0; i < parts; ++i) steps[before + i] = lane * 4 + i;
+        for (int i = 0; i < parts; ++i) steps[before + i] = lane | i << 8;
     }
     ptx::tc_fence_before();
     __syncthreads();
     ptx::tc_fence_after();
-    for (int i = tid; i < n_tiles * TILE; i += U_THREADS) ids[i] = (i & (TILE - 1)) < tiles[i / TILE].rows ? p.plan.order[tiles[i / TILE].first + (i & (TILE - 1))] : -1;
+    const int n = *count;
+    for (int i = tid; i < n * s.tokens; i += U_THREADS) {
+        const int k = i / s.tokens, t = (steps[k] >> 8) * s.tokens + i - k * s.tokens;
+        const Piece piece_of = tiles[steps[k] & 255];
+        ids[i] = t < piece_of.rows ? p.plan.order[piece_of.first + t] : -1;
+    }
+    __syncthreads();
+    if (tid < n) steps[tid] &= 255;
     __syncthreads();
     const uint32_t tmem = *slot;
     const auto run = [&](auto sum) {
@@ -412,7 +424,6 @@ __global__ void __launch_bounds__(U_THREADS, 1) sum_tiles(const __grid_constant_
         else
             sum.multiply(tmem);
     };
-    const int n = *count;
     if (job.mode == 0)
         run(Sum<0>{p, job, s, raw, ids, steps, tiles, full, empty, done, free_, abort_flag, tid, warp, lane, c0, n});
     else if (job.mode == 1)
