@@ -6,9 +6,9 @@
 // to the result, else each piece's part goes to the workspace and a second launch adds the parts in order.
 //
 // The reduction runs over rows, so both operands are MN-major: in^T fills the accumulator's 128 lanes with columns, mid its columns
-// with r, three times: the three bf16 parts of an fp32 mid (adapter_ptx.cuh) stand side by side, N = 3 * rank, and are added up as the accumulator is read.  Core
-// matrices are 8 rows x 16 bytes, each column of them 16 bytes longer than it needs to be, so that 16-byte columns of one row, as they come
-// from memory, fall into different banks.
+// with r, three times: the three bf16 parts of an fp32 mid (adapter_ptx.cuh) stand side by side, N = 3 * rank, and are added up as the accumulator is read.
+// in's rows keep their 128-byte lines (128-byte swizzle: copies that spread a line over shared memory are half as fast); mid's parts lie in core matrices of 8
+// rows x 16 bytes, each column of them 16 bytes longer than it needs to be, so that neighbours fall into different banks.
 //
 // bf16 rows come by cp.async into the operand's place, ring stages ahead; checkpoints, rows that are not whole vectors, and mid come through
 // registers, one or two stages ahead.  A checkpoint's integer becomes a bf16 number by bits: (m | 128) - 128 or 256, each with the scale in its exponent.
@@ -26,13 +26,14 @@ namespace ad {
 constexpr int U_WARPS = 16, U_LOADERS = 32 * U_WARPS, U_THREADS = U_LOADERS + 32;
 constexpr uint64_t U_WAIT_NS = 1000000000ull;
 
-// Shared memory of a stage of `tokens` rows: core matrices of a 16-byte column are `column` bytes, in's columns first, then mid's parts.
+// Shared memory of a stage of `tokens` rows: in by lines of 64 columns, then mid's parts, `column` bytes to a 16-byte column.
 struct SumSmem {
     int rp, tokens, blocks;  // blocks of 128 columns
     __host__ __device__ constexpr SumSmem(int rank) : rp((rank + 15) / 16 * 16), tokens(rp <= 64 ? 64 : 32), blocks(rp <= 80 ? 2 : 1) {}
     __host__ __device__ constexpr int column() const { return tokens * 16 + 16; }
-    __host__ __device__ constexpr int in_bytes() const { return 16 * blocks * column(); }
-    __host__ __device__ constexpr int stage() const { return in_bytes() + 3 * rp / 8 * column(); }
+    __host__ __device__ constexpr int lines() const { return tokens * 128; }  // of 64 columns
+    __host__ __device__ constexpr int in_bytes() const { return 2 * blocks * lines(); }
+    __host__ __device__ constexpr int stage() const { return (in_bytes() + 3 * rp / 8 * column() + 1023) / 1024 * 1024; }
     __host__ __device__ constexpr int stages() const { return 3; }
     // the plan's part: rows' numbers and each stage's tile by stage, the tiles
     __host__ __device__ constexpr int lists() const { return SUM_TILES * (TILE * 4 + 16) + SUM_TILES * 4 * 4 + 16; }
@@ -88,6 +89,8 @@ struct Sum {
             has_in = row < s.tokens && lane < 16 * s.blocks && col < job.cols;
         }
     }
+    // Where in's 16-byte column c (of 8) of token t lies.
+    __device__ __forceinline__ uint32_t in_at(int t, int c) const { return (c >> 3) * s.lines() + t * 128 + (((c ^ t) & 7) << 4); }
     // Whether the thread's part of in's place in a stage exists (it is zero where in has none).
     __device__ __forceinline__ bool stores_in() const
     {
@@ -172,14 +175,13 @@ struct Sum {
                         }
                     }
                 }
-                const uint32_t dst = at + (row + i) * 16 + 2 * (tid & 15) * s.column();
-                ptx::st_shared_v4(dst, o[0], o[1], o[2], o[3]);
-                ptx::st_shared_v4(dst + s.column(), o[4], o[5], o[6], o[7]);
+                ptx::st_shared_v4(at + in_at(row + i, 2 * (tid & 15)), o[0], o[1], o[2], o[3]);
+                ptx::st_shared_v4(at + in_at(row + i, 2 * (tid & 15) + 1), o[4], o[5], o[6], o[7]);
             }
         } else if constexpr (MODE == 1) {
             if (stores_in())
 #pragma unroll
-                for (int i = 0; i < 4; ++i) ptx::st_shared_v4(at + (row + i) * 16 + lane * s.column(), h.x[i].x, h.x[i].y, h.x[i].z, h.x[i].w);
+                for (int i = 0; i < 4; ++i) ptx::st_shared_v4(at + in_at(row + i, lane), h.x[i].x, h.x[i].y, h.x[i].z, h.x[i].w);
         }
         if (has_mid) {
             const float v[8] = {h.mid[0].x, h.mid[0].y, h.mid[0].z, h.mid[0].w, h.mid[1].x, h.mid[1].y, h.mid[1].z, h.mid[1].w};
@@ -208,13 +210,12 @@ struct Sum {
     __device__ __forceinline__ void copy(uint32_t at, int k) const
     {
         const int4 t = row < s.tokens ? *reinterpret_cast<const int4*>(ids + k * s.tokens + row) : make_int4(-1, -1, -1, -1);
-        const uint32_t dst = at + row * 16 + lane * s.column();
         const int rows[4] = {t.x, t.y, t.z, t.w};
         const bool mine = stores_in();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const bool have = has_in && rows[i] >= 0;
-            ptx::cp_async_16_fill_if(dst + 16 * i, have ? job.in + rows[i] * job.in_stride + col : job.in, have ? 16 : 0, mine);
+            ptx::cp_async_16_fill_if(at + in_at(row + i, lane), have ? job.in + rows[i] * job.in_stride + col : job.in, have ? 16 : 0, mine);
         }
     }
 
@@ -336,13 +337,13 @@ struct Sum {
             const uint32_t a = ptx::smem_addr(mem + at * s.stage()), b = a + s.in_bytes();
             const uint64_t bd = ptx::plain_mnmajor_desc(b, 128, s.column());
             for (int m = 0; m < s.blocks; ++m) {
-                const uint64_t ad = ptx::plain_mnmajor_desc(a + 16 * m * s.column(), 128, s.column());
+                const uint64_t ad = ptx::sw128_mnmajor_desc(a + 2 * m * s.lines(), s.lines(), 1024);
                 const uint32_t d = tmem + 3 * m * s.rp;
                 if (s.tokens == 64) {  // rank 64 and below: all three parts in one
-                    ptx::mma_bf16_elect_x4(d, ad, bd, 256 / 16, 256 / 16, ptx::idesc_bf16_f32_mn(128, 3 * s.rp), !begins);
+                    ptx::mma_bf16_elect_x4(d, ad, bd, 2048 / 16, 256 / 16, ptx::idesc_bf16_f32_mn(128, 3 * s.rp), !begins);
                 } else {
-                    ptx::mma_bf16_elect_x2(d, ad, bd, 256 / 16, 256 / 16, ptx::idesc_bf16_f32_mn(128, 2 * s.rp), !begins);
-                    ptx::mma_bf16_elect_x2(d + 2 * s.rp, ad, bd + (s.rp >> 2) * s.column() / 16, 256 / 16, 256 / 16, ptx::idesc_bf16_f32_mn(128, s.rp), !begins);
+                    ptx::mma_bf16_elect_x2(d, ad, bd, 2048 / 16, 256 / 16, ptx::idesc_bf16_f32_mn(128, 2 * s.rp), !begins);
+                    ptx::mma_bf16_elect_x2(d + 2 * s.rp, ad, bd + (s.rp >> 2) * s.column() / 16, 2048 / 16, 256 / 16, ptx::idesc_bf16_f32_mn(128, s.rp), !begins);
                 }
             }
             ptx::mma_commit_elect(&empty[at]);
