@@ -33,7 +33,7 @@ CALLS_NOTE = os.path.join(OBJ_DIR, "calls.txt")  # calls_for(), then "built", "l
 SOURCES = ["conv2d_api.cu", "conv2d_bn64.cu", "conv2d_bn128.cu", "conv2d_bn256.cu", "conv2d_rowwin.cu", "conv2d_direct.cu",
            "conv2d_noalloc.cu", "conv2d_pair_kb1.cu", "conv2d_pair_kb2.cu"]
 SOURCES_NN = ["layer_norm.cu", "ln_fwd_rows.cu", "ln_bwd_rows.cu", "mxfp4.cu", "mxfp4_matmul.cu", "mxint8.cu", "ln_bwd_mxint8.cu",
-              "adapter_plan.cu", "adapter.cu", "adapter_pass_fwd.cu", "adapter_pass_bwd.cu", "adapter_sum.cu"]
+              "adapter_plan.cu", "adapter.cu", "adapter_pass_fwd.cu", "adapter_pass_bwd.cu", "adapter_sum.cu", "adapter_small.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-I", INCLUDE, "-I", CSRC]

@@ -90,6 +90,8 @@ int launch_sums(SumParams& p, int64_t pieces, cudaStream_t stream);
 
 // halved: tiles of 64 rows, not 128.
 int launch_pass_fwd(const PassParams& p, int32_t base_dtype, int32_t out_dtype, bool vec, bool halved, cudaStream_t stream);
+// Up to rank 64.
+int launch_small_fwd(PassParams& p, int32_t base_dtype, int32_t out_dtype, bool vec, cudaStream_t stream);
 int launch_pass_bwd(const PassParams& p, int32_t base_dtype, int32_t out_dtype, bool vec, bool halved, cudaStream_t stream);
 
 }  // namespace ad

@@ -16,7 +16,7 @@ namespace ad {
 
 constexpr int TILE = 128;
 constexpr int SMALL = 8;
-constexpr int64_t SMALL_ROWS = 512;
+constexpr int64_t SMALL_ROWS = 640;
 constexpr int64_t MOST_ROWS = (int64_t(1) << 31) - (1 << 16), MOST_ADAPTERS = 65535;
 
 struct Piece {

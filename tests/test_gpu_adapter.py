@@ -15,7 +15,8 @@ U_BF16 = 2.0 ** -8
 SHAPES = [(1, 1, 1, 1, 1), (1, 4096, 512, 16, 9), (2, 64, 128, 8, 2), (7, 33, 40, 4, 3), (8, 256, 1024, 16, 1), (9, 1000, 96, 20, 5), (16, 72, 56, 33, 40),
           (64, 512, 768, 16, 32), (65, 130, 258, 24, 7), (127, 64, 64, 64, 1), (128, 128, 264, 128, 2), (129, 136, 72, 100, 3), (200, 1001, 2001, 20, 5),
           (257, 320, 192, 8, 300), (300, 96, 1111, 7, 4), (511, 40, 24, 16, 6), (512, 2056, 136, 32, 3), (513, 200, 328, 48, 11), (785, 1001, 777, 8, 3),
-          (1025, 256, 520, 16, 1), (1500, 64, 320, 64, 20), (2049, 136, 64, 128, 2), (640, 24, 16, 3, 5), (900, 2500, 72, 40, 2)]
+          (1025, 256, 520, 16, 1), (1500, 64, 320, 64, 20), (2049, 136, 64, 128, 2), (640, 24, 16, 3, 5), (900, 2500, 72, 40, 2),
+          (641, 520, 136, 24, 3), (1300, 1001, 200, 33, 2), (700, 256, 1000, 8, 40), (160, 72, 200, 64, 3), (161, 72, 200, 64, 3), (3000, 384, 384, 48, 2)]
 
 
 @pytest.fixture(scope="module")
@@ -71,7 +72,7 @@ def _within(got, want, bound, dtype=F32):
 
 
 # ------------------------------------------------------------------------------ plans
-@pytest.mark.parametrize("rows,adapters", [(0, 3), (1, 1), (1, 500), (31, 2), (32, 3), (33, 1000), (511, 5), (513, 5), (4096, 1), (5000, 64), (70001, 300),
+@pytest.mark.parametrize("rows,adapters", [(0, 3), (1, 1), (1, 500), (31, 2), (32, 3), (33, 1000), (511, 5), (640, 5), (641, 5), (4096, 1), (5000, 64), (70001, 300),
                                            (3000, 20000), (1000, 65535), (300001, 7)])
 @pytest.mark.parametrize("order", ["mixed", "runs"])
 def test_plan(sg, rows, adapters, order):
@@ -85,7 +86,7 @@ def test_plan(sg, rows, adapters, order):
     assert np.array_equal(words[adapters + 2:adapters + 2 + rows], np.argsort(e, kind="stable"))
     groups = min(adapters + 1, rows)
     at = (adapters + 2 + rows + 3) // 4 * 4
-    for size, n in ((128, rows // 128 + groups), (8, rows // 8 + groups if rows <= 512 else 0)):
+    for size, n in ((128, rows // 128 + groups), (8, rows // 8 + groups if rows <= 640 else 0)):
         want = [(g, f, min(size, starts[g + 1] - f), 0) for g in range(adapters + 1) for f in range(starts[g], starts[g + 1], size)] if n else []
         table = words[at:at + 4 * n].reshape(n, 4)
         assert len(want) <= n and [tuple(t) for t in table[:len(want)]] == want and not table[len(want):, 2].any()
