@@ -84,17 +84,6 @@ struct Pass {
     __device__ __forceinline__ uint8_t* w2_buf(int i) const { return i ? mem + s.area() - s.ring() - i * s.chunk() : mem + s.area(); }
     __device__ __forceinline__ uint32_t base_ring() const { return ptx::smem_addr(mem) + s.area() - s.ring() + 16 * tid; }
 
-    // 16 bytes of row elements from `src`, `valid` elements of them; aligned copies run by themselves, others go through registers.
-    __device__ __forceinline__ void copy8(uint32_t dst, const __nv_bfloat16* src, int valid) const
-    {
-        if constexpr (VEC) {
-            ptx::cp_async_16s(dst, valid > 0 ? src : p.w1, valid > 0 ? 16 : 0);
-        } else {
-            uint32_t v[4] = {0u, 0u, 0u, 0u};
-            if (valid > 0) mx::load_any<4, 2>(v, src, valid < 8 ? 2 * valid : 16);
-            ptx::st_shared_v4(dst, v[0], v[1], v[2], v[3]);
-        }
-    }
     // This warp's part of what `bar` counts is there (its threads have waited for their copies).  One arrival to a warp: a barrier takes its
     // arrivals one after another, and 512 of them cost as much as the stage.
     __device__ __forceinline__ void arrive(uint64_t* bar) const
@@ -142,20 +131,37 @@ struct Pass {
             }
             return;
         }
-#pragma unroll
-        for (int i = 0; i < ROWS / 64; ++i)
-            if (row + 64 * i < piece.rows) copy8(at + mine + 8192 * i, rows[i], p.from - f0 - 8 * c8);
+        // Through registers, all of them on their way at once: rows that are not whole vectors, and the last columns.
+        constexpr int MOST = ROWS / 64 + MOST_RANK / 64;
+        uint32_t v[MOST][4], to[MOST];
         const __nv_bfloat16* first = p.w1 + e * (static_cast<int64_t>(p.rank) * p.from);
-        if constexpr (!TRANS) {
-            for (int r = row; r < p.rank; r += 64)
-                copy8(w_at + r * 128 + swizzled, first + static_cast<int64_t>(r) * p.from + f0 + 8 * c8, p.from - f0 - 8 * c8);
-        } else {
-            for (int i = tid; i < s.rp * 8; i += P_LOADERS) {  // 64 rows of rp/8 16-byte columns
-                const int k = (i >> 1) & 63, n8 = 2 * (i >> 7) + (i & 1);
-                const int left = f0 + k < p.from ? p.rank - 8 * n8 : 0;
-                copy8(w_at + (k & 7) * 16 + n8 * W1_COLUMN + (k >> 3) * 128, first + static_cast<int64_t>(f0 + k) * p.rank + 8 * n8, left);
+#pragma unroll
+        for (int i = 0; i < MOST; ++i) {
+            const __nv_bfloat16* src;
+            int left;
+            if (i < ROWS / 64) {
+                src = rows[i < ROWS / 64 ? i : 0];
+                left = row + 64 * i < piece.rows ? p.from - f0 - 8 * c8 : 0;
+                to[i] = row + 64 * i < piece.rows ? at + mine + 8192 * i : 0u;
+            } else if constexpr (!TRANS) {
+                const int r = row + 64 * (i - ROWS / 64);
+                src = first + static_cast<int64_t>(r) * p.from + f0 + 8 * c8;
+                left = r < p.rank ? p.from - f0 - 8 * c8 : 0;
+                to[i] = r < p.rank ? w_at + r * 128 + swizzled : 0u;
+            } else {  // 64 rows of rp/8 16-byte columns
+                const int j = tid + P_LOADERS * (i - ROWS / 64), k = (j >> 1) & 63, n8 = 2 * (j >> 7) + (j & 1);
+                src = first + static_cast<int64_t>(f0 + k) * p.rank + 8 * n8;
+                left = j < s.rp * 8 && f0 + k < p.from ? p.rank - 8 * n8 : 0;
+                to[i] = j < s.rp * 8 ? w_at + (k & 7) * 16 + n8 * W1_COLUMN + (k >> 3) * 128 : 0u;
             }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) v[i][k] = 0u;
+            if (left > 0) mx::load_any<4, 2>(v[i], src, left < 8 ? 2 * left : 16);
         }
+#pragma unroll
+        for (int i = 0; i < MOST; ++i)
+            if (to[i]) ptx::st_shared_v4(to[i], v[i][0], v[i][1], v[i][2], v[i][3]);
+        if (VEC) ptx::fence_proxy_async_smem();
     }
 
     // A thread finishes vectors of 8 elements: of 32 columns, one run of 8 or, where base or out has 32 bits, two of 4 at 16 columns' distance, so that
@@ -196,24 +202,38 @@ struct Pass {
                     ptx::cp_async_4_if(to + 8 * 144, src + 64, true);
                 }
             }
-        } else if constexpr (!TRANS) {
-            for (int i = wt; i < s.rp * COLS / 8; i += P_W2_THREADS) {
-                const int per = s.rp >> 3, c = i / per, k8 = i - c * per, n = place_of(c);
-                copy8(at + (n & 7) * 16 + (n >> 3) * 144 + k8 * s.column(), w + static_cast<int64_t>(c0 + c) * p.rank + 8 * k8, c0 + c < p.to ? p.rank - 8 * k8 : 0);
-            }
         } else {
-            for (int i = wt; i < s.rp * COLS / 2; i += P_W2_THREADS) {
-                const int k = i / (COLS / 2), c = 2 * (i % (COLS / 2)), n = place_of(c);
-                const uint32_t dst = at + (k & 7) * 16 + (n & 7) * 2 + (n >> 3) * 144 + (k >> 3) * s.column();
-                const __nv_bfloat16* src = w + static_cast<int64_t>(k) * p.to + c0 + c;
-                const int left = k < p.rank ? p.to - c0 - c : 0;
-                if constexpr (VEC) {
-                    ptx::cp_async_4(dst, left > 0 ? src : p.w1, left > 0 ? 4 : 0);
-                } else {
-                    const uint32_t lo = left > 0 ? __bfloat16_as_ushort(__ldg(src)) : 0u, hi = left > 1 ? __bfloat16_as_ushort(__ldg(src + 1)) : 0u;
-                    asm volatile("st.shared.b32 [%0], %1;" ::"r"(dst), "r"(lo | hi << 16) : "memory");
+            // 8 elements of a row of w2 at a time through registers, BATCH of them on their way at once
+            constexpr int BATCH = 4;
+            const int all = s.rp * COLS / 8, per = TRANS ? COLS / 8 : s.rp >> 3;
+            for (int i0 = wt; i0 < all; i0 += BATCH * P_W2_THREADS) {
+                uint32_t v[BATCH][4];
+#pragma unroll
+                for (int u = 0; u < BATCH; ++u) {
+                    const int i = i0 + u * P_W2_THREADS, line = i / per, at8 = 8 * (i - line * per);  // a column's 8 ranks, or a rank's 8 columns
+                    const int left = i >= all ? 0 : TRANS ? (line < p.rank ? p.to - c0 - at8 : 0) : c0 + line < p.to ? p.rank - at8 : 0;
+                    const __nv_bfloat16* src = TRANS ? w + static_cast<int64_t>(line) * p.to + c0 + at8 : w + static_cast<int64_t>(c0 + line) * p.rank + at8;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) v[u][k] = 0u;
+                    if (left > 0) mx::load_any<4, 2>(v[u], src, left < 8 ? 2 * left : 16);
+                }
+#pragma unroll
+                for (int u = 0; u < BATCH; ++u) {
+                    const int i = i0 + u * P_W2_THREADS, line = i / per, at8 = 8 * (i - line * per);
+                    if (i >= all) break;
+                    if constexpr (TRANS) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const int n = place_of(at8 + 2 * k);
+                            asm volatile("st.shared.b32 [%0], %1;" ::"r"(at + (line & 7) * 16 + (n & 7) * 2 + (n >> 3) * 144 + (line >> 3) * s.column()), "r"(v[u][k]) : "memory");
+                        }
+                    } else {
+                        const int n = place_of(line);
+                        ptx::st_shared_v4(at + (n & 7) * 16 + (n >> 3) * 144 + (at8 >> 3) * s.column(), v[u][0], v[u][1], v[u][2], v[u][3]);
+                    }
                 }
             }
+            if (VEC) ptx::fence_proxy_async_smem();
         }
     }
     // The part of a chunk of w2 that pads an odd number of 8 ranks; whole copies do not reach it.

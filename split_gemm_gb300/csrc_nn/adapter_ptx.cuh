@@ -183,19 +183,8 @@ __device__ __forceinline__ void mbar_arrive_if(uint64_t* bar, bool p)
                  : "memory");
 }
 
-// Four bytes, zero where `src_bytes` is 0 (the address need only be valid for 4 bytes).
-__device__ __forceinline__ void cp_async_4(uint32_t dst, const void* src, uint32_t src_bytes)
-{
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
-}
-
 // The line that holds an address, to L2.
 __device__ __forceinline__ void prefetch_l2(const void* src) { asm volatile("prefetch.global.L2 [%0];" ::"l"(src)); }
-
-__device__ __forceinline__ void cp_async_16s(uint32_t dst, const void* src, uint32_t src_bytes)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
-}
 
 // A multiple of 16 bytes of this CTA's shared memory to another's of the cluster, counted on a barrier there.
 __device__ __forceinline__ void bulk_to_cluster(uint32_t dst_cluster, uint32_t src, uint32_t bytes, uint32_t bar_cluster)
