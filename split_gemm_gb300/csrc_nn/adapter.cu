@@ -21,8 +21,9 @@ constexpr int64_t MOST_COLS = int64_t(1) << 30;
 size_t size_of(int32_t t) { return t == CONV2D_OUT_BF16 ? 2 : 4; }
 
 // How a pass is cut up: tiles of 128 or 64 rows, and the CTAs that share one, one CTA to an SM.  A CTA costs some 3 us beside its rows, 3 more where sums
-// are joined over a cluster, and takes its bytes at 60 a ns at best and at its share of HBM's 6600; weights come from L2.
-bool shape_pass(PassParams& p, int64_t rows, int base_bytes, int out_bytes)
+// are joined over a cluster, and takes its bytes at 60 a ns at best (12 where they are not whole vectors) and at its share of HBM's 6600; weights come
+// from L2.
+bool shape_pass(PassParams& p, int64_t rows, int base_bytes, int out_bytes, bool vec)
 {
     bool halved = false;
     double best = 1e30;
@@ -37,8 +38,8 @@ bool shape_pass(PassParams& p, int64_t rows, int base_bytes, int out_bytes)
             const double on = static_cast<double>(ctas) < held ? static_cast<double>(ctas) : held;
             const double bytes = tile * (2.0 * p.from + static_cast<double>(base_bytes + out_bytes) * p.to) / splits;
             const double weights = 2.0 * p.rank * (static_cast<double>(p.from) + p.to) / splits;
-            const double rate = 6600.0 / on < 60.0 ? 6600.0 / on : 60.0;
-            const double own = (bytes + weights) / 60.0 / 1000.0, hbm = bytes / rate / 1000.0;
+            const double fast = vec ? 60.0 : 12.0, rate = 6600.0 / on < fast ? 6600.0 / on : fast;
+            const double own = (bytes + weights) / fast / 1000.0, hbm = bytes / rate / 1000.0;
             const double us = waves * (3.0 + (splits > 1 ? 3.0 : 0.0) + (own > hbm ? own : hbm));
             if (us < best) {
                 best = us;
@@ -122,8 +123,9 @@ extern "C" int adapter_fwd(const adapter_fwd_params* params, const void* plan_de
     // 128 rows 13.6 us, 256 rows 20 (by tiles, 520 rows, 14.8).
     if (q.rows * mx::cdiv<int64_t>(q.rank, 16) <= ad::SMALL_ROWS && q.rank <= 64)
         return ad::launch_small_fwd(p, q.y_dtype, q.out_dtype, ad::in_vectors(p, q.y_dtype, q.out_dtype), stream);
-    const bool halved = ad::shape_pass(p, q.rows, static_cast<int>(ad::size_of(q.y_dtype)), static_cast<int>(ad::size_of(q.out_dtype)));
-    return ad::launch_pass_fwd(p, q.y_dtype, q.out_dtype, ad::in_vectors(p, q.y_dtype, q.out_dtype), halved, stream);
+    const bool vec = ad::in_vectors(p, q.y_dtype, q.out_dtype);
+    const bool halved = ad::shape_pass(p, q.rows, static_cast<int>(ad::size_of(q.y_dtype)), static_cast<int>(ad::size_of(q.out_dtype)), vec);
+    return ad::launch_pass_fwd(p, q.y_dtype, q.out_dtype, vec, halved, stream);
 }
 
 extern "C" size_t adapter_bwd_workspace_bytes(const adapter_bwd_params* params)
@@ -181,14 +183,17 @@ extern "C" int adapter_bwd(const adapter_bwd_params* params, const void* plan_de
     p.from = static_cast<int>(q.outs);
     p.to = static_cast<int>(q.cols);
     if (!ad::status_word(&p.status)) return CONV2D_ERR_CUDA;
-    const bool halved = ad::shape_pass(p, q.rows, dx0_dev ? static_cast<int>(ad::size_of(q.dx0_dtype)) : 0, dx_dev ? static_cast<int>(ad::size_of(q.dx_dtype)) : 0);
+    const bool vec = ad::in_vectors(p, q.dx0_dtype, q.dx_dtype);
+    const bool halved = ad::shape_pass(p, q.rows, dx0_dev ? static_cast<int>(ad::size_of(q.dx0_dtype)) : 0, dx_dev ? static_cast<int>(ad::size_of(q.dx_dtype)) : 0, vec);
+    p.early = da_dev || db_dev;
     if (dx_dev || da_dev)
-        if (int rc = ad::launch_pass_bwd(p, q.dx0_dtype, q.dx_dtype, ad::in_vectors(p, q.dx0_dtype, q.dx_dtype), halved, stream)) return rc;
+        if (int rc = ad::launch_pass_bwd(p, q.dx0_dtype, q.dx_dtype, vec, halved, stream)) return rc;
     ad::SumParams s{};
     s.plan = p.plan;
     s.status = p.status;
     s.adapters = p.adapters;
     s.rank = p.rank;
+    s.beside = dx_dev || da_dev;
     s.tiles_each = ad::sum_tiles_each(q.rows, q.adapters, p.rank, q.cols, q.outs);
     const int64_t pieces = ad::sum_pieces(ad::PlanLayout(q.rows, q.adapters), s.tiles_each);
     float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace_dev) + ad::dh_bytes(q.rows, q.rank));

@@ -22,6 +22,7 @@ struct PassParams {
     int adapters, rank, from, to;
     int relu;
     int splits;  // CTAs of a cluster
+    int early;   // the next kernel may start: it waits itself for what it needs of this one
 };
 
 constexpr int P_BLOCK = 64, P_STEP = 2 * P_BLOCK;  // of `from`: in a block of operands, and in a stage
@@ -53,11 +54,10 @@ struct PassSmem {
     __host__ __device__ constexpr int sums() const { return TILE * pitch() * 4; }  // and mid's bytes
     __host__ __device__ constexpr int ring() const { return P_DEPTH * P_LOADERS * 64; }
     __host__ __device__ constexpr int chunks() const { return 1 + (area() - ring()) / chunk() < P_MOST_CHUNKS ? 1 + (area() - ring()) / chunk() : P_MOST_CHUNKS; }
-    __host__ __device__ constexpr int early_chunks() const  // that lie neither over the sums nor over mid
-    {
-        const int top = area() - ring() < area() - sums() ? area() - ring() : area() - sums(), n = 1 + (top > sums() ? (top - sums()) / chunk() : 0);
-        return n < chunks() ? n : chunks();
-    }
+    // Those that lie neither over the sums nor over mid, if there are two; else all, to be filled when mid is in tensor memory.
+    __host__ __device__ constexpr int apart() const { return 1 + (area() - ring() > sums() ? (area() - ring() - sums()) / chunk() : 0); }
+    __host__ __device__ constexpr bool late() const { return apart() < 2; }
+    __host__ __device__ constexpr int buffers() const { return late() || apart() > chunks() ? chunks() : apart(); }
 };
 static_assert(PassSmem(128).area() >= 2 * PassSmem(128).sums() && PassSmem(128).chunks() >= 2 && PassSmem(128).stages() >= 2 && PassSmem(128).ring() >= PassSmem(128).sums(),
               "the widest rank fits");
@@ -79,7 +79,9 @@ struct SumParams {
     Plan plan;
     SumJob jobs[2];  // without a result: not wanted
     uint32_t* status;
-    int adapters, rank, tiles_each, per_piece;
+    int adapters, rank, tiles_each;
+    int first_late;  // the first CTA of jobs[0], whose mid comes from the pass before
+    int beside;      // that pass lets this kernel start early
 };
 
 constexpr int SUM_TILES = 32;  // of a piece, at most

@@ -54,7 +54,7 @@ struct Pass {
     __device__ __forceinline__ Pass(const PassParams& p, uint8_t* raw) : p(p), s(p.rank), mem(raw)
     {
         n_stages = s.stages();
-        n_bufs = s.chunks();
+        n_bufs = s.buffers();
         full = reinterpret_cast<uint64_t*>(raw + s.area() + s.chunk());
         empty = full + P_MOST_STAGES;
         done = empty + P_MOST_STAGES;
@@ -164,12 +164,13 @@ struct Pass {
         if (VEC) ptx::fence_proxy_async_smem();
     }
 
-    // A thread finishes vectors of 8 elements: of 32 columns, one run of 8 or, where base or out has 32 bits, two of 4 at 16 columns' distance, so that
-    // four threads' runs are whole sectors.  It gets columns 8j + 2(lane%4) + {0, 1} of the accumulator, j = 0 .. 3; w2's column c becomes row
-    // place_of(c) of the operand for that.
-    static constexpr int RUN = sizeof(TB) == 2 && sizeof(TO) == 2 ? 8 : 4, RUNS = 8 / RUN;
+    // A thread finishes vectors of 8 elements, of 32 columns: one run of 8 or, where base or out has 32 bits, two of 4 at 16 columns' distance, so that
+    // four threads' runs are whole sectors; of rows that are not whole vectors four of 2, as four threads' single elements then lie in one sector.
+    // It gets columns 8j + 2(lane%4) + {0, 1} of the accumulator, j = 0 .. 3; w2's column c becomes row place_of(c) of the operand for that.
+    static constexpr int RUN = !VEC ? 2 : sizeof(TB) == 2 && sizeof(TO) == 2 ? 8 : 4, RUNS = 8 / RUN, APART = 4 * RUN;
     __device__ __forceinline__ static int place_of(int c)
     {
+        if constexpr (RUN == 2) return c;
         return (c & ~31) + (c & 1) + (RUN == 8 ? 8 * ((c >> 1) & 3) + 2 * ((c >> 3) & 3) : 8 * (2 * ((c >> 4) & 1) + ((c >> 1) & 1)) + 2 * ((c >> 2) & 3));
     }
     // w2's columns of a chunk from c0 on, by the warps that bring it.
@@ -245,26 +246,14 @@ struct Pass {
             ptx::st_shared_v4(ptx::smem_addr(buf) + (i & 7) * 16 + (i >> 3) * 144 + (p.rank >> 3) * s.column(), 0u, 0u, 0u, 0u);
         ptx::fence_proxy_async_smem();
     }
-    // w2's chunks i0 .. i1 of the CTA's n from c0 on, one after another as buffers come free; the word of each a chunk later.
-    __device__ __forceinline__ void bring_w2(int i0, int i1, int c0, bool& ok) const
+    // w2's chunk j (columns from c0 on), when its buffer is free.
+    __device__ __forceinline__ void bring_w2(int j, int c0, bool& ok) const
     {
-        for (int j = i0; j < i1; ++j) {
-            const int buf = j % n_bufs;
-            wait(&w2_empty[buf], (static_cast<uint32_t>(j / n_bufs) & 1u) ^ 1u, ok);
-            if (j < n_bufs) clear_pad(w2_buf(buf));
-            load_w2(w2_buf(buf), c0 + j * COLS);
-            if (VEC) {
-                ptx::cp_async_commit();
-                ptx::cp_async_wait<1>();
-                if (j > i0) arrive(&w2_full[(j - 1) % n_bufs]);
-            } else {
-                arrive(&w2_full[buf]);
-            }
-        }
-        if (VEC && i1 > i0) {
-            ptx::cp_async_wait_all();
-            arrive(&w2_full[(i1 - 1) % n_bufs]);
-        }
+        const int buf = j % n_bufs;
+        wait(&w2_empty[buf], (static_cast<uint32_t>(j / n_bufs) & 1u) ^ 1u, ok);
+        if (j < n_bufs) clear_pad(w2_buf(buf));
+        load_w2(w2_buf(buf), c0);
+        ptx::cp_async_commit();
     }
 
     // This CTA's rows of the sums over the cluster: scaled, to mid, and on to every CTA.
@@ -388,12 +377,12 @@ struct Pass {
                 const bool here = wanted && (upper ? base_here[(k + HOLD) % MINE] : base_here[k % MINE]);
 #pragma unroll
                 for (int r = 0; r < RUNS; ++r) {
-                    const bool in = here && (whole || col_of(0, c0) + 32 * side + 16 * r < p.to);
+                    const bool in = here && (whole || col_of(0, c0) + 32 * side + APART * r < p.to);
                     const uint32_t dst = at + (k * RUNS + r) * (P_LOADERS * PIECE);
                     if constexpr (PIECE == 16)
-                        ptx::cp_async_16_if(dst, src + 16 * r, in);
+                        ptx::cp_async_16_if(dst, src + APART * r, in);
                     else
-                        ptx::cp_async_8_if(dst, src + 16 * r, in);
+                        ptx::cp_async_8_if(dst, src + APART * r, in);
                 }
             }
         }
@@ -427,8 +416,8 @@ struct Pass {
             TB* v = reinterpret_cast<TB*>(b.u[k]);
 #pragma unroll
             for (int r = 0; r < RUNS; ++r) {
-                const TB* src = base_at[row_index(i)] + c0 + 32 * side_of(i) + 16 * r;
-                const int left = base_here[row_index(i)] ? p.to - col_of(i, c0) - 16 * r : 0;
+                const TB* src = base_at[row_index(i)] + c0 + 32 * side_of(i) + APART * r;
+                const int left = base_here[row_index(i)] ? p.to - col_of(i, c0) - APART * r : 0;
 #pragma unroll
                 for (int j = 0; j < RUN; ++j) v[r * RUN + j] = j < left ? src[j] : TB(0.f);
             }
@@ -460,9 +449,9 @@ struct Pass {
             const int i = turn * HOLD + k;
 #pragma unroll
             for (int r = 0; r < RUNS; ++r) {
-                TO* row = out_at[row_index(i)] + c0 + 32 * side_of(i) + 16 * r;
+                TO* row = out_at[row_index(i)] + c0 + 32 * side_of(i) + APART * r;
                 const float2* from = f[k] + r * (RUN / 2);
-                const int col = col_of(i, c0) + 16 * r;
+                const int col = col_of(i, c0) + APART * r;
                 const bool here = live && row_here[row_index(i)];
                 if constexpr (!VEC) {
 #pragma unroll
@@ -546,6 +535,7 @@ struct Pass {
         ptx::tc_fence_after();
         const uint32_t tmem = *slot;
         ptx::grid_dependency_wait();
+        if (p.early) ptx::grid_launch_dependents();
         const int block = blockIdx.x / p.splits;
         piece = p.plan.tiles[block >> HALVED];  // the same for the whole cluster
         if constexpr (HALVED) {
@@ -641,11 +631,16 @@ struct Pass {
             }
             ptx::mma_commit_elect(done);
         } else if (n > 0) {
-            bring_w2(0, 1, chunk0 * COLS, ok);
+            bring_w2(0, chunk0 * COLS, ok);
         }
         __syncwarp();
         wait(done, 0, ok);
         __syncwarp();
+        if (warp > P_WARPS && n > 0) {
+            ptx::cp_async_wait_all();
+            arrive(&w2_full[0]);
+            if (n > 1 && !s.late()) bring_w2(1, (chunk0 + 1) * COLS, ok);
+        }
         // The ring is free: the sums.
         float* sums = reinterpret_cast<float*>(mem);
         if (warp < P_WARPS) {
@@ -673,8 +668,6 @@ struct Pass {
             case 4: join<4>(sums, scale); break;
             default: join<8>(sums, scale); break;
         }
-        const int early = s.early_chunks() >= 2 && n >= 2 ? 2 : 1;  // chunks of w2 that are brought before all meet again: one to a group
-        if (warp > P_WARPS) bring_w2(1, early, chunk0 * COLS, ok);
         // All of mid is here: none of this CTA's peers reads its sums any more, and what they sent has come.
         if (p.splits > 1) {
             wait(mid_full, 0, ok);
@@ -686,7 +679,10 @@ struct Pass {
             store_parts(parts);
             ptx::tc_fence_before();
         }
-        __syncthreads();
+        if (s.late())
+            __syncthreads();
+        else if (warp <= P_WARPS)
+            ptx::named_bar_sync(1, P_LOADERS + 32);  // the warps that bring w2 are not waited for
         if (warp == P_WARPS) {
             ptx::tc_fence_after();
             int buf = 0;
@@ -710,7 +706,15 @@ struct Pass {
                 phase = buf ? phase : phase ^ 1u;
             }
         } else if (warp > P_WARPS) {
-            bring_w2(early, n, chunk0 * COLS, ok);
+            // the word of each a chunk later
+            if (n > 1 && s.late()) bring_w2(1, (chunk0 + 1) * COLS, ok);
+            for (int j = 2; j < n; ++j) {
+                bring_w2(j, (chunk0 + j) * COLS, ok);
+                ptx::cp_async_wait<1>();
+                arrive(&w2_full[(j - 1) % n_bufs]);
+            }
+            ptx::cp_async_wait_all();
+            if (n > 1) arrive(&w2_full[(n - 1) % n_bufs]);
         } else if (group < n) {
             // This group's chunks, every other one; base P_DEPTH turns ahead.
             const auto ask = [&](int slot, int j, int t) {  // turn t from chunk j's beginning on

@@ -50,7 +50,7 @@ struct Sum {
     const Piece* tiles;
     uint64_t *full, *empty, *done, *free_;
     volatile uint32_t* abort_flag;
-    int tid, warp, lane, c0, n;
+    int tid, warp, lane, c0, n, piece;
 
     // As in the pass: once a wait has run out, the thread waits no more.
     __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, bool& ok) const
@@ -222,7 +222,7 @@ struct Sum {
     // The finished accumulator of a run that ends with stage k: to the result, or to the piece's part of it.
     __device__ __forceinline__ void flush(uint32_t tmem, int k, int first, bool ok) const
     {
-        const int e = adapter_at(k), piece = blockIdx.x / p.per_piece;
+        const int e = adapter_at(k);
         const int t0 = piece * p.tiles_each + steps[first], t1 = piece * p.tiles_each + steps[k] + 1;
         const bool before = p.plan.tile_starts[e] < t0, after = p.plan.tile_starts[e + 1] > t1;
         const int64_t size = static_cast<int64_t>(p.rank) * job.cols;
@@ -372,9 +372,11 @@ __global__ void __launch_bounds__(U_THREADS, 1) sum_tiles(const __grid_constant_
     volatile uint32_t* abort_flag = slot + 1;
     volatile int* count = reinterpret_cast<volatile int*>(slot + 2);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
-    const int piece = blockIdx.x / p.per_piece, block = blockIdx.x % p.per_piece;
-    const SumJob& job = p.jobs[block >= p.jobs[0].col_blocks];
-    const int c0 = (block - (block >= p.jobs[0].col_blocks ? p.jobs[0].col_blocks : 0)) * 128 * s.blocks;
+    // db's CTAs first: they need nothing of the pass before them, and run beside it where it leaves SMs free.
+    const bool late = static_cast<int>(blockIdx.x) >= p.first_late;
+    const SumJob& job = p.jobs[late ? 0 : 1];
+    const int number = static_cast<int>(blockIdx.x) - (late ? p.first_late : 0), piece = number / job.col_blocks;
+    const int c0 = (number - piece * job.col_blocks) * 128 * s.blocks;
     if (tid == 0) {
         for (int i = 0; i < s.stages(); ++i) {
             ptx::mbar_init(&full[i], U_WARPS);
@@ -385,11 +387,16 @@ __global__ void __launch_bounds__(U_THREADS, 1) sum_tiles(const __grid_constant_
         *abort_flag = 0u;
         ptx::mbar_init_fence();
     }
-    ptx::grid_dependency_wait();
+    // The pass has waited for what came before it and lets this kernel start only then.
+    if (late || !p.beside) ptx::grid_dependency_wait();
     // The piece's tiles, rows and stages; tiles without an adapter, which come last, are left out.
     const int first = piece * p.tiles_each, left = p.plan.tile_starts[p.adapters] - first;
     const int n_tiles = left < p.tiles_each ? left : p.tiles_each;
-    if (n_tiles <= 0) return;
+    // This kernel ends after the pass, so that whatever waits for it has waited for both.
+    if (n_tiles <= 0) {
+        if (!late && p.beside) ptx::grid_dependency_wait();
+        return;
+    }
     if (warp == U_WARPS) {
         ptx::tmem_alloc(slot, 512);
         ptx::tmem_relinquish();
@@ -426,17 +433,18 @@ __global__ void __launch_bounds__(U_THREADS, 1) sum_tiles(const __grid_constant_
             sum.multiply(tmem);
     };
     if (job.mode == 0)
-        run(Sum<0>{p, job, s, raw, ids, steps, tiles, full, empty, done, free_, abort_flag, tid, warp, lane, c0, n});
+        run(Sum<0>{p, job, s, raw, ids, steps, tiles, full, empty, done, free_, abort_flag, tid, warp, lane, c0, n, piece});
     else if (job.mode == 1)
-        run(Sum<1>{p, job, s, raw, ids, steps, tiles, full, empty, done, free_, abort_flag, tid, warp, lane, c0, n});
+        run(Sum<1>{p, job, s, raw, ids, steps, tiles, full, empty, done, free_, abort_flag, tid, warp, lane, c0, n, piece});
     else
-        run(Sum<2>{p, job, s, raw, ids, steps, tiles, full, empty, done, free_, abort_flag, tid, warp, lane, c0, n});
+        run(Sum<2>{p, job, s, raw, ids, steps, tiles, full, empty, done, free_, abort_flag, tid, warp, lane, c0, n, piece});
     ptx::tc_fence_before();
     __syncthreads();
     if (warp == U_WARPS) {
         ptx::tc_fence_after();
         ptx::tmem_dealloc(tmem, 512);
     }
+    if (!late && p.beside) ptx::grid_dependency_wait();
 }
 
 constexpr int J_THREADS = 256;
@@ -503,21 +511,21 @@ int launch_sums(SumParams& p, int64_t pieces, cudaStream_t stream)
 {
     static std::atomic<uint64_t> done{0};
     const SumSmem s(p.rank);
-    p.per_piece = 0;
-    int64_t most = 0;
+    int64_t most = 0, ctas = 0;
     for (SumJob& job : p.jobs) {
         job.col_blocks = job.out ? mx::cdiv(job.cols, 128 * s.blocks) : 0;
-        p.per_piece += job.col_blocks;
+        ctas += pieces * job.col_blocks;
         const int64_t size = static_cast<int64_t>(p.rank) * job.cols;
         job.mid_vec = p.rank % 4 == 0 && reinterpret_cast<uintptr_t>(job.mid) % 16 == 0;
         job.out_vec = p.rank % 4 == 0 && reinterpret_cast<uintptr_t>(job.out) % 16 == 0;
         job.join_vec = size % 4 == 0 && (reinterpret_cast<uintptr_t>(job.out) | reinterpret_cast<uintptr_t>(job.part)) % 16 == 0;
         if (job.out && size > most) most = size;
     }
-    if (p.per_piece == 0) return CONV2D_OK;
-    if (pieces * p.per_piece > INT32_MAX) return CONV2D_ERR_UNSUPPORTED;
+    if (ctas == 0) return CONV2D_OK;
+    if (ctas > INT32_MAX) return CONV2D_ERR_UNSUPPORTED;
+    p.first_late = static_cast<int>(pieces * p.jobs[1].col_blocks);
     if (!mx::allow_smem(sum_tiles, 227 * 1024, done)) return CONV2D_ERR_CUDA;
-    if (mx::launch(sum_tiles, pieces * p.per_piece, U_THREADS, s.bytes(), stream, 1, p) != cudaSuccess) return CONV2D_ERR_CUDA;
+    if (mx::launch(sum_tiles, ctas, U_THREADS, s.bytes(), stream, 1, p) != cudaSuccess) return CONV2D_ERR_CUDA;
     const int64_t across = mx::cdiv<int64_t>(most, 4 * J_THREADS);
     const dim3 grid(static_cast<unsigned>(across < 4 * mx::SMS ? across : 4 * mx::SMS), static_cast<unsigned>(p.adapters < 8 ? p.adapters : 8));
     return mx::launch(join_sums, grid, J_THREADS, 0, stream, 1, p) == cudaSuccess ? CONV2D_OK : CONV2D_ERR_CUDA;

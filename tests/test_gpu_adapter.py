@@ -250,7 +250,7 @@ def test_gradients_one_by_one_and_into(sg):
     out, h = sg.adapter_fwd(d["y"], d["x"], d["a"], d["b"], plan, d["scale"])
     dx, da, db = sg.adapter_bwd(d["dy"], d["x"], h, d["a"], d["b"], plan, d["scale"], dx=d["dx0"])
     ws = torch.empty(sg.adapter_bwd_workspace_bytes(d["dy"], d["x"], d["a"], d["b"], plan), dtype=torch.uint8, device="cuda").fill_(255)
-    for keep in ((1, 0, 0), (0, 1, 0), (0, 0, 1), (1, 1, 0), (0, 1, 1)):
+    for keep in ((1, 0, 0), (0, 1, 0), (0, 0, 1), (1, 1, 0), (0, 1, 1), (1, 0, 1)):
         made = [torch.full_like(t, 9.0) if k else None for t, k in zip((dx, da, db), keep)]
         sg.adapter_bwd_into(*made, d["dy"], d["x"], h if keep[2] else None, d["a"], d["b"], plan, d["scale"], dx0=d["dx0"], workspace=ws)
         for m, t in zip(made, (dx, da, db)):
