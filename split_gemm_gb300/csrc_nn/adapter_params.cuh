@@ -43,6 +43,9 @@ constexpr int P_WARPS = 16, P_LOADERS = 32 * P_WARPS, P_DEPTH = 3;
 struct PassSmem {
     int rp;
     __host__ __device__ constexpr explicit PassSmem(int rank) : rp((rank + 15) / 16 * 16) {}
+    // Accumulators of the first product, taken in turn: matrix units cut their sums off at fp32's last bit, towards zero, and a chain of 256 such
+    // sums is off by 2e-6; joined by rounding additions, chains of 32 are off by a third of that (fp32 throughout 7e-7).
+    __host__ __device__ constexpr int accumulators() const { return 512 / rp < 8 ? 512 / rp : 8; }
     __host__ __device__ constexpr int block() const { return TILE * P_BLOCK * 2 + (rp / 8 * W1_COLUMN + 1023) / 1024 * 1024; }
     __host__ __device__ constexpr int stage() const { return 2 * block(); }
     __host__ __device__ constexpr int column() const { return P_COLS / 8 * 144 + 16; }  // of a chunk: 8 ranks

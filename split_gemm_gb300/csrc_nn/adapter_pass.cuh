@@ -611,8 +611,8 @@ struct Pass {
             }
             prefetch_base(chunk0, chunk1);
         } else if (warp == P_WARPS) {
-            int at = 0;
-            uint32_t phase = 0u;
+            int at = 0, acc = 0;
+            uint32_t phase = 0u, again = 0u;
             for (int it = 0; it < s1 - s0; ++it) {
                 wait(&full[at], phase, ok);
                 __syncwarp();  // what follows is the whole warp's
@@ -622,8 +622,10 @@ struct Pass {
                 for (int h = 0; h < 2; ++h) {
                     if ((s0 + it) * P_STEP + h * P_BLOCK >= p.from) break;
                     const uint32_t a = ptx::smem_addr(mem) + at * s.stage() + h * s.block(), b = a + TILE * P_BLOCK * 2;
-                    ptx::mma_bf16_elect_x4(tmem, ptx::sw128_kmajor_desc(a), TRANS ? ptx::plain_mnmajor_desc(b, 128, W1_COLUMN) : ptx::sw128_kmajor_desc(b),
-                                           32 / 16, (TRANS ? 256 : 32) / 16, TRANS ? ptx::idesc_bf16_f32_bmn(TILE, s.rp) : ptx::idesc_bf16_f32(TILE, s.rp), it > 0 || h > 0);
+                    ptx::mma_bf16_elect_x4(tmem + acc * s.rp, ptx::sw128_kmajor_desc(a), TRANS ? ptx::plain_mnmajor_desc(b, 128, W1_COLUMN) : ptx::sw128_kmajor_desc(b),
+                                           32 / 16, (TRANS ? 256 : 32) / 16, TRANS ? ptx::idesc_bf16_f32_bmn(TILE, s.rp) : ptx::idesc_bf16_f32(TILE, s.rp), again);
+                    acc = acc + 1 == s.accumulators() ? 0 : acc + 1;
+                    again = acc ? again : 1u;
                 }
                 ptx::mma_commit_elect(&empty[at]);
                 at = at + 1 == n_stages ? 0 : at + 1;
@@ -646,14 +648,27 @@ struct Pass {
         if (warp < P_WARPS) {
             ptx::tc_fence_after();
             const int row = LANES * (warp & 3) + lane;
+            const int blocks = ((s1 * P_STEP < p.from ? s1 * P_STEP : p.from) - s0 * P_STEP + P_BLOCK - 1) / P_BLOCK;
+            const int accs = blocks < s.accumulators() ? blocks : s.accumulators();
             for (int c = 16 * (warp >> 2); c < s.rp; c += 64) {
-                uint32_t v[16];
-                ptx::tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + c, v);
-                ptx::tmem_ld_wait();
+                const uint32_t from = tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + c;
+                float f[16] = {};
+                for (int i = 0; i < accs; i += 2) {
+                    uint32_t v[2][16];
+                    ptx::tmem_ld_32x32b_x16(from + i * s.rp, v[0]);
+                    ptx::tmem_ld_32x32b_x16(from + (i + 1 < accs ? i + 1 : i) * s.rp, v[1]);
+                    ptx::tmem_ld_wait();
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) f[k] += __uint_as_float(v[0][k]);
+                    if (i + 1 < accs)
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) f[k] += __uint_as_float(v[1][k]);
+                }
                 const uint32_t at = ptx::smem_addr(sums + row * s.pitch() + c);
                 if (lane < LANES)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) ptx::st_shared_v4(at + 16 * i, v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                    for (int i = 0; i < 16; i += 4)
+                        ptx::st_shared_v4(at + 4 * i, __float_as_uint(f[i]), __float_as_uint(f[i + 1]), __float_as_uint(f[i + 2]), __float_as_uint(f[i + 3]));
                 __syncwarp();
             }
             ptx::tc_fence_before();
