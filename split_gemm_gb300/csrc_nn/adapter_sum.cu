@@ -2,11 +2,14 @@
 // db (mid = h, in = dy) in one launch.
 //
 // HBM binds: `in` is read once, and with rank r there are 2r flops to its 1 or 2 bytes.  A CTA takes 256 columns of `in` (128 above
-// rank 80, by tensor memory) and a piece of up to 32 of the plan's tiles, whatever adapters those belong to; an adapter's sum that lies in one piece goes straight
+// rank 64, by tensor memory) and a piece of up to 32 of the plan's tiles, whatever adapters those belong to; an adapter's sum that lies in one piece goes straight
 // to the result, else each piece's part goes to the workspace and a second launch adds the parts in order.
 //
 // The reduction runs over rows, so both operands are MN-major: in^T fills the accumulator's 128 lanes with columns, mid its columns
 // with r, three times: the three bf16 parts of an fp32 mid (adapter_ptx.cuh) stand side by side, N = 3 * rank, and are added up as the accumulator is read.
+// Matrix units cut their sums off at fp32's last bit, towards zero, so that a chain of them is off by half its length of such bits: the first parts, whose bits
+// count, have two accumulators, taken by every other stage, with the small parts' between them: first | second | third | first.  An even stage's parts lie in
+// this order in shared memory, an odd one's as second | third | first, and go to the accumulators one further on.
 // in's rows keep their 128-byte lines (128-byte swizzle: copies that spread a line over shared memory are half as fast); mid's parts lie in core matrices of 8
 // rows x 16 bytes, each column of them 16 bytes longer than it needs to be, so that neighbours fall into different banks.
 //
@@ -29,7 +32,7 @@ constexpr uint64_t U_WAIT_NS = 1000000000ull;
 // Shared memory of a stage of `tokens` rows: in by lines of 64 columns, then mid's parts, `column` bytes to a 16-byte column.
 struct SumSmem {
     int rp, tokens, blocks;  // blocks of 128 columns
-    __host__ __device__ constexpr SumSmem(int rank) : rp((rank + 15) / 16 * 16), tokens(rp <= 64 ? 64 : 32), blocks(rp <= 80 ? 2 : 1) {}
+    __host__ __device__ constexpr SumSmem(int rank) : rp((rank + 15) / 16 * 16), tokens(rp <= 64 ? 64 : 32), blocks(rp <= 64 ? 2 : 1) {}
     __host__ __device__ constexpr int column() const { return tokens * 16 + 16; }
     __host__ __device__ constexpr int lines() const { return tokens * 128; }  // of 64 columns
     __host__ __device__ constexpr int in_bytes() const { return 2 * blocks * lines(); }
@@ -146,7 +149,7 @@ struct Sum {
         return make_uint2(o[0], o[1]);
     }
 
-    __device__ __forceinline__ void store(const Held& h, uint32_t at) const
+    __device__ __forceinline__ void store(const Held& h, uint32_t at, int turn) const
     {
         if constexpr (MODE == 2) {
             if (stores_in())
@@ -200,9 +203,10 @@ struct Sum {
 #pragma unroll
                 for (int q = 0; q < 3; ++q) o[q][i] = __byte_perm(b[0][q], b[1][q], 0x7632);
             }
-            const uint32_t dst = at + s.in_bytes() + mid_token * 16 + mid_rank * s.column();
+            const uint32_t part = (s.rp >> 3) * s.column(), dst = at + s.in_bytes() + mid_token * 16 + mid_rank * s.column();
+            const uint32_t to[3] = {turn ? dst + 2 * part : dst, turn ? dst : dst + part, turn ? dst + part : dst + 2 * part};
 #pragma unroll
-            for (int q = 0; q < 3; ++q) ptx::st_shared_v4(dst + q * (s.rp >> 3) * s.column(), o[q][0], o[q][1], o[q][2], o[q][3]);
+            for (int q = 0; q < 3; ++q) ptx::st_shared_v4(to[q], o[q][0], o[q][1], o[q][2], o[q][3]);
         }
     }
 
@@ -233,12 +237,14 @@ struct Sum {
             const int c = c0 + 128 * m + 32 * (warp & 3) + lane;
             float f[16];
 #pragma unroll
-            for (int q = 2; q >= 0; --q) {  // the smallest parts first
+            for (int i = 0; i < 4; ++i) {  // the smallest parts first
+                const int q = i < 2 ? 2 - i : 3 * (i - 2);
+                if (q == 3 && k == first) continue;
                 uint32_t v[16];
-                ptx::tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + (3 * m + q) * s.rp + r0, v);
+                ptx::tmem_ld_32x32b_x16(tmem + (static_cast<uint32_t>(32 * (warp & 3)) << 16) + (4 * m + q) * s.rp + r0, v);
                 ptx::tmem_ld_wait();
 #pragma unroll
-                for (int i = 0; i < 16; ++i) f[i] = q == 2 ? __uint_as_float(v[i]) : __uint_as_float(v[i]) + f[i];
+                for (int j = 0; j < 16; ++j) f[j] = i == 0 ? __uint_as_float(v[j]) : __uint_as_float(v[j]) + f[j];
             }
             if (!ok || c >= job.cols) {
                 __syncwarp();
@@ -288,7 +294,7 @@ struct Sum {
                     copy(st, k);
                     ptx::cp_async_commit();
                 }
-                store(held[i], st);
+                store(held[i], st, (k - first) & 1);
                 if (k + DEPTH < n) fetch(held[i], k + DEPTH);
                 ptx::fence_proxy_async_smem();
                 // One arrival to a warp (a barrier takes its arrivals one after another); copies' stages are told of a stage later.
@@ -326,9 +332,9 @@ struct Sum {
         bool ok = true;
         int runs = 0, at = 0;
         uint32_t phase = 0u;
-        bool begins = true;
+        int turn = 0;  // of the run's stages
         for (int k = 0; k < n; ++k) {
-            if (begins && runs > 0) wait(free_, static_cast<uint32_t>(runs - 1) & 1u, ok);
+            if (turn == 0 && runs > 0) wait(free_, static_cast<uint32_t>(runs - 1) & 1u, ok);
             const bool last = ends_run(k);
             wait(&full[at], phase, ok);
             __syncwarp();  // what follows is the whole warp's
@@ -338,18 +344,22 @@ struct Sum {
             const uint64_t bd = ptx::plain_mnmajor_desc(b, 128, s.column());
             for (int m = 0; m < s.blocks; ++m) {
                 const uint64_t ad = ptx::sw128_mnmajor_desc(a + 2 * m * s.lines(), s.lines(), 1024);
-                const uint32_t d = tmem + 3 * m * s.rp;
-                if (s.tokens == 64) {  // rank 64 and below: all three parts in one
-                    ptx::mma_bf16_elect_x4(d, ad, bd, 2048 / 16, 256 / 16, ptx::idesc_bf16_f32_mn(128, 3 * s.rp), !begins);
+                const uint32_t d = tmem + (4 * m + (turn & 1)) * s.rp;
+                const uint64_t bd2 = bd + (s.rp >> 2) * s.column() / 16;
+                if (s.tokens == 32) {  // ranks above 64
+                    ptx::mma_bf16_elect_x2(d, ad, bd, 2048 / 16, 256 / 16, ptx::idesc_bf16_f32_mn(128, 2 * s.rp), turn > 0);
+                    ptx::mma_bf16_elect_x2(d + 2 * s.rp, ad, bd2, 2048 / 16, 256 / 16, ptx::idesc_bf16_f32_mn(128, s.rp), turn > 1);
+                } else if (turn == 1) {  // the second accumulator begins
+                    ptx::mma_bf16_elect_x4(d, ad, bd, 2048 / 16, 256 / 16, ptx::idesc_bf16_f32_mn(128, 2 * s.rp), 1u);
+                    ptx::mma_bf16_elect_x4(d + 2 * s.rp, ad, bd2, 2048 / 16, 256 / 16, ptx::idesc_bf16_f32_mn(128, s.rp), 0u);
                 } else {
-                    ptx::mma_bf16_elect_x2(d, ad, bd, 2048 / 16, 256 / 16, ptx::idesc_bf16_f32_mn(128, 2 * s.rp), !begins);
-                    ptx::mma_bf16_elect_x2(d + 2 * s.rp, ad, bd + (s.rp >> 2) * s.column() / 16, 2048 / 16, 256 / 16, ptx::idesc_bf16_f32_mn(128, s.rp), !begins);
+                    ptx::mma_bf16_elect_x4(d, ad, bd, 2048 / 16, 256 / 16, ptx::idesc_bf16_f32_mn(128, 3 * s.rp), turn > 0);
                 }
             }
             ptx::mma_commit_elect(&empty[at]);
             at = at + 1 == s.stages() ? 0 : at + 1;
             phase = at ? phase : phase ^ 1u;
-            begins = last;
+            turn = last ? 0 : turn + 1;
             if (last) {
                 ptx::mma_commit_elect(done);
                 ++runs;
