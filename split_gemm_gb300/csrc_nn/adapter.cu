@@ -30,14 +30,16 @@ bool shape_pass(PassParams& p, int64_t rows, int base_bytes, int out_bytes, bool
     const int64_t groups = p.adapters + 1 < rows ? p.adapters + 1 : rows;
     for (int h = 0; h < 2; ++h)
         for (int splits = 1; splits <= 8; splits *= 2) {
-            if (splits > 1 && splits * P_STEP > p.from) break;
+            const int parts = static_cast<int>(mx::cdiv<int64_t>(p.from, P_STEP)), chunks = static_cast<int>(mx::cdiv<int64_t>(p.to, P_COLS));
+            if (splits > 1 && splits > parts && splits > chunks) break;
             const int tile = TILE >> h;
             const int64_t ctas = (rows / tile + (groups + 1) / 2) * splits;
             const double held = splits == 8 ? 120.0 : splits == 4 ? 144.0 : 152.0;  // CTAs of clusters that the SMs hold at once
             const double waves = static_cast<double>(mx::cdiv<int64_t>(ctas, static_cast<int64_t>(held)));
             const double on = static_cast<double>(ctas) < held ? static_cast<double>(ctas) : held;
-            const double bytes = tile * (2.0 * p.from + static_cast<double>(base_bytes + out_bytes) * p.to) / splits;
-            const double weights = 2.0 * p.rank * (static_cast<double>(p.from) + p.to) / splits;
+            const double from = static_cast<double>(p.from) / (splits < parts ? splits : parts), to = static_cast<double>(p.to) / (splits < chunks ? splits : chunks);
+            const double bytes = tile * (2.0 * from + (base_bytes + out_bytes) * to);
+            const double weights = 2.0 * p.rank * (from + to);
             const double fast = vec ? 60.0 : 12.0, rate = 6600.0 / on < fast ? 6600.0 / on : fast;
             const double own = (bytes + weights) / fast / 1000.0, hbm = bytes / rate / 1000.0;
             const double us = waves * (3.0 + (splits > 1 ? 3.0 : 0.0) + (own > hbm ? own : hbm));

@@ -165,12 +165,12 @@ struct Pass {
     }
 
     // A thread finishes vectors of 8 elements, of 32 columns: one run of 8 or, where base or out has 32 bits, two of 4 at 16 columns' distance, so that
-    // four threads' runs are whole sectors; of rows that are not whole vectors four of 2, as four threads' single elements then lie in one sector.
+    // four threads' runs are whole sectors (rows that are not whole vectors: finish_rows).
     // It gets columns 8j + 2(lane%4) + {0, 1} of the accumulator, j = 0 .. 3; w2's column c becomes row place_of(c) of the operand for that.
-    static constexpr int RUN = !VEC ? 2 : sizeof(TB) == 2 && sizeof(TO) == 2 ? 8 : 4, RUNS = 8 / RUN, APART = 4 * RUN;
+    static constexpr int RUN = sizeof(TB) == 2 && sizeof(TO) == 2 ? 8 : 4, RUNS = 8 / RUN, APART = 4 * RUN;
     __device__ __forceinline__ static int place_of(int c)
     {
-        if constexpr (RUN == 2) return c;
+        if constexpr (!VEC) return c;
         return (c & ~31) + (c & 1) + (RUN == 8 ? 8 * ((c >> 1) & 3) + 2 * ((c >> 3) & 3) : 8 * (2 * ((c >> 4) & 1) + ((c >> 1) & 1)) + 2 * ((c >> 2) & 3));
     }
     // w2's columns of a chunk from c0 on, by the warps that bring it.
@@ -387,7 +387,7 @@ struct Pass {
             }
         }
     }
-    __device__ __forceinline__ void get_base(Held& b, int slot, int turn, int c0) const
+    __device__ __forceinline__ void get_base(Held& b, int slot) const
     {
         if constexpr (VEC) {
             const uint32_t at = base_ring() + slot * (P_LOADERS * 64) - tid * (16 - PIECE);
@@ -403,8 +403,6 @@ struct Pass {
                     to[0] = q.x, to[1] = q.y;
                 }
             }
-        } else {
-            load_base(b, turn, c0);
         }
     }
     // The same straight from memory.
@@ -453,11 +451,7 @@ struct Pass {
                 const float2* from = f[k] + r * (RUN / 2);
                 const int col = col_of(i, c0) + APART * r;
                 const bool here = live && row_here[row_index(i)];
-                if constexpr (!VEC) {
-#pragma unroll
-                    for (int j = 0; j < RUN; ++j)
-                        if (here && col + j < p.to) mx::from_float(row[j], j % 2 ? from[j / 2].y : from[j / 2].x);
-                } else if constexpr (sizeof(TO) == 4) {
+                if constexpr (sizeof(TO) == 4) {
                     ptx::st_stream_v4_if(row, make_uint4(__float_as_uint(from[0].x), __float_as_uint(from[0].y), __float_as_uint(from[1].x), __float_as_uint(from[1].y)),
                                          here && (whole || col < p.to));
                 } else {
@@ -472,6 +466,54 @@ struct Pass {
                     else
                         ptx::st_stream_v2_if(row, make_uint2(o[0], o[1]), here && (whole || col < p.to));
                 }
+            }
+        }
+    }
+
+    // Rows that are not whole vectors: the warp's rows of 64 columns of the chunk at c0 one after another, 32 neighbouring elements at a time, one to a lane (in
+    // the accumulator's own order 8 rows' elements took 8 turns of a load or store: 12867 x 296 -> 659 56 us), by way of the warp's share of the ring.
+    // `at`: the warp's 64 columns of tensor memory, if there are sums.
+    static constexpr int BATCH = 16;
+    __device__ __forceinline__ void ask_rows(float (&b)[BATCH], int first, int col) const
+    {
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            const int row = LANES * (warp & 3) + first + i;
+            b[i] = 0.f;
+            if (p.base && row < piece.rows && col < p.to) b[i] = mx::to_float(static_cast<const TB*>(p.base)[ids[row] * p.base_stride + col]);
+        }
+    }
+    template <bool SUMS, typename Wait, typename Free>
+    __device__ __forceinline__ void finish_rows(uint32_t at, int c0, bool live, const Wait& wait_sums, const Free& free_sums) const
+    {
+        constexpr int PARTS = 2 * LANES / BATCH;  // batches of rows of both halves of the columns
+        float b[2][BATCH];
+        const int col0 = c0 + 64 * ((warp >> 2) & 1) + lane;
+        ask_rows(b[0], 0, col0);
+        wait_sums();
+        float* mine = reinterpret_cast<float*>(mem + s.area() - s.ring() + warp * (s.ring() / P_WARPS));  // [LANES][33]
+#pragma unroll
+        for (int k = 0; k < PARTS; ++k) {
+            const int half = k / (PARTS / 2), first = k % (PARTS / 2) * BATCH, col = col0 + 32 * half;
+            if (k + 1 < PARTS) ask_rows(b[(k + 1) & 1], (k + 1) % (PARTS / 2) * BATCH, col0 + 32 * ((k + 1) / (PARTS / 2)));
+            if (SUMS && first == 0) {
+                uint32_t v[2][16];
+                ptx::tmem_ld_32x32b_x16(at + 32 * half, v[0]);
+                ptx::tmem_ld_32x32b_x16(at + 32 * half + 16, v[1]);
+                ptx::tmem_ld_wait();
+                if (half) free_sums();
+                __syncwarp();
+                if (lane < LANES)
+#pragma unroll
+                    for (int c = 0; c < 32; ++c) mine[lane * 33 + c] = __uint_as_float(v[c >> 4][c & 15]);
+                __syncwarp();
+            }
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) {
+                const int row = LANES * (warp & 3) + first + i;
+                float f = b[k & 1][i] + (SUMS ? mine[(first + i) * 33 + lane] : 0.f);
+                if (p.relu) f = __uint_as_float(ptx::relu_nan(__float_as_uint(f)));
+                if (live && row < piece.rows && col < p.to) mx::from_float(static_cast<TO*>(p.out)[ids[row] * p.out_stride + col], f);
             }
         }
     }
@@ -495,14 +537,19 @@ struct Pass {
             for (int i = tid; i < piece.rows * p.rank; i += P_THREADS)
                 p.mid[static_cast<int64_t>(ids[i / p.rank]) * p.rank + i % p.rank] = 0.f;
         if (!p.out || warp >= P_WARPS) return;
-        for (int c = chunk0 + group; c < chunk1; c += 2)
+        for (int c = chunk0 + group; c < chunk1; c += 2) {
+            if constexpr (!VEC) {
+                finish_rows<false>(0u, c * COLS, true, [] {}, [] {});
+            } else {
 #pragma unroll
-            for (int turn = 0; turn < TURNS; ++turn) {
-                Held b;
-                load_base(b, turn, c * COLS);
-                const uint32_t none[2][16] = {};
-                finish(b, none, turn, c * COLS, false, true);
+                for (int turn = 0; turn < TURNS; ++turn) {
+                    Held b;
+                    load_base(b, turn, c * COLS);
+                    const uint32_t none[2][16] = {};
+                    finish(b, none, turn, c * COLS, false, true);
+                }
             }
+        }
     }
 
     __device__ __forceinline__ void run()
@@ -549,7 +596,7 @@ struct Pass {
         if (piece.rows > 0) {
             if (tid < TILE) ids[tid] = p.plan.order[piece.first + (tid < piece.rows ? tid : 0)];
             __syncthreads();
-            if (warp < P_WARPS) make_rows();
+            if (VEC && warp < P_WARPS) make_rows();
             if (e < p.adapters)
                 with(tmem, chunk0, chunk1);
             else
@@ -693,6 +740,7 @@ struct Pass {
         if (warp < P_WARPS) {
             store_parts(parts);
             ptx::tc_fence_before();
+            if (p.splits > 1) ptx::cluster_wait();  // what this CTA sent has been received: its place is the ring's now
         }
         if (s.late())
             __syncthreads();
@@ -730,6 +778,19 @@ struct Pass {
             }
             ptx::cp_async_wait_all();
             if (n > 1) arrive(&w2_full[(n - 1) % n_bufs]);
+        } else if (!VEC) {
+            for (int j = group; j < n; j += 2)
+                finish_rows<true>(
+                    tmem + COLS * group + 64 * ((warp >> 2) & 1) + (static_cast<uint32_t>(32 * (warp & 3)) << 16), (chunk0 + j) * COLS, ok,
+                    [&] {
+                        wait(&d_full[group], static_cast<uint32_t>(j >> 1) & 1u, ok);
+                        __syncwarp();
+                        ptx::tc_fence_after();
+                    },
+                    [&] {
+                        ptx::tc_fence_before();
+                        ptx::mbar_arrive_if(&d_empty[group], lane == 0);
+                    });
         } else if (group < n) {
             // This group's chunks, every other one; base P_DEPTH turns ahead.
             const auto ask = [&](int slot, int j, int t) {  // turn t from chunk j's beginning on
@@ -762,7 +823,7 @@ struct Pass {
                         const int t = q * (4 / HOLD) + h;
                         ptx::cp_async_wait<P_DEPTH - 1>();
                         Held held;
-                        get_base(held, slot, t, c0);
+                        get_base(held, slot);
                         finish(held, v, t, c0, whole, ok);
                         ask(slot, j, t + P_DEPTH);  // what the slot held is in registers
                         slot = slot + 1 == P_DEPTH ? 0 : slot + 1;
@@ -774,7 +835,7 @@ struct Pass {
         ptx::cp_async_wait_all();
         if (!ok && lane == 0 && p.status) atomicMax(p.status, 6u);
         __syncwarp();
-        if (p.splits > 1) ptx::cluster_wait();  // what this CTA sent has been received
+        if (p.splits > 1 && warp >= P_WARPS) ptx::cluster_wait();
     }
 };
 

@@ -16,7 +16,8 @@ SHAPES = [(1, 1, 1, 1, 1), (1, 4096, 512, 16, 9), (2, 64, 128, 8, 2), (7, 33, 40
           (64, 512, 768, 16, 32), (65, 130, 258, 24, 7), (127, 64, 64, 64, 1), (128, 128, 264, 128, 2), (129, 136, 72, 100, 3), (200, 1001, 2001, 20, 5),
           (257, 320, 192, 8, 300), (300, 96, 1111, 7, 4), (511, 40, 24, 16, 6), (512, 2056, 136, 32, 3), (513, 200, 328, 48, 11), (785, 1001, 777, 8, 3),
           (1025, 256, 520, 16, 1), (1500, 64, 320, 64, 20), (2049, 136, 64, 128, 2), (640, 24, 16, 3, 5), (900, 2500, 72, 40, 2),
-          (641, 520, 136, 24, 3), (1300, 1001, 200, 33, 2), (700, 256, 1000, 8, 40), (160, 72, 200, 64, 3), (161, 72, 200, 64, 3), (3000, 384, 384, 48, 2)]
+          (641, 520, 136, 24, 3), (1300, 1001, 200, 33, 2), (700, 256, 1000, 8, 40), (160, 72, 200, 64, 3), (161, 72, 200, 64, 3), (3000, 384, 384, 48, 2),
+          (153, 351, 2893, 78, 6), (700, 64, 1600, 32, 2)]
 
 
 @pytest.fixture(scope="module")
