@@ -27,13 +27,12 @@ bool shape_pass(PassParams& p, int64_t rows, int base_bytes, int out_bytes, bool
 {
     bool halved = false;
     double best = 1e30;
-    const int64_t groups = p.adapters + 1 < rows ? p.adapters + 1 : rows;
     for (int h = 0; h < 2; ++h)
         for (int splits = 1; splits <= 8; splits *= 2) {
             const int parts = static_cast<int>(mx::cdiv<int64_t>(p.from, P_STEP)), chunks = static_cast<int>(mx::cdiv<int64_t>(p.to, P_COLS));
             if (splits > 1 && splits > parts && splits > chunks) break;
             const int tile = TILE >> h;
-            const int64_t ctas = (rows / tile + (groups + 1) / 2) * splits;
+            const int64_t ctas = tiles_about(rows, p.adapters, tile) * splits;
             const double held = splits == 8 ? 120.0 : splits == 4 ? 144.0 : 152.0;  // CTAs of clusters that the SMs hold at once
             const double waves = static_cast<double>(mx::cdiv<int64_t>(ctas, static_cast<int64_t>(held)));
             const double on = static_cast<double>(ctas) < held ? static_cast<double>(ctas) : held;

@@ -25,6 +25,14 @@ struct PassParams {
     int early;   // the next kernel may start: it waits itself for what it needs of this one
 };
 
+// About how many pieces of up to `tile` rows there are: one to an adapter at least, and half a piece more to each than its rows fill.
+inline int64_t tiles_about(int64_t rows, int64_t groups, int tile)
+{
+    groups = groups < rows ? groups : rows;
+    const int64_t filled = rows / tile + (groups + 1) / 2;
+    return filled > groups ? filled : groups;
+}
+
 constexpr int P_BLOCK = 64, P_STEP = 2 * P_BLOCK;  // of `from`: in a block of operands, and in a stage
 constexpr int P_COLS = 128;                        // of `to`, in a chunk
 constexpr int P_MOST_STAGES = 4, P_MOST_CHUNKS = 8;
