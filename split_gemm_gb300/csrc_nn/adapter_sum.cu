@@ -13,7 +13,7 @@
 // in's rows keep their 128-byte lines (128-byte swizzle: copies that spread a line over shared memory are half as fast); mid's parts lie in core matrices of 8
 // rows x 16 bytes, each column of them 16 bytes longer than it needs to be, so that neighbours fall into different banks.
 //
-// bf16 rows come by cp.async into the operand's place, ring stages ahead; checkpoints, rows that are not whole vectors, and mid come through
+// bf16 rows come by cp.async into the operand's place, one stage ahead (ranks up to 128) to three (16); checkpoints, rows that are not whole vectors, and mid come through
 // registers, one or two stages ahead.  A checkpoint's integer becomes a bf16 number by bits: (m | 128) - 128 or 256, each with the scale in its exponent.
 //
 // Every wait is bounded, as in the pass (adapter_pass.cuh).
@@ -27,6 +27,7 @@ namespace sgb {
 namespace ad {
 
 constexpr int U_WARPS = 16, U_LOADERS = 32 * U_WARPS, U_THREADS = U_LOADERS + 32;
+constexpr int U_STAGES = 6;  // at most
 constexpr uint64_t U_WAIT_NS = 1000000000ull;
 
 // Shared memory of a stage of `tokens` rows: in by lines of 64 columns, then mid's parts, `column` bytes to a 16-byte column.
@@ -37,11 +38,17 @@ struct SumSmem {
     __host__ __device__ constexpr int lines() const { return tokens * 128; }  // of 64 columns
     __host__ __device__ constexpr int in_bytes() const { return 2 * blocks * lines(); }
     __host__ __device__ constexpr int stage() const { return (in_bytes() + 3 * rp / 8 * column() + 1023) / 1024 * 1024; }
-    __host__ __device__ constexpr int stages() const { return 3; }
     // the plan's part: rows' numbers and each stage's tile by stage, the tiles
     __host__ __device__ constexpr int lists() const { return SUM_TILES * (TILE * 4 + 16) + SUM_TILES * 4 * 4 + 16; }
+    __host__ __device__ constexpr int stages() const
+    {
+        const int fit = (227 * 1024 - lists() - 256) / stage();
+        return fit < U_STAGES ? fit : U_STAGES;
+    }
     __host__ __device__ constexpr int bytes() const { return stages() * stage() + lists() + 256; }
 };
+
+static_assert(SumSmem(16).stages() >= 3 && SumSmem(64).stages() >= 3 && SumSmem(128).stages() >= 3, "a stage filled, one multiplied and one on its way");
 
 template <int MODE>  // 0: bf16 rows of whole vectors, 1: bf16, 2: a checkpoint
 struct Sum {
@@ -279,9 +286,24 @@ struct Sum {
 #pragma unroll
         for (int i = 0; i < DEPTH; ++i)
             if (i < n) fetch(held[i], i);
-        int first = 0, runs = 0, told = 0;  // told: stages before it have been told of
-        int at = 0, before = 0;  // slots of this stage and of the last one
+        int first = 0, runs = 0;
+        int at = 0;  // the slot of this stage
         uint32_t free_phase = 1u;
+        // Copies run ahead of the stage that is told of by all slots but one, whose products go on meanwhile, and the stage's own.
+        const int ahead = s.stages() - 2;
+        int to = 0;
+        uint32_t to_phase = 1u;
+        const auto copy_next = [&](int k) {
+            if (k < n) {
+                wait(&empty[to], to_phase, ok);
+                copy(ptx::smem_addr(mem) + to * s.stage(), k);
+            }
+            ptx::cp_async_commit();
+            to = to + 1 == s.stages() ? 0 : to + 1;
+            to_phase = to ? to_phase : to_phase ^ 1u;
+        };
+        if constexpr (MODE == 0)
+            for (int k = 0; k < ahead; ++k) copy_next(k);
         for (int k0 = 0; k0 < n; k0 += DEPTH)
 #pragma unroll
             for (int i = 0; i < DEPTH; ++i) {
@@ -289,26 +311,24 @@ struct Sum {
                 if (k >= n) break;
                 const uint32_t st = ptx::smem_addr(mem) + at * s.stage();
                 const bool last = ends_run(k);
-                wait(&empty[at], free_phase, ok);
-                if constexpr (MODE == 0) {
-                    copy(st, k);
-                    ptx::cp_async_commit();
-                }
+                if constexpr (MODE == 0)
+                    copy_next(k + ahead);
+                else
+                    wait(&empty[at], free_phase, ok);
                 store(held[i], st, (k - first) & 1);
                 if (k + DEPTH < n) fetch(held[i], k + DEPTH);
-                ptx::fence_proxy_async_smem();
-                // One arrival to a warp (a barrier takes its arrivals one after another); copies' stages are told of a stage later.
                 if constexpr (MODE == 0) {
-                    if (last)
-                        ptx::cp_async_wait<0>();
-                    else
-                        ptx::cp_async_wait<1>();
+                    switch (ahead) {
+                        case 1: ptx::cp_async_wait<1>(); break;
+                        case 2: ptx::cp_async_wait<2>(); break;
+                        case 3: ptx::cp_async_wait<3>(); break;
+                        default: ptx::cp_async_wait<4>();
+                    }
                 }
+                ptx::fence_proxy_async_smem();
+                // One arrival to a warp: a barrier takes its arrivals one after another.
                 __syncwarp();
-                if (MODE == 0) ptx::mbar_arrive_if(&full[before], lane == 0 && k > told);
-                ptx::mbar_arrive_if(&full[at], lane == 0 && (MODE != 0 || last));
-                if (last) told = k + 1;
-                before = at;
+                ptx::mbar_arrive_if(&full[at], lane == 0);
                 at = at + 1 == s.stages() ? 0 : at + 1;
                 free_phase = at ? free_phase : free_phase ^ 1u;
                 if (last) {
@@ -377,7 +397,7 @@ __global__ void __launch_bounds__(U_THREADS, 1) sum_tiles(const __grid_constant_
     int* ids = reinterpret_cast<int*>(tiles + SUM_TILES);
     int* steps = ids + SUM_TILES * TILE;
     uint64_t* full = reinterpret_cast<uint64_t*>(lists + s.lists());
-    uint64_t *empty = full + 4, *done = empty + 4, *free_ = done + 1;
+    uint64_t *empty = full + U_STAGES, *done = empty + U_STAGES, *free_ = done + 1;
     uint32_t* slot = reinterpret_cast<uint32_t*>(free_ + 1);
     volatile uint32_t* abort_flag = slot + 1;
     volatile int* count = reinterpret_cast<volatile int*>(slot + 2);
