@@ -18,6 +18,8 @@
  *
  * x, a, b and dy are bf16, h and dh fp32.  Products of bf16 numbers are exact and their
  * sums fp32; h and dh enter their products as three bf16 parts that add up to all their 24 bits (down to 2^-110).
+ * Where a row meets an infinity or a NaN in its own x, dy, h, a[e] or b[e], the sums they enter are not finite, NaN wherever
+ * one of the parts is zero; they stay within that row, or that adapter's gradients.
  * A value is rounded once, where it is stored.  Sums over rows are joined in a fixed order:
  * the same call gives the same bits.
  *
@@ -50,7 +52,7 @@ typedef struct {
     int32_t activation;            /* conv2d_activation */
 } adapter_fwd_params;
 
-/* out may be y itself when type and stride are the same.  scale_dev: [adapters] fp32 or NULL (ones).
+/* out may be y itself when type and stride are the same, and overlaps no other operand.  scale_dev: [adapters] fp32 or NULL (ones).
  * h_dev: [rows][rank] fp32, dense, for the backward pass; may be NULL.  plan_dev: of the same rows and adapters. */
 int adapter_fwd(const adapter_fwd_params* params, const void* plan_dev, const void* y_dev, const void* x_dev,
                 const void* a_dev, const void* b_dev, const float* scale_dev, void* out_dev, float* h_dev,
@@ -66,7 +68,7 @@ typedef struct {
 } adapter_bwd_params;
 
 /* dx_dev, da_dev, db_dev: each may be NULL (not computed).  dx0_dev may be NULL (zeros), or dx itself when type and stride are
- * the same.  da [adapters][rank][cols] and db [adapters][outs][rank] fp32, dense.  x_dev (with x_scales_dev for MXINT8) is needed
+ * the same; no result overlaps another operand.  da [adapters][rank][cols] and db [adapters][outs][rank] fp32, dense.  x_dev (with x_scales_dev for MXINT8) is needed
  * for da, h_dev of the forward pass for db.  workspace_dev: at least
  * adapter_bwd_workspace_bytes() bytes of any content, 16-byte aligned. */
 size_t adapter_bwd_workspace_bytes(const adapter_bwd_params* params);

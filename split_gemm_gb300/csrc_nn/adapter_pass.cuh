@@ -4,9 +4,11 @@
 //
 // Forward w1 is a[e] and w2 is b[e], both K-major operands; backward (TRANS) w1 is b[e]^T and w2 a[e]^T, both MN-major.
 //
-// in, base and out each pass once over HBM and bind it: with rank r the matrix units have 2r flops to some 4 bytes.  A cluster
+// in, base and out each pass once over HBM and bind it: with rank r the matrix units have 2r flops to some 4 bytes.  What is reached is less, as a CTA's parts
+// follow one another: 8192 x 4096 -> 4096 of rank 64 takes 54 us (33 at HBM's rate, 4.1 TB/s), 12544 x 256 -> 1024 of rank 16, y fp32, 23 us (12.5).  A cluster
 // of S CTAs shares a tile: each takes a part of `from` for the first product, 128/S rows of the join and a part of `to` for the
-// second.  Two CTAs stay on an SM up to rank 64, each at a phase of its own.  mid never leaves the chip but for the copy that the gradients need.
+// second.  One CTA fills an SM: what HBM needs in flight are bytes, and 96 KB of base on their way to shared memory gave more than two CTAs with
+// theirs in registers.  mid never leaves the chip but for the copy that the gradients need.
 //
 // First product: rows of `in` are gathered by the plan's order with cp.async, 128 bytes of a row at a time, 128 x rank x 128 a stage (the loop around a stage costs its warps some
 // 600 clocks, more than its copies of half the size).  The sums over
@@ -15,8 +17,11 @@
 //
 // Second product: mid's parts are its A operand in tensor memory (from shared memory they would be read once for each chunk and take
 // most of its bandwidth), 128 columns of `to` its B.  Two groups of 8 warps finish chunks by turns, each with an accumulator of its own.  A thread reads the accumulator in the 16 x 256-bit layout, 2
-// neighbouring columns of a lane in each group of 8; w2's rows are placed in shared memory in an order that makes these 8 neighbouring columns of out, so base and
-// out move in 16-byte vectors straight between registers and memory, base a chunk ahead.
+// neighbouring columns of a lane in each group of 8; w2's rows are placed in shared memory in an order that makes these 8 (fp32: 4) neighbouring columns of out, so base and
+// out move in 16-byte vectors, base three turns ahead by way of a ring that each thread alone reads.
+//
+// Rows that are not whole vectors (VEC = false) come through registers without running ahead, and are finished one row at a time: 777 x 1001 -> 2001
+// of rank 20 takes 20 us, most of it latency (1.7 at HBM's rate).
 //
 // Every wait is bounded: on running out the status word is set and the CTA goes through its remaining barriers without waiting or storing.
 #pragma once

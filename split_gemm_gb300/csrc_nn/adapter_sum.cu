@@ -1,7 +1,8 @@
 // The adapters' weight gradients: sums over an adapter's rows, out[e] (r, c) = sum of mid[t][r] * in[t][c], for da (mid = dh, in = x) and
 // db (mid = h, in = dy) in one launch.
 //
-// HBM binds: `in` is read once, and with rank r there are 2r flops to its 1 or 2 bytes.  A CTA takes 256 columns of `in` (128 above
+// HBM would bind: `in` is read once, and with rank r there are 2r flops to its 1 or 2 bytes.  What is reached is half of its rate (db of 16384 x 4096, rank 64:
+// 46 us for 20 of HBM's, with two launches): a stage's mid is converted by the warps that also see to its copies, some 1.2 us for 64 KB or less.  A CTA takes 256 columns of `in` (128 above
 // rank 64, by tensor memory) and a piece of up to 32 of the plan's tiles, whatever adapters those belong to; an adapter's sum that lies in one piece goes straight
 // to the result, else each piece's part goes to the workspace and a second launch adds the parts in order.
 //
@@ -15,6 +16,9 @@
 //
 // bf16 rows come by cp.async into the operand's place, one stage ahead (ranks up to 128) to three (16); checkpoints, rows that are not whole vectors, and mid come through
 // registers, one or two stages ahead.  A checkpoint's integer becomes a bf16 number by bits: (m | 128) - 128 or 256, each with the scale in its exponent.
+//
+// db needs nothing of the pass before it, and its CTAs run beside that pass where it leaves SMs free; da's, which take dh, wait for it.  Both gradients of
+// 16384 x 4096 x 4096, rank 64, with dx take 182 us, where dx alone takes 96.
 //
 // Every wait is bounded, as in the pass (adapter_pass.cuh).
 #include "adapter.h"

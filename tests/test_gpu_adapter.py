@@ -393,3 +393,104 @@ def test_refusals(sg):
     for n in (0, 65536):
         with pytest.raises(ValueError):
             sg.adapter_plan(torch.zeros(4, dtype=torch.int32, device="cuda"), n)
+
+
+@pytest.mark.parametrize("rows", [20, 700])
+def test_offsets_past_2_to_31(sg, rows):
+    """Rows that lie further than 2^31 elements from the first: the bits of dense rows."""
+    c, index = _cuda(_case(rows, 64, 72, 16, 3)), _index(rows, 3).cuda()
+    stride = 2 ** 31 // (rows - 1) // 8 * 8 + 16
+
+    def far(t, filled=True):
+        v = torch.empty((rows - 1) * stride + t.shape[1], dtype=t.dtype, device="cuda").as_strided(t.shape, (stride, 1))
+        return v.copy_(t) if filled else v
+    plan = sg.adapter_plan(index, 3)
+    out, h = sg.adapter_fwd(c["y"], c["x"], c["a"], c["b"], plan, out_dtype=BF16)
+    x, y, made = far(c["x"]), far(c["y"]), far(out, False)
+    sg.adapter_fwd_into(made, y, x, c["a"], c["b"], plan)
+    assert torch.equal(made, out)
+    del y, made
+    dx, da, db = sg.adapter_bwd(c["dy"], c["x"], h, c["a"], c["b"], plan, dx=c["dx0"], out_dtype=BF16)
+    dy, made = far(c["dy"]), far(dx, False)
+    grads = torch.empty_like(da), torch.empty_like(db)
+    sg.adapter_bwd_into(made, *grads, dy, x, h, c["a"], c["b"], plan, dx0=c["dx0"])
+    assert torch.equal(made, dx) and torch.equal(grads[0], da) and torch.equal(grads[1], db)
+
+
+def test_a_checkpoint_past_2_to_31(sg):
+    """The last rows of a checkpoint of more than 2^31 bytes: the bits of those rows alone."""
+    rows, few = 530000, 100
+    c = _cuda(_case(few, 4096, 8, 8, 2))
+    small = sg.mxint8_quantize(c["x"])
+    big = sg.mxint8_empty(rows, 4096, "cuda")
+    big.data.zero_()
+    big.scales.zero_()
+    big.data.view(rows, -1)[-few:] = small.data.view(few, -1)
+    big.scales.view(rows, -1)[-few:] = small.scales.view(few, -1)
+    index = torch.full((rows,), -1, dtype=torch.int32, device="cuda")
+    index[-few:] = _index(few, 2, none=0).cuda()
+    dy, h = torch.zeros(rows, 8, dtype=BF16, device="cuda"), torch.zeros(rows, 8, device="cuda")
+    dy[-few:], h[-few:] = c["dy"], torch.randn(few, 8, device="cuda")
+    want = sg.adapter_bwd(c["dy"], small, h[-few:].contiguous(), c["a"], c["b"], sg.adapter_plan(index[-few:].contiguous(), 2))
+    got = sg.adapter_bwd(dy, big, h, c["a"], c["b"], sg.adapter_plan(index, 2))
+    # one block of columns to dh's sums and one piece to each adapter's: no other order in either call
+    assert torch.equal(got[0][-few:], want[0]) and not got[0][:-few].any()
+    assert torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])
+
+
+def test_every_python_call_makes_its_device_current(sg, monkeypatch):
+    """The calls that the compiled module does not take (here all of them) reach the library with their device current."""
+    import contextlib
+
+    from split_gemm_gb300 import _rows, adapter, mxint8
+    inside, reached = [], []
+
+    @contextlib.contextmanager
+    def on_device_of(t):
+        inside.append(t.get_device())
+        yield
+        inside.pop()
+
+    class Library:
+        def __getattr__(self, name):
+            fn = getattr(sg.load_library(), name)
+
+            def call(*args):
+                assert inside == [0] or name.endswith("_bytes"), name
+                reached.append(name)
+                return fn(*args)
+            return call
+
+    for module in (adapter, mxint8):
+        monkeypatch.setattr(module, "on_device_of", on_device_of)
+        monkeypatch.setattr(module, "library", Library)
+        monkeypatch.setattr(module, "calls", lambda: _rows._NoCalls)
+    c = _cuda(_case(20, 64, 72, 8, 3))
+    plan = sg.adapter_plan(_index(20, 3).cuda(), 3)
+    _, h = sg.adapter_fwd(c["y"], c["x"], c["a"], c["b"], plan)
+    q = sg.mxint8_quantize(c["x"])
+    sg.mxint8_dequantize(q)
+    sg.adapter_bwd(c["dy"], q, h, c["a"], c["b"], plan)
+    stats = torch.zeros(20, device="cuda")
+    sg.mxint8_layer_norm_bwd(c["dx0"], q, stats, stats)
+    assert {n for n in reached if not n.endswith("_bytes")} == {"adapter_plan", "adapter_fwd", "adapter_bwd", "mxint8_quantize", "mxint8_dequantize",
+                                                                "mxint8_layer_norm_bwd"}
+
+
+def test_another_device_or_stream_is_refused(sg):
+    c, plan = _cuda(_case(20, 64, 72, 8, 3)), sg.adapter_plan(_index(20, 3).cuda(), 3)
+    h = torch.zeros(20, 8, device="cuda")
+    for k in ("y", "a", "b"):
+        with pytest.raises(ValueError):
+            sg.adapter_fwd(**{**{n: c[n] for n in ("y", "x", "a", "b")}, k: c[k].cpu()}, plan=plan)
+    with pytest.raises(ValueError):
+        sg.adapter_fwd(c["y"], c["x"], c["a"], c["b"], plan._replace(data=plan.data.cpu()))
+    with pytest.raises(ValueError):
+        sg.adapter_bwd(c["dy"], c["x"], h.cpu(), c["a"], c["b"], plan)
+    q = sg.mxint8_quantize(c["x"])
+    with pytest.raises(ValueError):
+        sg.adapter_bwd(c["dy"], q._replace(scales=q.scales.cpu()), h, c["a"], c["b"], plan)
+    need = sg.adapter_bwd_workspace_bytes(c["dy"], c["x"], c["a"], c["b"], plan)
+    for workspace in (torch.zeros(need, dtype=torch.uint8), torch.zeros(1, dtype=torch.uint8, device="cuda").expand(need)):
+        with pytest.raises(ValueError, match="workspace"):
+            sg.adapter_bwd(c["dy"], c["x"], h, c["a"], c["b"], plan, workspace=workspace)
