@@ -63,6 +63,20 @@ bool in_vectors(const PassParams& p, int32_t base, int32_t out)
 // dh's bytes in the workspace, to whole vectors.
 size_t dh_bytes(int64_t rows, int64_t rank) { return (static_cast<size_t>(rows) * static_cast<size_t>(rank) * 4 + 15) / 16 * 16; }
 
+// Two parts of a gradient to a piece, to whole vectors.
+size_t part_bytes(const adapter_bwd_params& q, int64_t cols, int tiles_each)
+{
+    const int64_t pieces = sum_pieces(PlanLayout(q.rows, q.adapters), tiles_each);
+    return (2 * static_cast<size_t>(pieces) * q.rank * static_cast<size_t>(cols) * 4 + 15) / 16 * 16;
+}
+
+SumShape shape_sums(const adapter_bwd_params& q) { return shape_sums(q.rows, q.adapters, static_cast<int>(q.rank), q.cols, q.outs); }
+
+size_t bwd_bytes(const adapter_bwd_params& q, const SumShape& each)
+{
+    return dh_bytes(q.rows, q.rank) + part_bytes(q, q.cols, each.da) + part_bytes(q, q.outs, each.db);
+}
+
 bool status_word(uint32_t** word)
 {
     void* at = nullptr;
@@ -132,10 +146,7 @@ extern "C" int adapter_fwd(const adapter_fwd_params* params, const void* plan_de
 extern "C" size_t adapter_bwd_workspace_bytes(const adapter_bwd_params* params)
 {
     if (!params || ad::check(params->rows, params->cols, params->outs, params->rank, params->adapters)) return 0;
-    // dh, and two parts of each gradient to a piece
-    const int each = ad::sum_tiles_each(params->rows, params->adapters, static_cast<int>(params->rank), params->cols, params->outs);
-    const size_t pieces = static_cast<size_t>(ad::sum_pieces(ad::PlanLayout(params->rows, params->adapters), each));
-    return ad::dh_bytes(params->rows, params->rank) + 2 * pieces * params->rank * static_cast<size_t>(params->cols + params->outs) * 4;
+    return ad::bwd_bytes(*params, ad::shape_sums(*params));
 }
 
 extern "C" int adapter_bwd(const adapter_bwd_params* params, const void* plan_dev, const void* dy_dev, const void* x_dev,
@@ -151,6 +162,7 @@ extern "C" int adapter_bwd(const adapter_bwd_params* params, const void* plan_de
         (dx_dev && q.dx_stride < q.cols) || (dx0_dev && q.dx0_stride < q.cols) || (!eight && da_dev && q.x_stride < q.cols))
         return CONV2D_ERR_INVALID;
     if (!ad::aligned(da_dev, CONV2D_OUT_F32) || !ad::aligned(db_dev, CONV2D_OUT_F32)) return CONV2D_ERR_ALIGNMENT;
+    ad::SumShape each{1, 1};
     if (q.rows > 0) {
         if (!plan_dev || !dy_dev || !a_dev || !b_dev || (da_dev && (!x_dev || (eight && !x_scales_dev))) || (db_dev && !h_dev))
             return CONV2D_ERR_INVALID;
@@ -159,7 +171,8 @@ extern "C" int adapter_bwd(const adapter_bwd_params* params, const void* plan_de
             !ad::aligned(a_dev, CONV2D_OUT_BF16) || !ad::aligned(b_dev, CONV2D_OUT_BF16) || !ad::aligned(scale_dev, CONV2D_OUT_F32) ||
             !ad::aligned(dx0_dev, q.dx0_dtype) || !ad::aligned(dx_dev, q.dx_dtype))
             return CONV2D_ERR_ALIGNMENT;
-        const size_t need = adapter_bwd_workspace_bytes(params);
+        each = ad::shape_sums(q);
+        const size_t need = ad::bwd_bytes(q, each);
         if (need && (!workspace_dev || workspace_bytes < need)) return CONV2D_ERR_WORKSPACE;
     } else {
         const size_t grads = static_cast<size_t>(q.adapters) * q.rank * 4;
@@ -195,9 +208,7 @@ extern "C" int adapter_bwd(const adapter_bwd_params* params, const void* plan_de
     s.adapters = p.adapters;
     s.rank = p.rank;
     s.beside = dx_dev || da_dev;
-    s.tiles_each = ad::sum_tiles_each(q.rows, q.adapters, p.rank, q.cols, q.outs);
-    const int64_t pieces = ad::sum_pieces(ad::PlanLayout(q.rows, q.adapters), s.tiles_each);
-    float* part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace_dev) + ad::dh_bytes(q.rows, q.rank));
+    uint8_t* part = static_cast<uint8_t*>(workspace_dev) + ad::dh_bytes(q.rows, q.rank);
     if (da_dev) {
         ad::SumJob& job = s.jobs[0];
         job.in = static_cast<const __nv_bfloat16*>(x_dev);
@@ -205,7 +216,8 @@ extern "C" int adapter_bwd(const adapter_bwd_params* params, const void* plan_de
         job.scales = static_cast<const uint8_t*>(x_scales_dev);
         job.mid = p.mid;
         job.out = da_dev;
-        job.part = part;
+        job.part = reinterpret_cast<float*>(part);
+        job.tiles_each = each.da;
         job.in_stride = q.x_stride;
         job.blocks = mx::cdiv<int64_t>(q.cols, 32);
         job.cols = static_cast<int>(q.cols);
@@ -217,13 +229,14 @@ extern "C" int adapter_bwd(const adapter_bwd_params* params, const void* plan_de
         job.in = static_cast<const __nv_bfloat16*>(dy_dev);
         job.mid = h_dev;
         job.out = db_dev;
-        job.part = part + 2 * pieces * q.rank * q.cols;
+        job.part = reinterpret_cast<float*>(part + ad::part_bytes(q, q.cols, each.da));
+        job.tiles_each = each.db;
         job.in_stride = q.dy_stride;
         job.cols = static_cast<int>(q.outs);
         job.mode = q.outs % 8 == 0 && ad::vectors(dy_dev, q.dy_stride, 2) ? 0 : 1;
         job.out_col = 0;
     }
-    return ad::launch_sums(s, pieces, stream);
+    return ad::launch_sums(s, ad::PlanLayout(q.rows, q.adapters), stream);
 }
 
 extern "C" int adapter_status(conv2d_stream_t stream)

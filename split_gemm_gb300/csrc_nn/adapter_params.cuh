@@ -81,6 +81,7 @@ struct SumJob {
     float *out, *part;             // part: [2 * pieces][rank * cols], in out's order
     int64_t in_stride, blocks;     // blocks of 32 to a checkpoint's row
     int cols, col_blocks;
+    int tiles_each;                // of a piece
     int mode;                      // 0: bf16 rows of whole vectors, 1: bf16, 2: a checkpoint
     int out_col;                   // 1: out[r][c]; else out[c][r]
     int mid_vec, out_vec, join_vec;
@@ -90,16 +91,19 @@ struct SumParams {
     Plan plan;
     SumJob jobs[2];  // without a result: not wanted
     uint32_t* status;
-    int adapters, rank, tiles_each;
+    int adapters, rank;
     int first_late;  // the first CTA of jobs[0], whose mid comes from the pass before
     int beside;      // that pass lets this kernel start early
 };
 
 constexpr int SUM_TILES = 32;  // of a piece, at most
 
-int sum_tiles_each(int64_t rows, int64_t adapters, int rank, int64_t cols, int64_t outs);
+struct SumShape {
+    int da, db;  // tiles to a piece
+};
+SumShape shape_sums(int64_t rows, int64_t adapters, int rank, int64_t cols, int64_t outs);
 int64_t sum_pieces(const PlanLayout& l, int tiles_each);
-int launch_sums(SumParams& p, int64_t pieces, cudaStream_t stream);
+int launch_sums(SumParams& p, const PlanLayout& l, cudaStream_t stream);
 
 // halved: tiles of 64 rows, not 128.
 int launch_pass_fwd(const PassParams& p, int32_t base_dtype, int32_t out_dtype, bool vec, bool halved, cudaStream_t stream);

@@ -18,7 +18,7 @@
 // registers, one or two stages ahead.  A checkpoint's integer becomes a bf16 number by bits: (m | 128) - 128 or 256, each with the scale in its exponent.
 //
 // db needs nothing of the pass before it, and its CTAs run beside that pass where it leaves SMs free; da's, which take dh, wait for it.  Both gradients of
-// 16384 x 4096 x 4096, rank 64, with dx take 182 us, where dx alone takes 96.
+// 16384 x 4096 -> 4096, rank 64, with dx take 181 us, where dx alone takes 96.
 //
 // Every wait is bounded, as in the pass (adapter_pass.cuh).
 #include "adapter.h"
@@ -238,7 +238,7 @@ struct Sum {
     __device__ __forceinline__ void flush(uint32_t tmem, int k, int first, bool ok) const
     {
         const int e = adapter_at(k);
-        const int t0 = piece * p.tiles_each + steps[first], t1 = piece * p.tiles_each + steps[k] + 1;
+        const int t0 = piece * job.tiles_each + steps[first], t1 = piece * job.tiles_each + steps[k] + 1;
         const bool before = p.plan.tile_starts[e] < t0, after = p.plan.tile_starts[e + 1] > t1;
         const int64_t size = static_cast<int64_t>(p.rank) * job.cols;
         float* out = before || after ? job.part + (2 * piece + !before) * size : job.out + e * size;
@@ -421,14 +421,14 @@ __global__ void __launch_bounds__(U_THREADS, 1) sum_tiles(const __grid_constant_
         *abort_flag = 0u;
         ptx::mbar_init_fence();
     }
-    // The pass has waited for what came before it and lets this kernel start only then.
-    if (late || !p.beside) ptx::grid_dependency_wait();
+    // The pass has waited for what came before it, the plan with it, and lets this kernel start only then.
+    if (!p.beside) ptx::grid_dependency_wait();
     // The piece's tiles, rows and stages; tiles without an adapter, which come last, are left out.
-    const int first = piece * p.tiles_each, left = p.plan.tile_starts[p.adapters] - first;
-    const int n_tiles = left < p.tiles_each ? left : p.tiles_each;
+    const int first = piece * job.tiles_each, left = p.plan.tile_starts[p.adapters] - first;
+    const int n_tiles = left < job.tiles_each ? left : job.tiles_each;
     // This kernel ends after the pass, so that whatever waits for it has waited for both.
     if (n_tiles <= 0) {
-        if (!late && p.beside) ptx::grid_dependency_wait();
+        if (p.beside) ptx::grid_dependency_wait();
         return;
     }
     if (warp == U_WARPS) {
@@ -458,6 +458,7 @@ __global__ void __launch_bounds__(U_THREADS, 1) sum_tiles(const __grid_constant_
     }
     __syncthreads();
     if (tid < n) steps[tid] &= 255;
+    if (late && p.beside) ptx::grid_dependency_wait();  // for dh
     __syncthreads();
     const uint32_t tmem = *slot;
     const auto run = [&](auto sum) {
@@ -481,11 +482,39 @@ __global__ void __launch_bounds__(U_THREADS, 1) sum_tiles(const __grid_constant_
     if (!late && p.beside) ptx::grid_dependency_wait();
 }
 
-constexpr int J_THREADS = 256;
+constexpr int J_THREADS = 256, J_SLICES = 8;
+
+// The sum of an adapter's parts, V of type T at a time; parts first .. first + n - 1 in order.  From eight parts on a block's warps take an eighth of them each,
+// all on their way at once, and the eighths are added in order.
+template <typename T, typename Add>
+__device__ __forceinline__ void join_parts_of(const SumJob& job, float* out, int64_t size, int first, int n, T* eighths, const Add& add)
+{
+    constexpr int V = sizeof(T) / 4;
+    const int slices = n >= J_SLICES ? J_SLICES : 1, per = J_THREADS / slices, slice = threadIdx.x / per, lane = threadIdx.x - slice * per;
+    const int q0 = n * slice / slices, q1 = n * (slice + 1) / slices;
+    for (int64_t i0 = static_cast<int64_t>(blockIdx.x) * per; i0 < size / V; i0 += static_cast<int64_t>(gridDim.x) * per) {
+        const int64_t i = i0 + lane;
+        T v{};
+        if (i < size / V)
+#pragma unroll 8
+            for (int q = q0; q < q1; ++q)  // an adapter that begins in a piece has the second of its parts there, one that goes on the first
+                v = add(v, reinterpret_cast<const T*>(job.part + (2 * static_cast<int64_t>(first + q) + (q == 0)) * size)[i]);
+        if (slices > 1) {
+            __syncthreads();
+            eighths[threadIdx.x] = v;
+            __syncthreads();
+            if (slice == 0)
+#pragma unroll
+                for (int k = 1; k < J_SLICES; ++k) v = add(v, eighths[k * per + lane]);
+        }
+        if (slice == 0 && i < size / V) reinterpret_cast<T*>(out)[i] = v;
+    }
+}
 
 // Adds the pieces' parts of adapters that lie in more than one, in the pieces' order, and clears those without rows.
 __global__ void __launch_bounds__(J_THREADS) join_sums(const __grid_constant__ SumParams p)
 {
+    __shared__ float4 eighths[J_THREADS];
     ptx::grid_dependency_wait();
     for (int j = 0; j < 2; ++j) {
         const SumJob& job = p.jobs[j];
@@ -493,74 +522,76 @@ __global__ void __launch_bounds__(J_THREADS) join_sums(const __grid_constant__ S
         const int64_t size = static_cast<int64_t>(p.rank) * job.cols;
         for (int e = blockIdx.y; e < p.adapters; e += gridDim.y) {
             const int t0 = p.plan.tile_starts[e], t1 = p.plan.tile_starts[e + 1];
-            const int first = t0 / p.tiles_each, last = (t1 - 1) / p.tiles_each;
-            if (t1 > t0 && first == last) continue;
+            const int first = t0 / job.tiles_each, n = t1 > t0 ? (t1 - 1) / job.tiles_each - first + 1 : 0;
+            if (n == 1) continue;
             float* out = job.out + e * size;
-            if (job.join_vec) {
-                for (int64_t i = static_cast<int64_t>(blockIdx.x) * J_THREADS + threadIdx.x; i < size / 4; i += static_cast<int64_t>(gridDim.x) * J_THREADS) {
-                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-                    if (t1 > t0) {
-                        v = reinterpret_cast<const float4*>(job.part + (2 * first + 1) * size)[i];
-#pragma unroll 8
-                        for (int q = first + 1; q <= last; ++q) {
-                            const float4 u = reinterpret_cast<const float4*>(job.part + 2 * static_cast<int64_t>(q) * size)[i];
-                            v = make_float4(v.x + u.x, v.y + u.y, v.z + u.z, v.w + u.w);
-                        }
-                    }
-                    reinterpret_cast<float4*>(out)[i] = v;
-                }
-            } else {
-                for (int64_t i = static_cast<int64_t>(blockIdx.x) * J_THREADS + threadIdx.x; i < size; i += static_cast<int64_t>(gridDim.x) * J_THREADS) {
-                    float v = 0.f;
-                    if (t1 > t0) {
-                        v = job.part[(2 * first + 1) * size + i];
-#pragma unroll 8
-                        for (int q = first + 1; q <= last; ++q) v += job.part[2 * static_cast<int64_t>(q) * size + i];
-                    }
-                    out[i] = v;
-                }
-            }
+            if (job.join_vec)
+                join_parts_of(job, out, size, first, n, eighths, [](float4 a, float4 b) { return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w); });
+            else
+                join_parts_of(job, out, size, first, n, reinterpret_cast<float*>(eighths), [](float a, float b) { return a + b; });
         }
     }
 }
 
-// How many tiles a CTA takes: as few as fill the SMs in whole waves, against some 4 us that a CTA costs beside its tiles' 1.2 us each.
-int sum_tiles_each(int64_t rows, int64_t adapters, int rank, int64_t cols, int64_t outs)
+// How many tiles a CTA takes for each gradient: as few as fill the SMs in whole waves, against some 4 us that a CTA costs beside its tiles'
+// 1.2 us each (that of ranks up to 64; above, 3.5 would suit some sizes and spoil others): both gradients together, as where the pass leaves no SMs free, and
+// then da's, which waits for the pass, once more.  12544 x 256 -> 1024, rank 16: 32.4 us, with the same pieces for both 36.9.
+SumShape shape_sums(int64_t rows, int64_t adapters, int rank, int64_t cols, int64_t outs)
 {
     const SumSmem s(rank);
-    const int64_t tiles = rows / TILE + (adapters < rows ? adapters : rows) / 2 + 1;
-    const int64_t blocks = mx::cdiv<int64_t>(cols, 128 * s.blocks) + mx::cdiv<int64_t>(outs, 128 * s.blocks);
-    int best = 1;
-    double best_us = 1e30;
-    for (int each = 1; each <= SUM_TILES; ++each) {
-        const double us = static_cast<double>(mx::cdiv<int64_t>(mx::cdiv<int64_t>(tiles, each) * blocks, mx::SMS)) * (4.0 + 1.2 * each);
-        if (us < best_us) best = each, best_us = us;
+    const int64_t tiles = tiles_about(rows, adapters, TILE);
+    const int most = static_cast<int>(tiles < SUM_TILES ? tiles : SUM_TILES);
+    int64_t a_ctas[SUM_TILES + 1], b_ctas[SUM_TILES + 1];
+    for (int i = 1; i <= most; ++i) {
+        const int64_t pieces = mx::cdiv<int64_t>(tiles, i);
+        a_ctas[i] = pieces * mx::cdiv<int64_t>(cols, 128 * s.blocks);
+        b_ctas[i] = pieces * mx::cdiv<int64_t>(outs, 128 * s.blocks);
     }
+    const auto waves = [](int64_t ctas) { return mx::cdiv<int64_t>(ctas, mx::SMS); };
+    const auto time = [](int each) { return 4.0 + 1.2 * each; };
+    SumShape best{1, 1};
+    double best_us = 1e30;
+    for (int a = 1; a <= most; ++a) {
+        const double own = static_cast<double>(waves(a_ctas[a])) * time(a);
+        if (own >= best_us) continue;
+        for (int b = a; b <= most; ++b) {  // fewer for db than for da do not shorten the two
+            const double us = static_cast<double>(waves(a_ctas[a] + b_ctas[b])) * time(b) + own;
+            if (us < best_us) best = {a, b}, best_us = us;
+        }
+    }
+    // but cost nothing where they need no further wave, together or alone
+    const int64_t whole = waves(a_ctas[best.da] + b_ctas[best.db]), alone = waves(b_ctas[best.db]);
+    while (best.db > 1 && waves(a_ctas[best.da] + b_ctas[best.db - 1]) == whole && waves(b_ctas[best.db - 1]) == alone) --best.db;
     return best;
 }
 
 int64_t sum_pieces(const PlanLayout& l, int tiles_each) { return mx::cdiv<int64_t>(l.tiles, tiles_each); }
 
-int launch_sums(SumParams& p, int64_t pieces, cudaStream_t stream)
+int launch_sums(SumParams& p, const PlanLayout& l, cudaStream_t stream)
 {
     static std::atomic<uint64_t> done{0};
     const SumSmem s(p.rank);
     int64_t most = 0, ctas = 0;
+    bool many = false;  // parts to an adapter
     for (SumJob& job : p.jobs) {
         job.col_blocks = job.out ? mx::cdiv(job.cols, 128 * s.blocks) : 0;
-        ctas += pieces * job.col_blocks;
+        if (job.out) {
+            ctas += sum_pieces(l, job.tiles_each) * job.col_blocks;
+            many = many || sum_pieces(l, job.tiles_each) >= J_SLICES * p.adapters;
+        }
         const int64_t size = static_cast<int64_t>(p.rank) * job.cols;
         job.mid_vec = p.rank % 4 == 0 && reinterpret_cast<uintptr_t>(job.mid) % 16 == 0;
         job.out_vec = p.rank % 4 == 0 && reinterpret_cast<uintptr_t>(job.out) % 16 == 0;
         job.join_vec = size % 4 == 0 && (reinterpret_cast<uintptr_t>(job.out) | reinterpret_cast<uintptr_t>(job.part)) % 16 == 0;
-        if (job.out && size > most) most = size;
+        const int64_t units = job.join_vec ? size / 4 : size;
+        if (job.out && units > most) most = units;
     }
     if (ctas == 0) return CONV2D_OK;
     if (ctas > INT32_MAX) return CONV2D_ERR_UNSUPPORTED;
-    p.first_late = static_cast<int>(pieces * p.jobs[1].col_blocks);
+    p.first_late = p.jobs[1].out ? static_cast<int>(sum_pieces(l, p.jobs[1].tiles_each) * p.jobs[1].col_blocks) : 0;
     if (!mx::allow_smem(sum_tiles, 227 * 1024, done)) return CONV2D_ERR_CUDA;
     if (mx::launch(sum_tiles, ctas, U_THREADS, s.bytes(), stream, 1, p) != cudaSuccess) return CONV2D_ERR_CUDA;
-    const int64_t across = mx::cdiv<int64_t>(most, 4 * J_THREADS);
+    const int64_t across = mx::cdiv<int64_t>(most, many ? J_THREADS / J_SLICES : J_THREADS);
     const dim3 grid(static_cast<unsigned>(across < 4 * mx::SMS ? across : 4 * mx::SMS), static_cast<unsigned>(p.adapters < 8 ? p.adapters : 8));
     return mx::launch(join_sums, grid, J_THREADS, 0, stream, 1, p) == cudaSuccess ? CONV2D_OK : CONV2D_ERR_CUDA;
 }
