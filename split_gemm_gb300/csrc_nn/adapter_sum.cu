@@ -14,7 +14,7 @@
 // in's rows keep their 128-byte lines (128-byte swizzle: copies that spread a line over shared memory are half as fast); mid's parts lie in core matrices of 8
 // rows x 16 bytes, each column of them 16 bytes longer than it needs to be, so that neighbours fall into different banks.
 //
-// bf16 rows come by cp.async into the operand's place, one stage ahead (ranks up to 128) to three (16); checkpoints, rows that are not whole vectors, and mid come through
+// bf16 rows come by cp.async into the operand's place, ahead by all the stages that shared memory holds but two; checkpoints, rows that are not whole vectors, and mid come through
 // registers, one or two stages ahead.  A checkpoint's integer becomes a bf16 number by bits: (m | 128) - 128 or 256, each with the scale in its exponent.
 //
 // db needs nothing of the pass before it, and its CTAs run beside that pass where it leaves SMs free; da's, which take dh, wait for it.  Both gradients of

@@ -494,3 +494,16 @@ def test_another_device_or_stream_is_refused(sg):
     for workspace in (torch.zeros(need, dtype=torch.uint8), torch.zeros(1, dtype=torch.uint8, device="cuda").expand(need)):
         with pytest.raises(ValueError, match="workspace"):
             sg.adapter_bwd(c["dy"], c["x"], h, c["a"], c["b"], plan, workspace=workspace)
+
+
+@pytest.mark.parametrize("rows,cols,outs,rank", [(1, 64, 72, 8), (20, 200, 136, 16), (37, 33, 71, 5), (700, 256, 1000, 32), (900, 101, 333, 7)])
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_forward_in_place(sg, rows, cols, outs, rank, dtype):
+    """out = y: the bits of another out, rows without an adapter among them."""
+    c, index = _cuda(_case(rows, cols, outs, rank, 3)), _index(rows, 3).cuda()
+    plan = sg.adapter_plan(index, 3)
+    y = c["y"].to(dtype)
+    want, h = sg.adapter_fwd(y, c["x"], c["a"], c["b"], plan, c["scale"], relu=True)
+    kept = torch.empty_like(h)
+    sg.adapter_fwd_into(y, y, c["x"], c["a"], c["b"], plan, c["scale"], h=kept, relu=True)
+    assert torch.equal(y, want) and torch.equal(kept, h)
