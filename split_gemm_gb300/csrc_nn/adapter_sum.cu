@@ -141,7 +141,7 @@ struct Sum {
         } else {
             float* v = reinterpret_cast<float*>(h.mid);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) v[i] = r >= 0 && 8 * mid_rank + i < p.rank ? __ldg(m + i) : 0.f;
+            for (int i = 0; i < 8; ++i) v[i] = r >= 0 && 8 * mid_rank + i < p.rank ? m[i] : 0.f;  // dh, which the pass beside writes: no __ldg
         }
     }
 
