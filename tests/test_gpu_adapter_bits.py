@@ -106,3 +106,55 @@ def test_dh_of_ranks_that_are_not_whole_vectors(sg, shape, x_type):
     for _ in range(3):
         for got, want in zip(*_grads(sg, *shape, x_type)):
             _same(got, want)
+
+
+# One token to many tiles, each way that rows are cut up: few rows (rank up to 64), tiles of 64 and of 128 rows, clusters of 1 to 8; whole vectors
+# and not; 8 to 128 ranks, odd numbers of sixteens and eights among them; one stage of a sum and many, odd numbers and even
+SHAPES = [(1, 64, 136, 16, 1), (9, 1001, 72, 33, 2), (40, 200, 96, 24, 3), (300, 96, 264, 16, 4), (160, 72, 200, 64, 3),
+          (700, 256, 520, 32, 3), (641, 101, 333, 17, 3), (161, 72, 200, 64, 1), (129, 136, 264, 100, 3), (5, 4096, 512, 128, 2), (130, 64, 392, 128, 2),
+          (1500, 136, 200, 72, 2), (1300, 1001, 136, 20, 2), (2049, 64, 136, 64, 1), (3000, 384, 384, 48, 2), (2500, 72, 333, 90, 5), (12544, 64, 128, 16, 1)]
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("scaled", [True, False])
+def test_forward(sg, shape, scaled):
+    """out = b h where h has 24 bits: an odd weight times an odd scale, or two of x's columns whose products lie 2^15 apart."""
+    rows, cols, outs, rank, adapters = shape
+    d = Draw(rows + 3 * cols + 5 * outs + 7 * rank)
+    index = d.index(rows, adapters) if rows > 1 else torch.zeros(1, dtype=torch.long)
+    a = d.odd(129, 255, adapters, rank, cols)
+    b = torch.stack([d.one_of_each(outs, rank) for _ in range(adapters)])
+    x, scale = d.one_hot(rows, cols), None
+    if scaled:
+        scale = d.odd(32769, 65535, adapters) / 65536
+    else:  # the second column of a row: some other one, its value 2^-15 of the first's
+        at = x.abs().argmax(1, keepdim=True)
+        x = x.scatter(1, (at + 1 + torch.randint(cols - 1, (rows, 1), generator=d.g)) % cols, x.gather(1, at) * 2.0 ** -15)
+    h = _by_adapter(x, a.transpose(1, 2).double() * (1.0 if scale is None else scale.double()[:, None, None]), index)
+    assert (h.float().double() == h).all() and (_third_part(h.numpy()) != 0).mean() > 0.9
+    plan = sg.adapter_plan(index.int().cuda(), adapters)
+    out, got_h = sg.adapter_fwd(torch.zeros(rows, outs).cuda(), x.to(BF16).cuda(), a.to(BF16).cuda(), b.to(BF16).cuda(), plan,
+                                None if scale is None else scale.cuda())
+    _same(got_h, h)
+    _same(out, _by_adapter(h, b.transpose(1, 2), index))
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+@pytest.mark.parametrize("x_type", ["bf16", "int8"])
+def test_dx_and_da(sg, shape, x_type):
+    for got, want in zip(*_grads(sg, *shape, x_type)):
+        _same(got, want)
+
+
+@pytest.mark.parametrize("shape", SHAPES)
+def test_db(sg, shape):
+    """h of 24 bits that no other row, rank or part of one has; dy with one row of each adapter to a column."""
+    rows, cols, outs, rank, adapters = shape
+    d = Draw(rows + 3 * cols + 5 * outs + 7 * rank)
+    index = d.index(rows, adapters)
+    h, dy = d.odd(2 ** 23, 2 ** 24 - 1, rows, rank), d.one_row_to_a_column(index, adapters, outs)
+    assert (_third_part(h.numpy()) != 0).all()
+    zeros = torch.zeros(adapters, rank, cols, dtype=BF16).cuda(), torch.zeros(adapters, outs, rank, dtype=BF16).cuda()
+    db = sg.adapter_bwd(dy.to(BF16).cuda(), torch.zeros(rows, cols, dtype=BF16).cuda(), h.cuda(), *zeros,
+                        sg.adapter_plan(index.int().cuda(), adapters))[2]
+    _same(db, _sums(dy, h, index, adapters))
