@@ -20,37 +20,6 @@ constexpr int64_t MOST_COLS = int64_t(1) << 30;
 
 size_t size_of(int32_t t) { return t == CONV2D_OUT_BF16 ? 2 : 4; }
 
-// How a pass is cut up: tiles of 128 or 64 rows, and the CTAs that share one, one CTA to an SM.  A CTA costs some 3 us beside its rows, 3 more where sums
-// are joined over a cluster, and takes its bytes at 60 a ns at best (12 where they are not whole vectors) and at its share of HBM's 6600; weights come
-// from L2.
-bool shape_pass(PassParams& p, int64_t rows, int base_bytes, int out_bytes, bool vec)
-{
-    bool halved = false;
-    double best = 1e30;
-    for (int h = 0; h < 2; ++h)
-        for (int splits = 1; splits <= 8; splits *= 2) {
-            const int parts = static_cast<int>(mx::cdiv<int64_t>(p.from, P_STEP)), chunks = static_cast<int>(mx::cdiv<int64_t>(p.to, P_COLS));
-            if (splits > 1 && splits > parts && splits > chunks) break;
-            const int tile = TILE >> h;
-            const int64_t ctas = tiles_about(rows, p.adapters, tile) * splits;
-            const double held = splits == 8 ? 120.0 : splits == 4 ? 144.0 : 152.0;  // CTAs of clusters that the SMs hold at once
-            const double waves = static_cast<double>(mx::cdiv<int64_t>(ctas, static_cast<int64_t>(held)));
-            const double on = static_cast<double>(ctas) < held ? static_cast<double>(ctas) : held;
-            const double from = static_cast<double>(p.from) / (splits < parts ? splits : parts), to = static_cast<double>(p.to) / (splits < chunks ? splits : chunks);
-            const double bytes = tile * (2.0 * from + (base_bytes + out_bytes) * to);
-            const double weights = 2.0 * p.rank * (from + to);
-            const double fast = vec ? 60.0 : 12.0, rate = 6600.0 / on < fast ? 6600.0 / on : fast;
-            const double own = (bytes + weights) / fast / 1000.0, hbm = bytes / rate / 1000.0;
-            const double us = waves * (3.0 + (splits > 1 ? 3.0 : 0.0) + (own > hbm ? own : hbm));
-            if (us < best) {
-                best = us;
-                halved = h;
-                p.splits = splits;
-            }
-        }
-    return halved;
-}
-
 bool vectors(const void* p, int64_t stride, size_t elem) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && stride * elem % 16 == 0; }
 
 // Whether every row that the pass touches is whole 16-byte vectors.
@@ -70,9 +39,9 @@ size_t part_bytes(const adapter_bwd_params& q, int64_t cols, int tiles_each)
     return (2 * static_cast<size_t>(pieces) * q.rank * static_cast<size_t>(cols) * 4 + 15) / 16 * 16;
 }
 
-SumShape shape_sums(const adapter_bwd_params& q) { return shape_sums(q.rows, q.adapters, static_cast<int>(q.rank), q.cols, q.outs); }
+SumCut cut_sums(const adapter_bwd_params& q) { return cut_sums(q.rows, q.adapters, static_cast<int>(q.rank), q.cols, q.outs); }
 
-size_t bwd_bytes(const adapter_bwd_params& q, const SumShape& each)
+size_t bwd_bytes(const adapter_bwd_params& q, const SumCut& each)
 {
     return dh_bytes(q.rows, q.rank) + part_bytes(q, q.cols, each.da) + part_bytes(q, q.outs, each.db);
 }
@@ -139,14 +108,15 @@ extern "C" int adapter_fwd(const adapter_fwd_params* params, const void* plan_de
     if (q.rows * mx::cdiv<int64_t>(q.rank, 16) <= ad::SMALL_ROWS && q.rank <= 64)
         return ad::launch_small_fwd(p, q.y_dtype, q.out_dtype, ad::in_vectors(p, q.y_dtype, q.out_dtype), stream);
     const bool vec = ad::in_vectors(p, q.y_dtype, q.out_dtype);
-    const bool halved = ad::shape_pass(p, q.rows, static_cast<int>(ad::size_of(q.y_dtype)), static_cast<int>(ad::size_of(q.out_dtype)), vec);
-    return ad::launch_pass_fwd(p, q.y_dtype, q.out_dtype, vec, halved, stream);
+    const ad::PassCut cut = ad::cut_pass(q.rows, p.adapters, p.rank, p.from, p.to, static_cast<int>(ad::size_of(q.y_dtype)), static_cast<int>(ad::size_of(q.out_dtype)), vec);
+    p.splits = cut.splits;
+    return ad::launch_pass_fwd(p, q.y_dtype, q.out_dtype, vec, cut.halved, stream);
 }
 
 extern "C" size_t adapter_bwd_workspace_bytes(const adapter_bwd_params* params)
 {
     if (!params || ad::check(params->rows, params->cols, params->outs, params->rank, params->adapters)) return 0;
-    return ad::bwd_bytes(*params, ad::shape_sums(*params));
+    return ad::bwd_bytes(*params, ad::cut_sums(*params));
 }
 
 extern "C" int adapter_bwd(const adapter_bwd_params* params, const void* plan_dev, const void* dy_dev, const void* x_dev,
@@ -162,7 +132,7 @@ extern "C" int adapter_bwd(const adapter_bwd_params* params, const void* plan_de
         (dx_dev && q.dx_stride < q.cols) || (dx0_dev && q.dx0_stride < q.cols) || (!eight && da_dev && q.x_stride < q.cols))
         return CONV2D_ERR_INVALID;
     if (!ad::aligned(da_dev, CONV2D_OUT_F32) || !ad::aligned(db_dev, CONV2D_OUT_F32)) return CONV2D_ERR_ALIGNMENT;
-    ad::SumShape each{1, 1};
+    ad::SumCut each{1, 1};
     if (q.rows > 0) {
         if (!plan_dev || !dy_dev || !a_dev || !b_dev || (da_dev && (!x_dev || (eight && !x_scales_dev))) || (db_dev && !h_dev))
             return CONV2D_ERR_INVALID;
@@ -171,7 +141,7 @@ extern "C" int adapter_bwd(const adapter_bwd_params* params, const void* plan_de
             !ad::aligned(a_dev, CONV2D_OUT_BF16) || !ad::aligned(b_dev, CONV2D_OUT_BF16) || !ad::aligned(scale_dev, CONV2D_OUT_F32) ||
             !ad::aligned(dx0_dev, q.dx0_dtype) || !ad::aligned(dx_dev, q.dx_dtype))
             return CONV2D_ERR_ALIGNMENT;
-        each = ad::shape_sums(q);
+        each = ad::cut_sums(q);
         const size_t need = ad::bwd_bytes(q, each);
         if (need && (!workspace_dev || workspace_bytes < need)) return CONV2D_ERR_WORKSPACE;
     } else {
@@ -198,10 +168,11 @@ extern "C" int adapter_bwd(const adapter_bwd_params* params, const void* plan_de
     p.to = static_cast<int>(q.cols);
     if (!ad::status_word(&p.status)) return CONV2D_ERR_CUDA;
     const bool vec = ad::in_vectors(p, q.dx0_dtype, q.dx_dtype);
-    const bool halved = ad::shape_pass(p, q.rows, dx0_dev ? static_cast<int>(ad::size_of(q.dx0_dtype)) : 0, dx_dev ? static_cast<int>(ad::size_of(q.dx_dtype)) : 0, vec);
+    const ad::PassCut cut = ad::cut_pass(q.rows, p.adapters, p.rank, p.from, p.to, dx0_dev ? static_cast<int>(ad::size_of(q.dx0_dtype)) : 0, dx_dev ? static_cast<int>(ad::size_of(q.dx_dtype)) : 0, vec);
+    p.splits = cut.splits;
     p.early = da_dev || db_dev;
     if (dx_dev || da_dev)
-        if (int rc = ad::launch_pass_bwd(p, q.dx0_dtype, q.dx_dtype, vec, halved, stream)) return rc;
+        if (int rc = ad::launch_pass_bwd(p, q.dx0_dtype, q.dx_dtype, vec, cut.halved, stream)) return rc;
     ad::SumParams s{};
     s.plan = p.plan;
     s.status = p.status;

@@ -25,16 +25,7 @@ struct PassParams {
     int early;   // the next kernel may start: it waits itself for what it needs of this one
 };
 
-// About how many pieces of up to `tile` rows there are: one to an adapter at least, and half a piece more to each than its rows fill.
-inline int64_t tiles_about(int64_t rows, int64_t groups, int tile)
-{
-    groups = groups < rows ? groups : rows;
-    const int64_t filled = rows / tile + (groups + 1) / 2;
-    return filled > groups ? filled : groups;
-}
-
-constexpr int P_BLOCK = 64, P_STEP = 2 * P_BLOCK;  // of `from`: in a block of operands, and in a stage
-constexpr int P_COLS = 128;                        // of `to`, in a chunk
+constexpr int P_BLOCK = P_STEP / 2;  // of `from`: in a block of operands
 constexpr int P_MOST_STAGES = 4, P_MOST_CHUNKS = 8;
 constexpr int P_ROOM = 227 * 1024;  // bytes of shared memory
 
@@ -96,12 +87,6 @@ struct SumParams {
     int beside;      // that pass lets this kernel start early
 };
 
-constexpr int SUM_TILES = 32;  // of a piece, at most
-
-struct SumShape {
-    int da, db;  // tiles to a piece
-};
-SumShape shape_sums(int64_t rows, int64_t adapters, int rank, int64_t cols, int64_t outs);
 int64_t sum_pieces(const PlanLayout& l, int tiles_each);
 int launch_sums(SumParams& p, const PlanLayout& l, cudaStream_t stream);
 

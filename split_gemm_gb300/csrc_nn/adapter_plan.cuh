@@ -9,12 +9,13 @@
 //   counts [units][adapters + 1]   scratch of its making
 #pragma once
 
+#include "adapter_cuts.h"
 #include "mx_common.cuh"
 
 namespace sgb {
 namespace ad {
 
-constexpr int TILE = 128;
+static_assert(CARD_SMS == mx::SMS);
 constexpr int SMALL = 8;
 constexpr int64_t SMALL_ROWS = 640;
 constexpr int64_t MOST_ROWS = (int64_t(1) << 31) - (1 << 16), MOST_ADAPTERS = 65535;

@@ -37,7 +37,7 @@ constexpr uint64_t U_WAIT_NS = 1000000000ull;
 // Shared memory of a stage of `tokens` rows: in by lines of 64 columns, then mid's parts, `column` bytes to a 16-byte column.
 struct SumSmem {
     int rp, tokens, blocks;  // blocks of 128 columns
-    __host__ __device__ constexpr SumSmem(int rank) : rp((rank + 15) / 16 * 16), tokens(rp <= 64 ? 64 : 32), blocks(rp <= 64 ? 2 : 1) {}
+    __host__ __device__ constexpr SumSmem(int rank) : rp((rank + 15) / 16 * 16), tokens(rp <= 64 ? 64 : 32), blocks(sum_blocks(rank)) {}
     __host__ __device__ constexpr int column() const { return tokens * 16 + 16; }
     __host__ __device__ constexpr int lines() const { return tokens * 128; }  // of 64 columns
     __host__ __device__ constexpr int in_bytes() const { return 2 * blocks * lines(); }
@@ -531,38 +531,6 @@ __global__ void __launch_bounds__(J_THREADS) join_sums(const __grid_constant__ S
                 join_parts_of(job, out, size, first, n, reinterpret_cast<float*>(eighths), [](float a, float b) { return a + b; });
         }
     }
-}
-
-// How many tiles a CTA takes for each gradient: as few as fill the SMs in whole waves, against some 4 us that a CTA costs beside its tiles'
-// 1.2 us each (that of ranks up to 64; above, 3.5 would suit some sizes and spoil others): both gradients together, as where the pass leaves no SMs free, and
-// then da's, which waits for the pass, once more.  12544 x 256 -> 1024, rank 16: 32.4 us, with the same pieces for both 36.9.
-SumShape shape_sums(int64_t rows, int64_t adapters, int rank, int64_t cols, int64_t outs)
-{
-    const SumSmem s(rank);
-    const int64_t tiles = tiles_about(rows, adapters, TILE);
-    const int most = static_cast<int>(tiles < SUM_TILES ? tiles : SUM_TILES);
-    int64_t a_ctas[SUM_TILES + 1], b_ctas[SUM_TILES + 1];
-    for (int i = 1; i <= most; ++i) {
-        const int64_t pieces = mx::cdiv<int64_t>(tiles, i);
-        a_ctas[i] = pieces * mx::cdiv<int64_t>(cols, 128 * s.blocks);
-        b_ctas[i] = pieces * mx::cdiv<int64_t>(outs, 128 * s.blocks);
-    }
-    const auto waves = [](int64_t ctas) { return mx::cdiv<int64_t>(ctas, mx::SMS); };
-    const auto time = [](int each) { return 4.0 + 1.2 * each; };
-    SumShape best{1, 1};
-    double best_us = 1e30;
-    for (int a = 1; a <= most; ++a) {
-        const double own = static_cast<double>(waves(a_ctas[a])) * time(a);
-        if (own >= best_us) continue;
-        for (int b = a; b <= most; ++b) {  // fewer for db than for da do not shorten the two
-            const double us = static_cast<double>(waves(a_ctas[a] + b_ctas[b])) * time(b) + own;
-            if (us < best_us) best = {a, b}, best_us = us;
-        }
-    }
-    // but cost nothing where they need no further wave, together or alone
-    const int64_t whole = waves(a_ctas[best.da] + b_ctas[best.db]), alone = waves(b_ctas[best.db]);
-    while (best.db > 1 && waves(a_ctas[best.da] + b_ctas[best.db - 1]) == whole && waves(b_ctas[best.db - 1]) == alone) --best.db;
-    return best;
 }
 
 int64_t sum_pieces(const PlanLayout& l, int tiles_each) { return mx::cdiv<int64_t>(l.tiles, tiles_each); }
