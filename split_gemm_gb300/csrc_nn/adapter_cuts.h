@@ -33,9 +33,10 @@ struct PassCut {
 
 // How a pass is cut up: tiles of 128 or 64 rows, and the CTAs that share one, one CTA to an SM.  A CTA costs some 3 us beside its rows, 3 more where sums
 // are joined over a cluster, and takes its bytes at 60 a ns at best (12 where they are not whole vectors) and at its share of HBM's 6600; weights come
-// from L2.
+// from L2.  Without a result (out_bytes = 0) there is the first product alone to share.
 inline PassCut cut_pass(int64_t rows, int64_t adapters, int rank, int from, int to, int base_bytes, int out_bytes, bool vec)
 {
+    if (out_bytes == 0) to = 0;
     PassCut cut{1, false};
     double best = 1e30;
     const int parts = static_cast<int>(blocks_of(from, P_STEP)), chunks = static_cast<int>(blocks_of(to, P_COLS));
@@ -47,7 +48,7 @@ inline PassCut cut_pass(int64_t rows, int64_t adapters, int rank, int from, int 
             const double held = splits == 8 ? 120.0 : splits == 4 ? 144.0 : 152.0;  // CTAs of clusters that the SMs hold at once
             const double waves = static_cast<double>(blocks_of(ctas, static_cast<int64_t>(held)));
             const double on = static_cast<double>(ctas) < held ? static_cast<double>(ctas) : held;
-            const double from_each = static_cast<double>(from) / (splits < parts ? splits : parts), to_each = static_cast<double>(to) / (splits < chunks ? splits : chunks);
+            const double from_each = static_cast<double>(from) / (splits < parts ? splits : parts), to_each = to ? static_cast<double>(to) / (splits < chunks ? splits : chunks) : 0.0;
             const double bytes = tile * (2.0 * from_each + (base_bytes + out_bytes) * to_each);
             const double weights = 2.0 * rank * (from_each + to_each);
             const double fast = vec ? 60.0 : 12.0, rate = 6600.0 / on < fast ? 6600.0 / on : fast;

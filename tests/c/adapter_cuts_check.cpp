@@ -32,6 +32,9 @@ int main()
                         for (const bool vec : {false, true}) {
                             const PassCut p = cut_pass(rows, adapters, rank, static_cast<int>(cols), static_cast<int>(outs), 4, 2, vec);
                             want(p.splits == 1 || p.splits == 2 || p.splits == 4 || p.splits == 8, "splits", rows, adapters, rank, cols, outs);
+                            // without a result there are no more CTAs to a tile than the first product has steps
+                            const PassCut alone = cut_pass(rows, adapters, rank, static_cast<int>(cols), static_cast<int>(outs), 4, 0, vec);
+                            want(alone.splits >= 1 && (alone.splits == 1 || alone.splits <= blocks_of(cols, P_STEP)), "splits of the first product", rows, adapters, rank, cols, outs);
                         }
                     }
     std::printf("%llu checks, %llu wrong\n", checks, bad);
