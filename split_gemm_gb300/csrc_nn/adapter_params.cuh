@@ -10,6 +10,17 @@ namespace ad {
 
 constexpr int MOST_RANK = 128;
 
+// How long a wait may take.  Tests compile the kernels with another time and with barriers that count an arrival which does not come: that of
+// the first stage's rows, or of a product's end.  (As parameters of the kernels these cost 2% of a pass.)
+#ifndef SGB_ADAPTER_WAIT_NS
+#define SGB_ADAPTER_WAIT_NS 1000000000
+#define SGB_ADAPTER_LOST_ROWS 0
+#define SGB_ADAPTER_LOST_DONE 0
+#endif
+constexpr uint64_t WAIT_NS = SGB_ADAPTER_WAIT_NS;
+constexpr int LOST_ROWS = SGB_ADAPTER_LOST_ROWS, LOST_DONE = SGB_ADAPTER_LOST_DONE;
+constexpr uint64_t LAST_WAIT_NS = 1000000000;  // for what a CTA that is done with has in flight
+
 struct PassParams {
     Plan plan;
     const __nv_bfloat16 *in, *w1, *w2;

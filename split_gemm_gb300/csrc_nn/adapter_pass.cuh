@@ -23,7 +23,9 @@
 // Rows that are not whole vectors (VEC = false) come through registers without running ahead, and are finished one row at a time: 777 x 1001 -> 2001
 // of rank 20 takes 20 us, most of it latency (1.7 at HBM's rate).
 //
-// Every wait is bounded: on running out the status word is set and the CTA goes through its remaining barriers without waiting or storing.
+// Every wait is bounded.  A thread whose wait has run out waits no more and goes on with whatever is in memory: the status word is set, and what the call
+// stores, within its results, is undefined.  It waits again, as long at most, for what its cluster sends it, and the CTA for its MMAs, before the memory that these read and
+// write is given up.
 #pragma once
 
 #include "adapter_params.cuh"
@@ -35,7 +37,6 @@ namespace ad {
 
 constexpr int P_W2_WARPS = 3, P_W2_THREADS = 32 * P_W2_WARPS;  // that bring w2's chunks
 constexpr int P_THREADS = P_LOADERS + 32 + P_W2_THREADS;
-constexpr uint64_t P_WAIT_NS = 1000000000ull;
 constexpr uint32_t P_TMEM = 512;  // the first product's sums, then 256 columns of chunks; mid's parts at the end
 
 template <bool TRANS, bool VEC, int HALVED, typename TB, typename TO>
@@ -47,10 +48,9 @@ struct Pass {
     const PassParams& p;
     const PassSmem s;
     uint8_t* mem;
-    uint64_t *full, *empty, *done, *w2_full, *w2_empty, *d_full, *d_empty, *mid_full;
+    uint64_t *full, *empty, *done, *w2_full, *w2_empty, *d_full, *d_empty, *mid_full, *last;
     int* ids;  // numbers of the tile's rows
     uint32_t* slot;
-    volatile uint32_t* abort_flag;
     int tid, warp, lane, rank_in, e, n_stages, n_bufs;
     int group;  // of two that finish chunks by turns
 
@@ -68,22 +68,19 @@ struct Pass {
         d_full = w2_empty + P_MOST_CHUNKS;
         d_empty = d_full + BUFS;
         mid_full = d_empty + BUFS;
-        ids = reinterpret_cast<int*>(mid_full + 1);
+        last = mid_full + 1;
+        ids = reinterpret_cast<int*>(last + 1);
         slot = reinterpret_cast<uint32_t*>(ids + TILE);
-        abort_flag = slot + 1;
         tid = threadIdx.x;
         warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // the same in all lanes, as the compiler then knows
         lane = tid & 31;
         rank_in = blockIdx.x % p.splits;
         group = warp >> 3;
     }
-    // Once a wait has run out, `ok` is false and the thread waits no more: it goes on through its barriers with whatever is in memory.
+    // Once a wait has run out, `ok` is false and the thread waits no more.
     __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, bool& ok) const
     {
-        if (!ptx::mbar_try_wait(bar, parity) && ok && !ptx::mbar_wait(bar, parity, P_WAIT_NS)) {
-            ok = false;
-            *abort_flag = 1u;
-        }
+        if (!ptx::mbar_try_wait(bar, parity) && ok && !ptx::mbar_wait(bar, parity, WAIT_NS)) ok = false;
     }
     __device__ __forceinline__ float* mids() const { return reinterpret_cast<float*>(mem + s.area() - s.sums()); }
     __device__ __forceinline__ uint8_t* w2_buf(int i) const { return i ? mem + s.area() - s.ring() - i * s.chunk() : mem + s.area(); }
@@ -561,10 +558,10 @@ struct Pass {
     {
         if (tid == 0) {
             for (int i = 0; i < n_stages; ++i) {
-                ptx::mbar_init(&full[i], P_WARPS);
+                ptx::mbar_init(&full[i], i == 0 ? P_WARPS + LOST_ROWS : P_WARPS);
                 ptx::mbar_init(&empty[i], 1);
             }
-            ptx::mbar_init(done, 1);
+            ptx::mbar_init(done, 1 + LOST_DONE);
             for (int i = 0; i < n_bufs; ++i) {
                 ptx::mbar_init(&w2_full[i], P_W2_WARPS);
                 ptx::mbar_init(&w2_empty[i], 1);
@@ -574,8 +571,8 @@ struct Pass {
                 ptx::mbar_init(&d_empty[i], P_WARPS / 2);
             }
             ptx::mbar_init(mid_full, 1);
+            ptx::mbar_init(last, 1);
             if (p.splits > 1) ptx::mbar_arrive_expect_tx(mid_full, (ROWS - ROWS / p.splits) * s.pitch() * 4);
-            *abort_flag = 0u;
             ptx::mbar_init_fence();
         }
         if (warp == P_WARPS) {
@@ -735,9 +732,10 @@ struct Pass {
             case 4: join<4>(sums, scale); break;
             default: join<8>(sums, scale); break;
         }
-        // All of mid is here: none of this CTA's peers reads its sums any more, and what they sent has come.
+        // All of mid is here: none of this CTA's peers reads its sums any more, and what they sent has come.  Every thread waits for that, also after a wait
+        // that has run out, as the peers send in any case, and no memory that they send to or from may be given up.
         if (p.splits > 1) {
-            wait(mid_full, 0, ok);
+            if (!ptx::mbar_wait(mid_full, 0, LAST_WAIT_NS)) ok = false;
             __syncwarp();
             ptx::cluster_arrive_relaxed();
         }
@@ -773,6 +771,9 @@ struct Pass {
                 buf = buf + 1 == n_bufs ? 0 : buf + 1;
                 phase = buf ? phase : phase ^ 1u;
             }
+            // The CTA lives until its MMAs have ended, whatever waits have run out.
+            ptx::mma_commit_elect(last);
+            if (!ptx::mbar_wait(last, 0, LAST_WAIT_NS)) ok = false;
         } else if (warp > P_WARPS) {
             // the word of each a chunk later
             if (n > 1 && s.late()) bring_w2(1, (chunk0 + 1) * COLS, ok);

@@ -32,7 +32,6 @@ namespace ad {
 
 constexpr int U_WARPS = 16, U_LOADERS = 32 * U_WARPS, U_THREADS = U_LOADERS + 32;
 constexpr int U_STAGES = 6;  // at most
-constexpr uint64_t U_WAIT_NS = 1000000000ull;
 
 // Shared memory of a stage of `tokens` rows: in by lines of 64 columns, then mid's parts, `column` bytes to a 16-byte column.
 struct SumSmem {
@@ -62,17 +61,13 @@ struct Sum {
     uint8_t* mem;
     const int *ids, *steps;  // by stage: its rows' numbers (-1: none), its tile
     const Piece* tiles;
-    uint64_t *full, *empty, *done, *free_;
-    volatile uint32_t* abort_flag;
+    uint64_t *full, *empty, *done, *free_, *last;
     int tid, warp, lane, c0, n, piece;
 
     // As in the pass: once a wait has run out, the thread waits no more.
     __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, bool& ok) const
     {
-        if (!ptx::mbar_try_wait(bar, parity) && ok && !ptx::mbar_wait(bar, parity, U_WAIT_NS)) {
-            ok = false;
-            *abort_flag = 1u;
-        }
+        if (!ptx::mbar_try_wait(bar, parity) && ok && !ptx::mbar_wait(bar, parity, WAIT_NS)) ok = false;
     }
     __device__ __forceinline__ int adapter_at(int k) const { return tiles[steps[k]].adapter; }
     __device__ __forceinline__ bool ends_run(int k) const { return k + 1 == n || adapter_at(k + 1) != adapter_at(k); }
@@ -348,7 +343,7 @@ struct Sum {
                 }
             }
         if constexpr (MODE == 0) ptx::cp_async_wait_all();
-        if (!ok && p.status) atomicMax(p.status, 6u);
+        if (!ok) atomicMax(p.status, 6u);
     }
 
     __device__ __forceinline__ void multiply(uint32_t tmem)
@@ -389,6 +384,9 @@ struct Sum {
                 ++runs;
             }
         }
+        // as in the pass
+        ptx::mma_commit_elect(last);
+        ptx::mbar_wait(last, 0, LAST_WAIT_NS);
     }
 };
 
@@ -401,10 +399,9 @@ __global__ void __launch_bounds__(U_THREADS, 1) sum_tiles(const __grid_constant_
     int* ids = reinterpret_cast<int*>(tiles + SUM_TILES);
     int* steps = ids + SUM_TILES * TILE;
     uint64_t* full = reinterpret_cast<uint64_t*>(lists + s.lists());
-    uint64_t *empty = full + U_STAGES, *done = empty + U_STAGES, *free_ = done + 1;
-    uint32_t* slot = reinterpret_cast<uint32_t*>(free_ + 1);
-    volatile uint32_t* abort_flag = slot + 1;
-    volatile int* count = reinterpret_cast<volatile int*>(slot + 2);
+    uint64_t *empty = full + U_STAGES, *done = empty + U_STAGES, *free_ = done + 1, *last = free_ + 1;
+    uint32_t* slot = reinterpret_cast<uint32_t*>(last + 1);
+    volatile int* count = reinterpret_cast<volatile int*>(slot + 1);
     const int tid = threadIdx.x, warp = __shfl_sync(0xffffffffu, tid >> 5, 0), lane = tid & 31;
     // db's CTAs first: they need nothing of the pass before them, and run beside it where it leaves SMs free.
     const bool late = static_cast<int>(blockIdx.x) >= p.first_late;
@@ -413,12 +410,12 @@ __global__ void __launch_bounds__(U_THREADS, 1) sum_tiles(const __grid_constant_
     const int c0 = (number - piece * job.col_blocks) * 128 * s.blocks;
     if (tid == 0) {
         for (int i = 0; i < s.stages(); ++i) {
-            ptx::mbar_init(&full[i], U_WARPS);
+            ptx::mbar_init(&full[i], i == 0 ? U_WARPS + LOST_ROWS : U_WARPS);
             ptx::mbar_init(&empty[i], 1);
         }
-        ptx::mbar_init(done, 1);
+        ptx::mbar_init(done, 1 + LOST_DONE);
+        ptx::mbar_init(last, 1);
         ptx::mbar_init(free_, U_WARPS);
-        *abort_flag = 0u;
         ptx::mbar_init_fence();
     }
     // The pass has waited for what came before it, the plan with it, and lets this kernel start only then.
@@ -468,11 +465,11 @@ __global__ void __launch_bounds__(U_THREADS, 1) sum_tiles(const __grid_constant_
             sum.multiply(tmem);
     };
     if (job.mode == 0)
-        run(Sum<0>{p, job, s, raw, ids, steps, tiles, full, empty, done, free_, abort_flag, tid, warp, lane, c0, n, piece});
+        run(Sum<0>{p, job, s, raw, ids, steps, tiles, full, empty, done, free_, last, tid, warp, lane, c0, n, piece});
     else if (job.mode == 1)
-        run(Sum<1>{p, job, s, raw, ids, steps, tiles, full, empty, done, free_, abort_flag, tid, warp, lane, c0, n, piece});
+        run(Sum<1>{p, job, s, raw, ids, steps, tiles, full, empty, done, free_, last, tid, warp, lane, c0, n, piece});
     else
-        run(Sum<2>{p, job, s, raw, ids, steps, tiles, full, empty, done, free_, abort_flag, tid, warp, lane, c0, n, piece});
+        run(Sum<2>{p, job, s, raw, ids, steps, tiles, full, empty, done, free_, last, tid, warp, lane, c0, n, piece});
     ptx::tc_fence_before();
     __syncthreads();
     if (warp == U_WARPS) {
