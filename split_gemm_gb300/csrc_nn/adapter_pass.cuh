@@ -839,7 +839,7 @@ struct Pass {
         }
         __syncwarp();
         ptx::cp_async_wait_all();
-        if (!ok && lane == 0 && p.status) atomicMax(p.status, 6u);
+        if (!ok) atomicMax(p.status, 6u);
         __syncwarp();
         if (p.splits > 1 && warp >= P_WARPS) ptx::cluster_wait();
     }

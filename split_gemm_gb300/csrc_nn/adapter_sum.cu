@@ -386,7 +386,8 @@ struct Sum {
         }
         // as in the pass
         ptx::mma_commit_elect(last);
-        ptx::mbar_wait(last, 0, LAST_WAIT_NS);
+        if (!ptx::mbar_wait(last, 0, LAST_WAIT_NS)) ok = false;
+        if (!ok) atomicMax(p.status, 6u);
     }
 };
 

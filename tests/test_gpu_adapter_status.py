@@ -12,7 +12,7 @@ LIMIT = 5_000_000  # ns
 
 
 @pytest.mark.parametrize("lost", ["ROWS", "DONE"])
-def test_a_wait_that_runs_out_stays_in_its_call(tmp_path, lost):
+def test_a_wait_that_runs_out_is_reported_and_stays_in_its_call(tmp_path, lost):
     if not torch.cuda.is_available():
         pytest.fail("GPU tests need a CUDA device")
     from split_gemm_gb300 import _build
