@@ -43,7 +43,7 @@ int mxint8_dequantize(int64_t rows, int64_t cols, const void* data_dev, const vo
                       int32_t y_dtype, conv2d_stream_t stream);
 
 /* layer_norm_bwd with x as a checkpoint: data (16-byte aligned) and scales in the place of x_dev.  params: rows, cols, y_stride and
- * y_dtype (of dy) are used; dx is dense [rows][cols] of dy's type. */
+ * y_dtype (of dy) are used; dx is dense [rows][cols] of dy's type, may be dy itself where that is dense, and overlaps no other operand. */
 size_t mxint8_layer_norm_bwd_workspace_bytes(const layer_norm_params* params);
 
 int mxint8_layer_norm_bwd(const layer_norm_params* params, const void* dy_dev, const void* data_dev, const void* scales_dev,

@@ -39,7 +39,7 @@ constexpr int depth8()
 }
 
 template <typename TY, int E, int G, int MOST, bool SUMS, bool WHOLE>
-__global__ void __launch_bounds__(MOST, BWD_RESIDENT<G, E, MOST>) bwd8_rows(const TY* __restrict__ dy, const Checkpoint x, TY* __restrict__ dx, const BwdParams p)
+__global__ void __launch_bounds__(MOST, BWD_RESIDENT<G, E, MOST>) bwd8_rows(const TY* dy, const Checkpoint x, TY* dx, const BwdParams p)
 {
     constexpr int VEC = 8, ROWS = G ? MOST / G : 1, DEPTH = depth8<TY, E, G, MOST, WHOLE>();
     using Un = Units<VEC, E, WHOLE>;

@@ -157,19 +157,19 @@ int bwd8(BwdParams& k, const Checkpoint& x, const layer_norm_params* params, cud
         return rows8<TY>(k, x, s, stream);
     }
     k.chunks = static_cast<int>(mx::cdiv(k.rows, ANY_PART_ROWS) < ANY_PARTS ? mx::cdiv(k.rows, ANY_PART_ROWS) : ANY_PARTS);
-    if (held) {
-        if (int rc = rows8<TY>(k, x, s, stream)) return rc;
-    } else {
-        const unsigned grid = static_cast<unsigned>(k.rows < 65536 ? k.rows : 65536);
-        bwd8_dx_any<<<grid, THREADS, 0, stream>>>(dy, x, static_cast<TY*>(k.dx), k);
-    }
-    if (k.part) {
+    if (k.part) {  // first, as dx may take dy's place
         const bool vec = starts && (k.cols | k.dy_stride) % 8 == 0;
         const dim3 parts(static_cast<unsigned>(mx::cdiv<int64_t>(k.cols, THREADS * (vec ? 8 : 1))), static_cast<unsigned>(k.chunks));
         if (vec)
             bwd8_part_any<TY, 8><<<parts, THREADS, 0, stream>>>(dy, x, k);
         else
             bwd8_part_any<TY, 1><<<parts, THREADS, 0, stream>>>(dy, x, k);
+    }
+    if (held) {
+        if (int rc = rows8<TY>(k, x, s, stream)) return rc;
+    } else {
+        const unsigned grid = static_cast<unsigned>(k.rows < 65536 ? k.rows : 65536);
+        bwd8_dx_any<<<grid, THREADS, 0, stream>>>(dy, x, static_cast<TY*>(k.dx), k);
     }
     return cudaGetLastError() == cudaSuccess ? CONV2D_OK : CONV2D_ERR_CUDA;
 }

@@ -134,7 +134,7 @@ def _bwd(dx, dw_ptr, db_ptr, dy, x, mean, rstd, weight, workspace, stream) -> No
 
 
 def mxint8_layer_norm_bwd_into(dx, dweight, dbias, dy, x: Mxint8, mean, rstd, weight=None, *, workspace=None, stream=None) -> None:
-    """layer_norm_bwd_into with x as a checkpoint; ``dx`` is of dy's shape and type, dense.  ``workspace``: contiguous, on dy's
+    """layer_norm_bwd_into with x as a checkpoint; ``dx`` is of dy's shape and type, dense; a dense dy itself is allowed.  ``workspace``: contiguous, on dy's
     device, of mxint8_layer_norm_bwd_workspace_bytes (None: taken from torch).  Asynchronous."""
     cols = rows_of(dy, "dy")[1]
     if dx.shape != dy.shape or dx.dtype != dy.dtype or not dx.is_cuda or not dx.is_contiguous():
