@@ -96,7 +96,7 @@ def _check_weights(a, b, plan, cols, outs, like):
     return a.shape[1]
 
 
-def _fwd(out, h_ptr, y, x, a, b, plan, scale, relu, stream) -> None:
+def _fwd(out, h, y, x, a, b, plan, scale, relu, stream) -> None:
     rows, cols, x_stride = _bf16_rows(x, "x")
     y_rows, outs, y_stride = rows_of(y, "y")
     same_device(y, "y", x)
@@ -109,7 +109,7 @@ def _fwd(out, h_ptr, y, x, a, b, plan, scale, relu, stream) -> None:
     with on_device_of(x):
         rc = library().adapter_fwd(
             ctypes.byref(params), plan_ptr, y.data_ptr(), x.data_ptr(), a.data_ptr(), b.data_ptr(),
-            check_vector(scale, "scale", plan.adapters, x), out.data_ptr(), h_ptr, stream_handle(x, stream))
+            check_vector(scale, "scale", plan.adapters, x), out.data_ptr(), check_vector(h, "h", rows * rank, x), stream_handle(x, stream))
     if rc:
         raise Conv2dError(rc, "adapter_fwd")
 
@@ -117,13 +117,13 @@ def _fwd(out, h_ptr, y, x, a, b, plan, scale, relu, stream) -> None:
 def adapter_fwd_into(out, y, x, a, b, plan: AdapterPlan, scale=None, *, h=None, relu: bool = False, stream=None) -> None:
     """Writes act(y + b_e h) into ``out`` (y's shape, fp32 or bf16; y itself is allowed) and, where given, h = scale_e a_e x into
     ``h`` ([rows, R] fp32, contiguous).  ``relu``: after the sum; NaN stays NaN.  Asynchronous."""
-    rows = rows_of(x, "x")[0]
+    rows_of(x, "x")
+    rows_of(y, "y")
     rows_of(out, "out")
     if out.shape != y.shape:
         raise ValueError(f"out must be {list(y.shape)}, got {list(out.shape)}")
     same_device(out, "out", x)
-    h_ptr = None if h is None else check_vector(h, "h", rows * a.shape[1], x)
-    _fwd(out, h_ptr, y, x, a, b, plan, scale, relu, stream)
+    _fwd(out, h, y, x, a, b, plan, scale, relu, stream)
 
 
 def adapter_fwd(y, x, a, b, plan: AdapterPlan, scale=None, *, relu: bool = False, out_dtype=None, stream=None):
@@ -139,7 +139,7 @@ def adapter_fwd(y, x, a, b, plan: AdapterPlan, scale=None, *, relu: bool = False
         raise ValueError("a must be a tensor of [adapters, rank, cols]")
     out = empty_on(stream, y.shape, out_dtype, x.device)
     h = empty_on(stream, (rows, a.shape[1]), torch.float32, x.device)
-    _fwd(out, h.data_ptr(), y, x, a, b, plan, scale, relu, stream)
+    _fwd(out, h, y, x, a, b, plan, scale, relu, stream)
     return out, h
 
 
@@ -169,8 +169,9 @@ def _bwd_params(dy, x, a, b, plan, dx0, dx):
     return AdapterBwdParams(rows, cols, outs, rank, plan.adapters, dy_stride, x_stride, *strides, x_type, *codes), x_ptr
 
 
-def _bwd(dx, da_ptr, db_ptr, dy, x, h, a, b, plan, scale, dx0, workspace, stream) -> None:
+def _bwd(dx, da, db, dy, x, h, a, b, plan, scale, dx0, workspace, stream) -> None:
     params, x_ptr = _bwd_params(dy, x, a, b, plan, dx0, dx)
+    da_ptr, db_ptr = check_vector(da, "da", a.numel(), dy), check_vector(db, "db", b.numel(), dy)
     if h is None and db_ptr:
         raise ValueError("h of the forward pass is needed")
     h_ptr = check_vector(h, "h", params.rows * params.rank, dy)
@@ -200,7 +201,7 @@ def adapter_bwd_into(dx, da, db, dy, x, h, a, b, plan: AdapterPlan, scale=None, 
     (x's shape, fp32 or bf16) = ``dx0`` (None: zeros; dx itself is allowed) + a_e^T dh, and the fp32 ``da`` and ``db`` (a's and b's
     shapes); each of the three may be None: not computed.  ``workspace``: contiguous, on dy's device, of
     adapter_bwd_workspace_bytes (None: taken from torch).  Asynchronous."""
-    _bwd(dx, check_vector(da, "da", a.numel(), dy), check_vector(db, "db", b.numel(), dy), dy, x, h, a, b, plan, scale, dx0, workspace, stream)
+    _bwd(dx, da, db, dy, x, h, a, b, plan, scale, dx0, workspace, stream)
 
 
 def adapter_bwd(dy, x, h, a, b, plan: AdapterPlan, scale=None, *, dx=None, out_dtype=None, workspace=None, stream=None):
@@ -209,14 +210,14 @@ def adapter_bwd(dy, x, h, a, b, plan: AdapterPlan, scale=None, *, dx=None, out_d
     fp32.  ``x``: bf16, or a checkpoint of it, whose dx is [rows, C]."""
     if stream is None and workspace is None and (made := calls().adapter_bwd(dy, x, h, a, b, plan, scale, dx, out_dtype)) is not None:
         return made
+    params, _ = _bwd_params(dy, x, a, b, plan, dx, None)
     out_dtype = (torch.bfloat16 if dx is None else dx.dtype) if out_dtype is None else out_dtype
     check_out_dtype(out_dtype)
-    params, _ = _bwd_params(dy, x, a, b, plan, dx, None)
     shape = dx.shape if dx is not None else (params.rows, params.cols) if isinstance(x, Mxint8) else x.shape
     out = empty_on(stream, shape, out_dtype, dy.device)
     da = empty_on(stream, a.shape, torch.float32, dy.device)
     db = empty_on(stream, b.shape, torch.float32, dy.device)
-    _bwd(out, da.data_ptr(), db.data_ptr(), dy, x, h, a, b, plan, scale, dx, workspace, stream)
+    _bwd(out, da, db, dy, x, h, a, b, plan, scale, dx, workspace, stream)
     return out, da, db
 
 
