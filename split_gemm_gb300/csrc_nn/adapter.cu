@@ -103,8 +103,9 @@ extern "C" int adapter_fwd(const adapter_fwd_params* params, const void* plan_de
     p.from = static_cast<int>(q.cols);
     p.to = static_cast<int>(q.outs);
     p.relu = q.activation == CONV2D_ACT_RELU;
-    // Few rows by pieces of 8, which read an adapter's weights for each: 4096 x 4096, rank 16, 32 adapters, 512 rows 10.3 us (by tiles 17); rank 64, 8 adapters,
-    // 128 rows 13.6 us, 256 rows 20 (by tiles, 520 rows, 14.8).
+    // Few rows by pieces of 8, which read an adapter's weights for each.  The same calls by pieces and by tiles, us, 4096 -> 4096: rank 16, 32 adapters, 64 rows
+    // 5.2 and 17.6, 512 14.4 and 18.9, 640 16.1 and 20.5; rank 32, 8 adapters, 256 rows 8.5 and 12.4, 320 12.9 and 12.5; rank 64, 8 adapters, 160 rows 13.8 and 14.2, 256 20.5
+    // and 14.6.  Narrower layers would gain from pieces for longer (1024 -> 1024, rank 64, 256 rows 6.8 and 10.0).  Ranks above 64 have no such kernel.
     if (q.rows * mx::cdiv<int64_t>(q.rank, 16) <= ad::SMALL_ROWS && q.rank <= 64)
         return ad::launch_small_fwd(p, q.y_dtype, q.out_dtype, ad::in_vectors(p, q.y_dtype, q.out_dtype), stream);
     const bool vec = ad::in_vectors(p, q.y_dtype, q.out_dtype);

@@ -5,7 +5,7 @@
 // Forward w1 is a[e] and w2 is b[e], both K-major operands; backward (TRANS) w1 is b[e]^T and w2 a[e]^T, both MN-major.
 //
 // in, base and out each pass once over HBM and bind it: with rank r the matrix units have 2r flops to some 4 bytes.  What is reached is less, as a CTA's parts
-// follow one another: 8192 x 4096 -> 4096 of rank 64 takes 54 us (33 at HBM's rate, 4.1 TB/s), 12544 x 256 -> 1024 of rank 16, y fp32, 23 us (12.5).  A cluster
+// follow one another: 8192 x 4096 -> 4096 of rank 64 takes 53 to 57 us (33 at HBM's rate, 3.9 to 4.1 TB/s), 12544 x 256 -> 1024 of rank 16, y fp32, 23 to 24 us (12.5).  A cluster
 // of S CTAs shares a tile: each takes a part of `from` for the first product, 128/S rows of the join and a part of `to` for the
 // second.  One CTA fills an SM: what HBM needs in flight are bytes, and 96 KB of base on their way to shared memory gave more than two CTAs with
 // theirs in registers.  mid never leaves the chip but for the copy that the gradients need.

@@ -8,7 +8,7 @@
 // fp32, adapter_ptx.cuh) are the operand's 16 rows, half of them empty, and 32 columns of out its columns, in an order that leaves 8 neighbouring ones to a lane.
 // The products go by registers (mma.sync): at 8 rows they are no part of the time, and tcgen05's would first have to lie in shared memory and come back from tensor memory.
 //
-// One row of 4096 x 4096, rank 16, in a graph: 4.1 us, of which the launch and two cluster barriers are most; 64 rows, 32 adapters: 5.2 us, 10 MB at 1.9 TB/s.
+// One row of 4096 x 4096, rank 16, in a graph: 4.0 to 4.2 us, of which the launch and two cluster barriers are most; 64 rows, 32 adapters: 5.3 us, 10 MB at 1.9 TB/s.
 #include "conv2d.h"
 
 #include "adapter_params.cuh"

@@ -2,7 +2,7 @@
 // db (mid = h, in = dy) in one launch.
 //
 // HBM would bind: `in` is read once, and with rank r there are 2r flops to its 1 or 2 bytes.  What is reached is half of its rate (db of 16384 x 4096, rank 64:
-// 46 us for 20 of HBM's, with two launches): a stage's mid is converted by the warps that also see to its copies, some 1.2 us for 64 KB or less.  A CTA takes 256 columns of `in` (128 above
+// 47 us for 20 of HBM's, with two launches): a stage's mid is converted by the warps that also see to its copies, some 1.2 us for 64 KB or less.  A CTA takes 256 columns of `in` (128 above
 // rank 64, by tensor memory) and a piece of up to 32 of the plan's tiles, whatever adapters those belong to; an adapter's sum that lies in one piece goes straight
 // to the result, else each piece's part goes to the workspace and a second launch adds the parts in order.
 //
@@ -18,7 +18,7 @@
 // registers, one or two stages ahead.  A checkpoint's integer becomes a bf16 number by bits: (m | 128) - 128 or 256, each with the scale in its exponent.
 //
 // db needs nothing of the pass before it, and its CTAs run beside that pass where it leaves SMs free; da's, which take dh, wait for it.  Both gradients of
-// 16384 x 4096 -> 4096, rank 64, with dx take 181 us, where dx alone takes 96.
+// 16384 x 4096 -> 4096, rank 64, with dx take 184 us, where dx alone takes 96.
 //
 // Every wait is bounded, as in the pass (adapter_pass.cuh).
 #include "adapter.h"
