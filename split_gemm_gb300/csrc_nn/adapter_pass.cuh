@@ -77,10 +77,14 @@ struct Pass {
         rank_in = blockIdx.x % p.splits;
         group = warp >> 3;
     }
-    // Once a wait has run out, `ok` is false and the thread waits no more.
+    // Once a wait has run out, `ok` is false and the thread waits no more.  (Reported at the thread's end instead, it cost loaders of rows that are not whole
+    // vectors up to 7%.)
     __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, bool& ok) const
     {
-        if (!ptx::mbar_try_wait(bar, parity) && ok && !ptx::mbar_wait(bar, parity, WAIT_NS)) ok = false;
+        if (!ptx::mbar_try_wait(bar, parity) && ok && !ptx::mbar_wait(bar, parity, WAIT_NS)) {
+            ok = false;
+            atomicMax(p.status, 6u);
+        }
     }
     __device__ __forceinline__ float* mids() const { return reinterpret_cast<float*>(mem + s.area() - s.sums()); }
     __device__ __forceinline__ uint8_t* w2_buf(int i) const { return i ? mem + s.area() - s.ring() - i * s.chunk() : mem + s.area(); }
@@ -735,7 +739,10 @@ struct Pass {
         // All of mid is here: none of this CTA's peers reads its sums any more, and what they sent has come.  Every thread waits for that, also after a wait
         // that has run out, as the peers send in any case, and no memory that they send to or from may be given up.
         if (p.splits > 1) {
-            if (!ptx::mbar_wait(mid_full, 0, LAST_WAIT_NS)) ok = false;
+            if (!ptx::mbar_wait(mid_full, 0, LAST_WAIT_NS)) {
+                ok = false;
+                atomicMax(p.status, 6u);
+            }
             __syncwarp();
             ptx::cluster_arrive_relaxed();
         }
@@ -773,7 +780,7 @@ struct Pass {
             }
             // The CTA lives until its MMAs have ended, whatever waits have run out.
             ptx::mma_commit_elect(last);
-            if (!ptx::mbar_wait(last, 0, LAST_WAIT_NS)) ok = false;
+            if (!ptx::mbar_wait(last, 0, LAST_WAIT_NS)) atomicMax(p.status, 6u);
         } else if (warp > P_WARPS) {
             // the word of each a chunk later
             if (n > 1 && s.late()) bring_w2(1, (chunk0 + 1) * COLS, ok);
@@ -839,7 +846,6 @@ struct Pass {
         }
         __syncwarp();
         ptx::cp_async_wait_all();
-        if (!ok) atomicMax(p.status, 6u);
         __syncwarp();
         if (p.splits > 1 && warp >= P_WARPS) ptx::cluster_wait();
     }

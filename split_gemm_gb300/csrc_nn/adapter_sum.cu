@@ -69,7 +69,10 @@ struct Sum {
     // As in the pass: once a wait has run out, the thread waits no more.
     __device__ __forceinline__ void wait(uint64_t* bar, uint32_t parity, bool& ok) const
     {
-        if (!ptx::mbar_try_wait(bar, parity) && ok && !ptx::mbar_wait(bar, parity, WAIT_NS)) ok = false;
+        if (!ptx::mbar_try_wait(bar, parity) && ok && !ptx::mbar_wait(bar, parity, WAIT_NS)) {
+            ok = false;
+            atomicMax(p.status, 6u);
+        }
     }
     __device__ __forceinline__ int adapter_at(int k) const { return tiles[steps[k]].adapter; }
     __device__ __forceinline__ bool ends_run(int k) const { return k + 1 == n || adapter_at(k + 1) != adapter_at(k); }
@@ -345,7 +348,6 @@ struct Sum {
                 }
             }
         if constexpr (MODE == 0) ptx::cp_async_wait_all();
-        if (!ok) atomicMax(p.status, 6u);
     }
 
     __device__ __forceinline__ void multiply(uint32_t tmem)
@@ -388,8 +390,7 @@ struct Sum {
         }
         // as in the pass
         ptx::mma_commit_elect(last);
-        if (!ptx::mbar_wait(last, 0, LAST_WAIT_NS)) ok = false;
-        if (!ok) atomicMax(p.status, 6u);
+        if (!ptx::mbar_wait(last, 0, LAST_WAIT_NS)) atomicMax(p.status, 6u);
     }
 };
 
