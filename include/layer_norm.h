@@ -42,7 +42,7 @@ typedef struct {
 int layer_norm_fwd(const layer_norm_params* params, const void* x_dev, const float* weight_dev,
                    const float* bias_dev, void* y_dev, float* mean_dev, float* rstd_dev, conv2d_stream_t stream);
 
-/* dx [rows][cols], dense, of x's type; dweight_dev, dbias_dev [cols] fp32, each
+/* dx [rows][cols], dense, of x's type, overlapping no operand; dweight_dev, dbias_dev [cols] fp32, each
  * may be NULL (not computed); both are zero for no rows.  The sums over the
  * rows are joined in a fixed order.  workspace_dev: at least
  * layer_norm_bwd_workspace_bytes() bytes of any content, 16-byte aligned (may be
